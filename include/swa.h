@@ -36,6 +36,10 @@
  *             by the query at position t iff 0 <= pos_j <= t and either
  *             t - window < pos_j or pos_j < n_sink (the first n_sink positions
  *             pinned as attention sinks; window defaults to W).
+ * swa_paged_attend  New tokens of a ragged batch against a paged KV cache, in which the
+ *             tokens of a sequence lie in pages of one pool; swa_paged_append stores
+ *             tokens, and swa_pages_reserve / _free / _fork / _compact / _copy manage the
+ *             pages, their tables and their holders.
  *
  * Conventions
  * -----------
@@ -280,6 +284,172 @@ SWA_API size_t swa_prefill_chunk_workspace_size(const swa_chunk_params *p, const
 SWA_API swa_status swa_prefill_chunk(const swa_chunk_params *p, const swa_cache_params *c, void *workspace,
                              size_t workspace_bytes, swa_stream_t stream);
 
+/*
+ * A paged KV cache: the tokens of a sequence lie in pages of page_size positions taken
+ * from one pool.  Entry j of row b of the page table is the page that holds positions
+ * j * page_size .. (j + 1) * page_size - 1 of sequence b; a negative entry is no page
+ * (not yet reserved, or given up behind the window).  Sequences may share pages.
+ *   k_pages, v_pages  bf16 [n_pages, H_kv, page_size, d_h], contiguous
+ *   page_table        int32 [B, table_width], contiguous
+ * Requirements: d_h in {64, 128, 256}; page_size in {16, 32, 64, 128}; B <= 8192;
+ * table_width * page_size < 2^31; pointers 16-byte aligned (page_table: 4-byte).
+ */
+typedef struct swa_paged_cache {
+    void *k_pages;
+    void *v_pages;
+    const int32_t *page_table;
+    int32_t n_pages, page_size, H_kv, d_h, B, table_width;
+} swa_paged_cache;
+
+/*
+ * Attention of new tokens over a paged cache, for a batch in which every sequence has its
+ * own number of them (a chunk of a prompt, or the one token of a decode step).  The new
+ * tokens are packed: rows q_start[b] .. q_start[b+1]-1 of the N rows belong to sequence b,
+ * and its i-th has position p0[b] + i.  The query at position t keeps the keys at positions
+ * s <= t with t - window < s or s < n_sink (the rule of swa_decode; window 0: every s <= t).
+ *   q            bf16 [N, H_q, d_h]; q_strides = element strides of (token, head); d_h contiguous
+ *   o            bf16 [N, H_q, d_h]; o_strides likewise
+ *   lse          fp32 [N, H_q], contiguous; row_counts optional int32 [N, H_q], contiguous
+ *   p0           device int32 [B], each >= 0: tokens of the sequence stored before these
+ *   q_start      device int32 [B + 1], not decreasing, within [0, N]; NULL: one token a
+ *                sequence (N = B).  A sequence may have no new token.  Rows of q outside
+ *                [q_start[0], q_start[B]) are not read into any result, and their rows of
+ *                o, lse and row_counts are left as they were.
+ *   k_new, v_new optional bf16 [N, H_kv, d_h], kn_strides / vn_strides as q's: the new tokens'
+ *                keys and values, stored in their pages first (as swa_paged_append does);
+ *                both NULL: they are there already.
+ *   max_q        the most new tokens of one sequence, as far as the caller knows (0: not
+ *                known).  It chooses between kernels for few and for many rows; results are
+ *                right whatever it says.
+ * The cache must hold every position that a query keeps; the rows of a page at or past its
+ * sequence's end (p0 + its new tokens) may hold anything.  What the device finds broken is
+ * reported by swa_check_device_error as SWA_ERR_INVALID_ARG, and nothing outside the call's
+ * buffers is read or written: a sequence whose q_start or p0 is out of range or that does
+ * not fit its table row is skipped, its rows left as they were (SWA_DEVERR_BAD_POSITION); a
+ * page that is needed but is missing or not in the pool counts as rows of zeros
+ * (SWA_DEVERR_BAD_PAGE).
+ * Requirements: H_q % H_kv == 0 and H_q / H_kv <= 16; strides multiples of 8 elements and
+ * positive; window >= 0, n_sink >= 0; pointers 16-byte aligned (int32 and fp32 ones 4-byte).
+ * With new rows, no two sequences may share the pages that these are written to.  N = 0 is a no-op.
+ */
+typedef struct swa_paged_params {
+    const void *q;
+    const void *k_new;
+    const void *v_new;
+    const int32_t *p0;
+    const int32_t *q_start;
+    int64_t q_strides[2];
+    int64_t kn_strides[2];
+    int64_t vn_strides[2];
+    int64_t o_strides[2];
+    int32_t N, H_q, max_q;
+    int32_t window, n_sink;
+    float scale;
+    void *o;
+    float *lse;
+    int32_t *row_counts;
+} swa_paged_params;
+
+/* Bytes of device workspace swa_paged_attend needs (the partial results of sequences that
+ * several CTAs share); 0 for invalid params.  It does not depend on device data. */
+SWA_API size_t swa_paged_workspace_size(const swa_paged_params *p, const swa_paged_cache *c);
+SWA_API swa_status swa_paged_attend(const swa_paged_params *p, const swa_paged_cache *c, void *workspace,
+                                    size_t workspace_bytes, swa_stream_t stream);
+
+/*
+ * Stores the new tokens' keys and values in their pages: p->k_new, p->v_new, p->p0, p->q_start
+ * and p->N as above; nothing else of p is read.  A token whose page is missing is not stored
+ * (SWA_DEVERR_BAD_PAGE).
+ */
+SWA_API swa_status swa_paged_append(const swa_paged_params *p, const swa_paged_cache *c, swa_stream_t stream);
+
+/*
+ * Pages and who holds them.  ref[p] counts the holders of page p -- the table entries that
+ * name it, and whatever else the caller lets hold it; a page with ref 0 is free.  The calls
+ * below that change tables and counts read `table` and `ref` and write the whole of
+ * `out_table` [B, width] and `out_ref` [n_pages], which may be the same memory as `table`
+ * and `ref` where a call says so.  Pages are always taken lowest index first, so results do
+ * not depend on timing.  Entries outside the pool are treated as no page and reported
+ * (SWA_DEVERR_BAD_PAGE).
+ * Requirements: page_size >= 1; B, width, n_pages >= 1; width * page_size < 2^31;
+ * B * width < 2^31; pointers 4-byte aligned.
+ */
+typedef struct swa_page_tables {
+    const int32_t *table;
+    const int32_t *ref;
+    int32_t *out_table;
+    int32_t *out_ref;
+    int32_t B, width, n_pages, page_size;
+} swa_page_tables;
+
+/*
+ * The pool of all layers: bf16 [n_layers, n_pages, H_kv, page_size, d_h], contiguous but for
+ * layer_stride (elements from one layer to the next, a multiple of 8).  A page is the same
+ * one in every layer.  d_h any multiple of 8; pointers 16-byte aligned; n_pages and page_size
+ * as in swa_page_tables where both are given.
+ */
+typedef struct swa_page_pool {
+    void *k_pages;
+    void *v_pages;
+    int64_t layer_stride;
+    int32_t n_layers, n_pages, H_kv, page_size, d_h;
+} swa_page_pool;
+
+/* Bytes of device workspace that swa_pages_reserve, swa_pages_fork and swa_pages_compact
+ * need for such tables (one answer for all three); 0 for invalid ones. */
+SWA_API size_t swa_pages_workspace_size(const swa_page_tables *t);
+
+/*
+ * Gives row b a page for every position in [first[b], end[b]) that has none (device int32
+ * [B] each; nothing where end[b] <= first[b]): free pages, lowest first, to the rows in order
+ * and within a row to its entries in order; each gets ref 1.  When the pool runs out the
+ * remaining entries stay without a page (SWA_DEVERR_NO_PAGE); a row whose range is not within
+ * [0, width * page_size] is left out (SWA_DEVERR_BAD_POSITION).  In place only: out_table =
+ * table and out_ref = ref.
+ */
+SWA_API swa_status swa_pages_reserve(const swa_page_tables *t, const int32_t *first, const int32_t *end,
+                                     void *workspace, size_t workspace_bytes, swa_stream_t stream);
+
+/*
+ * Gives pages back: row b gives up every entry j whose positions all lie below below[b] and
+ * that holds none of the first n_sink positions ((j + 1) * page_size <= below[b] and
+ * j * page_size >= n_sink), and with below[b] < 0 every entry.  Each loses one holder.  A page
+ * that has no holder left to lose is reported (SWA_DEVERR_BAD_REF) and stays free.  May be in
+ * place (both or neither).
+ */
+SWA_API swa_status swa_pages_free(const swa_page_tables *t, const int32_t *below, int32_t n_sink,
+                                  swa_stream_t stream);
+
+/*
+ * Replaces the batch's rows: row i of out_table continues row src[i] of table, which holds
+ * len[src[i]] tokens (src, len: device int32 [B]; src[i] = -1: row i is empty).  Full pages
+ * are shared.  The last page, if it is not full, stays with the lowest i of the rows that
+ * continue the same row; each other one gets a page of its own, lowest free first in the
+ * order of i, and the tokens are copied into it in every layer.  Holders are counted anew: out_ref
+ * = ref, less the entries of `table`, plus those of out_table.  Entries past the last token
+ * are dropped.  Where the pool runs out a row stays without its last page
+ * (SWA_DEVERR_NO_PAGE).  A src or len out of range is reported (SWA_DEVERR_BAD_POSITION) and
+ * gives an empty row.  out_table must not overlap table; out_ref may be ref.
+ */
+SWA_API swa_status swa_pages_fork(const swa_page_tables *t, const swa_page_pool *pool, const int32_t *src,
+                                  const int32_t *len, void *workspace, size_t workspace_bytes, swa_stream_t stream);
+
+/*
+ * Moves the pool's live pages (ref > 0) to its low end: with M of them, the k-th live page at
+ * or above M moves to the k-th free one below M, in every layer; tables and counts follow, and
+ * *n_live (device int32) becomes M.  The pages left keep their old content.  May be in place
+ * (both or neither).
+ */
+SWA_API swa_status swa_pages_compact(const swa_page_tables *t, const swa_page_pool *pool, int32_t *n_live,
+                                     void *workspace, size_t workspace_bytes, swa_stream_t stream);
+
+/*
+ * Copies page src[i] to page dst[i] in every layer, i < n (device int32 [n] each).  The dst
+ * are distinct and none is also a src.  A pair outside the pool is skipped (SWA_DEVERR_BAD_PAGE).
+ */
+SWA_API swa_status swa_pages_copy(const swa_page_pool *pool, const int32_t *src, const int32_t *dst, int32_t n,
+                                  swa_stream_t stream);
+
 /* Bytes of the built-in scratch array used by swa_decode_noalloc (16 MiB per device). */
 #define SWA_DECODE_NOALLOC_SCRATCH_BYTES (16u << 20)
 
@@ -326,13 +496,16 @@ SWA_API swa_status swa_check_device_error(swa_stream_t stream);
 #define SWA_DEVERR_GLOBAL_LIST 4u   /* prefill: global_idx not strictly increasing within [0, T) */
 #define SWA_DEVERR_BAD_POSITION 1u  /* cache: a negative (or overflowing) append position */
 #define SWA_DEVERR_CACHE_MISMATCH 2u /* cache: a slot not holding a position a chunked prefill needs */
+#define SWA_DEVERR_BAD_PAGE 4u       /* cache: a page that is missing or not in the pool */
+#define SWA_DEVERR_NO_PAGE 16u       /* cache: the pool has no free page left */
+#define SWA_DEVERR_BAD_REF 32u       /* cache: a page given back that nobody holds */
 #define SWA_DEVERR_BOUNDS 8u         /* any word, debug library only: an index outside its tensor (access skipped) */
 
 /* The device error words, one per group of kernels. */
 typedef struct swa_device_errors {
-    uint32_t prefill; /* the band kernel of swa_fwd / swa_prefill_chunk */
-    uint32_t split;   /* decode and the global-row pass of swa_fwd (split-K and merge) */
-    uint32_t cache;   /* swa_cache_append, the history gather of swa_prefill_chunk */
+    uint32_t prefill; /* the band kernel of swa_fwd / swa_prefill_chunk; swa_paged_attend, many rows */
+    uint32_t split;   /* decode and the global-row pass of swa_fwd (split-K and merge); swa_paged_attend, few rows */
+    uint32_t cache;   /* swa_cache_append, the history gather of swa_prefill_chunk; pages and their contents */
 } swa_device_errors;
 
 /*

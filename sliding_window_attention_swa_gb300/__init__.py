@@ -2,7 +2,8 @@
 
 The functions here marshal torch tensors into the C ABI of ``include/swa.h``
 (``swa_fwd``, ``swa_decode``, ``swa_cache_append``, ``swa_decode_append``,
-``swa_prefill_chunk`` and their workspace queries) and call it on the current
+``swa_prefill_chunk``, ``swa_paged_attend``, ``swa_paged_append``, the
+``swa_pages_*`` calls and their workspace queries) and call it on the current
 CUDA stream.  Every step of the computation runs in the library's
 kernels; there is no fallback path.  If the library has not been built, the
 first call raises (``build()`` compiles it in-tree with nvcc).
@@ -23,9 +24,12 @@ __all__ = [
     "SwaFwdParams", "SwaDecodeParams", "GLOBAL_FULL", "GLOBAL_SINK",
     "SwaCacheParams", "SwaChunkParams", "swa_cache_append", "swa_decode_append", "swa_prefill_chunk",
     "SwaDeviceErrors", "SwaDebugFaults", "swa_read_device_errors", "swa_debug_set_faults",
+    "SwaPagedCache", "SwaPagedParams", "SwaPageTables", "SwaPagePool", "swa_paged_attend", "swa_paged_append",
+    "swa_pages_reserve", "swa_pages_free", "swa_pages_fork", "swa_pages_compact", "swa_pages_copy",
 ]
 
 _c_i64x3 = ctypes.c_int64 * 3
+_c_i64x2 = ctypes.c_int64 * 2
 
 
 class SwaFwdParams(ctypes.Structure):
@@ -78,6 +82,48 @@ class SwaChunkParams(ctypes.Structure):
     ]
 
 
+class SwaPagedCache(ctypes.Structure):
+    """Mirror of ``swa_paged_cache`` in include/swa.h."""
+
+    _fields_ = [
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("d_h", ctypes.c_int32),
+        ("B", ctypes.c_int32), ("table_width", ctypes.c_int32),
+    ]
+
+
+class SwaPagedParams(ctypes.Structure):
+    """Mirror of ``swa_paged_params`` in include/swa.h."""
+
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p), ("p0", ctypes.c_void_p),
+        ("q_start", ctypes.c_void_p), ("q_strides", _c_i64x2), ("kn_strides", _c_i64x2), ("vn_strides", _c_i64x2),
+        ("o_strides", _c_i64x2), ("N", ctypes.c_int32), ("H_q", ctypes.c_int32), ("max_q", ctypes.c_int32),
+        ("window", ctypes.c_int32), ("n_sink", ctypes.c_int32), ("scale", ctypes.c_float), ("o", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("row_counts", ctypes.c_void_p),
+    ]
+
+
+class SwaPageTables(ctypes.Structure):
+    """Mirror of ``swa_page_tables`` in include/swa.h."""
+
+    _fields_ = [
+        ("table", ctypes.c_void_p), ("ref", ctypes.c_void_p), ("out_table", ctypes.c_void_p),
+        ("out_ref", ctypes.c_void_p), ("B", ctypes.c_int32), ("width", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+    ]
+
+
+class SwaPagePool(ctypes.Structure):
+    """Mirror of ``swa_page_pool`` in include/swa.h."""
+
+    _fields_ = [
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("layer_stride", ctypes.c_int64),
+        ("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("d_h", ctypes.c_int32),
+    ]
+
+
 class SwaDeviceErrors(ctypes.Structure):
     """Mirror of ``swa_device_errors`` in include/swa.h."""
 
@@ -96,7 +142,10 @@ DEVERR_DRAIN_TIMEOUT = 2
 DEVERR_GLOBAL_LIST = 4
 DEVERR_BAD_POSITION = 1
 DEVERR_CACHE_MISMATCH = 2
+DEVERR_BAD_PAGE = 4
 DEVERR_BOUNDS = 8
+DEVERR_NO_PAGE = 16
+DEVERR_BAD_REF = 32
 
 GLOBAL_FULL = 0  # global tokens: full rows and columns
 GLOBAL_SINK = 1  # attention sinks: key columns only, never right of a row's band
@@ -155,6 +204,22 @@ def load_library(path: str | None = None):
     lib.swa_prefill_chunk_workspace_size.restype = sz
     lib.swa_prefill_chunk.argtypes = [ctypes.POINTER(SwaChunkParams), ctypes.POINTER(SwaCacheParams), vp, sz, vp]
     lib.swa_prefill_chunk.restype = ctypes.c_int
+    paged, cache = ctypes.POINTER(SwaPagedParams), ctypes.POINTER(SwaPagedCache)
+    tables, pool = ctypes.POINTER(SwaPageTables), ctypes.POINTER(SwaPagePool)
+    lib.swa_paged_workspace_size.argtypes = [paged, cache]
+    lib.swa_paged_workspace_size.restype = sz
+    lib.swa_paged_attend.argtypes = [paged, cache, vp, sz, vp]
+    lib.swa_paged_append.argtypes = [paged, cache, vp]
+    lib.swa_pages_workspace_size.argtypes = [tables]
+    lib.swa_pages_workspace_size.restype = sz
+    lib.swa_pages_reserve.argtypes = [tables, vp, vp, vp, sz, vp]
+    lib.swa_pages_free.argtypes = [tables, vp, ctypes.c_int32, vp]
+    lib.swa_pages_fork.argtypes = [tables, pool, vp, vp, vp, sz, vp]
+    lib.swa_pages_compact.argtypes = [tables, pool, vp, vp, sz, vp]
+    lib.swa_pages_copy.argtypes = [pool, vp, vp, ctypes.c_int32, vp]
+    for name in ("swa_paged_attend", "swa_paged_append", "swa_pages_reserve", "swa_pages_free", "swa_pages_fork",
+                 "swa_pages_compact", "swa_pages_copy"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.swa_check_device_error.argtypes = [vp]
     lib.swa_check_device_error.restype = ctypes.c_int
     lib.swa_read_device_errors.argtypes = [vp, ctypes.POINTER(SwaDeviceErrors)]
@@ -471,6 +536,246 @@ def swa_prefill_chunk(q, k_new, v_new, k_cache, v_cache, slot_pos, p0, window: i
     if st != 0:
         raise SwaError("swa_prefill_chunk", st)
     return o, lse, row_counts
+
+
+def _check_i32(name, t, shape, device):
+    import torch
+
+    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous int32 tensor of shape {list(shape)} on {device}")
+
+
+def _check_current(device):
+    """The library's calls go to the current device: tensors of another one are refused."""
+    import torch
+
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"expected tensors on the current CUDA device, got {device}")
+
+
+def _paged(q, k_pages, v_pages, page_table, p0, q_start, k_new, v_new):
+    """The cache and batch structures of a paged call, checked (q: any of the packed rows)."""
+    device = k_pages.device
+    _check_current(device)
+    _check_bf16("k_pages", k_pages, 4)
+    _check_bf16("v_pages", v_pages, 4)
+    if v_pages.shape != k_pages.shape or v_pages.device != device:
+        raise ValueError("v_pages: expected the shape and device of k_pages")
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
+    if page_table.dim() != 2:
+        raise ValueError("page_table: expected int32 [B, table_width]")
+    B, N = page_table.shape[0], q.shape[0]
+    _check_i32("page_table", page_table, page_table.shape, device)
+    _check_i32("p0", p0, (B,), device)
+    if q_start is not None:
+        _check_i32("q_start", q_start, (B + 1,), device)
+    elif N != B:
+        raise ValueError(f"q_start: needed unless every sequence has one token ({N} rows, {B} sequences)")
+    c = SwaPagedCache(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr())
+    c.n_pages, c.H_kv, c.page_size, c.d_h = k_pages.shape
+    c.B, c.table_width = page_table.shape
+    p = SwaPagedParams()
+    p.p0, p.q_start, p.N = p0.data_ptr(), None if q_start is None else q_start.data_ptr(), N
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    if k_new is not None:
+        for name, t in (("k_new", k_new), ("v_new", v_new)):
+            _check_bf16(name, t, 3)
+            if tuple(t.shape) != (N, c.H_kv, c.d_h) or t.device != device:
+                raise ValueError(f"{name}: expected shape {[N, c.H_kv, c.d_h]} on {device}")
+        p.k_new, p.v_new = k_new.data_ptr(), v_new.data_ptr()
+        p.kn_strides, p.vn_strides = k_new.stride()[:2], v_new.stride()[:2]
+    return p, c
+
+
+def swa_paged_attend(q, k_pages, v_pages, page_table, p0, window: int = 0, scale: float | None = None, *, q_start=None,
+                     n_sink: int = 0, max_q: int = 0, k_new=None, v_new=None, o=None, lse=None, row_counts=None,
+                     want_counts: bool = False, workspace=None, stream=None):
+    """Attention of new tokens over a paged cache: q [N,H_q,d] (bf16, any token and head strides),
+    pools [n_pages,H_kv,page_size,d], page_table int32 [B,table_width], p0 int32 [B].
+
+    Rows q_start[b] .. q_start[b+1]-1 (int32 [B+1]; None: one row a sequence) are sequence b's
+    new tokens at positions p0[b] + i; the query at position t keeps the keys at positions s <= t
+    with s > t - window (window 0: all) or s < n_sink.  k_new, v_new [N,H_kv,d]: stored in their
+    pages first.  max_q: the most new tokens of one sequence if known (a hint).  Rows outside
+    every sequence keep what o, lse and row_counts hold.
+    Returns (o [N,H_q,d] bf16, lse [N,H_q] fp32, row_counts [N,H_q] int32 or None).
+    """
+    import torch
+
+    lib = load_library()
+    _check_bf16("q", q, 3)
+    p, c = _paged(q, k_pages, v_pages, page_table, p0, q_start, k_new, v_new)
+    N, Hq, D = q.shape
+    if D != c.d_h or q.device != k_pages.device:
+        raise ValueError(f"q: expected shape [N, H_q, {c.d_h}] on {k_pages.device}")
+    if o is None:
+        o = torch.empty((N, Hq, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _check_bf16("o", o, 3)
+        if o.shape != q.shape or o.device != q.device:
+            raise ValueError("o: expected the shape and device of q")
+    lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (N, Hq) or not lse.is_contiguous() or lse.device != q.device:
+        raise ValueError("lse: expected a contiguous fp32 tensor [N, H_q]")
+    if row_counts is None and want_counts:
+        row_counts = torch.empty((N, Hq), dtype=torch.int32, device=q.device)
+    elif row_counts is not None:
+        _check_i32("row_counts", row_counts, (N, Hq), q.device)
+    p.q, p.q_strides, p.H_q, p.max_q = q.data_ptr(), q.stride()[:2], Hq, int(max_q)
+    p.window, p.n_sink, p.scale = int(window), int(n_sink), float(D ** -0.5 if scale is None else scale)
+    p.o, p.o_strides, p.lse = o.data_ptr(), o.stride()[:2], lse.data_ptr()
+    p.row_counts = None if row_counts is None else row_counts.data_ptr()
+    pp, pc = ctypes.byref(p), ctypes.byref(c)
+    if N == 0:
+        return o, lse, row_counts
+    if workspace is None:
+        workspace = torch.empty(max(int(lib.swa_paged_workspace_size(pp, pc)), 1), dtype=torch.uint8, device=q.device)
+    st = lib.swa_paged_attend(pp, pc, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                              _stream_handle(stream))
+    if st != 0:
+        raise SwaError("swa_paged_attend", st)
+    return o, lse, row_counts
+
+
+def swa_paged_append(k_pages, v_pages, page_table, k_new, v_new, p0, *, q_start=None, stream=None) -> None:
+    """Store k_new/v_new [N,H_kv,d] (packed rows as in swa_paged_attend) in their pages."""
+    p, c = _paged(k_new, k_pages, v_pages, page_table, p0, q_start, k_new, v_new)
+    if k_new.shape[0] == 0:
+        return
+    st = load_library().swa_paged_append(ctypes.byref(p), ctypes.byref(c), _stream_handle(stream))
+    if st != 0:
+        raise SwaError("swa_paged_append", st)
+
+
+def _page_tables(page_table, ref, page_size: int, out_table, out_ref) -> SwaPageTables:
+    device = page_table.device
+    _check_current(device)
+    if page_table.dim() != 2 or ref.dim() != 1:
+        raise ValueError("page_table: expected int32 [B, width], and ref int32 [n_pages]")
+    _check_i32("page_table", page_table, page_table.shape, device)
+    _check_i32("ref", ref, ref.shape, device)
+    _check_i32("out_table", out_table, page_table.shape, device)
+    _check_i32("out_ref", out_ref, ref.shape, device)
+    t = SwaPageTables(page_table.data_ptr(), ref.data_ptr(), out_table.data_ptr(), out_ref.data_ptr())
+    t.B, t.width = page_table.shape
+    t.n_pages, t.page_size = ref.shape[0], int(page_size)
+    return t
+
+
+def _page_pool(k_pages, v_pages, device) -> SwaPagePool:
+    """A pool [n_pages,H_kv,page_size,d] or [n_layers,n_pages,H_kv,page_size,d] (a layer contiguous)."""
+    _check_current(device)
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dim() not in (4, 5):
+            raise ValueError(f"{name}: expected [n_pages, H_kv, page_size, d] or [n_layers, n_pages, H_kv, page_size, d]")
+        _check_bf16(name, t, t.dim())
+        if t.shape != k_pages.shape or t.stride() != k_pages.stride() or t.device != device:
+            raise ValueError(f"{name}: expected the shape and strides of k_pages, on {device}")
+        if not (t if t.dim() == 4 else t[0]).is_contiguous():
+            raise ValueError(f"{name}: expected each layer's pages to be contiguous")
+    p = SwaPagePool(k_pages.data_ptr(), v_pages.data_ptr())
+    p.n_layers = 1 if k_pages.dim() == 4 else k_pages.shape[0]
+    p.layer_stride = 0 if k_pages.dim() == 4 else k_pages.stride(0)
+    p.n_pages, p.H_kv, p.page_size, p.d_h = k_pages.shape[-4:]
+    return p
+
+
+def _pages_workspace(lib, t, workspace, device):
+    import torch
+
+    if workspace is None:
+        workspace = torch.empty(max(int(lib.swa_pages_workspace_size(ctypes.byref(t))), 1), dtype=torch.uint8,
+                                device=device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def swa_pages_reserve(page_table, ref, first, end, page_size: int, *, workspace=None, stream=None) -> None:
+    """Give row b of page_table (in place, with ref) a page for every position in [first[b], end[b])
+    that has none: the lowest free pages, in the order of rows and entries."""
+    lib = load_library()
+    t = _page_tables(page_table, ref, page_size, page_table, ref)
+    _check_i32("first", first, (t.B,), page_table.device)
+    _check_i32("end", end, (t.B,), page_table.device)
+    workspace, n = _pages_workspace(lib, t, workspace, page_table.device)
+    st = lib.swa_pages_reserve(ctypes.byref(t), first.data_ptr(), end.data_ptr(), workspace.data_ptr(), n,
+                               _stream_handle(stream))
+    if st != 0:
+        raise SwaError("swa_pages_reserve", st)
+
+
+def swa_pages_free(page_table, ref, below, page_size: int, *, n_sink: int = 0, out_table=None, out_ref=None,
+                   stream=None):
+    """Row b gives up its pages whose positions all lie below below[b] and past the first n_sink
+    positions' pages (below[b] < 0: all its pages).  In place unless out_table and out_ref are
+    given.  Returns (out_table, out_ref)."""
+    out_table, out_ref = page_table if out_table is None else out_table, ref if out_ref is None else out_ref
+    t = _page_tables(page_table, ref, page_size, out_table, out_ref)
+    _check_i32("below", below, (t.B,), page_table.device)
+    st = load_library().swa_pages_free(ctypes.byref(t), below.data_ptr(), int(n_sink), _stream_handle(stream))
+    if st != 0:
+        raise SwaError("swa_pages_free", st)
+    return out_table, out_ref
+
+
+def swa_pages_fork(k_pages, v_pages, page_table, ref, src, seq_len, *, out_table=None, out_ref=None, workspace=None,
+                   stream=None):
+    """New row i continues row src[i] (-1: empty) of page_table, which holds seq_len[src[i]] tokens:
+    full pages are shared, a last page that is not full stays with the first row that continues
+    it and is copied for each other one (in every layer of k_pages/v_pages [n_layers,]
+    [n_pages,H_kv,page_size,d]).  out_table (not page_table itself; new if not given) and out_ref
+    (in place if not given) are written whole.  Returns (out_table, out_ref)."""
+    import torch
+
+    lib = load_library()
+    pool = _page_pool(k_pages, v_pages, page_table.device)
+    out_table = torch.empty_like(page_table) if out_table is None else out_table
+    out_ref = ref if out_ref is None else out_ref
+    t = _page_tables(page_table, ref, pool.page_size, out_table, out_ref)
+    _check_i32("src", src, (t.B,), page_table.device)
+    _check_i32("seq_len", seq_len, (t.B,), page_table.device)
+    workspace, n = _pages_workspace(lib, t, workspace, page_table.device)
+    st = lib.swa_pages_fork(ctypes.byref(t), ctypes.byref(pool), src.data_ptr(), seq_len.data_ptr(),
+                            workspace.data_ptr(), n, _stream_handle(stream))
+    if st != 0:
+        raise SwaError("swa_pages_fork", st)
+    return out_table, out_ref
+
+
+def swa_pages_compact(k_pages, v_pages, page_table, ref, *, out_table=None, out_ref=None, n_live=None, workspace=None,
+                      stream=None):
+    """Move the pool's live pages (ref > 0) to its low end, in every layer, and change page_table and
+    ref accordingly (in place unless out_table and out_ref are given).  Returns (out_table,
+    out_ref, n_live int32 [1], on the device)."""
+    import torch
+
+    lib = load_library()
+    pool = _page_pool(k_pages, v_pages, page_table.device)
+    out_table, out_ref = page_table if out_table is None else out_table, ref if out_ref is None else out_ref
+    t = _page_tables(page_table, ref, pool.page_size, out_table, out_ref)
+    n_live = torch.empty(1, dtype=torch.int32, device=page_table.device) if n_live is None else n_live
+    _check_i32("n_live", n_live, (1,), page_table.device)
+    workspace, n = _pages_workspace(lib, t, workspace, page_table.device)
+    st = lib.swa_pages_compact(ctypes.byref(t), ctypes.byref(pool), n_live.data_ptr(), workspace.data_ptr(), n,
+                               _stream_handle(stream))
+    if st != 0:
+        raise SwaError("swa_pages_compact", st)
+    return out_table, out_ref, n_live
+
+
+def swa_pages_copy(k_pages, v_pages, src, dst, *, stream=None) -> None:
+    """Copy page src[i] to page dst[i] in every layer (int32 lists; the dst distinct, none also a src)."""
+    pool = _page_pool(k_pages, v_pages, src.device)
+    if src.dim() != 1:
+        raise ValueError("src: expected int32 [n]")
+    _check_i32("src", src, src.shape, src.device)
+    _check_i32("dst", dst, src.shape, src.device)
+    st = load_library().swa_pages_copy(ctypes.byref(pool), src.data_ptr(), dst.data_ptr(), src.shape[0],
+                                       _stream_handle(stream))
+    if st != 0:
+        raise SwaError("swa_pages_copy", st)
 
 
 def swa_check_device_error(stream=None) -> None:

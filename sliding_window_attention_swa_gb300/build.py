@@ -21,7 +21,8 @@ LIB = os.path.join(BUILD, "libswa.so")
 # debug build: kernels compiled with -DSWA_DEBUG (bounds checks on every computed index)
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(BUILD_DEBUG, "libswa_debug.so")
-SOURCES = ["swa_abi.cu", "swa_band.cu", "swa_split.cu", "swa_noalloc.cu", "swa_cache.cu"]
+SOURCES = ["swa_abi.cu", "swa_band.cu", "swa_split.cu", "swa_noalloc.cu", "swa_cache.cu", "swa_paged.cu",
+           "swa_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

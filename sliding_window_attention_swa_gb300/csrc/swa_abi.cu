@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "swa_internal.h"
+#include "swa_paged.h"
 
 namespace {
 
@@ -237,6 +238,116 @@ cudaError_t launch_band_views(const swa_fwd_params *p, const swa::BandArgs &base
         g = g1;
     }
     return cudaSuccess;
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool strides2_ok(const int64_t st[2]) {
+    for (int i = 0; i < 2; ++i)
+        if (st[i] <= 0 || (st[i] % 8) != 0) return false;
+    return true;
+}
+
+swa_status paged_cache_check(const swa_paged_cache *c) {
+    if (!c || !c->k_pages || !c->v_pages || !c->page_table) return SWA_ERR_INVALID_ARG;
+    if (c->n_pages < 1 || c->page_size < 1 || c->H_kv < 1 || c->d_h < 1 || c->B < 1 || c->table_width < 1)
+        return SWA_ERR_INVALID_ARG;
+    if (!head_dim_ok(c->d_h)) return SWA_ERR_UNSUPPORTED;
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+        return SWA_ERR_UNSUPPORTED;
+    if (c->B > swa::kPagedMaxB || static_cast<int64_t>(c->table_width) * c->page_size > INT_MAX)
+        return SWA_ERR_UNSUPPORTED;
+    if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || !aligned4(c->page_table)) return SWA_ERR_UNSUPPORTED;
+    return SWA_OK;
+}
+
+// The checks that append and attention share: the batch's layout and the new rows.
+swa_status paged_rows_check(const swa_paged_params *p, const swa_paged_cache *c, bool need_new) {
+    const swa_status st = paged_cache_check(c);
+    if (st != SWA_OK) return st;
+    if (!p || !p->p0 || p->N < 0 || (!p->q_start && p->N != c->B)) return SWA_ERR_INVALID_ARG;
+    if ((p->k_new == nullptr) != (p->v_new == nullptr) || (need_new && !p->k_new)) return SWA_ERR_INVALID_ARG;
+    if (!aligned4(p->p0) || !aligned4(p->q_start)) return SWA_ERR_UNSUPPORTED;
+    if (p->k_new && (!strides2_ok(p->kn_strides) || !strides2_ok(p->vn_strides) || !aligned16(p->k_new) ||
+                     !aligned16(p->v_new)))
+        return SWA_ERR_UNSUPPORTED;
+    return SWA_OK;
+}
+
+swa_status paged_check(const swa_paged_params *p, const swa_paged_cache *c) {
+    const swa_status st = paged_rows_check(p, c, false);
+    if (st != SWA_OK) return st;
+    if (!p->q || !p->o || !p->lse || p->H_q < 1 || p->H_q % c->H_kv != 0) return SWA_ERR_INVALID_ARG;
+    if (p->max_q < 0 || p->window < 0 || p->n_sink < 0 || !std::isfinite(p->scale)) return SWA_ERR_INVALID_ARG;
+    if (p->H_q / c->H_kv > swa::kSplitRows || !scale_ok(p->scale)) return SWA_ERR_UNSUPPORTED;
+    if (!strides2_ok(p->q_strides) || !strides2_ok(p->o_strides) || !aligned16(p->q) || !aligned16(p->o) ||
+        !aligned4(p->lse) || !aligned4(p->row_counts))
+        return SWA_ERR_UNSUPPORTED;
+    return SWA_OK;
+}
+
+swa::PagedArgs paged_args(const swa_paged_params *p, const swa_paged_cache *c) {
+    swa::PagedArgs a{};
+    a.q = static_cast<const uint16_t *>(p->q);
+    a.kn = static_cast<const uint16_t *>(p->k_new);
+    a.vn = static_cast<const uint16_t *>(p->v_new);
+    a.o = static_cast<uint16_t *>(p->o);
+    for (int i = 0; i < 2; ++i) {
+        a.q_st[i] = p->q_strides[i];
+        a.kn_st[i] = p->kn_strides[i];
+        a.vn_st[i] = p->vn_strides[i];
+        a.o_st[i] = p->o_strides[i];
+    }
+    a.lse = p->lse;
+    a.counts = p->row_counts;
+    a.k_pages = static_cast<uint16_t *>(c->k_pages);
+    a.v_pages = static_cast<uint16_t *>(c->v_pages);
+    a.table = c->page_table;
+    a.p0 = p->p0;
+    a.q_start = p->q_start;
+    a.N = p->N;
+    a.B = c->B;
+    a.width = c->table_width;
+    a.n_pages = c->n_pages;
+    a.ps = c->page_size;
+    while ((1 << a.ps_log2) < a.ps) ++a.ps_log2;
+    a.H_q = p->H_q;
+    a.H_kv = c->H_kv;
+    a.G = p->H_q / c->H_kv;
+    a.D = c->d_h;
+    a.window = p->window > 0 ? p->window : INT_MAX;
+    a.n_sink = p->n_sink;
+    a.max_q = p->max_q;
+    a.scale_log2 = p->scale * kLog2e;
+    return a;
+}
+
+enum class InPlace { kNo, kYes, kEither };
+swa_status tables_check(const swa_page_tables *t, InPlace ip) {
+    if (!t || !t->table || !t->ref || !t->out_table || !t->out_ref) return SWA_ERR_INVALID_ARG;
+    if (t->B < 1 || t->width < 1 || t->n_pages < 1 || t->page_size < 1) return SWA_ERR_INVALID_ARG;
+    const bool same_t = t->out_table == t->table, same_r = t->out_ref == t->ref;
+    if (ip == InPlace::kYes && !(same_t && same_r)) return SWA_ERR_INVALID_ARG;
+    if (ip == InPlace::kNo && same_t) return SWA_ERR_INVALID_ARG;
+    if (ip == InPlace::kEither && same_t != same_r) return SWA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(t->width) * t->page_size > INT_MAX || static_cast<int64_t>(t->B) * t->width > INT_MAX)
+        return SWA_ERR_UNSUPPORTED;
+    if (!aligned4(t->table) || !aligned4(t->ref) || !aligned4(t->out_table) || !aligned4(t->out_ref))
+        return SWA_ERR_UNSUPPORTED;
+    return SWA_OK;
+}
+
+swa_status pool_check(const swa_page_pool *p, const swa_page_tables *t) {
+    if (!p || !p->k_pages || !p->v_pages) return SWA_ERR_INVALID_ARG;
+    if (p->n_layers < 1 || p->n_pages < 1 || p->H_kv < 1 || p->page_size < 1 || p->d_h < 1) return SWA_ERR_INVALID_ARG;
+    if (t && (t->n_pages != p->n_pages || t->page_size != p->page_size)) return SWA_ERR_INVALID_ARG;
+    // one page of one layer, and the (layer, keys or values, head) units of a page, count in 32 bits
+    const int64_t page = static_cast<int64_t>(p->H_kv) * p->page_size;
+    if (p->d_h % 8 != 0 || page > INT_MAX / p->d_h || static_cast<int64_t>(p->n_layers) * 2 > INT_MAX / p->H_kv)
+        return SWA_ERR_UNSUPPORTED;
+    if (p->n_layers > 1 && (p->layer_stride % 8 != 0 || p->layer_stride / p->n_pages < page * p->d_h))
+        return p->layer_stride % 8 != 0 ? SWA_ERR_UNSUPPORTED : SWA_ERR_INVALID_ARG;
+    if (!aligned16(p->k_pages) || !aligned16(p->v_pages)) return SWA_ERR_UNSUPPORTED;
+    return SWA_OK;
 }
 
 }  // namespace
@@ -594,13 +705,108 @@ swa_status swa_prefill_chunk(const swa_chunk_params *p, const swa_cache_params *
     return SWA_OK;
 }
 
+size_t swa_paged_workspace_size(const swa_paged_params *p, const swa_paged_cache *c) {
+    if (paged_check(p, c) != SWA_OK) return 0;
+    return swa::paged_workspace_bytes(paged_args(p, c));
+}
+
+swa_status swa_paged_attend(const swa_paged_params *p, const swa_paged_cache *c, void *workspace,
+                            size_t workspace_bytes, swa_stream_t stream) {
+    swa_status st = paged_check(p, c);
+    if (st != SWA_OK) return st;
+    const swa::PagedArgs a = paged_args(p, c);
+    st = workspace_ok(workspace, workspace_bytes, swa::paged_workspace_bytes(a));
+    if (st != SWA_OK || a.N == 0) return st;
+    if (failed(swa::launch_paged_attend(a, workspace, reinterpret_cast<cudaStream_t>(stream)))) return SWA_ERR_CUDA;
+    return SWA_OK;
+}
+
+swa_status swa_paged_append(const swa_paged_params *p, const swa_paged_cache *c, swa_stream_t stream) {
+    const swa_status st = paged_rows_check(p, c, true);
+    if (st != SWA_OK || p->N == 0) return st;
+    if (failed(swa::launch_paged_append(paged_args(p, c), reinterpret_cast<cudaStream_t>(stream)))) return SWA_ERR_CUDA;
+    return SWA_OK;
+}
+
+size_t swa_pages_workspace_size(const swa_page_tables *t) {
+    // (the same for every call: whether the tables are in place does not matter here)
+    if (tables_check(t, InPlace::kNo) != SWA_OK && tables_check(t, InPlace::kEither) != SWA_OK) return 0;
+    return swa::pages_workspace_bytes(t);
+}
+
+swa_status swa_pages_reserve(const swa_page_tables *t, const int32_t *first, const int32_t *end, void *workspace,
+                             size_t workspace_bytes, swa_stream_t stream) {
+    swa_status st = tables_check(t, InPlace::kYes);
+    if (st != SWA_OK) return st;
+    if (!first || !end) return SWA_ERR_INVALID_ARG;
+    if (!aligned4(first) || !aligned4(end)) return SWA_ERR_UNSUPPORTED;
+    st = workspace_ok(workspace, workspace_bytes, swa::pages_workspace_bytes(t));
+    if (st != SWA_OK) return st;
+    if (failed(swa::launch_reserve(t, first, end, workspace, reinterpret_cast<cudaStream_t>(stream))))
+        return SWA_ERR_CUDA;
+    return SWA_OK;
+}
+
+swa_status swa_pages_free(const swa_page_tables *t, const int32_t *below, int32_t n_sink, swa_stream_t stream) {
+    const swa_status st = tables_check(t, InPlace::kEither);
+    if (st != SWA_OK) return st;
+    if (!below || n_sink < 0) return SWA_ERR_INVALID_ARG;
+    if (!aligned4(below)) return SWA_ERR_UNSUPPORTED;
+    if (failed(swa::launch_free(t, below, n_sink, reinterpret_cast<cudaStream_t>(stream)))) return SWA_ERR_CUDA;
+    return SWA_OK;
+}
+
+swa_status swa_pages_fork(const swa_page_tables *t, const swa_page_pool *pool, const int32_t *src, const int32_t *len,
+                          void *workspace, size_t workspace_bytes, swa_stream_t stream) {
+    swa_status st = tables_check(t, InPlace::kNo);
+    if (st == SWA_OK) st = pool_check(pool, t);
+    if (st != SWA_OK) return st;
+    if (!src || !len) return SWA_ERR_INVALID_ARG;
+    if (!aligned4(src) || !aligned4(len)) return SWA_ERR_UNSUPPORTED;
+    st = workspace_ok(workspace, workspace_bytes, swa::pages_workspace_bytes(t));
+    if (st != SWA_OK) return st;
+    if (failed(swa::launch_fork(t, pool, src, len, workspace, reinterpret_cast<cudaStream_t>(stream))))
+        return SWA_ERR_CUDA;
+    return SWA_OK;
+}
+
+swa_status swa_pages_compact(const swa_page_tables *t, const swa_page_pool *pool, int32_t *n_live, void *workspace,
+                             size_t workspace_bytes, swa_stream_t stream) {
+    swa_status st = tables_check(t, InPlace::kEither);
+    if (st == SWA_OK) st = pool_check(pool, t);
+    if (st != SWA_OK) return st;
+    if (!n_live) return SWA_ERR_INVALID_ARG;
+    if (!aligned4(n_live)) return SWA_ERR_UNSUPPORTED;
+    st = workspace_ok(workspace, workspace_bytes, swa::pages_workspace_bytes(t));
+    if (st != SWA_OK) return st;
+    if (failed(swa::launch_compact(t, pool, n_live, workspace, reinterpret_cast<cudaStream_t>(stream))))
+        return SWA_ERR_CUDA;
+    return SWA_OK;
+}
+
+swa_status swa_pages_copy(const swa_page_pool *pool, const int32_t *src, const int32_t *dst, int32_t n,
+                          swa_stream_t stream) {
+    const swa_status st = pool_check(pool, nullptr);
+    if (st != SWA_OK) return st;
+    if (n < 0 || (n > 0 && (!src || !dst))) return SWA_ERR_INVALID_ARG;
+    if (n == 0) return SWA_OK;
+    if (!aligned4(src) || !aligned4(dst)) return SWA_ERR_UNSUPPORTED;
+    if (failed(swa::launch_page_copy(pool, src, dst, n, reinterpret_cast<cudaStream_t>(stream)))) return SWA_ERR_CUDA;
+    return SWA_OK;
+}
+
 swa_status swa_read_device_errors(swa_stream_t stream, swa_device_errors *out) {
     if (out) *out = swa_device_errors{};
     if (failed(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)))) return SWA_ERR_CUDA;
     swa_device_errors e;
     e.prefill = swa::band_read_clear_error();
     e.split = swa::split_read_clear_error();
-    e.cache = swa::cache_read_clear_error();
+    e.cache = swa::cache_read_clear_error() | swa::pages_read_clear_error();
+    unsigned int data, split, prefill;
+    swa::paged_read_clear_error(&data, &split, &prefill);
+    e.cache |= data;
+    e.split |= split;
+    e.prefill |= prefill;
     if (out) *out = e;
     constexpr uint32_t kTimeout = SWA_DEVERR_WAIT_TIMEOUT | SWA_DEVERR_DRAIN_TIMEOUT;
     if ((e.prefill | e.split) & kTimeout) return SWA_ERR_TIMEOUT;

@@ -1,0 +1,51 @@
+// swa_paged.h -- host-side interface of the paged cache's translation units
+// (swa_paged.cu, swa_pages.cu) to the C ABI.  Not installed.
+#pragma once
+
+#include "swa_internal.h"
+
+namespace swa {
+
+// One call of swa_paged_attend / swa_paged_append, as the kernels take it.
+struct PagedArgs {
+    const uint16_t *q;  // [N, H_q, D] bf16 bits; element strides of (token, head)
+    int64_t q_st[2];
+    const uint16_t *kn, *vn;  // [N, H_kv, D] (append) or nullptr
+    int64_t kn_st[2], vn_st[2];
+    uint16_t *o;
+    int64_t o_st[2];
+    float *lse;       // [N, H_q]
+    int32_t *counts;  // [N, H_q] or nullptr
+    uint16_t *k_pages, *v_pages;  // [n_pages, H_kv, ps, D]
+    const int32_t *table;         // [B, width]
+    const int32_t *p0;            // [B]
+    const int32_t *q_start;       // [B + 1] or nullptr (one token a sequence)
+    int N, B, width, n_pages, ps, ps_log2, H_q, H_kv, G, D;
+    int window;  // INT_MAX: none
+    int n_sink;
+    int max_q;  // 0: not known
+    float scale_log2;
+};
+
+constexpr int kPagedMaxB = 8192;
+
+int paged_sm_count();  // SMs of the current device
+size_t paged_workspace_bytes(const PagedArgs &a);
+cudaError_t launch_paged_append(const PagedArgs &a, cudaStream_t s);
+cudaError_t launch_paged_attend(const PagedArgs &a, void *ws, cudaStream_t s);
+// Errors of the data (cache word), of the few-row and of the many-row kernels.
+void paged_read_clear_error(unsigned int *data, unsigned int *split, unsigned int *prefill);
+
+size_t pages_workspace_bytes(const swa_page_tables *t);
+cudaError_t launch_reserve(const swa_page_tables *t, const int32_t *first, const int32_t *end, void *ws,
+                           cudaStream_t s);
+cudaError_t launch_free(const swa_page_tables *t, const int32_t *below, int n_sink, cudaStream_t s);
+cudaError_t launch_fork(const swa_page_tables *t, const swa_page_pool *pool, const int32_t *src, const int32_t *len,
+                        void *ws, cudaStream_t s);
+cudaError_t launch_compact(const swa_page_tables *t, const swa_page_pool *pool, int32_t *n_live, void *ws,
+                           cudaStream_t s);
+cudaError_t launch_page_copy(const swa_page_pool *pool, const int32_t *src, const int32_t *dst, int n,
+                             cudaStream_t s);
+unsigned int pages_read_clear_error();
+
+}  // namespace swa

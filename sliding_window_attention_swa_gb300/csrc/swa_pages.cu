@@ -1,0 +1,529 @@
+// swa_pages.cu -- the pages of a paged KV cache: reserving, giving back, forking,
+// compacting and copying them, with the page tables and the holders' counts.
+//
+// A page is free when its count is 0.  Free pages are always taken lowest index first, by
+// rank: the r-th page wanted (in the order of rows, then entries) is the r-th free one.
+// Counts change by integer atomics, whose order cannot show in a result.
+//
+// Tables and counts are small beside the pages: they are bound by launches and latency.  The
+// copies of page contents are bound by HBM (2 bytes moved per byte of page).
+#include <climits>
+
+#include "ptx.cuh"
+#include "swa_paged.h"
+
+namespace swa {
+namespace {
+
+__device__ unsigned int g_pages_err = 0;
+constexpr unsigned int kErrBadPosition = SWA_DEVERR_BAD_POSITION, kErrBadPage = SWA_DEVERR_BAD_PAGE,
+                       kErrNoPage = SWA_DEVERR_NO_PAGE, kErrBadRef = SWA_DEVERR_BAD_REF;
+
+constexpr int kThreads = 256;
+constexpr int kScanThreads = 1024, kScanWarps = kScanThreads / 32;
+constexpr int kScanItems = 16;  // counts per thread and scan step: as many loads in flight
+constexpr int kUnroll = 8;      // 16-byte loads in flight per thread of the page copy
+
+// One page copy: the first `rows` positions of page src go to page dst (src < 0: none).
+// ref: the moved page's holders (compaction).
+struct Move {
+    int32_t src, dst, rows, ref;
+};
+
+struct TableArgs {
+    const int32_t *table, *ref;
+    int32_t *out_table, *out_ref;
+    int B, width, n_pages, ps;
+};
+
+// ---------------------------------------------------------------------------------------------
+// ranks of the marked items of a list, one block of kScanThreads
+// ---------------------------------------------------------------------------------------------
+struct ScanSmem {
+    int cnt[kScanItems * kScanWarps];
+    int total;
+};
+
+// One step over items base .. base + kScanItems * kScanThreads - 1 (item base + k * kScanThreads
+// + tid is this thread's k-th, so loads are coalesced whatever the list's alignment).  mark(p)
+// tells whether item p counts; put(p, rank) is called for each that does, ranks starting at
+// `before`.  Returns the number of marked items up to the end of the step.
+template <class Mark, class Put>
+__device__ __forceinline__ int scan_step(ScanSmem &sm, int64_t base, int64_t n, int before, Mark mark, Put put) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    unsigned bal[kScanItems];
+    bool m[kScanItems];
+#pragma unroll
+    for (int k = 0; k < kScanItems; ++k) {
+        const int64_t p = base + static_cast<int64_t>(k) * kScanThreads + tid;
+        m[k] = p < n && mark(static_cast<int>(p));
+    }
+#pragma unroll
+    for (int k = 0; k < kScanItems; ++k) {
+        bal[k] = __ballot_sync(0xffffffffu, m[k]);
+        if (lane == 0) sm.cnt[k * kScanWarps + warp] = __popc(bal[k]);
+    }
+    __syncthreads();
+    if (warp == 0) {  // exclusive prefix of the kScanItems * kScanWarps counts
+        constexpr int kPer = kScanItems * kScanWarps / 32;
+        int v[kPer], s = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            v[i] = s;
+            s += sm.cnt[lane * kPer + i];
+        }
+        int inc = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += t;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sm.cnt[lane * kPer + i] = v[i] + inc - s;
+        if (lane == 31) sm.total = inc;
+    }
+    __syncthreads();
+    const int total = sm.total;
+#pragma unroll
+    for (int k = 0; k < kScanItems; ++k)
+        if (m[k])
+            put(static_cast<int>(base + static_cast<int64_t>(k) * kScanThreads + tid),
+                before + sm.cnt[k * kScanWarps + warp] + __popc(bal[k] & ((1u << lane) - 1u)));
+    __syncthreads();  // the counts are rewritten by the next step
+    return before + total;
+}
+
+// The `need` lowest free pages into list[0 ..]; returns how many there are (at most need).
+__device__ __forceinline__ int take_free(ScanSmem &sm, const int32_t *ref, int n_pages, int need, int32_t *list) {
+    int found = 0;
+    for (int64_t base = 0; base < n_pages && found < need; base += kScanItems * kScanThreads)
+        found = scan_step(
+            sm, base, n_pages, found, [&](int p) { return ref[p] == 0; },
+            [&](int p, int r) {
+                if (r < need) list[r] = p;
+            });
+    return min(found, need);
+}
+
+__global__ void __launch_bounds__(kThreads) copy_i32_kernel(const int32_t *src, int32_t *dst, int64_t n) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * kThreads)
+        dst[i] = src[i];
+}
+
+// ---------------------------------------------------------------------------------------------
+// reserve: one block.  ws_row [B]: first rank of each row; list [n_pages]: the pages taken.
+// ---------------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(kScanThreads) reserve_kernel(const TableArgs a, const int32_t *first,
+                                                               const int32_t *end, int32_t *ws_row, int32_t *list) {
+    __shared__ ScanSmem sm;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t cap = static_cast<int64_t>(a.width) * a.ps;
+    // entries [j0, j1) of row b are wanted
+    auto range = [&](int b, int &j0, int &j1) {
+        const int64_t f = first[b], e = end[b];
+        j0 = j1 = 0;
+        if (e <= f) return true;
+        if (f < 0 || e > cap) return false;
+        j0 = static_cast<int>(f / a.ps);
+        j1 = static_cast<int>((e + a.ps - 1) / a.ps);
+        return true;
+    };
+    auto missing = [&](int b, int j) {
+        const int e = a.out_table[static_cast<int64_t>(b) * a.width + j];
+        return e < 0 || e >= a.n_pages;
+    };
+    // 1. pages that each row lacks (a warp per row)
+    for (int b = warp; b < a.B; b += kScanWarps) {
+        int j0, j1, n = 0;
+        if (!range(b, j0, j1) && lane == 0) atomicOr(&g_pages_err, kErrBadPosition);
+        for (int j = j0 + lane; j < j1; j += 32) {
+            if (!missing(b, j)) continue;
+            if (a.out_table[static_cast<int64_t>(b) * a.width + j] >= a.n_pages) atomicOr(&g_pages_err, kErrBadPage);
+            ++n;
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) ws_row[b] = n;
+    }
+    __syncthreads();
+    // 2. each row's first rank: an exclusive prefix over the rows
+    __shared__ int wsum[kScanWarps];
+    int total = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kScanThreads) {
+        const int b = b0 + tid;
+        const int n = b < a.B ? ws_row[b] : 0;
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += t;
+        }
+        if (lane == 31) wsum[warp] = inc;
+        __syncthreads();
+        int before = 0, all = 0;
+        for (int w = 0; w < kScanWarps; ++w) {
+            if (w < warp) before += wsum[w];
+            all += wsum[w];
+        }
+        if (b < a.B) ws_row[b] = total + before + inc - n;
+        total += all;
+        __syncthreads();
+    }
+    if (total == 0) return;
+    // 3. the lowest free pages, 4. dealt to the rows in order
+    const int found = take_free(sm, a.out_ref, a.n_pages, min(total, a.n_pages), list);
+    __syncthreads();
+    for (int b = warp; b < a.B; b += kScanWarps) {
+        int j0, j1;
+        range(b, j0, j1);
+        int rank = ws_row[b];
+        for (int jb = j0; jb < j1; jb += 32) {
+            const int j = jb + lane;
+            const bool want = j < j1 && missing(b, j);
+            const unsigned bal = __ballot_sync(0xffffffffu, want);
+            if (want) {
+                const int r = rank + __popc(bal & ((1u << lane) - 1u));
+                int page = -1;
+                if (r < found) {
+                    page = list[r];
+                    a.out_ref[page] = 1;
+                } else {
+                    atomicOr(&g_pages_err, kErrNoPage);
+                }
+                a.out_table[static_cast<int64_t>(b) * a.width + j] = page;
+            }
+            rank += __popc(bal);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// free: every entry once
+// ---------------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(kThreads) free_kernel(const TableArgs a, const int32_t *below, int n_sink) {
+    const uint32_t n = static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.width);  // < 2^31
+    for (uint32_t x = blockIdx.x * kThreads + threadIdx.x; x < n; x += gridDim.x * kThreads) {
+        const int b = static_cast<int>(x / static_cast<uint32_t>(a.width));
+        const int64_t j = x - static_cast<uint32_t>(b) * static_cast<uint32_t>(a.width);
+        int e = a.table[x];
+        const int bl = __ldg(below + b);
+        if (e >= a.n_pages) {
+            atomicOr(&g_pages_err, kErrBadPage);
+            e = -1;
+        }
+        if (e >= 0 && (bl < 0 || ((j + 1) * a.ps <= bl && j * a.ps >= n_sink))) {
+            if (atomicSub(a.out_ref + e, 1) <= 0) {
+                atomicAdd(a.out_ref + e, 1);
+                atomicOr(&g_pages_err, kErrBadRef);
+            }
+            e = -1;
+        }
+        a.out_table[x] = e < 0 ? -1 : e;
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// fork
+// ---------------------------------------------------------------------------------------------
+// The row that row i continues and its tokens (-1, 0: none).
+__device__ __forceinline__ bool fork_source(const TableArgs &a, const int32_t *src, const int32_t *len, int i, int &s,
+                                            int &n) {
+    s = src[i];
+    n = 0;
+    if (s < 0) return s == -1;
+    if (s >= a.B) {
+        s = -1;
+        return false;
+    }
+    n = len[s];
+    if (n < 0 || n > static_cast<int64_t>(a.width) * a.ps) {
+        s = -1;
+        n = 0;
+        return false;
+    }
+    return true;
+}
+
+// Rows' tables and the holders of everything but the fresh pages.  Block (x, i): a stretch of
+// row i; an entry that both tables have at the same place keeps its holder (no atomics).
+// pend[i]: row i wants a page of its own.
+__global__ void __launch_bounds__(kThreads) fork_table_kernel(const TableArgs a, const int32_t *src,
+                                                              const int32_t *len, int32_t *pend) {
+    for (int i = blockIdx.y; i < a.B; i += gridDim.y) {
+        int s, n;
+        const bool ok = fork_source(a, src, len, i, s, n);
+        if (!ok && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(&g_pages_err, kErrBadPosition);
+        const int part = n % a.ps, last = n / a.ps, used = last + (part ? 1 : 0);
+        // the lowest row that continues s keeps its last page
+        int other = 0;
+        if (s >= 0 && part)
+            for (int k = threadIdx.x; k < i && !other; k += kThreads) other = src[k] == s;
+        const bool copies = __syncthreads_or(other) != 0;
+        if (blockIdx.x == 0 && threadIdx.x == 0) pend[i] = copies ? 1 : 0;
+        for (int j = blockIdx.x * kThreads + threadIdx.x; j < a.width; j += gridDim.x * kThreads) {
+            int in = a.table[static_cast<int64_t>(i) * a.width + j];
+            int out = s >= 0 && j < used ? a.table[static_cast<int64_t>(s) * a.width + j] : -1;
+            if (in >= a.n_pages || out >= a.n_pages) {
+                atomicOr(&g_pages_err, kErrBadPage);
+                in = in >= a.n_pages ? -1 : in;
+                out = out >= a.n_pages ? -1 : out;
+            }
+            if (copies && j == last) out = -1;
+            a.out_table[static_cast<int64_t>(i) * a.width + j] = out < 0 ? -1 : out;
+            if (in != out) {
+                if (in >= 0) atomicSub(a.out_ref + in, 1);
+                if (out >= 0) atomicAdd(a.out_ref + out, 1);
+            }
+        }
+    }
+}
+
+// One block: fresh pages for the rows that want one, lowest first in the order of the rows.
+__global__ void __launch_bounds__(kScanThreads) fork_alloc_kernel(const TableArgs a, const int32_t *src,
+                                                                  const int32_t *len, const int32_t *pend,
+                                                                  int32_t *row_of, int32_t *list, Move *moves,
+                                                                  int32_t *n_moves) {
+    __shared__ ScanSmem sm;
+    int want = 0;
+    for (int64_t base = 0; base < a.B; base += kScanItems * kScanThreads)
+        want = scan_step(
+            sm, base, a.B, want, [&](int i) { return pend[i] != 0; }, [&](int i, int r) { row_of[r] = i; });
+    const int found = want ? take_free(sm, a.out_ref, a.n_pages, min(want, a.n_pages), list) : 0;
+    __syncthreads();
+    for (int r = threadIdx.x; r < want; r += kScanThreads) {
+        const int i = row_of[r], s = src[i], n = len[s], last = n / a.ps;
+        const int old = a.table[static_cast<int64_t>(s) * a.width + last];
+        Move m{-1, -1, n % a.ps, 0};
+        if (r < found) {
+            m.dst = list[r];
+            a.out_ref[m.dst] = 1;
+            a.out_table[static_cast<int64_t>(i) * a.width + last] = m.dst;
+            if (old >= 0 && old < a.n_pages) m.src = old;
+            else atomicOr(&g_pages_err, kErrBadPage);
+        } else {
+            atomicOr(&g_pages_err, kErrNoPage);
+        }
+        moves[r] = m;
+    }
+    if (threadIdx.x == 0) *n_moves = want;
+}
+
+// ---------------------------------------------------------------------------------------------
+// compact
+// ---------------------------------------------------------------------------------------------
+// One block: M, the holes below it and the live pages at or above it by rank, and their pairing.
+// to[p]: where live page p >= M goes.
+__global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const TableArgs a, int32_t *holes, int32_t *movers,
+                                                                    int32_t *to, Move *moves, int32_t *n_moves,
+                                                                    int32_t *n_live) {
+    __shared__ ScanSmem sm;
+    int live = 0;
+    for (int64_t base = 0; base < a.n_pages; base += kScanItems * kScanThreads)
+        live = scan_step(sm, base, a.n_pages, live, [&](int p) { return a.ref[p] > 0; }, [](int, int) {});
+    int nh = 0, nm = 0;
+    for (int64_t base = 0; base < live; base += kScanItems * kScanThreads)
+        nh = scan_step(sm, base, live, nh, [&](int p) { return a.ref[p] <= 0; }, [&](int p, int r) { holes[r] = p; });
+    for (int64_t base = live; base < a.n_pages; base += kScanItems * kScanThreads)
+        nm = scan_step(
+            sm, base, a.n_pages, nm,
+            [&](int p) {
+                to[p] = -1;  // (a table entry may wrongly name a free page)
+                return a.ref[p] > 0;
+            },
+            [&](int p, int r) { movers[r] = p; });
+    __syncthreads();
+    for (int r = threadIdx.x; r < nm; r += kScanThreads) {  // nh == nm: as many holes below M as live pages above
+        const int s = movers[r], d = holes[r];
+        to[s] = d;
+        moves[r] = Move{s, d, a.ps, a.ref[s]};
+    }
+    if (threadIdx.x == 0) {
+        *n_moves = nm;
+        *n_live = live;
+    }
+}
+
+// Tables and counts after the moves.  Each count is written by one thread, from values that no
+// other thread writes (a hole's from its move), so the call may be in place.
+__global__ void __launch_bounds__(kThreads) compact_apply_kernel(const TableArgs a, const int32_t *to,
+                                                                 const Move *moves, const int32_t *n_moves,
+                                                                 const int32_t *n_live) {
+    const int nm = *n_moves, live = *n_live;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    for (int64_t x = t0; x < static_cast<int64_t>(a.B) * a.width; x += step) {
+        int e = a.table[x];
+        const bool named = e >= 0;
+        if (e >= live) e = e < a.n_pages ? to[e] : -1;
+        if (named && e < 0) atomicOr(&g_pages_err, kErrBadPage);
+        a.out_table[x] = e < 0 ? -1 : e;
+    }
+    for (int64_t p = t0; p < a.n_pages; p += step) {
+        if (p >= live) a.out_ref[p] = 0;
+        else if (a.ref != a.out_ref && a.ref[p] > 0) a.out_ref[p] = a.ref[p];
+    }
+    for (int64_t r = t0; r < nm; r += step) a.out_ref[moves[r].dst] = moves[r].ref;
+}
+
+// ---------------------------------------------------------------------------------------------
+// contents
+// ---------------------------------------------------------------------------------------------
+struct PoolArgs {
+    uint4 *pool[2];        // keys, values
+    int64_t layer_stride;  // 16-byte pieces from one layer to the next
+    int L, H, n_pages, ps, row;  // row: pieces of one position
+};
+
+// A warp per (move, layer, keys or values, head): rows * row consecutive pieces of both pages.
+template <bool kPairs>
+__global__ void __launch_bounds__(kThreads) move_kernel(const PoolArgs a, const Move *moves, const int32_t *n_moves,
+                                                        const int32_t *src, const int32_t *dst, int n_pairs) {
+    const int lane = threadIdx.x & 31;
+    const int n = kPairs ? n_pairs : *n_moves;
+    const int inner = a.L * 2 * a.H;
+    const int64_t units = static_cast<int64_t>(n) * inner;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+    for (int64_t u = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5; u < units; u += step) {
+        const int r = static_cast<int>(u / inner), x = static_cast<int>(u - static_cast<int64_t>(r) * inner);
+        const int h = x % a.H, kv = (x / a.H) & 1, l = x / (2 * a.H);
+        const Move m = kPairs ? Move{__ldg(src + r), __ldg(dst + r), a.ps, 0} : moves[r];
+        const bool bad = m.src < 0 || m.src >= a.n_pages || m.dst < 0 || m.dst >= a.n_pages;
+        if (bad) {
+            if (kPairs && x == 0 && lane == 0) atomicOr(&g_pages_err, kErrBadPage);
+            continue;
+        }
+        const int64_t head = static_cast<int64_t>(a.ps) * a.row, page = head * a.H;
+        uint4 *base = a.pool[kv] + l * a.layer_stride + h * head;
+        const uint4 *s = base + m.src * page;
+        uint4 *d = base + m.dst * page;
+        const int pieces = m.rows * a.row;
+        for (int i0 = lane; i0 < pieces; i0 += 32 * kUnroll) {
+            uint4 v[kUnroll];
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k)
+                if (i0 + 32 * k < pieces) v[k] = s[i0 + 32 * k];
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k)
+                if (i0 + 32 * k < pieces) d[i0 + 32 * k] = v[k];
+        }
+    }
+}
+
+TableArgs table_args(const swa_page_tables *t) {
+    return TableArgs{t->table, t->ref, t->out_table, t->out_ref, t->B, t->width, t->n_pages, t->page_size};
+}
+PoolArgs pool_args(const swa_page_pool *p) {
+    PoolArgs a{};
+    a.pool[0] = static_cast<uint4 *>(p->k_pages);
+    a.pool[1] = static_cast<uint4 *>(p->v_pages);
+    a.layer_stride = p->layer_stride / 8;
+    a.L = p->n_layers;
+    a.H = p->H_kv;
+    a.n_pages = p->n_pages;
+    a.ps = p->page_size;
+    a.row = p->d_h / 8;
+    return a;
+}
+int grid_for(int64_t n, int per_sm) {
+    const int64_t blocks = (n + kThreads - 1) / kThreads, cap = static_cast<int64_t>(paged_sm_count()) * per_sm;
+    return static_cast<int>(blocks < cap ? (blocks > 0 ? blocks : 1) : cap);
+}
+// The workspace: ints [2 * B], [3 * n_pages], moves [max(B, n_pages)], a count.
+struct PagesWs {
+    int32_t *rows0, *rows1, *list0, *list1, *list2, *count;
+    Move *moves;
+};
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+size_t moves_of(const swa_page_tables *t) { return t->B > t->n_pages ? t->B : t->n_pages; }
+PagesWs carve(const swa_page_tables *t, void *ws) {
+    char *p = static_cast<char *>(ws);
+    PagesWs w;
+    w.count = reinterpret_cast<int32_t *>(p);
+    p += 256;
+    w.moves = reinterpret_cast<Move *>(p);
+    p += up256(moves_of(t) * sizeof(Move));
+    w.rows0 = reinterpret_cast<int32_t *>(p);
+    w.rows1 = w.rows0 + t->B;
+    w.list0 = w.rows1 + t->B;
+    w.list1 = w.list0 + t->n_pages;
+    w.list2 = w.list1 + t->n_pages;
+    return w;
+}
+cudaError_t copy_ref(const TableArgs &a, cudaStream_t s) {
+    if (a.ref == a.out_ref) return cudaSuccess;
+    copy_i32_kernel<<<grid_for(a.n_pages, 8), kThreads, 0, s>>>(a.ref, a.out_ref, a.n_pages);
+    return cudaGetLastError();
+}
+cudaError_t launch_moves(const swa_page_pool *p, const PagesWs &w, int64_t most, cudaStream_t s) {
+    const PoolArgs a = pool_args(p);
+    const int64_t units = most * a.L * 2 * a.H;
+    move_kernel<false><<<grid_for(units * 32, 8), kThreads, 0, s>>>(a, w.moves, w.count, nullptr, nullptr, 0);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t pages_workspace_bytes(const swa_page_tables *t) {
+    return 256 + up256(moves_of(t) * sizeof(Move)) +
+           up256((2 * static_cast<size_t>(t->B) + 3 * static_cast<size_t>(t->n_pages)) * sizeof(int32_t));
+}
+
+cudaError_t launch_reserve(const swa_page_tables *t, const int32_t *first, const int32_t *end, void *ws,
+                           cudaStream_t s) {
+    const PagesWs w = carve(t, ws);
+    reserve_kernel<<<1, kScanThreads, 0, s>>>(table_args(t), first, end, w.rows0, w.list0);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_free(const swa_page_tables *t, const int32_t *below, int n_sink, cudaStream_t s) {
+    const TableArgs a = table_args(t);
+    cudaError_t e = copy_ref(a, s);
+    if (e != cudaSuccess) return e;
+    free_kernel<<<grid_for(static_cast<int64_t>(a.B) * a.width, 8), kThreads, 0, s>>>(a, below, n_sink);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_fork(const swa_page_tables *t, const swa_page_pool *pool, const int32_t *src, const int32_t *len,
+                        void *ws, cudaStream_t s) {
+    const TableArgs a = table_args(t);
+    const PagesWs w = carve(t, ws);
+    cudaError_t e = copy_ref(a, s);
+    if (e != cudaSuccess) return e;
+    const int gx = (a.width + kThreads - 1) / kThreads;
+    fork_table_kernel<<<dim3(gx < 64 ? gx : 64, a.B < 65535 ? a.B : 65535), kThreads, 0, s>>>(a, src, len, w.rows0);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    fork_alloc_kernel<<<1, kScanThreads, 0, s>>>(a, src, len, w.rows0, w.rows1, w.list0, w.moves, w.count);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_moves(pool, w, a.B, s);
+}
+
+cudaError_t launch_compact(const swa_page_tables *t, const swa_page_pool *pool, int32_t *n_live, void *ws,
+                           cudaStream_t s) {
+    const TableArgs a = table_args(t);
+    const PagesWs w = carve(t, ws);
+    compact_plan_kernel<<<1, kScanThreads, 0, s>>>(a, w.list0, w.list1, w.list2, w.moves, w.count, n_live);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int64_t entries = static_cast<int64_t>(a.B) * a.width;
+    compact_apply_kernel<<<grid_for(entries > a.n_pages ? entries : a.n_pages, 8), kThreads, 0, s>>>(
+        a, w.list2, w.moves, w.count, n_live);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_moves(pool, w, a.n_pages / 2 + 1, s);
+}
+
+cudaError_t launch_page_copy(const swa_page_pool *pool, const int32_t *src, const int32_t *dst, int n,
+                             cudaStream_t s) {
+    const PoolArgs a = pool_args(pool);
+    const int64_t units = static_cast<int64_t>(n) * a.L * 2 * a.H;
+    move_kernel<true><<<grid_for(units * 32, 8), kThreads, 0, s>>>(a, nullptr, nullptr, src, dst, n);
+    return cudaGetLastError();
+}
+
+unsigned int pages_read_clear_error() {
+    unsigned int v = 0, z = 0;
+    if (cudaMemcpyFromSymbol(&v, g_pages_err, sizeof v) != cudaSuccess) return 0;
+    cudaMemcpyToSymbol(g_pages_err, &z, sizeof z);
+    return v;
+}
+
+}  // namespace swa

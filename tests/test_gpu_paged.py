@@ -1,0 +1,328 @@
+"""Attention of ragged batches of new tokens over a paged cache, and the append that stores them,
+against a plain 64-bit computation (every row; counts exact; see paged_reference.check for
+the bounds)."""
+import pytest
+import torch
+
+import paged_reference as R
+
+pytestmark = pytest.mark.gpu
+
+
+def run(swa, x, append=False, want_counts=True, **kw):
+    """The call on batch x, checked against the reference; returns (o, lse, counts, k_pages, v_pages)."""
+    k, v = x.without_new() if append else (x.k_pages, x.v_pages)
+    k, v = k.cuda(), v.cuda()
+    o = torch.full((x.N, x.Hq, x.D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((x.N, x.Hq), 7.0, device="cuda")
+    cnt = torch.full((x.N, x.Hq), 7, dtype=torch.int32, device="cuda") if want_counts else None
+    if append:
+        kw.update(k_new=x.k_new.cuda(), v_new=x.v_new.cuda())
+    kw.setdefault("q_start", x.q_start.cuda())
+    swa.swa_paged_attend(x.q.cuda(), k, v, x.table.cuda(), x.p0.cuda(), x.window, n_sink=x.n_sink, o=o, lse=lse,
+                         row_counts=cnt, **kw)
+    swa.swa_check_device_error()
+    verify(x, o, lse, cnt)
+    return o, lse, cnt, k, v
+
+
+def verify(x, o, lse, cnt, skip=()):
+    mine = torch.zeros(x.N, dtype=torch.bool)
+    for b, q0, n in x.rows():
+        if b in skip:
+            continue
+        mine[q0:q0 + n] = True
+        R.check(o[q0:q0 + n], lse[q0:q0 + n], None if cnt is None else cnt[q0:q0 + n], x.reference(b), f"sequence {b}")
+    rest = ~mine
+    assert (o.cpu()[rest] == 7).all() and (lse.cpu()[rest] == 7).all(), "rows of no sequence were written"
+    assert cnt is None or (cnt.cpu()[rest] == 7).all()
+
+
+@pytest.fixture(scope="module")
+def swa():
+    import sliding_window_attention_swa_gb300 as m
+
+    m.load_library()
+    return m
+
+
+ONE = [(0, 1), (1, 1), (14, 1), (15, 1), (16, 1), (62, 1), (63, 1), (64, 1), (127, 1), (128, 1), (129, 1), (1000, 1),
+       (3001, 1)]
+RAGGED = [(0, 1), (5, 33), (0, 0), (130, 1), (64, 64), (0, 257), (0, 0), (1111, 7), (300, 129), (2000, 1)]
+DECODE = [
+    # Hq, Hkv, D, page, window, sinks
+    (8, 2, 128, 16, 0, 0), (8, 2, 128, 64, 100, 4), (4, 4, 64, 32, 1, 0), (32, 2, 64, 16, 257, 37),
+    (7, 1, 128, 128, 128, 0), (6, 2, 256, 64, 1000, 1), (16, 1, 256, 16, 0, 0), (3, 3, 256, 128, 2, 130),
+    (5, 1, 64, 128, 64, 0),
+]
+CHUNK = DECODE + [(12, 1, 128, 32, 300, 3), (24, 8, 64, 64, 0, 0), (16, 8, 256, 16, 129, 5), (2, 2, 128, 16, 17, 0),
+                  (16, 1, 128, 64, 0, 0)]
+
+
+@pytest.mark.parametrize("append", [False, True], ids=["stored", "append"])
+@pytest.mark.parametrize("case", DECODE, ids=str)
+def test_one_token_a_sequence(swa, case, append):
+    Hq, Hkv, D, ps, w, ns = case
+    x = R.Batch(1, ONE, Hq, Hkv, D, ps, w, ns)
+    *_, k, v = run(swa, x, append, q_start=None)
+    assert (R.bits(k) == R.bits(x.k_pages)).all() and (R.bits(v) == R.bits(x.v_pages)).all()
+
+
+@pytest.mark.parametrize("append", [False, True], ids=["stored", "append"])
+@pytest.mark.parametrize("case", CHUNK, ids=str)
+def test_ragged_batch(swa, case, append):
+    Hq, Hkv, D, ps, w, ns = case
+    x = R.Batch(2, RAGGED, Hq, Hkv, D, ps, w, ns, lead=3, tail=5)
+    *_, k, v = run(swa, x, append)
+    assert (R.bits(k) == R.bits(x.k_pages)).all() and (R.bits(v) == R.bits(x.v_pages)).all()
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 16, 17, 31, 63, 64, 65, 100, 128, 300])
+@pytest.mark.parametrize("heads", [(8, 2, 128), (4, 4, 64), (4, 2, 256)], ids=str)
+def test_chunk_lengths(swa, heads, n):
+    Hq, Hkv, D = heads
+    for p0, w in ((0, 0), (777, 200), (127, 0)):
+        run(swa, R.Batch(3, [(p0, n)], Hq, Hkv, D, 16, w), max_q=n)
+
+
+@pytest.mark.parametrize("D,ps", [(64, 16), (128, 32), (256, 64)])
+def test_the_hint_chooses_no_result(swa, D, ps):
+    # a wrong or absent max_q: both kernels on batches of few and of many new tokens
+    for seqs in (ONE, RAGGED):
+        x = R.Batch(4, seqs, 8, 2, D, ps, 500, 2)
+        for hint in (0, 1, 4, 100000):
+            run(swa, x, max_q=hint)
+
+
+@pytest.mark.parametrize("seqs", [[(20000, 1)], [(9000, 3), (100, 1)], [(12000, 40)], [(0, 1)], [(15, 1)] * 40,
+                                  [(70, 2)] * 300, [(0, 0), (0, 0)]], ids=lambda s: f"{len(s)}x{s[0]}")
+def test_long_histories_and_many_sequences(swa, seqs):
+    # one sequence spread over every CTA, joined again; several sequences in one CTA's share
+    for D, ps in ((64, 64), (128, 16), (256, 128)):
+        run(swa, R.Batch(5, seqs, 4, 1, D, ps), want_counts=False)
+        run(swa, R.Batch(6, seqs, 4, 1, D, ps), max_q=max(n for _, n in seqs))
+
+
+def test_values_of_the_extremes(swa):
+    # scores of +-1000s: one key carries all the weight, and the running maximum jumps
+    x = R.Batch(7, [(500, 70), (900, 1)], 8, 2, 128, 32)
+    for t in (x.keys[0], x.keys[1]):
+        t *= 100
+    y = R.Batch(7, [(500, 70), (900, 1)], 8, 2, 128, 32)
+    for b, (p, n) in enumerate(x.seqs):  # lay the scaled keys into the pages
+        for t in range(p + n):
+            y.k_pages[int(y.table[b, t // 32]), :, t % 32] = x.keys[b][t]
+    y.keys = x.keys
+    run(swa, y)
+    run(swa, y, max_q=1)
+
+
+def test_strided_rows(swa):
+    # q, k_new, v_new as views of one fused projection, o as a view with rows apart
+    x = R.Batch(8, RAGGED, 8, 2, 128, 16, 300, 4)
+    qkv = torch.cat([x.q, x.k_new, x.v_new], 1).cuda()
+    out = torch.full((x.N, 2, 8, 128 + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    o = out[:, 1, :, :128]
+    k, v = (t.cuda() for t in x.without_new())
+    _, lse, cnt = swa.swa_paged_attend(qkv[:, :8], k, v, x.table.cuda(), x.p0.cuda(), 300, n_sink=4,
+                                       q_start=x.q_start.cuda(), k_new=qkv[:, 8:10], v_new=qkv[:, 10:], o=o,
+                                       want_counts=True)
+    swa.swa_check_device_error()
+    verify(x, o, lse, cnt)
+    assert (out[:, 0] == 7).all() and (out[:, 1, :, 128:] == 7).all()
+    assert (R.bits(k) == R.bits(x.k_pages)).all() and (R.bits(v) == R.bits(x.v_pages)).all()
+
+
+def test_scale(swa):
+    x = R.Batch(9, [(40, 20), (3, 1)], 4, 2, 64, 16)
+    o, lse, _ = swa.swa_paged_attend(x.q.cuda(), x.k_pages.cuda(), x.v_pages.cuda(), x.table.cuda(), x.p0.cuda(), 0,
+                                     0.3, q_start=x.q_start.cuda())
+    for b, q0, n in x.rows():
+        p = x.seqs[b][0]
+        R.check(o[q0:q0 + n], lse[q0:q0 + n], None,
+                R.attend(x.q[q0:q0 + n], x.keys[b], x.vals[b], p, 0, 0, scale=0.3))
+
+
+def test_append_alone(swa):
+    x = R.Batch(10, RAGGED, 8, 4, 64, 32, lead=2, tail=2)
+    k, v = (t.cuda() for t in x.without_new())
+    swa.swa_paged_append(k, v, x.table.cuda(), x.k_new.cuda(), x.v_new.cuda(), x.p0.cuda(), q_start=x.q_start.cuda())
+    swa.swa_check_device_error()
+    assert (R.bits(k) == R.bits(x.k_pages)).all() and (R.bits(v) == R.bits(x.v_pages)).all()
+
+
+def test_offsets_past_32_bits(swa):
+    # the pages lie past element 2^31 of their pools
+    x = R.Batch(11, [(70, 1), (10, 90)], 8, 8, 128, 64)
+    per = 8 * 64 * 128
+    first = (1 << 31) // per + 5
+    k = torch.empty((first + x.n_pages, 8, 64, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    k[first:], v[first:] = x.k_pages.cuda(), x.v_pages.cuda()
+    table = torch.where(x.table >= 0, x.table + first, x.table).cuda()
+    for hint in (1, 0):
+        o, lse, cnt = swa.swa_paged_attend(x.q.cuda(), k, v, table, x.p0.cuda(), q_start=x.q_start.cuda(), max_q=hint,
+                                           k_new=x.k_new.cuda(), v_new=x.v_new.cuda(), want_counts=True)
+        swa.swa_check_device_error()
+        verify(x, o, lse, cnt)
+
+
+def error_bits(swa):
+    st, words = swa.swa_read_device_errors()
+    return st, words
+
+
+@pytest.mark.parametrize("hint", [0, 1])
+def test_broken_device_data(swa, hint):
+    """What the device finds broken is reported, its sequence skipped, and the others are right."""
+    def call(x, table=None, p0=None, q_start=None):
+        o = torch.full((x.N, x.Hq, x.D), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((x.N, x.Hq), 7.0, device="cuda")
+        swa.swa_paged_attend(x.q.cuda(), x.k_pages.cuda(), x.v_pages.cuda(), (x.table if table is None else table).cuda(),
+                             (x.p0 if p0 is None else p0).cuda(), x.window, o=o, lse=lse, max_q=hint,
+                             q_start=(x.q_start if q_start is None else q_start).cuda())
+        return o, lse
+
+    x = R.Batch(12, [(50, 9), (20, 3), (7, 1)], 4, 2, 64, 16)
+    # a negative position, one past the table's end
+    for p in (-1, 16 * x.width):
+        p0 = x.p0.clone()
+        p0[1] = p
+        o, lse = call(x, p0=p0)
+        assert error_bits(swa) == (1, {"prefill": 0, "split": 0, "cache": swa.DEVERR_BAD_POSITION})
+        verify(x, o, lse, None, skip=(1,))
+    # a row list that goes down, or past the rows
+    for at, to in ((1, -3), (3, x.N + 1)):
+        q_start = x.q_start.clone()
+        q_start[at] = to
+        o, lse = call(x, q_start=q_start)
+        st, words = error_bits(swa)
+        assert st == 1 and words["cache"] == swa.DEVERR_BAD_POSITION
+        if at == 3:
+            verify(x, o, lse, None, skip=(2,))
+    # a page that is needed and missing, or not in the pool
+    for e in (-1, x.n_pages, 2 ** 31 - 1, -2 ** 31):
+        table = x.table.clone()
+        table[0, 1] = e
+        o, lse = call(x, table=table)
+        assert error_bits(swa) == (1, {"prefill": 0, "split": 0, "cache": swa.DEVERR_BAD_PAGE})
+        assert torch.isfinite(o).all()
+        for b, q0, n in x.rows()[1:]:
+            R.check(o[q0:q0 + n], lse[q0:q0 + n], None, x.reference(b))
+    # ... which rows of zeros stand in for
+    y = R.Batch(12, [(50, 9), (20, 3), (7, 1)], 4, 2, 64, 16)
+    y.keys[0][16:32] = 0
+    y.vals[0][16:32] = 0
+    R.check(o[:9], lse[:9], None, y.reference(0))
+    # an append to a missing page stores nothing there
+    k, v = x.k_pages.cuda(), x.v_pages.cuda()
+    table = torch.full_like(x.table, -1)
+    swa.swa_paged_append(k, v, table.cuda(), x.k_new.cuda(), x.v_new.cuda(), x.p0.cuda(), q_start=x.q_start.cuda())
+    assert error_bits(swa)[1]["cache"] == swa.DEVERR_BAD_PAGE
+    assert (R.bits(k) == R.bits(x.k_pages)).all()
+    # and the next call is clean
+    run(swa, x)
+
+
+@pytest.mark.parametrize("hint", [0, 1])
+def test_captured_and_replayed(swa, hint):
+    # two graphs with workspaces of their own, replayed in turn with other lengths and pages
+    def batch(seed, seqs):
+        return R.Batch(seed, seqs, 8, 2, 128, 16, 400, 2, width=80, spare=200 - 0)
+
+    lens = {0: [(100, 5), (1200, 1), (0, 30)], 1: [(900, 20), (3, 15), (640, 1)]}
+    graphs = []
+    for g in range(2):
+        x = batch(20 + g, lens[g])
+        t = dict(q=x.q.cuda(), k=x.k_pages.cuda(), v=x.v_pages.cuda(), table=x.table.cuda(), p0=x.p0.cuda(),
+                 start=x.q_start.cuda())
+        o = torch.full((x.N, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((x.N, 8), 7.0, device="cuda")
+
+        def call(t=t, o=o, lse=lse):
+            swa.swa_paged_attend(t["q"], t["k"], t["v"], t["table"], t["p0"], 400, n_sink=2, q_start=t["start"],
+                                 max_q=hint, o=o, lse=lse)
+
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        graphs.append((graph, t, o, lse))
+    for turn in range(3):
+        for g in range(2):
+            graph, t, o, lse = graphs[g]
+            # the same sizes of everything, other lengths: the tokens dealt another way
+            seqs = {0: [(100 + turn, 5 + turn), (1200, 1), (7 * turn, 30 - turn)],
+                    1: [(900 - turn, 20), (3, 15 - turn), (640, 1 + turn)]}[g]
+            x = batch(30 + 2 * turn + g, seqs)
+            assert x.N == o.shape[0]
+            k = torch.full_like(t["k"], float("nan"))
+            v = torch.full_like(k, float("nan"))
+            n = min(k.shape[0], x.n_pages)
+            assert int(x.table.max()) < n
+            k[:n], v[:n] = x.k_pages[:n].cuda(), x.v_pages[:n].cuda()
+            for name, val in dict(q=x.q, k=k, v=v, table=x.table, p0=x.p0, start=x.q_start).items():
+                t[name].copy_(val)
+            o.fill_(7)
+            graph.replay()
+            swa.swa_check_device_error()
+            verify(x, o, lse, None)
+
+
+def test_two_streams_at_once(swa):
+    xs = [R.Batch(40 + i, [(3000, 70), (10, 1), (900, 200)], 8, 2, 128, 32, 1000) for i in range(4)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    args = [(x.q.cuda(), x.k_pages.cuda(), x.v_pages.cuda(), x.table.cuda(), x.p0.cuda(), x.q_start.cuda()) for x in xs]
+    torch.cuda.synchronize()
+    outs = []
+    for i, a in enumerate(args):
+        with torch.cuda.stream(streams[i % 2]):
+            outs.append(swa.swa_paged_attend(*a[:5], 1000, q_start=a[5], max_q=[0, 1][i // 2], want_counts=True))
+    torch.cuda.synchronize()
+    swa.swa_check_device_error()
+    for x, (o, lse, cnt) in zip(xs, outs):
+        verify(x, o, lse, cnt)
+
+
+def test_same_call_same_bits(swa):
+    x = R.Batch(50, [(5000, 300), (77, 1), (4000, 1)], 8, 2, 128, 16)
+    for hint in (0, 1):
+        a, b = (run(swa, x, max_q=hint) for _ in range(2))
+        assert (R.bits(a[0]) == R.bits(b[0])).all() and torch.equal(a[1], b[1])
+
+
+def test_refusals(swa):
+    x = R.Batch(60, [(5, 2), (3, 1)], 4, 2, 64, 16)
+    a = dict(q=x.q.cuda(), k_pages=x.k_pages.cuda(), v_pages=x.v_pages.cuda(), page_table=x.table.cuda(),
+             p0=x.p0.cuda(), q_start=x.q_start.cuda())
+
+    def refused(**kw):
+        with pytest.raises((ValueError, swa.SwaError)):
+            swa.swa_paged_attend(**{**a, **kw})
+
+    refused(q=a["q"].float())
+    refused(q=a["q"][:, :, :32])
+    refused(q=a["q"].cpu())
+    refused(q=a["q"][:, :3])                       # heads not a multiple of the kv heads
+    refused(q=a["q"].expand(3, 4, 64)[:, :1].expand(3, 4, 64))  # a head stride of 0
+    refused(k_pages=a["k_pages"].transpose(1, 2))
+    refused(v_pages=a["v_pages"][:-1])
+    refused(page_table=a["page_table"].long())
+    refused(page_table=a["page_table"].cpu())
+    refused(p0=a["p0"][:1])
+    refused(q_start=a["q_start"][:2])
+    refused(q_start=None)                          # three rows, two sequences
+    refused(k_new=x.k_new.cuda())                  # without v_new
+    refused(k_new=x.k_new.cuda()[:2], v_new=x.v_new.cuda()[:2])
+    refused(window=-1)
+    refused(n_sink=-1)
+    refused(scale=float("nan"))
+    refused(o=torch.empty(3, 4, 32, dtype=torch.bfloat16, device="cuda"))
+    refused(lse=torch.empty(3, 4, dtype=torch.float64, device="cuda"))
+    refused(row_counts=torch.empty(3, 4, device="cuda"))
+    refused(k_pages=a["k_pages"][:, :, :8].contiguous(), v_pages=a["v_pages"][:, :, :8].contiguous())  # pages of 8
+    o, lse, _ = swa.swa_paged_attend(x.q[:0].cuda(), *(a[n] for n in ("k_pages", "v_pages", "page_table", "p0")),
+                                     q_start=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    swa.swa_check_device_error()

@@ -1,0 +1,281 @@
+"""Reserving, giving back, forking, compacting and copying the pages of a paged cache, against models
+on Python lists (tables, counts and page contents equal), and a run of them together with the
+attention that reads the pages."""
+import numpy as np
+import pytest
+import torch
+
+import paged_reference as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def swa():
+    import sliding_window_attention_swa_gb300 as m
+
+    m.load_library()
+    return m
+
+
+def tables(seed, B, width, n_pages, fill=0.7, shared=0.2):
+    """A random table with its counts (and some pages held by someone else)."""
+    rng = np.random.default_rng(seed)
+    free = list(rng.permutation(n_pages))
+    table = np.full((B, width), -1, dtype=np.int32)
+    for b in range(B):
+        for j in range(width):
+            if rng.random() < fill and free:
+                table[b, j] = free.pop()
+    for b in range(1, B):
+        m = (rng.random(width) < shared) & (table[b - 1] >= 0)
+        table[b, m] = table[b - 1, m]
+    ref = np.bincount(table[table >= 0], minlength=n_pages).astype(np.int32)
+    others = rng.random(n_pages) < 0.05
+    ref[others] += 1
+    return table, ref
+
+
+def same(got, want):
+    np.testing.assert_array_equal(got.cpu().numpy(), np.asarray(want))
+
+
+@pytest.mark.parametrize("B,width,n_pages,ps", [(1, 1, 1, 16), (3, 7, 40, 16), (40, 9, 700, 1), (5, 3000, 40000, 16),
+                                                (1500, 4, 20000, 128)])
+def test_reserve(swa, B, width, n_pages, ps):
+    table, ref = tables(1, B, width, n_pages, fill=0.4)
+    rng = np.random.default_rng(2)
+    first = rng.integers(0, width * ps + 1, B)
+    end = np.minimum(width * ps, first + rng.integers(-3, width * ps + 1, B))
+    first[0], end[0] = 0, width * ps
+    if B > 1500 // 2 or width > 1000:  # keep the model's search short
+        first, end = first // 2, np.minimum(end, first // 2 + 3 * ps)
+    want = R.reserve(table.tolist(), ref.tolist(), first.tolist(), end.tolist(), ps)
+    t, r = R.i32(table), R.i32(ref)
+    swa.swa_pages_reserve(t, r, R.i32(first), R.i32(end), ps)
+    st, words = swa.swa_read_device_errors()
+    lacks = any(want[0][b][j] < 0 for b in range(B) if end[b] > first[b]
+                for j in range(first[b] // ps, -(-end[b] // ps)))
+    assert words["cache"] == (swa.DEVERR_NO_PAGE if lacks else 0)
+    same(t, want[0])
+    same(r, want[1])
+
+
+def test_reserve_when_the_pool_runs_out(swa):
+    t, r = R.i32([[-1, -1, -1], [-1, -1, -1]]), R.i32([0, 1, 0, 0])
+    swa.swa_pages_reserve(t, r, R.i32([0, 0]), R.i32([33, 48]), 16)
+    assert swa.swa_read_device_errors() == (1, {"prefill": 0, "split": 0, "cache": swa.DEVERR_NO_PAGE})
+    same(t, [[0, 2, 3], [-1, -1, -1]])
+    same(r, [1, 1, 1, 1])
+    # a range outside the row: reported, the row left as it is
+    t, r = R.i32([[-1, -1], [-1, -1], [-1, -1]]), R.i32([0, 0, 0])
+    swa.swa_pages_reserve(t, r, R.i32([-1, 0, 5]), R.i32([3, 33, 6]), 16)
+    assert swa.swa_read_device_errors()[1]["cache"] == swa.DEVERR_BAD_POSITION
+    same(t, [[-1, -1], [-1, -1], [0, -1]])
+
+
+@pytest.mark.parametrize("inplace", [True, False])
+@pytest.mark.parametrize("B,width,n_pages,ps,ns", [(1, 1, 1, 16, 0), (3, 7, 40, 16, 4), (40, 90, 4000, 32, 0),
+                                                   (700, 33, 20000, 1, 3)])
+def test_free(swa, B, width, n_pages, ps, ns, inplace):
+    table, ref = tables(3, B, width, n_pages)
+    rng = np.random.default_rng(4)
+    below = rng.integers(-1, width * ps + 2, B)
+    below[::3] = -1
+    want = R.free(table.tolist(), ref.tolist(), below.tolist(), ps, ns)
+    t, r = R.i32(table), R.i32(ref)
+    kw = {} if inplace else dict(out_table=torch.full_like(t, 99), out_ref=torch.full_like(r, 99))
+    ot, orf = swa.swa_pages_free(t, r, R.i32(below), ps, n_sink=ns, **kw)
+    swa.swa_check_device_error()
+    same(ot, want[0])
+    same(orf, want[1])
+    assert (ot is t) == inplace
+    if not inplace:
+        same(t, table)
+        same(r, ref)
+
+
+def test_free_of_what_nobody_holds(swa):
+    t, r = R.i32([[0, 1], [2, 9]]), R.i32([1, 0, 1])
+    swa.swa_pages_free(t, r, R.i32([-1, -1]), 16)
+    assert swa.swa_read_device_errors()[1]["cache"] == swa.DEVERR_BAD_REF | swa.DEVERR_BAD_PAGE
+    same(t, [[-1, -1], [-1, -1]])
+    same(r, [0, 0, 0])
+
+
+def pools(seed, L, n_pages, H, ps, D):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn(L, n_pages, H, ps, D, generator=g).to(torch.bfloat16) for _ in range(2)]
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 16, 64), (3, 2, 32, 128), (2, 5, 64, 8), (1, 3, 1, 24), (2, 1, 128, 256)],
+                         ids=str)
+@pytest.mark.parametrize("B,most", [(1, 40), (6, 200), (70, 130)])
+def test_fork(swa, B, most, shape):
+    L, H, ps, D = shape
+    rng = np.random.default_rng(B + most)
+    lens = rng.integers(0, most + 1, B)
+    lens[0] = most
+    if B > 2:
+        lens[2] = lens[2] // ps * ps  # no page in part
+    width = -(-most // ps) + 1
+    n_pages = int(sum(-(-n // ps) for n in lens)) + 2 * B
+    perm = rng.permutation(n_pages).tolist()
+    table = np.full((B, width), -1, dtype=np.int32)
+    for b, n in enumerate(lens):
+        for j in range(-(-int(n) // ps) + (b % 2)):  # some rows hold a page past their last token
+            table[b, j] = perm.pop()
+    ref = np.bincount(table[table >= 0], minlength=n_pages).astype(np.int32)
+    for kind in ("random", "one", "same", "none"):
+        src = {"random": rng.integers(-1, B, B), "one": np.zeros(B, int), "same": np.arange(B),
+               "none": np.full(B, -1)}[kind]
+        k, v = pools(7, L, n_pages, H, ps, D)
+        wk, wv = R.bits(k), R.bits(v)
+        want = R.fork(table.tolist(), ref.tolist(), src.tolist(), lens.tolist(), ps, (wk, wv))
+        kd, vd, t, r = k.cuda(), v.cuda(), R.i32(table), R.i32(ref)
+        out_ref = torch.full_like(r, 99) if kind == "random" else None
+        ot, orf = swa.swa_pages_fork(kd, vd, t, r, R.i32(src), R.i32(lens), out_ref=out_ref)
+        swa.swa_check_device_error()
+        same(ot, want[0])
+        same(orf, want[1])
+        same(t, table)
+        np.testing.assert_array_equal(R.bits(kd), wk)
+        np.testing.assert_array_equal(R.bits(vd), wv)
+
+
+def test_fork_refusals_and_broken_data(swa):
+    k, v = (x.cuda() for x in pools(8, 1, 5, 1, 16, 8))
+    t, r = R.i32([[0, 1], [2, -1], [3, 4]]), R.i32([1, 1, 1, 1, 1])
+    lens = R.i32([20, 3, 32])
+    with pytest.raises(swa.SwaError):
+        swa.swa_pages_fork(k, v, t, r, R.i32([0, 1, 2]), lens, out_table=t)
+    with pytest.raises(ValueError):
+        swa.swa_pages_fork(k[:, :4], v[:, :4], t, r[:4].contiguous(), R.i32([0, 1]), lens)
+    with pytest.raises(swa.SwaError):
+        swa.swa_pages_fork(k[:, :4].contiguous(), v[:, :4].contiguous(), t, r, R.i32([0, 1, 2]), lens)
+    # rows that do not exist, lengths that do not fit: empty rows, reported
+    for src, ln in (([0, 7, -2], [20, 3, 32]), ([0, 1, 2], [20, -1, 33])):
+        ot, orf = swa.swa_pages_fork(k, v, t, r.clone(), R.i32(src), R.i32(ln))
+        assert swa.swa_read_device_errors()[1]["cache"] == swa.DEVERR_BAD_POSITION
+        same(ot, [[0, 1], [-1, -1], [-1, -1]])
+        same(orf, [1, 1, 0, 0, 0])
+    # no page left for the second copy
+    r2 = R.i32([1, 1, 2, 2, 2])
+    k2 = k.clone()
+    ot, orf = swa.swa_pages_fork(k2, v, t, r2, R.i32([0, 0, 0]), lens)
+    assert swa.swa_read_device_errors()[1]["cache"] == swa.DEVERR_NO_PAGE
+    same(ot, [[0, 1], [0, -1], [0, -1]])
+    same(orf, [3, 1, 1, 1, 1])
+    np.testing.assert_array_equal(R.bits(k2), R.bits(k))
+
+
+@pytest.mark.parametrize("inplace", [True, False])
+@pytest.mark.parametrize("B,width,n_pages,shape", [(1, 1, 1, (1, 1, 16, 64)), (4, 5, 30, (2, 3, 16, 8)),
+                                                   (30, 9, 400, (1, 2, 32, 64)), (9, 4000, 50000, (1, 1, 1, 8))])
+def test_compact(swa, B, width, n_pages, shape, inplace):
+    L, H, ps, D = shape
+    for fill in (0.0, 0.3, 0.95):
+        table, ref = tables(9, B, width, n_pages, fill=fill)
+        k, v = pools(10, L, n_pages, H, ps, D)
+        wk, wv = R.bits(k), R.bits(v)
+        wt, wr, live = R.compact(table.tolist(), ref.tolist(), (wk, wv))
+        kd, vd, t, r = k.cuda(), v.cuda(), R.i32(table), R.i32(ref)
+        kw = {} if inplace else dict(out_table=torch.full_like(t, 99), out_ref=torch.full_like(r, 99))
+        ot, orf, n_live = swa.swa_pages_compact(kd, vd, t, r, **kw)
+        swa.swa_check_device_error()
+        assert n_live.item() == live
+        same(ot, wt)
+        same(orf, wr)
+        np.testing.assert_array_equal(R.bits(kd), wk)
+        np.testing.assert_array_equal(R.bits(vd), wv)
+        if not inplace:
+            same(t, table)
+            same(r, ref)
+
+
+@pytest.mark.parametrize("layers", [None, 3])
+def test_copy(swa, layers):
+    k, v = pools(11, layers or 1, 9, 2, 32, 64)
+    if layers is None:
+        k, v = k[0], v[0]
+    kd, vd = k.cuda(), v.cuda()
+    swa.swa_pages_copy(kd, vd, R.i32([0, 0, 8]), R.i32([3, 7, 1]))
+    swa.swa_check_device_error()
+    for a, d in ((k, kd), (v, vd)):
+        w = a.clone()
+        for s, t in ((0, 3), (0, 7), (8, 1)):
+            (w[t] if layers is None else w[:, t]).copy_(a[s] if layers is None else a[:, s])
+        np.testing.assert_array_equal(R.bits(d), R.bits(w))
+    swa.swa_pages_copy(kd, vd, R.i32([]), R.i32([]))
+    before = R.bits(kd)
+    swa.swa_pages_copy(kd, vd, R.i32([0, -1, 9]), R.i32([9, 2, 2]))  # pairs outside the pool: skipped
+    assert swa.swa_read_device_errors()[1]["cache"] == swa.DEVERR_BAD_PAGE
+    np.testing.assert_array_equal(R.bits(kd), before)
+
+
+def test_layers_apart(swa):
+    # a pool whose layers lie further apart than their pages need: the rest is not touched
+    big = torch.randn(2, 7, 2, 16, 8, device="cuda").to(torch.bfloat16)
+    k, v = big[:, :5], big.clone()[:, :5]
+    want = big.clone()
+    want[:, 4] = want[:, 1]
+    swa.swa_pages_copy(k, v, R.i32([1]), R.i32([4]))
+    assert torch.equal(big, want)
+
+
+def test_serving_run(swa):
+    """Pages reserved, two prompts prefilled in chunks, forked, decoded, trimmed behind the window,
+    compacted and decoded on, in two layers: every step's attention is that of the tokens
+    themselves, and at the end the pool is empty again."""
+    L, Hq, Hkv, D, ps, W, ns, B, width, n_pages = 2, 8, 2, 64, 16, 40, 2, 4, 12, 40
+    g = torch.Generator().manual_seed(12)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16)  # noqa: E731
+    k_pool = torch.full((L, n_pages, Hkv, ps, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    v_pool = torch.full_like(k_pool, float("nan"))
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    ref = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+    hist = [[(torch.empty(0, Hkv, D), torch.empty(0, Hkv, D)) for _ in range(B)] for _ in range(L)]  # tokens so far
+    lens = [0] * B
+
+    def step(new):
+        nonlocal lens
+        p0, end = R.i32(lens), R.i32([a + n for a, n in zip(lens, new)])
+        swa.swa_pages_reserve(table, ref, p0, end, ps)
+        start = R.i32([sum(new[:i]) for i in range(B + 1)])
+        N = sum(new)
+        for layer in range(L):
+            q, k, v = rnd(N, Hq, D), rnd(N, Hkv, D), rnd(N, Hkv, D)
+            o, lse, cnt = swa.swa_paged_attend(q.cuda(), k_pool[layer], v_pool[layer], table, p0, W, n_sink=ns,
+                                               q_start=start, max_q=max(new), k_new=k.cuda(), v_new=v.cuda(),
+                                               want_counts=True)
+            swa.swa_check_device_error()
+            for b, n in enumerate(new):
+                if n:
+                    a = sum(new[:b])
+                    hk, hv = hist[layer][b]
+                    hist[layer][b] = (torch.cat([hk, k[a:a + n]]), torch.cat([hv, v[a:a + n]]))
+                    R.check(o[a:a + n], lse[a:a + n], cnt[a:a + n],
+                            R.attend(q[a:a + n], *hist[layer][b], lens[b], W, ns), f"layer {layer}, row {b}")
+        lens = [a + n for a, n in zip(lens, new)]
+        # what lies behind the next token's window goes back
+        swa.swa_pages_free(table, ref, R.i32([max(0, n - W + 1) for n in lens]), ps, n_sink=ns)
+
+    step([37, 0, 0, 20])
+    step([50, 0, 0, 1])
+    new_table, _ = swa.swa_pages_fork(k_pool, v_pool, table, ref, R.i32([0, 0, 0, 3]), R.i32(lens))
+    table.copy_(new_table)
+    for layer in range(L):
+        hist[layer] = [hist[layer][i] for i in (0, 0, 0, 3)]
+    lens = [lens[i] for i in (0, 0, 0, 3)]
+    for _ in range(3):
+        step([1, 1, 1, 1])
+    _, _, n_live = swa.swa_pages_compact(k_pool, v_pool, table, ref)
+    assert int((ref > 0).sum()) == n_live.item() and (ref[n_live.item():] == 0).all()
+    k_pool[:, n_live.item():] = float("nan")  # what no sequence holds may be overwritten
+    v_pool[:, n_live.item():] = float("nan")
+    for _ in range(3):
+        step([1, 1, 2, 1])
+    step([18, 1, 1, 0])
+    swa.swa_pages_free(table, ref, R.i32([-1] * B), ps)
+    swa.swa_check_device_error()
+    assert (table == -1).all() and (ref == 0).all()
