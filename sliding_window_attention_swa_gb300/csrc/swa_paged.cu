@@ -1,5 +1,5 @@
 // swa_paged.cu -- a paged KV cache: storing new tokens in their pages, and attention of a
-// ragged batch of new tokens over it.
+// ragged batch of new tokens over it (the choice of its kernel, and the merge of shared units).
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -48,65 +48,85 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedArgs 
 }
 
 // ---------------------------------------------------------------------------------------------
-// attention, a warp per (new token, query head): one pass over the keys with the running
-// maximum and sum of the softmax
+// merge of the units that several CTAs share: block (c, y) takes eight rows of the unit that CTA
+// c began and left open, a warp per row.  The pieces lie in the slots 2c + 1, 2(c+1), 2(c+2), ...
+// A row's weight of a piece is 2^(m_piece - m), o = sum of weighted values / sum of weighted sums.
+// Bound by the latency of a few dependent loads; launched as a programmatic dependent of the
+// kernel that wrote the pieces.
 // ---------------------------------------------------------------------------------------------
+constexpr int kMergeRows = kThreads / 32;
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) paged_attend_kernel(const PagedArgs a) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t rows = static_cast<int64_t>(a.N) * a.H_q;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-    for (int64_t r = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5; r < rows; r += step) {
-        const int n = static_cast<int>(r / a.H_q), h = static_cast<int>(r % a.H_q), kvh = h / a.G;
-        const int b = find_sequence(a, n, lane);
-        if (b < 0) continue;
-        const Seq s = load_seq(a, b);
-        if (!s.ok) {
-            if (lane == 0) atomicOr(&g_paged_err, SWA_DEVERR_BAD_POSITION);
-            continue;
-        }
-        const int t = s.p0 + (n - s.q0);
-        float q[E], acc[E];
-        const auto *qp = reinterpret_cast<const __nv_bfloat16 *>(a.q) + static_cast<int64_t>(n) * a.q_st[0] + h * a.q_st[1];
+__global__ void __launch_bounds__(kThreads) paged_merge_kernel(const PagedArgs a, const PagedWs w, const PagedShape x) {
+    constexpr int E = D / 32;  // columns of a lane
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 rec = w.open[blockIdx.x];
+    const int np = rec.x;
+    if (np == 0) return;
+    const int row = blockIdx.y * kMergeRows + warp;  // of the unit: tile * x.rows + token * G + head
+    const int tile = row / x.rows, r = row % x.rows;
+    const Seq s = load_seq(a, rec.y);
+    const int i = (rec.w * x.tiles + tile) * x.TQ + r / a.G;  // token of the sequence
+    if (tile >= x.tiles || r >= x.TQ * a.G || i >= s.n) return;
+    const int rows = x.tiles * x.rows;
+    auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * rows + row; };
+    float m = -INFINITY;
+    for (int k = lane; k < np; k += 32) m = fmaxf(m, w.ml[slot(k) * 2]);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            q[e] = __bfloat162float(qp[e * 32 + lane]) * a.scale_log2;
-            acc[e] = 0.f;
-        }
-        float m = -INFINITY, l = 0.f;
-        int count = 0;
-        const int lo = t >= a.window ? t - a.window + 1 : 0;
-        for (int p = lo > 0 && a.n_sink > 0 ? 0 : lo; p <= t; ++p) {
-            if (p >= a.n_sink && p < lo) {
-                p = lo - 1;
-                continue;
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float acc[E], L = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int k0 = 0; k0 < np; k0 += 32) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (k0 + lane < np) ml = *reinterpret_cast<const float2 *>(w.ml + slot(k0 + lane) * 2);
+        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+        L += f * ml.y;
+        const int n = min(32, np - k0);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            const float *v = w.acc + slot(k0 + k) * D + lane * E;
+            // (a piece that kept nothing of this row has weight 0 and finite values)
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 t = *reinterpret_cast<const float2 *>(v + e);
+                acc[e] += fk * t.x;
+                acc[e + 1] += fk * t.y;
             }
-            const int page = page_of(a, b, p >> a.ps_log2);
-            const bool there = page < a.n_pages;
-            if (!there && lane == 0) atomicOr(&g_paged_err, SWA_DEVERR_BAD_PAGE);
-            const int64_t row = ((static_cast<int64_t>(page) * a.H_kv + kvh) * a.ps + (p & (a.ps - 1))) * D;
-            const auto *kp = reinterpret_cast<const __nv_bfloat16 *>(a.k_pages) + row;
-            const auto *vp = reinterpret_cast<const __nv_bfloat16 *>(a.v_pages) + row;
-            float x = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) x += there ? q[e] * __bfloat162float(kp[e * 32 + lane]) : 0.f;
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            const float mn = fmaxf(m, x), al = ex2(m - mn), w = ex2(x - mn);
-            m = mn;
-            l = l * al + w;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = acc[e] * al + (there ? w * __bfloat162float(vp[e * 32 + lane]) : 0.f);
-            ++count;
         }
-        auto *op = reinterpret_cast<__nv_bfloat16 *>(a.o) + static_cast<int64_t>(n) * a.o_st[0] + h * a.o_st[1];
+    }
 #pragma unroll
-        for (int e = 0; e < E; ++e) op[e * 32 + lane] = __float2bfloat16_rn(acc[e] / l);
-        if (lane == 0) {
-            a.lse[r] = (m + log2f(l)) * 0.69314718055994531f;
-            if (a.counts) a.counts[r] = count;
-        }
+    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const int64_t tok = s.q0 + i;
+    const int h = rec.z * a.G + r % a.G;
+    if (!SWA_IN_BOUNDS(tok < a.N && h < a.H_q, &g_paged_err)) return;
+    const float inv = 1.f / L;  // every row keeps its own key
+    uint16_t *op = a.o + tok * a.o_st[0] + h * a.o_st[1] + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(op + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0) {
+        a.lse[tok * a.H_q + h] = (m + log2f(L)) * 0.69314718055994531f;
+        if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, s.p0 + i);
+    }
+}
+
+cudaError_t launch_merge(const PagedArgs &a, const PagedWs &w, const PagedShape &x, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(x.ctas, (x.tiles * x.rows + kMergeRows - 1) / kMergeRows);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    switch (a.D) {
+        case 64: return cudaLaunchKernelEx(&cfg, paged_merge_kernel<64>, a, w, x);
+        case 128: return cudaLaunchKernelEx(&cfg, paged_merge_kernel<128>, a, w, x);
+        case 256: return cudaLaunchKernelEx(&cfg, paged_merge_kernel<256>, a, w, x);
+        default: return cudaErrorInvalidValue;
     }
 }
 
@@ -124,7 +144,7 @@ int paged_sm_count() {
     return v;
 }
 
-size_t paged_workspace_bytes(const PagedArgs &) { return 0; }
+size_t paged_workspace_bytes(const PagedArgs &a) { return paged_ws_bytes(paged_split_shape(a), a.D); }
 
 cudaError_t launch_paged_append(const PagedArgs &a, cudaStream_t s) {
     const int64_t blocks = (static_cast<int64_t>(a.N) * 32 + kThreads - 1) / kThreads;
@@ -133,29 +153,26 @@ cudaError_t launch_paged_append(const PagedArgs &a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_paged_attend(const PagedArgs &a, void *, cudaStream_t s) {
-    if (a.kn) {
+cudaError_t launch_paged_attend(const PagedArgs &args, void *ws, cudaStream_t s) {
+    PagedArgs a = args;
+    if (a.kn && a.q_start) {  // (one token a sequence: stored by the attention kernel)
         const cudaError_t e = launch_paged_append(a, s);
         if (e != cudaSuccess) return e;
+        a.kn = a.vn = nullptr;
     }
-    const int64_t blocks = (static_cast<int64_t>(a.N) * a.H_q * 32 + kThreads - 1) / kThreads;
-    const int64_t cap = static_cast<int64_t>(paged_sm_count()) * 8;
-    const int grid = static_cast<int>(blocks < cap ? blocks : cap);
-    switch (a.D) {
-        case 64: paged_attend_kernel<64><<<grid, kThreads, 0, s>>>(a); break;
-        case 128: paged_attend_kernel<128><<<grid, kThreads, 0, s>>>(a); break;
-        case 256: paged_attend_kernel<256><<<grid, kThreads, 0, s>>>(a); break;
-        default: return cudaErrorInvalidValue;
-    }
-    return cudaGetLastError();
+    const PagedShape x = paged_split_shape(a);
+    const PagedWs w = paged_carve(ws, x, a.D);
+    const cudaError_t e = launch_paged_split(a, w, s);
+    return e != cudaSuccess ? e : launch_merge(a, w, x, s);
 }
 
 void paged_read_clear_error(unsigned int *data, unsigned int *split, unsigned int *prefill) {
     unsigned int v = 0, z = 0;
-    *data = *split = *prefill = 0;
+    *prefill = 0;
+    paged_split_read_clear_error(data, split);
     if (cudaMemcpyFromSymbol(&v, g_paged_err, sizeof v) != cudaSuccess) return;
     cudaMemcpyToSymbol(g_paged_err, &z, sizeof z);
-    *data = v;
+    *data |= v;
 }
 
 }  // namespace swa

@@ -29,6 +29,43 @@ struct PagedArgs {
 
 constexpr int kPagedMaxB = 8192;
 
+// Partial results of units that several CTAs share.  CTA c has two slots of `rows` rows: 2c for
+// the unit that an earlier CTA began, 2c + 1 for one that it begins and leaves open (only its
+// last unit can be).
+struct PagedWs {
+    float *ml;   // [2 * CTAs][rows][2]: maximum (log2 units), sum
+    float *acc;  // [2 * CTAs][rows][D]: unnormalised weighted values
+    int4 *open;  // [CTAs]: {pieces of the unit left open (0: none), b, kvh, ut}
+};
+// A kernel's grid and the shape of its units: tiles of query rows (row r of a tile is token
+// r / G, head r % G of the group), tokens a tile.
+struct PagedShape {
+    int ctas, tiles, rows, TQ;
+};
+inline size_t paged_ws_bytes(const PagedShape &x, int D) {
+    auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+    const size_t rows = static_cast<size_t>(x.ctas) * 2 * x.tiles * x.rows;
+    return up(rows * 2 * sizeof(float)) + up(rows * D * sizeof(float)) + up(x.ctas * sizeof(int4));
+}
+inline PagedWs paged_carve(void *ws, const PagedShape &x, int D) {
+    auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+    const size_t rows = static_cast<size_t>(x.ctas) * 2 * x.tiles * x.rows;
+    char *p = static_cast<char *>(ws);
+    PagedWs w;
+    w.ml = reinterpret_cast<float *>(p);
+    p += up(rows * 2 * sizeof(float));
+    w.acc = reinterpret_cast<float *>(p);
+    p += up(rows * D * sizeof(float));
+    w.open = reinterpret_cast<int4 *>(p);
+    return w;
+}
+
+// Few rows (swa_paged_split.cu).  It stores the new rows itself where every sequence has one
+// new token (q_start null).
+PagedShape paged_split_shape(const PagedArgs &a);
+cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, cudaStream_t s);
+void paged_split_read_clear_error(unsigned int *data, unsigned int *wait);
+
 int paged_sm_count();  // SMs of the current device
 size_t paged_workspace_bytes(const PagedArgs &a);
 cudaError_t launch_paged_append(const PagedArgs &a, cudaStream_t s);

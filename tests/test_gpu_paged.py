@@ -322,6 +322,7 @@ def test_refusals(swa):
     refused(lse=torch.empty(3, 4, dtype=torch.float64, device="cuda"))
     refused(row_counts=torch.empty(3, 4, device="cuda"))
     refused(k_pages=a["k_pages"][:, :, :8].contiguous(), v_pages=a["v_pages"][:, :, :8].contiguous())  # pages of 8
+    refused(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))  # too small
     o, lse, _ = swa.swa_paged_attend(x.q[:0].cuda(), *(a[n] for n in ("k_pages", "v_pages", "page_table", "p0")),
                                      q_start=torch.zeros(3, dtype=torch.int32, device="cuda"))
     assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
