@@ -22,7 +22,7 @@ LIB = os.path.join(BUILD, "libswa.so")
 BUILD_DEBUG = os.path.join(HERE, "_build_debug")
 LIB_DEBUG = os.path.join(BUILD_DEBUG, "libswa_debug.so")
 SOURCES = ["swa_abi.cu", "swa_band.cu", "swa_split.cu", "swa_noalloc.cu", "swa_cache.cu", "swa_paged.cu",
-           "swa_paged_split.cu", "swa_pages.cu"]
+           "swa_paged_split.cu", "swa_paged_tile.cu", "swa_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

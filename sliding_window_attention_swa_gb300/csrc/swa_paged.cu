@@ -4,6 +4,8 @@
 #include <climits>
 #include <cmath>
 
+#include <cudaTypedefs.h>
+
 #include "ptx.cuh"
 #include "swa_paged.cuh"
 
@@ -144,7 +146,34 @@ int paged_sm_count() {
     return v;
 }
 
-size_t paged_workspace_bytes(const PagedArgs &a) { return paged_ws_bytes(paged_split_shape(a), a.D); }
+bool paged_map(CUtensorMap *m, const void *base, int D, int64_t n1, int64_t n2, int64_t n3, int64_t s1, int64_t s2,
+               int64_t s3, int b1, int b2) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void *p = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2),
+                          static_cast<cuuint64_t>(n3)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2,
+                             static_cast<cuuint64_t>(s3) * 2};
+    cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2), 1u};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Few rows: every sequence's new tokens fit one unit of the split kernel (16 rows).  With more of
+// them that kernel would read the keys once per 16 rows.
+static bool few_rows(const PagedArgs &a) { return !a.q_start || (a.max_q > 0 && a.max_q * a.G <= 16); }
+static PagedShape shape_of(const PagedArgs &a) { return few_rows(a) ? paged_split_shape(a) : paged_tile_shape(a); }
+
+size_t paged_workspace_bytes(const PagedArgs &a) { return paged_ws_bytes(shape_of(a), a.D); }
 
 cudaError_t launch_paged_append(const PagedArgs &a, cudaStream_t s) {
     const int64_t blocks = (static_cast<int64_t>(a.N) * 32 + kThreads - 1) / kThreads;
@@ -160,16 +189,17 @@ cudaError_t launch_paged_attend(const PagedArgs &args, void *ws, cudaStream_t s)
         if (e != cudaSuccess) return e;
         a.kn = a.vn = nullptr;
     }
-    const PagedShape x = paged_split_shape(a);
+    const PagedShape x = shape_of(a);
     const PagedWs w = paged_carve(ws, x, a.D);
-    const cudaError_t e = launch_paged_split(a, w, s);
+    const cudaError_t e = few_rows(a) ? launch_paged_split(a, w, s) : launch_paged_tile(a, w, s);
     return e != cudaSuccess ? e : launch_merge(a, w, x, s);
 }
 
 void paged_read_clear_error(unsigned int *data, unsigned int *split, unsigned int *prefill) {
     unsigned int v = 0, z = 0;
-    *prefill = 0;
     paged_split_read_clear_error(data, split);
+    paged_tile_read_clear_error(&v, prefill);
+    *data |= v;
     if (cudaMemcpyFromSymbol(&v, g_paged_err, sizeof v) != cudaSuccess) return;
     cudaMemcpyToSymbol(g_paged_err, &z, sizeof z);
     *data |= v;

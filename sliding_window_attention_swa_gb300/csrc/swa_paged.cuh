@@ -105,14 +105,15 @@ struct Piece {
 // Walks a share piece by piece; every role of a CTA walks it alike.
 template <int BN>
 struct Walk {
-    const PagedArgs &a;
+    const PagedArgs *args;
     int TT, b, kvh, ut, j, left;
     Seq s;
-    __device__ __forceinline__ Walk(const PagedArgs &args, int tt, const Share &sh)
-        : a(args), TT(tt), b(sh.b), kvh(sh.kvh), ut(sh.ut), j(sh.j), left(sh.left) {
+    __device__ __forceinline__ Walk(const PagedArgs &a, int tt, const Share &sh)
+        : args(&a), TT(tt), b(sh.b), kvh(sh.kvh), ut(sh.ut), j(sh.j), left(sh.left) {
         if (left > 0) s = load_seq(a, b);
     }
     __device__ __forceinline__ bool next(Piece &p) {
+        const PagedArgs &a = *args;
         if (left <= 0) return false;
         if (j < 0) {  // the unit after the last piece's
             j = 0;
@@ -142,6 +143,52 @@ struct Walk {
         return p.j1 > p.j0;
     }
 };
+
+// A walk kept in shared memory, one per warp: warps whose registers are taken by their tiles read
+// what they need of the current piece from here.
+struct WalkState {
+    int b, kvh, ut, j, left, q0, n, p0;  // the walk
+    int sink, lo, nt, j0, j1;            // the piece (its unit is (b, kvh, ut) of the walk)
+    __device__ __forceinline__ int tile(int i) const volatile { return j0 + i < sink ? j0 + i : lo + (j0 + i - sink); }
+    __device__ __forceinline__ bool begun() const volatile { return j0 > 0; }
+    __device__ __forceinline__ bool open() const volatile { return j1 < nt; }
+};
+// The warp's next piece (all lanes take part); the first call starts the share.
+template <int BN>
+__device__ __forceinline__ bool walk_step(const PagedArgs &a, int TT, const volatile Share *sh, bool first,
+                                          volatile WalkState *w) {
+    Walk<BN> walk(a, TT, Share{0, 0, 0, 0, 0, 0});
+    if (first) {
+        walk = Walk<BN>(a, TT, Share{sh->b, sh->kvh, sh->ut, sh->j, sh->left, 0});
+    } else {
+        walk.b = w->b;
+        walk.kvh = w->kvh;
+        walk.ut = w->ut;
+        walk.j = w->j;
+        walk.left = w->left;
+        walk.s = Seq{w->q0, w->n, w->p0, true};
+    }
+    __syncwarp();
+    Piece p;
+    const bool more = walk.next(p);
+    if (more && (threadIdx.x & 31) == 0) {
+        w->b = walk.b;
+        w->kvh = walk.kvh;
+        w->ut = walk.ut;
+        w->j = walk.j;
+        w->left = walk.left;
+        w->q0 = walk.s.q0;
+        w->n = walk.s.n;
+        w->p0 = walk.s.p0;
+        w->sink = p.u.sink;
+        w->lo = p.u.lo;
+        w->nt = p.u.n;
+        w->j0 = p.j0;
+        w->j1 = p.j1;
+    }
+    __syncwarp();
+    return more;
+}
 
 __device__ __forceinline__ int piece_slot(const Piece &p) { return 2 * static_cast<int>(blockIdx.x) + (p.begun() ? 0 : 1); }
 __device__ __forceinline__ int4 open_record(const Piece &p, int R) {

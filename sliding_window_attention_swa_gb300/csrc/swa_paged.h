@@ -2,6 +2,8 @@
 // (swa_paged.cu, swa_pages.cu) to the C ABI.  Not installed.
 #pragma once
 
+#include <cuda.h>
+
 #include "swa_internal.h"
 
 namespace swa {
@@ -65,6 +67,15 @@ inline PagedWs paged_carve(void *ws, const PagedShape &x, int D) {
 PagedShape paged_split_shape(const PagedArgs &a);
 cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, cudaStream_t s);
 void paged_split_read_clear_error(unsigned int *data, unsigned int *wait);
+// Many rows (swa_paged_tile.cu).
+PagedShape paged_tile_shape(const PagedArgs &a);
+cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, cudaStream_t s);
+void paged_tile_read_clear_error(unsigned int *data, unsigned int *wait);
+
+// bf16 map over (d, d1, d2, d3) of n1, n2, n3 with element strides s1, s2, s3, a box of 64 x b1 x b2 x 1
+// and 128-B swizzle.
+bool paged_map(CUtensorMap *m, const void *base, int D, int64_t n1, int64_t n2, int64_t n3, int64_t s1, int64_t s2,
+               int64_t s3, int b1, int b2);
 
 int paged_sm_count();  // SMs of the current device
 size_t paged_workspace_bytes(const PagedArgs &a);

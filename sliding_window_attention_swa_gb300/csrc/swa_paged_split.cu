@@ -21,8 +21,6 @@
 #include <climits>
 #include <cmath>
 
-#include <cudaTypedefs.h>
-
 #include "swa_paged.cuh"
 
 namespace swa {
@@ -402,28 +400,6 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
     }
 }
 
-// Map of a pool over (d, row of a page, kv head, page) with a (64, min(page, 64), 1, 1) box.
-bool page_map(CUtensorMap *m, const void *base, const PagedArgs &a, int rows) {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        cudaDriverEntryPointQueryResult q;
-        void *p = nullptr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    if (!fn) return false;
-    const cuuint64_t row = static_cast<cuuint64_t>(a.D) * 2;
-    cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.ps), static_cast<cuuint64_t>(a.H_kv),
-                          static_cast<cuuint64_t>(a.n_pages)};
-    cuuint64_t strides[3] = {row, row * a.ps, row * a.ps * a.H_kv};
-    cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(rows), 1u, 1u};
-    cuuint32_t es[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D>
 cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, cudaStream_t s) {
     using C = SplitCfg<D>;
@@ -438,7 +414,10 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, cudaStream_t s) {
     }
     CUtensorMap mk, mv;
     const int rows = a.ps < CH ? a.ps : CH;
-    if (!page_map(&mk, a.k_pages, a, rows) || !page_map(&mv, a.v_pages, a, rows)) return cudaErrorInvalidValue;
+    const int64_t page = static_cast<int64_t>(a.ps) * D;
+    if (!paged_map(&mk, a.k_pages, D, a.ps, a.H_kv, a.n_pages, D, page, page * a.H_kv, rows, 1) ||
+        !paged_map(&mv, a.v_pages, D, a.ps, a.H_kv, a.n_pages, D, page, page * a.H_kv, rows, 1))
+        return cudaErrorInvalidValue;
     const PagedShape x = paged_split_shape(a);
     paged_split_kernel<D><<<x.ctas, kThreads, C::SMEM, s>>>(mk, mv, a, w, x.TQ, 2, fault_plan().split_stop_stage);
     return cudaGetLastError();

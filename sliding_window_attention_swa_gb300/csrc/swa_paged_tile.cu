@@ -1,0 +1,822 @@
+// swa_paged_tile.cu -- attention of many new tokens over a paged cache on 5th-generation tensor
+// cores (sm_103a).
+//
+// Work unit: one (sequence, kv head, block of NQT query tiles).  A query tile is 128 rows = TQ
+// consecutive new tokens x the G query heads of the group (row = token * G + head), so every
+// key/value tile is loaded once for the whole group.  A unit reads the tiles of BN keys that its
+// tokens reach; the batch's tiles are shared out evenly over one persistent CTA per SM
+// (swa_paged.cuh), a part of a unit that a CTA has is a piece.
+// Roles:
+//   warp 0        K/V producer: K_0, V_0, K_1, V_1, ... of every piece into a ring of NSLOT
+//                 shared-memory slots by TMA, one box per page (or part of a page) and 64 elements
+//                 of the head, one lane each; the pages are looked up two tiles ahead.  V_j and
+//                 K_{j+1} are copied together and signal one barrier, that of K_{j+1}'s slot.
+//                 Pages past the sequence's end or not there read past the pool: zeros.
+//   warp 1        TMEM owner and MMA issuer (warp-uniform loop, one elected lane issues):
+//                   S  = Q K_j^T (A = Q from shared memory, at head dim 256 from tensor memory)
+//                   O += P V_j   (A = P from tensor memory)
+//   warp 2        Q loader.
+//   softmax WGs   NQT warpgroups; one row per thread (TMEM lane).  Running max in the log2
+//                 domain; P = 2^(x - m) is rounded to bf16 over the S columns it came from, the
+//                 row sum takes it unrounded; O is rescaled in TMEM only when a row's max grows by
+//                 more than 2^8 (numerator and denominator share the stale max, so the result is
+//                 the same either way).
+// NQT = 2 (head dim <= 128), a full unit: two query tiles ping-pong -- while one warpgroup turns
+//   S_A into P_A the tensor cores run S_B and P_B V -- with TMEM S_A | S_B | O_A | O_B.
+// NQT = 2, a unit whose tokens fill one query tile at most (the single tokens of a mixed batch, the
+//   end of a chunk): the warpgroups share that tile and take its key tiles in turn, each with
+//   its own S, O, maximum and sum, which meet in the epilogue.  With one warpgroup alone S(j + 1)
+//   could not start before P(j) was used up.
+// NQT = 1 (head dim 256): one query tile, S double-buffered, TMEM S0 | S1 | Q | O.
+// Rows of V past the sequence's end may hold anything (even NaN): the warpgroup that turns the
+// last tile's scores into P zeroes them in shared memory before it hands P over.
+// Bound by the tensor cores and the exponentials for full units over long histories, by HBM for
+// units of few rows.
+// Every wait is bounded; on expiry the CTA records an error word, drains its copies and MMAs,
+// frees TMEM and returns.
+#include <atomic>
+#include <climits>
+#include <cmath>
+
+#include "swa_paged.cuh"
+
+namespace swa {
+namespace {
+
+__device__ unsigned int g_ptile_err = 0;   // waits and bounds
+__device__ unsigned int g_ptile_data = 0;  // broken device data
+
+constexpr int BM = 128;              // query rows per tile (TMEM lanes)
+constexpr float kRescaleTau = 8.0f;  // log2 units: rescale O when the max grows by > 2^8
+
+template <int D>
+struct TileCfg {
+    static constexpr int NQT = D <= 128 ? 2 : 1;    // query tiles per unit
+    static constexpr int BN = D == 256 ? 64 : 128;  // keys per K/V tile
+    // NQT = 2: twelve warps put three on each SM sub-partition, whose 16K-register file caps the
+    // launch at 168 registers a thread; setmaxnreg then moves registers from warpgroup 0 (104) to
+    // the softmax warpgroups (200): 128 * 104 + 256 * 200 = 64512 = 384 * 168.
+    static constexpr int THREADS = NQT == 2 ? 384 : 256;
+    static constexpr int SOFTMAX_WARP0 = 4;
+    static constexpr int REG_CTRL = 104, REG_SOFTMAX = 200;
+    static_assert(NQT == 1 || 128 * REG_CTRL + 256 * REG_SOFTMAX <= THREADS * 168, "register split");
+    static constexpr int QBYTES = BM * D * 2;  // one query tile
+    static constexpr int TBYTES = BN * D * 2;  // one K or V tile
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_RING = NQT * QBYTES;
+    static constexpr int XBYTES = NQT == 2 ? 2 * BM * 8 : 0;  // (max, sum) of both warpgroups' rows
+    static constexpr int NSLOT_RAW = (232448 - 512 - XBYTES - OFF_RING) / TBYTES;
+    // (one query tile: value fills release their slots, which needs an odd ring)
+    static constexpr int NSLOT = D == 64 ? 8 : NQT == 1 && NSLOT_RAW % 2 == 0 ? NSLOT_RAW - 1 : NSLOT_RAW;
+    static constexpr int OFF_X = OFF_RING + NSLOT * TBYTES;
+    static constexpr int OFF_BAR = OFF_X + XBYTES;
+    // q_full[2], q_empty[2], kv_full[NSLOT], kv_empty[NSLOT], s_full[2], p_full[2], o_done[2],
+    // o_free[2], meet, drain
+    static constexpr int NBAR = 2 * NSLOT + 14;
+    static constexpr int OFF_TMEMPTR = OFF_BAR + NBAR * 8;  // TMEM address, abort flag
+    static constexpr int OFF_SHARE = OFF_TMEMPTR + 16;
+    static constexpr int OFF_WALK = OFF_SHARE + 32;
+    // (all of it: the kernel has no static shared memory)
+    static constexpr int SMEM = OFF_WALK + THREADS / 32 * static_cast<int>(sizeof(WalkState));
+    static_assert(sizeof(Share) <= 32, "share");
+    static constexpr uint32_t TMEM_COLS = 512;
+    __host__ __device__ static constexpr uint32_t tm_s(int slot) { return static_cast<uint32_t>(slot * BN); }
+    __host__ __device__ static constexpr uint32_t tm_o(int tile) { return 256u + static_cast<uint32_t>(tile * 128); }
+    static constexpr bool QTM = NQT == 1;  // the query tile in tensor memory, 128 columns
+    static constexpr uint32_t TM_Q = 128;
+    static_assert(NSLOT >= 3, "K/V ring too shallow");
+    static_assert(SMEM <= 232448, "shared memory budget");
+    static_assert(NSLOT * TBYTES >= kPagedMaxB * 8, "scratch of the work split");
+    static_assert(!QTM || (tm_s(1) + BN <= TM_Q && TM_Q + D / 2 <= tm_o(0)), "query tile in tensor memory");
+    static_assert(tm_o(NQT - 1) + D <= TMEM_COLS && tm_s(1) + BN <= 256, "tensor memory budget");
+};
+
+struct TileArgs {
+    PagedArgs a;
+    PagedWs ws;
+    int TQ;             // tokens per query tile
+    int min_tiles;      // least share of a CTA
+    int o_align32;      // o and its strides are 32-byte aligned: rows stored 32 bytes at a time
+    int fault_stop_fill;  // planted fault: no ring fill numbered at or past this (INT_MAX: off)
+};
+
+// Every lane waits (each acquires the barrier); the warp proceeds only if all did,
+// so the .sync.aligned tcgen05 instructions that follow stay convergent.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    const bool ok = mbar_wait(bar, parity, abort, &g_ptile_err);
+    return __all_sync(0xffffffffu, ok);
+}
+
+template <int D>
+__global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
+    paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TileArgs ta) {
+    using C = TileCfg<D>;
+    constexpr int BN = C::BN, NSLOT = C::NSLOT, NQT = C::NQT;
+    const PagedArgs &a = ta.a;
+    extern __shared__ __align__(1024) uint8_t sgen[];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t sbase = smem_u32(sgen);
+    if (sbase & 1023u) {  // (the swizzled tiles rely on it)
+        if (tid == 0) atomicOr(&g_ptile_err, kErrBounds);
+        return;
+    }
+
+    const uint32_t sQ = sbase + C::OFF_Q, sRing = sbase + C::OFF_RING;
+    const uint32_t bars = sbase + C::OFF_BAR;
+    auto bar_qf = [&](int x) { return bars + 8u * x; };
+    auto bar_qe = [&](int x) { return bars + 8u * (2 + x); };
+    auto bar_full = [&](int s) { return bars + 8u * (4 + s); };
+    auto bar_empty = [&](int s) { return bars + 8u * (4 + NSLOT + s); };
+    auto bar_sf = [&](int i) { return bars + 8u * (4 + 2 * NSLOT + i); };
+    auto bar_pf = [&](int i) { return bars + 8u * (6 + 2 * NSLOT + i); };
+    auto bar_od = [&](int i) { return bars + 8u * (8 + 2 * NSLOT + i); };
+    auto bar_of = [&](int i) { return bars + 8u * (10 + 2 * NSLOT + i); };
+    const uint32_t bar_meet = bars + 8u * (12 + 2 * NSLOT);
+    const uint32_t bar_drain = bars + 8u * (13 + 2 * NSLOT);
+    // Ring fills are numbered over the CTA's share: 2g is the key tile, 2g + 1 the value tile of
+    // its g-th tile; fill p lies in slot p % NSLOT.
+    // Slot releases.  NQT = 1: value fills release (a tile's S MMAs precede its P V, so V_g's
+    // release also frees K_g's slot); with an odd ring a slot alternates key and value fills, so
+    // its barrier counts value fills only (vpar).  NQT = 2: key fills release, once their S MMAs
+    // and the P V of the value tile before them are done (kpar).
+    static_assert(NQT == 2 || NSLOT % 2 == 1, "value-only slot releases need an odd ring");
+    auto vpar = [&](int p) -> uint32_t {
+        const int sl = p % NSLOT, i = p / NSLOT;
+        return static_cast<uint32_t>(((i - ((1 + sl) & 1)) / 2) & 1);
+    };
+    auto kpar = [&](int p) -> uint32_t {
+        const int sl = p % NSLOT, i = p / NSLOT;
+        return static_cast<uint32_t>((NSLOT % 2 == 1 ? (i - (sl & 1)) / 2 : i) & 1);
+    };
+    // V_g and K_{g+1} land on K_{g+1}'s slot barrier, which thus completes for key fills only (and
+    // for the CTA's last value fill, which has no key fill after it): fpar(q) is the parity of
+    // owner fill q's completion.
+    auto fpar = [&](int q) -> uint32_t {
+        const int sl = q % NSLOT, i = q / NSLOT;
+        const int n = NSLOT % 2 == 1 ? (i - (sl & 1) + 1) / 2 : (sl % 2 == 0 ? i : 0);
+        return static_cast<uint32_t>(n & 1);
+    };
+    Share *share = reinterpret_cast<Share *>(sgen + C::OFF_SHARE);
+    volatile int *abort = reinterpret_cast<volatile int *>(sgen + C::OFF_TMEMPTR + 4);
+    volatile uint32_t *tmem_holder = reinterpret_cast<volatile uint32_t *>(sgen + C::OFF_TMEMPTR);
+
+    // ---- setup: barriers, TMEM (once per CTA), this CTA's share
+    if (tid == 0) {
+        *abort = 0;
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(bar_qf(x), 1);
+            // the four warps of a softmax warpgroup; with the tile in tensor memory, the MMA
+            // warp's one commit after the copy
+            mbar_init(bar_qe(x), C::QTM ? 1 : 4);
+            mbar_init(bar_sf(x), 1);
+            mbar_init(bar_pf(x), 4);
+            mbar_init(bar_od(x), 1);
+            mbar_init(bar_of(x), 4);
+        }
+        for (int s = 0; s < NSLOT; ++s) {
+            mbar_init(bar_full(s), 1);
+            mbar_init(bar_empty(s), 1);
+        }
+        mbar_init(bar_meet, 8);
+        mbar_init(bar_drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_holder)), C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    const int TT = NQT * ta.TQ;
+    tc_fence_before();
+    // (its block barriers also publish the mbarriers and the TMEM address)
+    find_share<BN, C::THREADS>(a, TT, ta.min_tiles, reinterpret_cast<long long *>(sgen + C::OFF_RING), share,
+                               &g_ptile_data);
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    // the merge grid may be scheduled from here on: its blocks wait for this grid to complete
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Share sh = *share;
+    const int cta_tiles = sh.left;
+    volatile WalkState *wk = reinterpret_cast<volatile WalkState *>(sgen + C::OFF_WALK) + warp;
+    // a unit whose tokens fill one of its two query tiles at most (tokens: of its sequence)
+    auto is_single = [&](int tokens, int ut) { return NQT == 2 && tokens - ut * TT <= ta.TQ; };
+
+    if (warp == 0) {
+        // ============================ K/V producer ============================
+        if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
+        // the scratch of the work split lies in the ring: order its generic accesses before the copies
+        fence_proxy_async_smem();
+        // a tile is npg boxes (pages or parts of one) times D / 64 column blocks, one lane each
+        const int box = min(a.ps, BN), npg = BN / box, nbox = npg * (D / 64);
+        const int my_pg = lane % npg, my_c = lane / npg;
+        const uint32_t my_off = static_cast<uint32_t>(my_c * (BN * 128) + my_pg * box * 128);
+        struct Ref {
+            int kvh, row, page;
+        };
+        Walk<BN> walk(a, TT, sh);
+        Piece p;
+        p.j1 = 0;
+        int j = 0, lo = 0, t1 = 0, end = 0;
+        int4 open = make_int4(0, 0, 0, 0);
+        // this lane's box of the share's next tile
+        auto next_tile = [&]() -> Ref {
+            if (j >= p.j1) {
+                if (!walk.next(p)) return Ref{0, 0, a.n_pages};
+                j = p.j0;
+                const int t0 = p.s.p0 + p.ut * TT;
+                t1 = p.s.p0 + min(p.s.n, (p.ut + 1) * TT) - 1;
+                lo = t0 >= a.window ? t0 - a.window + 1 : 0;
+                end = p.s.p0 + p.s.n;
+                if (p.open() && !p.begun()) open = open_record(p, sh.R);
+            }
+            const int kp = p.u.tile(j) * BN + my_pg * box;
+            ++j;
+            const int page = kp < end ? page_of(a, p.b, kp >> a.ps_log2) : a.n_pages;
+            // a page that some row keeps a key of has to be there
+            if (page == a.n_pages && kp <= t1 && (kp + box > lo || kp < a.n_sink))
+                atomicOr(&g_ptile_data, SWA_DEVERR_BAD_PAGE);
+            return Ref{p.kvh, kp & (a.ps - 1), page};
+        };
+        auto copy = [&](const Ref &r, bool is_v, int slot, uint32_t bar) {
+            if (lane < nbox) {
+                // debug build: the box lies in the page, the head exists
+                (void)SWA_IN_BOUNDS(r.row + box <= a.ps && r.kvh < a.H_kv && r.page <= a.n_pages, &g_ptile_err);
+                tma_load_4d(sRing + slot * C::TBYTES + my_off, is_v ? &tm_v : &tm_k, bar, my_c * 64, r.row, r.kvh,
+                            r.page);
+            }
+        };
+        // a fill's slot is free once the fill that releases its last occupant has done so
+        auto slot_free = [&](int q) -> bool {
+            if (q < NSLOT) return true;
+            const int prev = q - NSLOT;
+            if constexpr (NQT == 1) {
+                const int vp = (prev & 1) ? prev : prev + 1;
+                return warp_wait(bar_empty(vp % NSLOT), vpar(vp), abort);
+            } else {
+                const int kp = (prev & 1) ? prev + 1 : prev;
+                return warp_wait(bar_empty(kp % NSLOT), kpar(kp), abort);
+            }
+        };
+        const int nfill = 2 * cta_tiles;
+        int g = 0;  // ring fills issued so far
+        // planted fault: only the steps whose fills all lie below the stop run (step t issues
+        // fills up to 2t + 2; the last step, fill nfill - 1 alone)
+        const int n_steps = ta.fault_stop_fill >= nfill ? cta_tiles : max(0, (ta.fault_stop_fill - 1) / 2);
+        bool ok = n_steps == cta_tiles;
+        if (nfill > 0) {
+            Ref cur = next_tile(), nxt = next_tile();
+            if (ta.fault_stop_fill > 0) {
+                if (lane == 0) mbar_arrive_expect_tx(bar_full(0), C::TBYTES);
+                __syncwarp();
+                copy(cur, false, 0, bar_full(0));  // K_0 alone
+                g = 1;
+            }
+#pragma unroll 1
+            for (int t = 0; t < n_steps; ++t) {
+                const bool has_next = t + 1 < cta_tiles;
+                const Ref ahead = t + 2 < cta_tiles ? next_tile() : nxt;
+                const int pv = 2 * t + 1, own = has_next ? pv + 1 : pv;
+                if (!(slot_free(pv) && (!has_next || slot_free(own)))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = bar_full(own % NSLOT);
+                if (lane == 0) mbar_arrive_expect_tx(bar, (has_next ? 2 : 1) * C::TBYTES);
+                __syncwarp();
+                copy(cur, true, pv % NSLOT, bar);
+                if (has_next) copy(nxt, false, own % NSLOT, bar);
+                g = own + 1;
+                cur = nxt;
+                nxt = ahead;
+            }
+        }
+        if (lane == 0) ta.ws.open[blockIdx.x] = ok ? open : make_int4(0, 0, 0, 0);
+        if (!ok && lane == 0) {
+            // drain the owner barriers of the copies that may still be in flight: fills below
+            // g - NSLOT have landed (their slots were released by readers that waited for them)
+            for (int q = max(0, g - NSLOT); q < g; ++q)
+                if ((q & 1) == 0 || q + 1 == nfill) mbar_drain(bar_full(q % NSLOT), fpar(q), &g_ptile_err);
+        }
+    } else if (warp == 2) {
+        // ============================ Q loader ============================
+        if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
+        int k = 0;
+        int loads[2] = {0, 0};  // phases of each tile's barrier
+        bool ok = true;
+        Walk<BN> walk(a, TT, sh);
+        Piece p;
+#pragma unroll 1
+        for (; ok && walk.next(p); ++k) {
+#pragma unroll 1
+            for (int x = 0; x < NQT; ++x) {
+                // the previous piece's S MMAs are done with this tile's shared memory
+                if (k >= 1) ok = warp_wait(bar_qe(x), (k - 1) & 1, abort);
+                if (!ok) break;
+                if (lane == 0) {
+                    const int i = p.ut * TT + x * ta.TQ;  // the tile's first token
+                    if (i < p.s.n) {
+                        // debug build: the tile's tokens and its group's heads exist
+                        (void)SWA_IN_BOUNDS(p.s.q0 + i < a.N && (p.kvh + 1) * a.G <= a.H_q, &g_ptile_err);
+                        mbar_arrive_expect_tx(bar_qf(x), static_cast<uint32_t>(a.G * ta.TQ * D * 2));
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_4d(sQ + x * C::QBYTES + c * (BM * 128), &tm_q, bar_qf(x), c * 64, p.kvh * a.G,
+                                        p.s.q0 + i, 0);
+                    } else {
+                        mbar_arrive(bar_qf(x));  // the unit has no such tile
+                    }
+                }
+                __syncwarp();
+                ++loads[x];
+            }
+        }
+        if (!ok && lane == 0) {
+            for (int x = 0; x < NQT; ++x)
+                if (loads[x] > 0) mbar_drain(bar_qf(x), (loads[x] - 1) & 1, &g_ptile_err);
+        }
+    } else if (warp == 1) {
+        // ============================ MMA issuer ============================
+        if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
+        constexpr uint32_t idS = idesc_bf16_f32(BM, BN, false, false);
+        constexpr uint32_t idPV = idesc_bf16_f32(BM, D, false, true);
+        bool ok = true, was_single = false;
+        int J = 0;                // tiles of this CTA's previous pieces
+        int k = 0;                // pieces so far
+        int kw = -1;              // key fills (and with each the value fill before it) waited for
+        uint32_t np0 = 0, np1 = 0;  // P tiles of each slot used so far
+        // the A descriptors of the first query tile's slices never move; the second tile's lie
+        // QBYTES further
+        constexpr bool kQDesc = !C::QTM;
+        uint64_t qdesc[D / 16];
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+            qdesc[kk] = kQDesc ? smem_desc(sQ + (kk >> 2) * (BM * 128) + (kk & 3) * 32, 16, 1024, kSwizzle128B) : 0ull;
+        // K_g (and V_{g-1}) has landed
+        auto have_k = [&](int g) -> bool {
+            while (kw < g) {
+                ++kw;
+                if (!warp_wait(bar_full((2 * kw) % NSLOT), fpar(2 * kw), abort)) return false;
+            }
+            return true;
+        };
+        auto have_v = [&](int g) -> bool {
+            if (g + 1 < cta_tiles) return have_k(g + 1);
+            return warp_wait(bar_full((2 * g + 1) % NSLOT), fpar(2 * g + 1), abort);
+        };
+        // S of tile g into TMEM slot `slot` from query tile qt
+        auto mma_s = [&](int slot, int qt, int g) -> bool {
+            if (!have_k(g)) return false;
+            tc_fence_after();
+            const uint64_t b0 = smem_desc(sRing + ((2 * g) % NSLOT) * C::TBYTES, 16, 1024, kSwizzle128B);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t bd = desc_offset(b0, (kk >> 2) * (BN * 128) + (kk & 3) * 32);
+                if constexpr (C::QTM)
+                    tc_mma_ts_e(tmem + C::tm_s(slot), tmem + C::TM_Q + kk * 8, bd, idS, kk > 0 ? 1u : 0u);
+                else tc_mma_ss_e(tmem + C::tm_s(slot), desc_offset(qdesc[kk], qt * C::QBYTES), bd, idS, kk > 0 ? 1u : 0u);
+            }
+            return true;
+        };
+        // O_ot (+)= P(slot) V_g; `first`: a fresh O, once the epilogue of the previous piece has read it
+        auto mma_pv = [&](int slot, int ot, int g, bool first, uint32_t n_used) -> bool {
+            if (!warp_wait(bar_pf(slot), n_used & 1, abort)) return false;
+            if (!have_v(g)) return false;
+            if (first && k >= 1) {
+                if (!warp_wait(bar_of(ot), (k - 1) & 1, abort)) return false;
+                // (both warpgroups read both accumulators of a piece of one query tile)
+                if (NQT == 2 && was_single && !warp_wait(bar_of(ot ^ 1), (k - 1) & 1, abort)) return false;
+            }
+            tc_fence_after();
+            const uint64_t v0 = smem_desc(sRing + ((2 * g + 1) % NSLOT) * C::TBYTES, BN * 128, 1024, kSwizzle128B);
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+                tc_mma_ts_e(tmem + C::tm_o(ot), tmem + C::tm_s(slot) + kk * 8, desc_offset(v0, kk * 2048), idPV,
+                            (!first || kk > 0) ? 1u : 0u);
+            return true;
+        };
+#pragma unroll 1
+        for (; ok && walk_step<BN>(a, TT, share, k == 0, wk); ++k) {
+            const int n = wk->j1 - wk->j0;
+            ok = warp_wait(bar_qf(0), k & 1, abort);
+            if (!ok) break;
+            if constexpr (NQT == 2) {
+                // Step e: P V from slot x = e & 1, then the next S into it.  A full unit's slots are its
+                // two query tiles, each with every key tile; with one query tile they take the
+                // key tiles in turn.
+                const bool single = is_single(wk->n, wk->ut);
+                ok = warp_wait(bar_qf(1), k & 1, abort);
+                if (!ok) break;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int i = single ? x : 0;
+                    if (i >= n) break;
+                    ok = mma_s(x, single ? 0 : x, J + i);
+                    if (!ok) break;
+                    tc_commit_e(bar_sf(x));
+                    if (single && x == 0) tc_commit_e(bar_empty((2 * J) % NSLOT));
+                }
+                if (!ok) break;
+                auto step = [&](int x, int i, bool first, uint32_t n_used) -> bool {
+                    if (!mma_pv(x, x, J + i, first, n_used)) return false;
+                    // (S of tile i + 1 was issued before this P V: the commit covers both)
+                    if (single && i + 1 < n) tc_commit_e(bar_empty((2 * (J + i + 1)) % NSLOT));
+                    const int i2 = single ? i + 2 : i + 1;
+                    if (i2 < n) {
+                        if (!mma_s(x, single ? 0 : x, J + i2)) return false;
+                        tc_commit_e(bar_sf(x));
+                    } else if (!single) {
+                        tc_commit_e(bar_od(x));
+                    }
+                    return true;
+                };
+#pragma unroll 1
+                for (int i = 0; i < n; i += single ? 2 : 1) {
+                    ok = step(0, i, i == 0, np0++);
+                    if (!ok) break;
+                    const int i1 = single ? i + 1 : i;
+                    if (i1 >= n) break;
+                    ok = step(1, i1, i == 0, np1++);
+                    if (!ok) break;
+                }
+                if (!ok) break;
+                if (single) {
+                    tc_commit_e(bar_od(0));
+                    tc_commit_e(bar_od(1));
+                }
+                was_single = single;
+            } else {
+                if constexpr (C::QTM) {
+                    // the piece's query tile into tensor memory, 16 columns per copy (the previous
+                    // piece's last S MMA precedes the copies in the tensor pipe); its shared memory is
+                    // free for the next piece once they complete
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc_cp_128x256b_e(tmem + C::TM_Q + kk * 8,
+                                         smem_desc(sQ + (kk >> 2) * (BM * 128) + (kk & 3) * 32, 16, 1024, kSwizzle128B));
+                    tc_commit_e(bar_qe(0));
+                }
+                ok = mma_s(J & 1, 0, J);
+                if (!ok) break;
+                tc_commit_e(bar_sf(J & 1));
+#pragma unroll 1
+                for (int i = 0; i < n; ++i) {
+                    const int g = J + i;
+                    if (i + 1 < n) {
+                        // slot (g+1) & 1 last held P of tile g-1, consumed by its P V issued earlier
+                        ok = mma_s((g + 1) & 1, 0, g + 1);
+                        if (!ok) break;
+                        tc_commit_e(bar_sf((g + 1) & 1));
+                    }
+                    ok = mma_pv(g & 1, 0, g, i == 0, static_cast<uint32_t>(g >> 1));
+                    if (!ok) break;
+                    tc_commit_e(bar_empty((2 * g + 1) % NSLOT));
+                    if (i + 1 == n) tc_commit_e(bar_od(0));
+                }
+            }
+            J += n;
+        }
+        if (!ok) {
+            tc_commit_e(bar_drain);
+            mbar_drain(bar_drain, 0, &g_ptile_err);
+        }
+        __syncwarp();
+    } else if (warp >= C::SOFTMAX_WARP0) {
+        // ============================ softmax / epilogue ============================
+        if constexpr (NQT == 2) regs_inc<C::REG_SOFTMAX>();
+        const int wg = (warp - C::SOFTMAX_WARP0) >> 2;
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane;  // row == TMEM lane
+        const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t o_addr = tmem + lane_addr + C::tm_o(wg);
+        float2 *meet = reinterpret_cast<float2 *>(sgen + C::OFF_X);
+        bool ok = true;
+        int J = 0, k = 0;
+        uint32_t ns = 0, n_meet = 0;  // S tiles of this warpgroup's slot so far; single pieces so far
+#pragma unroll 1
+        for (; ok && walk_step<BN>(a, TT, share, k == 0, wk); ++k) {
+            const int n = wk->j1 - wk->j0;
+            const bool single = is_single(wk->n, wk->ut);
+            const int t = wk->p0 + wk->ut * TT + (single ? 0 : wg * ta.TQ) + r / a.G;  // this row's position
+            // the tile's first position, and the first key that its last row's window keeps
+            const int tlo = t - r / a.G;
+            const int thi = min(tlo + ta.TQ, max(wk->p0 + wk->n, tlo + 1)) - 1;
+            const int lo_thi = thi >= a.window ? thi - a.window + 1 : 0;
+            float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+            for (int i = single ? wg : 0; i < n; i += single ? 2 : 1) {
+                const int g = J + i;
+                const int slot = NQT == 2 ? wg : (g & 1);
+                const uint32_t parity = NQT == 2 ? (ns & 1) : ((g >> 1) & 1);
+                if (!warp_wait(bar_sf(slot), parity, abort)) {
+                    ok = false;
+                    break;
+                }
+                ++ns;
+                if (NQT == 2 && !single) {
+                    // the piece's last S from this query tile: the next piece's rows may load
+                    if (i + 1 == n && lane == 0) mbar_arrive(bar_qe(wg));
+                    // S_B(g) was the last MMA issued before this commit: every reader of K_g and of
+                    // V_{g-1} is done
+                    if (wg == 1 && quarter == 0 && lane == 0) mbar_arrive(bar_empty((2 * g) % NSLOT));
+                }
+                tc_fence_after();
+                const uint32_t s_addr = tmem + lane_addr + C::tm_s(slot);
+                const int k0 = wk->tile(i) * BN;
+                float x[BN];
+                {
+                    uint32_t raw[BN / 32][32];
+#pragma unroll
+                    for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_addr + c * 32, raw[c]);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < BN / 32; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(raw[c][e]);
+                }
+                // ---- mask: columns [lo, hi) and those of sinks (only tiles that some row cuts)
+                const bool interior = k0 + BN - 1 <= tlo && (k0 >= lo_thi || k0 + BN <= a.n_sink);
+                if (!interior) {
+                    const int hi = min(max(t - k0 + 1, 0), BN);
+                    int lo = min(max((t >= a.window ? t - a.window + 1 : 0) - k0, 0), BN);
+                    const int sk = min(max(a.n_sink - k0, 0), hi);
+                    if (sk >= lo) lo = 0;
+                    {
+                        // 32 columns at a time, as a word of bits
+#pragma unroll
+                        for (int wd = 0; wd < BN / 32; ++wd) {
+                            auto below = [&](int n) {  // the columns below n of this word
+                                const int v = min(max(n - 32 * wd, 0), 32);
+                                return v == 32 ? 0xffffffffu : (1u << v) - 1u;
+                            };
+                            const uint32_t keep = (below(hi) & ~below(lo)) | below(sk);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                x[32 * wd + e] = (keep >> e) & 1u ? x[32 * wd + e] : -INFINITY;
+                        }
+                    }
+                }
+                // ---- running max (log2 domain): eight chains of three-input maxima
+                float mx8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mx8[e] = x[e];
+#pragma unroll
+                for (int c = 8; c + 8 < BN; c += 16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mx8[e] = fmax3(mx8[e], x[c + e], x[c + 8 + e]);
+                if constexpr ((BN / 8) % 2 == 0) {  // one column block of 8 left over
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(mx8[e], x[BN - 8 + e]);
+                }
+                const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                                       fmaxf(mx8[6], mx8[7]));
+                const float mt = mx * a.scale_log2;
+                const bool need = mt > m + kRescaleTau;
+                const float mu = need ? mt : m;
+                const float alpha = need ? ex2(m - mu) : 1.f;  // m = -inf gives 0
+                if (__any_sync(0xffffffffu, need) && i >= (single ? 2 : 1)) {
+                    // O holds the P V of this piece's earlier tiles (of this warpgroup) and must be
+                    // complete: with two query tiles S(i) was issued after them; with one, the release
+                    // of tile g-1's V slot is committed right after its P V
+                    if constexpr (NQT == 1) {
+                        if (!warp_wait(bar_empty((2 * (g - 1) + 1) % NSLOT), vpar(2 * (g - 1) + 1), abort)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t ov[32];
+                        tmem_ld32(o_addr + c * 32, ov);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                        tmem_st32(o_addr + c * 32, ov);
+                    }
+                }
+                m = mu;
+                const float msub = mu == -INFINITY ? 0.f : mu;
+                // ---- P = 2^(x*scale_log2 - m) as bf16 pairs over the first BN/2 S columns;
+                // the scale-and-shift and the row sum run on column pairs (fp32x2)
+                const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), nm2 = f2_pack(-msub, -msub);
+                uint64_t rs2[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) rs2[e] = f2_pack(0.f, 0.f);
+#pragma unroll
+                for (int hlf = 0; hlf < BN / 64; ++hlf) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float t0, t1;
+                        f2_unpack(f2_fma(f2_pack(x[hlf * 64 + 2 * e], x[hlf * 64 + 2 * e + 1]), sc2, nm2), t0, t1);
+                        const float p0 = ex2(t0), p1 = ex2(t1);
+                        rs2[e & 3] = f2_add(rs2[e & 3], f2_pack(p0, p1));
+                        pk[e] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st32(s_addr + hlf * 32, pk);
+                }
+                tc_wait_st();
+                float rsum;
+                {
+                    const uint64_t r01 = f2_add(rs2[0], rs2[1]), r23 = f2_add(rs2[2], rs2[3]);
+                    float lo, hi;
+                    f2_unpack(f2_add(r01, r23), lo, hi);
+                    rsum = lo + hi;
+                }
+                l = l * alpha + rsum;
+                const int end = wk->p0 + wk->n;
+                if (k0 + BN > end && (NQT == 1 || single || wg == 0)) {
+                    // the sequence ends in this tile: zero the value rows of its last page past the
+                    // end (later pages came as zeros).  The first P V of the tile waits for this
+                    // warpgroup's P, and with two query tiles the second is issued after it.
+                    const int own = g + 1 < cta_tiles ? 2 * g + 2 : 2 * g + 1;  // V_g lands with K_{g+1}
+                    if (!warp_wait(bar_full(own % NSLOT), fpar(own), abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const int box = min(a.ps, BN);
+                    const int z0 = end - k0, z1 = min(BN, (z0 + box - 1) / box * box);
+                    uint8_t *vt = sgen + C::OFF_RING + ((2 * g + 1) % NSLOT) * C::TBYTES;
+                    for (int idx = r; idx < (z1 - z0) * (D / 8); idx += BM) {
+                        const int row = z0 + idx / (D / 8), pc = idx % (D / 8);
+                        *reinterpret_cast<uint4 *>(vt + (pc >> 3) * (BN * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4)) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_pf(slot));
+            }
+            if (!ok) break;
+
+            // ---- epilogue: O is final once the piece's last P V completes
+            if (!warp_wait(bar_od(wg), k & 1, abort) || (single && !warp_wait(bar_od(wg ^ 1), k & 1, abort))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            // weights of this row's two accumulators (one unless the warpgroups shared the tile)
+            float wa = 1.f, wb = 0.f;
+            if (single) {
+                // every MMA of the piece has completed: the Q loader may refill the tile
+                if (lane == 0) mbar_arrive(bar_qe(wg));
+                // (the other warpgroup has read the last meeting's values: this piece's first P V
+                // waited for both epilogues)
+                meet[wg * BM + r] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_meet);
+                if (!warp_wait(bar_meet, n_meet & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                ++n_meet;
+                const float2 ma = meet[r], mb = meet[BM + r];
+                m = fmaxf(ma.x, mb.x);
+                wa = ma.x == -INFINITY ? 0.f : ex2(ma.x - m);
+                wb = mb.x == -INFINITY ? 0.f : ex2(mb.x - m);
+                l = ma.y * wa + mb.y * wb;
+            }
+            const bool whole = !wk->begun() && !wk->open();
+            const float inv_l = whole ? 1.f / l : 1.f;  // (of a whole unit: every row keeps its own key)
+            wa *= inv_l;
+            wb *= inv_l;
+            const int tq = r / a.G, i0 = wk->ut * TT + (single ? 0 : wg * ta.TQ);  // the tile's first token
+            const int64_t tok = static_cast<int64_t>(wk->q0) + i0 + tq;
+            const int h = wk->kvh * a.G + r % a.G;
+            const bool store = tq < min(wk->n - i0, ta.TQ) && SWA_IN_BOUNDS(tok < a.N && h < a.H_q, &g_ptile_err);
+            uint16_t *orow = a.o + tok * a.o_st[0] + h * a.o_st[1];
+            const int64_t prow = static_cast<int64_t>(2 * static_cast<int>(blockIdx.x) + (wk->begun() ? 0 : 1)) * (NQT * BM) + (single ? 0 : wg * BM) + r;
+            float *arow = ta.ws.acc + prow * D;
+            // a shared tile's columns are read out half by each warpgroup
+            const int c0 = single ? wg * (D / 64) : 0, c1 = single ? c0 + D / 64 : D / 32;
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) {
+                uint32_t ov[32];
+                tmem_ld32(tmem + lane_addr + C::tm_o(single ? 0 : wg) + c * 32, ov);
+                tc_wait_ld();
+                float f[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(ov[e]) * wa;
+                if (single && n > 1) {
+                    tmem_ld32(tmem + lane_addr + C::tm_o(NQT - 1) + c * 32, ov);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] += __uint_as_float(ov[e]) * wb;
+                }
+                if (!store) continue;
+                if (!whole) {
+#pragma unroll
+                    for (int q8 = 0; q8 < 4; ++q8) {
+                        uint32_t wv[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) wv[e] = __float_as_uint(f[q8 * 8 + e]);
+                        st_global_v8(arow + c * 32 + q8 * 8, wv);
+                    }
+                } else if (ta.o_align32) {
+                    // 32-byte stores: each lane of a store writes one whole sector of its row
+#pragma unroll
+                    for (int q8 = 0; q8 < 2; ++q8) {
+                        uint32_t wv[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) wv[e] = pack_bf16x2(f[q8 * 16 + 2 * e], f[q8 * 16 + 2 * e + 1]);
+                        st_global_v8(orow + c * 32 + q8 * 16, wv);
+                    }
+                } else {
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        uint32_t wv[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) wv[e] = pack_bf16x2(f[q4 * 8 + 2 * e], f[q4 * 8 + 2 * e + 1]);
+                        *reinterpret_cast<uint4 *>(orow + c * 32 + q4 * 8) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+                    }
+                }
+            }
+            // O has been read out: the next piece's first P V may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_of(wg));
+            if (store && (!single || wg == 0)) {
+                if (whole) {
+                    a.lse[tok * a.H_q + h] = (m + log2f(l)) * 0.69314718055994531f;
+                    if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, t);
+                } else {
+                    *reinterpret_cast<float2 *>(ta.ws.ml + prow * 2) = make_float2(m, l);
+                }
+            }
+            J += n;
+        }
+    } else {
+        // idle warp of warpgroup 0 gives its registers to the softmax warpgroups
+        if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+template <int D>
+cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, cudaStream_t s) {
+    using C = TileCfg<D>;
+    // the dynamic shared-memory limit is a per-device function attribute: set once per device
+    static std::atomic<bool> configured[64];
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) dev = -1;
+    if (dev < 0 || !configured[dev].load(std::memory_order_acquire)) {
+        cudaError_t e = cudaFuncSetAttribute(paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0) configured[dev].store(true, std::memory_order_release);
+    }
+    const PagedShape x = paged_tile_shape(a);
+    const int box = a.ps < C::BN ? a.ps : C::BN;
+    CUtensorMap mq, mk, mv;
+    const int64_t row = D, page = static_cast<int64_t>(a.ps) * D;
+    if (!paged_map(&mq, a.q, D, a.H_q, a.N, 1, a.q_st[1], a.q_st[0], a.q_st[0], a.G, x.TQ) ||
+        !paged_map(&mk, a.k_pages, D, a.ps, a.H_kv, a.n_pages, row, page, page * a.H_kv, box, 1) ||
+        !paged_map(&mv, a.v_pages, D, a.ps, a.H_kv, a.n_pages, row, page, page * a.H_kv, box, 1))
+        return cudaErrorInvalidValue;
+    TileArgs t{};
+    t.a = a;
+    t.ws = w;
+    t.TQ = x.TQ;
+    t.min_tiles = 4;
+    t.o_align32 = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.o_st[0] % 16 == 0 && a.o_st[1] % 16 == 0;
+    t.fault_stop_fill = fault_plan().band_stop_fill;
+    paged_tile_kernel<D><<<x.ctas, C::THREADS, C::SMEM, s>>>(mq, mk, mv, t);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+PagedShape paged_tile_shape(const PagedArgs &a) {
+    return PagedShape{paged_sm_count(), a.D <= 128 ? 2 : 1, BM, BM / a.G};
+}
+
+cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, cudaStream_t s) {
+    switch (a.D) {
+        case 64: return launch_d<64>(a, w, s);
+        case 128: return launch_d<128>(a, w, s);
+        case 256: return launch_d<256>(a, w, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+void paged_tile_read_clear_error(unsigned int *data, unsigned int *wait) {
+    unsigned int z = 0;
+    *data = *wait = 0;
+    if (cudaMemcpyFromSymbol(wait, g_ptile_err, sizeof z) != cudaSuccess) return;
+    cudaMemcpyToSymbol(g_ptile_err, &z, sizeof z);
+    if (cudaMemcpyFromSymbol(data, g_ptile_data, sizeof z) != cudaSuccess) return;
+    cudaMemcpyToSymbol(g_ptile_data, &z, sizeof z);
+}
+
+}  // namespace swa
