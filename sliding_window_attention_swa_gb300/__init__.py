@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import build as _build_mod
 
@@ -204,19 +205,18 @@ def load_library(path: str | None = None):
     lib.swa_prefill_chunk_workspace_size.restype = sz
     lib.swa_prefill_chunk.argtypes = [ctypes.POINTER(SwaChunkParams), ctypes.POINTER(SwaCacheParams), vp, sz, vp]
     lib.swa_prefill_chunk.restype = ctypes.c_int
-    paged, cache = ctypes.POINTER(SwaPagedParams), ctypes.POINTER(SwaPagedCache)
-    tables, pool = ctypes.POINTER(SwaPageTables), ctypes.POINTER(SwaPagePool)
-    lib.swa_paged_workspace_size.argtypes = [paged, cache]
+    # (structures of the paged calls: a reference to one, or its packed bytes)
+    lib.swa_paged_workspace_size.argtypes = [vp, vp]
     lib.swa_paged_workspace_size.restype = sz
-    lib.swa_paged_attend.argtypes = [paged, cache, vp, sz, vp]
-    lib.swa_paged_append.argtypes = [paged, cache, vp]
-    lib.swa_pages_workspace_size.argtypes = [tables]
+    lib.swa_paged_attend.argtypes = [vp, vp, vp, sz, vp]
+    lib.swa_paged_append.argtypes = [vp, vp, vp]
+    lib.swa_pages_workspace_size.argtypes = [vp]
     lib.swa_pages_workspace_size.restype = sz
-    lib.swa_pages_reserve.argtypes = [tables, vp, vp, vp, sz, vp]
-    lib.swa_pages_free.argtypes = [tables, vp, ctypes.c_int32, vp]
-    lib.swa_pages_fork.argtypes = [tables, pool, vp, vp, vp, sz, vp]
-    lib.swa_pages_compact.argtypes = [tables, pool, vp, vp, sz, vp]
-    lib.swa_pages_copy.argtypes = [pool, vp, vp, ctypes.c_int32, vp]
+    lib.swa_pages_reserve.argtypes = [vp, vp, vp, vp, sz, vp]
+    lib.swa_pages_free.argtypes = [vp, vp, ctypes.c_int32, vp]
+    lib.swa_pages_fork.argtypes = [vp, vp, vp, vp, vp, sz, vp]
+    lib.swa_pages_compact.argtypes = [vp, vp, vp, vp, sz, vp]
+    lib.swa_pages_copy.argtypes = [vp, vp, vp, ctypes.c_int32, vp]
     for name in ("swa_paged_attend", "swa_paged_append", "swa_pages_reserve", "swa_pages_free", "swa_pages_fork",
                  "swa_pages_compact", "swa_pages_copy"):
         getattr(lib, name).restype = ctypes.c_int
@@ -538,56 +538,80 @@ def swa_prefill_chunk(q, k_new, v_new, k_cache, v_cache, slot_pos, p0, window: i
     return o, lse, row_counts
 
 
-def _check_i32(name, t, shape, device):
-    import torch
+# The paged calls are made once a layer and step, so what they cost on the host counts: arguments
+# are packed in one go (the layouts of the structures above, without trailing padding), and
+# checks look at a tensor's device index, not at device objects.
+_PAGED_PARAMS = struct.Struct("5P8q5if3P")
+_PAGED_CACHE = struct.Struct("3P6i")
+_PAGE_TABLES = struct.Struct("4P4i")
+_PAGE_POOL = struct.Struct("2Pq5i")
 
-    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous int32 tensor of shape {list(shape)} on {device}")
+
+def _i32_wrong(name, shape, index):
+    return ValueError(f"{name}: expected a contiguous int32 tensor of shape {list(shape)} on cuda:{index}")
 
 
-def _check_current(device):
+def _device_index(name, t) -> int:
     """The library's calls go to the current device: tensors of another one are refused."""
     import torch
 
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"expected tensors on the current CUDA device, got {device}")
+    index = t.get_device()
+    if index < 0 or index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device, got {t.device}")
+    return index
 
 
-def _paged(q, k_pages, v_pages, page_table, p0, q_start, k_new, v_new):
-    """The cache and batch structures of a paged call, checked (q: any of the packed rows)."""
-    device = k_pages.device
-    _check_current(device)
-    _check_bf16("k_pages", k_pages, 4)
-    _check_bf16("v_pages", v_pages, 4)
-    if v_pages.shape != k_pages.shape or v_pages.device != device:
-        raise ValueError("v_pages: expected the shape and device of k_pages")
+def _raw_stream(stream, index: int) -> int:
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _paged_cache(k_pages, v_pages, page_table, p0, q_start, N: int):
+    """(device index, swa_paged_cache, H_kv, d_h), the cache and the batch's lists checked."""
+    import torch
+
+    index = _device_index("k_pages", k_pages)
+    shape, bf16, i32 = k_pages.shape, torch.bfloat16, torch.int32
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous tensor")
-    if page_table.dim() != 2:
-        raise ValueError("page_table: expected int32 [B, table_width]")
-    B, N = page_table.shape[0], q.shape[0]
-    _check_i32("page_table", page_table, page_table.shape, device)
-    _check_i32("p0", p0, (B,), device)
-    if q_start is not None:
-        _check_i32("q_start", q_start, (B + 1,), device)
-    elif N != B:
-        raise ValueError(f"q_start: needed unless every sequence has one token ({N} rows, {B} sequences)")
-    c = SwaPagedCache(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr())
-    c.n_pages, c.H_kv, c.page_size, c.d_h = k_pages.shape
-    c.B, c.table_width = page_table.shape
-    p = SwaPagedParams()
-    p.p0, p.q_start, p.N = p0.data_ptr(), None if q_start is None else q_start.data_ptr(), N
-    if (k_new is None) != (v_new is None):
+        if t.dtype is not bf16 or t.get_device() != index or len(shape) != 4 or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous CUDA bf16 tensor [n_pages, H_kv, page_size, d], the same "
+                             "for keys and values")
+    if page_table.dim() != 2 or page_table.dtype is not i32 or page_table.get_device() != index or \
+            not page_table.is_contiguous():
+        raise _i32_wrong("page_table", ("B", "table_width"), index)
+    B, width = page_table.shape
+    if p0.dtype is not i32 or p0.get_device() != index or p0.shape != (B,) or not p0.is_contiguous():
+        raise _i32_wrong("p0", (B,), index)
+    if q_start is None:
+        if N != B:
+            raise ValueError(f"q_start: needed unless every sequence has one token ({N} rows, {B} sequences)")
+    elif q_start.dtype is not i32 or q_start.get_device() != index or q_start.shape != (B + 1,) or \
+            not q_start.is_contiguous():
+        raise _i32_wrong("q_start", (B + 1,), index)
+    n_pages, H_kv, page_size, D = shape
+    return index, _PAGED_CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), n_pages, page_size,
+                                    H_kv, D, B, width), H_kv, D
+
+
+def _rows(name, t, index: int, shape) -> tuple:
+    """The token and head strides of packed rows [N, heads, d], checked."""
+    import torch
+
+    st = t.stride()
+    if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape or st[2] != 1:
+        raise ValueError(f"{name}: expected a bf16 tensor {list(shape)} with a contiguous last dim on cuda:{index}")
+    return st[0], st[1]
+
+
+def _new_rows(k_new, v_new, index: int, shape) -> tuple:
+    """(addresses, strides) of the new tokens' keys and values (zeros without them)."""
+    if k_new is None and v_new is None:
+        return (0, 0), (0, 0, 0, 0)
+    if k_new is None or v_new is None:
         raise ValueError("k_new and v_new go together")
-    if k_new is not None:
-        for name, t in (("k_new", k_new), ("v_new", v_new)):
-            _check_bf16(name, t, 3)
-            if tuple(t.shape) != (N, c.H_kv, c.d_h) or t.device != device:
-                raise ValueError(f"{name}: expected shape {[N, c.H_kv, c.d_h]} on {device}")
-        p.k_new, p.v_new = k_new.data_ptr(), v_new.data_ptr()
-        p.kn_strides, p.vn_strides = k_new.stride()[:2], v_new.stride()[:2]
-    return p, c
+    st = _rows("k_new", k_new, index, shape) + _rows("v_new", v_new, index, shape)
+    return (k_new.data_ptr(), v_new.data_ptr()), st
 
 
 def swa_paged_attend(q, k_pages, v_pages, page_table, p0, window: int = 0, scale: float | None = None, *, q_start=None,
@@ -606,35 +630,37 @@ def swa_paged_attend(q, k_pages, v_pages, page_table, p0, window: int = 0, scale
     import torch
 
     lib = load_library()
-    _check_bf16("q", q, 3)
-    p, c = _paged(q, k_pages, v_pages, page_table, p0, q_start, k_new, v_new)
-    N, Hq, D = q.shape
-    if D != c.d_h or q.device != k_pages.device:
-        raise ValueError(f"q: expected shape [N, H_q, {c.d_h}] on {k_pages.device}")
+    if q.dim() != 3:
+        raise ValueError("q: expected [N, H_q, d]")
+    N, Hq, D = shape = q.shape
+    index, cache, H_kv, d_h = _paged_cache(k_pages, v_pages, page_table, p0, q_start, N)
+    q_st = _rows("q", q, index, (N, Hq, d_h))
+    new, new_st = _new_rows(k_new, v_new, index, (N, H_kv, d_h))
+    device = q.device
     if o is None:
-        o = torch.empty((N, Hq, D), dtype=torch.bfloat16, device=q.device)
+        o, o_st = torch.empty(shape, dtype=torch.bfloat16, device=device), (Hq * D, D)
     else:
-        _check_bf16("o", o, 3)
-        if o.shape != q.shape or o.device != q.device:
-            raise ValueError("o: expected the shape and device of q")
-    lse = torch.empty((N, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (N, Hq) or not lse.is_contiguous() or lse.device != q.device:
-        raise ValueError("lse: expected a contiguous fp32 tensor [N, H_q]")
-    if row_counts is None and want_counts:
-        row_counts = torch.empty((N, Hq), dtype=torch.int32, device=q.device)
-    elif row_counts is not None:
-        _check_i32("row_counts", row_counts, (N, Hq), q.device)
-    p.q, p.q_strides, p.H_q, p.max_q = q.data_ptr(), q.stride()[:2], Hq, int(max_q)
-    p.window, p.n_sink, p.scale = int(window), int(n_sink), float(D ** -0.5 if scale is None else scale)
-    p.o, p.o_strides, p.lse = o.data_ptr(), o.stride()[:2], lse.data_ptr()
-    p.row_counts = None if row_counts is None else row_counts.data_ptr()
-    pp, pc = ctypes.byref(p), ctypes.byref(c)
+        o_st = _rows("o", o, index, shape)
+    if lse is None:
+        lse = torch.empty((N, Hq), dtype=torch.float32, device=device)
+    elif lse.dtype is not torch.float32 or lse.get_device() != index or lse.shape != (N, Hq) or not lse.is_contiguous():
+        raise ValueError(f"lse: expected a contiguous fp32 tensor {[N, Hq]} on cuda:{index}")
+    if row_counts is None:
+        if want_counts:
+            row_counts = torch.empty((N, Hq), dtype=torch.int32, device=device)
+    elif row_counts.dtype is not torch.int32 or row_counts.get_device() != index or row_counts.shape != (N, Hq) or \
+            not row_counts.is_contiguous():
+        raise _i32_wrong("row_counts", (N, Hq), index)
     if N == 0:
         return o, lse, row_counts
+    params = _PAGED_PARAMS.pack(
+        q.data_ptr(), *new, p0.data_ptr(), 0 if q_start is None else q_start.data_ptr(), *q_st, *new_st, *o_st, N, Hq,
+        int(max_q), int(window), int(n_sink), D ** -0.5 if scale is None else float(scale), o.data_ptr(),
+        lse.data_ptr(), 0 if row_counts is None else row_counts.data_ptr())
     if workspace is None:
-        workspace = torch.empty(max(int(lib.swa_paged_workspace_size(pp, pc)), 1), dtype=torch.uint8, device=q.device)
-    st = lib.swa_paged_attend(pp, pc, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                              _stream_handle(stream))
+        workspace = torch.empty(lib.swa_paged_workspace_size(params, cache) or 1, dtype=torch.uint8, device=device)
+    st = lib.swa_paged_attend(params, cache, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                              _raw_stream(stream, index))
     if st != 0:
         raise SwaError("swa_paged_attend", st)
     return o, lse, row_counts
@@ -642,53 +668,63 @@ def swa_paged_attend(q, k_pages, v_pages, page_table, p0, window: int = 0, scale
 
 def swa_paged_append(k_pages, v_pages, page_table, k_new, v_new, p0, *, q_start=None, stream=None) -> None:
     """Store k_new/v_new [N,H_kv,d] (packed rows as in swa_paged_attend) in their pages."""
-    p, c = _paged(k_new, k_pages, v_pages, page_table, p0, q_start, k_new, v_new)
-    if k_new.shape[0] == 0:
+    N = k_new.shape[0]
+    index, cache, H_kv, D = _paged_cache(k_pages, v_pages, page_table, p0, q_start, N)
+    new, new_st = _new_rows(k_new, v_new, index, (N, H_kv, D))
+    if N == 0:
         return
-    st = load_library().swa_paged_append(ctypes.byref(p), ctypes.byref(c), _stream_handle(stream))
+    params = _PAGED_PARAMS.pack(0, *new, p0.data_ptr(), 0 if q_start is None else q_start.data_ptr(), 0, 0, *new_st,
+                                0, 0, N, 0, 0, 0, 0, 0.0, 0, 0, 0)
+    st = load_library().swa_paged_append(params, cache, _raw_stream(stream, index))
     if st != 0:
         raise SwaError("swa_paged_append", st)
 
 
-def _page_tables(page_table, ref, page_size: int, out_table, out_ref) -> SwaPageTables:
-    device = page_table.device
-    _check_current(device)
+def _lists(index: int, *named) -> None:
+    """Each (name, tensor, shape): a contiguous int32 tensor of that shape on the device."""
+    import torch
+
+    for name, t, shape in named:
+        if t.dtype is not torch.int32 or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+            raise _i32_wrong(name, shape, index)
+
+
+def _page_tables(page_table, ref, page_size: int, out_table, out_ref):
+    """(device index, swa_page_tables, B), checked."""
+    index = _device_index("page_table", page_table)
     if page_table.dim() != 2 or ref.dim() != 1:
         raise ValueError("page_table: expected int32 [B, width], and ref int32 [n_pages]")
-    _check_i32("page_table", page_table, page_table.shape, device)
-    _check_i32("ref", ref, ref.shape, device)
-    _check_i32("out_table", out_table, page_table.shape, device)
-    _check_i32("out_ref", out_ref, ref.shape, device)
-    t = SwaPageTables(page_table.data_ptr(), ref.data_ptr(), out_table.data_ptr(), out_ref.data_ptr())
-    t.B, t.width = page_table.shape
-    t.n_pages, t.page_size = ref.shape[0], int(page_size)
-    return t
+    shape, n = page_table.shape, ref.shape
+    _lists(index, ("page_table", page_table, shape), ("ref", ref, n), ("out_table", out_table, shape),
+           ("out_ref", out_ref, n))
+    return index, _PAGE_TABLES.pack(page_table.data_ptr(), ref.data_ptr(), out_table.data_ptr(), out_ref.data_ptr(),
+                                    shape[0], shape[1], n[0], int(page_size)), shape[0]
 
 
-def _page_pool(k_pages, v_pages, device) -> SwaPagePool:
-    """A pool [n_pages,H_kv,page_size,d] or [n_layers,n_pages,H_kv,page_size,d] (a layer contiguous)."""
-    _check_current(device)
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dim() not in (4, 5):
-            raise ValueError(f"{name}: expected [n_pages, H_kv, page_size, d] or [n_layers, n_pages, H_kv, page_size, d]")
-        _check_bf16(name, t, t.dim())
-        if t.shape != k_pages.shape or t.stride() != k_pages.stride() or t.device != device:
-            raise ValueError(f"{name}: expected the shape and strides of k_pages, on {device}")
-        if not (t if t.dim() == 4 else t[0]).is_contiguous():
-            raise ValueError(f"{name}: expected each layer's pages to be contiguous")
-    p = SwaPagePool(k_pages.data_ptr(), v_pages.data_ptr())
-    p.n_layers = 1 if k_pages.dim() == 4 else k_pages.shape[0]
-    p.layer_stride = 0 if k_pages.dim() == 4 else k_pages.stride(0)
-    p.n_pages, p.H_kv, p.page_size, p.d_h = k_pages.shape[-4:]
-    return p
+def _page_pool(k_pages, v_pages):
+    """(device index, swa_page_pool, page_size) of a pool [n_pages,H_kv,page_size,d] or
+    [n_layers,n_pages,H_kv,page_size,d] whose layers are each contiguous."""
+    import torch
+
+    index = _device_index("k_pages", k_pages)
+    shape, st = k_pages.shape, k_pages.stride()
+    layers = shape[0] if len(shape) == 5 else 1
+    if len(shape) not in (4, 5) or v_pages.shape != shape or v_pages.stride() != st or \
+            k_pages.dtype is not torch.bfloat16 or v_pages.dtype is not torch.bfloat16 or v_pages.get_device() != index:
+        raise ValueError("k_pages, v_pages: expected bf16 [n_pages, H_kv, page_size, d] or [n_layers, n_pages, H_kv, "
+                         f"page_size, d], the same shape and strides for both, on cuda:{index}")
+    n, H, ps, D = shape[-4:]
+    if st[-4:] != (H * ps * D, ps * D, D, 1) and not (k_pages if len(shape) == 4 else k_pages[0]).is_contiguous():
+        raise ValueError("k_pages, v_pages: expected each layer's pages to be contiguous")
+    return index, _PAGE_POOL.pack(k_pages.data_ptr(), v_pages.data_ptr(), st[0] if len(shape) == 5 else 0, layers, n, H,
+                                  ps, D), ps
 
 
-def _pages_workspace(lib, t, workspace, device):
+def _pages_workspace(lib, tables, workspace, device):
     import torch
 
     if workspace is None:
-        workspace = torch.empty(max(int(lib.swa_pages_workspace_size(ctypes.byref(t))), 1), dtype=torch.uint8,
-                                device=device)
+        workspace = torch.empty(lib.swa_pages_workspace_size(tables) or 1, dtype=torch.uint8, device=device)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -696,12 +732,10 @@ def swa_pages_reserve(page_table, ref, first, end, page_size: int, *, workspace=
     """Give row b of page_table (in place, with ref) a page for every position in [first[b], end[b])
     that has none: the lowest free pages, in the order of rows and entries."""
     lib = load_library()
-    t = _page_tables(page_table, ref, page_size, page_table, ref)
-    _check_i32("first", first, (t.B,), page_table.device)
-    _check_i32("end", end, (t.B,), page_table.device)
+    index, t, B = _page_tables(page_table, ref, page_size, page_table, ref)
+    _lists(index, ("first", first, (B,)), ("end", end, (B,)))
     workspace, n = _pages_workspace(lib, t, workspace, page_table.device)
-    st = lib.swa_pages_reserve(ctypes.byref(t), first.data_ptr(), end.data_ptr(), workspace.data_ptr(), n,
-                               _stream_handle(stream))
+    st = lib.swa_pages_reserve(t, first.data_ptr(), end.data_ptr(), workspace.data_ptr(), n, _raw_stream(stream, index))
     if st != 0:
         raise SwaError("swa_pages_reserve", st)
 
@@ -712,9 +746,9 @@ def swa_pages_free(page_table, ref, below, page_size: int, *, n_sink: int = 0, o
     positions' pages (below[b] < 0: all its pages).  In place unless out_table and out_ref are
     given.  Returns (out_table, out_ref)."""
     out_table, out_ref = page_table if out_table is None else out_table, ref if out_ref is None else out_ref
-    t = _page_tables(page_table, ref, page_size, out_table, out_ref)
-    _check_i32("below", below, (t.B,), page_table.device)
-    st = load_library().swa_pages_free(ctypes.byref(t), below.data_ptr(), int(n_sink), _stream_handle(stream))
+    index, t, B = _page_tables(page_table, ref, page_size, out_table, out_ref)
+    _lists(index, ("below", below, (B,)))
+    st = load_library().swa_pages_free(t, below.data_ptr(), int(n_sink), _raw_stream(stream, index))
     if st != 0:
         raise SwaError("swa_pages_free", st)
     return out_table, out_ref
@@ -730,15 +764,14 @@ def swa_pages_fork(k_pages, v_pages, page_table, ref, src, seq_len, *, out_table
     import torch
 
     lib = load_library()
-    pool = _page_pool(k_pages, v_pages, page_table.device)
+    pool_index, pool, page_size = _page_pool(k_pages, v_pages)
     out_table = torch.empty_like(page_table) if out_table is None else out_table
     out_ref = ref if out_ref is None else out_ref
-    t = _page_tables(page_table, ref, pool.page_size, out_table, out_ref)
-    _check_i32("src", src, (t.B,), page_table.device)
-    _check_i32("seq_len", seq_len, (t.B,), page_table.device)
+    index, t, B = _page_tables(page_table, ref, page_size, out_table, out_ref)
+    _lists(index, ("src", src, (B,)), ("seq_len", seq_len, (B,)))
     workspace, n = _pages_workspace(lib, t, workspace, page_table.device)
-    st = lib.swa_pages_fork(ctypes.byref(t), ctypes.byref(pool), src.data_ptr(), seq_len.data_ptr(),
-                            workspace.data_ptr(), n, _stream_handle(stream))
+    st = lib.swa_pages_fork(t, pool, src.data_ptr(), seq_len.data_ptr(), workspace.data_ptr(), n,
+                            _raw_stream(stream, pool_index))
     if st != 0:
         raise SwaError("swa_pages_fork", st)
     return out_table, out_ref
@@ -752,14 +785,13 @@ def swa_pages_compact(k_pages, v_pages, page_table, ref, *, out_table=None, out_
     import torch
 
     lib = load_library()
-    pool = _page_pool(k_pages, v_pages, page_table.device)
+    pool_index, pool, page_size = _page_pool(k_pages, v_pages)
     out_table, out_ref = page_table if out_table is None else out_table, ref if out_ref is None else out_ref
-    t = _page_tables(page_table, ref, pool.page_size, out_table, out_ref)
+    index, t, _ = _page_tables(page_table, ref, page_size, out_table, out_ref)
     n_live = torch.empty(1, dtype=torch.int32, device=page_table.device) if n_live is None else n_live
-    _check_i32("n_live", n_live, (1,), page_table.device)
+    _lists(index, ("n_live", n_live, (1,)))
     workspace, n = _pages_workspace(lib, t, workspace, page_table.device)
-    st = lib.swa_pages_compact(ctypes.byref(t), ctypes.byref(pool), n_live.data_ptr(), workspace.data_ptr(), n,
-                               _stream_handle(stream))
+    st = lib.swa_pages_compact(t, pool, n_live.data_ptr(), workspace.data_ptr(), n, _raw_stream(stream, pool_index))
     if st != 0:
         raise SwaError("swa_pages_compact", st)
     return out_table, out_ref, n_live
@@ -767,13 +799,11 @@ def swa_pages_compact(k_pages, v_pages, page_table, ref, *, out_table=None, out_
 
 def swa_pages_copy(k_pages, v_pages, src, dst, *, stream=None) -> None:
     """Copy page src[i] to page dst[i] in every layer (int32 lists; the dst distinct, none also a src)."""
-    pool = _page_pool(k_pages, v_pages, src.device)
+    index, pool, _ = _page_pool(k_pages, v_pages)
     if src.dim() != 1:
         raise ValueError("src: expected int32 [n]")
-    _check_i32("src", src, src.shape, src.device)
-    _check_i32("dst", dst, src.shape, src.device)
-    st = load_library().swa_pages_copy(ctypes.byref(pool), src.data_ptr(), dst.data_ptr(), src.shape[0],
-                                       _stream_handle(stream))
+    _lists(index, ("src", src, src.shape), ("dst", dst, src.shape))
+    st = load_library().swa_pages_copy(pool, src.data_ptr(), dst.data_ptr(), src.shape[0], _raw_stream(stream, index))
     if st != 0:
         raise SwaError("swa_pages_copy", st)
 

@@ -217,3 +217,19 @@ def test_pool_has_to_match_the_tables(lib):
         assert lib.swa_pages_fork(ctypes.byref(t), ctypes.byref(p), FAKE, FAKE, FAKE, BIG, None) == 1
         assert lib.swa_pages_compact(ctypes.byref(t), ctypes.byref(p), FAKE, FAKE, BIG, None) == 1
     assert pool.n_pages == t.n_pages
+
+
+def test_packed_layouts_match_the_structures():
+    # the Python calls pack these structures in one go: every field at its offset
+    for packed, struct in ((swa._PAGED_PARAMS, swa.SwaPagedParams), (swa._PAGED_CACHE, swa.SwaPagedCache),
+                           (swa._PAGE_TABLES, swa.SwaPageTables), (swa._PAGE_POOL, swa.SwaPagePool)):
+        fields = [(name, getattr(struct, name).offset + 8 * i) for name, t in struct._fields_
+                  for i in range(2 if t is swa._c_i64x2 else 1)]
+        data = packed.pack(*range(1, len(fields) + 1))
+        assert packed.size <= ctypes.sizeof(struct) < packed.size + 8
+        got = struct.from_buffer_copy(data + bytes(8))
+        want = 1
+        for name, t in struct._fields_:
+            for v in getattr(got, name) if t is swa._c_i64x2 else [getattr(got, name)]:
+                assert v == want, name
+                want += 1
