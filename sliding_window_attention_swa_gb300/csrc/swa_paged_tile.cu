@@ -346,32 +346,34 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         constexpr uint32_t idS = idesc_bf16_f32(BM, BN, false, false);
         constexpr uint32_t idPV = idesc_bf16_f32(BM, D, false, true);
         bool ok = true, was_single = false;
-        int J = 0;                // tiles of this CTA's previous pieces
-        int k = 0;                // pieces so far
-        int kw = -1;              // key fills (and with each the value fill before it) waited for
+        int J = 0;                  // tiles of this CTA's previous pieces
+        int k = 0;                  // pieces so far
         uint32_t np0 = 0, np1 = 0;  // P tiles of each slot used so far
-        // the A descriptors of the first query tile's slices never move; the second tile's lie
-        // QBYTES further
+        // The query tiles never move: the A descriptor of every K slice of each is built once, and
+        // the V slice descriptors once per tile for both P V of a full unit, since the MMA warp's
+        // instruction count per tile is part of the tile period.
         constexpr bool kQDesc = !C::QTM;
-        uint64_t qdesc[D / 16];
+        uint64_t qdesc[NQT][D / 16], vd[BN / 16];
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-            qdesc[kk] = kQDesc ? smem_desc(sQ + (kk >> 2) * (BM * 128) + (kk & 3) * 32, 16, 1024, kSwizzle128B) : 0ull;
-        // K_g (and V_{g-1}) has landed
-        auto have_k = [&](int g) -> bool {
-            while (kw < g) {
-                ++kw;
-                if (!warp_wait(bar_full((2 * kw) % NSLOT), fpar(2 * kw), abort)) return false;
-            }
-            return true;
+        for (int qt = 0; qt < NQT; ++qt)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                qdesc[qt][kk] = kQDesc ? smem_desc(sQ + qt * C::QBYTES + (kk >> 2) * (BM * 128) + (kk & 3) * 32, 16,
+                                                   1024, kSwizzle128B)
+                                       : 0ull;
+        auto v_descs = [&](int g) {
+            const uint64_t v0 = smem_desc(sRing + ((2 * g + 1) % NSLOT) * C::TBYTES, BN * 128, 1024, kSwizzle128B);
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk) vd[kk] = desc_offset(v0, kk * 2048);
         };
+        // K_g, and with it V_{g-1}, has landed
+        auto have_k = [&](int g) -> bool { return warp_wait(bar_full((2 * g) % NSLOT), fpar(2 * g), abort); };
         auto have_v = [&](int g) -> bool {
-            if (g + 1 < cta_tiles) return have_k(g + 1);
-            return warp_wait(bar_full((2 * g + 1) % NSLOT), fpar(2 * g + 1), abort);
+            const int own = g + 1 < cta_tiles ? 2 * g + 2 : 2 * g + 1;
+            return warp_wait(bar_full(own % NSLOT), fpar(own), abort);
         };
-        // S of tile g into TMEM slot `slot` from query tile qt
-        auto mma_s = [&](int slot, int qt, int g) -> bool {
-            if (!have_k(g)) return false;
+        // S of tile g (landed) into TMEM slot `slot` from query tile qt
+        auto mma_s = [&](int slot, int qt, int g) {
             tc_fence_after();
             const uint64_t b0 = smem_desc(sRing + ((2 * g) % NSLOT) * C::TBYTES, 16, 1024, kSwizzle128B);
 #pragma unroll
@@ -379,77 +381,78 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 const uint64_t bd = desc_offset(b0, (kk >> 2) * (BN * 128) + (kk & 3) * 32);
                 if constexpr (C::QTM)
                     tc_mma_ts_e(tmem + C::tm_s(slot), tmem + C::TM_Q + kk * 8, bd, idS, kk > 0 ? 1u : 0u);
-                else tc_mma_ss_e(tmem + C::tm_s(slot), desc_offset(qdesc[kk], qt * C::QBYTES), bd, idS, kk > 0 ? 1u : 0u);
+                else tc_mma_ss_e(tmem + C::tm_s(slot), qdesc[qt][kk], bd, idS, kk > 0 ? 1u : 0u);
             }
-            return true;
+            tc_commit_e(bar_sf(slot));
         };
-        // O_ot (+)= P(slot) V_g; `first`: a fresh O, once the epilogue of the previous piece has read it
-        auto mma_pv = [&](int slot, int ot, int g, bool first, uint32_t n_used) -> bool {
+        // O_ot (+)= P(slot) V (descriptors in vd) once P is there, and for a fresh O once the epilogue
+        // of the previous piece has read it; wait_v: V of tile g may not have landed yet
+        auto mma_pv = [&](int slot, int ot, bool first, uint32_t n_used, bool wait_v, int g) -> bool {
             if (!warp_wait(bar_pf(slot), n_used & 1, abort)) return false;
-            if (!have_v(g)) return false;
+            if (wait_v && !have_v(g)) return false;
             if (first && k >= 1) {
                 if (!warp_wait(bar_of(ot), (k - 1) & 1, abort)) return false;
                 // (both warpgroups read both accumulators of a piece of one query tile)
                 if (NQT == 2 && was_single && !warp_wait(bar_of(ot ^ 1), (k - 1) & 1, abort)) return false;
             }
             tc_fence_after();
-            const uint64_t v0 = smem_desc(sRing + ((2 * g + 1) % NSLOT) * C::TBYTES, BN * 128, 1024, kSwizzle128B);
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)
-                tc_mma_ts_e(tmem + C::tm_o(ot), tmem + C::tm_s(slot) + kk * 8, desc_offset(v0, kk * 2048), idPV,
-                            (!first || kk > 0) ? 1u : 0u);
+                tc_mma_ts_e(tmem + C::tm_o(ot), tmem + C::tm_s(slot) + kk * 8, vd[kk], idPV, (!first || kk > 0) ? 1u : 0u);
             return true;
         };
 #pragma unroll 1
         for (; ok && walk_step<BN>(a, TT, share, k == 0, wk); ++k) {
             const int n = wk->j1 - wk->j0;
             ok = warp_wait(bar_qf(0), k & 1, abort);
+            // (the key tile of a later piece came with the value tile of the last one)
+            if (ok && J == 0) ok = have_k(0);
             if (!ok) break;
-            if constexpr (NQT == 2) {
-                // Step e: P V from slot x = e & 1, then the next S into it.  A full unit's slots are its
-                // two query tiles, each with every key tile; with one query tile they take the
-                // key tiles in turn.
-                const bool single = is_single(wk->n, wk->ut);
+            if (NQT == 2 && !is_single(wk->n, wk->ut)) {
+                mma_s(0, 0, J);
                 ok = warp_wait(bar_qf(1), k & 1, abort);
                 if (!ok) break;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int i = single ? x : 0;
-                    if (i >= n) break;
-                    ok = mma_s(x, single ? 0 : x, J + i);
-                    if (!ok) break;
-                    tc_commit_e(bar_sf(x));
-                    if (single && x == 0) tc_commit_e(bar_empty((2 * J) % NSLOT));
-                }
-                if (!ok) break;
-                auto step = [&](int x, int i, bool first, uint32_t n_used) -> bool {
-                    if (!mma_pv(x, x, J + i, first, n_used)) return false;
-                    // (S of tile i + 1 was issued before this P V: the commit covers both)
-                    if (single && i + 1 < n) tc_commit_e(bar_empty((2 * (J + i + 1)) % NSLOT));
-                    const int i2 = single ? i + 2 : i + 1;
-                    if (i2 < n) {
-                        if (!mma_s(x, single ? 0 : x, J + i2)) return false;
-                        tc_commit_e(bar_sf(x));
-                    } else if (!single) {
-                        tc_commit_e(bar_od(x));
-                    }
-                    return true;
-                };
+                mma_s(1, NQT - 1, J);
 #pragma unroll 1
-                for (int i = 0; i < n; i += single ? 2 : 1) {
-                    ok = step(0, i, i == 0, np0++);
+                for (int i = 0; i < n; ++i) {
+                    const int g = J + i;
+                    v_descs(g);
+                    ok = mma_pv(0, 0, i == 0, np0 + i, true, g);  // (K_{g+1} has landed too then)
                     if (!ok) break;
-                    const int i1 = single ? i + 1 : i;
-                    if (i1 >= n) break;
-                    ok = step(1, i1, i == 0, np1++);
+                    if (i + 1 < n) mma_s(0, 0, g + 1);
+                    else tc_commit_e(bar_od(0));
+                    ok = mma_pv(1, 1, i == 0, np1 + i, false, g);
                     if (!ok) break;
+                    if (i + 1 < n) mma_s(1, NQT - 1, g + 1);
+                    else tc_commit_e(bar_od(1));
+                }
+                np0 += n;
+                np1 += n;
+                was_single = false;
+            } else if (NQT == 2) {
+                // one query tile, its key tiles in slot 0 and 1 in turn.  S of tile i + 1 is issued
+                // before P V of tile i, so the commit after that P V releases K_{i+1}.
+                ok = warp_wait(bar_qf(1), k & 1, abort);
+                if (!ok) break;
+                mma_s(0, 0, J);
+                tc_commit_e(bar_empty((2 * J) % NSLOT));
+#pragma unroll 1
+                for (int i = 0; i < n; ++i) {
+                    const int g = J + i, x = i & 1;
+                    if (i + 1 < n) {  // S of tile i + 1 into the other slot, whose P V is issued
+                        ok = have_k(g + 1);
+                        if (!ok) break;
+                        mma_s(x ^ 1, 0, g + 1);
+                    }
+                    v_descs(g);
+                    ok = mma_pv(x, x, i < 2, x ? np1++ : np0++, i + 1 == n, g);
+                    if (!ok) break;
+                    if (i + 1 < n) tc_commit_e(bar_empty((2 * (g + 1)) % NSLOT));
                 }
                 if (!ok) break;
-                if (single) {
-                    tc_commit_e(bar_od(0));
-                    tc_commit_e(bar_od(1));
-                }
-                was_single = single;
+                tc_commit_e(bar_od(0));
+                tc_commit_e(bar_od(1));
+                was_single = true;
             } else {
                 if constexpr (C::QTM) {
                     // the piece's query tile into tensor memory, 16 columns per copy (the previous
@@ -462,19 +465,18 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                                          smem_desc(sQ + (kk >> 2) * (BM * 128) + (kk & 3) * 32, 16, 1024, kSwizzle128B));
                     tc_commit_e(bar_qe(0));
                 }
-                ok = mma_s(J & 1, 0, J);
-                if (!ok) break;
-                tc_commit_e(bar_sf(J & 1));
+                mma_s(J & 1, 0, J);
 #pragma unroll 1
                 for (int i = 0; i < n; ++i) {
                     const int g = J + i;
                     if (i + 1 < n) {
                         // slot (g+1) & 1 last held P of tile g-1, consumed by its P V issued earlier
-                        ok = mma_s((g + 1) & 1, 0, g + 1);
+                        ok = have_k(g + 1);
                         if (!ok) break;
-                        tc_commit_e(bar_sf((g + 1) & 1));
+                        mma_s((g + 1) & 1, 0, g + 1);
                     }
-                    ok = mma_pv(g & 1, 0, g, i == 0, static_cast<uint32_t>(g >> 1));
+                    v_descs(g);
+                    ok = mma_pv(g & 1, 0, i == 0, static_cast<uint32_t>(g >> 1), i + 1 == n, g);
                     if (!ok) break;
                     tc_commit_e(bar_empty((2 * g + 1) % NSLOT));
                     if (i + 1 == n) tc_commit_e(bar_od(0));
@@ -507,7 +509,15 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             // the tile's first position, and the first key that its last row's window keeps
             const int tlo = t - r / a.G;
             const int thi = min(tlo + ta.TQ, max(wk->p0 + wk->n, tlo + 1)) - 1;
-            const int lo_thi = thi >= a.window ? thi - a.window + 1 : 0;
+            // tiles [ia, ib) of the piece lie in every row's window; iz is the one the sequence ends in
+            int ia, ib, iz;
+            {
+                const int lo_thi = thi >= a.window ? thi - a.window + 1 : 0;
+                const int first = wk->sink - wk->j0 - wk->lo;  // index of tile x of the window: first + x
+                ia = max(first + wk->lo, first + (lo_thi + BN - 1) / BN);
+                ib = first + (tlo + 1) / BN;
+                iz = !wk->open() && (wk->tile(n - 1) + 1) * BN > wk->p0 + wk->n ? n - 1 : -1;
+            }
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
             for (int i = single ? wg : 0; i < n; i += single ? 2 : 1) {
@@ -528,7 +538,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 }
                 tc_fence_after();
                 const uint32_t s_addr = tmem + lane_addr + C::tm_s(slot);
-                const int k0 = wk->tile(i) * BN;
                 float x[BN];
                 {
                     uint32_t raw[BN / 32][32];
@@ -541,8 +550,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                         for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(raw[c][e]);
                 }
                 // ---- mask: columns [lo, hi) and those of sinks (only tiles that some row cuts)
-                const bool interior = k0 + BN - 1 <= tlo && (k0 >= lo_thi || k0 + BN <= a.n_sink);
-                if (!interior) {
+                if (i < ia || i >= ib) {
+                    const int k0 = wk->tile(i) * BN;
                     const int hi = min(max(t - k0 + 1, 0), BN);
                     int lo = min(max((t >= a.window ? t - a.window + 1 : 0) - k0, 0), BN);
                     const int sk = min(max(a.n_sink - k0, 0), hi);
@@ -631,8 +640,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     rsum = lo + hi;
                 }
                 l = l * alpha + rsum;
-                const int end = wk->p0 + wk->n;
-                if (k0 + BN > end && (NQT == 1 || single || wg == 0)) {
+                if (i == iz && (NQT == 1 || single || wg == 0)) {
                     // the sequence ends in this tile: zero the value rows of its last page past the
                     // end (later pages came as zeros).  The first P V of the tile waits for this
                     // warpgroup's P, and with two query tiles the second is issued after it.
@@ -642,7 +650,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                         break;
                     }
                     const int box = min(a.ps, BN);
-                    const int z0 = end - k0, z1 = min(BN, (z0 + box - 1) / box * box);
+                    const int z0 = wk->p0 + wk->n - wk->tile(i) * BN, z1 = min(BN, (z0 + box - 1) / box * box);
                     uint8_t *vt = sgen + C::OFF_RING + ((2 * g + 1) % NSLOT) * C::TBYTES;
                     for (int idx = r; idx < (z1 - z0) * (D / 8); idx += BM) {
                         const int row = z0 + idx / (D / 8), pc = idx % (D / 8);
