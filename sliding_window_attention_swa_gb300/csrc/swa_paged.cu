@@ -73,8 +73,13 @@ __global__ void __launch_bounds__(kThreads) paged_merge_kernel(const PagedArgs a
     if (tile >= x.tiles || r >= x.TQ * a.G || i >= s.n) return;
     const int rows = x.tiles * x.rows;
     auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * rows + row; };
+    // (a CTA between two of the unit's may have no tiles of it)
+    auto piece = [&](int k) {
+        return k == 0 || w.any[blockIdx.x + k] ? *reinterpret_cast<const float2 *>(w.ml + slot(k) * 2)
+                                               : make_float2(-INFINITY, 0.f);
+    };
     float m = -INFINITY;
-    for (int k = lane; k < np; k += 32) m = fmaxf(m, w.ml[slot(k) * 2]);
+    for (int k = lane; k < np; k += 32) m = fmaxf(m, piece(k).x);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float acc[E], L = 0.f;
@@ -82,15 +87,15 @@ __global__ void __launch_bounds__(kThreads) paged_merge_kernel(const PagedArgs a
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
     for (int k0 = 0; k0 < np; k0 += 32) {
         float2 ml = make_float2(-INFINITY, 0.f);
-        if (k0 + lane < np) ml = *reinterpret_cast<const float2 *>(w.ml + slot(k0 + lane) * 2);
+        if (k0 + lane < np) ml = piece(k0 + lane);
         const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
         L += f * ml.y;
         const int n = min(32, np - k0);
 #pragma unroll 4
         for (int k = 0; k < n; ++k) {
             const float fk = __shfl_sync(0xffffffffu, f, k);
+            if (fk == 0.f) continue;  // (nothing kept, or nothing written)
             const float *v = w.acc + slot(k0 + k) * D + lane * E;
-            // (a piece that kept nothing of this row has weight 0 and finite values)
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
                 const float2 t = *reinterpret_cast<const float2 *>(v + e);

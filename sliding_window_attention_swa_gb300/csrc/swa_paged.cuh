@@ -68,10 +68,16 @@ __device__ __forceinline__ int kept_keys(const PagedArgs &a, int t) {
 // ---------------------------------------------------------------------------------------------
 // Work: a unit is (sequence, kv head, block of TT new tokens); it reads the tiles of BN keys
 // that its tokens can reach -- those of the sinks, then those of the window -- as one list of
-// n_tiles.  Lengths are only known on the device, so the work is shared out there: all units'
-// tiles, in the order (sequence, kv head, block), form one list, and CTA c takes the tiles
-// c * R .. (c + 1) * R - 1 of it.  Every CTA thus has the same number of tiles whatever the
-// batch looks like; a unit that crosses a border is finished by a merge of its pieces.
+// n tiles.  Lengths are only known on the device, so the work is shared out there.  All units,
+// in the order (sequence, kv head, block), and their tiles form one list.
+//   Waves (tile kernel, from two units a CTA): whole units are dealt one a CTA in waves of
+//   alternating direction, so that the CTAs work on neighbouring units, which read the same
+//   keys, at the same time: with a stretch of the list for each CTA instead, their working sets
+//   together (1.1 MB each for the Gemma-shape window) exceed L2 and every tile comes from HBM.
+//   Tail: the tiles of the last units (between one and two waves of them, or all units of a
+//   smaller batch) are cut into one stretch a CTA, of such lengths that all CTAs end up with the
+//   same number of tiles, whatever the batch looks like.  A unit that crosses a border is
+//   finished by a merge of its pieces.
 // ---------------------------------------------------------------------------------------------
 struct UnitTiles {
     int sink, lo, n;  // tiles 0 .. sink - 1, then lo, lo + 1, ...: n in all
@@ -88,9 +94,11 @@ __device__ __forceinline__ UnitTiles unit_tiles(const PagedArgs &a, const Seq &s
     return u;
 }
 
-// A CTA's share: from tile j of unit (b, kvh, ut), `left` tiles in list order.
+// A CTA's share: `waves` whole units, then from tile j of unit (b, kvh, ut) `left` tiles in list
+// order; `tiles` in all.  span: CTAs from this one to the one that has the last tile of the unit
+// that this CTA's last tile belongs to (1: this one).
 struct Share {
-    int b, kvh, ut, j, left, R;
+    int b, kvh, ut, j, left, waves, tiles, span;
 };
 
 // One unit's part of a CTA's share: tiles j0 .. j1 - 1.
@@ -144,149 +152,232 @@ struct Walk {
     }
 };
 
-// A walk kept in shared memory, one per warp: warps whose registers are taken by their tiles read
-// what they need of the current piece from here.
-struct WalkState {
-    int b, kvh, ut, j, left, q0, n, p0;  // the walk
-    int sink, lo, nt, j0, j1;            // the piece (its unit is (b, kvh, ut) of the walk)
-    __device__ __forceinline__ int tile(int i) const volatile { return j0 + i < sink ? j0 + i : lo + (j0 + i - sink); }
-    __device__ __forceinline__ bool begun() const volatile { return j0 > 0; }
-    __device__ __forceinline__ bool open() const volatile { return j1 < nt; }
-};
-// The warp's next piece (all lanes take part); the first call starts the share.
-template <int BN>
-__device__ __forceinline__ bool walk_step(const PagedArgs &a, int TT, const volatile Share *sh, bool first,
-                                          volatile WalkState *w) {
-    Walk<BN> walk(a, TT, Share{0, 0, 0, 0, 0, 0});
-    if (first) {
-        walk = Walk<BN>(a, TT, Share{sh->b, sh->kvh, sh->ut, sh->j, sh->left, 0});
-    } else {
-        walk.b = w->b;
-        walk.kvh = w->kvh;
-        walk.ut = w->ut;
-        walk.j = w->j;
-        walk.left = w->left;
-        walk.s = Seq{w->q0, w->n, w->p0, true};
-    }
-    __syncwarp();
-    Piece p;
-    const bool more = walk.next(p);
-    if (more && (threadIdx.x & 31) == 0) {
-        w->b = walk.b;
-        w->kvh = walk.kvh;
-        w->ut = walk.ut;
-        w->j = walk.j;
-        w->left = walk.left;
-        w->q0 = walk.s.q0;
-        w->n = walk.s.n;
-        w->p0 = walk.s.p0;
-        w->sink = p.u.sink;
-        w->lo = p.u.lo;
-        w->nt = p.u.n;
-        w->j0 = p.j0;
-        w->j1 = p.j1;
-    }
-    __syncwarp();
-    return more;
-}
-
 __device__ __forceinline__ int piece_slot(const Piece &p) { return 2 * static_cast<int>(blockIdx.x) + (p.begun() ? 0 : 1); }
-__device__ __forceinline__ int4 open_record(const Piece &p, int R) {
-    return make_int4(1 + (p.u.n - p.j1 + R - 1) / R, p.b, p.kvh, p.ut);
+
+// Where a tile of the list lies: tile j of unit (b, kvh, ut), whose n tiles start at `at`.
+struct Place {
+    int b, kvh, ut, j, n;
+    long long at;
+};
+// Looks up tile X (within the list) with one warp; tiles: tiles of one kv head of each sequence.
+template <int BN>
+__device__ __forceinline__ Place find_place(const PagedArgs &a, int TT, const long long *tiles, long long X, int lane) {
+    Place r{0, 0, 0, 0, 0, 0};
+    long long before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const long long v = b0 + lane < a.B ? tiles[b0 + lane] * a.H_kv : 0;
+        long long inc = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += t;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + inc > X);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            before += __shfl_sync(0xffffffffu, inc - v, l);
+            r.b = b0 + l;
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    const long long per = max(tiles[r.b], 1ll), rel = X - before;
+    r.kvh = static_cast<int>(rel / per);
+    r.at = before + r.kvh * per;
+    const Seq s = load_seq(a, r.b);
+    const int nu = (s.n + TT - 1) / TT;
+    for (int u0 = 0; u0 < nu; u0 += 32) {
+        const int v = u0 + lane < nu ? unit_tiles<BN>(a, s, u0 + lane, TT).n : 0;
+        long long inc = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += t;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, r.at + inc > X);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            r.at += __shfl_sync(0xffffffffu, inc - v, l);
+            r.ut = u0 + l;
+            r.n = __shfl_sync(0xffffffffu, v, l);
+            break;
+        }
+        r.at += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    r.j = static_cast<int>(X - r.at);
+    return r;
 }
 
-// This CTA's share, found by the whole block (kThreads threads; tiles: scratch for B sums in
-// shared memory; two block barriers inside, the result valid after the last).  min_tiles: no
-// CTA gets fewer, so that short work is not cut into pieces that cost more than they save.
-template <int BN, int kThreads>
-__device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_tiles, long long *tiles,
-                                           Share *out, unsigned int *err) {
+constexpr int kMaxWaveCtas = 256;
+// Scratch of find_share: tiles [B] (64 bits), units [B], loads [CTAs].
+constexpr int kShareScratch = kPagedMaxB * 12 + kMaxWaveCtas * 4;
+
+// Unit u of the list goes to this CTA in wave u / grid.
+__device__ __forceinline__ int dealt_to(int u, int grid) {
+    const int w = u / grid, c = u - w * grid;
+    return w & 1 ? grid - 1 - c : c;
+}
+
+// This CTA's share, found by the whole block (kThreads threads; scratch in shared memory; block
+// barriers inside, the result valid after the last).  min_tiles: no stretch of the tail is
+// shorter, so that little work is not cut into pieces that cost more than they save.
+template <int BN, int kThreads, bool kWaves>
+__device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_tiles, uint8_t *scratch, Share *out,
+                                           unsigned int *err) {
     constexpr int kSerial = 4;  // units of a sequence that one thread counts
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // tiles of each sequence (one kv head): by one thread where there are few units
-    for (int b0 = warp * 32; b0 < a.B; b0 += kThreads) {
-        const int b = b0 + lane;
-        Seq s{};
-        if (b < a.B) {
-            s = load_seq(a, b);
-            if (!s.ok && blockIdx.x == 0) atomicOr(err, SWA_DEVERR_BAD_POSITION);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grid = static_cast<int>(gridDim.x);
+    long long *tiles = reinterpret_cast<long long *>(scratch);
+    int *units = reinterpret_cast<int *>(scratch + a.B * 8), *loads = units + a.B;
+    // visit(b, s, ut) for every unit of one kv head: by one thread for a sequence of few units, by
+    // the warp's lanes for one of many; done(b, nu) for every sequence afterwards
+    auto for_units = [&](auto visit, auto done) {
+        for (int b0 = warp * 32; b0 < a.B; b0 += kThreads) {
+            const int b = b0 + lane;
+            Seq s{};
+            if (b < a.B) s = load_seq(a, b);
+            const int nu = (s.n + TT - 1) / TT;
+            if (nu <= kSerial)
+                for (int ut = 0; ut < nu; ++ut) visit(b, s, ut);
+            unsigned many = __ballot_sync(0xffffffffu, nu > kSerial);
+            while (many) {
+                const int l = __ffs(many) - 1;
+                many &= many - 1;
+                Seq t{0, __shfl_sync(0xffffffffu, s.n, l), __shfl_sync(0xffffffffu, s.p0, l), true};
+                for (int ut = lane; ut < (t.n + TT - 1) / TT; ut += 32) visit(b0 + l, t, ut);
+            }
+            if (b < a.B) done(b, s, nu);
         }
-        const int nu = (s.n + TT - 1) / TT;
-        long long sum = 0;
-        if (nu <= kSerial)
-            for (int ut = 0; ut < nu; ++ut) sum += unit_tiles<BN>(a, s, ut, TT).n;
-        unsigned many = __ballot_sync(0xffffffffu, nu > kSerial);
-        while (many) {  // ... by the warp's lanes where there are many
-            const int l = __ffs(many) - 1;
-            many &= many - 1;
-            Seq t;
-            t.n = __shfl_sync(0xffffffffu, s.n, l);
-            t.p0 = __shfl_sync(0xffffffffu, s.p0, l);
-            long long part = 0;
-            for (int ut = lane; ut * static_cast<long long>(TT) < t.n; ut += 32) part += unit_tiles<BN>(a, t, ut, TT).n;
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-            if (lane == l) sum = part;
-        }
-        if (b < a.B) tiles[b] = sum;
-    }
+    };
+    for (int b = tid; b < a.B; b += kThreads) tiles[b] = 0;
     __syncthreads();
+    for_units(
+        [&](int b, const Seq &s, int ut) {
+            atomicAdd(reinterpret_cast<unsigned long long *>(tiles + b),
+                      static_cast<unsigned long long>(unit_tiles<BN>(a, s, ut, TT).n));
+        },
+        [&](int b, const Seq &s, int nu) {
+            if (!s.ok && blockIdx.x == 0) atomicOr(err, SWA_DEVERR_BAD_POSITION);
+            if (kWaves) units[b] = nu * a.H_kv;
+        });
+    __syncthreads();
+    int waves = 0;
+    if constexpr (kWaves) {
+        if (warp == 0) {  // first unit of each sequence
+            int before = 0;
+            for (int b0 = 0; b0 < a.B; b0 += 32) {
+                const int v = b0 + lane < a.B ? units[b0 + lane] : 0;
+                int inc = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int t = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += t;
+                }
+                if (b0 + lane < a.B) units[b0 + lane] = before + inc - v;
+                before += __shfl_sync(0xffffffffu, inc, 31);
+            }
+            if (lane == 0) out->waves = grid <= kMaxWaveCtas ? max(0, before / grid - 1) : 0;
+        }
+        __syncthreads();
+        waves = out->waves;
+        if (waves > 0) {  // tiles that the waves give each CTA
+            for (int c = tid; c < grid; c += kThreads) loads[c] = 0;
+            __syncthreads();
+            const int bulk = waves * grid;
+            for_units(
+                [&](int b, const Seq &s, int ut) {
+                    const int nu = (s.n + TT - 1) / TT, n = unit_tiles<BN>(a, s, ut, TT).n;
+                    for (int h = 0, u = units[b] + ut; h < a.H_kv && u < bulk; ++h, u += nu)
+                        atomicAdd(loads + dealt_to(u, grid), n);
+                },
+                [](int, const Seq &, int) {});
+            __syncthreads();
+        }
+    }
     if (warp == 0) {
         long long all = 0;
         for (int b = lane; b < a.B; b += 32) all += tiles[b];
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-        const long long total = all * a.H_kv, grid = gridDim.x;
-        const long long R = max((total + grid - 1) / grid, static_cast<long long>(min_tiles));
-        const long long X = R * blockIdx.x;
-        Share sh{0, 0, 0, 0, 0, 0};
-        if (X < total) {
-            sh.R = static_cast<int>(min(R, static_cast<long long>(INT_MAX)));
-            sh.left = static_cast<int>(min(static_cast<long long>(sh.R), total - X));
-            // the sequence that has tile X
-            long long before = 0;
-            int b0 = 0;
-            while (true) {
-                const long long v = b0 + lane < a.B ? tiles[b0 + lane] * a.H_kv : 0;
-                long long inc = v;
+        const long long total = all * a.H_kv;
+        const int c = static_cast<int>(blockIdx.x);
+        long long X, len, R = 0;    // this CTA's stretch of the list
+        int mine = 0;               // tiles from the waves
+        constexpr int kPer = kMaxWaveCtas / 32;
+        long long first[kPer];      // start of the stretch of CTA 32 * i + lane
+        if (waves == 0) {
+            R = max((total + grid - 1) / grid, static_cast<long long>(min_tiles));
+            X = R * c;
+            len = R;
+        } else {
+            // the level to which the tail fills the CTAs up: the least at which it all fits
+            int ld[kPer];
+            int top = 0;
+            long long bulk_tiles = 0;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += t;
+            for (int i = 0; i < kPer; ++i) {
+                const int ci = 32 * i + lane;
+                ld[i] = ci < grid ? loads[ci] : INT_MAX;
+                if (ci < grid) {
+                    bulk_tiles += ld[i];
+                    top = max(top, ld[i]);
                 }
-                const unsigned past = __ballot_sync(0xffffffffu, before + inc > X);
-                if (past) {
-                    const int l = __ffs(past) - 1;
-                    before += __shfl_sync(0xffffffffu, inc - v, l);
-                    sh.b = b0 + l;
-                    break;
-                }
-                before += __shfl_sync(0xffffffffu, inc, 31);
-                b0 += 32;
-                if (b0 >= a.B) break;  // (cannot be: X < total)
             }
-            const long long per = max(tiles[sh.b], 1ll), rel = X - before;
-            sh.kvh = static_cast<int>(rel / per);
-            // the block of tokens that has tile rel % per of its kv head
-            const Seq s = load_seq(a, sh.b);
-            long long r = rel % per;
-            const int nu = (s.n + TT - 1) / TT;
-            for (int u0 = 0; u0 < nu; u0 += 32) {
-                const int v = u0 + lane < nu ? unit_tiles<BN>(a, s, u0 + lane, TT).n : 0;
-                long long inc = v;
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) {
+                bulk_tiles += __shfl_xor_sync(0xffffffffu, bulk_tiles, o);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            }
+            const long long tail = total - bulk_tiles;
+            long long lo = 0, hi = top + (tail + grid - 1) / grid;
+            while (lo < hi) {
+                const long long mid = (lo + hi) >> 1;
+                long long room = 0;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) room += ld[i] < mid ? mid - ld[i] : 0;
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) room += __shfl_xor_sync(0xffffffffu, room, o);
+                if (room >= tail) hi = mid;
+                else lo = mid + 1;
+            }
+            long long at = bulk_tiles;
+            X = len = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const long long q = ld[i] < lo ? lo - ld[i] : 0;
+                long long inc = q;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const long long t = __shfl_up_sync(0xffffffffu, inc, o);
                     if (lane >= o) inc += t;
                 }
-                const unsigned past = __ballot_sync(0xffffffffu, inc > r);
-                if (past) {
-                    const int l = __ffs(past) - 1;
-                    sh.ut = u0 + l;
-                    sh.j = static_cast<int>(r - __shfl_sync(0xffffffffu, inc - v, l));
-                    break;
+                first[i] = at + inc - q;
+                if (i == c / 32) {
+                    X = __shfl_sync(0xffffffffu, first[i], c % 32);
+                    len = __shfl_sync(0xffffffffu, q, c % 32);
+                    mine = __shfl_sync(0xffffffffu, ld[i], c % 32);
                 }
-                r -= __shfl_sync(0xffffffffu, inc, 31);
+                at += __shfl_sync(0xffffffffu, inc, 31);
+            }
+        }
+        Share sh{0, 0, 0, 0, 0, waves, mine, 1};
+        len = min(len, total - X);
+        if (len > 0) {
+            const Place p = find_place<BN>(a, TT, tiles, X, lane), q = find_place<BN>(a, TT, tiles, X + len - 1, lane);
+            sh.b = p.b;
+            sh.kvh = p.kvh;
+            sh.ut = p.ut;
+            sh.j = p.j;
+            sh.left = static_cast<int>(len);
+            sh.tiles += sh.left;
+            const long long end = q.at + q.n;  // of the unit of the last tile
+            if (waves == 0) {
+                sh.span = 1 + static_cast<int>((end - X - len + R - 1) / R);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int ci = 32 * i + lane;
+                    sh.span += __popc(__ballot_sync(0xffffffffu, ci > c && ci < grid && first[i] < end));
+                }
             }
         }
         if (lane == 0) *out = sh;

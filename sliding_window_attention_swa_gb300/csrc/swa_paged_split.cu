@@ -96,7 +96,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
         tma_prefetch_desc(&tm_v);
     }
     // (its block barriers also publish the mbarriers)
-    find_share<CH, kThreads>(a, TT, min_tiles, reinterpret_cast<long long *>(sgen), &share, &g_psplit_data);
+    find_share<CH, kThreads, false>(a, TT, min_tiles, sgen, &share, &g_psplit_data);
     volatile int *abort = &abort_flag;
     // the merge grid may be scheduled from here on: its blocks wait (griddepcontrol.wait)
     // for this grid to complete before they read the partials
@@ -116,7 +116,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
         const int nbox = npg * (D / 64) * 2;            // copies of a stage, one lane each
         const int my_pg = lane % npg, my_c = (lane / npg) % (D / 64), my_v = lane / (npg * (D / 64));
         while (ok && walk.next(p)) {
-            if (p.open() && !p.begun()) open = open_record(p, sh.R);
+            if (p.open() && !p.begun()) open = make_int4(sh.span, p.b, p.kvh, p.ut);
             const int t0 = p.s.p0 + p.ut * TT, t1 = p.s.p0 + min(p.s.n, (p.ut + 1) * TT) - 1;
             const int lo = t0 >= a.window ? t0 - a.window + 1 : 0;
             auto entry = [&](int j) { return page_of(a, p.b, (p.u.tile(j) * CH + my_pg * box) >> a.ps_log2); };
@@ -168,7 +168,10 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
                 page = ahead;
             }
         }
-        if (lane == 0) ws.open[blockIdx.x] = ok ? open : make_int4(0, 0, 0, 0);
+        if (lane == 0) {
+            ws.open[blockIdx.x] = ok ? open : make_int4(0, 0, 0, 0);
+            ws.any[blockIdx.x] = sh.left > 0;
+        }
         if (!ok && lane == 0) {
             // drain the copies still in flight (at most the last NST stages)
             for (int s = max(0, seq - NST); s < seq; ++s) mbar_drain(bar_full(s % NST), (s / NST) & 1, &g_psplit_err);

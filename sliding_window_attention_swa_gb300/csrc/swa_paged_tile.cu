@@ -16,6 +16,8 @@
 //                   S  = Q K_j^T (A = Q from shared memory, at head dim 256 from tensor memory)
 //                   O += P V_j   (A = P from tensor memory)
 //   warp 2        Q loader.
+//   warp 3        planner: finds the CTA's pieces, up to NP ahead of the others, and hands them over
+//                 through shared memory, so that no other role spends its time on that.
 //   softmax WGs   NQT warpgroups; one row per thread (TMEM lane).  Running max in the log2
 //                 domain; P = 2^(x - m) is rounded to bf16 over the S columns it came from, the
 //                 row sum takes it unrounded; O is rescaled in TMEM only when a row's max grows by
@@ -49,6 +51,15 @@ __device__ unsigned int g_ptile_data = 0;  // broken device data
 constexpr int BM = 128;              // query rows per tile (TMEM lanes)
 constexpr float kRescaleTau = 8.0f;  // log2 units: rescale O when the max grows by > 2^8
 
+// A piece as the planner hands it to the other roles: tiles j0 .. j1 - 1 of unit (b, kvh, ut),
+// which has nt; q0, n, p0 of its sequence.  j0 == j1: there are no more.
+struct TilePiece {
+    int b, kvh, ut, q0, n, p0, sink, lo, nt, j0, j1;
+    __device__ __forceinline__ int tile(int i) const volatile { return j0 + i < sink ? j0 + i : lo + (j0 + i - sink); }
+    __device__ __forceinline__ bool begun() const volatile { return j0 > 0; }
+    __device__ __forceinline__ bool open() const volatile { return j1 < nt; }
+};
+
 template <int D>
 struct TileCfg {
     static constexpr int NQT = D <= 128 ? 2 : 1;    // query tiles per unit
@@ -71,13 +82,14 @@ struct TileCfg {
     static constexpr int OFF_X = OFF_RING + NSLOT * TBYTES;
     static constexpr int OFF_BAR = OFF_X + XBYTES;
     // q_full[2], q_empty[2], kv_full[NSLOT], kv_empty[NSLOT], s_full[2], p_full[2], o_done[2],
-    // o_free[2], meet, drain
-    static constexpr int NBAR = 2 * NSLOT + 14;
+    // o_free[2], meet, drain, piece_full[NP], piece_empty[NP]
+    static constexpr int NP = 4;  // pieces planned ahead
+    static constexpr int NBAR = 2 * NSLOT + 14 + 2 * NP;
     static constexpr int OFF_TMEMPTR = OFF_BAR + NBAR * 8;  // TMEM address, abort flag
     static constexpr int OFF_SHARE = OFF_TMEMPTR + 16;
-    static constexpr int OFF_WALK = OFF_SHARE + 32;
+    static constexpr int OFF_PIECE = OFF_SHARE + 32;
     // (all of it: the kernel has no static shared memory)
-    static constexpr int SMEM = OFF_WALK + THREADS / 32 * static_cast<int>(sizeof(WalkState));
+    static constexpr int SMEM = OFF_PIECE + NP * static_cast<int>(sizeof(TilePiece));
     static_assert(sizeof(Share) <= 32, "share");
     static constexpr uint32_t TMEM_COLS = 512;
     __host__ __device__ static constexpr uint32_t tm_s(int slot) { return static_cast<uint32_t>(slot * BN); }
@@ -86,7 +98,7 @@ struct TileCfg {
     static constexpr uint32_t TM_Q = 128;
     static_assert(NSLOT >= 3, "K/V ring too shallow");
     static_assert(SMEM <= 232448, "shared memory budget");
-    static_assert(NSLOT * TBYTES >= kPagedMaxB * 8, "scratch of the work split");
+    static_assert(NSLOT * TBYTES >= kShareScratch, "scratch of the work split");
     static_assert(!QTM || (tm_s(1) + BN <= TM_Q && TM_Q + D / 2 <= tm_o(0)), "query tile in tensor memory");
     static_assert(tm_o(NQT - 1) + D <= TMEM_COLS && tm_s(1) + BN <= 256, "tensor memory budget");
 };
@@ -135,6 +147,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     auto bar_of = [&](int i) { return bars + 8u * (10 + 2 * NSLOT + i); };
     const uint32_t bar_meet = bars + 8u * (12 + 2 * NSLOT);
     const uint32_t bar_drain = bars + 8u * (13 + 2 * NSLOT);
+    auto bar_piece = [&](int i) { return bars + 8u * (14 + 2 * NSLOT + i); };
+    auto bar_used = [&](int i) { return bars + 8u * (14 + 2 * NSLOT + C::NP + i); };
     // Ring fills are numbered over the CTA's share: 2g is the key tile, 2g + 1 the value tile of
     // its g-th tile; fill p lies in slot p % NSLOT.
     // Slot releases.  NQT = 1: value fills release (a tile's S MMAs precede its P V, so V_g's
@@ -179,6 +193,10 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             mbar_init(bar_full(s), 1);
             mbar_init(bar_empty(s), 1);
         }
+        for (int i = 0; i < C::NP; ++i) {
+            mbar_init(bar_piece(i), 1);
+            mbar_init(bar_used(i), 3 + 4 * NQT);  // the other roles' warps
+        }
         mbar_init(bar_meet, 8);
         mbar_init(bar_drain, 1);
         fence_mbar_init();
@@ -195,15 +213,27 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     const int TT = NQT * ta.TQ;
     tc_fence_before();
     // (its block barriers also publish the mbarriers and the TMEM address)
-    find_share<BN, C::THREADS>(a, TT, ta.min_tiles, reinterpret_cast<long long *>(sgen + C::OFF_RING), share,
-                               &g_ptile_data);
+    find_share<BN, C::THREADS, true>(a, TT, ta.min_tiles, sgen + C::OFF_RING, share, &g_ptile_data);
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     // the merge grid may be scheduled from here on: its blocks wait for this grid to complete
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Share sh = *share;
-    const int cta_tiles = sh.left;
-    volatile WalkState *wk = reinterpret_cast<volatile WalkState *>(sgen + C::OFF_WALK) + warp;
+    const int cta_tiles = share->tiles;
+    volatile TilePiece *pieces = reinterpret_cast<volatile TilePiece *>(sgen + C::OFF_PIECE);
+    // This warp's k-th piece (nullptr: there are no more, or a wait ran out: then ok is false); the
+    // warp gives it back once it has read all it needs of it.
+    auto get_piece = [&](int k, bool &ok) -> volatile TilePiece * {
+        if (!warp_wait(bar_piece(k % C::NP), (k / C::NP) & 1, abort)) {
+            ok = false;
+            return nullptr;
+        }
+        volatile TilePiece *p = pieces + k % C::NP;
+        return p->j1 > p->j0 ? p : nullptr;
+    };
+    auto give_back = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_used(k % C::NP));
+    };
     // a unit whose tokens fill one of its two query tiles at most (tokens: of its sequence)
     auto is_single = [&](int tokens, int ut) { return NQT == 2 && tokens - ut * TT <= ta.TQ; };
 
@@ -219,29 +249,34 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         struct Ref {
             int kvh, row, page;
         };
-        Walk<BN> walk(a, TT, sh);
-        Piece p;
-        p.j1 = 0;
-        int j = 0, lo = 0, t1 = 0, end = 0;
-        int4 open = make_int4(0, 0, 0, 0);
+        bool ok = true;
+        int np = 0, i = 0, n = 0;  // pieces taken, next tile of the current one, its tiles
+        int b = 0, kvh = 0, lo = 0, t1 = 0, end = 0, sink = 0, t_first = 0, j0 = 0;
         // this lane's box of the share's next tile
         auto next_tile = [&]() -> Ref {
-            if (j >= p.j1) {
-                if (!walk.next(p)) return Ref{0, 0, a.n_pages};
-                j = p.j0;
-                const int t0 = p.s.p0 + p.ut * TT;
-                t1 = p.s.p0 + min(p.s.n, (p.ut + 1) * TT) - 1;
+            if (i >= n) {
+                volatile TilePiece *p = get_piece(np, ok);
+                if (!p) return Ref{0, 0, a.n_pages};
+                i = 0;
+                n = p->j1 - p->j0;
+                b = p->b;
+                kvh = p->kvh;
+                j0 = p->j0;
+                sink = p->sink;
+                t_first = p->lo;
+                const int t0 = p->p0 + p->ut * TT;
+                t1 = p->p0 + min(p->n, (p->ut + 1) * TT) - 1;
                 lo = t0 >= a.window ? t0 - a.window + 1 : 0;
-                end = p.s.p0 + p.s.n;
-                if (p.open() && !p.begun()) open = open_record(p, sh.R);
+                end = p->p0 + p->n;
+                give_back(np++);
             }
-            const int kp = p.u.tile(j) * BN + my_pg * box;
-            ++j;
-            const int page = kp < end ? page_of(a, p.b, kp >> a.ps_log2) : a.n_pages;
+            const int j = j0 + i++;
+            const int kp = (j < sink ? j : t_first + (j - sink)) * BN + my_pg * box;
+            const int page = kp < end ? page_of(a, b, kp >> a.ps_log2) : a.n_pages;
             // a page that some row keeps a key of has to be there
             if (page == a.n_pages && kp <= t1 && (kp + box > lo || kp < a.n_sink))
                 atomicOr(&g_ptile_data, SWA_DEVERR_BAD_PAGE);
-            return Ref{p.kvh, kp & (a.ps - 1), page};
+            return Ref{kvh, kp & (a.ps - 1), page};
         };
         auto copy = [&](const Ref &r, bool is_v, int slot, uint32_t bar) {
             if (lane < nbox) {
@@ -268,21 +303,20 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         // planted fault: only the steps whose fills all lie below the stop run (step t issues
         // fills up to 2t + 2; the last step, fill nfill - 1 alone)
         const int n_steps = ta.fault_stop_fill >= nfill ? cta_tiles : max(0, (ta.fault_stop_fill - 1) / 2);
-        bool ok = n_steps == cta_tiles;
         if (nfill > 0) {
-            Ref cur = next_tile(), nxt = next_tile();
-            if (ta.fault_stop_fill > 0) {
+            Ref cur = next_tile(), nxt = cta_tiles > 1 ? next_tile() : cur;
+            if (ok && ta.fault_stop_fill > 0) {
                 if (lane == 0) mbar_arrive_expect_tx(bar_full(0), C::TBYTES);
                 __syncwarp();
                 copy(cur, false, 0, bar_full(0));  // K_0 alone
                 g = 1;
             }
 #pragma unroll 1
-            for (int t = 0; t < n_steps; ++t) {
+            for (int t = 0; t < n_steps && ok; ++t) {
                 const bool has_next = t + 1 < cta_tiles;
                 const Ref ahead = t + 2 < cta_tiles ? next_tile() : nxt;
                 const int pv = 2 * t + 1, own = has_next ? pv + 1 : pv;
-                if (!(slot_free(pv) && (!has_next || slot_free(own)))) {
+                if (!ok || !(slot_free(pv) && (!has_next || slot_free(own)))) {
                     ok = false;
                     break;
                 }
@@ -296,7 +330,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 nxt = ahead;
             }
         }
-        if (lane == 0) ta.ws.open[blockIdx.x] = ok ? open : make_int4(0, 0, 0, 0);
+        ok = ok && n_steps == cta_tiles;
         if (!ok && lane == 0) {
             // drain the owner barriers of the copies that may still be in flight: fills below
             // g - NSLOT have landed (their slots were released by readers that waited for them)
@@ -309,25 +343,27 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         int k = 0;
         int loads[2] = {0, 0};  // phases of each tile's barrier
         bool ok = true;
-        Walk<BN> walk(a, TT, sh);
-        Piece p;
 #pragma unroll 1
-        for (; ok && walk.next(p); ++k) {
+        for (; ok; ++k) {
+            volatile TilePiece *p = get_piece(k, ok);
+            if (!p) break;
+            const int tokens = p->n, i0 = p->ut * TT, q0 = p->q0, kvh = p->kvh;
+            give_back(k);
 #pragma unroll 1
             for (int x = 0; x < NQT; ++x) {
                 // the previous piece's S MMAs are done with this tile's shared memory
                 if (k >= 1) ok = warp_wait(bar_qe(x), (k - 1) & 1, abort);
                 if (!ok) break;
                 if (lane == 0) {
-                    const int i = p.ut * TT + x * ta.TQ;  // the tile's first token
-                    if (i < p.s.n) {
+                    const int i = i0 + x * ta.TQ;  // the tile's first token
+                    if (i < tokens) {
                         // debug build: the tile's tokens and its group's heads exist
-                        (void)SWA_IN_BOUNDS(p.s.q0 + i < a.N && (p.kvh + 1) * a.G <= a.H_q, &g_ptile_err);
+                        (void)SWA_IN_BOUNDS(q0 + i < a.N && (kvh + 1) * a.G <= a.H_q, &g_ptile_err);
                         mbar_arrive_expect_tx(bar_qf(x), static_cast<uint32_t>(a.G * ta.TQ * D * 2));
 #pragma unroll
                         for (int c = 0; c < D / 64; ++c)
-                            tma_load_4d(sQ + x * C::QBYTES + c * (BM * 128), &tm_q, bar_qf(x), c * 64, p.kvh * a.G,
-                                        p.s.q0 + i, 0);
+                            tma_load_4d(sQ + x * C::QBYTES + c * (BM * 128), &tm_q, bar_qf(x), c * 64, kvh * a.G,
+                                        q0 + i, 0);
                     } else {
                         mbar_arrive(bar_qf(x));  // the unit has no such tile
                     }
@@ -402,13 +438,17 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             return true;
         };
 #pragma unroll 1
-        for (; ok && walk_step<BN>(a, TT, share, k == 0, wk); ++k) {
-            const int n = wk->j1 - wk->j0;
+        for (; ok; ++k) {
+            volatile TilePiece *p = get_piece(k, ok);
+            if (!p) break;
+            const int n = p->j1 - p->j0;
+            const bool single = is_single(p->n, p->ut);
+            give_back(k);
             ok = warp_wait(bar_qf(0), k & 1, abort);
             // (the key tile of a later piece came with the value tile of the last one)
             if (ok && J == 0) ok = have_k(0);
             if (!ok) break;
-            if (NQT == 2 && !is_single(wk->n, wk->ut)) {
+            if (NQT == 2 && !single) {
                 mma_s(0, 0, J);
                 ok = warp_wait(bar_qf(1), k & 1, abort);
                 if (!ok) break;
@@ -502,7 +542,9 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         int J = 0, k = 0;
         uint32_t ns = 0, n_meet = 0;  // S tiles of this warpgroup's slot so far; single pieces so far
 #pragma unroll 1
-        for (; ok && walk_step<BN>(a, TT, share, k == 0, wk); ++k) {
+        for (; ok; ++k) {
+            volatile TilePiece *wk = get_piece(k, ok);
+            if (!wk) break;
             const int n = wk->j1 - wk->j0;
             const bool single = is_single(wk->n, wk->ut);
             const int t = wk->p0 + wk->ut * TT + (single ? 0 : wg * ta.TQ) + r / a.G;  // this row's position
@@ -759,11 +801,85 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     *reinterpret_cast<float2 *>(ta.ws.ml + prow * 2) = make_float2(m, l);
                 }
             }
+            give_back(k);
             J += n;
         }
     } else {
-        // idle warp of warpgroup 0 gives its registers to the softmax warpgroups
+        // ============================ planner ============================
         if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
+        const Share sh = *share;
+        bool ok = true;
+        int k = 0;
+        int4 open = make_int4(0, 0, 0, 0);
+        auto hand_over = [&](const Piece &p) {
+            if (ok && k >= C::NP) ok = warp_wait(bar_used(k % C::NP), (k / C::NP - 1) & 1, abort);
+            if (!ok) return;
+            if (lane == 0) {
+                volatile TilePiece *t = pieces + k % C::NP;
+                t->b = p.b;
+                t->kvh = p.kvh;
+                t->ut = p.ut;
+                t->q0 = p.s.q0;
+                t->n = p.s.n;
+                t->p0 = p.s.p0;
+                t->sink = p.u.sink;
+                t->lo = p.u.lo;
+                t->nt = p.u.n;
+                t->j0 = p.j0;
+                t->j1 = p.j1;
+                mbar_arrive(bar_piece(k % C::NP));
+            }
+            __syncwarp();
+            ++k;
+        };
+        Piece p{};
+        // whole units, one a wave: the sequences are searched 32 at a time from block b0, whose
+        // first unit is u0
+        int b0 = 0, u0 = 0;
+        for (int w = 0; w < sh.waves && ok; ++w) {
+            const int grid = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+            const int u = w * grid + (w & 1 ? grid - 1 - c : c);
+            while (b0 < a.B) {
+                Seq s{};
+                if (b0 + lane < a.B) s = load_seq(a, b0 + lane);
+                const int nu = (s.n + TT - 1) / TT, v = nu * a.H_kv;
+                int inc = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int t = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += t;
+                }
+                const unsigned past = __ballot_sync(0xffffffffu, u0 + inc > u);
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    const int rel = u - u0 - __shfl_sync(0xffffffffu, inc - v, l);
+                    const int units = max(__shfl_sync(0xffffffffu, nu, l), 1);
+                    p.b = b0 + l;
+                    p.kvh = rel / units;
+                    p.ut = rel % units;
+                    p.s = Seq{__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.n, l),
+                              __shfl_sync(0xffffffffu, s.p0, l), true};
+                    p.u = unit_tiles<BN>(a, p.s, p.ut, TT);
+                    p.j0 = 0;
+                    p.j1 = p.u.n;
+                    hand_over(p);
+                    break;
+                }
+                u0 += __shfl_sync(0xffffffffu, inc, 31);
+                b0 += 32;
+            }
+        }
+        Walk<BN> walk(a, TT, sh);
+        while (ok && walk.next(p)) {
+            if (p.open() && !p.begun()) open = make_int4(sh.span, p.b, p.kvh, p.ut);
+            hand_over(p);
+        }
+        p.j0 = p.j1 = 0;
+        hand_over(p);
+        if (lane == 0) {
+            ta.ws.open[blockIdx.x] = open;
+            ta.ws.any[blockIdx.x] = sh.left > 0;
+        }
     }
 
     tc_fence_before();

@@ -87,3 +87,71 @@ def test_tiles_cover_the_kept_keys(seed):
             # the count that the kernels compute
             behind = t - window + 1 if t >= window else 0
             assert len(kept) == t + 1 - behind + min(behind, n_sink)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_waves_and_tail(seed):
+    """The tile kernel's sharing from two units a CTA: whole units in waves of alternating direction,
+    the rest cut into stretches that fill every CTA up to one level."""
+    rng = random.Random(200 + seed)
+    BN, TT, grid = rng.choice([(64, 64, 7), (128, 64, 152), (128, 20, 31), (64, 128, 16)])
+    window, n_sink, H = rng.choice([1 << 31, 100, 1000]), rng.choice([0, 37]), rng.choice([1, 2, 8])
+    seqs = [(rng.choice([0, rng.randrange(5000)]), rng.choice([0, 1, rng.randrange(1, 2000)]))
+            for _ in range(rng.randrange(1, 60))]
+    us = units(seqs, H, TT, BN, window, n_sink)
+    waves = max(0, len(us) // grid - 1)
+    if waves == 0:
+        return
+    starts = [0]
+    for u in us:
+        starts.append(starts[-1] + u[3])
+    total, bulk = starts[-1], waves * grid
+
+    def dealt_to(u):
+        w, c = divmod(u, grid)
+        return grid - 1 - c if w & 1 else c
+
+    loads = [0] * grid
+    for u in range(bulk):
+        loads[dealt_to(u)] += us[u][3]
+    mine = [[w * grid + (grid - 1 - c if w & 1 else c) for w in range(waves)] for c in range(grid)]
+    assert sorted(u for m in mine for u in m) == list(range(bulk))
+    assert [sum(us[u][3] for u in m) for m in mine] == loads
+    tail = total - sum(loads)
+    lo, hi = 0, max(loads) + -(-tail // grid)
+    while lo < hi:
+        mid = (lo + hi) // 2
+        if sum(max(0, mid - x) for x in loads) >= tail:
+            hi = mid
+        else:
+            lo = mid + 1
+    at, first, left = sum(loads), [], []
+    for x in loads:
+        q = max(0, lo - x)
+        first.append(at)
+        left.append(max(0, min(q, total - at)))
+        at += q
+    assert sum(left) == tail
+    # no CTA has more than the level, unless its waves alone have
+    assert all(x + q <= max(lo, x) for x, q in zip(loads, left))
+    seen, slots, opened = set(), {}, {}
+    for c in range(grid):
+        if not left[c]:
+            continue
+        u = next(i for i in range(len(us)) if starts[i + 1] > first[c])
+        assert u >= bulk
+        last = next(i for i in range(len(us)) if starts[i + 1] > first[c] + left[c] - 1)
+        span = 1 + sum(x > c and first[x] < starts[last + 1] for x in range(grid))
+        for u, j0, j1 in walk(us, (u, first[c] - starts[u], left[c])):
+            for j in range(j0, j1):
+                assert (u, j) not in seen
+                seen.add((u, j))
+            if j0 > 0:
+                slots[u].append(c)
+            elif j1 < us[u][3]:
+                slots[u] = [c]
+                opened[c] = (span, u)
+    assert len(seen) == tail
+    for c, (span, u) in opened.items():
+        # the CTAs that the merge looks at, but for those without tiles, have exactly the unit's pieces
+        assert slots[u] == [x for x in range(c, c + span) if left[x]]
