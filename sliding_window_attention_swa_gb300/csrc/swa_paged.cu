@@ -64,18 +64,27 @@ __global__ void __launch_bounds__(kThreads) paged_merge_kernel(const PagedArgs a
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int4 rec = w.open[blockIdx.x];
-    const int np = rec.x;
-    if (np == 0) return;
+    const long long start = w.first[blockIdx.x];
+    const int own = w.left[blockIdx.x], c = static_cast<int>(blockIdx.x);
+    if (rec.x == 0) return;
+    // the unit's tiles end at `end` of the list: CTAs c + 1 .. c + np - 1 start before that
+    const long long end = start + own + rec.x;
+    int np = 1;
+    for (int k0 = c + 1; k0 < x.ctas; k0 += 32) {
+        const int n = __popc(__ballot_sync(0xffffffffu, k0 + lane < x.ctas && w.first[k0 + lane] < end));
+        np += n;
+        if (n < 32) break;
+    }
     const int row = blockIdx.y * kMergeRows + warp;  // of the unit: tile * x.rows + token * G + head
     const int tile = row / x.rows, r = row % x.rows;
     const Seq s = load_seq(a, rec.y);
     const int i = (rec.w * x.tiles + tile) * x.TQ + r / a.G;  // token of the sequence
     if (tile >= x.tiles || r >= x.TQ * a.G || i >= s.n) return;
     const int rows = x.tiles * x.rows;
-    auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)) * rows + row; };
+    auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)); };
     // (a CTA between two of the unit's may have no tiles of it)
     auto piece = [&](int k) {
-        return k == 0 || w.any[blockIdx.x + k] ? *reinterpret_cast<const float2 *>(w.ml + slot(k) * 2)
+        return k == 0 || w.left[c + k] > 0 ? *reinterpret_cast<const float2 *>(w.ml + (slot(k) * rows + row) * 2)
                                                : make_float2(-INFINITY, 0.f);
     };
     float m = -INFINITY;
@@ -95,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) paged_merge_kernel(const PagedArgs a
         for (int k = 0; k < n; ++k) {
             const float fk = __shfl_sync(0xffffffffu, f, k);
             if (fk == 0.f) continue;  // (nothing kept, or nothing written)
-            const float *v = w.acc + slot(k0 + k) * D + lane * E;
+            const float *v = w.acc + partial_at<D>(slot(k0 + k), rows, row, lane * E);
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
                 const float2 t = *reinterpret_cast<const float2 *>(v + e);

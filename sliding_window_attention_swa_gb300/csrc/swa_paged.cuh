@@ -94,11 +94,11 @@ __device__ __forceinline__ UnitTiles unit_tiles(const PagedArgs &a, const Seq &s
     return u;
 }
 
-// A CTA's share: `waves` whole units, then from tile j of unit (b, kvh, ut) `left` tiles in list
-// order; `tiles` in all.  span: CTAs from this one to the one that has the last tile of the unit
-// that this CTA's last tile belongs to (1: this one).
+// A CTA's share: `waves` whole units, then from tile j of unit (b, kvh, ut), tile `first` of the
+// list, `left` tiles in list order; `tiles` in all.
 struct Share {
-    int b, kvh, ut, j, left, waves, tiles, span;
+    long long first;
+    int b, kvh, ut, j, left, waves, tiles;
 };
 
 // One unit's part of a CTA's share: tiles j0 .. j1 - 1.
@@ -152,17 +152,20 @@ struct Walk {
     }
 };
 
+// Element (row, col) of the partial results of a slot of `rows` rows: 8 columns of a row together,
+// then the same columns of the next row, so that a warp whose lanes have a row each stores whole
+// lines.
+template <int D>
+__device__ __forceinline__ int64_t partial_at(int64_t slot, int rows, int row, int col) {
+    return ((slot * (D / 8) + col / 8) * rows + row) * 8 + col % 8;
+}
 __device__ __forceinline__ int piece_slot(const Piece &p) { return 2 * static_cast<int>(blockIdx.x) + (p.begun() ? 0 : 1); }
 
-// Where a tile of the list lies: tile j of unit (b, kvh, ut), whose n tiles start at `at`.
-struct Place {
-    int b, kvh, ut, j, n;
-    long long at;
-};
-// Looks up tile X (within the list) with one warp; tiles: tiles of one kv head of each sequence.
+// Tile X of the list, looked up by one warp, as the start of a share; tiles: tiles of one kv head
+// of each sequence.
 template <int BN>
-__device__ __forceinline__ Place find_place(const PagedArgs &a, int TT, const long long *tiles, long long X, int lane) {
-    Place r{0, 0, 0, 0, 0, 0};
+__device__ __forceinline__ void find_tile(const PagedArgs &a, int TT, const long long *tiles, long long X, int lane,
+                                          Share &r) {
     long long before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
         const long long v = b0 + lane < a.B ? tiles[b0 + lane] * a.H_kv : 0;
@@ -181,9 +184,9 @@ __device__ __forceinline__ Place find_place(const PagedArgs &a, int TT, const lo
         }
         before += __shfl_sync(0xffffffffu, inc, 31);
     }
-    const long long per = max(tiles[r.b], 1ll), rel = X - before;
-    r.kvh = static_cast<int>(rel / per);
-    r.at = before + r.kvh * per;
+    const long long per = max(tiles[r.b], 1ll);
+    r.kvh = static_cast<int>((X - before) / per);
+    long long rel = X - before - r.kvh * per;
     const Seq s = load_seq(a, r.b);
     const int nu = (s.n + TT - 1) / TT;
     for (int u0 = 0; u0 < nu; u0 += 32) {
@@ -194,25 +197,22 @@ __device__ __forceinline__ Place find_place(const PagedArgs &a, int TT, const lo
             const long long t = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += t;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, r.at + inc > X);
+        const unsigned past = __ballot_sync(0xffffffffu, inc > rel);
         if (past) {
             const int l = __ffs(past) - 1;
-            r.at += __shfl_sync(0xffffffffu, inc - v, l);
             r.ut = u0 + l;
-            r.n = __shfl_sync(0xffffffffu, v, l);
+            r.j = static_cast<int>(rel - __shfl_sync(0xffffffffu, inc - v, l));
             break;
         }
-        r.at += __shfl_sync(0xffffffffu, inc, 31);
+        rel -= __shfl_sync(0xffffffffu, inc, 31);
     }
-    r.j = static_cast<int>(X - r.at);
-    return r;
 }
 
 constexpr int kMaxWaveCtas = 256;
-// Scratch of find_share: tiles [B] (64 bits), units [B], loads [CTAs].
-constexpr int kShareScratch = kPagedMaxB * 12 + kMaxWaveCtas * 4;
+// Scratch of find_share: tiles [B] (64 bits), first units [B + 1], loads [CTAs].
+constexpr int kShareScratch = kPagedMaxB * 12 + 4 + kMaxWaveCtas * 4;
 
-// Unit u of the list goes to this CTA in wave u / grid.
+// The CTA that unit u of the list goes to, in wave u / grid.
 __device__ __forceinline__ int dealt_to(int u, int grid) {
     const int w = u / grid, c = u - w * grid;
     return w & 1 ? grid - 1 - c : c;
@@ -224,75 +224,78 @@ __device__ __forceinline__ int dealt_to(int u, int grid) {
 template <int BN, int kThreads, bool kWaves>
 __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_tiles, uint8_t *scratch, Share *out,
                                            unsigned int *err) {
-    constexpr int kSerial = 4;  // units of a sequence that one thread counts
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grid = static_cast<int>(gridDim.x);
     long long *tiles = reinterpret_cast<long long *>(scratch);
-    int *units = reinterpret_cast<int *>(scratch + a.B * 8), *loads = units + a.B;
-    // visit(b, s, ut) for every unit of one kv head: by one thread for a sequence of few units, by
-    // the warp's lanes for one of many; done(b, nu) for every sequence afterwards
-    auto for_units = [&](auto visit, auto done) {
-        for (int b0 = warp * 32; b0 < a.B; b0 += kThreads) {
-            const int b = b0 + lane;
-            Seq s{};
-            if (b < a.B) s = load_seq(a, b);
-            const int nu = (s.n + TT - 1) / TT;
-            if (nu <= kSerial)
-                for (int ut = 0; ut < nu; ++ut) visit(b, s, ut);
-            unsigned many = __ballot_sync(0xffffffffu, nu > kSerial);
-            while (many) {
-                const int l = __ffs(many) - 1;
-                many &= many - 1;
-                Seq t{0, __shfl_sync(0xffffffffu, s.n, l), __shfl_sync(0xffffffffu, s.p0, l), true};
-                for (int ut = lane; ut < (t.n + TT - 1) / TT; ut += 32) visit(b0 + l, t, ut);
-            }
-            if (b < a.B) done(b, s, nu);
-        }
-    };
-    for (int b = tid; b < a.B; b += kThreads) tiles[b] = 0;
+    int *units = reinterpret_cast<int *>(scratch + a.B * 8), *loads = units + a.B + 1;
+    // 1. units of one kv head of each sequence, 2. their running sum
+    for (int b = tid; b < a.B; b += kThreads) {
+        const Seq s = load_seq(a, b);
+        if (!s.ok && blockIdx.x == 0) atomicOr(err, SWA_DEVERR_BAD_POSITION);
+        units[b] = (s.n + TT - 1) / TT;
+        tiles[b] = 0;
+    }
+    if (kWaves && grid <= kMaxWaveCtas)
+        for (int c = tid; c < grid; c += kThreads) loads[c] = 0;
     __syncthreads();
-    for_units(
-        [&](int b, const Seq &s, int ut) {
-            atomicAdd(reinterpret_cast<unsigned long long *>(tiles + b),
-                      static_cast<unsigned long long>(unit_tiles<BN>(a, s, ut, TT).n));
-        },
-        [&](int b, const Seq &s, int nu) {
-            if (!s.ok && blockIdx.x == 0) atomicOr(err, SWA_DEVERR_BAD_POSITION);
-            if (kWaves) units[b] = nu * a.H_kv;
-        });
-    __syncthreads();
-    int waves = 0;
-    if constexpr (kWaves) {
-        if (warp == 0) {  // first unit of each sequence
-            int before = 0;
-            for (int b0 = 0; b0 < a.B; b0 += 32) {
-                const int v = b0 + lane < a.B ? units[b0 + lane] : 0;
-                int inc = v;
+    if (warp == 0) {
+        int before = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const int v = b0 + lane < a.B ? units[b0 + lane] : 0;
+            int inc = v;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int t = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += t;
-                }
-                if (b0 + lane < a.B) units[b0 + lane] = before + inc - v;
-                before += __shfl_sync(0xffffffffu, inc, 31);
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += t;
             }
-            if (lane == 0) out->waves = grid <= kMaxWaveCtas ? max(0, before / grid - 1) : 0;
+            if (b0 + lane < a.B) units[b0 + lane] = before + inc - v;
+            before += __shfl_sync(0xffffffffu, inc, 31);
         }
-        __syncthreads();
-        waves = out->waves;
-        if (waves > 0) {  // tiles that the waves give each CTA
-            for (int c = tid; c < grid; c += kThreads) loads[c] = 0;
-            __syncthreads();
-            const int bulk = waves * grid;
-            for_units(
-                [&](int b, const Seq &s, int ut) {
-                    const int nu = (s.n + TT - 1) / TT, n = unit_tiles<BN>(a, s, ut, TT).n;
-                    for (int h = 0, u = units[b] + ut; h < a.H_kv && u < bulk; ++h, u += nu)
-                        atomicAdd(loads + dealt_to(u, grid), n);
-                },
-                [](int, const Seq &, int) {});
-            __syncthreads();
+        if (lane == 0) units[a.B] = before;
+    }
+    __syncthreads();
+    // 3. tiles of every sequence, and those that the waves give each CTA: a thread per unit
+    const int n_units = units[a.B];  // of one kv head
+    const long long all_units = static_cast<long long>(n_units) * a.H_kv;
+    const int waves = kWaves && grid <= kMaxWaveCtas && all_units < (1 << 26)
+                          ? max(0, static_cast<int>(all_units) / grid - 1)
+                          : 0;
+    for (int x0 = warp * 32; x0 < n_units; x0 += kThreads) {
+        const int x = x0 + lane;
+        int b = 0, len = a.B;  // the last sequence whose first unit is <= x
+        while (len > 1) {
+            const int half = len >> 1;
+            if (units[b + half] <= x) {
+                b += half;
+                len -= half;
+            } else {
+                len = half;
+            }
+        }
+        const bool in = x < n_units;
+        int n = 0;
+        if (in) {
+            const Seq s = load_seq(a, b);
+            const int ut = x - units[b];
+            n = unit_tiles<BN>(a, s, ut, TT).n;
+            if (waves > 0) {
+                const int nu = (s.n + TT - 1) / TT;
+                for (int h = 0, u = units[b] * a.H_kv + ut; h < a.H_kv && u < waves * grid; ++h, u += nu)
+                    atomicAdd(loads + dealt_to(u, grid), n);
+            }
+        }
+        // (lanes of one sequence add up first)
+        const int b_first = __shfl_sync(0xffffffffu, b, 0);
+        if (__all_sync(0xffffffffu, !in || b == b_first)) {
+            long long sum = n;
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long *>(tiles + b), static_cast<unsigned long long>(sum));
+        } else if (in) {
+            atomicAdd(reinterpret_cast<unsigned long long *>(tiles + b), static_cast<unsigned long long>(n));
         }
     }
+    __syncthreads();
+    // 4. this CTA's stretch of the list
     if (warp == 0) {
         long long all = 0;
         for (int b = lane; b < a.B; b += 32) all += tiles[b];
@@ -300,86 +303,61 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
         for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
         const long long total = all * a.H_kv;
         const int c = static_cast<int>(blockIdx.x);
-        long long X, len, R = 0;    // this CTA's stretch of the list
-        int mine = 0;               // tiles from the waves
-        constexpr int kPer = kMaxWaveCtas / 32;
-        long long first[kPer];      // start of the stretch of CTA 32 * i + lane
+        Share sh{0, 0, 0, 0, 0, 0, waves, 0};
+        long long len;
         if (waves == 0) {
-            R = max((total + grid - 1) / grid, static_cast<long long>(min_tiles));
-            X = R * c;
-            len = R;
+            len = max((total + grid - 1) / grid, static_cast<long long>(min_tiles));
+            sh.first = len * c;
         } else {
-            // the level to which the tail fills the CTAs up: the least at which it all fits
-            int ld[kPer];
-            int top = 0;
-            long long bulk_tiles = 0;
+            // the tail fills the CTAs up to one level: the least at which all of it fits
+            constexpr int kPer = kMaxWaveCtas / 32;
+            int ld[kPer], top = 0;
+            long long bulk = 0;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                const int ci = 32 * i + lane;
-                ld[i] = ci < grid ? loads[ci] : INT_MAX;
-                if (ci < grid) {
-                    bulk_tiles += ld[i];
+                ld[i] = 32 * i + lane < grid ? loads[32 * i + lane] : INT_MAX;
+                if (32 * i + lane < grid) {
+                    bulk += ld[i];
                     top = max(top, ld[i]);
                 }
             }
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) {
-                bulk_tiles += __shfl_xor_sync(0xffffffffu, bulk_tiles, o);
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            }
-            const long long tail = total - bulk_tiles;
-            long long lo = 0, hi = top + (tail + grid - 1) / grid;
-            while (lo < hi) {
-                const long long mid = (lo + hi) >> 1;
-                long long room = 0;
+            for (int o = 16; o >= 1; o >>= 1) bulk += __shfl_xor_sync(0xffffffffu, bulk, o);
+            top = __reduce_max_sync(0xffffffffu, top);
+            const long long tail = total - bulk;
+            int level = static_cast<int>((total + grid - 1) / grid);
+            if (top > level) {  // (some waves alone are above the mean: the others share what is left)
+                int lo = level, hi = top + static_cast<int>((tail + grid - 1) / grid);
+                while (lo < hi) {
+                    const int mid = lo + ((hi - lo) >> 1);
+                    long long room = 0;
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) room += ld[i] < mid ? mid - ld[i] : 0;
+                    for (int i = 0; i < kPer; ++i) room += ld[i] < mid ? mid - ld[i] : 0;
 #pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) room += __shfl_xor_sync(0xffffffffu, room, o);
-                if (room >= tail) hi = mid;
-                else lo = mid + 1;
+                    for (int o = 16; o >= 1; o >>= 1) room += __shfl_xor_sync(0xffffffffu, room, o);
+                    if (room >= tail) hi = mid;
+                    else lo = mid + 1;
+                }
+                level = lo;
             }
-            long long at = bulk_tiles;
-            X = len = 0;
+            // before this CTA's stretch: those of the CTAs below
+            long long before = 0;
+            int mine = 0;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                const long long q = ld[i] < lo ? lo - ld[i] : 0;
-                long long inc = q;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += t;
-                }
-                first[i] = at + inc - q;
-                if (i == c / 32) {
-                    X = __shfl_sync(0xffffffffu, first[i], c % 32);
-                    len = __shfl_sync(0xffffffffu, q, c % 32);
-                    mine = __shfl_sync(0xffffffffu, ld[i], c % 32);
-                }
-                at += __shfl_sync(0xffffffffu, inc, 31);
+                if (32 * i + lane < c) before += ld[i] < level ? level - ld[i] : 0;
+                if (32 * i + lane == c) mine = ld[i];
             }
-        }
-        Share sh{0, 0, 0, 0, 0, waves, mine, 1};
-        len = min(len, total - X);
-        if (len > 0) {
-            const Place p = find_place<BN>(a, TT, tiles, X, lane), q = find_place<BN>(a, TT, tiles, X + len - 1, lane);
-            sh.b = p.b;
-            sh.kvh = p.kvh;
-            sh.ut = p.ut;
-            sh.j = p.j;
-            sh.left = static_cast<int>(len);
-            sh.tiles += sh.left;
-            const long long end = q.at + q.n;  // of the unit of the last tile
-            if (waves == 0) {
-                sh.span = 1 + static_cast<int>((end - X - len + R - 1) / R);
-            } else {
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const int ci = 32 * i + lane;
-                    sh.span += __popc(__ballot_sync(0xffffffffu, ci > c && ci < grid && first[i] < end));
-                }
-            }
+            for (int o = 16; o >= 1; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+            sh.tiles = __shfl_sync(0xffffffffu, mine, c % 32);
+            sh.first = bulk + before;
+            len = max(0, level - sh.tiles);
         }
+        sh.first = min(sh.first, total);
+        sh.left = static_cast<int>(min(len, total - sh.first));
+        sh.tiles += sh.left;
+        if (sh.left > 0) find_tile<BN>(a, TT, tiles, sh.first, lane, sh);
         if (lane == 0) *out = sh;
     }
     __syncthreads();

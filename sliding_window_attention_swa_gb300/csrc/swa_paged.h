@@ -36,11 +36,10 @@ constexpr int kPagedMaxB = 8192;
 // last unit can be).
 struct PagedWs {
     float *ml;   // [2 * CTAs][rows][2]: maximum (log2 units), sum
-    float *acc;  // [2 * CTAs][rows][D]: unnormalised weighted values
-    // [CTAs] {CTAs that share the unit left open (0: none), b, kvh, ut}, and whether the CTA has
-    // tiles of a shared-out list at all
-    int4 *open;
-    int32_t *any;
+    float *acc;  // [2 * CTAs][D / 8][rows][8]: unnormalised weighted values
+    int4 *open;        // [CTAs] {tiles that the unit left open still has for later CTAs (0: none), b, kvh, ut}
+    long long *first;  // [CTAs] where its stretch of the list starts
+    int32_t *left;     // [CTAs] and its tiles
 };
 // A kernel's grid and the shape of its units: tiles of query rows (row r of a tile is token
 // r / G, head r % G of the group), tokens a tile.
@@ -51,7 +50,7 @@ inline size_t paged_ws_bytes(const PagedShape &x, int D) {
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     const size_t rows = static_cast<size_t>(x.ctas) * 2 * x.tiles * x.rows;
     return up(rows * 2 * sizeof(float)) + up(rows * D * sizeof(float)) + up(x.ctas * sizeof(int4)) +
-           up(x.ctas * sizeof(int32_t));
+           up(x.ctas * sizeof(long long)) + up(x.ctas * sizeof(int32_t));
 }
 inline PagedWs paged_carve(void *ws, const PagedShape &x, int D) {
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
@@ -64,7 +63,9 @@ inline PagedWs paged_carve(void *ws, const PagedShape &x, int D) {
     p += up(rows * D * sizeof(float));
     w.open = reinterpret_cast<int4 *>(p);
     p += up(x.ctas * sizeof(int4));
-    w.any = reinterpret_cast<int32_t *>(p);
+    w.first = reinterpret_cast<long long *>(p);
+    p += up(x.ctas * sizeof(long long));
+    w.left = reinterpret_cast<int32_t *>(p);
     return w;
 }
 

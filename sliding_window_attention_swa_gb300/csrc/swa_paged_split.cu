@@ -116,7 +116,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
         const int nbox = npg * (D / 64) * 2;            // copies of a stage, one lane each
         const int my_pg = lane % npg, my_c = (lane / npg) % (D / 64), my_v = lane / (npg * (D / 64));
         while (ok && walk.next(p)) {
-            if (p.open() && !p.begun()) open = make_int4(sh.span, p.b, p.kvh, p.ut);
+            if (p.open() && !p.begun()) open = make_int4(p.u.n - p.j1, p.b, p.kvh, p.ut);
             const int t0 = p.s.p0 + p.ut * TT, t1 = p.s.p0 + min(p.s.n, (p.ut + 1) * TT) - 1;
             const int lo = t0 >= a.window ? t0 - a.window + 1 : 0;
             auto entry = [&](int j) { return page_of(a, p.b, (p.u.tile(j) * CH + my_pg * box) >> a.ps_log2); };
@@ -170,7 +170,8 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
         }
         if (lane == 0) {
             ws.open[blockIdx.x] = ok ? open : make_int4(0, 0, 0, 0);
-            ws.any[blockIdx.x] = sh.left > 0;
+            ws.first[blockIdx.x] = sh.first;
+            ws.left[blockIdx.x] = sh.left;
         }
         if (!ok && lane == 0) {
             // drain the copies still in flight (at most the last NST stages)
@@ -385,7 +386,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
                         *reinterpret_cast<uint2 *>(o + col) = make_uint2(pack_bf16x2(acc4.x * inv, acc4.y * inv),
                                                                          pack_bf16x2(acc4.z * inv, acc4.w * inv));
                     else
-                        *reinterpret_cast<float4 *>(ws.acc + slot * D + col) = acc4;
+                        *reinterpret_cast<float4 *>(ws.acc + partial_at<D>(slot / ROWS, ROWS, r, col)) = acc4;
                 }
                 if (part == 0) {
                     if (whole) {

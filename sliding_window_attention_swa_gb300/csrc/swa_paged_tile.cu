@@ -9,7 +9,7 @@
 // Roles:
 //   warp 0        K/V producer: K_0, V_0, K_1, V_1, ... of every piece into a ring of NSLOT
 //                 shared-memory slots by TMA, one box per page (or part of a page) and 64 elements
-//                 of the head, one lane each; the pages are looked up two tiles ahead.  V_j and
+//                 of the head; the pages are looked up two tiles ahead.  V_j and
 //                 K_{j+1} are copied together and signal one barrier, that of K_{j+1}'s slot.
 //                 Pages past the sequence's end or not there read past the pool: zeros.
 //   warp 1        TMEM owner and MMA issuer (warp-uniform loop, one elected lane issues):
@@ -87,10 +87,10 @@ struct TileCfg {
     static constexpr int NBAR = 2 * NSLOT + 14 + 2 * NP;
     static constexpr int OFF_TMEMPTR = OFF_BAR + NBAR * 8;  // TMEM address, abort flag
     static constexpr int OFF_SHARE = OFF_TMEMPTR + 16;
-    static constexpr int OFF_PIECE = OFF_SHARE + 32;
+    static constexpr int OFF_PIECE = OFF_SHARE + 48;
     // (all of it: the kernel has no static shared memory)
     static constexpr int SMEM = OFF_PIECE + NP * static_cast<int>(sizeof(TilePiece));
-    static_assert(sizeof(Share) <= 32, "share");
+    static_assert(sizeof(Share) <= 48, "share");
     static constexpr uint32_t TMEM_COLS = 512;
     __host__ __device__ static constexpr uint32_t tm_s(int slot) { return static_cast<uint32_t>(slot * BN); }
     __host__ __device__ static constexpr uint32_t tm_o(int tile) { return 256u + static_cast<uint32_t>(tile * 128); }
@@ -242,21 +242,20 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
         // the scratch of the work split lies in the ring: order its generic accesses before the copies
         fence_proxy_async_smem();
-        // a tile is npg boxes (pages or parts of one) times D / 64 column blocks, one lane each
-        const int box = min(a.ps, BN), npg = BN / box, nbox = npg * (D / 64);
-        const int my_pg = lane % npg, my_c = lane / npg;
-        const uint32_t my_off = static_cast<uint32_t>(my_c * (BN * 128) + my_pg * box * 128);
-        struct Ref {
-            int kvh, row, page;
+        // A tile is npg boxes (pages or a part of one) times D / 64 column blocks.  The pages are looked
+        // up 32 boxes at a time, lane i that of box i, a group ahead of their use.
+        const int box = min(a.ps, BN), npg = BN / box, per_group = 32 / npg;
+        struct Group {
+            int tiles, kvh, row, entry;  // row, entry: of this lane's box
+            bool need;                   // some query row keeps a key of this lane's box
         };
         bool ok = true;
         int np = 0, i = 0, n = 0;  // pieces taken, next tile of the current one, its tiles
-        int b = 0, kvh = 0, lo = 0, t1 = 0, end = 0, sink = 0, t_first = 0, j0 = 0;
-        // this lane's box of the share's next tile
-        auto next_tile = [&]() -> Ref {
+        int b = 0, kvh = 0, lo = 0, t1 = 0, end = 0, sink = 0, t_first = 0, j0 = 0, looked = 0;
+        auto look_up = [&]() -> Group {
             if (i >= n) {
                 volatile TilePiece *p = get_piece(np, ok);
-                if (!p) return Ref{0, 0, a.n_pages};
+                if (!p) return Group{INT_MAX, 0, 0, -1, false};
                 i = 0;
                 n = p->j1 - p->j0;
                 b = p->b;
@@ -270,21 +269,42 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 end = p->p0 + p->n;
                 give_back(np++);
             }
-            const int j = j0 + i++;
-            const int kp = (j < sink ? j : t_first + (j - sink)) * BN + my_pg * box;
-            const int page = kp < end ? page_of(a, b, kp >> a.ps_log2) : a.n_pages;
-            // a page that some row keeps a key of has to be there
-            if (page == a.n_pages && kp <= t1 && (kp + box > lo || kp < a.n_sink))
-                atomicOr(&g_ptile_data, SWA_DEVERR_BAD_PAGE);
-            return Ref{kvh, kp & (a.ps - 1), page};
+            const int tiles = min(n - i, per_group), j = j0 + i + lane / npg;
+            const int kp = (j < sink ? j : t_first + (j - sink)) * BN + lane % npg * box;
+            const bool there = lane < tiles * npg && kp < end;
+            i += tiles;
+            looked += tiles;
+            return Group{tiles, kvh, kp & (a.ps - 1),
+                         there ? __ldg(a.table + static_cast<int64_t>(b) * a.width + (kp >> a.ps_log2)) : -1,
+                         there && kp <= t1 && (kp + box > lo || kp < a.n_sink)};
         };
-        auto copy = [&](const Ref &r, bool is_v, int slot, uint32_t bar) {
-            if (lane < nbox) {
-                // debug build: the box lies in the page, the head exists
-                (void)SWA_IN_BOUNDS(r.row + box <= a.ps && r.kvh < a.H_kv && r.page <= a.n_pages, &g_ptile_err);
-                tma_load_4d(sRing + slot * C::TBYTES + my_off, is_v ? &tm_v : &tm_k, bar, my_c * 64, r.row, r.kvh,
-                            r.page);
+        // A step copies a tile's values (lanes 16 ..) and the next tile's keys (lanes 0 ..), one lane a
+        // box: lanes issue faster than one lane that walks through the boxes.
+        const int my = lane & 15, my_pg = my % npg, my_c = my / npg;
+        const bool my_v = lane >= 16, mine = my < npg * (D / 64);
+        const uint32_t my_off = static_cast<uint32_t>(my_c * (BN * 128) + my_pg * box * 128);
+        struct Ref {  // this lane's box of a tile
+            int kvh, row, page;
+        };
+        Group now{0, 0, 0, 0, false}, then{0, 0, 0, 0, false};
+        int at = 0, page = 0;  // next tile of the group; this lane's page
+        auto next_tile = [&]() -> Ref {
+            if (at >= now.tiles) {
+                now = then;
+                if (looked < cta_tiles) then = look_up();
+                at = 0;
+                const bool in_pool = static_cast<unsigned>(now.entry) < static_cast<unsigned>(a.n_pages);
+                page = in_pool ? now.entry : a.n_pages;
+                if (now.need && !in_pool) atomicOr(&g_ptile_data, SWA_DEVERR_BAD_PAGE);
             }
+            const int from = (at * npg + my_pg) & 31;
+            ++at;
+            return Ref{now.kvh, __shfl_sync(0xffffffffu, now.row, from), __shfl_sync(0xffffffffu, page, from)};
+        };
+        auto copy = [&](const Ref &r, int slot, uint32_t bar) {
+            // debug build: the box lies in the page, the head exists
+            (void)SWA_IN_BOUNDS(r.row + box <= a.ps && r.kvh < a.H_kv && r.page <= a.n_pages, &g_ptile_err);
+            tma_load_4d(sRing + slot * C::TBYTES + my_off, my_v ? &tm_v : &tm_k, bar, my_c * 64, r.row, r.kvh, r.page);
         };
         // a fill's slot is free once the fill that releases its last occupant has done so
         auto slot_free = [&](int q) -> bool {
@@ -304,30 +324,30 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         // fills up to 2t + 2; the last step, fill nfill - 1 alone)
         const int n_steps = ta.fault_stop_fill >= nfill ? cta_tiles : max(0, (ta.fault_stop_fill - 1) / 2);
         if (nfill > 0) {
-            Ref cur = next_tile(), nxt = cta_tiles > 1 ? next_tile() : cur;
+            then = look_up();
+            Ref cur = next_tile(), nxt = cur;
             if (ok && ta.fault_stop_fill > 0) {
                 if (lane == 0) mbar_arrive_expect_tx(bar_full(0), C::TBYTES);
                 __syncwarp();
-                copy(cur, false, 0, bar_full(0));  // K_0 alone
+                if (mine && !my_v) copy(cur, 0, bar_full(0));  // K_0 alone
+                __syncwarp();
                 g = 1;
             }
+            if (cta_tiles > 1) nxt = next_tile();
 #pragma unroll 1
             for (int t = 0; t < n_steps && ok; ++t) {
                 const bool has_next = t + 1 < cta_tiles;
-                const Ref ahead = t + 2 < cta_tiles ? next_tile() : nxt;
                 const int pv = 2 * t + 1, own = has_next ? pv + 1 : pv;
-                if (!ok || !(slot_free(pv) && (!has_next || slot_free(own)))) {
-                    ok = false;
-                    break;
-                }
+                ok = slot_free(pv) && (!has_next || slot_free(own));
+                if (!ok) break;
                 const uint32_t bar = bar_full(own % NSLOT);
                 if (lane == 0) mbar_arrive_expect_tx(bar, (has_next ? 2 : 1) * C::TBYTES);
                 __syncwarp();
-                copy(cur, true, pv % NSLOT, bar);
-                if (has_next) copy(nxt, false, own % NSLOT, bar);
+                if (mine && (my_v || has_next)) copy(my_v ? cur : nxt, (my_v ? pv : own) % NSLOT, bar);
+                __syncwarp();
                 g = own + 1;
                 cur = nxt;
-                nxt = ahead;
+                if (t + 2 < cta_tiles) nxt = next_tile();
             }
         }
         ok = ok && n_steps == cta_tiles;
@@ -743,8 +763,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             const int h = wk->kvh * a.G + r % a.G;
             const bool store = tq < min(wk->n - i0, ta.TQ) && SWA_IN_BOUNDS(tok < a.N && h < a.H_q, &g_ptile_err);
             uint16_t *orow = a.o + tok * a.o_st[0] + h * a.o_st[1];
-            const int64_t prow = static_cast<int64_t>(2 * static_cast<int>(blockIdx.x) + (wk->begun() ? 0 : 1)) * (NQT * BM) + (single ? 0 : wg * BM) + r;
-            float *arow = ta.ws.acc + prow * D;
+            const int pslot = 2 * static_cast<int>(blockIdx.x) + (wk->begun() ? 0 : 1);
+            const int prow = (single ? 0 : wg * BM) + r;
             // a shared tile's columns are read out half by each warpgroup
             const int c0 = single ? wg * (D / 64) : 0, c1 = single ? c0 + D / 64 : D / 32;
 #pragma unroll 1
@@ -768,7 +788,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                         uint32_t wv[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) wv[e] = __float_as_uint(f[q8 * 8 + e]);
-                        st_global_v8(arow + c * 32 + q8 * 8, wv);
+                        st_global_v8(ta.ws.acc + partial_at<D>(pslot, NQT * BM, prow, c * 32 + q8 * 8), wv);
                     }
                 } else if (ta.o_align32) {
                     // 32-byte stores: each lane of a store writes one whole sector of its row
@@ -798,7 +818,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     a.lse[tok * a.H_q + h] = (m + log2f(l)) * 0.69314718055994531f;
                     if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, t);
                 } else {
-                    *reinterpret_cast<float2 *>(ta.ws.ml + prow * 2) = make_float2(m, l);
+                    *reinterpret_cast<float2 *>(ta.ws.ml + (static_cast<int64_t>(pslot) * (NQT * BM) + prow) * 2) =
+                        make_float2(m, l);
                 }
             }
             give_back(k);
@@ -871,14 +892,15 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         }
         Walk<BN> walk(a, TT, sh);
         while (ok && walk.next(p)) {
-            if (p.open() && !p.begun()) open = make_int4(sh.span, p.b, p.kvh, p.ut);
+            if (p.open() && !p.begun()) open = make_int4(p.u.n - p.j1, p.b, p.kvh, p.ut);
             hand_over(p);
         }
         p.j0 = p.j1 = 0;
         hand_over(p);
         if (lane == 0) {
             ta.ws.open[blockIdx.x] = open;
-            ta.ws.any[blockIdx.x] = sh.left > 0;
+            ta.ws.first[blockIdx.x] = sh.first;
+            ta.ws.left[blockIdx.x] = sh.left;
         }
     }
 

@@ -64,7 +64,10 @@ def test_every_tile_once(seed):
             elif is_open:
                 n_open += 1
                 slots[u] = [2 * c + 1]
-                opened[c] = (1 + -(-(us[u][3] - j1) // R), u)
+                # what the merge finds: the CTAs whose stretches start before the unit's end
+                end = X + min(R, total - X) + us[u][3] - j1
+                assert end == starts[u + 1]
+                opened[c] = (1 + sum(min(x * R, total) < end for x in range(c + 1, grid)), u)
         assert n_open <= 1 and n_begun <= 1
     assert len(seen) == total
     for c, (pieces, u) in opened.items():
@@ -118,7 +121,8 @@ def test_waves_and_tail(seed):
     assert sorted(u for m in mine for u in m) == list(range(bulk))
     assert [sum(us[u][3] for u in m) for m in mine] == loads
     tail = total - sum(loads)
-    lo, hi = 0, max(loads) + -(-tail // grid)
+    lo = -(-total // grid)
+    hi = max(loads) + -(-tail // grid) if max(loads) > lo else lo
     while lo < hi:
         mid = (lo + hi) // 2
         if sum(max(0, mid - x) for x in loads) >= tail:
@@ -141,7 +145,7 @@ def test_waves_and_tail(seed):
         u = next(i for i in range(len(us)) if starts[i + 1] > first[c])
         assert u >= bulk
         last = next(i for i in range(len(us)) if starts[i + 1] > first[c] + left[c] - 1)
-        span = 1 + sum(x > c and first[x] < starts[last + 1] for x in range(grid))
+        span = 1 + sum(x > c and min(first[x], total) < starts[last + 1] for x in range(grid))
         for u, j0, j1 in walk(us, (u, first[c] - starts[u], left[c])):
             for j in range(j0, j1):
                 assert (u, j) not in seen
