@@ -5,7 +5,7 @@
 // Persistent kernel, several CTAs per SM, five warps.  A CTA takes its share of the batch's
 // tiles of 64 keys (swa_paged.cuh) and streams it:
 //   warp 0     producer: looks up the pages of a tile (one tile ahead) and copies its keys and
-//              values by TMA, one box per page (or half a page of 128) and 64 elements of the
+//              values by TMA, a box per page (or half a page of 128) and 64 elements of the
 //              head, into a ring of NST stages with 128B swizzle.  A page that is not there is
 //              read past the pool's end, which gives zeros.
 //   warps 1-4  consumers: 16 keys of every tile each, S = Q K^T and O += P V by mma.sync, with a
@@ -20,6 +20,7 @@
 #include <atomic>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "swa_paged.cuh"
 
@@ -112,9 +113,21 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
         int4 open = make_int4(0, 0, 0, 0);
         int seq = 0;  // stages emitted so far
         bool ok = true;
-        const int box = min(a.ps, CH), npg = CH / box;  // rows of a box, boxes of 64 rows
-        const int nbox = npg * (D / 64) * 2;            // copies of a stage, one lane each
-        const int my_pg = lane % npg, my_c = (lane / npg) % (D / 64), my_v = lane / (npg * (D / 64));
+        const int box = min(a.ps, CH), npg = CH / box;  // rows of a box, boxes of a tile
+        const int my_pg = lane % npg;                   // lane i looks up the page of box i % npg
+        auto copy_boxes = [&](auto boxes, int st, int kvh, int row, int page) {
+            constexpr int kBoxes = decltype(boxes)::value;
+#pragma unroll
+            for (int e = 0; e < kBoxes; ++e) {
+                const int pg = __shfl_sync(0xffffffffu, page, e);
+                // debug build: the box lies in the page, the head exists
+                (void)SWA_IN_BOUNDS(row + box <= a.ps && kvh < a.H_kv && pg <= a.n_pages, &g_psplit_err);
+#pragma unroll
+                for (int c = 0; c < 2 * (D / 64); ++c)  // keys, then values
+                    tma_load_4d_e(sbase + C::OFF_RING + st * C::STAGE + c * (CH * 128) + e * (CH / kBoxes) * 128,
+                                  c < D / 64 ? &tm_k : &tm_v, bar_full(st), c % (D / 64) * 64, row, kvh, pg);
+            }
+        };
         while (ok && walk.next(p)) {
             if (p.open() && !p.begun()) open = make_int4(p.u.n - p.j1, p.b, p.kvh, p.ut);
             const int t0 = p.s.p0 + p.ut * TT, t1 = p.s.p0 + min(p.s.n, (p.ut + 1) * TT) - 1;
@@ -155,15 +168,10 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
                 }
                 if (lane == 0) mbar_arrive_expect_tx(bar_full(st), C::STAGE);
                 __syncwarp();
-                if (lane < nbox) {
-                    const uint32_t dst = sbase + C::OFF_RING + st * C::STAGE + my_v * (C::STAGE / 2) + my_c * (CH * 128) +
-                                         my_pg * box * 128;
-                    // debug build: the box lies in the page, the head exists
-                    (void)SWA_IN_BOUNDS((kp & (a.ps - 1)) + box <= a.ps && p.kvh < a.H_kv && page <= a.n_pages,
-                                        &g_psplit_err);
-                    tma_load_4d(dst, my_v ? &tm_v : &tm_k, bar_full(st), my_c * 64, kp & (a.ps - 1), p.kvh, page);
-                }
-                __syncwarp();
+                const int row = npg == 1 ? k0 & (a.ps - 1) : 0;  // (a tile may be part of one page)
+                if (npg == 1) copy_boxes(std::integral_constant<int, 1>(), st, p.kvh, row, page);
+                else if (npg == 2) copy_boxes(std::integral_constant<int, 2>(), st, p.kvh, row, page);
+                else copy_boxes(std::integral_constant<int, 4>(), st, p.kvh, row, page);
                 ++seq;
                 page = ahead;
             }

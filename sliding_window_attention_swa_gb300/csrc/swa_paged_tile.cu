@@ -15,7 +15,8 @@
 //   warp 1        TMEM owner and MMA issuer (warp-uniform loop, one elected lane issues):
 //                   S  = Q K_j^T (A = Q from shared memory, at head dim 256 from tensor memory)
 //                   O += P V_j   (A = P from tensor memory)
-//   warp 2        Q loader.
+//   warp 2        Q loader; at head dim 256, where the query tile passes through the ring, producer of
+//                 the values beside warp 0.
 //   warp 3        planner: finds the CTA's pieces, up to NP ahead of the others, and hands them over
 //                 through shared memory, so that no other role spends its time on that.
 //   softmax WGs   NQT warpgroups; one row per thread (TMEM lane).  Running max in the log2
@@ -39,6 +40,7 @@
 #include <atomic>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "swa_paged.cuh"
 
@@ -74,11 +76,14 @@ struct TileCfg {
     static constexpr int QBYTES = BM * D * 2;  // one query tile
     static constexpr int TBYTES = BN * D * 2;  // one K or V tile
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_RING = NQT * QBYTES;
+    static constexpr int OFF_RING = NQT == 2 ? NQT * QBYTES : 0;
     static constexpr int XBYTES = NQT == 2 ? 2 * BM * 8 : 0;  // (max, sum) of both warpgroups' rows
     static constexpr int NSLOT_RAW = (232448 - 512 - XBYTES - OFF_RING) / TBYTES;
-    // (one query tile: value fills release their slots, which needs an odd ring)
-    static constexpr int NSLOT = D == 64 ? 8 : NQT == 1 && NSLOT_RAW % 2 == 0 ? NSLOT_RAW - 1 : NSLOT_RAW;
+    // K/V ring.  At head dim 256 the query tile, which the MMAs read from tensor memory, passes
+    // through it as two fills of its own instead of holding two slots' worth of shared memory:
+    // seven slots instead of five.
+    static constexpr int NSLOT = D == 64 ? 8 : NSLOT_RAW;
+    static_assert(NQT == 2 || QBYTES == 2 * TBYTES, "a query tile is two fills");
     static constexpr int OFF_X = OFF_RING + NSLOT * TBYTES;
     static constexpr int OFF_BAR = OFF_X + XBYTES;
     // q_full[2], q_empty[2], kv_full[NSLOT], kv_empty[NSLOT], s_full[2], p_full[2], o_done[2],
@@ -149,24 +154,20 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     const uint32_t bar_drain = bars + 8u * (13 + 2 * NSLOT);
     auto bar_piece = [&](int i) { return bars + 8u * (14 + 2 * NSLOT + i); };
     auto bar_used = [&](int i) { return bars + 8u * (14 + 2 * NSLOT + C::NP + i); };
-    // Ring fills are numbered over the CTA's share: 2g is the key tile, 2g + 1 the value tile of
-    // its g-th tile; fill p lies in slot p % NSLOT.
-    // Slot releases.  NQT = 1: value fills release (a tile's S MMAs precede its P V, so V_g's
-    // release also frees K_g's slot); with an odd ring a slot alternates key and value fills, so
-    // its barrier counts value fills only (vpar).  NQT = 2: key fills release, once their S MMAs
-    // and the P V of the value tile before them are done (kpar).
-    static_assert(NQT == 2 || NSLOT % 2 == 1, "value-only slot releases need an odd ring");
-    auto vpar = [&](int p) -> uint32_t {
-        const int sl = p % NSLOT, i = p / NSLOT;
-        return static_cast<uint32_t>(((i - ((1 + sl) & 1)) / 2) & 1);
-    };
+    // Ring fills, numbered over the CTA's share; fill p lies in slot p % NSLOT.
+    // NQT = 1: a piece's query tile (two fills), then K and V of each of its tiles.  Every fill
+    // has its own arrival and its own release: phase (p / NSLOT) & 1 of the slot's barriers.
+    auto fphase = [&](int p) -> uint32_t { return static_cast<uint32_t>((p / NSLOT) & 1); };
+    auto kfill = [&](int k, int g) { return 2 * (k + 1) + 2 * g; };  // K of tile g, in piece k (V: the next)
+    // NQT = 2: fill 2g is the key tile, 2g + 1 the value tile of the g-th tile.  Key fills release
+    // slots, once their S MMAs and the P V of the value tile before them are done (kpar).
+    // V_g and K_{g+1} land on K_{g+1}'s slot barrier, which thus completes for key fills only (and
+    // for the CTA's last value fill, which has no key fill after it): fpar(q) is the parity of
+    // owner fill q's completion.  An odd ring's slots alternate key and value fills.
     auto kpar = [&](int p) -> uint32_t {
         const int sl = p % NSLOT, i = p / NSLOT;
         return static_cast<uint32_t>((NSLOT % 2 == 1 ? (i - (sl & 1)) / 2 : i) & 1);
     };
-    // V_g and K_{g+1} land on K_{g+1}'s slot barrier, which thus completes for key fills only (and
-    // for the CTA's last value fill, which has no key fill after it): fpar(q) is the parity of
-    // owner fill q's completion.
     auto fpar = [&](int q) -> uint32_t {
         const int sl = q % NSLOT, i = q / NSLOT;
         const int n = NSLOT % 2 == 1 ? (i - (sl & 1) + 1) / 2 : (sl % 2 == 0 ? i : 0);
@@ -181,9 +182,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         *abort = 0;
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar_qf(x), 1);
-            // the four warps of a softmax warpgroup; with the tile in tensor memory, the MMA
-            // warp's one commit after the copy
-            mbar_init(bar_qe(x), C::QTM ? 1 : 4);
+            mbar_init(bar_qe(x), 4);  // the four warps of a softmax warpgroup
             mbar_init(bar_sf(x), 1);
             mbar_init(bar_pf(x), 4);
             mbar_init(bar_od(x), 1);
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     // a unit whose tokens fill one of its two query tiles at most (tokens: of its sequence)
     auto is_single = [&](int tokens, int ut) { return NQT == 2 && tokens - ut * TT <= ta.TQ; };
 
-    if (warp == 0) {
+    if (warp == 0 || (NQT == 1 && warp == 2)) {
         // ============================ K/V producer ============================
         if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
         // the scratch of the work split lies in the ring: order its generic accesses before the copies
@@ -245,17 +244,19 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         // A tile is npg boxes (pages or a part of one) times D / 64 column blocks.  The pages are looked
         // up 32 boxes at a time, lane i that of box i, a group ahead of their use.
         const int box = min(a.ps, BN), npg = BN / box, per_group = 32 / npg;
+        constexpr int kMaxBoxes = BN / 16;
         struct Group {
             int tiles, kvh, row, entry;  // row, entry: of this lane's box
             bool need;                   // some query row keeps a key of this lane's box
+            int token;                   // the piece's first token if the group starts it, else -1
         };
         bool ok = true;
         int np = 0, i = 0, n = 0;  // pieces taken, next tile of the current one, its tiles
-        int b = 0, kvh = 0, lo = 0, t1 = 0, end = 0, sink = 0, t_first = 0, j0 = 0, looked = 0;
+        int b = 0, kvh = 0, lo = 0, t1 = 0, end = 0, sink = 0, t_first = 0, j0 = 0, looked = 0, token = 0;
         auto look_up = [&]() -> Group {
             if (i >= n) {
                 volatile TilePiece *p = get_piece(np, ok);
-                if (!p) return Group{INT_MAX, 0, 0, -1, false};
+                if (!p) return Group{INT_MAX, 0, 0, -1, false, -1};
                 i = 0;
                 n = p->j1 - p->j0;
                 b = p->b;
@@ -267,26 +268,29 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 t1 = p->p0 + min(p->n, (p->ut + 1) * TT) - 1;
                 lo = t0 >= a.window ? t0 - a.window + 1 : 0;
                 end = p->p0 + p->n;
+                token = p->q0 + p->ut * TT;
                 give_back(np++);
             }
             const int tiles = min(n - i, per_group), j = j0 + i + lane / npg;
             const int kp = (j < sink ? j : t_first + (j - sink)) * BN + lane % npg * box;
             const bool there = lane < tiles * npg && kp < end;
+            const int head = i == 0 ? token : -1;
             i += tiles;
             looked += tiles;
             return Group{tiles, kvh, kp & (a.ps - 1),
                          there ? __ldg(a.table + static_cast<int64_t>(b) * a.width + (kp >> a.ps_log2)) : -1,
-                         there && kp <= t1 && (kp + box > lo || kp < a.n_sink)};
+                         there && kp <= t1 && (kp + box > lo || kp < a.n_sink), head};
         };
-        // A step copies a tile's values (lanes 16 ..) and the next tile's keys (lanes 0 ..), one lane a
-        // box: lanes issue faster than one lane that walks through the boxes.
-        const int my = lane & 15, my_pg = my % npg, my_c = my / npg;
-        const bool my_v = lane >= 16, mine = my < npg * (D / 64);
-        const uint32_t my_off = static_cast<uint32_t>(my_c * (BN * 128) + my_pg * box * 128);
-        struct Ref {  // this lane's box of a tile
-            int kvh, row, page;
+        // Where a tile's boxes are.  Head dim <= 128: the same in every lane, and the copies are issued
+        // by the converged warp (43 cycles each: pages of 16 make 32 of them a step; 1394 TFLOP/s
+        // with the Mistral window against 1366 with a lane a box).  Head dim 256: lane i issues box
+        // i % npg of column block i / npg (pages of 128: 975 TFLOP/s with the Gemma window against
+        // 922 for the converged warp).
+        constexpr bool kLanes = NQT == 1;
+        struct Ref {
+            int kvh, row, token, page[kLanes ? 1 : kMaxBoxes];
         };
-        Group now{0, 0, 0, 0, false}, then{0, 0, 0, 0, false};
+        Group now{0, 0, 0, 0, false, -1}, then = now;
         int at = 0, page = 0;  // next tile of the group; this lane's page
         auto next_tile = [&]() -> Ref {
             if (at >= now.tiles) {
@@ -297,26 +301,104 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 page = in_pool ? now.entry : a.n_pages;
                 if (now.need && !in_pool) atomicOr(&g_ptile_data, SWA_DEVERR_BAD_PAGE);
             }
-            const int from = (at * npg + my_pg) & 31;
+            Ref r;
+            r.kvh = now.kvh;
+            r.token = at == 0 ? now.token : -1;
+            r.row = __shfl_sync(0xffffffffu, now.row, at * npg);  // (not 0 only if a tile is part of one page)
+            if constexpr (kLanes) {
+                r.page[0] = __shfl_sync(0xffffffffu, page, (at * npg + lane % npg) & 31);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kMaxBoxes; ++e) r.page[e] = __shfl_sync(0xffffffffu, page, (at * npg + e) & 31);
+            }
             ++at;
-            return Ref{now.kvh, __shfl_sync(0xffffffffu, now.row, from), __shfl_sync(0xffffffffu, page, from)};
+            return r;
         };
-        auto copy = [&](const Ref &r, int slot, uint32_t bar) {
-            // debug build: the box lies in the page, the head exists
-            (void)SWA_IN_BOUNDS(r.row + box <= a.ps && r.kvh < a.H_kv && r.page <= a.n_pages, &g_ptile_err);
-            tma_load_4d(sRing + slot * C::TBYTES + my_off, my_v ? &tm_v : &tm_k, bar, my_c * 64, r.row, r.kvh, r.page);
+        auto copy_boxes = [&](auto boxes, const Ref &r, const CUtensorMap *map, int slot, uint32_t bar) {
+            constexpr int kBoxes = decltype(boxes)::value;
+            const uint32_t dst = sRing + slot * C::TBYTES;
+#pragma unroll
+            for (int e = 0; e < kBoxes; ++e) {
+                // debug build: the box lies in the page, the head exists
+                (void)SWA_IN_BOUNDS(r.row + box <= a.ps && r.kvh < a.H_kv && r.page[e] <= a.n_pages, &g_ptile_err);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d_e(dst + c * (BN * 128) + e * (BN / kBoxes) * 128, map, bar, c * 64, r.row, r.kvh,
+                                  r.page[e]);
+            }
         };
-        // a fill's slot is free once the fill that releases its last occupant has done so
+        const int my_c = lane / npg;
+        const uint32_t my_off = static_cast<uint32_t>(my_c * (BN * 128) + lane % npg * box * 128);
+        auto copy = [&](const Ref &r, const CUtensorMap *map, int slot, uint32_t bar) {
+            if constexpr (kLanes) {
+                (void)SWA_IN_BOUNDS(r.row + box <= a.ps && r.kvh < a.H_kv && r.page[0] <= a.n_pages, &g_ptile_err);
+                if (my_c < D / 64)
+                    tma_load_4d(sRing + slot * C::TBYTES + my_off, map, bar, my_c * 64, r.row, r.kvh, r.page[0]);
+                __syncwarp();
+            } else if (npg == 1) copy_boxes(std::integral_constant<int, 1>(), r, map, slot, bar);
+            else if (npg == 2) copy_boxes(std::integral_constant<int, 2>(), r, map, slot, bar);
+            else if (npg == 4) copy_boxes(std::integral_constant<int, 4>(), r, map, slot, bar);
+            else if constexpr (kMaxBoxes == 8) copy_boxes(std::integral_constant<int, 8>(), r, map, slot, bar);
+        };
+        if constexpr (NQT == 1) {
+            // warp 0 copies the query tiles and keys, warp 2 the values: with pages of 16 a tile is 32
+            // copies, more than one warp issues in a tile's time
+            const bool values = warp == 2;
+            int last = 0;       // this warp's last fill
+            uint32_t mine = 0;  // bit i: it issued fill last - i
+            // fill f's slot, once its last occupant has been released, with `bytes` expected on its barrier
+            auto next_slot = [&](int f, int bytes) -> bool {
+                if (f >= ta.fault_stop_fill) return false;  // planted fault: this fill is never issued
+                const int slot = f % NSLOT;
+                if (f >= NSLOT && !warp_wait(bar_empty(slot), fphase(f - NSLOT), abort)) return false;
+                if (lane == 0) mbar_arrive_expect_tx(bar_full(slot), static_cast<uint32_t>(bytes));
+                __syncwarp();
+                mine = (f - last < 32 ? mine << (f - last) : 0u) | 1u;
+                last = f;
+                return true;
+            };
+            Ref r{};
+            int pc = 0;  // pieces begun
+            if (cta_tiles > 0) {
+                then = look_up();
+                r = next_tile();
+            }
+#pragma unroll 1
+            for (int t = 0; t < cta_tiles && ok; ++t) {
+                if (r.token >= 0) ++pc;
+                const int f = kfill(pc - 1, t);
+                if (values) {
+                    ok = next_slot(f + 1, C::TBYTES);
+                    if (ok) copy(r, &tm_v, (f + 1) % NSLOT, bar_full((f + 1) % NSLOT));
+                } else {
+                    if (r.token >= 0) {
+#pragma unroll 1
+                        for (int q = f - 2; q < f && ok; ++q) {
+                            ok = next_slot(q, a.G * ta.TQ * D);
+                            if (!ok) break;
+                            // debug build: the tile's tokens and its group's heads exist
+                            (void)SWA_IN_BOUNDS(r.token < a.N && (r.kvh + 1) * a.G <= a.H_q, &g_ptile_err);
+                            if (lane < D / 128)
+                                tma_load_4d(sRing + q % NSLOT * C::TBYTES + lane * (BM * 128), &tm_q,
+                                            bar_full(q % NSLOT), (q - f + 2) * (D / 2) + lane * 64, r.kvh * a.G,
+                                            r.token, 0);
+                            __syncwarp();
+                        }
+                    }
+                    ok = ok && next_slot(f, C::TBYTES);
+                    if (ok) copy(r, &tm_k, f % NSLOT, bar_full(f % NSLOT));
+                }
+                if (t + 1 < cta_tiles) r = next_tile();
+            }
+            if (!ok && lane == 0)  // drain this warp's copies that may still be in flight: at most one a slot
+                for (int i2 = 0; i2 < NSLOT; ++i2)
+                    if ((mine >> i2) & 1u) mbar_drain(bar_full((last - i2) % NSLOT), fphase(last - i2), &g_ptile_err);
+        } else {
+        // a fill's slot is free once the key fill that releases its last occupant has done so
         auto slot_free = [&](int q) -> bool {
             if (q < NSLOT) return true;
-            const int prev = q - NSLOT;
-            if constexpr (NQT == 1) {
-                const int vp = (prev & 1) ? prev : prev + 1;
-                return warp_wait(bar_empty(vp % NSLOT), vpar(vp), abort);
-            } else {
-                const int kp = (prev & 1) ? prev + 1 : prev;
-                return warp_wait(bar_empty(kp % NSLOT), kpar(kp), abort);
-            }
+            const int prev = q - NSLOT, kp = (prev & 1) ? prev + 1 : prev;
+            return warp_wait(bar_empty(kp % NSLOT), kpar(kp), abort);
         };
         const int nfill = 2 * cta_tiles;
         int g = 0;  // ring fills issued so far
@@ -329,8 +411,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             if (ok && ta.fault_stop_fill > 0) {
                 if (lane == 0) mbar_arrive_expect_tx(bar_full(0), C::TBYTES);
                 __syncwarp();
-                if (mine && !my_v) copy(cur, 0, bar_full(0));  // K_0 alone
-                __syncwarp();
+                copy(cur, &tm_k, 0, bar_full(0));  // K_0 alone
                 g = 1;
             }
             if (cta_tiles > 1) nxt = next_tile();
@@ -343,8 +424,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 const uint32_t bar = bar_full(own % NSLOT);
                 if (lane == 0) mbar_arrive_expect_tx(bar, (has_next ? 2 : 1) * C::TBYTES);
                 __syncwarp();
-                if (mine && (my_v || has_next)) copy(my_v ? cur : nxt, (my_v ? pv : own) % NSLOT, bar);
-                __syncwarp();
+                if (has_next) copy(nxt, &tm_k, own % NSLOT, bar);
+                copy(cur, &tm_v, pv % NSLOT, bar);
                 g = own + 1;
                 cur = nxt;
                 if (t + 2 < cta_tiles) nxt = next_tile();
@@ -356,6 +437,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             // g - NSLOT have landed (their slots were released by readers that waited for them)
             for (int q = max(0, g - NSLOT); q < g; ++q)
                 if ((q & 1) == 0 || q + 1 == nfill) mbar_drain(bar_full(q % NSLOT), fpar(q), &g_ptile_err);
+        }
         }
     } else if (warp == 2) {
         // ============================ Q loader ============================
@@ -417,8 +499,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 qdesc[qt][kk] = kQDesc ? smem_desc(sQ + qt * C::QBYTES + (kk >> 2) * (BM * 128) + (kk & 3) * 32, 16,
                                                    1024, kSwizzle128B)
                                        : 0ull;
-        auto v_descs = [&](int g) {
-            const uint64_t v0 = smem_desc(sRing + ((2 * g + 1) % NSLOT) * C::TBYTES, BN * 128, 1024, kSwizzle128B);
+        auto v_descs = [&](int slot) {
+            const uint64_t v0 = smem_desc(sRing + slot * C::TBYTES, BN * 128, 1024, kSwizzle128B);
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk) vd[kk] = desc_offset(v0, kk * 2048);
         };
@@ -428,10 +510,10 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             const int own = g + 1 < cta_tiles ? 2 * g + 2 : 2 * g + 1;
             return warp_wait(bar_full(own % NSLOT), fpar(own), abort);
         };
-        // S of tile g (landed) into TMEM slot `slot` from query tile qt
-        auto mma_s = [&](int slot, int qt, int g) {
+        // S of the key tile in ring slot ks (landed) into TMEM slot `slot` from query tile qt
+        auto mma_s = [&](int slot, int qt, int ks) {
             tc_fence_after();
-            const uint64_t b0 = smem_desc(sRing + ((2 * g) % NSLOT) * C::TBYTES, 16, 1024, kSwizzle128B);
+            const uint64_t b0 = smem_desc(sRing + ks * C::TBYTES, 16, 1024, kSwizzle128B);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint64_t bd = desc_offset(b0, (kk >> 2) * (BN * 128) + (kk & 3) * 32);
@@ -445,7 +527,12 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         // of the previous piece has read it; wait_v: V of tile g may not have landed yet
         auto mma_pv = [&](int slot, int ot, bool first, uint32_t n_used, bool wait_v, int g) -> bool {
             if (!warp_wait(bar_pf(slot), n_used & 1, abort)) return false;
-            if (wait_v && !have_v(g)) return false;
+            if constexpr (NQT == 1) {
+                const int f = kfill(k, g) + 1;
+                if (!warp_wait(bar_full(f % NSLOT), fphase(f), abort)) return false;
+            } else {
+                if (wait_v && !have_v(g)) return false;
+            }
             if (first && k >= 1) {
                 if (!warp_wait(bar_of(ot), (k - 1) & 1, abort)) return false;
                 // (both warpgroups read both accumulators of a piece of one query tile)
@@ -464,47 +551,49 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             const int n = p->j1 - p->j0;
             const bool single = is_single(p->n, p->ut);
             give_back(k);
+            if constexpr (NQT == 2) {
             ok = warp_wait(bar_qf(0), k & 1, abort);
             // (the key tile of a later piece came with the value tile of the last one)
             if (ok && J == 0) ok = have_k(0);
             if (!ok) break;
-            if (NQT == 2 && !single) {
-                mma_s(0, 0, J);
+            const int ks0 = (2 * J) % NSLOT;
+            if (!single) {
+                mma_s(0, 0, ks0);
                 ok = warp_wait(bar_qf(1), k & 1, abort);
                 if (!ok) break;
-                mma_s(1, NQT - 1, J);
+                mma_s(1, NQT - 1, ks0);
 #pragma unroll 1
                 for (int i = 0; i < n; ++i) {
-                    const int g = J + i;
-                    v_descs(g);
+                    const int g = J + i, ks = (2 * g + 2) % NSLOT;
+                    v_descs((2 * g + 1) % NSLOT);
                     ok = mma_pv(0, 0, i == 0, np0 + i, true, g);  // (K_{g+1} has landed too then)
                     if (!ok) break;
-                    if (i + 1 < n) mma_s(0, 0, g + 1);
+                    if (i + 1 < n) mma_s(0, 0, ks);
                     else tc_commit_e(bar_od(0));
                     ok = mma_pv(1, 1, i == 0, np1 + i, false, g);
                     if (!ok) break;
-                    if (i + 1 < n) mma_s(1, NQT - 1, g + 1);
+                    if (i + 1 < n) mma_s(1, NQT - 1, ks);
                     else tc_commit_e(bar_od(1));
                 }
                 np0 += n;
                 np1 += n;
                 was_single = false;
-            } else if (NQT == 2) {
+            } else {
                 // one query tile, its key tiles in slot 0 and 1 in turn.  S of tile i + 1 is issued
                 // before P V of tile i, so the commit after that P V releases K_{i+1}.
                 ok = warp_wait(bar_qf(1), k & 1, abort);
                 if (!ok) break;
-                mma_s(0, 0, J);
-                tc_commit_e(bar_empty((2 * J) % NSLOT));
+                mma_s(0, 0, ks0);
+                tc_commit_e(bar_empty(ks0));
 #pragma unroll 1
                 for (int i = 0; i < n; ++i) {
                     const int g = J + i, x = i & 1;
                     if (i + 1 < n) {  // S of tile i + 1 into the other slot, whose P V is issued
                         ok = have_k(g + 1);
                         if (!ok) break;
-                        mma_s(x ^ 1, 0, g + 1);
+                        mma_s(x ^ 1, 0, (2 * g + 2) % NSLOT);
                     }
-                    v_descs(g);
+                    v_descs((2 * g + 1) % NSLOT);
                     ok = mma_pv(x, x, i < 2, x ? np1++ : np0++, i + 1 == n, g);
                     if (!ok) break;
                     if (i + 1 < n) tc_commit_e(bar_empty((2 * (g + 1)) % NSLOT));
@@ -513,32 +602,43 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 tc_commit_e(bar_od(0));
                 tc_commit_e(bar_od(1));
                 was_single = true;
+            }
             } else {
-                if constexpr (C::QTM) {
-                    // the piece's query tile into tensor memory, 16 columns per copy (the previous
-                    // piece's last S MMA precedes the copies in the tensor pipe); its shared memory is
-                    // free for the next piece once they complete
-                    tc_fence_after();
+                // the piece's query tile into tensor memory, 16 columns per copy (the previous piece's
+                // last S MMA precedes the copies in the tensor pipe), which frees its two slots
+                const int fq = 2 * k + 2 * J;
+                ok = warp_wait(bar_full(fq % NSLOT), fphase(fq), abort) &&
+                     warp_wait(bar_full((fq + 1) % NSLOT), fphase(fq + 1), abort);
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        tc_cp_128x256b_e(tmem + C::TM_Q + kk * 8,
-                                         smem_desc(sQ + (kk >> 2) * (BM * 128) + (kk & 3) * 32, 16, 1024, kSwizzle128B));
-                    tc_commit_e(bar_qe(0));
-                }
-                mma_s(J & 1, 0, J);
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_cp_128x256b_e(tmem + C::TM_Q + kk * 8,
+                                     smem_desc(sRing + ((fq + kk / (D / 32)) % NSLOT) * C::TBYTES +
+                                                   (kk % (D / 32) >> 2) * (BM * 128) + (kk & 3) * 32,
+                                               16, 1024, kSwizzle128B));
+                tc_commit_e(bar_empty(fq % NSLOT));
+                tc_commit_e(bar_empty((fq + 1) % NSLOT));
+                // S of tile g, whose slot is free once it is done
+                auto next_s = [&](int g) -> bool {
+                    const int f = kfill(k, g), slot = f % NSLOT;
+                    if (!warp_wait(bar_full(slot), fphase(f), abort)) return false;
+                    mma_s(g & 1, 0, slot);
+                    tc_commit_e(bar_empty(slot));
+                    return true;
+                };
+                ok = next_s(J);
+                if (!ok) break;
 #pragma unroll 1
                 for (int i = 0; i < n; ++i) {
-                    const int g = J + i;
-                    if (i + 1 < n) {
-                        // slot (g+1) & 1 last held P of tile g-1, consumed by its P V issued earlier
-                        ok = have_k(g + 1);
-                        if (!ok) break;
-                        mma_s((g + 1) & 1, 0, g + 1);
-                    }
-                    v_descs(g);
-                    ok = mma_pv(g & 1, 0, i == 0, static_cast<uint32_t>(g >> 1), i + 1 == n, g);
+                    const int g = J + i, vs = (kfill(k, g) + 1) % NSLOT;
+                    // slot (g+1) & 1 last held P of tile g-1, consumed by its P V issued earlier
+                    if (i + 1 < n) ok = next_s(g + 1);
                     if (!ok) break;
-                    tc_commit_e(bar_empty((2 * g + 1) % NSLOT));
+                    v_descs(vs);
+                    ok = mma_pv(g & 1, 0, i == 0, static_cast<uint32_t>(g >> 1), true, g);
+                    if (!ok) break;
+                    tc_commit_e(bar_empty(vs));
                     if (i + 1 == n) tc_commit_e(bar_od(0));
                 }
             }
@@ -656,7 +756,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     // complete: with two query tiles S(i) was issued after them; with one, the release
                     // of tile g-1's V slot is committed right after its P V
                     if constexpr (NQT == 1) {
-                        if (!warp_wait(bar_empty((2 * (g - 1) + 1) % NSLOT), vpar(2 * (g - 1) + 1), abort)) {
+                        const int f = kfill(k, g - 1) + 1;
+                        if (!warp_wait(bar_empty(f % NSLOT), fphase(f), abort)) {
                             ok = false;
                             break;
                         }
@@ -706,14 +807,16 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     // the sequence ends in this tile: zero the value rows of its last page past the
                     // end (later pages came as zeros).  The first P V of the tile waits for this
                     // warpgroup's P, and with two query tiles the second is issued after it.
-                    const int own = g + 1 < cta_tiles ? 2 * g + 2 : 2 * g + 1;  // V_g lands with K_{g+1}
-                    if (!warp_wait(bar_full(own % NSLOT), fpar(own), abort)) {
+                    // (with two query tiles V_g lands with K_{g+1})
+                    const int fv = NQT == 1 ? kfill(k, g) + 1 : 2 * g + 1;
+                    const int own = NQT == 2 && g + 1 < cta_tiles ? fv + 1 : fv;
+                    if (!warp_wait(bar_full(own % NSLOT), NQT == 1 ? fphase(own) : fpar(own), abort)) {
                         ok = false;
                         break;
                     }
                     const int box = min(a.ps, BN);
                     const int z0 = wk->p0 + wk->n - wk->tile(i) * BN, z1 = min(BN, (z0 + box - 1) / box * box);
-                    uint8_t *vt = sgen + C::OFF_RING + ((2 * g + 1) % NSLOT) * C::TBYTES;
+                    uint8_t *vt = sgen + C::OFF_RING + (fv % NSLOT) * C::TBYTES;
                     for (int idx = r; idx < (z1 - z0) * (D / 8); idx += BM) {
                         const int row = z0 + idx / (D / 8), pc = idx % (D / 8);
                         *reinterpret_cast<uint4 *>(vt + (pc >> 3) * (BN * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4)) =
