@@ -20,6 +20,8 @@ constexpr int kThreads = 256;
 // append: a warp per token
 // ---------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedArgs a) {
+    // the attention kernel behind this one may start: it waits for this grid before it reads a page
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31;
     const int step = gridDim.x * (kThreads / 32);
     for (int n = (blockIdx.x * kThreads + threadIdx.x) >> 5; n < a.N; n += step) {
@@ -129,19 +131,11 @@ __global__ void __launch_bounds__(kThreads) paged_merge_kernel(const PagedArgs a
 }
 
 cudaError_t launch_merge(const PagedArgs &a, const PagedWs &w, const PagedShape &x, cudaStream_t s) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(x.ctas, (x.tiles * x.rows + kMergeRows - 1) / kMergeRows);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    const dim3 grid(x.ctas, (x.tiles * x.rows + kMergeRows - 1) / kMergeRows);
     switch (a.D) {
-        case 64: return cudaLaunchKernelEx(&cfg, paged_merge_kernel<64>, a, w, x);
-        case 128: return cudaLaunchKernelEx(&cfg, paged_merge_kernel<128>, a, w, x);
-        case 256: return cudaLaunchKernelEx(&cfg, paged_merge_kernel<256>, a, w, x);
+        case 64: return launch_dependent(true, paged_merge_kernel<64>, grid, kThreads, 0, s, a, w, x);
+        case 128: return launch_dependent(true, paged_merge_kernel<128>, grid, kThreads, 0, s, a, w, x);
+        case 256: return launch_dependent(true, paged_merge_kernel<256>, grid, kThreads, 0, s, a, w, x);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -198,14 +192,15 @@ cudaError_t launch_paged_append(const PagedArgs &a, cudaStream_t s) {
 
 cudaError_t launch_paged_attend(const PagedArgs &args, void *ws, cudaStream_t s) {
     PagedArgs a = args;
-    if (a.kn && a.q_start) {  // (one token a sequence: stored by the attention kernel)
+    const bool after_append = a.kn && a.q_start;  // (one token a sequence: stored by the attention kernel)
+    if (after_append) {
         const cudaError_t e = launch_paged_append(a, s);
         if (e != cudaSuccess) return e;
         a.kn = a.vn = nullptr;
     }
     const PagedShape x = shape_of(a);
     const PagedWs w = paged_carve(ws, x, a.D);
-    const cudaError_t e = few_rows(a) ? launch_paged_split(a, w, s) : launch_paged_tile(a, w, s);
+    const cudaError_t e = few_rows(a) ? launch_paged_split(a, w, after_append, s) : launch_paged_tile(a, w, after_append, s);
     return e != cudaSuccess ? e : launch_merge(a, w, x, s);
 }
 

@@ -72,11 +72,13 @@ inline PagedWs paged_carve(void *ws, const PagedShape &x, int D) {
 // Few rows (swa_paged_split.cu).  It stores the new rows itself where every sequence has one
 // new token (q_start null).
 PagedShape paged_split_shape(const PagedArgs &a);
-cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, cudaStream_t s);
+// after_append: launched as a programmatic dependent of the append kernel just before it on the
+// stream (everything up to the first copy of a page overlaps that kernel).
+cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s);
 void paged_split_read_clear_error(unsigned int *data, unsigned int *wait);
 // Many rows (swa_paged_tile.cu).
 PagedShape paged_tile_shape(const PagedArgs &a);
-cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, cudaStream_t s);
+cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s);
 void paged_tile_read_clear_error(unsigned int *data, unsigned int *wait);
 
 // bf16 map over (d, d1, d2, d3) of n1, n2, n3 with element strides s1, s2, s3, a box of 64 x b1 x b2 x 1
@@ -85,6 +87,22 @@ bool paged_map(CUtensorMap *m, const void *base, int D, int64_t n1, int64_t n2, 
                int64_t s3, int b1, int b2);
 
 int paged_sm_count();  // SMs of the current device
+
+template <class... P, class... A>
+cudaError_t launch_dependent(bool dependent, void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s,
+                             const A &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 size_t paged_workspace_bytes(const PagedArgs &a);
 cudaError_t launch_paged_append(const PagedArgs &a, cudaStream_t s);
 cudaError_t launch_paged_attend(const PagedArgs &a, void *ws, cudaStream_t s);

@@ -33,6 +33,7 @@ __device__ unsigned int g_psplit_data = 0;  // broken device data
 constexpr int CH = 64;  // keys a tile
 constexpr int kThreads = 160;
 constexpr int ROWS = 16;  // mma.sync M
+constexpr int kMinTiles = 2;  // least share of a CTA
 
 template <int D>
 struct SplitCfg {
@@ -110,6 +111,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
         // ============================ producer ============================
         // the scratch of the work split lies in the ring: order its generic accesses before the copies
         fence_proxy_async_smem();
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // (the append before this kernel has stored its rows)
         int4 open = make_int4(0, 0, 0, 0);
         int seq = 0;  // stages emitted so far
         bool ok = true;
@@ -413,7 +415,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
 }
 
 template <int D>
-cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, cudaStream_t s) {
+cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s) {
     using C = SplitCfg<D>;
     // the dynamic shared-memory limit is a per-device function attribute: set once per device
     static std::atomic<bool> configured[64];
@@ -431,8 +433,8 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, cudaStream_t s) {
         !paged_map(&mv, a.v_pages, D, a.ps, a.H_kv, a.n_pages, D, page, page * a.H_kv, rows, 1))
         return cudaErrorInvalidValue;
     const PagedShape x = paged_split_shape(a);
-    paged_split_kernel<D><<<x.ctas, kThreads, C::SMEM, s>>>(mk, mv, a, w, x.TQ, 2, fault_plan().split_stop_stage);
-    return cudaGetLastError();
+    return launch_dependent(after_append, paged_split_kernel<D>, dim3(x.ctas), kThreads, C::SMEM, s, mk, mv, a, w, x.TQ,
+                            kMinTiles, fault_plan().split_stop_stage);
 }
 
 }  // namespace
@@ -444,11 +446,11 @@ PagedShape paged_split_shape(const PagedArgs &a) {
     return PagedShape{paged_sm_count() * per_sm, 1, ROWS, ROWS / a.G};
 }
 
-cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, cudaStream_t s) {
+cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s) {
     switch (a.D) {
-        case 64: return launch_d<64>(a, w, s);
-        case 128: return launch_d<128>(a, w, s);
-        case 256: return launch_d<256>(a, w, s);
+        case 64: return launch_d<64>(a, w, after_append, s);
+        case 128: return launch_d<128>(a, w, after_append, s);
+        case 256: return launch_d<256>(a, w, after_append, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
         // the scratch of the work split lies in the ring: order its generic accesses before the copies
         fence_proxy_async_smem();
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // (the append before this kernel has stored its rows)
         // A tile is npg boxes (pages or a part of one) times D / 64 column blocks.  The pages are looked
         // up 32 boxes at a time, lane i that of box i, a group ahead of their use.
         const int box = min(a.ps, BN), npg = BN / box, per_group = 32 / npg;
@@ -1014,7 +1015,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
 }
 
 template <int D>
-cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, cudaStream_t s) {
+cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s) {
     using C = TileCfg<D>;
     // the dynamic shared-memory limit is a per-device function attribute: set once per device
     static std::atomic<bool> configured[64];
@@ -1040,8 +1041,7 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, cudaStream_t s) {
     t.min_tiles = 4;
     t.o_align32 = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.o_st[0] % 16 == 0 && a.o_st[1] % 16 == 0;
     t.fault_stop_fill = fault_plan().band_stop_fill;
-    paged_tile_kernel<D><<<x.ctas, C::THREADS, C::SMEM, s>>>(mq, mk, mv, t);
-    return cudaGetLastError();
+    return launch_dependent(after_append, paged_tile_kernel<D>, dim3(x.ctas), C::THREADS, C::SMEM, s, mq, mk, mv, t);
 }
 
 }  // namespace
@@ -1050,11 +1050,11 @@ PagedShape paged_tile_shape(const PagedArgs &a) {
     return PagedShape{paged_sm_count(), a.D <= 128 ? 2 : 1, BM, BM / a.G};
 }
 
-cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, cudaStream_t s) {
+cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s) {
     switch (a.D) {
-        case 64: return launch_d<64>(a, w, s);
-        case 128: return launch_d<128>(a, w, s);
-        case 256: return launch_d<256>(a, w, s);
+        case 64: return launch_d<64>(a, w, after_append, s);
+        case 128: return launch_d<128>(a, w, after_append, s);
+        case 256: return launch_d<256>(a, w, after_append, s);
         default: return cudaErrorInvalidValue;
     }
 }
