@@ -33,7 +33,7 @@ __device__ unsigned int g_psplit_data = 0;  // broken device data
 constexpr int CH = 64;  // keys a tile
 constexpr int kThreads = 160;
 constexpr int ROWS = 16;  // mma.sync M
-constexpr int kMinTiles = 2;  // least share of a CTA
+constexpr int kMinTiles = 4;  // least share of a CTA
 
 template <int D>
 struct SplitCfg {

@@ -40,7 +40,6 @@
 #include <atomic>
 #include <climits>
 #include <cmath>
-#include <type_traits>
 
 #include "swa_paged.cuh"
 
@@ -82,7 +81,7 @@ struct TileCfg {
     // K/V ring.  At head dim 256 the query tile, which the MMAs read from tensor memory, passes
     // through it as two fills of its own instead of holding two slots' worth of shared memory:
     // seven slots instead of five.
-    static constexpr int NSLOT = D == 64 ? 8 : NSLOT_RAW;
+    static constexpr int NSLOT = D == 64 ? 7 : NSLOT_RAW;
     static_assert(NQT == 2 || QBYTES == 2 * TBYTES, "a query tile is two fills");
     static constexpr int OFF_X = OFF_RING + NSLOT * TBYTES;
     static constexpr int OFF_BAR = OFF_X + XBYTES;
@@ -245,7 +244,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         // A tile is npg boxes (pages or a part of one) times D / 64 column blocks.  The pages are looked
         // up 32 boxes at a time, lane i that of box i, a group ahead of their use.
         const int box = min(a.ps, BN), npg = BN / box, per_group = 32 / npg;
-        constexpr int kMaxBoxes = BN / 16;
         struct Group {
             int tiles, kvh, row, entry;  // row, entry: of this lane's box
             bool need;                   // some query row keeps a key of this lane's box
@@ -282,14 +280,12 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                          there ? __ldg(a.table + static_cast<int64_t>(b) * a.width + (kp >> a.ps_log2)) : -1,
                          there && kp <= t1 && (kp + box > lo || kp < a.n_sink), head};
         };
-        // Where a tile's boxes are.  Head dim <= 128: the same in every lane, and the copies are issued
-        // by the converged warp (43 cycles each: pages of 16 make 32 of them a step; 1394 TFLOP/s
-        // with the Mistral window against 1366 with a lane a box).  Head dim 256: lane i issues box
-        // i % npg of column block i / npg (pages of 128: 975 TFLOP/s with the Gemma window against
-        // 922 for the converged warp).
-        constexpr bool kLanes = NQT == 1;
+        // Where a tile's boxes are: lane i has the page of box i % npg and issues that box's copy of
+        // column block i / npg.  (Copies that the converged warp issues one after the other, though
+        // faster by themselves -- 43 cycles each instead of 77 --, made every case slower: the
+        // Mistral window on pages of 16 674 -> 748 us, chunks of 2048 tokens behind 30000 1017 -> 1097 us.)
         struct Ref {
-            int kvh, row, token, page[kLanes ? 1 : kMaxBoxes];
+            int kvh, row, token, page;
         };
         Group now{0, 0, 0, 0, false, -1}, then = now;
         int at = 0, page = 0;  // next tile of the group; this lane's page
@@ -306,40 +302,18 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             r.kvh = now.kvh;
             r.token = at == 0 ? now.token : -1;
             r.row = __shfl_sync(0xffffffffu, now.row, at * npg);  // (not 0 only if a tile is part of one page)
-            if constexpr (kLanes) {
-                r.page[0] = __shfl_sync(0xffffffffu, page, (at * npg + lane % npg) & 31);
-            } else {
-#pragma unroll
-                for (int e = 0; e < kMaxBoxes; ++e) r.page[e] = __shfl_sync(0xffffffffu, page, (at * npg + e) & 31);
-            }
+            r.page = __shfl_sync(0xffffffffu, page, (at * npg + lane % npg) & 31);
             ++at;
             return r;
-        };
-        auto copy_boxes = [&](auto boxes, const Ref &r, const CUtensorMap *map, int slot, uint32_t bar) {
-            constexpr int kBoxes = decltype(boxes)::value;
-            const uint32_t dst = sRing + slot * C::TBYTES;
-#pragma unroll
-            for (int e = 0; e < kBoxes; ++e) {
-                // debug build: the box lies in the page, the head exists
-                (void)SWA_IN_BOUNDS(r.row + box <= a.ps && r.kvh < a.H_kv && r.page[e] <= a.n_pages, &g_ptile_err);
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d_e(dst + c * (BN * 128) + e * (BN / kBoxes) * 128, map, bar, c * 64, r.row, r.kvh,
-                                  r.page[e]);
-            }
         };
         const int my_c = lane / npg;
         const uint32_t my_off = static_cast<uint32_t>(my_c * (BN * 128) + lane % npg * box * 128);
         auto copy = [&](const Ref &r, const CUtensorMap *map, int slot, uint32_t bar) {
-            if constexpr (kLanes) {
-                (void)SWA_IN_BOUNDS(r.row + box <= a.ps && r.kvh < a.H_kv && r.page[0] <= a.n_pages, &g_ptile_err);
-                if (my_c < D / 64)
-                    tma_load_4d(sRing + slot * C::TBYTES + my_off, map, bar, my_c * 64, r.row, r.kvh, r.page[0]);
-                __syncwarp();
-            } else if (npg == 1) copy_boxes(std::integral_constant<int, 1>(), r, map, slot, bar);
-            else if (npg == 2) copy_boxes(std::integral_constant<int, 2>(), r, map, slot, bar);
-            else if (npg == 4) copy_boxes(std::integral_constant<int, 4>(), r, map, slot, bar);
-            else if constexpr (kMaxBoxes == 8) copy_boxes(std::integral_constant<int, 8>(), r, map, slot, bar);
+            // debug build: the box lies in the page, the head exists
+            (void)SWA_IN_BOUNDS(r.row + box <= a.ps && r.kvh < a.H_kv && r.page <= a.n_pages, &g_ptile_err);
+            if (my_c < D / 64)
+                tma_load_4d(sRing + slot * C::TBYTES + my_off, map, bar, my_c * 64, r.row, r.kvh, r.page);
+            __syncwarp();
         };
         if constexpr (NQT == 1) {
             // warp 0 copies the query tiles and keys, warp 2 the values: with pages of 16 a tile is 32
@@ -1038,7 +1012,7 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cu
     t.a = a;
     t.ws = w;
     t.TQ = x.TQ;
-    t.min_tiles = 4;
+    t.min_tiles = 2;
     t.o_align32 = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.o_st[0] % 16 == 0 && a.o_st[1] % 16 == 0;
     t.fault_stop_fill = fault_plan().band_stop_fill;
     return launch_dependent(after_append, paged_tile_kernel<D>, dim3(x.ctas), C::THREADS, C::SMEM, s, mq, mk, mv, t);
