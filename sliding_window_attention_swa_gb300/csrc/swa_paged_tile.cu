@@ -7,18 +7,18 @@
 // tokens reach; the batch's tiles are shared out evenly over one persistent CTA per SM
 // (swa_paged.cuh), a part of a unit that a CTA has is a piece.
 // Roles:
-//   warp 0        K/V producer: K_0, V_0, K_1, V_1, ... of every piece into a ring of NSLOT
-//                 shared-memory slots by TMA, one box per page (or part of a page) and 64 elements
-//                 of the head; the pages are looked up two tiles ahead.  V_j and
-//                 K_{j+1} are copied together and signal one barrier, that of K_{j+1}'s slot.
-//                 Pages past the sequence's end or not there read past the pool: zeros.
+//   warps 0, 2    producers of the keys and of the values: K_0, V_0, K_1, V_1, ... of every piece into
+//                 a ring of NSLOT shared-memory slots by TMA, one box per page (or part of a page)
+//                 and 64 elements of the head, one lane each; the pages are looked up 32 boxes ahead.
+//                 Pages past the sequence's end or not there read past the pool: zeros.  Two warps,
+//                 since a copy takes about 70 cycles of the warp that issues it and a tile on pages
+//                 of 16 is 32 copies.  Every fill has its own arrival and its own release.
 //   warp 1        TMEM owner and MMA issuer (warp-uniform loop, one elected lane issues):
 //                   S  = Q K_j^T (A = Q from shared memory, at head dim 256 from tensor memory)
 //                   O += P V_j   (A = P from tensor memory)
-//   warp 2        Q loader; at head dim 256, where the query tile passes through the ring, producer of
-//                 the values beside warp 0.
 //   warp 3        planner: finds the CTA's pieces, up to NP ahead of the others, and hands them over
-//                 through shared memory, so that no other role spends its time on that.
+//                 through shared memory, so that no other role spends its time on that; it also
+//                 loads the query tiles (at head dim 256 they pass through the ring, by warp 0).
 //   softmax WGs   NQT warpgroups; one row per thread (TMEM lane).  Running max in the log2
 //                 domain; P = 2^(x - m) is rounded to bf16 over the S columns it came from, the
 //                 row sum takes it unrounded; O is rescaled in TMEM only when a row's max grows by
@@ -153,25 +153,11 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     const uint32_t bar_drain = bars + 8u * (13 + 2 * NSLOT);
     auto bar_piece = [&](int i) { return bars + 8u * (14 + 2 * NSLOT + i); };
     auto bar_used = [&](int i) { return bars + 8u * (14 + 2 * NSLOT + C::NP + i); };
-    // Ring fills, numbered over the CTA's share; fill p lies in slot p % NSLOT.
-    // NQT = 1: a piece's query tile (two fills), then K and V of each of its tiles.  Every fill
-    // has its own arrival and its own release: phase (p / NSLOT) & 1 of the slot's barriers.
+    // Ring fills, numbered over the CTA's share; fill p lies in slot p % NSLOT, phase (p / NSLOT) & 1
+    // of the slot's barriers.  A piece's query tile comes first at head dim 256 (two fills), then K
+    // and V of each of its tiles: kfill is K of the share's g-th tile, in its k-th piece, V the next.
     auto fphase = [&](int p) -> uint32_t { return static_cast<uint32_t>((p / NSLOT) & 1); };
-    auto kfill = [&](int k, int g) { return 2 * (k + 1) + 2 * g; };  // K of tile g, in piece k (V: the next)
-    // NQT = 2: fill 2g is the key tile, 2g + 1 the value tile of the g-th tile.  Key fills release
-    // slots, once their S MMAs and the P V of the value tile before them are done (kpar).
-    // V_g and K_{g+1} land on K_{g+1}'s slot barrier, which thus completes for key fills only (and
-    // for the CTA's last value fill, which has no key fill after it): fpar(q) is the parity of
-    // owner fill q's completion.  An odd ring's slots alternate key and value fills.
-    auto kpar = [&](int p) -> uint32_t {
-        const int sl = p % NSLOT, i = p / NSLOT;
-        return static_cast<uint32_t>((NSLOT % 2 == 1 ? (i - (sl & 1)) / 2 : i) & 1);
-    };
-    auto fpar = [&](int q) -> uint32_t {
-        const int sl = q % NSLOT, i = q / NSLOT;
-        const int n = NSLOT % 2 == 1 ? (i - (sl & 1) + 1) / 2 : (sl % 2 == 0 ? i : 0);
-        return static_cast<uint32_t>(n & 1);
-    };
+    auto kfill = [&](int k, int g) { return (NQT == 1 ? 2 * (k + 1) : 0) + 2 * g; };
     Share *share = reinterpret_cast<Share *>(sgen + C::OFF_SHARE);
     volatile int *abort = reinterpret_cast<volatile int *>(sgen + C::OFF_TMEMPTR + 4);
     volatile uint32_t *tmem_holder = reinterpret_cast<volatile uint32_t *>(sgen + C::OFF_TMEMPTR);
@@ -193,7 +179,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         }
         for (int i = 0; i < C::NP; ++i) {
             mbar_init(bar_piece(i), 1);
-            mbar_init(bar_used(i), 3 + 4 * NQT);  // the other roles' warps
+            // the roles' warps: producers, MMA, softmax and (two query tiles) the query loader
+            mbar_init(bar_used(i), 2 + NQT + 4 * NQT);
         }
         mbar_init(bar_meet, 8);
         mbar_init(bar_drain, 1);
@@ -235,8 +222,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     // a unit whose tokens fill one of its two query tiles at most (tokens: of its sequence)
     auto is_single = [&](int tokens, int ut) { return NQT == 2 && tokens - ut * TT <= ta.TQ; };
 
-    if (warp == 0 || (NQT == 1 && warp == 2)) {
-        // ============================ K/V producer ============================
+    if (warp == 0 || warp == 2) {
+        // ============================ K/V producers ============================
         if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
         // the scratch of the work split lies in the ring: order its generic accesses before the copies
         fence_proxy_async_smem();
@@ -315,144 +302,51 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 tma_load_4d(sRing + slot * C::TBYTES + my_off, map, bar, my_c * 64, r.row, r.kvh, r.page);
             __syncwarp();
         };
-        if constexpr (NQT == 1) {
-            // warp 0 copies the query tiles and keys, warp 2 the values: with pages of 16 a tile is 32
-            // copies, more than one warp issues in a tile's time
-            const bool values = warp == 2;
-            int last = 0;       // this warp's last fill
-            uint32_t mine = 0;  // bit i: it issued fill last - i
-            // fill f's slot, once its last occupant has been released, with `bytes` expected on its barrier
-            auto next_slot = [&](int f, int bytes) -> bool {
-                if (f >= ta.fault_stop_fill) return false;  // planted fault: this fill is never issued
-                const int slot = f % NSLOT;
-                if (f >= NSLOT && !warp_wait(bar_empty(slot), fphase(f - NSLOT), abort)) return false;
-                if (lane == 0) mbar_arrive_expect_tx(bar_full(slot), static_cast<uint32_t>(bytes));
-                __syncwarp();
-                mine = (f - last < 32 ? mine << (f - last) : 0u) | 1u;
-                last = f;
-                return true;
-            };
-            Ref r{};
-            int pc = 0;  // pieces begun
-            if (cta_tiles > 0) {
-                then = look_up();
-                r = next_tile();
-            }
-#pragma unroll 1
-            for (int t = 0; t < cta_tiles && ok; ++t) {
-                if (r.token >= 0) ++pc;
-                const int f = kfill(pc - 1, t);
-                if (values) {
-                    ok = next_slot(f + 1, C::TBYTES);
-                    if (ok) copy(r, &tm_v, (f + 1) % NSLOT, bar_full((f + 1) % NSLOT));
-                } else {
-                    if (r.token >= 0) {
-#pragma unroll 1
-                        for (int q = f - 2; q < f && ok; ++q) {
-                            ok = next_slot(q, a.G * ta.TQ * D);
-                            if (!ok) break;
-                            // debug build: the tile's tokens and its group's heads exist
-                            (void)SWA_IN_BOUNDS(r.token < a.N && (r.kvh + 1) * a.G <= a.H_q, &g_ptile_err);
-                            if (lane < D / 128)
-                                tma_load_4d(sRing + q % NSLOT * C::TBYTES + lane * (BM * 128), &tm_q,
-                                            bar_full(q % NSLOT), (q - f + 2) * (D / 2) + lane * 64, r.kvh * a.G,
-                                            r.token, 0);
-                            __syncwarp();
-                        }
-                    }
-                    ok = ok && next_slot(f, C::TBYTES);
-                    if (ok) copy(r, &tm_k, f % NSLOT, bar_full(f % NSLOT));
-                }
-                if (t + 1 < cta_tiles) r = next_tile();
-            }
-            if (!ok && lane == 0)  // drain this warp's copies that may still be in flight: at most one a slot
-                for (int i2 = 0; i2 < NSLOT; ++i2)
-                    if ((mine >> i2) & 1u) mbar_drain(bar_full((last - i2) % NSLOT), fphase(last - i2), &g_ptile_err);
-        } else {
-        // a fill's slot is free once the key fill that releases its last occupant has done so
-        auto slot_free = [&](int q) -> bool {
-            if (q < NSLOT) return true;
-            const int prev = q - NSLOT, kp = (prev & 1) ? prev + 1 : prev;
-            return warp_wait(bar_empty(kp % NSLOT), kpar(kp), abort);
+        const bool values = warp == 2;
+        int last = 0;       // this warp's last fill
+        uint32_t mine = 0;  // bit i: it issued fill last - i
+        // fill f's slot, once its last occupant has been released, with `bytes` expected on its barrier
+        auto next_slot = [&](int f, int bytes) -> bool {
+            if (f >= ta.fault_stop_fill) return false;  // planted fault: this fill is never issued
+            const int slot = f % NSLOT;
+            if (f >= NSLOT && !warp_wait(bar_empty(slot), fphase(f - NSLOT), abort)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(bar_full(slot), static_cast<uint32_t>(bytes));
+            __syncwarp();
+            mine = (f - last < 32 ? mine << (f - last) : 0u) | 1u;
+            last = f;
+            return true;
         };
-        const int nfill = 2 * cta_tiles;
-        int g = 0;  // ring fills issued so far
-        // planted fault: only the steps whose fills all lie below the stop run (step t issues
-        // fills up to 2t + 2; the last step, fill nfill - 1 alone)
-        const int n_steps = ta.fault_stop_fill >= nfill ? cta_tiles : max(0, (ta.fault_stop_fill - 1) / 2);
-        if (nfill > 0) {
+        Ref r{};
+        int pc = 0;  // pieces begun
+        if (cta_tiles > 0) {
             then = look_up();
-            Ref cur = next_tile(), nxt = cur;
-            if (ok && ta.fault_stop_fill > 0) {
-                if (lane == 0) mbar_arrive_expect_tx(bar_full(0), C::TBYTES);
-                __syncwarp();
-                copy(cur, &tm_k, 0, bar_full(0));  // K_0 alone
-                g = 1;
-            }
-            if (cta_tiles > 1) nxt = next_tile();
-#pragma unroll 1
-            for (int t = 0; t < n_steps && ok; ++t) {
-                const bool has_next = t + 1 < cta_tiles;
-                const int pv = 2 * t + 1, own = has_next ? pv + 1 : pv;
-                ok = slot_free(pv) && (!has_next || slot_free(own));
-                if (!ok) break;
-                const uint32_t bar = bar_full(own % NSLOT);
-                if (lane == 0) mbar_arrive_expect_tx(bar, (has_next ? 2 : 1) * C::TBYTES);
-                __syncwarp();
-                if (has_next) copy(nxt, &tm_k, own % NSLOT, bar);
-                copy(cur, &tm_v, pv % NSLOT, bar);
-                g = own + 1;
-                cur = nxt;
-                if (t + 2 < cta_tiles) nxt = next_tile();
-            }
+            r = next_tile();
         }
-        ok = ok && n_steps == cta_tiles;
-        if (!ok && lane == 0) {
-            // drain the owner barriers of the copies that may still be in flight: fills below
-            // g - NSLOT have landed (their slots were released by readers that waited for them)
-            for (int q = max(0, g - NSLOT); q < g; ++q)
-                if ((q & 1) == 0 || q + 1 == nfill) mbar_drain(bar_full(q % NSLOT), fpar(q), &g_ptile_err);
-        }
-        }
-    } else if (warp == 2) {
-        // ============================ Q loader ============================
-        if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
-        int k = 0;
-        int loads[2] = {0, 0};  // phases of each tile's barrier
-        bool ok = true;
 #pragma unroll 1
-        for (; ok; ++k) {
-            volatile TilePiece *p = get_piece(k, ok);
-            if (!p) break;
-            const int tokens = p->n, i0 = p->ut * TT, q0 = p->q0, kvh = p->kvh;
-            give_back(k);
+        for (int t = 0; t < cta_tiles && ok; ++t) {
+            if (r.token >= 0) ++pc;
+            const int f = kfill(pc - 1, t) + (values ? 1 : 0);
+            if (NQT == 1 && !values && r.token >= 0) {
+                // the piece's query tile, in two halves
 #pragma unroll 1
-            for (int x = 0; x < NQT; ++x) {
-                // the previous piece's S MMAs are done with this tile's shared memory
-                if (k >= 1) ok = warp_wait(bar_qe(x), (k - 1) & 1, abort);
-                if (!ok) break;
-                if (lane == 0) {
-                    const int i = i0 + x * ta.TQ;  // the tile's first token
-                    if (i < tokens) {
-                        // debug build: the tile's tokens and its group's heads exist
-                        (void)SWA_IN_BOUNDS(q0 + i < a.N && (kvh + 1) * a.G <= a.H_q, &g_ptile_err);
-                        mbar_arrive_expect_tx(bar_qf(x), static_cast<uint32_t>(a.G * ta.TQ * D * 2));
-#pragma unroll
-                        for (int c = 0; c < D / 64; ++c)
-                            tma_load_4d(sQ + x * C::QBYTES + c * (BM * 128), &tm_q, bar_qf(x), c * 64, kvh * a.G,
-                                        q0 + i, 0);
-                    } else {
-                        mbar_arrive(bar_qf(x));  // the unit has no such tile
-                    }
+                for (int q = f - 2; q < f && ok; ++q) {
+                    ok = next_slot(q, a.G * ta.TQ * D);
+                    if (!ok) break;
+                    // debug build: the tile's tokens and its group's heads exist
+                    (void)SWA_IN_BOUNDS(r.token < a.N && (r.kvh + 1) * a.G <= a.H_q, &g_ptile_err);
+                    if (lane < D / 128)
+                        tma_load_4d(sRing + q % NSLOT * C::TBYTES + lane * (BM * 128), &tm_q, bar_full(q % NSLOT),
+                                    (q - f + 2) * (D / 2) + lane * 64, r.kvh * a.G, r.token, 0);
+                    __syncwarp();
                 }
-                __syncwarp();
-                ++loads[x];
             }
+            ok = ok && next_slot(f, C::TBYTES);
+            if (ok) copy(r, values ? &tm_v : &tm_k, f % NSLOT, bar_full(f % NSLOT));
+            if (t + 1 < cta_tiles) r = next_tile();
         }
-        if (!ok && lane == 0) {
-            for (int x = 0; x < NQT; ++x)
-                if (loads[x] > 0) mbar_drain(bar_qf(x), (loads[x] - 1) & 1, &g_ptile_err);
-        }
+        if (!ok && lane == 0)  // drain this warp's copies that may still be in flight: at most one a slot
+            for (int i2 = 0; i2 < NSLOT; ++i2)
+                if ((mine >> i2) & 1u) mbar_drain(bar_full((last - i2) % NSLOT), fphase(last - i2), &g_ptile_err);
     } else if (warp == 1) {
         // ============================ MMA issuer ============================
         if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
@@ -479,12 +373,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk) vd[kk] = desc_offset(v0, kk * 2048);
         };
-        // K_g, and with it V_{g-1}, has landed
-        auto have_k = [&](int g) -> bool { return warp_wait(bar_full((2 * g) % NSLOT), fpar(2 * g), abort); };
-        auto have_v = [&](int g) -> bool {
-            const int own = g + 1 < cta_tiles ? 2 * g + 2 : 2 * g + 1;
-            return warp_wait(bar_full(own % NSLOT), fpar(own), abort);
-        };
+        auto landed = [&](int f) -> bool { return warp_wait(bar_full(f % NSLOT), fphase(f), abort); };
         // S of the key tile in ring slot ks (landed) into TMEM slot `slot` from query tile qt
         auto mma_s = [&](int slot, int qt, int ks) {
             tc_fence_after();
@@ -498,16 +387,11 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             }
             tc_commit_e(bar_sf(slot));
         };
-        // O_ot (+)= P(slot) V (descriptors in vd) once P is there, and for a fresh O once the epilogue
-        // of the previous piece has read it; wait_v: V of tile g may not have landed yet
-        auto mma_pv = [&](int slot, int ot, bool first, uint32_t n_used, bool wait_v, int g) -> bool {
+        // O_ot (+)= P(slot) V (descriptors in vd) once P is there and, if wait_v >= 0, that fill, and for a
+        // fresh O once the epilogue of the previous piece has read it
+        auto mma_pv = [&](int slot, int ot, bool first, uint32_t n_used, int wait_v) -> bool {
             if (!warp_wait(bar_pf(slot), n_used & 1, abort)) return false;
-            if constexpr (NQT == 1) {
-                const int f = kfill(k, g) + 1;
-                if (!warp_wait(bar_full(f % NSLOT), fphase(f), abort)) return false;
-            } else {
-                if (wait_v && !have_v(g)) return false;
-            }
+            if (wait_v >= 0 && !landed(wait_v)) return false;
             if (first && k >= 1) {
                 if (!warp_wait(bar_of(ot), (k - 1) & 1, abort)) return false;
                 // (both warpgroups read both accumulators of a piece of one query tile)
@@ -527,63 +411,63 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             const bool single = is_single(p->n, p->ut);
             give_back(k);
             if constexpr (NQT == 2) {
-            ok = warp_wait(bar_qf(0), k & 1, abort);
-            // (the key tile of a later piece came with the value tile of the last one)
-            if (ok && J == 0) ok = have_k(0);
-            if (!ok) break;
-            const int ks0 = (2 * J) % NSLOT;
-            if (!single) {
-                mma_s(0, 0, ks0);
-                ok = warp_wait(bar_qf(1), k & 1, abort);
+                ok = warp_wait(bar_qf(0), k & 1, abort) && landed(2 * J);
                 if (!ok) break;
-                mma_s(1, NQT - 1, ks0);
-#pragma unroll 1
-                for (int i = 0; i < n; ++i) {
-                    const int g = J + i, ks = (2 * g + 2) % NSLOT;
-                    v_descs((2 * g + 1) % NSLOT);
-                    ok = mma_pv(0, 0, i == 0, np0 + i, true, g);  // (K_{g+1} has landed too then)
+                mma_s(0, 0, (2 * J) % NSLOT);
+                if (!single) {
+                    ok = warp_wait(bar_qf(1), k & 1, abort);
                     if (!ok) break;
-                    if (i + 1 < n) mma_s(0, 0, ks);
-                    else tc_commit_e(bar_od(0));
-                    ok = mma_pv(1, 1, i == 0, np1 + i, false, g);
-                    if (!ok) break;
-                    if (i + 1 < n) mma_s(1, NQT - 1, ks);
-                    else tc_commit_e(bar_od(1));
-                }
-                np0 += n;
-                np1 += n;
-                was_single = false;
-            } else {
-                // one query tile, its key tiles in slot 0 and 1 in turn.  S of tile i + 1 is issued
-                // before P V of tile i, so the commit after that P V releases K_{i+1}.
-                ok = warp_wait(bar_qf(1), k & 1, abort);
-                if (!ok) break;
-                mma_s(0, 0, ks0);
-                tc_commit_e(bar_empty(ks0));
+                    mma_s(1, NQT - 1, (2 * J) % NSLOT);
 #pragma unroll 1
-                for (int i = 0; i < n; ++i) {
-                    const int g = J + i, x = i & 1;
-                    if (i + 1 < n) {  // S of tile i + 1 into the other slot, whose P V is issued
-                        ok = have_k(g + 1);
+                    for (int i = 0; i < n; ++i) {
+                        const int f = 2 * (J + i), ks = (f + 2) % NSLOT;
+                        v_descs((f + 1) % NSLOT);
+                        ok = mma_pv(0, 0, i == 0, np0 + i, f + 1);
                         if (!ok) break;
-                        mma_s(x ^ 1, 0, (2 * g + 2) % NSLOT);
+                        if (i + 1 < n) {
+                            ok = landed(f + 2);
+                            if (!ok) break;
+                            mma_s(0, 0, ks);
+                        } else {
+                            tc_commit_e(bar_od(0));
+                        }
+                        ok = mma_pv(1, 1, i == 0, np1 + i, -1);
+                        if (!ok) break;
+                        if (i + 1 < n) mma_s(1, NQT - 1, ks);
+                        else tc_commit_e(bar_od(1));
                     }
-                    v_descs((2 * g + 1) % NSLOT);
-                    ok = mma_pv(x, x, i < 2, x ? np1++ : np0++, i + 1 == n, g);
+                    np0 += n;
+                    np1 += n;
+                } else {
+                    // one query tile, its key tiles in slot 0 and 1 in turn
+                    tc_commit_e(bar_empty((2 * J) % NSLOT));
+                    ok = warp_wait(bar_qf(1), k & 1, abort);
                     if (!ok) break;
-                    if (i + 1 < n) tc_commit_e(bar_empty((2 * (g + 1)) % NSLOT));
+#pragma unroll 1
+                    for (int i = 0; i < n; ++i) {
+                        const int f = 2 * (J + i), x = i & 1;
+                        if (i + 1 < n) {  // S of tile i + 1 into the other slot, whose P V is issued
+                            ok = landed(f + 2);
+                            if (!ok) break;
+                            mma_s(x ^ 1, 0, (f + 2) % NSLOT);
+                            tc_commit_e(bar_empty((f + 2) % NSLOT));
+                        }
+                        v_descs((f + 1) % NSLOT);
+                        ok = mma_pv(x, x, i < 2, x ? np1++ : np0++, f + 1);
+                        if (!ok) break;
+                        tc_commit_e(bar_empty((f + 1) % NSLOT));
+                    }
+                    if (!ok) break;
+                    tc_commit_e(bar_od(0));
+                    tc_commit_e(bar_od(1));
                 }
                 if (!ok) break;
-                tc_commit_e(bar_od(0));
-                tc_commit_e(bar_od(1));
-                was_single = true;
-            }
+                was_single = single;
             } else {
                 // the piece's query tile into tensor memory, 16 columns per copy (the previous piece's
                 // last S MMA precedes the copies in the tensor pipe), which frees its two slots
                 const int fq = 2 * k + 2 * J;
-                ok = warp_wait(bar_full(fq % NSLOT), fphase(fq), abort) &&
-                     warp_wait(bar_full((fq + 1) % NSLOT), fphase(fq + 1), abort);
+                ok = landed(fq) && landed(fq + 1);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -597,7 +481,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 // S of tile g, whose slot is free once it is done
                 auto next_s = [&](int g) -> bool {
                     const int f = kfill(k, g), slot = f % NSLOT;
-                    if (!warp_wait(bar_full(slot), fphase(f), abort)) return false;
+                    if (!landed(f)) return false;
                     mma_s(g & 1, 0, slot);
                     tc_commit_e(bar_empty(slot));
                     return true;
@@ -606,12 +490,12 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 if (!ok) break;
 #pragma unroll 1
                 for (int i = 0; i < n; ++i) {
-                    const int g = J + i, vs = (kfill(k, g) + 1) % NSLOT;
+                    const int g = J + i, fv = kfill(k, g) + 1, vs = fv % NSLOT;
                     // slot (g+1) & 1 last held P of tile g-1, consumed by its P V issued earlier
                     if (i + 1 < n) ok = next_s(g + 1);
                     if (!ok) break;
                     v_descs(vs);
-                    ok = mma_pv(g & 1, 0, i == 0, static_cast<uint32_t>(g >> 1), true, g);
+                    ok = mma_pv(g & 1, 0, i == 0, static_cast<uint32_t>(g >> 1), fv);
                     if (!ok) break;
                     tc_commit_e(bar_empty(vs));
                     if (i + 1 == n) tc_commit_e(bar_od(0));
@@ -670,8 +554,11 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     // the piece's last S from this query tile: the next piece's rows may load
                     if (i + 1 == n && lane == 0) mbar_arrive(bar_qe(wg));
                     // S_B(g) was the last MMA issued before this commit: every reader of K_g and of
-                    // V_{g-1} is done
-                    if (wg == 1 && quarter == 0 && lane == 0) mbar_arrive(bar_empty((2 * g) % NSLOT));
+                    // V_{g-1} is done (released here, not by more commits of the MMA warp)
+                    if (wg == 1 && quarter == 0 && lane == 0) {
+                        mbar_arrive(bar_empty((2 * g) % NSLOT));
+                        if (i > 0) mbar_arrive(bar_empty((2 * g - 1) % NSLOT));
+                    }
                 }
                 tc_fence_after();
                 const uint32_t s_addr = tmem + lane_addr + C::tm_s(slot);
@@ -782,10 +669,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     // the sequence ends in this tile: zero the value rows of its last page past the
                     // end (later pages came as zeros).  The first P V of the tile waits for this
                     // warpgroup's P, and with two query tiles the second is issued after it.
-                    // (with two query tiles V_g lands with K_{g+1})
-                    const int fv = NQT == 1 ? kfill(k, g) + 1 : 2 * g + 1;
-                    const int own = NQT == 2 && g + 1 < cta_tiles ? fv + 1 : fv;
-                    if (!warp_wait(bar_full(own % NSLOT), NQT == 1 ? fphase(own) : fpar(own), abort)) {
+                    const int fv = kfill(k, g) + 1;
+                    if (!warp_wait(bar_full(fv % NSLOT), fphase(fv), abort)) {
                         ok = false;
                         break;
                     }
@@ -811,10 +696,12 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 break;
             }
             tc_fence_after();
+            if (NQT == 2 && !single && wg == 1 && quarter == 0 && lane == 0)
+                mbar_arrive(bar_empty((2 * (J + n) - 1) % NSLOT));  // the piece's last value tile
             // weights of this row's two accumulators (one unless the warpgroups shared the tile)
             float wa = 1.f, wb = 0.f;
             if (single) {
-                // every MMA of the piece has completed: the Q loader may refill the tile
+                // every MMA of the piece has completed: the tile may be refilled
                 if (lane == 0) mbar_arrive(bar_qe(wg));
                 // (the other warpgroup has read the last meeting's values: this piece's first P V
                 // waited for both epilogues)
@@ -907,37 +794,22 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         // ============================ planner ============================
         if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
         const Share sh = *share;
+        const int grid = static_cast<int>(gridDim.x);
         bool ok = true;
-        int k = 0;
         int4 open = make_int4(0, 0, 0, 0);
-        auto hand_over = [&](const Piece &p) {
-            if (ok && k >= C::NP) ok = warp_wait(bar_used(k % C::NP), (k / C::NP - 1) & 1, abort);
-            if (!ok) return;
-            if (lane == 0) {
-                volatile TilePiece *t = pieces + k % C::NP;
-                t->b = p.b;
-                t->kvh = p.kvh;
-                t->ut = p.ut;
-                t->q0 = p.s.q0;
-                t->n = p.s.n;
-                t->p0 = p.s.p0;
-                t->sink = p.u.sink;
-                t->lo = p.u.lo;
-                t->nt = p.u.n;
-                t->j0 = p.j0;
-                t->j1 = p.j1;
-                mbar_arrive(bar_piece(k % C::NP));
-            }
-            __syncwarp();
-            ++k;
-        };
         Piece p{};
-        // whole units, one a wave: the sequences are searched 32 at a time from block b0, whose
-        // first unit is u0
-        int b0 = 0, u0 = 0;
-        for (int w = 0; w < sh.waves && ok; ++w) {
-            const int grid = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-            const int u = w * grid + (w & 1 ? grid - 1 - c : c);
+        Walk<BN> walk(a, TT, sh);
+        // Whole units, one a wave: the sequences are searched 32 at a time from block b0, whose first
+        // unit is u0.  Then the share's stretch.
+        int w = 0, b0 = 0, u0 = 0;
+        auto next_piece = [&]() -> bool {
+            if (w >= sh.waves) {
+                const bool more = walk.next(p);
+                if (more && p.open() && !p.begun()) open = make_int4(p.u.n - p.j1, p.b, p.kvh, p.ut);
+                return more;
+            }
+            const int c = static_cast<int>(blockIdx.x), u = w * grid + (w & 1 ? grid - 1 - c : c);
+            ++w;
             while (b0 < a.B) {
                 Seq s{};
                 if (b0 + lane < a.B) s = load_seq(a, b0 + lane);
@@ -961,20 +833,85 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     p.u = unit_tiles<BN>(a, p.s, p.ut, TT);
                     p.j0 = 0;
                     p.j1 = p.u.n;
-                    hand_over(p);
-                    break;
+                    return true;
                 }
                 u0 += __shfl_sync(0xffffffffu, inc, 31);
                 b0 += 32;
             }
+            return false;  // (cannot be: the waves' units exist)
+        };
+        int k = 0, kq = 0;  // pieces handed over, query tiles loaded
+        int loads[2] = {0, 0};
+        bool more = true;
+#pragma unroll 1
+        while (ok && (more || (NQT == 2 && kq < k))) {
+            // hand over while there are free places; with query tiles to load, without waiting for one
+#pragma unroll 1
+            while (more) {
+                const int e = k % C::NP;
+                if (k >= C::NP) {
+                    const uint32_t parity = (k / C::NP - 1) & 1;
+                    if (NQT == 2 && kq < k) {
+                        if (!__all_sync(0xffffffffu, mbar_test_wait(bar_used(e), parity))) break;
+                    } else {
+                        ok = warp_wait(bar_used(e), parity, abort);
+                        if (!ok) break;
+                    }
+                }
+                more = next_piece();
+                if (!more) p.j0 = p.j1 = 0;  // the end of the list
+                if (lane == 0) {
+                    volatile TilePiece *t = pieces + e;
+                    t->b = p.b;
+                    t->kvh = p.kvh;
+                    t->ut = p.ut;
+                    t->q0 = p.s.q0;
+                    t->n = p.s.n;
+                    t->p0 = p.s.p0;
+                    t->sink = p.u.sink;
+                    t->lo = p.u.lo;
+                    t->nt = p.u.n;
+                    t->j0 = p.j0;
+                    t->j1 = p.j1;
+                    mbar_arrive(bar_piece(e));
+                }
+                __syncwarp();
+                if (more) ++k;
+            }
+            if constexpr (NQT == 2) {
+                if (!ok || kq >= k) continue;
+                volatile TilePiece *t = pieces + kq % C::NP;
+                const int tokens = t->n, i0 = t->ut * TT, q0 = t->q0, kvh = t->kvh;
+                give_back(kq);
+#pragma unroll 1
+                for (int x = 0; x < NQT; ++x) {
+                    // the previous piece's S MMAs are done with this tile's shared memory
+                    if (kq >= 1) ok = warp_wait(bar_qe(x), (kq - 1) & 1, abort);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const int i = i0 + x * ta.TQ;  // the tile's first token
+                        if (i < tokens) {
+                            // debug build: the tile's tokens and its group's heads exist
+                            (void)SWA_IN_BOUNDS(q0 + i < a.N && (kvh + 1) * a.G <= a.H_q, &g_ptile_err);
+                            mbar_arrive_expect_tx(bar_qf(x), static_cast<uint32_t>(a.G * ta.TQ * D * 2));
+#pragma unroll
+                            for (int c = 0; c < D / 64; ++c)
+                                tma_load_4d(sQ + x * C::QBYTES + c * (BM * 128), &tm_q, bar_qf(x), c * 64, kvh * a.G,
+                                            q0 + i, 0);
+                        } else {
+                            mbar_arrive(bar_qf(x));  // the unit has no such tile
+                        }
+                    }
+                    __syncwarp();
+                    ++loads[x];
+                }
+                ++kq;
+            }
         }
-        Walk<BN> walk(a, TT, sh);
-        while (ok && walk.next(p)) {
-            if (p.open() && !p.begun()) open = make_int4(p.u.n - p.j1, p.b, p.kvh, p.ut);
-            hand_over(p);
+        if (!ok && lane == 0) {
+            for (int x = 0; x < NQT; ++x)
+                if (loads[x] > 0) mbar_drain(bar_qf(x), (loads[x] - 1) & 1, &g_ptile_err);
         }
-        p.j0 = p.j1 = 0;
-        hand_over(p);
         if (lane == 0) {
             ta.ws.open[blockIdx.x] = open;
             ta.ws.first[blockIdx.x] = sh.first;
