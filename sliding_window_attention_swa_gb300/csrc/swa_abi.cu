@@ -724,7 +724,8 @@ swa_status swa_paged_attend(const swa_paged_params *p, const swa_paged_cache *c,
 swa_status swa_paged_append(const swa_paged_params *p, const swa_paged_cache *c, swa_stream_t stream) {
     const swa_status st = paged_rows_check(p, c, true);
     if (st != SWA_OK || p->N == 0) return st;
-    if (failed(swa::launch_paged_append(paged_args(p, c), reinterpret_cast<cudaStream_t>(stream)))) return SWA_ERR_CUDA;
+    if (failed(swa::launch_paged_append(paged_args(p, c), nullptr, 0, reinterpret_cast<cudaStream_t>(stream))))
+        return SWA_ERR_CUDA;
     return SWA_OK;
 }
 

@@ -95,10 +95,12 @@ __device__ __forceinline__ UnitTiles unit_tiles(const PagedArgs &a, const Seq &s
 }
 
 // A CTA's share: `waves` whole units, then from tile j of unit (b, kvh, ut), tile `first` of the
-// list, `left` tiles in list order; `tiles` in all.
+// list, `left` tiles in list order; `tiles` in all.  turn: its number among the CTAs that have a
+// stretch.  owner, pieces: the turn of the CTA that begins the unit of the first tile, and the
+// CTAs that share it; open_pieces: those that share the unit of the last tile.
 struct Share {
     long long first;
-    int b, kvh, ut, j, left, waves, tiles;
+    int b, kvh, ut, j, left, waves, tiles, turn, owner, pieces, open_pieces;
 };
 
 // One unit's part of a CTA's share: tiles j0 .. j1 - 1.
@@ -159,13 +161,19 @@ template <int D>
 __device__ __forceinline__ int64_t partial_at(int64_t slot, int rows, int row, int col) {
     return ((slot * (D / 8) + col / 8) * rows + row) * 8 + col % 8;
 }
-__device__ __forceinline__ int piece_slot(const Piece &p) { return 2 * static_cast<int>(blockIdx.x) + (p.begun() ? 0 : 1); }
+// The split kernel's slot of a piece (a CTA's turn is its index).
+__device__ __forceinline__ int piece_slot(const Piece &p) {
+    return 2 * static_cast<int>(blockIdx.x) + (p.begun() ? 0 : 1);
+}
 
-// Tile X of the list, looked up by one warp, as the start of a share; tiles: tiles of one kv head
-// of each sequence.
+// Tile X of the list: tile j of unit (b, kvh, ut), which has n.
+struct Place {
+    int b, kvh, ut, j, n;
+};
+// Looked up by one warp; tiles: tiles of one kv head of each sequence.
 template <int BN>
-__device__ __forceinline__ void find_tile(const PagedArgs &a, int TT, const long long *tiles, long long X, int lane,
-                                          Share &r) {
+__device__ __forceinline__ Place find_tile(const PagedArgs &a, int TT, const long long *tiles, long long X, int lane) {
+    Place r{0, 0, 0, 0, 1};
     long long before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
         const long long v = b0 + lane < a.B ? tiles[b0 + lane] * a.H_kv : 0;
@@ -202,10 +210,12 @@ __device__ __forceinline__ void find_tile(const PagedArgs &a, int TT, const long
             const int l = __ffs(past) - 1;
             r.ut = u0 + l;
             r.j = static_cast<int>(rel - __shfl_sync(0xffffffffu, inc - v, l));
+            r.n = __shfl_sync(0xffffffffu, v, l);
             break;
         }
         rel -= __shfl_sync(0xffffffffu, inc, 31);
     }
+    return r;
 }
 
 constexpr int kMaxWaveCtas = 256;
@@ -229,6 +239,7 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
     // latency of a small batch; 2.3 us less than the general way for one sequence of one token)
     if (a.B <= 32) {
         constexpr int kFew = 4;
+        bool found = false;
         if (warp == 0) {
             Seq s{};
             if (lane < a.B) {
@@ -253,34 +264,51 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
                 }
                 const long long total = __shfl_sync(0xffffffffu, inc, 31);
                 const long long len = max((total + grid - 1) / grid, static_cast<long long>(min_tiles));
-                Share sh{min(len * static_cast<long long>(blockIdx.x), total), 0, 0, 0, 0, 0, 0, 0};
-                sh.left = sh.tiles = static_cast<int>(min(len, total - sh.first));
-                const unsigned past = __ballot_sync(0xffffffffu, inc > sh.first);
-                if (past) {
-                    const int l = __ffs(past) - 1;
-                    if (lane == l) {  // tile `rel` of sequence l: its kv head, then the unit
-                        const long long rel = sh.first - (inc - static_cast<long long>(sum) * a.H_kv);
-                        sh.b = l;
-                        sh.kvh = static_cast<int>(rel / sum);
-                        int j = static_cast<int>(rel - static_cast<long long>(sh.kvh) * sum);
+                const int c = static_cast<int>(blockIdx.x);
+                const long long first = min(len * c, total);
+                const int left = static_cast<int>(min(len, total - first));
+                // tile X, in the lane of its sequence
+                auto place = [&](long long X) -> Place {
+                    const long long rel = X - (inc - static_cast<long long>(sum) * a.H_kv);
+                    Place p{lane, static_cast<int>(rel / sum), 0, 0, n[0]};
+                    p.j = static_cast<int>(rel - static_cast<long long>(p.kvh) * sum);
 #pragma unroll
-                        for (int ut = 0; ut < kFew - 1; ++ut)
-                            if (sh.ut == ut && j >= n[ut]) {
-                                j -= n[ut];
-                                ++sh.ut;
-                            }
-                        sh.j = j;
-                        *out = sh;
+                    for (int ut = 0; ut < kFew - 1; ++ut)
+                        if (p.ut == ut && p.j >= n[ut]) {
+                            p.j -= n[ut];
+                            ++p.ut;
+                            p.n = n[ut + 1];
+                        }
+                    return p;
+                };
+                if (left == 0) {
+                    if (lane == 0) *out = Share{first, 0, 0, 0, 0, 0, 0, 0, c, 0, 0, 0};
+                } else {
+                    const int l0 = __ffs(__ballot_sync(0xffffffffu, inc > first)) - 1;
+                    const int l1 = __ffs(__ballot_sync(0xffffffffu, inc > first + left - 1)) - 1;
+                    if (lane == l0) {
+                        const Place p = place(first);
+                        const long long u0 = first - p.j;  // the unit's first tile
+                        out->first = first;
+                        out->b = p.b;
+                        out->kvh = p.kvh;
+                        out->ut = p.ut;
+                        out->j = p.j;
+                        out->left = out->tiles = left;
+                        out->waves = 0;
+                        out->turn = c;
+                        out->owner = static_cast<int>(u0 / len);
+                        out->pieces = static_cast<int>((u0 + p.n - 1) / len) - out->owner + 1;
                     }
-                } else if (lane == 0) {
-                    *out = sh;
+                    if (lane == l1) {
+                        const Place p = place(first + left - 1);
+                        out->open_pieces = static_cast<int>((first + left - 1 - p.j + p.n - 1) / len) - c + 1;
+                    }
                 }
             }
-            if (lane == 0) scratch[0] = few;
+            found = few;
         }
-        __syncthreads();
-        if (scratch[0]) return;
-        __syncthreads();  // the scratch is rewritten below
+        if (__syncthreads_or(found)) return;
     }
     long long *tiles = reinterpret_cast<long long *>(scratch);
     int *units = reinterpret_cast<int *>(scratch + a.B * 8), *loads = units + a.B + 1;
@@ -352,22 +380,22 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
         }
     }
     __syncthreads();
-    // 4. this CTA's stretch of the list
-    if (warp == 0) {
+    // 4. this CTA's stretch of the list, by warp 0 with its first tile, by warp 1 with its last
+    if (warp < 2) {
         long long all = 0;
         for (int b = lane; b < a.B; b += 32) all += tiles[b];
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
         const long long total = all * a.H_kv;
         const int c = static_cast<int>(blockIdx.x);
-        Share sh{0, 0, 0, 0, 0, 0, waves, 0};
-        long long len;
+        constexpr int kPer = kMaxWaveCtas / 32;
+        long long first, len, begin[kPer];  // begin, q: the stretch of CTA 32 * i + lane (waves > 0)
+        int q[kPer], mine = 0, turn = c;
         if (waves == 0) {
             len = max((total + grid - 1) / grid, static_cast<long long>(min_tiles));
-            sh.first = len * c;
+            first = len * c;
         } else {
             // the tail fills the CTAs up to one level: the least at which all of it fits
-            constexpr int kPer = kMaxWaveCtas / 32;
             int ld[kPer], top = 0;
             long long bulk = 0;
 #pragma unroll
@@ -397,25 +425,71 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
                 }
                 level = lo;
             }
-            // before this CTA's stretch: those of the CTAs below
-            long long before = 0;
-            int mine = 0;
+            long long at = bulk;
+            first = len = 0;
+            turn = 0;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                if (32 * i + lane < c) before += ld[i] < level ? level - ld[i] : 0;
-                if (32 * i + lane == c) mine = ld[i];
-            }
+                const int want = ld[i] < level ? level - ld[i] : 0;
+                long long inc = want;
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-            sh.tiles = __shfl_sync(0xffffffffu, mine, c % 32);
-            sh.first = bulk + before;
-            len = max(0, level - sh.tiles);
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += t;
+                }
+                begin[i] = at + inc - want;
+                q[i] = static_cast<int>(max(min(static_cast<long long>(want), total - begin[i]), 0ll));
+                turn += __popc(__ballot_sync(0xffffffffu, q[i] > 0 && 32 * i + lane < c));
+                if (i == c / 32) {
+                    first = __shfl_sync(0xffffffffu, begin[i], c % 32);
+                    len = __shfl_sync(0xffffffffu, q[i], c % 32);
+                    mine = __shfl_sync(0xffffffffu, ld[i], c % 32);
+                }
+                at += __shfl_sync(0xffffffffu, inc, 31);
+            }
         }
-        sh.first = min(sh.first, total);
-        sh.left = static_cast<int>(min(len, total - sh.first));
-        sh.tiles += sh.left;
-        if (sh.left > 0) find_tile<BN>(a, TT, tiles, sh.first, lane, sh);
-        if (lane == 0) *out = sh;
+        first = min(first, total);
+        const int left = static_cast<int>(min(len, total - first));
+        // the turn of the CTA that has tile X of the tail, and the CTAs that have some of [X, Y)
+        auto turn_of = [&](long long X) -> int {
+            if (waves == 0) return static_cast<int>(X / len);
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) n += __popc(__ballot_sync(0xffffffffu, q[i] > 0 && begin[i] + q[i] <= X));
+            return n;
+        };
+        if (warp == 0) {
+            Share sh{first, 0, 0, 0, 0, left, waves, mine + left, turn, 0, 0, 0};
+            if (left > 0) {
+                const Place p = find_tile<BN>(a, TT, tiles, first, lane);
+                sh.b = p.b;
+                sh.kvh = p.kvh;
+                sh.ut = p.ut;
+                sh.j = p.j;
+                if (kWaves) {
+                    sh.owner = turn_of(first - p.j);
+                    sh.pieces = turn_of(first - p.j + p.n - 1) - sh.owner + 1;
+                }
+            }
+            if (lane == 0) {  // (open_pieces is warp 1's)
+                out->first = sh.first;
+                out->b = sh.b;
+                out->kvh = sh.kvh;
+                out->ut = sh.ut;
+                out->j = sh.j;
+                out->left = sh.left;
+                out->waves = sh.waves;
+                out->tiles = sh.tiles;
+                out->turn = sh.turn;
+                out->owner = sh.owner;
+                out->pieces = sh.pieces;
+            }
+        } else if (kWaves && left > 0) {
+            const long long X = first + left - 1;
+            const Place p = find_tile<BN>(a, TT, tiles, X, lane);
+            const int n = turn_of(X - p.j + p.n - 1) - turn + 1;
+            if (lane == 0) out->open_pieces = n;
+        }
     }
     __syncthreads();
 }

@@ -31,52 +31,54 @@ struct PagedArgs {
 
 constexpr int kPagedMaxB = 8192;
 
-// Partial results of units that several CTAs share.  CTA c has two slots of `rows` rows: 2c for
-// the unit that an earlier CTA began, 2c + 1 for one that it begins and leaves open (only its
-// last unit can be).
+// Partial results of units that several CTAs share.  The CTAs that have a stretch of the shared-out
+// list are numbered t = 0, 1, ... in its order; number t has two slots of `rows` rows: 2t for the
+// unit that an earlier CTA began, 2t + 1 for one that it begins and leaves open (only its last
+// unit can be).
 struct PagedWs {
-    float *ml;   // [2 * CTAs][rows][2]: maximum (log2 units), sum
-    float *acc;  // [2 * CTAs][D / 8][rows][8]: unnormalised weighted values
-    int4 *open;        // [CTAs] {tiles that the unit left open still has for later CTAs (0: none), b, kvh, ut}
-    long long *first;  // [CTAs] where its stretch of the list starts
-    int32_t *left;     // [CTAs] and its tiles
+    float *ml;    // [2 * CTAs][rows][2]: maximum (log2 units), sum
+    float *acc;   // [2 * CTAs][D / 8][rows][8]: unnormalised weighted values
+    int32_t *done;  // tile kernel, [CTAs][8]: pieces of the unit that CTA t began which are written, by warp
+    int4 *open;     // split kernel, [CTAs]: {tiles that the unit left open still has for later CTAs (0: none), b, kvh, ut}
+    long long *first;  // split kernel, [CTAs]: where its stretch of the list starts
+    int32_t *left;     // split kernel, [CTAs]: and its tiles
 };
 // A kernel's grid and the shape of its units: tiles of query rows (row r of a tile is token
 // r / G, head r % G of the group), tokens a tile.
 struct PagedShape {
     int ctas, tiles, rows, TQ;
 };
+inline size_t paged_up(size_t v) { return (v + 255) & ~size_t(255); }
 inline size_t paged_ws_bytes(const PagedShape &x, int D) {
-    auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     const size_t rows = static_cast<size_t>(x.ctas) * 2 * x.tiles * x.rows;
-    return up(rows * 2 * sizeof(float)) + up(rows * D * sizeof(float)) + up(x.ctas * sizeof(int4)) +
-           up(x.ctas * sizeof(long long)) + up(x.ctas * sizeof(int32_t));
+    return paged_up(rows * 2 * sizeof(float)) + paged_up(rows * D * sizeof(float)) +
+           paged_up(static_cast<size_t>(x.ctas) * 32);
 }
 inline PagedWs paged_carve(void *ws, const PagedShape &x, int D) {
-    auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     const size_t rows = static_cast<size_t>(x.ctas) * 2 * x.tiles * x.rows;
     char *p = static_cast<char *>(ws);
     PagedWs w;
     w.ml = reinterpret_cast<float *>(p);
-    p += up(rows * 2 * sizeof(float));
+    p += paged_up(rows * 2 * sizeof(float));
     w.acc = reinterpret_cast<float *>(p);
-    p += up(rows * D * sizeof(float));
+    p += paged_up(rows * D * sizeof(float));
+    w.done = reinterpret_cast<int32_t *>(p);  // 32 bytes a CTA, one use or the other
     w.open = reinterpret_cast<int4 *>(p);
-    p += up(x.ctas * sizeof(int4));
-    w.first = reinterpret_cast<long long *>(p);
-    p += up(x.ctas * sizeof(long long));
-    w.left = reinterpret_cast<int32_t *>(p);
+    w.first = reinterpret_cast<long long *>(p + static_cast<size_t>(x.ctas) * 16);
+    w.left = reinterpret_cast<int32_t *>(p + static_cast<size_t>(x.ctas) * 24);
     return w;
 }
 
 // Few rows (swa_paged_split.cu).  It stores the new rows itself where every sequence has one
 // new token (q_start null).
 PagedShape paged_split_shape(const PagedArgs &a);
+// Its shared units are joined by launch_paged_merge.
 // after_append: launched as a programmatic dependent of the append kernel just before it on the
 // stream (everything up to the first copy of a page overlaps that kernel).
 cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s);
 void paged_split_read_clear_error(unsigned int *data, unsigned int *wait);
-// Many rows (swa_paged_tile.cu).
+cudaError_t launch_paged_merge(const PagedArgs &a, const PagedWs &w, const PagedShape &x, cudaStream_t s);
+// Many rows (swa_paged_tile.cu); w.done is zero at its start.
 PagedShape paged_tile_shape(const PagedArgs &a);
 cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s);
 void paged_tile_read_clear_error(unsigned int *data, unsigned int *wait);
@@ -104,7 +106,8 @@ cudaError_t launch_dependent(bool dependent, void (*kernel)(P...), dim3 grid, in
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 size_t paged_workspace_bytes(const PagedArgs &a);
-cudaError_t launch_paged_append(const PagedArgs &a, cudaStream_t s);
+// zero, n_zero: words that the kernel sets to 0 beside its own work (n_zero may be 0).
+cudaError_t launch_paged_append(const PagedArgs &a, int32_t *zero, int n_zero, cudaStream_t s);
 cudaError_t launch_paged_attend(const PagedArgs &a, void *ws, cudaStream_t s);
 // Errors of the data (cache word), of the few-row and of the many-row kernels.
 void paged_read_clear_error(unsigned int *data, unsigned int *split, unsigned int *prefill);

@@ -414,6 +414,82 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
     }
 }
 
+// ---------------------------------------------------------------------------------------------
+// merge of the units that several CTAs share: block (c, y) takes eight rows of the unit that CTA c
+// began and left open, a warp per row.  The pieces lie in the slots 2c + 1, 2(c+1), 2(c+2), ...
+// A row's weight of a piece is 2^(m_piece - m), o = sum of weighted values / sum of weighted sums.
+// Bound by the latency of three dependent loads; launched as a programmatic dependent of the
+// kernel that wrote the pieces.
+// ---------------------------------------------------------------------------------------------
+constexpr int kMergeThreads = 256, kMergeRows = kMergeThreads / 32;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedArgs a, const PagedWs w, const int ctas,
+                                                                    const int TT) {
+    constexpr int E = D / 32;  // columns of a lane
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = static_cast<int>(blockIdx.x), row = blockIdx.y * kMergeRows + warp;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 rec = w.open[c];
+    const long long start = w.first[c];
+    const int own = w.left[c];
+    long long later = c + 1 + lane < ctas ? w.first[c + 1 + lane] : LLONG_MAX;
+    if (rec.x == 0 || row >= TT * a.G) return;
+    // the unit's tiles end at `end` of the list: CTAs c + 1 .. c + np - 1 start before that
+    const long long end = start + own + rec.x;
+    int np = 1;
+    for (int k0 = c + 1; k0 < ctas; k0 += 32) {
+        if (k0 > c + 1) later = k0 + lane < ctas ? w.first[k0 + lane] : LLONG_MAX;
+        const int n = __popc(__ballot_sync(0xffffffffu, later < end));
+        np += n;
+        if (n < 32) break;
+    }
+    const Seq s = load_seq(a, rec.y);
+    const int i = rec.w * TT + row / a.G;  // token of the sequence
+    if (i >= s.n) return;
+    auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)); };
+    auto piece = [&](int k) { return *reinterpret_cast<const float2 *>(w.ml + (slot(k) * ROWS + row) * 2); };
+    float m = -INFINITY;
+    for (int k = lane; k < np; k += 32) m = fmaxf(m, piece(k).x);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float acc[E], L = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int k0 = 0; k0 < np; k0 += 32) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (k0 + lane < np) ml = piece(k0 + lane);
+        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+        L += f * ml.y;
+        const int n = min(32, np - k0);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            const float *v = w.acc + partial_at<D>(slot(k0 + k), ROWS, row, lane * E);
+            // (a piece that kept nothing of this row has weight 0 and finite values)
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 t = *reinterpret_cast<const float2 *>(v + e);
+                acc[e] += fk * t.x;
+                acc[e + 1] += fk * t.y;
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const int64_t tok = s.q0 + i;
+    const int h = rec.z * a.G + row % a.G;
+    if (!SWA_IN_BOUNDS(tok < a.N && h < a.H_q, &g_psplit_err)) return;
+    const float inv = 1.f / L;  // every row keeps its own key
+    uint16_t *op = a.o + tok * a.o_st[0] + h * a.o_st[1] + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(op + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0) {
+        a.lse[tok * a.H_q + h] = (m + log2f(L)) * 0.69314718055994531f;
+        if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, s.p0 + i);
+    }
+}
+
 template <int D>
 cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s) {
     using C = SplitCfg<D>;
@@ -451,6 +527,16 @@ cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, bool after_
         case 64: return launch_d<64>(a, w, after_append, s);
         case 128: return launch_d<128>(a, w, after_append, s);
         case 256: return launch_d<256>(a, w, after_append, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_paged_merge(const PagedArgs &a, const PagedWs &w, const PagedShape &x, cudaStream_t s) {
+    const dim3 grid(x.ctas, (x.TQ * a.G + kMergeRows - 1) / kMergeRows);
+    switch (a.D) {
+        case 64: return launch_dependent(true, paged_merge_kernel<64>, grid, kMergeThreads, 0, s, a, w, x.ctas, x.TQ);
+        case 128: return launch_dependent(true, paged_merge_kernel<128>, grid, kMergeThreads, 0, s, a, w, x.ctas, x.TQ);
+        case 256: return launch_dependent(true, paged_merge_kernel<256>, grid, kMergeThreads, 0, s, a, w, x.ctas, x.TQ);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -31,6 +31,8 @@
 //   its own S, O, maximum and sum, which meet in the epilogue.  With one warpgroup alone S(j + 1)
 //   could not start before P(j) was used up.
 // NQT = 1 (head dim 256): one query tile, S double-buffered, TMEM S0 | S1 | Q | O.
+// A unit that several CTAs share: each writes its piece's unnormalised result, and the last to do so
+// joins them, while the others work on.  (A kernel of its own for that cost 8 to 19 us.)
 // Rows of V past the sequence's end may hold anything (even NaN): the warpgroup that turns the
 // last tile's scores into P zeroes them in shared memory before it hands P over.
 // Bound by the tensor cores and the exponentials for full units over long histories, by HBM for
@@ -53,11 +55,11 @@ constexpr int BM = 128;              // query rows per tile (TMEM lanes)
 constexpr float kRescaleTau = 8.0f;  // log2 units: rescale O when the max grows by > 2^8
 
 // A piece as the planner hands it to the other roles: tiles j0 .. j1 - 1 of unit (b, kvh, ut),
-// which has nt; q0, n, p0 of its sequence.  j0 == j1: there are no more.
+// which has nt; q0, n, p0 of its sequence.  j0 == j1: there are no more.  slot: where its partial
+// result goes; the unit's others lie in 2 * owner + 1, 2 * owner + 2, 2 * owner + 4, ...: `pieces`.
 struct TilePiece {
-    int b, kvh, ut, q0, n, p0, sink, lo, nt, j0, j1;
+    int b, kvh, ut, q0, n, p0, sink, lo, nt, j0, j1, slot, owner, pieces;
     __device__ __forceinline__ int tile(int i) const volatile { return j0 + i < sink ? j0 + i : lo + (j0 + i - sink); }
-    __device__ __forceinline__ bool begun() const volatile { return j0 > 0; }
     __device__ __forceinline__ bool open() const volatile { return j1 < nt; }
 };
 
@@ -91,10 +93,10 @@ struct TileCfg {
     static constexpr int NBAR = 2 * NSLOT + 14 + 2 * NP;
     static constexpr int OFF_TMEMPTR = OFF_BAR + NBAR * 8;  // TMEM address, abort flag
     static constexpr int OFF_SHARE = OFF_TMEMPTR + 16;
-    static constexpr int OFF_PIECE = OFF_SHARE + 48;
+    static constexpr int OFF_PIECE = OFF_SHARE + 64;
     // (all of it: the kernel has no static shared memory)
     static constexpr int SMEM = OFF_PIECE + NP * static_cast<int>(sizeof(TilePiece));
-    static_assert(sizeof(Share) <= 48, "share");
+    static_assert(sizeof(Share) <= 64, "share");
     static constexpr uint32_t TMEM_COLS = 512;
     __host__ __device__ static constexpr uint32_t tm_s(int slot) { return static_cast<uint32_t>(slot * BN); }
     __host__ __device__ static constexpr uint32_t tm_o(int tile) { return 256u + static_cast<uint32_t>(tile * 128); }
@@ -121,6 +123,20 @@ struct TileArgs {
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
     const bool ok = mbar_wait(bar, parity, abort, &g_ptile_err);
     return __all_sync(0xffffffffu, ok);
+}
+
+// 16 columns of a row of o (align32: 32-byte aligned).  32-byte stores: each lane of a
+// store writes one whole sector of its row.
+__device__ __forceinline__ void store_row16(uint16_t *dst, const float *f, bool align32) {
+    uint32_t wv[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wv[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+    if (align32) {
+        st_global_v8(dst, wv);
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(wv[4], wv[5], wv[6], wv[7]);
+    }
 }
 
 template <int D>
@@ -201,8 +217,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     find_share<BN, C::THREADS, true>(a, TT, ta.min_tiles, sgen + C::OFF_RING, share, &g_ptile_data);
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    // the merge grid may be scheduled from here on: its blocks wait for this grid to complete
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int cta_tiles = share->tiles;
     volatile TilePiece *pieces = reinterpret_cast<volatile TilePiece *>(sgen + C::OFF_PIECE);
     // This warp's k-th piece (nullptr: there are no more, or a wait ran out: then ok is false); the
@@ -719,7 +733,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 wb = mb.x == -INFINITY ? 0.f : ex2(mb.x - m);
                 l = ma.y * wa + mb.y * wb;
             }
-            const bool whole = !wk->begun() && !wk->open();
+            const int unit_pieces = wk->pieces;
+            const bool whole = unit_pieces == 0;
             const float inv_l = whole ? 1.f / l : 1.f;  // (of a whole unit: every row keeps its own key)
             wa *= inv_l;
             wb *= inv_l;
@@ -728,12 +743,17 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             const int h = wk->kvh * a.G + r % a.G;
             const bool store = tq < min(wk->n - i0, ta.TQ) && SWA_IN_BOUNDS(tok < a.N && h < a.H_q, &g_ptile_err);
             uint16_t *orow = a.o + tok * a.o_st[0] + h * a.o_st[1];
-            const int pslot = 2 * static_cast<int>(blockIdx.x) + (wk->begun() ? 0 : 1);
-            const int prow = (single ? 0 : wg * BM) + r;
+            const int pslot = wk->slot, prow = (single ? 0 : wg * BM) + r;
+            // (a shared query tile: each warpgroup keeps the maximum and sum beside its half of the columns)
+            const int mrow = wg * BM + r;
+            auto ml_at = [&](int slot) {
+                return reinterpret_cast<float2 *>(ta.ws.ml + (static_cast<int64_t>(slot) * (NQT * BM) + mrow) * 2);
+            };
             // a shared tile's columns are read out half by each warpgroup
             const int c0 = single ? wg * (D / 64) : 0, c1 = single ? c0 + D / 64 : D / 32;
 #pragma unroll 1
             for (int c = c0; c < c1; ++c) {
+                __syncwarp();  // tcgen05.ld is executed by the converged warp: lanes that store come back here
                 uint32_t ov[32];
                 tmem_ld32(tmem + lane_addr + C::tm_o(single ? 0 : wg) + c * 32, ov);
                 tc_wait_ld();
@@ -746,8 +766,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) f[e] += __uint_as_float(ov[e]) * wb;
                 }
-                if (!store) continue;
-                if (!whole) {
+                if (store && !whole) {
 #pragma unroll
                     for (int q8 = 0; q8 < 4; ++q8) {
                         uint32_t wv[8];
@@ -755,37 +774,91 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                         for (int e = 0; e < 8; ++e) wv[e] = __float_as_uint(f[q8 * 8 + e]);
                         st_global_v8(ta.ws.acc + partial_at<D>(pslot, NQT * BM, prow, c * 32 + q8 * 8), wv);
                     }
-                } else if (ta.o_align32) {
-                    // 32-byte stores: each lane of a store writes one whole sector of its row
-#pragma unroll
-                    for (int q8 = 0; q8 < 2; ++q8) {
-                        uint32_t wv[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) wv[e] = pack_bf16x2(f[q8 * 16 + 2 * e], f[q8 * 16 + 2 * e + 1]);
-                        st_global_v8(orow + c * 32 + q8 * 16, wv);
-                    }
-                } else {
-#pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        uint32_t wv[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) wv[e] = pack_bf16x2(f[q4 * 8 + 2 * e], f[q4 * 8 + 2 * e + 1]);
-                        *reinterpret_cast<uint4 *>(orow + c * 32 + q4 * 8) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
-                    }
+                } else if (store) {
+                    store_row16(orow + c * 32, f, ta.o_align32);
+                    store_row16(orow + c * 32 + 16, f + 16, ta.o_align32);
                 }
             }
             // O has been read out: the next piece's first P V may overwrite it
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_of(wg));
-            if (store && (!single || wg == 0)) {
-                if (whole) {
-                    a.lse[tok * a.H_q + h] = (m + log2f(l)) * 0.69314718055994531f;
-                    if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, t);
-                } else {
-                    *reinterpret_cast<float2 *>(ta.ws.ml + (static_cast<int64_t>(pslot) * (NQT * BM) + prow) * 2) =
-                        make_float2(m, l);
+            bool joined = false;
+            if (!whole) {
+                // The piece is written.  Warps of the same place have the same rows and columns of it in
+                // every CTA that shares the unit, so the last of them to arrive joins those: a row's
+                // weight of a piece is 2^(m_piece - m), o = sum of weighted values / sum of weighted sums.
+                if (store) *ml_at(pslot) = make_float2(m, l);
+                __threadfence();
+                __syncwarp();
+                const int owner = wk->owner;
+                int before = 0;
+                if (lane == 0) before = atomicAdd(ta.ws.done + owner * 8 + wg * 4 + quarter, 1);
+                before = __shfl_sync(0xffffffffu, before, 0);
+                joined = before == unit_pieces - 1;
+                if (joined) {
+                    __threadfence();
+                    auto slot_of = [&](int e) { return e == 0 ? 2 * owner + 1 : 2 * (owner + e); };
+                    // four pieces' loads in flight at a time
+                    auto four = [&](int e0, float2 (&v)[4]) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = store && e0 + e < unit_pieces ? __ldcg(ml_at(slot_of(e0 + e)))
+                                                                 : make_float2(-INFINITY, 0.f);
+                    };
+                    float2 v4[4];
+                    m = -INFINITY;
+                    l = 0.f;
+                    for (int e0 = 0; e0 < unit_pieces; e0 += 4) {
+                        four(e0, v4);
+                        const float mn = fmaxf(fmaxf(m, fmaxf(v4[0].x, v4[1].x)), fmaxf(v4[2].x, v4[3].x));
+                        const float ms = mn == -INFINITY ? 0.f : mn;
+                        l *= ex2(m - ms);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) l += v4[e].y * ex2(v4[e].x - ms);
+                        m = mn;
+                    }
+                    const float inv = 1.f / l;  // (a row keeps its own key: some piece's maximum is finite)
+                    if (unit_pieces > 4) four(0, v4);
+                    if (store) {
+#pragma unroll 1
+                        for (int c = 2 * c0; c < 2 * c1; ++c) {  // 16 columns at a time
+                            float f[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) f[e] = 0.f;
+#pragma unroll 1
+                            for (int e0 = 0; e0 < unit_pieces; e0 += 4) {
+                                if (unit_pieces > 4) four(e0, v4);
+                                float4 v[4][4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                                    for (int x = 0; x < 4; ++x)
+                                        v[e][x] = e0 + e < unit_pieces
+                                                      ? __ldcg(reinterpret_cast<const float4 *>(
+                                                            ta.ws.acc + partial_at<D>(slot_of(e0 + e), NQT * BM, prow,
+                                                                                      c * 16 + x * 4)))
+                                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float wt = ex2(v4[e].x - m) * inv;  // (0 past the last piece)
+#pragma unroll
+                                    for (int x = 0; x < 4; ++x) {
+                                        f[4 * x] += wt * v[e][x].x;
+                                        f[4 * x + 1] += wt * v[e][x].y;
+                                        f[4 * x + 2] += wt * v[e][x].z;
+                                        f[4 * x + 3] += wt * v[e][x].w;
+                                    }
+                                }
+                            }
+                            store_row16(orow + c * 16, f, ta.o_align32);
+                        }
+                    }
                 }
+            }
+            if (store && (!single || wg == 0) && (whole || joined)) {
+                a.lse[tok * a.H_q + h] = (m + log2f(l)) * 0.69314718055994531f;
+                if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, t);
             }
             give_back(k);
             J += n;
@@ -796,7 +869,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         const Share sh = *share;
         const int grid = static_cast<int>(gridDim.x);
         bool ok = true;
-        int4 open = make_int4(0, 0, 0, 0);
         Piece p{};
         Walk<BN> walk(a, TT, sh);
         // Whole units, one a wave: the sequences are searched 32 at a time from block b0, whose first
@@ -804,9 +876,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         int w = 0, b0 = 0, u0 = 0;
         auto next_piece = [&]() -> bool {
             if (w >= sh.waves) {
-                const bool more = walk.next(p);
-                if (more && p.open() && !p.begun()) open = make_int4(p.u.n - p.j1, p.b, p.kvh, p.ut);
-                return more;
+                return walk.next(p);
             }
             const int c = static_cast<int>(blockIdx.x), u = w * grid + (w & 1 ? grid - 1 - c : c);
             ++w;
@@ -873,6 +943,9 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     t->nt = p.u.n;
                     t->j0 = p.j0;
                     t->j1 = p.j1;
+                    t->slot = 2 * sh.turn + (p.begun() ? 0 : 1);
+                    t->owner = p.begun() ? sh.owner : sh.turn;
+                    t->pieces = p.begun() ? sh.pieces : p.open() ? sh.open_pieces : 0;
                     mbar_arrive(bar_piece(e));
                 }
                 __syncwarp();
@@ -912,11 +985,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             for (int x = 0; x < NQT; ++x)
                 if (loads[x] > 0) mbar_drain(bar_qf(x), (loads[x] - 1) & 1, &g_ptile_err);
         }
-        if (lane == 0) {
-            ta.ws.open[blockIdx.x] = open;
-            ta.ws.first[blockIdx.x] = sh.first;
-            ta.ws.left[blockIdx.x] = sh.left;
-        }
     }
 
     tc_fence_before();
@@ -949,7 +1017,7 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cu
     t.a = a;
     t.ws = w;
     t.TQ = x.TQ;
-    t.min_tiles = 2;
+    t.min_tiles = 4;
     t.o_align32 = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.o_st[0] % 16 == 0 && a.o_st[1] % 16 == 0;
     t.fault_stop_fill = fault_plan().band_stop_fill;
     return launch_dependent(after_append, paged_tile_kernel<D>, dim3(x.ctas), C::THREADS, C::SMEM, s, mq, mk, mv, t);

@@ -76,7 +76,10 @@ class Batch:
     def reference(self, b):
         p, n = self.seqs[b]
         q0 = int(self.q_start[b])
-        return attend(self.q[q0:q0 + n], self.keys[b], self.vals[b], p, self.window, self.n_sink)
+        args = self.q[q0:q0 + n], self.keys[b], self.vals[b]
+        if n * (p + n) * self.Hq > 1 << 25:  # the larger ones on the GPU, in 64 bits too
+            return tuple(x.cpu() for x in attend(*(x.cuda() for x in args), p, self.window, self.n_sink))
+        return attend(*args, p, self.window, self.n_sink)
 
 
 def attend(q, k, v, p0, window, n_sink, scale=None):
@@ -87,7 +90,8 @@ def attend(q, k, v, p0, window, n_sink, scale=None):
     G = Hq // k.shape[1]
     scale = D ** -0.5 if scale is None else scale
     q, k, v = q.double(), k.double().repeat_interleave(G, 1), v.double().repeat_interleave(G, 1)
-    t, s = torch.arange(p0, p0 + n)[:, None], torch.arange(k.shape[0])[None, :]
+    t, s = (torch.arange(a, b, device=q.device) for a, b in ((p0, p0 + n), (0, k.shape[0])))
+    t = t[:, None]
     keep = s <= t
     if window:
         keep &= (s > t - window) | (s < n_sink)

@@ -103,6 +103,28 @@ def test_long_histories_and_many_sequences(swa, seqs):
         run(swa, R.Batch(6, seqs, 4, 1, D, ps), max_q=max(n for _, n in seqs))
 
 
+@pytest.mark.parametrize("heads", [(16, 1, 128), (16, 1, 64), (16, 1, 256)], ids=str)
+def test_more_units_than_two_waves(swa, heads):
+    # whole units dealt to the CTAs first: one long chunk, a batch of many, one whose first units are
+    # far longer than the others (some CTAs are above the mean before the rest is shared out)
+    Hq, Hkv, D = heads
+    tokens = 16 if D < 256 else 8  # of a unit
+    u = 304
+    for seqs, w in (([(0, u * tokens + 5)], 300), ([(37 * i, 9 * tokens + i) for i in range(40)], 0),
+                    ([(30000, 20 * tokens)] + [(0, 3)] * 330, 0), ([(5, 1)] * 200 + [(3, 2 * tokens + 1)] * 70, 0)):
+        x = R.Batch(13, seqs, Hq, Hkv, D, 64, w, 3 if w else 0)
+        run(swa, x, want_counts=False)
+
+
+@pytest.mark.parametrize("heads", [(12, 4, 128), (5, 5, 64), (6, 2, 256)], ids=str)
+def test_shared_units_with_rows_missing(swa, heads):
+    # units spread over many CTAs whose last query tile is not full, in one and two query tiles
+    Hq, Hkv, D = heads
+    for n in (3, 40, 45, 70, 131):
+        for p0 in (2000, 9000):
+            run(swa, R.Batch(14, [(p0, n), (100, 1)], Hq, Hkv, D, 32), append=n == 45)
+
+
 def test_values_of_the_extremes(swa):
     # scores of +-1000s: one key carries all the weight, and the running maximum jumps
     x = R.Batch(7, [(500, 70), (900, 1)], 8, 2, 128, 32)

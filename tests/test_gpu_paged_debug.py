@@ -1,0 +1,65 @@
+"""The paged cache's operators through the debug build of the library (libswa_debug.so), whose kernels
+check every index they compute -- page boxes, query tiles, rows of o, lse and counts -- against
+the tensor it addresses before the access.  The results must match the references as before, and
+no check may fire."""
+import pytest
+
+import test_gpu_pages as PAGES
+import test_gpu_paged as PAGED
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def swa():
+    import sliding_window_attention_swa_gb300 as m
+
+    prev = m.use_library(m.load_library(m.build(debug=True)))
+    try:
+        yield m
+    finally:
+        m.use_library(prev)
+
+
+@pytest.fixture(autouse=True)
+def clean(swa):
+    yield
+    assert swa.load_library()._name.endswith("libswa_debug.so")
+    st, words = swa.swa_read_device_errors()
+    assert st == 0 and words == {"prefill": 0, "split": 0, "cache": 0}, words
+
+
+@pytest.mark.parametrize("append", [False, True], ids=["stored", "append"])
+@pytest.mark.parametrize("case", PAGED.DECODE, ids=str)
+def test_one_token_a_sequence(swa, case, append):
+    PAGED.test_one_token_a_sequence(swa, case, append)
+
+
+@pytest.mark.parametrize("case", PAGED.CHUNK, ids=str)
+def test_ragged_batch(swa, case):
+    PAGED.test_ragged_batch(swa, case, True)
+
+
+@pytest.mark.parametrize("heads", [(16, 1, 128), (16, 1, 256)], ids=str)
+def test_more_units_than_two_waves(swa, heads):
+    PAGED.test_more_units_than_two_waves(swa, heads)
+
+
+@pytest.mark.parametrize("heads", [(12, 4, 128), (5, 5, 64), (6, 2, 256)], ids=str)
+def test_shared_units_with_rows_missing(swa, heads):
+    PAGED.test_shared_units_with_rows_missing(swa, heads)
+
+
+def test_layouts_and_sizes(swa):
+    PAGED.test_strided_rows(swa)
+    PAGED.test_append_alone(swa)
+    for hint in (0, 1):
+        PAGED.test_broken_device_data(swa, hint)
+
+
+def test_pages(swa):
+    PAGES.test_reserve_when_the_pool_runs_out(swa)
+    PAGES.test_free(swa, 40, 90, 4000, 32, 0, True)
+    PAGES.test_fork(swa, 6, 200, (3, 2, 32, 128))
+    PAGES.test_compact(swa, 30, 9, 400, (1, 2, 32, 64), False)
+    PAGES.test_serving_run(swa)

@@ -72,6 +72,8 @@ def test_every_tile_once(seed):
     assert len(seen) == total
     for c, (pieces, u) in opened.items():
         assert slots[u] == [2 * c + 1] + [2 * (c + k) for k in range(1, pieces)]
+        # what the tile kernel's pieces carry: the owner and the number of pieces, from the unit's tiles
+        assert starts[u] // R == c and (starts[u + 1] - 1) // R - c + 1 == pieces
     assert sorted(u for _, u in opened.values()) == sorted(slots)
 
 
@@ -138,14 +140,16 @@ def test_waves_and_tail(seed):
     assert sum(left) == tail
     # no CTA has more than the level, unless its waves alone have
     assert all(x + q <= max(lo, x) for x, q in zip(loads, left))
-    seen, slots, opened = set(), {}, {}
+    seen, slots, opened, carried = set(), {}, {}, {}
+
+    def turn_of(X):
+        return sum(n > 0 and f + n <= X for f, n in zip(first, left))
+
     for c in range(grid):
         if not left[c]:
             continue
         u = next(i for i in range(len(us)) if starts[i + 1] > first[c])
         assert u >= bulk
-        last = next(i for i in range(len(us)) if starts[i + 1] > first[c] + left[c] - 1)
-        span = 1 + sum(x > c and min(first[x], total) < starts[last + 1] for x in range(grid))
         for u, j0, j1 in walk(us, (u, first[c] - starts[u], left[c])):
             for j in range(j0, j1):
                 assert (u, j) not in seen
@@ -154,8 +158,13 @@ def test_waves_and_tail(seed):
                 slots[u].append(c)
             elif j1 < us[u][3]:
                 slots[u] = [c]
-                opened[c] = (span, u)
+                opened[c] = u
+            # what the piece carries: turns count the CTAs with a stretch
+            if j0 > 0 or j1 < us[u][3]:
+                owner, end = turn_of(starts[u]), turn_of(starts[u + 1] - 1)
+                carried.setdefault(u, set()).add((owner, end - owner + 1))
     assert len(seen) == tail
-    for c, (span, u) in opened.items():
-        # the CTAs that the merge looks at, but for those without tiles, have exactly the unit's pieces
-        assert slots[u] == [x for x in range(c, c + span) if left[x]]
+    for c, u in opened.items():
+        (owner, pieces), = carried[u]
+        turns = [sum(left[x] > 0 for x in range(y)) for y in slots[u]]
+        assert turns == list(range(owner, owner + pieces))
