@@ -70,14 +70,15 @@ __device__ __forceinline__ int kept_keys(const PagedArgs &a, int t) {
 // that its tokens can reach -- those of the sinks, then those of the window -- as one list of
 // n tiles.  Lengths are only known on the device, so the work is shared out there.  All units,
 // in the order (sequence, kv head, block), and their tiles form one list.
-//   Waves (tile kernel, from two units a CTA): whole units are dealt one a CTA in waves of
-//   alternating direction, so that the CTAs work on neighbouring units, which read the same
-//   keys, at the same time: with a stretch of the list for each CTA instead, their working sets
-//   together (1.1 MB each for the Gemma-shape window) exceed L2 and every tile comes from HBM.
+//   Waves (tile kernel): whole units are dealt one a CTA in waves of alternating direction, so that
+//   the CTAs work on neighbouring units, which read the same keys, at the same time: with a
+//   stretch of the list for each CTA instead, their working sets together (1.1 MB each for the
+//   Gemma-shape window) exceed L2 and every tile comes from HBM.
 //   Tail: the tiles of the last units (between one and two waves of them, or all units of a
 //   smaller batch) are cut into one stretch a CTA, of such lengths that all CTAs end up with the
-//   same number of tiles, whatever the batch looks like.  A unit that crosses a border is
-//   finished by a merge of its pieces.
+//   same number of tiles, whatever the batch looks like.  The pieces of a unit that crosses a
+//   border are joined at the end, which takes as long as about kJoinTiles tiles (10 us); where
+//   dealing every unit whole leaves no CTA further above the mean than that, there is no tail.
 // ---------------------------------------------------------------------------------------------
 struct UnitTiles {
     int sink, lo, n;  // tiles 0 .. sink - 1, then lo, lo + 1, ...: n in all
@@ -219,8 +220,9 @@ __device__ __forceinline__ Place find_tile(const PagedArgs &a, int TT, const lon
 }
 
 constexpr int kMaxWaveCtas = 256;
-// Scratch of find_share: tiles [B] (64 bits), first units [B + 1], loads [CTAs].
-constexpr int kShareScratch = kPagedMaxB * 12 + 4 + kMaxWaveCtas * 4;
+constexpr int kJoinTiles = 12;
+// Scratch of find_share: tiles [B] (64 bits), first units [B + 1], loads [2][CTAs].
+constexpr int kShareScratch = kPagedMaxB * 12 + 4 + 2 * kMaxWaveCtas * 4;
 
 // The CTA that unit u of the list goes to, in wave u / grid.
 __device__ __forceinline__ int dealt_to(int u, int grid) {
@@ -248,7 +250,7 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
             }
             const int nu = (s.n + TT - 1) / TT;
             const bool few = __all_sync(0xffffffffu, nu <= kFew && s.p0 + s.n < (1 << 24)) && a.H_kv <= 64 &&
-                             (!kWaves || __reduce_add_sync(0xffffffffu, nu <= kFew ? nu : 0) * a.H_kv < 2 * grid);
+                             (!kWaves || __reduce_add_sync(0xffffffffu, nu <= kFew ? nu : 0) * a.H_kv <= grid);
             if (few) {  // (32 sequences of 4 units of < 2^19 tiles of 64 heads: 32 bits hold every sum but one)
                 int n[kFew], sum = 0;
 #pragma unroll
@@ -281,7 +283,28 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
                         }
                     return p;
                 };
-                if (left == 0) {
+                int longest = 0;
+#pragma unroll
+                for (int ut = 0; ut < kFew; ++ut) longest = max(longest, n[ut]);
+                longest = __reduce_max_sync(0xffffffffu, longest);
+                if (kWaves && longest <= len + kJoinTiles) {  // unit c whole
+                    int units = nu * a.H_kv;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int t = __shfl_up_sync(0xffffffffu, units, o);
+                        if (lane >= o) units += t;
+                    }
+                    const unsigned past = __ballot_sync(0xffffffffu, units > c);
+                    if (past == 0) {
+                        if (lane == 0) *out = Share{total, 0, 0, 0, 0, 0, 1, 0, 0, 0, 0, 0};
+                    } else if (lane == __ffs(past) - 1) {
+                        const int ut = (c - (units - nu * a.H_kv)) % nu;
+                        int mine = n[0];
+#pragma unroll
+                        for (int i = 1; i < kFew; ++i) mine = ut == i ? n[i] : mine;
+                        *out = Share{total, 0, 0, 0, 0, 0, 1, mine, 0, 0, 0, 0};
+                    }
+                } else if (left == 0) {
                     if (lane == 0) *out = Share{first, 0, 0, 0, 0, 0, 0, 0, c, 0, 0, 0};
                 } else {
                     const int l0 = __ffs(__ballot_sync(0xffffffffu, inc > first)) - 1;
@@ -311,7 +334,8 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
         if (__syncthreads_or(found)) return;
     }
     long long *tiles = reinterpret_cast<long long *>(scratch);
-    int *units = reinterpret_cast<int *>(scratch + a.B * 8), *loads = units + a.B + 1;
+    int *units = reinterpret_cast<int *>(scratch + a.B * 8);
+    int *all_loads = units + a.B + 1, *bulk_loads = all_loads + kMaxWaveCtas;
     // 1. units of one kv head of each sequence, 2. their running sum
     for (int b = tid; b < a.B; b += kThreads) {
         const Seq s = load_seq(a, b);
@@ -320,7 +344,7 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
         tiles[b] = 0;
     }
     if (kWaves && grid <= kMaxWaveCtas)
-        for (int c = tid; c < grid; c += kThreads) loads[c] = 0;
+        for (int c = tid; c < grid; c += kThreads) all_loads[c] = bulk_loads[c] = 0;
     __syncthreads();
     if (warp == 0) {
         int before = 0;
@@ -338,12 +362,12 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
         if (lane == 0) units[a.B] = before;
     }
     __syncthreads();
-    // 3. tiles of every sequence, and those that the waves give each CTA: a thread per unit
+    // 3. tiles of every sequence, and those that each CTA gets if all units are dealt whole, or if
+    // all but the last are: a thread per unit
     const int n_units = units[a.B];  // of one kv head
     const long long all_units = static_cast<long long>(n_units) * a.H_kv;
-    const int waves = kWaves && grid <= kMaxWaveCtas && all_units < (1 << 26)
-                          ? max(0, static_cast<int>(all_units) / grid - 1)
-                          : 0;
+    const bool deal = kWaves && grid <= kMaxWaveCtas && all_units < (1 << 26);
+    const int bulk_waves = deal ? max(0, static_cast<int>(all_units) / grid - 1) : 0;
     for (int x0 = warp * 32; x0 < n_units; x0 += kThreads) {
         const int x = x0 + lane;
         int b = 0, len = a.B;  // the last sequence whose first unit is <= x
@@ -362,10 +386,13 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
             const Seq s = load_seq(a, b);
             const int ut = x - units[b];
             n = unit_tiles<BN>(a, s, ut, TT).n;
-            if (waves > 0) {
+            if (deal) {
                 const int nu = (s.n + TT - 1) / TT;
-                for (int h = 0, u = units[b] * a.H_kv + ut; h < a.H_kv && u < waves * grid; ++h, u += nu)
-                    atomicAdd(loads + dealt_to(u, grid), n);
+                for (int h = 0, u = units[b] * a.H_kv + ut; h < a.H_kv; ++h, u += nu) {
+                    const int c = dealt_to(u, grid);
+                    atomicAdd(all_loads + c, n);
+                    if (u < bulk_waves * grid) atomicAdd(bulk_loads + c, n);
+                }
             }
         }
         // (lanes of one sequence add up first)
@@ -390,8 +417,23 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
         const int c = static_cast<int>(blockIdx.x);
         constexpr int kPer = kMaxWaveCtas / 32;
         long long first, len, begin[kPer];  // begin, q: the stretch of CTA 32 * i + lane (waves > 0)
-        int q[kPer], mine = 0, turn = c;
-        if (waves == 0) {
+        int q[kPer], mine = 0, turn = c, waves = bulk_waves;
+        if (deal) {  // all units whole?
+            int top = 0;
+            for (int i = lane; i < grid; i += 32) top = max(top, all_loads[i]);
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (top <= max((total + grid - 1) / grid, static_cast<long long>(min_tiles)) + kJoinTiles) {
+                if (warp == 0 && lane == 0)
+                    *out = Share{total, 0, 0, 0, 0, 0, static_cast<int>((all_units + grid - 1) / grid), all_loads[c],
+                                 0, 0, 0, 0};
+                waves = -1;
+            }
+        }
+        const int *loads = bulk_loads;
+        if (waves < 0) {
+            first = total;
+            len = 0;
+        } else if (waves == 0) {
             len = max((total + grid - 1) / grid, static_cast<long long>(min_tiles));
             first = len * c;
         } else {
@@ -458,7 +500,7 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
             for (int i = 0; i < kPer; ++i) n += __popc(__ballot_sync(0xffffffffu, q[i] > 0 && begin[i] + q[i] <= X));
             return n;
         };
-        if (warp == 0) {
+        if (warp == 0 && waves >= 0) {
             Share sh{first, 0, 0, 0, 0, left, waves, mine + left, turn, 0, 0, 0};
             if (left > 0) {
                 const Place p = find_tile<BN>(a, TT, tiles, first, lane);
@@ -484,7 +526,7 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
                 out->owner = sh.owner;
                 out->pieces = sh.pieces;
             }
-        } else if (kWaves && left > 0) {
+        } else if (kWaves && warp == 1 && left > 0) {
             const long long X = first + left - 1;
             const Place p = find_tile<BN>(a, TT, tiles, X, lane);
             const int n = turn_of(X - p.j + p.n - 1) - turn + 1;

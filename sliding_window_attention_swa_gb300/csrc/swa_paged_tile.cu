@@ -1,7 +1,7 @@
 // swa_paged_tile.cu -- attention of many new tokens over a paged cache on 5th-generation tensor
 // cores (sm_103a).
 //
-// Work unit: one (sequence, kv head, block of NQT query tiles).  A query tile is 128 rows = TQ
+// Work unit: one (sequence, kv head, block of one or two query tiles).  A query tile is 128 rows = TQ
 // consecutive new tokens x the G query heads of the group (row = token * G + head), so every
 // key/value tile is loaded once for the whole group.  A unit reads the tiles of BN keys that its
 // tokens reach; the batch's tiles are shared out evenly over one persistent CTA per SM
@@ -24,12 +24,11 @@
 //                 row sum takes it unrounded; O is rescaled in TMEM only when a row's max grows by
 //                 more than 2^8 (numerator and denominator share the stale max, so the result is
 //                 the same either way).
-// NQT = 2 (head dim <= 128), a full unit: two query tiles ping-pong -- while one warpgroup turns
-//   S_A into P_A the tensor cores run S_B and P_B V -- with TMEM S_A | S_B | O_A | O_B.
-// NQT = 2, a unit whose tokens fill one query tile at most (the single tokens of a mixed batch, the
-//   end of a chunk): the warpgroups share that tile and take its key tiles in turn, each with
-//   its own S, O, maximum and sum, which meet in the epilogue.  With one warpgroup alone S(j + 1)
-//   could not start before P(j) was used up.
+// Head dim 128, a unit of two query tiles: they ping-pong -- while one warpgroup turns S_A into P_A
+//   the tensor cores run S_B and P_B V -- with TMEM S_A | S_B | O_A | O_B.
+// Head dim <= 128, a unit of one query tile: the warpgroups share it and take its key tiles in turn,
+//   each with its own S, O, maximum and sum, which meet in the epilogue.  With one warpgroup
+//   alone S(j + 1) could not start before P(j) was used up.
 // NQT = 1 (head dim 256): one query tile, S double-buffered, TMEM S0 | S1 | Q | O.
 // A unit that several CTAs share: each writes its piece's unnormalised result, and the last to do so
 // joins them, while the others work on.  (A kernel of its own for that cost 8 to 19 us.)
@@ -65,7 +64,8 @@ struct TilePiece {
 
 template <int D>
 struct TileCfg {
-    static constexpr int NQT = D <= 128 ? 2 : 1;    // query tiles per unit
+    static constexpr int NQT = D <= 128 ? 2 : 1;    // softmax warpgroups
+    static constexpr bool kPairs = D == 128;        // units of two query tiles, too
     static constexpr int BN = D == 256 ? 64 : 128;  // keys per K/V tile
     // NQT = 2: twelve warps put three on each SM sub-partition, whose 16K-register file caps the
     // launch at 168 registers a thread; setmaxnreg then moves registers from warpgroup 0 (104) to
@@ -113,6 +113,7 @@ struct TileArgs {
     PagedArgs a;
     PagedWs ws;
     int TQ;             // tokens per query tile
+    int TT;             // tokens per unit: TQ or (head dim 128) 2 * TQ
     int min_tiles;      // least share of a CTA
     int o_align32;      // o and its strides are 32-byte aligned: rows stored 32 bytes at a time
     int fault_stop_fill;  // planted fault: no ring fill numbered at or past this (INT_MAX: off)
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    const int TT = NQT * ta.TQ;
+    const int TT = ta.TT;
     tc_fence_before();
     // (its block barriers also publish the mbarriers and the TMEM address)
     find_share<BN, C::THREADS, true>(a, TT, ta.min_tiles, sgen + C::OFF_RING, share, &g_ptile_data);
@@ -233,8 +234,10 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_used(k % C::NP));
     };
-    // a unit whose tokens fill one of its two query tiles at most (tokens: of its sequence)
-    auto is_single = [&](int tokens, int ut) { return NQT == 2 && tokens - ut * TT <= ta.TQ; };
+    // a unit of one query tile, which both warpgroups share (tokens: of its sequence)
+    auto is_single = [&](int tokens, int ut) {
+        return NQT == 2 && (!C::kPairs || TT == ta.TQ || tokens - ut * TT <= ta.TQ);
+    };
 
     if (warp == 0 || warp == 2) {
         // ============================ K/V producers ============================
@@ -428,7 +431,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 ok = warp_wait(bar_qf(0), k & 1, abort) && landed(2 * J);
                 if (!ok) break;
                 mma_s(0, 0, (2 * J) % NSLOT);
-                if (!single) {
+                if (C::kPairs && !single) {
                     ok = warp_wait(bar_qf(1), k & 1, abort);
                     if (!ok) break;
                     mma_s(1, NQT - 1, (2 * J) % NSLOT);
@@ -963,7 +966,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     if (!ok) break;
                     if (lane == 0) {
                         const int i = i0 + x * ta.TQ;  // the tile's first token
-                        if (i < tokens) {
+                        if (i < tokens && (x == 0 || !is_single(tokens, i0 / TT))) {
                             // debug build: the tile's tokens and its group's heads exist
                             (void)SWA_IN_BOUNDS(q0 + i < a.N && (kvh + 1) * a.G <= a.H_q, &g_ptile_err);
                             mbar_arrive_expect_tx(bar_qf(x), static_cast<uint32_t>(a.G * ta.TQ * D * 2));
@@ -993,6 +996,17 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
 }
 
+// Query tiles of a unit.  At head dim 128 pairs take 6% less time where there are enough of them
+// (chunks of 2048 tokens behind 30000: 989 against 1047 us), and single tiles, twice as many
+// units, where there are not (two chunks of 100 tokens 25 against 33 us, a mixed step 78
+// against 91): pairs from two units a CTA, by what the host knows of the batch.  At head dim 64
+// the exponentials bound both alike (856 and 857 us).
+int tiles_of_unit(const PagedArgs &a) {
+    if (a.D != 128) return 1;
+    const int64_t pairs = static_cast<int64_t>(a.N) / (2 * (BM / a.G)) * a.H_kv;
+    return pairs >= 2 * static_cast<int64_t>(paged_sm_count()) ? 2 : 1;
+}
+
 template <int D>
 cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s) {
     using C = TileCfg<D>;
@@ -1017,6 +1031,7 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cu
     t.a = a;
     t.ws = w;
     t.TQ = x.TQ;
+    t.TT = x.TQ * tiles_of_unit(a);
     t.min_tiles = 4;
     t.o_align32 = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.o_st[0] % 16 == 0 && a.o_st[1] % 16 == 0;
     t.fault_stop_fill = fault_plan().band_stop_fill;
