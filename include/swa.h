@@ -292,7 +292,8 @@ SWA_API swa_status swa_prefill_chunk(const swa_chunk_params *p, const swa_cache_
  *   k_pages, v_pages  bf16 [n_pages, H_kv, page_size, d_h], contiguous
  *   page_table        int32 [B, table_width], contiguous
  * Requirements: d_h in {64, 128, 256}; page_size in {16, 32, 64, 128}; B <= 8192;
- * table_width * page_size < 2^31; pointers 16-byte aligned (page_table: 4-byte).
+ * table_width * page_size < 2^31; (n_pages + 1) * H_kv * page_size / 8 < 2^31; pointers 16-byte
+ * aligned (page_table: 4-byte).
  */
 typedef struct swa_paged_cache {
     void *k_pages;

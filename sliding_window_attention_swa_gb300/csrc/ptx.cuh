@@ -233,20 +233,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// Warp-convergent form: every lane executes the call with the same operands, elect.sync picks the
-// lane that issues the copy.  A copy then takes 43-48 cycles of its warp instead of the 77-84 of
-// one that diverged lanes or a single lane issue (2 KB boxes, one warp an SM), which is what
-// bounds copies of small boxes.
-__device__ __forceinline__ void tma_load_4d_e(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1,
-                                              int c2, int c3) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-        "%5}], [%6];\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
-        : "memory");
-}
-
 // Orders this thread's generic-proxy shared-memory writes before later async-proxy
 // reads (tcgen05.mma operands).
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -256,6 +256,8 @@ swa_status paged_cache_check(const swa_paged_cache *c) {
         return SWA_ERR_UNSUPPORTED;
     if (c->B > swa::kPagedMaxB || static_cast<int64_t>(c->table_width) * c->page_size > INT_MAX)
         return SWA_ERR_UNSUPPORTED;
+    // the kernels count the pool's groups of 8 rows, and one page more, in 32 bits
+    if ((static_cast<int64_t>(c->n_pages) + 1) * c->H_kv > INT_MAX / (c->page_size / 8)) return SWA_ERR_UNSUPPORTED;
     if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || !aligned4(c->page_table)) return SWA_ERR_UNSUPPORTED;
     return SWA_OK;
 }

@@ -66,8 +66,9 @@ int paged_sm_count() {
     return v;
 }
 
-bool paged_map(CUtensorMap *m, const void *base, int D, int64_t n1, int64_t n2, int64_t n3, int64_t s1, int64_t s2,
-               int64_t s3, int b1, int b2) {
+namespace {
+bool encode(CUtensorMap *m, const void *base, const int64_t (&dims)[4], const int64_t (&strides)[3],
+            const int (&box)[4]) {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         cudaDriverEntryPointQueryResult q;
         void *p = nullptr;
@@ -77,15 +78,27 @@ bool paged_map(CUtensorMap *m, const void *base, int D, int64_t n1, int64_t n2, 
         return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
     }();
     if (!fn) return false;
-    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2),
-                          static_cast<cuuint64_t>(n3)};
-    cuuint64_t strides[3] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2,
-                             static_cast<cuuint64_t>(s3) * 2};
-    cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2), 1u};
-    cuuint32_t es[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es,
+    cuuint64_t d[4], st[3];
+    cuuint32_t bx[4], es[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) {
+        d[i] = static_cast<cuuint64_t>(dims[i]);
+        bx[i] = static_cast<cuuint32_t>(box[i]);
+        if (i < 3) st[i] = static_cast<cuuint64_t>(strides[i]) * 2;
+    }
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), d, st, bx, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace
+
+bool paged_query_map(CUtensorMap *m, const PagedArgs &a, int heads, int tokens) {
+    return encode(m, a.q, {a.D, a.H_q, a.N, 1}, {a.q_st[1], a.q_st[0], a.q_st[0]}, {64, heads, tokens, 1});
+}
+
+bool paged_pool_map(CUtensorMap *m, const PagedArgs &a, const void *pool, int rows) {
+    const int64_t groups = static_cast<int64_t>(a.n_pages) * a.H_kv * (a.ps / 8);
+    return encode(m, pool, {64, 8, a.D / 64, groups}, {a.D, 64, static_cast<int64_t>(8) * a.D},
+                  {64, 8, a.D / 64, rows / 8});
 }
 
 // Few rows: every sequence's new tokens fit one unit of the split kernel (16 rows).  With more of

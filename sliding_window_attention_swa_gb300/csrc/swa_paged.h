@@ -83,10 +83,15 @@ PagedShape paged_tile_shape(const PagedArgs &a);
 cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s);
 void paged_tile_read_clear_error(unsigned int *data, unsigned int *wait);
 
-// bf16 map over (d, d1, d2, d3) of n1, n2, n3 with element strides s1, s2, s3, a box of 64 x b1 x b2 x 1
-// and 128-B swizzle.
-bool paged_map(CUtensorMap *m, const void *base, int D, int64_t n1, int64_t n2, int64_t n3, int64_t s1, int64_t s2,
-               int64_t s3, int b1, int b2);
+// bf16 maps with 128-B swizzle.
+// The rows q [N, H_q, D]: (64 of d, head, token), a box of 64 x heads x tokens.
+bool paged_query_map(CUtensorMap *m, const PagedArgs &a, int heads, int tokens);
+// A pool: (64 of d, 8 rows, column block, group of 8 rows), a box of `rows` rows of one page and
+// head.  The groups of all pages and heads count through, group (page * H_kv + head) * ps / 8 being
+// a page's first, so one copy brings a page's rows whole, whatever the head dim, and a tile's
+// pages follow one another in shared memory without a gap: column block c of row r lies at
+// (r / 8) * D / 64 * 1024 + c * 1024 + r % 8 * 128.
+bool paged_pool_map(CUtensorMap *m, const PagedArgs &a, const void *pool, int rows);
 
 int paged_sm_count();  // SMs of the current device
 

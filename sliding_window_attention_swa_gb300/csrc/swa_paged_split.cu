@@ -5,8 +5,7 @@
 // Persistent kernel, several CTAs per SM, five warps.  A CTA takes its share of the batch's
 // tiles of 64 keys (swa_paged.cuh) and streams it:
 //   warp 0     producer: looks up the pages of a tile (one tile ahead) and copies its keys and
-//              values by TMA, a box per page (or half a page of 128) and 64 elements of the
-//              head, into a ring of NST stages with 128B swizzle.  A page that is not there is
+//              values by TMA, a copy per page (or half a page of 128) into a ring of NST stages with 128B swizzle.  A page that is not there is
 //              read past the pool's end, which gives zeros.
 //   warps 1-4  consumers: 16 keys of every tile each, S = Q K^T and O += P V by mma.sync, with a
 //              running maximum and sum per row in the log2 domain.  P is rounded to bf16 for the
@@ -20,7 +19,6 @@
 #include <atomic>
 #include <climits>
 #include <cmath>
-#include <type_traits>
 
 #include "swa_paged.cuh"
 
@@ -55,10 +53,11 @@ struct SplitCfg {
     static_assert(OFF_RED >= kPagedMaxB * 8, "scratch of the work split");
 };
 
-// Offset of 16-byte piece `pc` of row `row` in a 128B-swizzled tile of CH rows written by TMA
-// boxes of 64 elements (one 128-byte row per box row).
+// Offset of 16-byte piece `pc` of row `row` in a 128B-swizzled tile (layout of paged_pool_map).
+template <int D>
 __device__ __forceinline__ uint32_t sw128(int row, int pc) {
-    return static_cast<uint32_t>((pc >> 3) * (CH * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
+    return static_cast<uint32_t>((row >> 3) * (D * 16) + (pc >> 3) * 1024 + (row & 7) * 128 +
+                                 (((pc & 7) ^ (row & 7)) << 4));
 }
 
 template <int D>
@@ -117,19 +116,6 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
         bool ok = true;
         const int box = min(a.ps, CH), npg = CH / box;  // rows of a box, boxes of a tile
         const int my_pg = lane % npg;                   // lane i looks up the page of box i % npg
-        auto copy_boxes = [&](auto boxes, int st, int kvh, int row, int page) {
-            constexpr int kBoxes = decltype(boxes)::value;
-#pragma unroll
-            for (int e = 0; e < kBoxes; ++e) {
-                const int pg = __shfl_sync(0xffffffffu, page, e);
-                // debug build: the box lies in the page, the head exists
-                (void)SWA_IN_BOUNDS(row + box <= a.ps && kvh < a.H_kv && pg <= a.n_pages, &g_psplit_err);
-#pragma unroll
-                for (int c = 0; c < 2 * (D / 64); ++c)  // keys, then values
-                    tma_load_4d_e(sbase + C::OFF_RING + st * C::STAGE + c * (CH * 128) + e * (CH / kBoxes) * 128,
-                                  c < D / 64 ? &tm_k : &tm_v, bar_full(st), c % (D / 64) * 64, row, kvh, pg);
-            }
-        };
         while (ok && walk.next(p)) {
             if (p.open() && !p.begun()) open = make_int4(p.u.n - p.j1, p.b, p.kvh, p.ut);
             const int t0 = p.s.p0 + p.ut * TT, t1 = p.s.p0 + min(p.s.n, (p.ut + 1) * TT) - 1;
@@ -171,9 +157,15 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
                 if (lane == 0) mbar_arrive_expect_tx(bar_full(st), C::STAGE);
                 __syncwarp();
                 const int row = npg == 1 ? k0 & (a.ps - 1) : 0;  // (a tile may be part of one page)
-                if (npg == 1) copy_boxes(std::integral_constant<int, 1>(), st, p.kvh, row, page);
-                else if (npg == 2) copy_boxes(std::integral_constant<int, 2>(), st, p.kvh, row, page);
-                else copy_boxes(std::integral_constant<int, 4>(), st, p.kvh, row, page);
+                // debug build: the box lies in the page, the head exists
+                (void)SWA_IN_BOUNDS(row + box <= a.ps && p.kvh < a.H_kv && page <= a.n_pages, &g_psplit_err);
+                if (lane < 2 * npg) {  // keys, then values, a lane each
+                    const int v = lane / npg;
+                    tma_load_4d(sbase + C::OFF_RING + st * C::STAGE + v * (C::STAGE / 2) + my_pg * box * D * 2,
+                                v ? &tm_v : &tm_k, bar_full(st), 0, 0, 0,
+                                (page * a.H_kv + p.kvh) * (a.ps >> 3) + (row >> 3));
+                }
+                __syncwarp();
                 ++seq;
                 page = ahead;
             }
@@ -241,7 +233,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
                         for (int idx = lane; idx < 16 * (D / 8); idx += 32) {
                             const int rr = idx / (D / 8), pc = idx % (D / 8);
                             if (k0 + rr >= end)
-                                *reinterpret_cast<uint4 *>(vg + sw128(16 * w + rr, pc)) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4 *>(vg + sw128<D>(16 * w + rr, pc)) = make_uint4(0, 0, 0, 0);
                         }
                         __syncwarp();
                     }
@@ -254,7 +246,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
 #pragma unroll
                         for (int k2 = 0; k2 < D / 32; ++k2) {
                             uint32_t b0, b1, b2, b3;
-                            ldsm_x4(ks + sw128(row, k2 * 4 + (lane >> 3)), b0, b1, b2, b3);
+                            ldsm_x4(ks + sw128<D>(row, k2 * 4 + (lane >> 3)), b0, b1, b2, b3);
                             mma_bf16_16816(sc[nt], qa[2 * k2], b0, b1);
                             mma_bf16_16816(sc[nt], qa[2 * k2 + 1], b2, b3);
                         }
@@ -314,7 +306,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
 #pragma unroll
                     for (int d2 = 0; d2 < D / 16; ++d2) {
                         uint32_t b0, b1, b2, b3;
-                        ldsm_x4_t(vs + sw128(vrow, 2 * d2 + (lane >> 4)), b0, b1, b2, b3);
+                        ldsm_x4_t(vs + sw128<D>(vrow, 2 * d2 + (lane >> 4)), b0, b1, b2, b3);
                         mma_bf16_16816(acc[2 * d2], pa, b0, b1);
                         mma_bf16_16816(acc[2 * d2 + 1], pa, b2, b3);
                     }
@@ -504,9 +496,7 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cu
     }
     CUtensorMap mk, mv;
     const int rows = a.ps < CH ? a.ps : CH;
-    const int64_t page = static_cast<int64_t>(a.ps) * D;
-    if (!paged_map(&mk, a.k_pages, D, a.ps, a.H_kv, a.n_pages, D, page, page * a.H_kv, rows, 1) ||
-        !paged_map(&mv, a.v_pages, D, a.ps, a.H_kv, a.n_pages, D, page, page * a.H_kv, rows, 1))
+    if (!paged_pool_map(&mk, a, a.k_pages, rows) || !paged_pool_map(&mv, a, a.v_pages, rows))
         return cudaErrorInvalidValue;
     const PagedShape x = paged_split_shape(a);
     return launch_dependent(after_append, paged_split_kernel<D>, dim3(x.ctas), kThreads, C::SMEM, s, mk, mv, a, w, x.TQ,

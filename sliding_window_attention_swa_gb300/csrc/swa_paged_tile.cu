@@ -8,11 +8,11 @@
 // (swa_paged.cuh), a part of a unit that a CTA has is a piece.
 // Roles:
 //   warps 0, 2    producers of the keys and of the values: K_0, V_0, K_1, V_1, ... of every piece into
-//                 a ring of NSLOT shared-memory slots by TMA, one box per page (or part of a page)
-//                 and 64 elements of the head, one lane each; the pages are looked up 32 boxes ahead.
-//                 Pages past the sequence's end or not there read past the pool: zeros.  Two warps,
-//                 since a copy takes about 70 cycles of the warp that issues it and a tile on pages
-//                 of 16 is 32 copies.  Every fill has its own arrival and its own release.
+//                 a ring of NSLOT shared-memory slots by TMA, one copy per page (or part of one), one
+//                 lane each; the pages are looked up 32 copies ahead.  Pages past the sequence's end
+//                 or not there read past the pool: zeros.  Two warps, since a copy takes 77 cycles of
+//                 the warp that issues it and a tile on pages of 16 is 16 of them.  Every fill has
+//                 its own arrival and its own release.
 //   warp 1        TMEM owner and MMA issuer (warp-uniform loop, one elected lane issues):
 //                   S  = Q K_j^T (A = Q from shared memory, at head dim 256 from tensor memory)
 //                   O += P V_j   (A = P from tensor memory)
@@ -245,8 +245,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         // the scratch of the work split lies in the ring: order its generic accesses before the copies
         fence_proxy_async_smem();
         asm volatile("griddepcontrol.wait;" ::: "memory");  // (the append before this kernel has stored its rows)
-        // A tile is npg boxes (pages or a part of one) times D / 64 column blocks.  The pages are looked
-        // up 32 boxes at a time, lane i that of box i, a group ahead of their use.
+        // A tile is npg boxes (pages or a part of one).  The pages are looked up 32 boxes at a time,
+        // lane i that of box i, a group ahead of their use.
         const int box = min(a.ps, BN), npg = BN / box, per_group = 32 / npg;
         struct Group {
             int tiles, kvh, row, entry;  // row, entry: of this lane's box
@@ -284,10 +284,11 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                          there ? __ldg(a.table + static_cast<int64_t>(b) * a.width + (kp >> a.ps_log2)) : -1,
                          there && kp <= t1 && (kp + box > lo || kp < a.n_sink), head};
         };
-        // Where a tile's boxes are: lane i has the page of box i % npg and issues that box's copy of
-        // column block i / npg.  (Copies that the converged warp issues one after the other, though
-        // faster by themselves -- 43 cycles each instead of 77 --, made every case slower: the
-        // Mistral window on pages of 16 674 -> 748 us, chunks of 2048 tokens behind 30000 1017 -> 1097 us.)
+        // Where a tile's boxes are: lane i has the page of box i % npg, and the lanes below npg issue
+        // the copies.  (Copies that the converged warp issues one after the other, by elect.sync, take
+        // 43 cycles each instead of 77, and yet made every case slower: with one per column block
+        // the Mistral window on pages of 16 674 -> 748 us, chunks of 2048 tokens behind 30000 1017 ->
+        // 1097 us.)
         struct Ref {
             int kvh, row, token, page;
         };
@@ -310,13 +311,12 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             ++at;
             return r;
         };
-        const int my_c = lane / npg;
-        const uint32_t my_off = static_cast<uint32_t>(my_c * (BN * 128) + lane % npg * box * 128);
         auto copy = [&](const Ref &r, const CUtensorMap *map, int slot, uint32_t bar) {
             // debug build: the box lies in the page, the head exists
             (void)SWA_IN_BOUNDS(r.row + box <= a.ps && r.kvh < a.H_kv && r.page <= a.n_pages, &g_ptile_err);
-            if (my_c < D / 64)
-                tma_load_4d(sRing + slot * C::TBYTES + my_off, map, bar, my_c * 64, r.row, r.kvh, r.page);
+            if (lane < npg)
+                tma_load_4d(sRing + slot * C::TBYTES + lane * box * D * 2, map, bar, 0, 0, 0,
+                            (r.page * a.H_kv + r.kvh) * (a.ps >> 3) + (r.row >> 3));
             __syncwarp();
         };
         const bool values = warp == 2;
@@ -386,18 +386,18 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                                                    1024, kSwizzle128B)
                                        : 0ull;
         auto v_descs = [&](int slot) {
-            const uint64_t v0 = smem_desc(sRing + slot * C::TBYTES, BN * 128, 1024, kSwizzle128B);
+            const uint64_t v0 = smem_desc(sRing + slot * C::TBYTES, 1024, D * 16, kSwizzle128B);
 #pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk) vd[kk] = desc_offset(v0, kk * 2048);
+            for (int kk = 0; kk < BN / 16; ++kk) vd[kk] = desc_offset(v0, kk * D * 32);
         };
         auto landed = [&](int f) -> bool { return warp_wait(bar_full(f % NSLOT), fphase(f), abort); };
         // S of the key tile in ring slot ks (landed) into TMEM slot `slot` from query tile qt
         auto mma_s = [&](int slot, int qt, int ks) {
             tc_fence_after();
-            const uint64_t b0 = smem_desc(sRing + ks * C::TBYTES, 16, 1024, kSwizzle128B);
+            const uint64_t b0 = smem_desc(sRing + ks * C::TBYTES, 16, D * 16, kSwizzle128B);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t bd = desc_offset(b0, (kk >> 2) * (BN * 128) + (kk & 3) * 32);
+                const uint64_t bd = desc_offset(b0, (kk >> 2) * 1024 + (kk & 3) * 32);
                 if constexpr (C::QTM)
                     tc_mma_ts_e(tmem + C::tm_s(slot), tmem + C::TM_Q + kk * 8, bd, idS, kk > 0 ? 1u : 0u);
                 else tc_mma_ss_e(tmem + C::tm_s(slot), qdesc[qt][kk], bd, idS, kk > 0 ? 1u : 0u);
@@ -556,6 +556,10 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 ib = first + (tlo + 1) / BN;
                 iz = !wk->open() && (wk->tile(n - 1) + 1) * BN > wk->p0 + wk->n ? n - 1 : -1;
             }
+            // A warp without a row hands its P over as it finds it: rows of other warps do not see it,
+            // and its own are not stored.  The exponentials of one sub-partition's warps are what bounds a
+            // tile, so the others' (a single token has rows in one warp of four) are not spent.
+            const bool idle = __all_sync(0xffffffffu, (r / a.G >= ta.TQ) || t >= wk->p0 + wk->n);
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
             for (int i = single ? wg : 0; i < n; i += single ? 2 : 1) {
@@ -579,6 +583,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 }
                 tc_fence_after();
                 const uint32_t s_addr = tmem + lane_addr + C::tm_s(slot);
+                if (!idle) {
                 float x[BN];
                 {
                     uint32_t raw[BN / 32][32];
@@ -682,6 +687,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     rsum = lo + hi;
                 }
                 l = l * alpha + rsum;
+                }
                 if (i == iz && (NQT == 1 || single || wg == 0)) {
                     // the sequence ends in this tile: zero the value rows of its last page past the
                     // end (later pages came as zeros).  The first P V of the tile waits for this
@@ -696,8 +702,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     uint8_t *vt = sgen + C::OFF_RING + (fv % NSLOT) * C::TBYTES;
                     for (int idx = r; idx < (z1 - z0) * (D / 8); idx += BM) {
                         const int row = z0 + idx / (D / 8), pc = idx % (D / 8);
-                        *reinterpret_cast<uint4 *>(vt + (pc >> 3) * (BN * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4)) =
-                            make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(vt + (row >> 3) * (D * 16) + (pc >> 3) * 1024 + (row & 7) * 128 +
+                                                   (((pc & 7) ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                 }
@@ -755,7 +761,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             // a shared tile's columns are read out half by each warpgroup
             const int c0 = single ? wg * (D / 64) : 0, c1 = single ? c0 + D / 64 : D / 32;
 #pragma unroll 1
-            for (int c = c0; c < c1; ++c) {
+            for (int c = idle ? c1 : c0; c < c1; ++c) {
                 __syncwarp();  // tcgen05.ld is executed by the converged warp: lanes that store come back here
                 uint32_t ov[32];
                 tmem_ld32(tmem + lane_addr + C::tm_o(single ? 0 : wg) + c * 32, ov);
@@ -1022,10 +1028,8 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cu
     const PagedShape x = paged_tile_shape(a);
     const int box = a.ps < C::BN ? a.ps : C::BN;
     CUtensorMap mq, mk, mv;
-    const int64_t row = D, page = static_cast<int64_t>(a.ps) * D;
-    if (!paged_map(&mq, a.q, D, a.H_q, a.N, 1, a.q_st[1], a.q_st[0], a.q_st[0], a.G, x.TQ) ||
-        !paged_map(&mk, a.k_pages, D, a.ps, a.H_kv, a.n_pages, row, page, page * a.H_kv, box, 1) ||
-        !paged_map(&mv, a.v_pages, D, a.ps, a.H_kv, a.n_pages, row, page, page * a.H_kv, box, 1))
+    if (!paged_query_map(&mq, a, a.G, x.TQ) || !paged_pool_map(&mk, a, a.k_pages, box) ||
+        !paged_pool_map(&mv, a, a.v_pages, box))
         return cudaErrorInvalidValue;
     TileArgs t{};
     t.a = a;

@@ -84,6 +84,7 @@ def pair(x, y):
     (lambda p, c: setattr(c, "d_h", 96), 2),
     (lambda p, c: setattr(c, "table_width", 1 << 28), 2),   # positions past 2^31
     (lambda p, c: setattr(c, "B", 8193), 2),
+    (lambda p, c: setattr(c, "n_pages", 1 << 29), 2),       # 2^31 groups of eight rows
     (lambda p, c: setattr(c, "v_pages", FAKE + 4), 2),
 ])
 def test_attend_rejects(lib, mutate, status):
