@@ -87,10 +87,10 @@ struct TileCfg {
     static_assert(NQT == 2 || QBYTES == 2 * TBYTES, "a query tile is two fills");
     static constexpr int OFF_X = OFF_RING + NSLOT * TBYTES;
     static constexpr int OFF_BAR = OFF_X + XBYTES;
-    // q_full[2], q_empty[2], kv_full[NSLOT], kv_empty[NSLOT], s_full[2], p_full[2], o_done[2],
-    // o_free[2], meet, drain, piece_full[NP], piece_empty[NP]
+    // q_full[2], q_empty[2], kv_full[NSLOT], kv_empty[NSLOT], s_full[3], p_full[3], o_done[2],
+    // o_free[2], meet, drain, pv_done[2], piece_full[NP], piece_empty[NP]
     static constexpr int NP = 4;  // pieces planned ahead
-    static constexpr int NBAR = 2 * NSLOT + 14 + 2 * NP;
+    static constexpr int NBAR = 2 * NSLOT + 18 + 2 * NP;
     static constexpr int OFF_TMEMPTR = OFF_BAR + NBAR * 8;  // TMEM address, abort flag
     static constexpr int OFF_SHARE = OFF_TMEMPTR + 16;
     static constexpr int OFF_PIECE = OFF_SHARE + 64;
@@ -98,15 +98,20 @@ struct TileCfg {
     static constexpr int SMEM = OFF_PIECE + NP * static_cast<int>(sizeof(TilePiece));
     static_assert(sizeof(Share) <= 64, "share");
     static constexpr uint32_t TMEM_COLS = 512;
+    // S slots: two, or three where tensor memory has room (head dim 64), so that S(j + 2) is there
+    // when the warpgroup that had tile j is done with it (full causal 890 -> ... us, see below)
+    static constexpr int NS = D == 64 ? 3 : 2;
     __host__ __device__ static constexpr uint32_t tm_s(int slot) { return static_cast<uint32_t>(slot * BN); }
-    __host__ __device__ static constexpr uint32_t tm_o(int tile) { return 256u + static_cast<uint32_t>(tile * 128); }
+    __host__ __device__ static constexpr uint32_t tm_o(int tile) {
+        return D == 64 ? 384u + static_cast<uint32_t>(tile * 64) : 256u + static_cast<uint32_t>(tile * 128);
+    }
     static constexpr bool QTM = NQT == 1;  // the query tile in tensor memory, 128 columns
     static constexpr uint32_t TM_Q = 128;
     static_assert(NSLOT >= 3, "K/V ring too shallow");
     static_assert(SMEM <= 232448, "shared memory budget");
     static_assert(NSLOT * TBYTES >= kShareScratch, "scratch of the work split");
     static_assert(!QTM || (tm_s(1) + BN <= TM_Q && TM_Q + D / 2 <= tm_o(0)), "query tile in tensor memory");
-    static_assert(tm_o(NQT - 1) + D <= TMEM_COLS && tm_s(1) + BN <= 256, "tensor memory budget");
+    static_assert(tm_o(NQT - 1) + D <= TMEM_COLS && tm_s(NS - 1) + BN <= tm_o(0), "tensor memory budget");
 };
 
 struct TileArgs {
@@ -163,13 +168,14 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     auto bar_full = [&](int s) { return bars + 8u * (4 + s); };
     auto bar_empty = [&](int s) { return bars + 8u * (4 + NSLOT + s); };
     auto bar_sf = [&](int i) { return bars + 8u * (4 + 2 * NSLOT + i); };
-    auto bar_pf = [&](int i) { return bars + 8u * (6 + 2 * NSLOT + i); };
-    auto bar_od = [&](int i) { return bars + 8u * (8 + 2 * NSLOT + i); };
-    auto bar_of = [&](int i) { return bars + 8u * (10 + 2 * NSLOT + i); };
-    const uint32_t bar_meet = bars + 8u * (12 + 2 * NSLOT);
-    const uint32_t bar_drain = bars + 8u * (13 + 2 * NSLOT);
-    auto bar_piece = [&](int i) { return bars + 8u * (14 + 2 * NSLOT + i); };
-    auto bar_used = [&](int i) { return bars + 8u * (14 + 2 * NSLOT + C::NP + i); };
+    auto bar_pf = [&](int i) { return bars + 8u * (7 + 2 * NSLOT + i); };
+    auto bar_od = [&](int i) { return bars + 8u * (10 + 2 * NSLOT + i); };
+    auto bar_of = [&](int i) { return bars + 8u * (12 + 2 * NSLOT + i); };
+    const uint32_t bar_meet = bars + 8u * (14 + 2 * NSLOT);
+    const uint32_t bar_drain = bars + 8u * (15 + 2 * NSLOT);
+    auto bar_pv = [&](int i) { return bars + 8u * (16 + 2 * NSLOT + i); };
+    auto bar_piece = [&](int i) { return bars + 8u * (18 + 2 * NSLOT + i); };
+    auto bar_used = [&](int i) { return bars + 8u * (18 + 2 * NSLOT + C::NP + i); };
     // Ring fills, numbered over the CTA's share; fill p lies in slot p % NSLOT, phase (p / NSLOT) & 1
     // of the slot's barriers.  A piece's query tile comes first at head dim 256 (two fills), then K
     // and V of each of its tiles: kfill is K of the share's g-th tile, in its k-th piece, V the next.
@@ -185,10 +191,13 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar_qf(x), 1);
             mbar_init(bar_qe(x), 4);  // the four warps of a softmax warpgroup
+            mbar_init(bar_od(x), 1);
+            mbar_init(bar_pv(x), 1);
+            mbar_init(bar_of(x), 4);
+        }
+        for (int x = 0; x < 3; ++x) {
             mbar_init(bar_sf(x), 1);
             mbar_init(bar_pf(x), 4);
-            mbar_init(bar_od(x), 1);
-            mbar_init(bar_of(x), 4);
         }
         for (int s = 0; s < NSLOT; ++s) {
             mbar_init(bar_full(s), 1);
@@ -248,6 +257,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         // A tile is npg boxes (pages or a part of one).  The pages are looked up 32 boxes at a time,
         // lane i that of box i, a group ahead of their use.
         const int box = min(a.ps, BN), npg = BN / box, per_group = 32 / npg;
+        const bool values = warp == 2;
         struct Group {
             int tiles, kvh, row, entry;  // row, entry: of this lane's box
             bool need;                   // some query row keeps a key of this lane's box
@@ -284,86 +294,78 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                          there ? __ldg(a.table + static_cast<int64_t>(b) * a.width + (kp >> a.ps_log2)) : -1,
                          there && kp <= t1 && (kp + box > lo || kp < a.n_sink), head};
         };
-        // Where a tile's boxes are: lane i has the page of box i % npg, and the lanes below npg issue
-        // the copies.  (Copies that the converged warp issues one after the other, by elect.sync, take
-        // 43 cycles each instead of 77, and yet made every case slower: with one per column block
-        // the Mistral window on pages of 16 674 -> 748 us, chunks of 2048 tokens behind 30000 1017 ->
-        // 1097 us.)
-        struct Ref {
-            int kvh, row, token, page;
+        // The next fill: its slot and its phase.  The loop below is kept short: beside two softmax warps
+        // on its sub-partition an instruction of this warp takes about ten cycles.
+        int slot = 0, fills = 0;
+        uint32_t phase = 0;
+        auto skip_fills = [&](int c) {
+            slot += c;
+            fills += c;
+            if (slot >= NSLOT) {
+                slot -= NSLOT;
+                phase ^= 1u;
+            }
         };
+        uint32_t mine = 0, mine_phase = 0;  // slots that hold a fill of this warp, and its phase
+        // the slot is free (its last occupant released; at first it is) and `bytes` are expected on it
+        auto take_slot = [&](int bytes) -> bool {
+            if (fills >= ta.fault_stop_fill) return false;  // planted fault: this fill is never issued
+            if (!warp_wait(bar_empty(slot), phase ^ 1u, abort)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(bar_full(slot), static_cast<uint32_t>(bytes));
+            __syncwarp();
+            mine |= 1u << slot;
+            mine_phase = (mine_phase & ~(1u << slot)) | (phase << slot);
+            return true;
+        };
+        // The copies of a tile: the lanes below npg issue one each.  (Copies that the converged warp
+        // issues one after the other, by elect.sync, take 43 cycles each instead of 77, and yet made
+        // every case slower: with one per column block the Mistral window on pages of 16 674 -> 748 us,
+        // chunks of 2048 tokens behind 30000 1017 -> 1097 us.)
+        const CUtensorMap *map = values ? &tm_v : &tm_k;
+        const uint32_t my_off = sRing + static_cast<uint32_t>(lane * box * D * 2);
         Group now{0, 0, 0, 0, false, -1}, then = now;
-        int at = 0, page = 0;  // next tile of the group; this lane's page
-        auto next_tile = [&]() -> Ref {
+        if (cta_tiles > 0) then = look_up();
+        int at = 0, group8 = 0;  // next tile of the group; this lane's box as a group of eight rows of the pool
+        if (values) skip_fills(1);
+#pragma unroll 1
+        for (int t = 0; t < cta_tiles && ok; ++t) {
             if (at >= now.tiles) {
                 now = then;
                 if (looked < cta_tiles) then = look_up();
                 at = 0;
                 const bool in_pool = static_cast<unsigned>(now.entry) < static_cast<unsigned>(a.n_pages);
-                page = in_pool ? now.entry : a.n_pages;
                 if (now.need && !in_pool) atomicOr(&g_ptile_data, SWA_DEVERR_BAD_PAGE);
-            }
-            Ref r;
-            r.kvh = now.kvh;
-            r.token = at == 0 ? now.token : -1;
-            r.row = __shfl_sync(0xffffffffu, now.row, at * npg);  // (not 0 only if a tile is part of one page)
-            r.page = __shfl_sync(0xffffffffu, page, (at * npg + lane % npg) & 31);
-            ++at;
-            return r;
-        };
-        auto copy = [&](const Ref &r, const CUtensorMap *map, int slot, uint32_t bar) {
-            // debug build: the box lies in the page, the head exists
-            (void)SWA_IN_BOUNDS(r.row + box <= a.ps && r.kvh < a.H_kv && r.page <= a.n_pages, &g_ptile_err);
-            if (lane < npg)
-                tma_load_4d(sRing + slot * C::TBYTES + lane * box * D * 2, map, bar, 0, 0, 0,
-                            (r.page * a.H_kv + r.kvh) * (a.ps >> 3) + (r.row >> 3));
-            __syncwarp();
-        };
-        const bool values = warp == 2;
-        int last = 0;       // this warp's last fill
-        uint32_t mine = 0;  // bit i: it issued fill last - i
-        // fill f's slot, once its last occupant has been released, with `bytes` expected on its barrier
-        auto next_slot = [&](int f, int bytes) -> bool {
-            if (f >= ta.fault_stop_fill) return false;  // planted fault: this fill is never issued
-            const int slot = f % NSLOT;
-            if (f >= NSLOT && !warp_wait(bar_empty(slot), fphase(f - NSLOT), abort)) return false;
-            if (lane == 0) mbar_arrive_expect_tx(bar_full(slot), static_cast<uint32_t>(bytes));
-            __syncwarp();
-            mine = (f - last < 32 ? mine << (f - last) : 0u) | 1u;
-            last = f;
-            return true;
-        };
-        Ref r{};
-        int pc = 0;  // pieces begun
-        if (cta_tiles > 0) {
-            then = look_up();
-            r = next_tile();
-        }
+                // debug build: the box lies in the page, the head exists
+                (void)SWA_IN_BOUNDS(now.row + box <= a.ps && now.kvh < a.H_kv, &g_ptile_err);
+                group8 = ((in_pool ? now.entry : a.n_pages) * a.H_kv + now.kvh) * (a.ps >> 3) + (now.row >> 3);
+                if (NQT == 1 && now.token >= 0) {
+                    // a new piece: its query tile, in two halves, comes before its first key tile
 #pragma unroll 1
-        for (int t = 0; t < cta_tiles && ok; ++t) {
-            if (r.token >= 0) ++pc;
-            const int f = kfill(pc - 1, t) + (values ? 1 : 0);
-            if (NQT == 1 && !values && r.token >= 0) {
-                // the piece's query tile, in two halves
-#pragma unroll 1
-                for (int q = f - 2; q < f && ok; ++q) {
-                    ok = next_slot(q, a.G * ta.TQ * D);
+                    for (int hlf = 0; hlf < 2 && ok; ++hlf) {
+                        if (!values) {
+                            ok = take_slot(a.G * ta.TQ * D);
+                            // debug build: the tile's tokens and its group's heads exist
+                            (void)SWA_IN_BOUNDS(now.token < a.N && (now.kvh + 1) * a.G <= a.H_q, &g_ptile_err);
+                            if (ok && lane < D / 128)
+                                tma_load_4d(sRing + slot * C::TBYTES + lane * (BM * 128), &tm_q, bar_full(slot),
+                                            hlf * (D / 2) + lane * 64, now.kvh * a.G, now.token, 0);
+                            __syncwarp();
+                        }
+                        skip_fills(1);
+                    }
                     if (!ok) break;
-                    // debug build: the tile's tokens and its group's heads exist
-                    (void)SWA_IN_BOUNDS(r.token < a.N && (r.kvh + 1) * a.G <= a.H_q, &g_ptile_err);
-                    if (lane < D / 128)
-                        tma_load_4d(sRing + q % NSLOT * C::TBYTES + lane * (BM * 128), &tm_q, bar_full(q % NSLOT),
-                                    (q - f + 2) * (D / 2) + lane * 64, r.kvh * a.G, r.token, 0);
-                    __syncwarp();
                 }
             }
-            ok = ok && next_slot(f, C::TBYTES);
-            if (ok) copy(r, values ? &tm_v : &tm_k, f % NSLOT, bar_full(f % NSLOT));
-            if (t + 1 < cta_tiles) r = next_tile();
+            const int from = __shfl_sync(0xffffffffu, group8, (at * npg + lane) & 31);
+            ++at;
+            ok = ok && take_slot(C::TBYTES);
+            if (ok && lane < npg) tma_load_4d(my_off + slot * C::TBYTES, map, bar_full(slot), 0, 0, 0, from);
+            __syncwarp();
+            if (ok) skip_fills(2);
         }
-        if (!ok && lane == 0)  // drain this warp's copies that may still be in flight: at most one a slot
+        if (!ok && lane == 0)  // drain this warp's copies that may still be in flight: the last of each slot
             for (int i2 = 0; i2 < NSLOT; ++i2)
-                if ((mine >> i2) & 1u) mbar_drain(bar_full((last - i2) % NSLOT), fphase(last - i2), &g_ptile_err);
+                if ((mine >> i2) & 1u) mbar_drain(bar_full(i2), (mine_phase >> i2) & 1u, &g_ptile_err);
     } else if (warp == 1) {
         // ============================ MMA issuer ============================
         if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             if constexpr (NQT == 2) {
                 ok = warp_wait(bar_qf(0), k & 1, abort) && landed(2 * J);
                 if (!ok) break;
-                mma_s(0, 0, (2 * J) % NSLOT);
+                mma_s(C::NS == 3 ? J % 3 : 0, 0, (2 * J) % NSLOT);
                 if (C::kPairs && !single) {
                     ok = warp_wait(bar_qf(1), k & 1, abort);
                     if (!ok) break;
@@ -456,23 +458,33 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     np0 += n;
                     np1 += n;
                 } else {
-                    // one query tile, its key tiles in slot 0 and 1 in turn
+                    // one query tile, its key tiles in the S slots in turn, for one warpgroup and the other
+                    auto s_slot = [&](int i2) { return C::NS == 3 ? (J + i2) % 3 : i2 & 1; };
                     tc_commit_e(bar_empty((2 * J) % NSLOT));
                     ok = warp_wait(bar_qf(1), k & 1, abort);
                     if (!ok) break;
+                    if (C::NS == 3 && n > 1) {
+                        ok = landed(2 * J + 2);
+                        if (!ok) break;
+                        mma_s(s_slot(1), 0, (2 * J + 2) % NSLOT);
+                        tc_commit_e(bar_empty((2 * J + 2) % NSLOT));
+                    }
 #pragma unroll 1
                     for (int i = 0; i < n; ++i) {
                         const int f = 2 * (J + i), x = i & 1;
-                        if (i + 1 < n) {  // S of tile i + 1 into the other slot, whose P V is issued
-                            ok = landed(f + 2);
+                        if (i + C::NS - 1 < n) {  // an S slot whose P V is issued
+                            const int fk = f + 2 * (C::NS - 1);
+                            ok = landed(fk);
                             if (!ok) break;
-                            mma_s(x ^ 1, 0, (f + 2) % NSLOT);
-                            tc_commit_e(bar_empty((f + 2) % NSLOT));
+                            mma_s(s_slot(i + C::NS - 1), 0, fk % NSLOT);
+                            tc_commit_e(bar_empty(fk % NSLOT));
                         }
                         v_descs((f + 1) % NSLOT);
-                        ok = mma_pv(x, x, i < 2, x ? np1++ : np0++, f + 1);
+                        const uint32_t used = C::NS == 3 ? static_cast<uint32_t>((J + i) / 3) : x ? np1++ : np0++;
+                        ok = mma_pv(s_slot(i), x, i < 2, used, f + 1);
                         if (!ok) break;
                         tc_commit_e(bar_empty((f + 1) % NSLOT));
+                        if constexpr (C::NS == 3) tc_commit_e(bar_pv(x));
                     }
                     if (!ok) break;
                     tc_commit_e(bar_od(0));
@@ -564,8 +576,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
 #pragma unroll 1
             for (int i = single ? wg : 0; i < n; i += single ? 2 : 1) {
                 const int g = J + i;
-                const int slot = NQT == 2 ? wg : (g & 1);
-                const uint32_t parity = NQT == 2 ? (ns & 1) : ((g >> 1) & 1);
+                const int slot = C::NS == 3 ? g % 3 : NQT == 2 ? wg : (g & 1);
+                const uint32_t parity = C::NS == 3 ? (g / 3) & 1 : NQT == 2 ? (ns & 1) : ((g >> 1) & 1);
                 if (!warp_wait(bar_sf(slot), parity, abort)) {
                     ok = false;
                     break;
@@ -637,8 +649,16 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 const float alpha = need ? ex2(m - mu) : 1.f;  // m = -inf gives 0
                 if (__any_sync(0xffffffffu, need) && i >= (single ? 2 : 1)) {
                     // O holds the P V of this piece's earlier tiles (of this warpgroup) and must be
-                    // complete: with two query tiles S(i) was issued after them; with one, the release
-                    // of tile g-1's V slot is committed right after its P V
+                    // complete: with two S slots and two warpgroups S(i) was issued after them; with three
+                    // each P V has a commit of its own; with one warpgroup the release of tile g-1's V
+                    // slot is committed right after its P V
+                    if constexpr (C::NS == 3) {
+                        if (!warp_wait(bar_pv(wg), ns & 1, abort)) {  // (this is the warpgroup's tile ns - 1)
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
                     if constexpr (NQT == 1) {
                         const int f = kfill(k, g - 1) + 1;
                         if (!warp_wait(bar_empty(f % NSLOT), fphase(f), abort)) {
