@@ -592,6 +592,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                         mbar_arrive(bar_empty((2 * g) % NSLOT));
                         if (i > 0) mbar_arrive(bar_empty((2 * g - 1) % NSLOT));
                     }
+                    __syncwarp();  // tcgen05.ld is executed by the converged warp
                 }
                 tc_fence_after();
                 const uint32_t s_addr = tmem + lane_addr + C::tm_s(slot);
