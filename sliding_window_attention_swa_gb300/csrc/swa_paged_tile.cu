@@ -371,7 +371,9 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
         constexpr uint32_t idS = idesc_bf16_f32(BM, BN, false, false);
         constexpr uint32_t idPV = idesc_bf16_f32(BM, D, false, true);
-        bool ok = true, was_single = false;
+        bool ok = true, was_single = false, both = false;
+        int y = 1;                  // the query tile's buffer of the last unit of one
+        uint32_t nq[2] = {0, 0};    // uses of each buffer so far
         int J = 0;                  // tiles of this CTA's previous pieces
         int k = 0;                  // pieces so far
         uint32_t np0 = 0, np1 = 0;  // P tiles of each slot used so far
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         };
         auto landed = [&](int f) -> bool { return warp_wait(bar_full(f % NSLOT), fphase(f), abort); };
         // S of the key tile in ring slot ks (landed) into TMEM slot `slot` from query tile qt
-        auto mma_s = [&](int slot, int qt, int ks) {
+        auto mma_s = [&](int slot, int qt, int ks, uint32_t q_bytes = 0) {
             tc_fence_after();
             const uint64_t b0 = smem_desc(sRing + ks * C::TBYTES, 16, D * 16, kSwizzle128B);
 #pragma unroll
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 const uint64_t bd = desc_offset(b0, (kk >> 2) * 1024 + (kk & 3) * 32);
                 if constexpr (C::QTM)
                     tc_mma_ts_e(tmem + C::tm_s(slot), tmem + C::TM_Q + kk * 8, bd, idS, kk > 0 ? 1u : 0u);
-                else tc_mma_ss_e(tmem + C::tm_s(slot), qdesc[qt][kk], bd, idS, kk > 0 ? 1u : 0u);
+                else tc_mma_ss_e(tmem + C::tm_s(slot), desc_offset(qdesc[qt][kk], q_bytes), bd, idS, kk > 0 ? 1u : 0u);
             }
             tc_commit_e(bar_sf(slot));
         };
@@ -413,8 +415,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             if (wait_v >= 0 && !landed(wait_v)) return false;
             if (first && k >= 1) {
                 if (!warp_wait(bar_of(ot), (k - 1) & 1, abort)) return false;
-                // (both warpgroups read both accumulators of a piece of one query tile)
-                if (NQT == 2 && was_single && !warp_wait(bar_of(ot ^ 1), (k - 1) & 1, abort)) return false;
+                // (of a piece of one query tile both warpgroups read both accumulators, and both finish with it)
+                if (NQT == 2 && both && !warp_wait(bar_of(ot ^ 1), (k - 1) & 1, abort)) return false;
             }
             tc_fence_after();
 #pragma unroll
@@ -429,12 +431,13 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             const int n = p->j1 - p->j0;
             const bool single = is_single(p->n, p->ut);
             give_back(k);
+            both = was_single || single;
             if constexpr (NQT == 2) {
-                ok = warp_wait(bar_qf(0), k & 1, abort) && landed(2 * J);
-                if (!ok) break;
-                mma_s(C::NS == 3 ? J % 3 : 0, 0, (2 * J) % NSLOT);
                 if (C::kPairs && !single) {
-                    ok = warp_wait(bar_qf(1), k & 1, abort);
+                    ok = warp_wait(bar_qf(0), nq[0]++ & 1, abort) && landed(2 * J);
+                    if (!ok) break;
+                    mma_s(0, 0, (2 * J) % NSLOT);
+                    ok = warp_wait(bar_qf(1), nq[1]++ & 1, abort);
                     if (!ok) break;
                     mma_s(1, NQT - 1, (2 * J) % NSLOT);
 #pragma unroll 1
@@ -460,13 +463,16 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 } else {
                     // one query tile, its key tiles in the S slots in turn, for one warpgroup and the other
                     auto s_slot = [&](int i2) { return C::NS == 3 ? (J + i2) % 3 : i2 & 1; };
-                    tc_commit_e(bar_empty((2 * J) % NSLOT));
-                    ok = warp_wait(bar_qf(1), k & 1, abort);
+                    y ^= 1;
+                    const uint32_t q_bytes = y ? C::QBYTES : 0;
+                    ok = warp_wait(bar_qf(y), (y ? nq[1]++ : nq[0]++) & 1, abort) && landed(2 * J);
                     if (!ok) break;
+                    mma_s(s_slot(0), 0, (2 * J) % NSLOT, q_bytes);
+                    tc_commit_e(bar_empty((2 * J) % NSLOT));
                     if (C::NS == 3 && n > 1) {
                         ok = landed(2 * J + 2);
                         if (!ok) break;
-                        mma_s(s_slot(1), 0, (2 * J + 2) % NSLOT);
+                        mma_s(s_slot(1), 0, (2 * J + 2) % NSLOT, q_bytes);
                         tc_commit_e(bar_empty((2 * J + 2) % NSLOT));
                     }
 #pragma unroll 1
@@ -476,7 +482,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                             const int fk = f + 2 * (C::NS - 1);
                             ok = landed(fk);
                             if (!ok) break;
-                            mma_s(s_slot(i + C::NS - 1), 0, fk % NSLOT);
+                            mma_s(s_slot(i + C::NS - 1), 0, fk % NSLOT, q_bytes);
                             tc_commit_e(bar_empty(fk % NSLOT));
                         }
                         v_descs((f + 1) % NSLOT);
@@ -547,7 +553,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         const uint32_t o_addr = tmem + lane_addr + C::tm_o(wg);
         float2 *meet = reinterpret_cast<float2 *>(sgen + C::OFF_X);
         bool ok = true;
-        int J = 0, k = 0;
+        int J = 0, k = 0, y = 1;  // y: as the MMA warp's
         uint32_t ns = 0, n_meet = 0;  // S tiles of this warpgroup's slot so far; single pieces so far
 #pragma unroll 1
         for (; ok; ++k) {
@@ -746,7 +752,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             float wa = 1.f, wb = 0.f;
             if (single) {
                 // every MMA of the piece has completed: the tile may be refilled
-                if (lane == 0) mbar_arrive(bar_qe(wg));
+                y ^= 1;
+                if (wg == y && lane == 0) mbar_arrive(bar_qe(y));
                 // (the other warpgroup has read the last meeting's values: this piece's first P V
                 // waited for both epilogues)
                 meet[wg * BM + r] = make_float2(m, l);
@@ -941,7 +948,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             return false;  // (cannot be: the waves' units exist)
         };
         int k = 0, kq = 0;  // pieces handed over, query tiles loaded
-        int loads[2] = {0, 0};
+        int loads0 = 0, loads1 = 0, y = 1;  // query tiles of each buffer; y: the last unit of one took that
         bool more = true;
 #pragma unroll 1
         while (ok && (more || (NQT == 2 && kq < k))) {
@@ -984,36 +991,36 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             if constexpr (NQT == 2) {
                 if (!ok || kq >= k) continue;
                 volatile TilePiece *t = pieces + kq % C::NP;
-                const int tokens = t->n, i0 = t->ut * TT, q0 = t->q0, kvh = t->kvh;
+                const int tokens = t->n, ut = t->ut, q0 = t->q0, kvh = t->kvh;
                 give_back(kq);
+                const bool one = is_single(tokens, ut);
+                if (one) y ^= 1;
 #pragma unroll 1
-                for (int x = 0; x < NQT; ++x) {
-                    // the previous piece's S MMAs are done with this tile's shared memory
-                    if (kq >= 1) ok = warp_wait(bar_qe(x), (kq - 1) & 1, abort);
+                for (int x = one ? y : 0; x <= (one ? y : 1); ++x) {
+                    // the S MMAs of the last tile in this buffer are done with it
+                    const int before = x ? loads1 : loads0;
+                    if (before > 0) ok = warp_wait(bar_qe(x), (before - 1) & 1, abort);
                     if (!ok) break;
                     if (lane == 0) {
-                        const int i = i0 + x * ta.TQ;  // the tile's first token
-                        if (i < tokens && (x == 0 || !is_single(tokens, i0 / TT))) {
-                            // debug build: the tile's tokens and its group's heads exist
-                            (void)SWA_IN_BOUNDS(q0 + i < a.N && (kvh + 1) * a.G <= a.H_q, &g_ptile_err);
-                            mbar_arrive_expect_tx(bar_qf(x), static_cast<uint32_t>(a.G * ta.TQ * D * 2));
+                        const int i = ut * TT + (one ? 0 : x * ta.TQ);  // the tile's first token
+                        // debug build: the tile's tokens and its group's heads exist
+                        (void)SWA_IN_BOUNDS(q0 + i < a.N && (kvh + 1) * a.G <= a.H_q, &g_ptile_err);
+                        mbar_arrive_expect_tx(bar_qf(x), static_cast<uint32_t>(a.G * ta.TQ * D * 2));
 #pragma unroll
-                            for (int c = 0; c < D / 64; ++c)
-                                tma_load_4d(sQ + x * C::QBYTES + c * (BM * 128), &tm_q, bar_qf(x), c * 64, kvh * a.G,
-                                            q0 + i, 0);
-                        } else {
-                            mbar_arrive(bar_qf(x));  // the unit has no such tile
-                        }
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_4d(sQ + x * C::QBYTES + c * (BM * 128), &tm_q, bar_qf(x), c * 64, kvh * a.G, q0 + i,
+                                        0);
                     }
                     __syncwarp();
-                    ++loads[x];
+                    if (x) ++loads1;
+                    else ++loads0;
                 }
                 ++kq;
             }
         }
         if (!ok && lane == 0) {
-            for (int x = 0; x < NQT; ++x)
-                if (loads[x] > 0) mbar_drain(bar_qf(x), (loads[x] - 1) & 1, &g_ptile_err);
+            if (loads0 > 0) mbar_drain(bar_qf(0), (loads0 - 1) & 1, &g_ptile_err);
+            if (loads1 > 0) mbar_drain(bar_qf(1), (loads1 - 1) & 1, &g_ptile_err);
         }
     }
 
