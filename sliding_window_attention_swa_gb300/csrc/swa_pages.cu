@@ -23,6 +23,17 @@ constexpr int kThreads = 256;
 constexpr int kScanThreads = 1024, kScanWarps = kScanThreads / 32;
 constexpr int kScanItems = 16;  // counts per thread and scan step: as many loads in flight
 constexpr int kUnroll = 8;      // 16-byte loads in flight per thread of the page copy
+constexpr int kForkCtas = 8;    // a cluster (the largest portable one)
+// Table entries and pages up to which one cluster plans a fork: one launch instead of three, which
+// a short call waits for (32 rows of 250 entries: a call 24 -> 19 us, though 13.1 -> 14.5 us on the
+// GPU); above that the copies bound the call and the grids' plan is the faster one (400 rows of
+// head dim 256: 95.6 against 100 us).
+constexpr int kFew = 16 * 1024;
+
+// A kernel whose successor in the stream is launched with launch_dependent lets it be scheduled
+// early; the successor waits for it (and its stores) before it reads anything.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // One page copy: the first `rows` positions of page src go to page dst (src < 0: none).
 // ref: the moved page's holders (compaction).
@@ -106,6 +117,7 @@ __device__ __forceinline__ int take_free(ScanSmem &sm, const int32_t *ref, int n
 }
 
 __global__ void __launch_bounds__(kThreads) copy_i32_kernel(const int32_t *src, int32_t *dst, int64_t n) {
+    let_next_start();
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
          i += static_cast<int64_t>(gridDim.x) * kThreads)
         dst[i] = src[i];
@@ -198,9 +210,11 @@ __global__ void __launch_bounds__(kScanThreads) reserve_kernel(const TableArgs a
 }
 
 // ---------------------------------------------------------------------------------------------
-// free: every entry once
+// free: every entry once.  Bound by the atomics of a large table (1024 x 4096 entries: 23 us; four
+// entries a thread, with vector loads, took as long).
 // ---------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(kThreads) free_kernel(const TableArgs a, const int32_t *below, int n_sink) {
+    wait_for_previous();
     const uint32_t n = static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.width);  // < 2^31
     for (uint32_t x = blockIdx.x * kThreads + threadIdx.x; x < n; x += gridDim.x * kThreads) {
         const int b = static_cast<int>(x / static_cast<uint32_t>(a.width));
@@ -244,11 +258,30 @@ __device__ __forceinline__ bool fork_source(const TableArgs &a, const int32_t *s
     return true;
 }
 
+// Row i keeps its own holders where both tables have the same entry (no atomics); the others change.
+// copies: the row wants a page of its own instead of its last one.
+__device__ __forceinline__ void fork_entry(const TableArgs &a, int i, int j, int s, int used, int last, bool copies) {
+    int in = a.table[static_cast<int64_t>(i) * a.width + j];
+    int out = s >= 0 && j < used ? a.table[static_cast<int64_t>(s) * a.width + j] : -1;
+    if (in >= a.n_pages || out >= a.n_pages) {
+        atomicOr(&g_pages_err, kErrBadPage);
+        in = in >= a.n_pages ? -1 : in;
+        out = out >= a.n_pages ? -1 : out;
+    }
+    if (copies && j == last) out = -1;
+    a.out_table[static_cast<int64_t>(i) * a.width + j] = out < 0 ? -1 : out;
+    if (in != out) {
+        if (in >= 0) atomicSub(a.out_ref + in, 1);
+        if (out >= 0) atomicAdd(a.out_ref + out, 1);
+    }
+}
+
 // Rows' tables and the holders of everything but the fresh pages.  Block (x, i): a stretch of
-// row i; an entry that both tables have at the same place keeps its holder (no atomics).
-// pend[i]: row i wants a page of its own.
+// row i.  pend[i]: row i wants a page of its own.
 __global__ void __launch_bounds__(kThreads) fork_table_kernel(const TableArgs a, const int32_t *src,
                                                               const int32_t *len, int32_t *pend) {
+    let_next_start();
+    wait_for_previous();
     for (int i = blockIdx.y; i < a.B; i += gridDim.y) {
         int s, n;
         const bool ok = fork_source(a, src, len, i, s, n);
@@ -260,30 +293,15 @@ __global__ void __launch_bounds__(kThreads) fork_table_kernel(const TableArgs a,
             for (int k = threadIdx.x; k < i && !other; k += kThreads) other = src[k] == s;
         const bool copies = __syncthreads_or(other) != 0;
         if (blockIdx.x == 0 && threadIdx.x == 0) pend[i] = copies ? 1 : 0;
-        for (int j = blockIdx.x * kThreads + threadIdx.x; j < a.width; j += gridDim.x * kThreads) {
-            int in = a.table[static_cast<int64_t>(i) * a.width + j];
-            int out = s >= 0 && j < used ? a.table[static_cast<int64_t>(s) * a.width + j] : -1;
-            if (in >= a.n_pages || out >= a.n_pages) {
-                atomicOr(&g_pages_err, kErrBadPage);
-                in = in >= a.n_pages ? -1 : in;
-                out = out >= a.n_pages ? -1 : out;
-            }
-            if (copies && j == last) out = -1;
-            a.out_table[static_cast<int64_t>(i) * a.width + j] = out < 0 ? -1 : out;
-            if (in != out) {
-                if (in >= 0) atomicSub(a.out_ref + in, 1);
-                if (out >= 0) atomicAdd(a.out_ref + out, 1);
-            }
-        }
+        for (int j = blockIdx.x * kThreads + threadIdx.x; j < a.width; j += gridDim.x * kThreads)
+            fork_entry(a, i, j, s, used, last, copies);
     }
 }
 
 // One block: fresh pages for the rows that want one, lowest first in the order of the rows.
-__global__ void __launch_bounds__(kScanThreads) fork_alloc_kernel(const TableArgs a, const int32_t *src,
-                                                                  const int32_t *len, const int32_t *pend,
-                                                                  int32_t *row_of, int32_t *list, Move *moves,
-                                                                  int32_t *n_moves) {
-    __shared__ ScanSmem sm;
+__device__ __forceinline__ void fork_alloc(ScanSmem &sm, const TableArgs &a, const int32_t *src, const int32_t *len,
+                                           const int32_t *pend, int32_t *row_of, int32_t *list, Move *moves,
+                                           int32_t *n_moves) {
     int want = 0;
     for (int64_t base = 0; base < a.B; base += kScanItems * kScanThreads)
         want = scan_step(
@@ -308,6 +326,50 @@ __global__ void __launch_bounds__(kScanThreads) fork_alloc_kernel(const TableArg
     if (threadIdx.x == 0) *n_moves = want;
 }
 
+__global__ void __launch_bounds__(kScanThreads) fork_alloc_kernel(const TableArgs a, const int32_t *src,
+                                                                  const int32_t *len, const int32_t *pend,
+                                                                  int32_t *row_of, int32_t *list, Move *moves,
+                                                                  int32_t *n_moves) {
+    __shared__ ScanSmem sm;
+    let_next_start();
+    wait_for_previous();
+    fork_alloc(sm, a, src, len, pend, row_of, list, moves, n_moves);
+}
+
+// All of that for small tables by one cluster, whose barriers order the counts' copy, the rows and
+// the fresh pages: one launch instead of three.  A warp per 32 entries of a row.
+__global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kScanThreads)
+    fork_plan_kernel(const TableArgs a, const int32_t *src, const int32_t *len, int32_t *pend, int32_t *row_of,
+                     int32_t *list, Move *moves, int32_t *n_moves) {
+    __shared__ ScanSmem sm;
+    let_next_start();
+    const int lane = threadIdx.x & 31;
+    const int t = static_cast<int>(blockIdx.x) * kScanThreads + static_cast<int>(threadIdx.x);
+    auto cluster_sync = [] {
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    };
+    if (a.ref != a.out_ref) {
+        for (int p = t; p < a.n_pages; p += kForkCtas * kScanThreads) a.out_ref[p] = a.ref[p];
+        cluster_sync();
+    }
+    const int parts = (a.width + 31) / 32;
+    for (int u = t >> 5; u < a.B * parts; u += kForkCtas * kScanWarps) {
+        const int i = u / parts, j = u % parts * 32 + lane;
+        int s, n;
+        const bool ok = fork_source(a, src, len, i, s, n);
+        if (!ok && j == 0) atomicOr(&g_pages_err, kErrBadPosition);
+        const int part = n % a.ps, last = n / a.ps, used = last + (part ? 1 : 0);
+        int other = 0;  // (a lower row that continues s keeps its last page)
+        if (s >= 0 && part)
+            for (int k = lane; k < i && !other; k += 32) other = src[k] == s;
+        const bool copies = __any_sync(0xffffffffu, other != 0);
+        if (j == 0) pend[i] = copies ? 1 : 0;
+        if (j < a.width) fork_entry(a, i, j, s, used, last, copies);
+    }
+    cluster_sync();
+    if (blockIdx.x == 0) fork_alloc(sm, a, src, len, pend, row_of, list, moves, n_moves);
+}
+
 // ---------------------------------------------------------------------------------------------
 // compact
 // ---------------------------------------------------------------------------------------------
@@ -317,6 +379,7 @@ __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const TableA
                                                                     int32_t *to, Move *moves, int32_t *n_moves,
                                                                     int32_t *n_live) {
     __shared__ ScanSmem sm;
+    let_next_start();
     int live = 0;
     for (int64_t base = 0; base < a.n_pages; base += kScanItems * kScanThreads)
         live = scan_step(sm, base, a.n_pages, live, [&](int p) { return a.ref[p] > 0; }, [](int, int) {});
@@ -345,10 +408,14 @@ __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const TableA
 
 // Tables and counts after the moves.  Each count is written by one thread, from values that no
 // other thread writes (a hole's from its move), so the call may be in place.
-__global__ void __launch_bounds__(kThreads) compact_apply_kernel(const TableArgs a, const int32_t *to,
-                                                                 const Move *moves, const int32_t *n_moves,
-                                                                 const int32_t *n_live) {
-    const int nm = *n_moves, live = *n_live;
+struct ApplyArgs {
+    TableArgs t;
+    const int32_t *to, *n_live;
+};
+__device__ __forceinline__ void compact_apply(const ApplyArgs &x, const Move *moves, int nm) {
+    const TableArgs &a = x.t;
+    const int32_t *to = x.to;
+    const int live = *x.n_live;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
     for (int64_t x = t0; x < static_cast<int64_t>(a.B) * a.width; x += step) {
@@ -374,12 +441,22 @@ struct PoolArgs {
     int L, H, n_pages, ps, row;  // row: pieces of one position
 };
 
-// A warp per (move, layer, keys or values, head): rows * row consecutive pieces of both pages.
-template <bool kPairs>
+// What a copy's moves come from: a list of pairs, or a fork's or a compaction's plan (with the latter
+// the tables and counts change in the same kernel: 24 rows on 700 pages 18.7 -> 15.5 us).
+enum class Moves { kPairs, kFork, kCompact };
+
+// A warp per (move, layer, keys or values, head): rows * row consecutive pieces of both pages.  (A
+// warp per 4 KB of them was no faster: forking 400 rows of head dim 256 95 against 96 us,
+// compacting 4001 pages 324 against 329 us.)
+template <Moves kWhich>
 __global__ void __launch_bounds__(kThreads) move_kernel(const PoolArgs a, const Move *moves, const int32_t *n_moves,
-                                                        const int32_t *src, const int32_t *dst, int n_pairs) {
+                                                        const int32_t *src, const int32_t *dst, int n_pairs,
+                                                        const ApplyArgs apply) {
+    constexpr bool kPairs = kWhich == Moves::kPairs;
+    if constexpr (!kPairs) wait_for_previous();
     const int lane = threadIdx.x & 31;
     const int n = kPairs ? n_pairs : *n_moves;
+    if constexpr (kWhich == Moves::kCompact) compact_apply(apply, moves, n);
     const int inner = a.L * 2 * a.H;
     const int64_t units = static_cast<int64_t>(n) * inner;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
@@ -393,7 +470,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const PoolArgs a, const 
             continue;
         }
         const int64_t head = static_cast<int64_t>(a.ps) * a.row, page = head * a.H;
-        uint4 *base = a.pool[kv] + l * a.layer_stride + h * head;
+        uint4 *base = (kv ? a.pool[1] : a.pool[0]) + l * a.layer_stride + h * head;
         const uint4 *s = base + m.src * page;
         uint4 *d = base + m.dst * page;
         const int pieces = m.rows * a.row;
@@ -454,11 +531,13 @@ cudaError_t copy_ref(const TableArgs &a, cudaStream_t s) {
     copy_i32_kernel<<<grid_for(a.n_pages, 8), kThreads, 0, s>>>(a.ref, a.out_ref, a.n_pages);
     return cudaGetLastError();
 }
-cudaError_t launch_moves(const swa_page_pool *p, const PagesWs &w, int64_t most, cudaStream_t s) {
+template <Moves kWhich>
+cudaError_t launch_moves(const swa_page_pool *p, const PagesWs &w, int64_t most, const ApplyArgs &apply,
+                         cudaStream_t s) {
     const PoolArgs a = pool_args(p);
     const int64_t units = most * a.L * 2 * a.H;
-    move_kernel<false><<<grid_for(units * 32, 8), kThreads, 0, s>>>(a, w.moves, w.count, nullptr, nullptr, 0);
-    return cudaGetLastError();
+    return launch_dependent(true, move_kernel<kWhich>, dim3(grid_for(units * 32, 8)), kThreads, 0, s, a, w.moves,
+                            w.count, nullptr, nullptr, 0, apply);
 }
 
 }  // namespace
@@ -479,22 +558,30 @@ cudaError_t launch_free(const swa_page_tables *t, const int32_t *below, int n_si
     const TableArgs a = table_args(t);
     cudaError_t e = copy_ref(a, s);
     if (e != cudaSuccess) return e;
-    free_kernel<<<grid_for(static_cast<int64_t>(a.B) * a.width, 8), kThreads, 0, s>>>(a, below, n_sink);
-    return cudaGetLastError();
+    const int64_t n = static_cast<int64_t>(a.B) * a.width;
+    return launch_dependent(a.ref != a.out_ref, free_kernel, dim3(grid_for(n, 8)), kThreads, 0, s, a, below, n_sink);
 }
 
 cudaError_t launch_fork(const swa_page_tables *t, const swa_page_pool *pool, const int32_t *src, const int32_t *len,
                         void *ws, cudaStream_t s) {
     const TableArgs a = table_args(t);
     const PagesWs w = carve(t, ws);
-    cudaError_t e = copy_ref(a, s);
-    if (e != cudaSuccess) return e;
-    const int gx = (a.width + kThreads - 1) / kThreads;
-    fork_table_kernel<<<dim3(gx < 64 ? gx : 64, a.B < 65535 ? a.B : 65535), kThreads, 0, s>>>(a, src, len, w.rows0);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    fork_alloc_kernel<<<1, kScanThreads, 0, s>>>(a, src, len, w.rows0, w.rows1, w.list0, w.moves, w.count);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_moves(pool, w, a.B, s);
+    cudaError_t e;
+    if (static_cast<int64_t>(a.B) * a.width + a.n_pages <= kFew) {
+        fork_plan_kernel<<<kForkCtas, kScanThreads, 0, s>>>(a, src, len, w.rows0, w.rows1, w.list0, w.moves, w.count);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    } else {
+        if ((e = copy_ref(a, s)) != cudaSuccess) return e;
+        const int gx = (a.width + kThreads - 1) / kThreads;
+        const dim3 grid(gx < 64 ? gx : 64, a.B < 65535 ? a.B : 65535);
+        if ((e = launch_dependent(a.ref != a.out_ref, fork_table_kernel, grid, kThreads, 0, s, a, src, len, w.rows0)) !=
+            cudaSuccess)
+            return e;
+        if ((e = launch_dependent(true, fork_alloc_kernel, dim3(1), kScanThreads, 0, s, a, src, len, w.rows0, w.rows1,
+                                  w.list0, w.moves, w.count)) != cudaSuccess)
+            return e;
+    }
+    return launch_moves<Moves::kFork>(pool, w, a.B, ApplyArgs{}, s);
 }
 
 cudaError_t launch_compact(const swa_page_tables *t, const swa_page_pool *pool, int32_t *n_live, void *ws,
@@ -504,18 +591,17 @@ cudaError_t launch_compact(const swa_page_tables *t, const swa_page_pool *pool, 
     compact_plan_kernel<<<1, kScanThreads, 0, s>>>(a, w.list0, w.list1, w.list2, w.moves, w.count, n_live);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    // (as many warps as the moves and the table's entries want)
     const int64_t entries = static_cast<int64_t>(a.B) * a.width;
-    compact_apply_kernel<<<grid_for(entries > a.n_pages ? entries : a.n_pages, 8), kThreads, 0, s>>>(
-        a, w.list2, w.moves, w.count, n_live);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_moves(pool, w, a.n_pages / 2 + 1, s);
+    const int64_t most = a.n_pages / 2 + 1 + entries / (32 * 2 * pool->H_kv);
+    return launch_moves<Moves::kCompact>(pool, w, most, ApplyArgs{a, w.list2, n_live}, s);
 }
 
 cudaError_t launch_page_copy(const swa_page_pool *pool, const int32_t *src, const int32_t *dst, int n,
                              cudaStream_t s) {
     const PoolArgs a = pool_args(pool);
     const int64_t units = static_cast<int64_t>(n) * a.L * 2 * a.H;
-    move_kernel<true><<<grid_for(units * 32, 8), kThreads, 0, s>>>(a, nullptr, nullptr, src, dst, n);
+    move_kernel<Moves::kPairs><<<grid_for(units * 32, 8), kThreads, 0, s>>>(a, nullptr, nullptr, src, dst, n, ApplyArgs{});
     return cudaGetLastError();
 }
 
