@@ -29,7 +29,9 @@
 // Head dim <= 128, a unit of one query tile: the warpgroups share it and take its key tiles in turn,
 //   each with its own S, O, maximum and sum, which meet in the epilogue.  With one warpgroup
 //   alone S(j + 1) could not start before P(j) was used up.
-// NQT = 1 (head dim 256): one query tile, S double-buffered, TMEM S0 | S1 | Q | O.
+// NQT = 1 (head dim 256): one query tile, S double-buffered, TMEM S0 | S1 | Q | O.  The other
+//   warpgroup has the epilogues, so that the next piece's first tiles need not wait for them
+//   (16384 tokens, window 1024: 223 us, 272 with the epilogues in the softmax warpgroup).
 // A unit that several CTAs share: each writes its piece's unnormalised result, and the last to do so
 // joins them, while the others work on.  (A kernel of its own for that cost 8 to 19 us.)
 // Rows of V past the sequence's end may hold anything (even NaN): the warpgroup that turns the
@@ -67,18 +69,18 @@ struct TileCfg {
     static constexpr int NQT = D <= 128 ? 2 : 1;    // softmax warpgroups
     static constexpr bool kPairs = D == 128;        // units of two query tiles, too
     static constexpr int BN = D == 256 ? 64 : 128;  // keys per K/V tile
-    // NQT = 2: twelve warps put three on each SM sub-partition, whose 16K-register file caps the
-    // launch at 168 registers a thread; setmaxnreg then moves registers from warpgroup 0 (104) to
-    // the softmax warpgroups (200): 128 * 104 + 256 * 200 = 64512 = 384 * 168.
-    static constexpr int THREADS = NQT == 2 ? 384 : 256;
+    // Twelve warps put three on each SM sub-partition, whose 16K-register file caps the launch at
+    // 168 registers a thread; setmaxnreg then moves registers from warpgroup 0 (104) to the other
+    // two (200): 128 * 104 + 256 * 200 = 64512 = 384 * 168.
+    static constexpr int THREADS = 384;
     static constexpr int SOFTMAX_WARP0 = 4;
     static constexpr int REG_CTRL = 104, REG_SOFTMAX = 200;
-    static_assert(NQT == 1 || 128 * REG_CTRL + 256 * REG_SOFTMAX <= THREADS * 168, "register split");
+    static_assert(128 * REG_CTRL + 256 * REG_SOFTMAX <= THREADS * 168, "register split");
     static constexpr int QBYTES = BM * D * 2;  // one query tile
     static constexpr int TBYTES = BN * D * 2;  // one K or V tile
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = NQT == 2 ? NQT * QBYTES : 0;
-    static constexpr int XBYTES = NQT == 2 ? 2 * BM * 8 : 0;  // (max, sum) of both warpgroups' rows
+    static constexpr int XBYTES = NQT * BM * 8;  // (max, sum) of the softmax warpgroups' rows
     static constexpr int NSLOT_RAW = (232448 - 512 - XBYTES - OFF_RING) / TBYTES;
     // K/V ring.  At head dim 256 the query tile, which the MMAs read from tensor memory, passes
     // through it as two fills of its own instead of holding two slots' worth of shared memory:
@@ -205,10 +207,10 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         }
         for (int i = 0; i < C::NP; ++i) {
             mbar_init(bar_piece(i), 1);
-            // the roles' warps: producers, MMA, softmax and (two query tiles) the query loader
-            mbar_init(bar_used(i), 2 + NQT + 4 * NQT);
+            // the roles' warps: producers, MMA, softmax, epilogue and (two query tiles) the query loader
+            mbar_init(bar_used(i), 2 + NQT + 8);
         }
-        mbar_init(bar_meet, 8);
+        mbar_init(bar_meet, 4 * NQT);
         mbar_init(bar_drain, 1);
         fence_mbar_init();
     }
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
 
     if (warp == 0 || warp == 2) {
         // ============================ K/V producers ============================
-        if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
+        regs_dec<C::REG_CTRL>();
         // the scratch of the work split lies in the ring: order its generic accesses before the copies
         fence_proxy_async_smem();
         asm volatile("griddepcontrol.wait;" ::: "memory");  // (the append before this kernel has stored its rows)
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 if ((mine >> i2) & 1u) mbar_drain(bar_full(i2), (mine_phase >> i2) & 1u, &g_ptile_err);
     } else if (warp == 1) {
         // ============================ MMA issuer ============================
-        if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
+        regs_dec<C::REG_CTRL>();
         constexpr uint32_t idS = idesc_bf16_f32(BM, BN, false, false);
         constexpr uint32_t idPV = idesc_bf16_f32(BM, D, false, true);
         bool ok = true, was_single = false, both = false;
@@ -545,12 +547,15 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         __syncwarp();
     } else if (warp >= C::SOFTMAX_WARP0) {
         // ============================ softmax / epilogue ============================
-        if constexpr (NQT == 2) regs_inc<C::REG_SOFTMAX>();
+        regs_inc<C::REG_SOFTMAX>();
         const int wg = (warp - C::SOFTMAX_WARP0) >> 2;
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;  // row == TMEM lane
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t o_addr = tmem + lane_addr + C::tm_o(wg);
+        // head dim 256: warpgroup 0 has the softmax, warpgroup 1 the epilogues; else each has both
+        const bool takes_tiles = NQT == 2 || wg == 0;
+        const int ow = NQT == 2 ? wg : 0;
+        const uint32_t o_addr = tmem + lane_addr + C::tm_o(ow);
         float2 *meet = reinterpret_cast<float2 *>(sgen + C::OFF_X);
         bool ok = true;
         int J = 0, k = 0, y = 1;  // y: as the MMA warp's
@@ -561,7 +566,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             if (!wk) break;
             const int n = wk->j1 - wk->j0;
             const bool single = is_single(wk->n, wk->ut);
-            const int t = wk->p0 + wk->ut * TT + (single ? 0 : wg * ta.TQ) + r / a.G;  // this row's position
+            const int t = wk->p0 + wk->ut * TT + (single ? 0 : ow * ta.TQ) + r / a.G;  // this row's position
             // the tile's first position, and the first key that its last row's window keeps
             const int tlo = t - r / a.G;
             const int thi = min(tlo + ta.TQ, max(wk->p0 + wk->n, tlo + 1)) - 1;
@@ -580,7 +585,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             const bool idle = __all_sync(0xffffffffu, (r / a.G >= ta.TQ) || t >= wk->p0 + wk->n);
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-            for (int i = single ? wg : 0; i < n; i += single ? 2 : 1) {
+            for (int i = takes_tiles ? (single ? wg : 0) : n; i < n; i += single ? 2 : 1) {
                 const int g = J + i;
                 const int slot = C::NS == 3 ? g % 3 : NQT == 2 ? wg : (g & 1);
                 const uint32_t parity = C::NS == 3 ? (g / 3) & 1 : NQT == 2 ? (ns & 1) : ((g >> 1) & 1);
@@ -739,9 +744,30 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 if (lane == 0) mbar_arrive(bar_pf(slot));
             }
             if (!ok) break;
+            if constexpr (NQT == 1) {
+                // the rows' maxima and sums to the epilogue warpgroup, once it has read the last piece's
+                if (takes_tiles) {
+                    if (k > 0 && !warp_wait(bar_of(0), (k - 1) & 1, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    meet[r] = make_float2(m, l);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_meet);
+                    give_back(k);
+                    J += n;
+                    continue;
+                }
+                if (!warp_wait(bar_meet, k & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                m = meet[r].x;
+                l = meet[r].y;
+            }
 
             // ---- epilogue: O is final once the piece's last P V completes
-            if (!warp_wait(bar_od(wg), k & 1, abort) || (single && !warp_wait(bar_od(wg ^ 1), k & 1, abort))) {
+            if (!warp_wait(bar_od(ow), k & 1, abort) || (single && !warp_wait(bar_od(wg ^ 1), k & 1, abort))) {
                 ok = false;
                 break;
             }
@@ -775,14 +801,14 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             const float inv_l = whole ? 1.f / l : 1.f;  // (of a whole unit: every row keeps its own key)
             wa *= inv_l;
             wb *= inv_l;
-            const int tq = r / a.G, i0 = wk->ut * TT + (single ? 0 : wg * ta.TQ);  // the tile's first token
+            const int tq = r / a.G, i0 = wk->ut * TT + (single ? 0 : ow * ta.TQ);  // the tile's first token
             const int64_t tok = static_cast<int64_t>(wk->q0) + i0 + tq;
             const int h = wk->kvh * a.G + r % a.G;
             const bool store = tq < min(wk->n - i0, ta.TQ) && SWA_IN_BOUNDS(tok < a.N && h < a.H_q, &g_ptile_err);
             uint16_t *orow = a.o + tok * a.o_st[0] + h * a.o_st[1];
-            const int pslot = wk->slot, prow = (single ? 0 : wg * BM) + r;
+            const int pslot = wk->slot, prow = (single ? 0 : ow * BM) + r;
             // (a shared query tile: each warpgroup keeps the maximum and sum beside its half of the columns)
-            const int mrow = wg * BM + r;
+            const int mrow = ow * BM + r;
             auto ml_at = [&](int slot) {
                 return reinterpret_cast<float2 *>(ta.ws.ml + (static_cast<int64_t>(slot) * (NQT * BM) + mrow) * 2);
             };
@@ -792,7 +818,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             for (int c = idle ? c1 : c0; c < c1; ++c) {
                 __syncwarp();  // tcgen05.ld is executed by the converged warp: lanes that store come back here
                 uint32_t ov[32];
-                tmem_ld32(tmem + lane_addr + C::tm_o(single ? 0 : wg) + c * 32, ov);
+                tmem_ld32(tmem + lane_addr + C::tm_o(single ? 0 : ow) + c * 32, ov);
                 tc_wait_ld();
                 float f[32];
 #pragma unroll
@@ -819,7 +845,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             // O has been read out: the next piece's first P V may overwrite it
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_of(wg));
+            if (lane == 0) mbar_arrive(bar_of(ow));
             bool joined = false;
             if (!whole) {
                 // The piece is written.  Warps of the same place have the same rows and columns of it in
@@ -830,7 +856,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 __syncwarp();
                 const int owner = wk->owner;
                 int before = 0;
-                if (lane == 0) before = atomicAdd(ta.ws.done + owner * 8 + wg * 4 + quarter, 1);
+                if (lane == 0) before = atomicAdd(ta.ws.done + owner * 8 + ow * 4 + quarter, 1);
                 before = __shfl_sync(0xffffffffu, before, 0);
                 joined = before == unit_pieces - 1;
                 if (joined) {
@@ -893,7 +919,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     }
                 }
             }
-            if (store && (!single || wg == 0) && (whole || joined)) {
+            if (store && (!single || ow == 0) && (whole || joined)) {
                 a.lse[tok * a.H_q + h] = (m + log2f(l)) * 0.69314718055994531f;
                 if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, t);
             }
@@ -902,7 +928,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         }
     } else {
         // ============================ planner ============================
-        if constexpr (NQT == 2) regs_dec<C::REG_CTRL>();
+        regs_dec<C::REG_CTRL>();
         const Share sh = *share;
         const int grid = static_cast<int>(gridDim.x);
         bool ok = true;
