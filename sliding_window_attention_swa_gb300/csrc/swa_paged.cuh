@@ -221,8 +221,9 @@ __device__ __forceinline__ Place find_tile(const PagedArgs &a, int TT, const lon
 
 constexpr int kMaxWaveCtas = 256;
 constexpr int kJoinTiles = 12;
-// Scratch of find_share: tiles [B] (64 bits), first units [B + 1], loads [2][CTAs].
-constexpr int kShareScratch = kPagedMaxB * 12 + 4 + 2 * kMaxWaveCtas * 4;
+// Scratch of find_share: tiles [B] (64 bits), first units [B + 1], and with waves loads [2][CTAs].
+__host__ __device__ constexpr int share_scratch(int B) { return B * 12 + 4; }
+constexpr int kShareScratch = share_scratch(kPagedMaxB) + 2 * kMaxWaveCtas * 4;
 
 // The CTA that unit u of the list goes to, in wave u / grid.
 __device__ __forceinline__ int dealt_to(int u, int grid) {

@@ -50,7 +50,11 @@ struct SplitCfg {
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 1024;
     static_assert(NST >= 2, "ring too shallow");
     static_assert(SMEM * CTAS_PER_SM <= 232448, "shared memory budget");
-    static_assert(OFF_RED >= kPagedMaxB * 8, "scratch of the work split");
+    // The scratch of the work split lies in the ring and the combine buffer, or, for more sequences
+    // than they have room for (5631 at head dim 64), behind everything else.
+    static constexpr int scratch_off(int B) { return share_scratch(B) <= OFF_RED ? 0 : SMEM - 1024; }
+    static constexpr int smem(int B) { return share_scratch(B) <= OFF_RED ? SMEM : SMEM + share_scratch(B); }
+    static_assert(SMEM % 8 == 0 && smem(kPagedMaxB) <= 232448, "scratch of the work split");
 };
 
 // Offset of 16-byte piece `pc` of row `row` in a 128B-swizzled tile (layout of paged_pool_map).
@@ -63,7 +67,8 @@ __device__ __forceinline__ uint32_t sw128(int row, int pc) {
 template <int D>
 __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::CTAS_PER_SM == 2 ? 168 : 255)
     paged_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const PagedArgs a, const PagedWs ws, const int TT, const int min_tiles, const int fault_stop) {
+                       const PagedArgs a, const PagedWs ws, const int TT, const int min_tiles, const int scratch_off,
+                       const int fault_stop) {
     using C = SplitCfg<D>;
     constexpr int NST = C::NST;
     extern __shared__ uint8_t smem_raw[];
@@ -97,7 +102,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
         tma_prefetch_desc(&tm_v);
     }
     // (its block barriers also publish the mbarriers)
-    find_share<CH, kThreads, false>(a, TT, min_tiles, sgen, &share, &g_psplit_data);
+    find_share<CH, kThreads, false>(a, TT, min_tiles, sgen + scratch_off, &share, &g_psplit_data);
     volatile int *abort = &abort_flag;
     // the merge grid may be scheduled from here on: its blocks wait (griddepcontrol.wait)
     // for this grid to complete before they read the partials
@@ -490,7 +495,8 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cu
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) dev = -1;
     if (dev < 0 || !configured[dev].load(std::memory_order_acquire)) {
-        cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             C::smem(kPagedMaxB));
         if (e != cudaSuccess) return e;
         if (dev >= 0) configured[dev].store(true, std::memory_order_release);
     }
@@ -499,8 +505,8 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cu
     if (!paged_pool_map(&mk, a, a.k_pages, rows) || !paged_pool_map(&mv, a, a.v_pages, rows))
         return cudaErrorInvalidValue;
     const PagedShape x = paged_split_shape(a);
-    return launch_dependent(after_append, paged_split_kernel<D>, dim3(x.ctas), kThreads, C::SMEM, s, mk, mv, a, w, x.TQ,
-                            kMinTiles, fault_plan().split_stop_stage);
+    return launch_dependent(after_append, paged_split_kernel<D>, dim3(x.ctas), kThreads, C::smem(a.B), s, mk, mv, a, w,
+                            x.TQ, kMinTiles, C::scratch_off(a.B), fault_plan().split_stop_stage);
 }
 
 }  // namespace

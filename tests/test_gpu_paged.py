@@ -103,6 +103,21 @@ def test_long_histories_and_many_sequences(swa, seqs):
         run(swa, R.Batch(6, seqs, 4, 1, D, ps), max_q=max(n for _, n in seqs))
 
 
+def test_as_many_sequences_as_a_call_takes(swa):
+    seqs = [(i % 40, 1 if i % 31 == 0 else 0) for i in range(8192)]
+    seqs[77] = (1000, 200)
+    run(swa, R.Batch(8, seqs, 2, 1, 64, 16, 20, 1))
+    k = torch.zeros(1, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+    table, p0 = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in ((8193, 1), 8193))
+    with pytest.raises(swa.SwaError):
+        swa.swa_paged_attend(torch.zeros(8193, 1, 64, dtype=torch.bfloat16, device="cuda"), k, k.clone(), table, p0)
+    # one token a sequence
+    o, lse, _ = swa.swa_paged_attend(torch.ones(8192, 1, 64, dtype=torch.bfloat16, device="cuda"), k, k.clone(),
+                                     table[:8192], p0[:8192])
+    swa.swa_check_device_error()
+    assert (o == 0).all() and (lse == 0).all()  # one key, its score 0
+
+
 @pytest.mark.parametrize("heads", [(16, 1, 128), (16, 1, 64), (16, 1, 256)], ids=str)
 def test_more_units_than_two_waves(swa, heads):
     # whole units dealt to the CTAs first: one long chunk, a batch of many, one whose first units are
