@@ -292,7 +292,7 @@ SWA_API swa_status swa_prefill_chunk(const swa_chunk_params *p, const swa_cache_
  *   k_pages, v_pages  bf16 [n_pages, H_kv, page_size, d_h], contiguous
  *   page_table        int32 [B, table_width], contiguous
  * Requirements: d_h in {64, 128, 256}; page_size in {16, 32, 64, 128}; B <= 8192;
- * table_width * page_size < 2^31; (n_pages + 1) * H_kv * page_size / 8 < 2^31; pointers 16-byte
+ * table_width * page_size <= 2^30; (n_pages + 1) * H_kv * page_size / 8 < 2^31; pointers 16-byte
  * aligned (page_table: 4-byte).
  */
 typedef struct swa_paged_cache {
@@ -322,8 +322,10 @@ typedef struct swa_paged_cache {
  *   max_q        the most new tokens of one sequence, as far as the caller knows (0: not
  *                known).  It chooses between kernels for few and for many rows; results are
  *                right whatever it says.
- * The cache must hold every position that a query keeps; the rows of a page at or past its
- * sequence's end (p0 + its new tokens) may hold anything.  What the device finds broken is
+ * The cache must hold every position that a query keeps, in finite numbers (a position that some
+ * queries of a sequence keep and others do not shows in the others if it is not finite); what
+ * no query of the sequence keeps -- between the sinks and its first new token's window, at or
+ * past its end (p0 + its new tokens) -- may hold anything.  What the device finds broken is
  * reported by swa_check_device_error as SWA_ERR_INVALID_ARG, and nothing outside the call's
  * buffers is read or written: a sequence whose q_start or p0 is out of range or that does
  * not fit its table row is skipped, its rows left as they were (SWA_DEVERR_BAD_POSITION); a

@@ -254,7 +254,8 @@ swa_status paged_cache_check(const swa_paged_cache *c) {
     if (!head_dim_ok(c->d_h)) return SWA_ERR_UNSUPPORTED;
     if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
         return SWA_ERR_UNSUPPORTED;
-    if (c->B > swa::kPagedMaxB || static_cast<int64_t>(c->table_width) * c->page_size > INT_MAX)
+    // (the kernels round positions up to whole tiles in 32 bits)
+    if (c->B > swa::kPagedMaxB || static_cast<int64_t>(c->table_width) * c->page_size > (1 << 30))
         return SWA_ERR_UNSUPPORTED;
     // the kernels count the pool's groups of 8 rows, and one page more, in 32 bits
     if ((static_cast<int64_t>(c->n_pages) + 1) * c->H_kv > INT_MAX / (c->page_size / 8)) return SWA_ERR_UNSUPPORTED;

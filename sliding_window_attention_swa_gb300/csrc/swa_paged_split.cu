@@ -232,12 +232,13 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
                 if (k0 <= t1 && (k0 + 15 >= lo_first || k0 < a.n_sink)) {
                     const uint32_t ks = sbase + C::OFF_RING + st * C::STAGE;
                     const uint32_t vs = ks + C::STAGE / 2;
-                    if (k0 + 15 >= end) {
-                        // zero the value rows past the sequence's end
+                    if (k0 + 15 >= end || (k0 < lo_first && k0 + 15 >= a.n_sink)) {
+                        // zero the value rows that no row keeps: past the sequence's end, or between the
+                        // sinks and the window (they may hold anything, even NaN)
                         uint8_t *vg = sgen + C::OFF_RING + st * C::STAGE + C::STAGE / 2;
                         for (int idx = lane; idx < 16 * (D / 8); idx += 32) {
                             const int rr = idx / (D / 8), pc = idx % (D / 8);
-                            if (k0 + rr >= end)
+                            if (k0 + rr >= end || (k0 + rr < lo_first && k0 + rr >= a.n_sink))
                                 *reinterpret_cast<uint4 *>(vg + sw128<D>(16 * w + rr, pc)) = make_uint4(0, 0, 0, 0);
                         }
                         __syncwarp();

@@ -9,8 +9,8 @@
 // Roles:
 //   warps 0, 2    producers of the keys and of the values: K_0, V_0, K_1, V_1, ... of every piece into
 //                 a ring of NSLOT shared-memory slots by TMA, one copy per page (or part of one), one
-//                 lane each; the pages are looked up 32 copies ahead.  Pages past the sequence's end
-//                 or not there read past the pool: zeros.  Two warps, since a copy takes 77 cycles of
+//                 lane each; the pages are looked up 32 copies ahead.  Pages that no row keeps a key
+//                 of, or that are not there, read past the pool: zeros.  Two warps, since a copy takes 77 cycles of
 //                 the warp that issues it and a tile on pages of 16 is 16 of them.  Every fill has
 //                 its own arrival and its own release.
 //   warp 1        TMEM owner and MMA issuer (warp-uniform loop, one elected lane issues):
@@ -34,8 +34,10 @@
 //   (16384 tokens, window 1024: 223 us, 272 with the epilogues in the softmax warpgroup).
 // A unit that several CTAs share: each writes its piece's unnormalised result, and the last to do so
 // joins them, while the others work on.  (A kernel of its own for that cost 8 to 19 us.)
-// Rows of V past the sequence's end may hold anything (even NaN): the warpgroup that turns the
-// last tile's scores into P zeroes them in shared memory before it hands P over.
+// Rows of V that no query of the sequence keeps -- past its end, or between the sinks and the
+// window of its first new token -- may hold anything (even NaN, which a weight of zero does not take
+// out): the warpgroup that turns such a tile's scores into P zeroes them in shared memory before
+// it hands P over.
 // Bound by the tensor cores and the exponentials for full units over long histories, by HBM for
 // units of few rows.
 // Every wait is bounded; on expiry the CTA records an error word, drains its copies and MMAs,
@@ -335,7 +337,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 now = then;
                 if (looked < cta_tiles) then = look_up();
                 at = 0;
-                const bool in_pool = static_cast<unsigned>(now.entry) < static_cast<unsigned>(a.n_pages);
+                // (a box that no row keeps a key of comes as zeros)
+                const bool in_pool = now.need && static_cast<unsigned>(now.entry) < static_cast<unsigned>(a.n_pages);
                 if (now.need && !in_pool) atomicOr(&g_ptile_data, SWA_DEVERR_BAD_PAGE);
                 // debug build: the box lies in the page, the head exists
                 (void)SWA_IN_BOUNDS(now.row + box <= a.ps && now.kvh < a.H_kv, &g_ptile_err);
@@ -570,13 +573,16 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             // the tile's first position, and the first key that its last row's window keeps
             const int tlo = t - r / a.G;
             const int thi = min(tlo + ta.TQ, max(wk->p0 + wk->n, tlo + 1)) - 1;
-            // tiles [ia, ib) of the piece lie in every row's window; iz is the one the sequence ends in
-            int ia, ib, iz;
+            // tiles [ia, ib) of the piece lie in every row's window; iz is the one the sequence ends in, iw
+            // the first of the window if in it or in the one before are keys that no query keeps
+            int ia, ib, iz, iw;
             {
                 const int lo_thi = thi >= a.window ? thi - a.window + 1 : 0;
                 const int first = wk->sink - wk->j0 - wk->lo;  // index of tile x of the window: first + x
                 ia = max(first + wk->lo, first + (lo_thi + BN - 1) / BN);
                 ib = first + (tlo + 1) / BN;
+                const int lo_p0 = wk->p0 >= a.window ? wk->p0 - a.window + 1 : 0;
+                iw = lo_p0 > a.n_sink && (wk->sink > 0 || wk->lo * BN < lo_p0) ? wk->sink - wk->j0 : -8;
                 iz = !wk->open() && (wk->tile(n - 1) + 1) * BN > wk->p0 + wk->n ? n - 1 : -1;
             }
             // A warp without a row hands its P over as it finds it: rows of other warps do not see it,
@@ -589,6 +595,35 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 const int g = J + i;
                 const int slot = C::NS == 3 ? g % 3 : NQT == 2 ? wg : (g & 1);
                 const uint32_t parity = C::NS == 3 ? (g / 3) & 1 : NQT == 2 ? (ns & 1) : ((g >> 1) & 1);
+                if ((i == iz || static_cast<unsigned>(iw - i) <= 1u) && (NQT == 1 || single || wg == 0)) {
+                    // zero the value rows that no query keeps, in boxes that also hold others (the rest came as
+                    // zeros), while S is under way.  The first P V of the tile waits for this warpgroup's P, and
+                    // with two query tiles the second is issued after it.
+                    const int box = min(a.ps, BN), k0 = wk->tile(i) * BN, p0 = wk->p0, end = p0 + wk->n;
+                    const int lo = p0 >= a.window ? p0 - a.window + 1 : 0;
+                    const bool below = k0 < lo && k0 + BN > a.n_sink, past = k0 + BN > end;
+                    const int fv = kfill(k, g) + 1;
+                    if ((below || past) && !warp_wait(bar_full(fv % NSLOT), fphase(fv), abort)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *vt = sgen + C::OFF_RING + (fv % NSLOT) * C::TBYTES;
+                    auto zero = [&](int from, int to) {  // positions
+                        from = min(max(from - k0, 0), BN);
+                        to = min(to - k0, BN);
+                        for (int idx = r; idx < (to - from) * (D / 8); idx += BM) {
+                            const int row = from + idx / (D / 8), pc = idx % (D / 8);
+                            *reinterpret_cast<uint4 *>(vt + (row >> 3) * (D * 16) + (pc >> 3) * 1024 + (row & 7) * 128 +
+                                                       (((pc & 7) ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                        }
+                    };
+                    if (past) zero(end, (end + box - 1) & -box);
+                    if (below) {
+                        zero(a.n_sink, min(lo, (a.n_sink + box - 1) & -box));
+                        zero(max(a.n_sink, lo & -box), lo);
+                    }
+                    if (below || past) fence_proxy_async_smem();
+                }
                 if (!warp_wait(bar_sf(slot), parity, abort)) {
                     ok = false;
                     break;
@@ -719,25 +754,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     rsum = lo + hi;
                 }
                 l = l * alpha + rsum;
-                }
-                if (i == iz && (NQT == 1 || single || wg == 0)) {
-                    // the sequence ends in this tile: zero the value rows of its last page past the
-                    // end (later pages came as zeros).  The first P V of the tile waits for this
-                    // warpgroup's P, and with two query tiles the second is issued after it.
-                    const int fv = kfill(k, g) + 1;
-                    if (!warp_wait(bar_full(fv % NSLOT), fphase(fv), abort)) {
-                        ok = false;
-                        break;
-                    }
-                    const int box = min(a.ps, BN);
-                    const int z0 = wk->p0 + wk->n - wk->tile(i) * BN, z1 = min(BN, (z0 + box - 1) / box * box);
-                    uint8_t *vt = sgen + C::OFF_RING + (fv % NSLOT) * C::TBYTES;
-                    for (int idx = r; idx < (z1 - z0) * (D / 8); idx += BM) {
-                        const int row = z0 + idx / (D / 8), pc = idx % (D / 8);
-                        *reinterpret_cast<uint4 *>(vt + (row >> 3) * (D * 16) + (pc >> 3) * 1024 + (row & 7) * 128 +
-                                                   (((pc & 7) ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
                 }
                 tc_fence_before();
                 __syncwarp();

@@ -140,6 +140,24 @@ def test_shared_units_with_rows_missing(swa, heads):
             run(swa, R.Batch(14, [(p0, n), (100, 1)], Hq, Hkv, D, 32), append=n == 45)
 
 
+@pytest.mark.parametrize("hint", [0, 1])
+@pytest.mark.parametrize("case", [(8, 2, 128, 16, 100, 4), (16, 16, 128, 128, 130, 0), (4, 4, 64, 64, 300, 130),
+                                  (6, 2, 256, 32, 65, 37), (2, 1, 64, 128, 1, 1)], ids=str)
+def test_positions_that_no_query_keeps_may_hold_anything(swa, case, hint):
+    # rows between the sinks and the first new token's window, in pages that are there all the same
+    Hq, Hkv, D, ps, w, sinks = case
+    seqs = [(500, 1), (129, 1), (1000, 1), (0, 1)] if hint else [(500, 33), (129, 300), (1000, 1), (257, 140), (0, 9)]
+    if Hq == 16 and not hint:
+        seqs.append((600, 3000))  # (units of two query tiles)
+    x = R.Batch(51, seqs, Hq, Hkv, D, ps, w, sinks, freed=False)
+    for b, (p, _) in enumerate(seqs):
+        for t in range(sinks, p - w + 1):
+            page = int(x.table[b, t // ps])
+            x.k_pages[page, :, t % ps] = float("nan")
+            x.v_pages[page, :, t % ps] = float("inf") if t % 2 else float("nan")
+    run(swa, x, max_q=hint, q_start=None if hint else x.q_start.cuda())
+
+
 def test_values_of_the_extremes(swa):
     # scores of +-1000s: one key carries all the weight, and the running maximum jumps
     x = R.Batch(7, [(500, 70), (900, 1)], 8, 2, 128, 32)

@@ -57,6 +57,12 @@ def test_layouts_and_sizes(swa):
         PAGED.test_broken_device_data(swa, hint)
 
 
+@pytest.mark.parametrize("hint", [0, 1])
+def test_positions_that_no_query_keeps(swa, hint):
+    for case in ((16, 16, 128, 128, 130, 0), (4, 4, 64, 64, 300, 130), (6, 2, 256, 32, 65, 37)):
+        PAGED.test_positions_that_no_query_keeps_may_hold_anything(swa, case, hint)
+
+
 def test_pages(swa):
     PAGES.test_reserve_when_the_pool_runs_out(swa)
     PAGES.test_free(swa, 40, 90, 4000, 32, 0, True)

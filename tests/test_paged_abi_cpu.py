@@ -83,6 +83,7 @@ def pair(x, y):
     (lambda p, c: setattr(c, "page_size", 256), 2),
     (lambda p, c: setattr(c, "d_h", 96), 2),
     (lambda p, c: setattr(c, "table_width", 1 << 28), 2),   # positions past 2^31
+    (lambda p, c: setattr(c, "table_width", (1 << 30) // c.page_size + 1), 2),  # positions past 2^30
     (lambda p, c: setattr(c, "B", 8193), 2),
     (lambda p, c: setattr(c, "n_pages", 1 << 29), 2),       # 2^31 groups of eight rows
     (lambda p, c: setattr(c, "v_pages", FAKE + 4), 2),
