@@ -541,6 +541,7 @@ def swa_prefill_chunk(q, k_new, v_new, k_cache, v_cache, slot_pos, p0, window: i
 # The paged calls are made once a layer and step, so what they cost on the host counts: arguments
 # are packed in one go (the layouts of the structures above, without trailing padding), and
 # checks look at a tensor's device index, not at device objects.
+_paged_ws_size: dict = {}
 _PAGED_PARAMS = struct.Struct("5P8q5if3P")
 _PAGED_CACHE = struct.Struct("3P6i")
 _PAGE_TABLES = struct.Struct("4P4i")
@@ -658,7 +659,14 @@ def swa_paged_attend(q, k_pages, v_pages, page_table, p0, window: int = 0, scale
         int(max_q), int(window), int(n_sink), D ** -0.5 if scale is None else float(scale), o.data_ptr(),
         lse.data_ptr(), 0 if row_counts is None else row_counts.data_ptr())
     if workspace is None:
-        workspace = torch.empty(lib.swa_paged_workspace_size(params, cache) or 1, dtype=torch.uint8, device=device)
+        # (asked once for each of what it depends on: the question takes 2 us of a 24 us call)
+        key = lib._name, index, Hq, H_kv, d_h, max_q, q_start is None
+        size = _paged_ws_size.get(key)
+        if size is None:
+            size = lib.swa_paged_workspace_size(params, cache)
+            if size:  # (0: refused, below)
+                _paged_ws_size[key] = size
+        workspace = torch.empty(size or 1, dtype=torch.uint8, device=device)
     st = lib.swa_paged_attend(params, cache, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                               _raw_stream(stream, index))
     if st != 0:
