@@ -143,6 +143,12 @@ def test_fork(swa, B, most, shape):
         np.testing.assert_array_equal(R.bits(vd), wv)
 
 
+@pytest.mark.parametrize("B,most,ps", [(300, 400, 8), (9, 3000, 1), (1500, 20, 4)])
+def test_fork_of_a_large_table(swa, B, most, ps):
+    # tables and pools that the grids plan, instead of one cluster
+    test_fork(swa, B, most, (1, 1, ps, 8))
+
+
 def test_fork_refusals_and_broken_data(swa):
     k, v = (x.cuda() for x in pools(8, 1, 5, 1, 16, 8))
     t, r = R.i32([[0, 1], [2, -1], [3, 4]]), R.i32([1, 1, 1, 1, 1])
