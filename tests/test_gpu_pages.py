@@ -285,3 +285,54 @@ def test_serving_run(swa):
     swa.swa_pages_free(table, ref, R.i32([-1] * B), ps)
     swa.swa_check_device_error()
     assert (table == -1).all() and (ref == 0).all()
+
+
+@pytest.mark.parametrize("few", [True, False], ids=["single-tokens", "chunks"])
+def test_a_captured_step_is_the_called_one(swa, few):
+    """Reserve, append and attend, free, fork and compact as one graph, replayed: the tables, counts,
+    pages and rows are bit for bit those of the same calls made one by one."""
+    Hq, Hkv, D, ps, W, B, width, n_pages = 8, 2, 128, 16, 100, 6, 30, 220
+    n = 1 if few else 30
+    g = torch.Generator().manual_seed(13)
+    steps = [tuple(torch.randn(B * n, h, D, generator=g).to(torch.bfloat16).cuda() for h in (Hq, Hkv, Hkv))
+             for _ in range(6)]
+
+    def state():
+        z = dict(dtype=torch.int32, device="cuda")
+        s = dict(k=torch.zeros(n_pages, Hkv, ps, D, dtype=torch.bfloat16, device="cuda"),
+                 table=torch.full((B, width), -1, **z), ref=torch.zeros(n_pages, **z), p0=torch.zeros(B, **z),
+                 src=R.i32([0, 0, 2, 3, 3, 5]), start=R.i32([i * n for i in range(B + 1)]),
+                 new_table=torch.zeros(B, width, **z), live=torch.zeros(1, **z),
+                 o=torch.zeros(B * n, Hq, D, dtype=torch.bfloat16, device="cuda"), lse=torch.zeros(B * n, Hq, device="cuda"))
+        s["v"] = torch.zeros_like(s["k"])
+        s["q"], s["kn"], s["vn"] = (torch.zeros_like(x) for x in steps[0])
+        return s
+
+    def step(s):
+        end = s["p0"] + n
+        swa.swa_pages_reserve(s["table"], s["ref"], s["p0"], end, ps)
+        swa.swa_paged_attend(s["q"], s["k"], s["v"], s["table"], s["p0"], W, q_start=None if few else s["start"],
+                             k_new=s["kn"], v_new=s["vn"], o=s["o"], lse=s["lse"])
+        swa.swa_pages_free(s["table"], s["ref"], (end - W).clamp(min=0), ps, n_sink=1)
+        swa.swa_pages_fork(s["k"], s["v"], s["table"], s["ref"], s["src"], end, out_table=s["new_table"])
+        s["table"].copy_(s["new_table"])
+        swa.swa_pages_compact(s["k"], s["v"], s["table"], s["ref"], n_live=s["live"])
+        s["p0"].copy_(end)
+
+    a, b = state(), state()
+    step(state())  # (one-time setup before the capture)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(b)
+    for q, k, v in steps:
+        for s in (a, b):
+            for name, x in zip(("q", "kn", "vn"), (q, k, v)):
+                s[name].copy_(x)
+        step(a)
+        graph.replay()
+        swa.swa_check_device_error()
+        for name in ("table", "ref", "p0", "live", "lse"):
+            assert torch.equal(a[name], b[name]), name
+        for name in ("o", "k", "v"):
+            np.testing.assert_array_equal(R.bits(a[name]), R.bits(b[name]), err_msg=name)
