@@ -325,6 +325,17 @@ def test_captured_and_replayed(swa, hint):
             verify(x, o, lse, None)
 
 
+def test_one_workspace_for_many_calls(swa):
+    # whatever it holds: other calls' partial results and counters, of other shapes
+    ws = torch.full((96 << 20,), 255, dtype=torch.uint8, device="cuda")
+    xs = [R.Batch(45 + D, [(5000, 40), (9, 1), (700, 130)], 8, 2, D, 32) for D in (64, 128, 256)]
+    xs += [R.Batch(46 + D, [(5000, 1), (9, 1), (12000, 1)], 8, 2, D, 32) for D in (64, 128, 256)]
+    for turn in range(2):
+        for x in xs[::1 - 2 * turn]:
+            one = x.N == 3
+            run(swa, x, append=turn == 1, workspace=ws, q_start=None if one else x.q_start.cuda())
+
+
 def test_two_streams_at_once(swa):
     xs = [R.Batch(40 + i, [(3000, 70), (10, 1), (900, 200)], 8, 2, 128, 32, 1000) for i in range(4)]
     streams = [torch.cuda.Stream() for _ in range(2)]
