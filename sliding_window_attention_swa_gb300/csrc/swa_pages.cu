@@ -23,6 +23,9 @@ constexpr int kThreads = 256;
 constexpr int kScanThreads = 1024, kScanWarps = kScanThreads / 32;
 constexpr int kScanItems = 16;  // counts per thread and scan step: as many loads in flight
 constexpr int kUnroll = 8;      // 16-byte loads in flight per thread of the page copy
+// Blocks of the page copy per SM at most: blocks that come and go even out the end better than
+// few that stay (compacting 4001 pages 320 us with 8, 315 with 16, 312 with 64 or more).
+constexpr int kMoveBlocks = 64;
 constexpr int kForkCtas = 8;    // a cluster (the largest portable one)
 // Table entries and pages up to which one cluster plans a fork: one launch instead of three, which
 // a short call waits for (32 rows of 250 entries: a call 24 -> 19 us, though 13.1 -> 14.5 us on the
@@ -447,7 +450,8 @@ enum class Moves { kPairs, kFork, kCompact };
 
 // A warp per (move, layer, keys or values, head): rows * row consecutive pieces of both pages.  (A
 // warp per 4 KB of them was no faster: forking 400 rows of head dim 256 95 against 96 us,
-// compacting 4001 pages 324 against 329 us.)
+// compacting 4001 pages 324 against 329 us.)  Stores are marked as not to be read again, which
+// leaves L2 to pages that several copies read (those 400 rows 88 -> 84 us).
 template <Moves kWhich>
 __global__ void __launch_bounds__(kThreads) move_kernel(const PoolArgs a, const Move *moves, const int32_t *n_moves,
                                                         const int32_t *src, const int32_t *dst, int n_pairs,
@@ -481,7 +485,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const PoolArgs a, const 
                 if (i0 + 32 * k < pieces) v[k] = s[i0 + 32 * k];
 #pragma unroll
             for (int k = 0; k < kUnroll; ++k)
-                if (i0 + 32 * k < pieces) d[i0 + 32 * k] = v[k];
+                if (i0 + 32 * k < pieces) __stcs(d + i0 + 32 * k, v[k]);
         }
     }
 }
@@ -536,7 +540,7 @@ cudaError_t launch_moves(const swa_page_pool *p, const PagesWs &w, int64_t most,
                          cudaStream_t s) {
     const PoolArgs a = pool_args(p);
     const int64_t units = most * a.L * 2 * a.H;
-    return launch_dependent(true, move_kernel<kWhich>, dim3(grid_for(units * 32, 8)), kThreads, 0, s, a, w.moves,
+    return launch_dependent(true, move_kernel<kWhich>, dim3(grid_for(units * 32, kMoveBlocks)), kThreads, 0, s, a, w.moves,
                             w.count, nullptr, nullptr, 0, apply);
 }
 
@@ -601,7 +605,7 @@ cudaError_t launch_page_copy(const swa_page_pool *pool, const int32_t *src, cons
                              cudaStream_t s) {
     const PoolArgs a = pool_args(pool);
     const int64_t units = static_cast<int64_t>(n) * a.L * 2 * a.H;
-    move_kernel<Moves::kPairs><<<grid_for(units * 32, 8), kThreads, 0, s>>>(a, nullptr, nullptr, src, dst, n, ApplyArgs{});
+    move_kernel<Moves::kPairs><<<grid_for(units * 32, kMoveBlocks), kThreads, 0, s>>>(a, nullptr, nullptr, src, dst, n, ApplyArgs{});
     return cudaGetLastError();
 }
 
