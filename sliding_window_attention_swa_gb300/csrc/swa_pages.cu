@@ -213,8 +213,10 @@ __global__ void __launch_bounds__(kScanThreads) reserve_kernel(const TableArgs a
 }
 
 // ---------------------------------------------------------------------------------------------
-// free: every entry once.  Bound by the atomics of a large table (1024 x 4096 entries: 23 us; four
-// entries a thread, with vector loads, took as long).
+// free: every entry once.  Bound by the atomics of a large table (1024 x 4096 entries, most of which
+// go: 21 us; 23 with at most 8 blocks an SM instead of 64; 18 if the
+// atomics returned nothing, but a page without a holder to lose has to be seen; four entries a
+// thread, with vector loads, took as long).
 // ---------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(kThreads) free_kernel(const TableArgs a, const int32_t *below, int n_sink) {
     wait_for_previous();
@@ -563,7 +565,8 @@ cudaError_t launch_free(const swa_page_tables *t, const int32_t *below, int n_si
     cudaError_t e = copy_ref(a, s);
     if (e != cudaSuccess) return e;
     const int64_t n = static_cast<int64_t>(a.B) * a.width;
-    return launch_dependent(a.ref != a.out_ref, free_kernel, dim3(grid_for(n, 8)), kThreads, 0, s, a, below, n_sink);
+    return launch_dependent(a.ref != a.out_ref, free_kernel, dim3(grid_for(n, 64)), kThreads, 0, s, a, below,
+                            n_sink);
 }
 
 cudaError_t launch_fork(const swa_page_tables *t, const swa_page_pool *pool, const int32_t *src, const int32_t *len,
