@@ -31,7 +31,9 @@ __device__ unsigned int g_psplit_data = 0;  // broken device data
 constexpr int CH = 64;  // keys a tile
 constexpr int kThreads = 160;
 constexpr int ROWS = 16;  // mma.sync M
-constexpr int kMinTiles = 4;  // least share of a CTA
+// Least share of a CTA.  Pieces of one tile each join as fast as pieces of four, and small batches are
+// done sooner: one token behind 900 13.1 -> 12.6 us, eight behind up to 500 13.9 -> 11.5 us.
+constexpr int kMinTiles = 1;
 
 template <int D>
 struct SplitCfg {

@@ -16,7 +16,7 @@ pytestmark = pytest.mark.gpu
 
 SWA_ERR_TIMEOUT = 4
 
-# (a CTA's share has at least four tiles, two fills each, and at head dim 256 two of the query tile)
+# (a CTA's share of these: at least four tiles, two fills each, and at head dim 256 two of the query tile)
 STOPS = [
     # Hq, Hkv, D, (history, new tokens) of each sequence, window, fault, word that reports it
     pytest.param(8, 2, 64, [(900, 70), (30, 5)], 0, dict(band_stop_fill=0), "prefill", id="d64-first-fill"),
@@ -26,7 +26,7 @@ STOPS = [
     pytest.param(4, 2, 256, [(3000, 70), (30, 5)], 0, dict(band_stop_fill=1), "prefill", id="d256-query-tile"),
     pytest.param(4, 2, 256, [(3000, 70), (30, 5)], 0, dict(band_stop_fill=6), "prefill", id="d256"),
     pytest.param(8, 2, 128, [(3000, 1), (30, 1)], 0, dict(split_stop_stage=0), "split", id="few-rows-first-stage"),
-    pytest.param(8, 2, 128, [(9000, 1), (9000, 1)], 0, dict(split_stop_stage=2), "split", id="few-rows"),
+    pytest.param(8, 2, 128, [(40000, 1), (9000, 1)], 0, dict(split_stop_stage=2), "split", id="few-rows"),
 ]
 
 
