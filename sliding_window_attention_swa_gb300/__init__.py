@@ -562,10 +562,19 @@ def _device_index(name, t) -> int:
     return index
 
 
-def _raw_stream(stream, index: int) -> int:
+def _raw_stream(index: int) -> int:
     import torch
 
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on(stream, call, *args, **kw):
+    """The call with `stream` as the current one, so that the memory that it allocates, and lets go
+    of when it returns, belongs to that stream."""
+    import torch
+
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
 
 
 def _paged_cache(k_pages, v_pages, page_table, p0, q_start, N: int):
@@ -630,6 +639,10 @@ def swa_paged_attend(q, k_pages, v_pages, page_table, p0, window: int = 0, scale
     """
     import torch
 
+    if stream is not None:
+        return _on(stream, swa_paged_attend, q, k_pages, v_pages, page_table, p0, window, scale, q_start=q_start,
+                   n_sink=n_sink, max_q=max_q, k_new=k_new, v_new=v_new, o=o, lse=lse, row_counts=row_counts,
+                   want_counts=want_counts, workspace=workspace)
     lib = load_library()
     if q.dim() != 3:
         raise ValueError("q: expected [N, H_q, d]")
@@ -668,7 +681,7 @@ def swa_paged_attend(q, k_pages, v_pages, page_table, p0, window: int = 0, scale
                 _paged_ws_size[key] = size
         workspace = torch.empty(size or 1, dtype=torch.uint8, device=device)
     st = lib.swa_paged_attend(params, cache, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                              _raw_stream(stream, index))
+                              _raw_stream(index))
     if st != 0:
         raise SwaError("swa_paged_attend", st)
     return o, lse, row_counts
@@ -676,6 +689,8 @@ def swa_paged_attend(q, k_pages, v_pages, page_table, p0, window: int = 0, scale
 
 def swa_paged_append(k_pages, v_pages, page_table, k_new, v_new, p0, *, q_start=None, stream=None) -> None:
     """Store k_new/v_new [N,H_kv,d] (packed rows as in swa_paged_attend) in their pages."""
+    if stream is not None:
+        return _on(stream, swa_paged_append, k_pages, v_pages, page_table, k_new, v_new, p0, q_start=q_start)
     N = k_new.shape[0]
     index, cache, H_kv, D = _paged_cache(k_pages, v_pages, page_table, p0, q_start, N)
     new, new_st = _new_rows(k_new, v_new, index, (N, H_kv, D))
@@ -683,7 +698,7 @@ def swa_paged_append(k_pages, v_pages, page_table, k_new, v_new, p0, *, q_start=
         return
     params = _PAGED_PARAMS.pack(0, *new, p0.data_ptr(), 0 if q_start is None else q_start.data_ptr(), 0, 0, *new_st,
                                 0, 0, N, 0, 0, 0, 0, 0.0, 0, 0, 0)
-    st = load_library().swa_paged_append(params, cache, _raw_stream(stream, index))
+    st = load_library().swa_paged_append(params, cache, _raw_stream(index))
     if st != 0:
         raise SwaError("swa_paged_append", st)
 
@@ -739,11 +754,13 @@ def _pages_workspace(lib, tables, workspace, device):
 def swa_pages_reserve(page_table, ref, first, end, page_size: int, *, workspace=None, stream=None) -> None:
     """Give row b of page_table (in place, with ref) a page for every position in [first[b], end[b])
     that has none: the lowest free pages, in the order of rows and entries."""
+    if stream is not None:
+        return _on(stream, swa_pages_reserve, page_table, ref, first, end, page_size, workspace=workspace)
     lib = load_library()
     index, t, B = _page_tables(page_table, ref, page_size, page_table, ref)
     _lists(index, ("first", first, (B,)), ("end", end, (B,)))
     workspace, n = _pages_workspace(lib, t, workspace, page_table.device)
-    st = lib.swa_pages_reserve(t, first.data_ptr(), end.data_ptr(), workspace.data_ptr(), n, _raw_stream(stream, index))
+    st = lib.swa_pages_reserve(t, first.data_ptr(), end.data_ptr(), workspace.data_ptr(), n, _raw_stream(index))
     if st != 0:
         raise SwaError("swa_pages_reserve", st)
 
@@ -753,10 +770,13 @@ def swa_pages_free(page_table, ref, below, page_size: int, *, n_sink: int = 0, o
     """Row b gives up its pages whose positions all lie below below[b] and past the first n_sink
     positions' pages (below[b] < 0: all its pages).  In place unless out_table and out_ref are
     given.  Returns (out_table, out_ref)."""
+    if stream is not None:
+        return _on(stream, swa_pages_free, page_table, ref, below, page_size, n_sink=n_sink, out_table=out_table,
+                   out_ref=out_ref)
     out_table, out_ref = page_table if out_table is None else out_table, ref if out_ref is None else out_ref
     index, t, B = _page_tables(page_table, ref, page_size, out_table, out_ref)
     _lists(index, ("below", below, (B,)))
-    st = load_library().swa_pages_free(t, below.data_ptr(), int(n_sink), _raw_stream(stream, index))
+    st = load_library().swa_pages_free(t, below.data_ptr(), int(n_sink), _raw_stream(index))
     if st != 0:
         raise SwaError("swa_pages_free", st)
     return out_table, out_ref
@@ -771,6 +791,9 @@ def swa_pages_fork(k_pages, v_pages, page_table, ref, src, seq_len, *, out_table
     (in place if not given) are written whole.  Returns (out_table, out_ref)."""
     import torch
 
+    if stream is not None:
+        return _on(stream, swa_pages_fork, k_pages, v_pages, page_table, ref, src, seq_len, out_table=out_table,
+                   out_ref=out_ref, workspace=workspace)
     lib = load_library()
     pool_index, pool, page_size = _page_pool(k_pages, v_pages)
     out_table = torch.empty_like(page_table) if out_table is None else out_table
@@ -779,7 +802,7 @@ def swa_pages_fork(k_pages, v_pages, page_table, ref, src, seq_len, *, out_table
     _lists(index, ("src", src, (B,)), ("seq_len", seq_len, (B,)))
     workspace, n = _pages_workspace(lib, t, workspace, page_table.device)
     st = lib.swa_pages_fork(t, pool, src.data_ptr(), seq_len.data_ptr(), workspace.data_ptr(), n,
-                            _raw_stream(stream, pool_index))
+                            _raw_stream(pool_index))
     if st != 0:
         raise SwaError("swa_pages_fork", st)
     return out_table, out_ref
@@ -792,6 +815,9 @@ def swa_pages_compact(k_pages, v_pages, page_table, ref, *, out_table=None, out_
     out_ref, n_live int32 [1], on the device)."""
     import torch
 
+    if stream is not None:
+        return _on(stream, swa_pages_compact, k_pages, v_pages, page_table, ref, out_table=out_table, out_ref=out_ref,
+                   n_live=n_live, workspace=workspace)
     lib = load_library()
     pool_index, pool, page_size = _page_pool(k_pages, v_pages)
     out_table, out_ref = page_table if out_table is None else out_table, ref if out_ref is None else out_ref
@@ -799,7 +825,7 @@ def swa_pages_compact(k_pages, v_pages, page_table, ref, *, out_table=None, out_
     n_live = torch.empty(1, dtype=torch.int32, device=page_table.device) if n_live is None else n_live
     _lists(index, ("n_live", n_live, (1,)))
     workspace, n = _pages_workspace(lib, t, workspace, page_table.device)
-    st = lib.swa_pages_compact(t, pool, n_live.data_ptr(), workspace.data_ptr(), n, _raw_stream(stream, pool_index))
+    st = lib.swa_pages_compact(t, pool, n_live.data_ptr(), workspace.data_ptr(), n, _raw_stream(pool_index))
     if st != 0:
         raise SwaError("swa_pages_compact", st)
     return out_table, out_ref, n_live
@@ -807,11 +833,13 @@ def swa_pages_compact(k_pages, v_pages, page_table, ref, *, out_table=None, out_
 
 def swa_pages_copy(k_pages, v_pages, src, dst, *, stream=None) -> None:
     """Copy page src[i] to page dst[i] in every layer (int32 lists; the dst distinct, none also a src)."""
+    if stream is not None:
+        return _on(stream, swa_pages_copy, k_pages, v_pages, src, dst)
     index, pool, _ = _page_pool(k_pages, v_pages)
     if src.dim() != 1:
         raise ValueError("src: expected int32 [n]")
     _lists(index, ("src", src, src.shape), ("dst", dst, src.shape))
-    st = load_library().swa_pages_copy(pool, src.data_ptr(), dst.data_ptr(), src.shape[0], _raw_stream(stream, index))
+    st = load_library().swa_pages_copy(pool, src.data_ptr(), dst.data_ptr(), src.shape[0], _raw_stream(index))
     if st != 0:
         raise SwaError("swa_pages_copy", st)
 

@@ -351,6 +351,45 @@ def test_two_streams_at_once(swa):
         verify(x, o, lse, cnt)
 
 
+def test_on_a_stream_that_is_not_the_current_one(swa):
+    # the call's own memory belongs to its stream: the current stream's blocks come and go meanwhile
+    side = torch.cuda.Stream()
+    for seqs, hint in (([(3000, 70), (10, 1), (900, 200)], 0), ([(3000, 1), (10, 1), (9000, 1)], 1)):
+        x = R.Batch(47, seqs, 8, 2, 128, 32, 1000)
+        a = (x.q.cuda(), x.k_pages.cuda(), x.v_pages.cuda(), x.table.cuda(), x.p0.cuda())
+        start = None if hint else x.q_start.cuda()
+        want = swa.swa_paged_attend(*a, 1000, q_start=start, max_q=hint, want_counts=True)
+        torch.cuda.synchronize()
+        got = []
+        for _ in range(20):
+            for n in (1 << 20, 10 << 20, 40 << 20):
+                torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+            got.append(swa.swa_paged_attend(*a, 1000, q_start=start, max_q=hint, want_counts=True, stream=side))
+        torch.cuda.synchronize()
+        swa.swa_check_device_error(side)
+        for g in got:
+            assert all(torch.equal(p, q) for p, q in zip(g, want))
+    # the pages' calls take one, too
+    table, ref = torch.full((2, 4), -1, dtype=torch.int32, device="cuda"), torch.zeros(20, dtype=torch.int32, device="cuda")
+    k = torch.randn(20, 2, 16, 64, device="cuda").to(torch.bfloat16)
+    v, kn = k.clone(), torch.randn(2, 2, 64, device="cuda").to(torch.bfloat16)
+    zero, end, src, one, last = R.i32([0, 0]), R.i32([20, 20]), R.i32([0, 0]), R.i32([0]), R.i32([19])
+    torch.cuda.synchronize()
+    swa.swa_pages_reserve(table, ref, zero, end, 16, stream=side)
+    swa.swa_paged_append(k, v, table, kn, kn, zero, stream=side)
+    t2, r2 = swa.swa_pages_fork(k, v, table, ref, src, end, stream=side)
+    swa.swa_pages_compact(k, v, t2, r2, stream=side)
+    swa.swa_pages_copy(k, v, one, last, stream=side)
+    torch.cuda.synchronize()
+    swa.swa_check_device_error(side)
+    # (row 0's first page stays with it and its copy, both rows' others are their own)
+    assert t2.tolist() == [[0, 1, -1, -1], [0, 2, -1, -1]] and r2.tolist()[:4] == [2, 1, 1, 0]
+    assert torch.equal(k[19], k[0]) and torch.equal(k[0, :, 0], kn[0]) and torch.equal(k[1, :, :4], k[2, :, :4])
+    swa.swa_pages_free(t2, r2, R.i32([-1, -1]), 16, stream=side)
+    torch.cuda.synchronize()
+    assert (t2 == -1).all() and (r2 == 0).all()
+
+
 def test_same_call_same_bits(swa):
     x = R.Batch(50, [(5000, 300), (77, 1), (4000, 1)], 8, 2, 128, 16)
     for hint in (0, 1):
