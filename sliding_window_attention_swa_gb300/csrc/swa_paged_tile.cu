@@ -413,11 +413,11 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             }
             tc_commit_e(bar_sf(slot));
         };
-        // O_ot (+)= P(slot) V (descriptors in vd) once P is there and, if wait_v >= 0, that fill, and for a
-        // fresh O once the epilogue of the previous piece has read it
+        // O_ot (+)= P(slot) V (descriptors in vd) once, if wait_v >= 0, that fill is there, then P (the last
+        // to come), and for a fresh O once the epilogue of the previous piece has read it
         auto mma_pv = [&](int slot, int ot, bool first, uint32_t n_used, int wait_v) -> bool {
-            if (!warp_wait(bar_pf(slot), n_used & 1, abort)) return false;
             if (wait_v >= 0 && !landed(wait_v)) return false;
+            if (!warp_wait(bar_pf(slot), n_used & 1, abort)) return false;
             if (first && k >= 1) {
                 if (!warp_wait(bar_of(ot), (k - 1) & 1, abort)) return false;
                 // (of a piece of one query tile both warpgroups read both accumulators, and both finish with it)
@@ -449,11 +449,11 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     for (int i = 0; i < n; ++i) {
                         const int f = 2 * (J + i), ks = (f + 2) % NSLOT;
                         v_descs((f + 1) % NSLOT);
-                        ok = mma_pv(0, 0, i == 0, np0 + i, f + 1);
+                        // (the next keys are waited for here, not between the two products, where a wait leaves
+                        // the tensor cores idle: the Mistral window on pages of 16 651 -> 638 us)
+                        ok = landed(f + 1) && (i + 1 == n || landed(f + 2)) && mma_pv(0, 0, i == 0, np0 + i, -1);
                         if (!ok) break;
                         if (i + 1 < n) {
-                            ok = landed(f + 2);
-                            if (!ok) break;
                             mma_s(0, 0, ks);
                         } else {
                             tc_commit_e(bar_od(0));
