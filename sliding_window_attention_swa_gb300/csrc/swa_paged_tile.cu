@@ -473,12 +473,10 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     ok = warp_wait(bar_qf(y), (y ? nq[1]++ : nq[0]++) & 1, abort) && landed(2 * J);
                     if (!ok) break;
                     mma_s(s_slot(0), 0, (2 * J) % NSLOT, q_bytes);
-                    tc_commit_e(bar_empty((2 * J) % NSLOT));
                     if (C::NS == 3 && n > 1) {
                         ok = landed(2 * J + 2);
                         if (!ok) break;
                         mma_s(s_slot(1), 0, (2 * J + 2) % NSLOT, q_bytes);
-                        tc_commit_e(bar_empty((2 * J + 2) % NSLOT));
                     }
 #pragma unroll 1
                     for (int i = 0; i < n; ++i) {
@@ -488,7 +486,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                             ok = landed(fk);
                             if (!ok) break;
                             mma_s(s_slot(i + C::NS - 1), 0, fk % NSLOT, q_bytes);
-                            tc_commit_e(bar_empty(fk % NSLOT));
                         }
                         v_descs((f + 1) % NSLOT);
                         const uint32_t used = C::NS == 3 ? static_cast<uint32_t>((J + i) / 3) : x ? np1++ : np0++;
@@ -639,6 +636,11 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                         if (i > 0) mbar_arrive(bar_empty((2 * g - 1) % NSLOT));
                     }
                     __syncwarp();  // tcgen05.ld is executed by the converged warp
+                } else if (NQT == 2) {
+                    // S was K_g's only reader (released here, not by a commit of the MMA warp: 8192 tokens
+                    // of head dim 64 behind 8000 804 -> 782 us)
+                    if (quarter == 0 && lane == 0) mbar_arrive(bar_empty((2 * g) % NSLOT));
+                    __syncwarp();
                 }
                 tc_fence_after();
                 const uint32_t s_addr = tmem + lane_addr + C::tm_s(slot);
