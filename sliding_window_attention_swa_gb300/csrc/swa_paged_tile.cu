@@ -87,14 +87,14 @@ struct TileCfg {
     // K/V ring.  At head dim 256 the query tile, which the MMAs read from tensor memory, passes
     // through it as two fills of its own instead of holding two slots' worth of shared memory:
     // seven slots instead of five.
-    static constexpr int NSLOT = D == 64 ? 7 : NSLOT_RAW;
+    static constexpr int NSLOT = D == 64 ? 8 : NSLOT_RAW;
     static_assert(NQT == 2 || QBYTES == 2 * TBYTES, "a query tile is two fills");
     static constexpr int OFF_X = OFF_RING + NSLOT * TBYTES;
     static constexpr int OFF_BAR = OFF_X + XBYTES;
     // q_full[2], q_empty[2], kv_full[NSLOT], kv_empty[NSLOT], s_full[3], p_full[3], o_done[2],
-    // o_free[2], meet, drain, pv_done[2], piece_full[NP], piece_empty[NP]
+    // o_free[2], meet, drain, piece_full[NP], piece_empty[NP]
     static constexpr int NP = 4;  // pieces planned ahead
-    static constexpr int NBAR = 2 * NSLOT + 18 + 2 * NP;
+    static constexpr int NBAR = 2 * NSLOT + 16 + 2 * NP;
     static constexpr int OFF_TMEMPTR = OFF_BAR + NBAR * 8;  // TMEM address, abort flag
     static constexpr int OFF_SHARE = OFF_TMEMPTR + 16;
     static constexpr int OFF_PIECE = OFF_SHARE + 64;
@@ -112,6 +112,7 @@ struct TileCfg {
     static constexpr bool QTM = NQT == 1;  // the query tile in tensor memory, 128 columns
     static constexpr uint32_t TM_Q = 128;
     static_assert(NSLOT >= 3, "K/V ring too shallow");
+    static_assert(D == 128 || NSLOT >= (D == 64 ? 8 : 7), "a slot's next release waits for P (the rescaling's wait)");
     static_assert(SMEM <= 232448, "shared memory budget");
     static_assert(NSLOT * TBYTES >= kShareScratch, "scratch of the work split");
     static_assert(!QTM || (tm_s(1) + BN <= TM_Q && TM_Q + D / 2 <= tm_o(0)), "query tile in tensor memory");
@@ -177,9 +178,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     auto bar_of = [&](int i) { return bars + 8u * (12 + 2 * NSLOT + i); };
     const uint32_t bar_meet = bars + 8u * (14 + 2 * NSLOT);
     const uint32_t bar_drain = bars + 8u * (15 + 2 * NSLOT);
-    auto bar_pv = [&](int i) { return bars + 8u * (16 + 2 * NSLOT + i); };
-    auto bar_piece = [&](int i) { return bars + 8u * (18 + 2 * NSLOT + i); };
-    auto bar_used = [&](int i) { return bars + 8u * (18 + 2 * NSLOT + C::NP + i); };
+    auto bar_piece = [&](int i) { return bars + 8u * (16 + 2 * NSLOT + i); };
+    auto bar_used = [&](int i) { return bars + 8u * (16 + 2 * NSLOT + C::NP + i); };
     // Ring fills, numbered over the CTA's share; fill p lies in slot p % NSLOT, phase (p / NSLOT) & 1
     // of the slot's barriers.  A piece's query tile comes first at head dim 256 (two fills), then K
     // and V of each of its tiles: kfill is K of the share's g-th tile, in its k-th piece, V the next.
@@ -196,7 +196,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             mbar_init(bar_qf(x), 1);
             mbar_init(bar_qe(x), 4);  // the four warps of a softmax warpgroup
             mbar_init(bar_od(x), 1);
-            mbar_init(bar_pv(x), 1);
             mbar_init(bar_of(x), 4);
         }
         for (int x = 0; x < 3; ++x) {
@@ -492,7 +491,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                         ok = mma_pv(s_slot(i), x, i < 2, used, f + 1);
                         if (!ok) break;
                         tc_commit_e(bar_empty((f + 1) % NSLOT));
-                        if constexpr (C::NS == 3) tc_commit_e(bar_pv(x));
                     }
                     if (!ok) break;
                     tc_commit_e(bar_od(0));
@@ -698,18 +696,12 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 const float alpha = need ? ex2(m - mu) : 1.f;  // m = -inf gives 0
                 if (__any_sync(0xffffffffu, need) && i >= (single ? 2 : 1)) {
                     // O holds the P V of this piece's earlier tiles (of this warpgroup) and must be
-                    // complete: with two S slots and two warpgroups S(i) was issued after them; with three
-                    // each P V has a commit of its own; with one warpgroup the release of tile g-1's V
-                    // slot is committed right after its P V
-                    if constexpr (C::NS == 3) {
-                        if (!warp_wait(bar_pv(wg), ns & 1, abort)) {  // (this is the warpgroup's tile ns - 1)
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                    }
-                    if constexpr (NQT == 1) {
-                        const int f = kfill(k, g - 1) + 1;
+                    // complete: with two S slots and two warpgroups S(i) was issued after them; else the
+                    // release of the V slot of this warpgroup's last tile is committed right after its P V.
+                    // (That slot's next release cannot come before this warp's P of tile g: with eight slots
+                    // and two warpgroups it is that of V of tile g + 2, with seven and one of K of g + 3.)
+                    if constexpr (C::NS == 3 || NQT == 1) {
+                        const int f = kfill(k, g - NQT) + 1;
                         if (!warp_wait(bar_empty(f % NSLOT), fphase(f), abort)) {
                             ok = false;
                             break;
