@@ -103,7 +103,7 @@ struct TileCfg {
     static_assert(sizeof(Share) <= 64, "share");
     static constexpr uint32_t TMEM_COLS = 512;
     // S slots: two, or three where tensor memory has room (head dim 64), so that S(j + 2) is there
-    // when the warpgroup that had tile j is done with it (8192 tokens behind 8000, full causal: 910 -> 816 us)
+    // when the warpgroup that had tile j is done with it (8192 tokens behind 8000: 910 -> 816 us; now 708)
     static constexpr int NS = D == 64 ? 3 : 2;
     __host__ __device__ static constexpr uint32_t tm_s(int slot) { return static_cast<uint32_t>(slot * BN); }
     __host__ __device__ static constexpr uint32_t tm_o(int tile) {
@@ -1070,7 +1070,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
 // (chunks of 2048 tokens behind 30000: 989 against 1047 us), and single tiles, twice as many
 // units, where there are not (two chunks of 100 tokens 25 against 33 us, a mixed step 78
 // against 91): pairs from two units a CTA, by what the host knows of the batch.  At head dim 64
-// the exponentials bound both alike (856 and 857 us).
+// there was nothing between them (856 and 857 us, of what is now 708), so it has no pairs.
 int tiles_of_unit(const PagedArgs &a) {
     if (a.D != 128) return 1;
     const int64_t pairs = static_cast<int64_t>(a.N) / (2 * (BM / a.G)) * a.H_kv;
