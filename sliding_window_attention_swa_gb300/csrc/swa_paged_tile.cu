@@ -87,7 +87,7 @@ struct TileCfg {
     // K/V ring.  At head dim 256 the query tile, which the MMAs read from tensor memory, passes
     // through it as two fills of its own instead of holding two slots' worth of shared memory:
     // seven slots instead of five.
-    static constexpr int NSLOT = D == 64 ? 8 : NSLOT_RAW;
+    static constexpr int NSLOT = D == 64 ? 10 : NSLOT_RAW;
     static_assert(NQT == 2 || QBYTES == 2 * TBYTES, "a query tile is two fills");
     static constexpr int OFF_X = OFF_RING + NSLOT * TBYTES;
     static constexpr int OFF_BAR = OFF_X + XBYTES;
@@ -113,6 +113,13 @@ struct TileCfg {
     static constexpr uint32_t TM_Q = 128;
     static_assert(NSLOT >= 3, "K/V ring too shallow");
     static_assert(D == 128 || NSLOT >= (D == 64 ? 8 : 7), "a slot's next release waits for P (the rescaling's wait)");
+    // Waits name a phase by its parity.  A softmax warp that zeroes value rows waits for the copy of
+    // V(g) when it has seen the scores of the tile before it took (g - 2 where two warpgroups share a query
+    // tile, g - 1 at head dim 256).  The fill that the slot had before, K(g - (NSLOT - 1) / 2) in an odd
+    // ring, V(g - NSLOT / 2) in an even one, must have landed by then: scores come from landed keys,
+    // and are issued behind P V of the tile NS before theirs, so behind its values' landing.
+    static constexpr int SEEN = NQT == 2 ? 2 : 1;  // the tile whose scores were seen: g - SEEN
+    static_assert(NSLOT % 2 ? (NSLOT - 1) / 2 >= SEEN : NSLOT / 2 >= SEEN + NS, "the wait before value rows are zeroed");
     static_assert(SMEM <= 232448, "shared memory budget");
     static_assert(NSLOT * TBYTES >= kShareScratch, "scratch of the work split");
     static_assert(!QTM || (tm_s(1) + BN <= TM_Q && TM_Q + D / 2 <= tm_o(0)), "query tile in tensor memory");
@@ -698,8 +705,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     // O holds the P V of this piece's earlier tiles (of this warpgroup) and must be
                     // complete: with two S slots and two warpgroups S(i) was issued after them; else the
                     // release of the V slot of this warpgroup's last tile is committed right after its P V.
-                    // (That slot's next release cannot come before this warp's P of tile g: with eight slots
-                    // and two warpgroups it is that of V of tile g + 2, with seven and one of K of g + 3.)
+                    // (That slot's next release cannot come before this warp's P of tile g: with ten slots
+                    // and two warpgroups it is that of V of tile g + 3, with seven and one of K of g + 3.)
                     if constexpr (C::NS == 3 || NQT == 1) {
                         const int f = kfill(k, g - NQT) + 1;
                         if (!warp_wait(bar_empty(f % NSLOT), fphase(f), abort)) {

@@ -158,6 +158,34 @@ def test_positions_that_no_query_keeps_may_hold_anything(swa, case, hint):
     run(swa, x, max_q=hint, q_start=None if hint else x.q_start.cuda())
 
 
+@pytest.mark.parametrize("ps", [32, 128])
+@pytest.mark.parametrize("w,sinks", [(1024, 0), (0, 0), (1024, 400)], ids=str)
+def test_tiles_that_come_from_hbm(swa, w, sinks, ps):
+    """Single tokens in the many-row kernel at head dim 64, their keys and values out of L2 before each
+    call, so that copies land late and unevenly; NaN in every tail and between sinks and window."""
+    seqs = [(1000 + 8003 * i // 60 + i % 37, 1) for i in range(61)]
+    x = R.Batch(52, seqs, 4, 4, 64, ps, w, sinks, freed=not sinks)
+    if sinks:
+        for b, (p, _) in enumerate(seqs):
+            for j in range(x.width):
+                lo, hi = max(sinks - j * ps, 0), min(p - w + 1 - j * ps, ps)
+                if lo < hi:
+                    for t in (x.k_pages, x.v_pages):
+                        t[int(x.table[b, j]), :, lo:hi] = float("nan")
+    q, k, v, table, p0, start = (t.cuda() for t in (x.q, x.k_pages, x.v_pages, x.table, x.p0, x.q_start))
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")  # more than L2
+    first = None
+    for turn in range(40):
+        flush.fill_(turn)
+        got = swa.swa_paged_attend(q, k, v, table, p0, w, n_sink=sinks, q_start=start, want_counts=True)
+        if first is None:
+            first = got
+            swa.swa_check_device_error()
+            verify(x, *first)
+        assert all(torch.equal(a, b) for a, b in zip(got, first)), f"call {turn} differs from the first"
+    swa.swa_check_device_error()
+
+
 def test_values_of_the_extremes(swa):
     # scores of +-1000s: one key carries all the weight, and the running maximum jumps
     x = R.Batch(7, [(500, 70), (900, 1)], 8, 2, 128, 32)
