@@ -426,8 +426,10 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             if (!warp_wait(bar_pf(slot), n_used & 1, abort)) return false;
             if (first && k >= 1) {
                 if (!warp_wait(bar_of(ot), (k - 1) & 1, abort)) return false;
-                // (of a piece of one query tile both warpgroups read both accumulators, and both finish with it)
-                if (NQT == 2 && both && !warp_wait(bar_of(ot ^ 1), (k - 1) & 1, abort)) return false;
+                // (of a piece of one query tile both warpgroups read both accumulators, and both finish with it;
+                // asked before the first product only: behind it the first warpgroup may be done with
+                // this piece, too, and its barrier two phases on)
+                if (NQT == 2 && both && ot == 0 && !warp_wait(bar_of(1), (k - 1) & 1, abort)) return false;
             }
             tc_fence_after();
 #pragma unroll

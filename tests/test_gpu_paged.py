@@ -131,6 +131,17 @@ def test_more_units_than_two_waves(swa, heads):
         run(swa, x, want_counts=False)
 
 
+@pytest.mark.parametrize("heads", [(32, 8, 128), (16, 1, 128)], ids=str)
+def test_pairs_of_one_key_tile_behind_single_query_tiles(swa, heads):
+    # units of two query tiles that read one tile of keys, in turn with units of one query tile: dealt
+    # whole, and behind long units that several CTAs share
+    Hq, Hkv, D = heads
+    pair = 2 * (128 // (Hq // Hkv))  # tokens of a unit of two query tiles
+    few = 60 if Hkv > 1 else 240
+    seqs = [(0, pair + pair // 4)] * few + [(9000, pair // 3), (0, pair)] * 6 + [(0, 3), (0, 2 * pair)] * 4
+    run(swa, R.Batch(15, seqs, Hq, Hkv, D, 64), want_counts=False)
+
+
 @pytest.mark.parametrize("heads", [(12, 4, 128), (5, 5, 64), (6, 2, 256)], ids=str)
 def test_shared_units_with_rows_missing(swa, heads):
     # units spread over many CTAs whose last query tile is not full, in one and two query tiles

@@ -63,6 +63,8 @@ class Barrier:
 class Kernel:
     """pieces: [(tiles, single)]; nqt, ns: query tiles of a CTA, score slots."""
 
+    waits_twice = False  # (a fault that the model catches)
+
     def __init__(self, pieces, nslot, nqt, ns, rng):
         self.pieces, self.nslot, self.nqt, self.ns, self.rng = pieces, nslot, nqt, ns, rng
         b = lambda name, n, count: [Barrier(f"{name}[{i}]", count) for i in range(n)]  # noqa: E731
@@ -200,7 +202,7 @@ class Kernel:
                 yield self.pf[slot], phase
                 if first and k >= 1:
                     yield self.of[acc], k - 1
-                    if self.nqt == 2 and both:
+                    if self.nqt == 2 and both and (acc == 0 or self.waits_twice):
                         yield self.of[acc ^ 1], k - 1
                 self.mma("P V", fv, acc)
 
@@ -367,6 +369,7 @@ FLAVOURS = {
     "d64": (64, 3, 2, (True,)),
     "d128-single": (128, 2, 2, (True,)),
     "d128-pairs": (128, 2, 2, (False,)),
+    "d128-mixed": (128, 2, 2, (True, False)),
     "d256": (256, 2, 1, (False,)),
 }
 
@@ -381,7 +384,7 @@ def runs(name, nslot, count):
 
 @pytest.mark.parametrize("name", FLAVOURS)
 def test_every_wait_names_its_phase(name):
-    for kernel in runs(name, ring_slots(FLAVOURS[name][0]), 500):
+    for kernel in runs(name, ring_slots(FLAVOURS[name][0]), 300):
         kernel.run()
 
 
@@ -407,3 +410,11 @@ def test_model_catches_a_ring_of_seven_slots():
     """... and with seven the slot of V(g - 2) is released once more, of K(g + 2), which does not wait for
     P(g): the rescaling's wait before that may miss its phase."""
     assert premature("d64", 7, 100, "deadlock") > 0
+
+
+def test_model_catches_a_second_wait_for_an_accumulator(monkeypatch):
+    """A unit of two query tiles and one key tile behind a piece of one query tile: the second product
+    must not wait again until the first accumulator is free of the last piece, since by then
+    the first warpgroup may be done with this one."""
+    monkeypatch.setattr(Kernel, "waits_twice", True)
+    assert premature("d128-mixed", ring_slots(128), 1500, r"deadlock.*'o_free\[0\]") > 0
