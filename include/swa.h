@@ -426,9 +426,11 @@ SWA_API swa_status swa_pages_free(const swa_page_tables *t, const int32_t *below
 /*
  * Replaces the batch's rows: row i of out_table continues row src[i] of table, which holds
  * len[src[i]] tokens (src, len: device int32 [B]; src[i] = -1: row i is empty).  Full pages
- * are shared.  The last page, if it is not full, stays with the lowest i of the rows that
- * continue the same row; each other one gets a page of its own, lowest free first in the
- * order of i, and the tokens are copied into it in every layer.  Holders are counted anew: out_ref
+ * are shared.  A last page that is not full will be written to, so no other row may have it: it
+ * stays with the lowest i of the rows whose last page it is, unless it is one of the full pages
+ * of some row (rows that shared it and were cut back to different lengths); each other row
+ * gets a page of its own, lowest free first in the order of i, and the tokens are copied into
+ * it in every layer.  (Holders outside the tables do not matter here.)  Holders are counted anew: out_ref
  * = ref, less the entries of `table`, plus those of out_table.  Entries past the last token
  * are dropped.  Where the pool runs out a row stays without its last page
  * (SWA_DEVERR_NO_PAGE).  A src or len out of range is reported (SWA_DEVERR_BAD_POSITION) and

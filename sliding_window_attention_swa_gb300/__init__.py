@@ -785,9 +785,9 @@ def swa_pages_free(page_table, ref, below, page_size: int, *, n_sink: int = 0, o
 def swa_pages_fork(k_pages, v_pages, page_table, ref, src, seq_len, *, out_table=None, out_ref=None, workspace=None,
                    stream=None):
     """New row i continues row src[i] (-1: empty) of page_table, which holds seq_len[src[i]] tokens:
-    full pages are shared, a last page that is not full stays with the first row that continues
-    it and is copied for each other one (in every layer of k_pages/v_pages [n_layers,]
-    [n_pages,H_kv,page_size,d]).  out_table (not page_table itself; new if not given) and out_ref
+    full pages are shared, a last page that is not full stays with the first row whose last page it
+    is (with none if it is a full page of some row) and is copied for each other one (in every
+    layer of k_pages/v_pages [n_layers,][n_pages,H_kv,page_size,d]).  out_table (not page_table itself; new if not given) and out_ref
     (in place if not given) are written whole.  Returns (out_table, out_ref)."""
     import torch
 

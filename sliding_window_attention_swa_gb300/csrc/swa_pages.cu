@@ -119,11 +119,14 @@ __device__ __forceinline__ int take_free(ScanSmem &sm, const int32_t *ref, int n
     return min(found, need);
 }
 
-__global__ void __launch_bounds__(kThreads) copy_i32_kernel(const int32_t *src, int32_t *dst, int64_t n) {
+// dst = src (n), and `fill` [n_fill] all INT_MAX.
+__global__ void __launch_bounds__(kThreads) copy_i32_kernel(const int32_t *src, int32_t *dst, int64_t n, int32_t *fill,
+                                                            int64_t n_fill) {
     let_next_start();
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-         i += static_cast<int64_t>(gridDim.x) * kThreads)
-        dst[i] = src[i];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    for (int64_t i = t; i < n; i += step) dst[i] = src[i];
+    for (int64_t i = t; i < n_fill; i += step) fill[i] = INT_MAX;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -263,18 +266,38 @@ __device__ __forceinline__ bool fork_source(const TableArgs &a, const int32_t *s
     return true;
 }
 
+// Who keeps a last page that is not full, and so may be written to: keep[p] becomes the lowest row
+// whose last page is p, or -1 if a row has p as a full page.  Both are minima, so their order cannot
+// show.  (A missing page is told apart by the row that it is missing in: keep[n_pages + s].)
+// last_of[i] is row i's last page if that is not full: p, or -2 - s for a missing one; -1: none.
+struct ForkWs {
+    int32_t *last_of, *keep;
+};
+__device__ __forceinline__ bool wants_own(const TableArgs &a, const ForkWs &w, int i) {
+    const int p = w.last_of[i];
+    return p != -1 && w.keep[p >= 0 ? p : static_cast<int64_t>(a.n_pages) + (-2 - p)] != i;
+}
+
 // Row i keeps its own holders where both tables have the same entry (no atomics); the others change.
-// copies: the row wants a page of its own instead of its last one.
-__device__ __forceinline__ void fork_entry(const TableArgs &a, int i, int j, int s, int used, int last, bool copies) {
+// Every row gets its last page here; those that want one of their own lose it again in fork_alloc.
+__device__ __forceinline__ void fork_entry(const TableArgs &a, const ForkWs &w, int i, int j, int s, int part, int last) {
     int in = a.table[static_cast<int64_t>(i) * a.width + j];
-    int out = s >= 0 && j < used ? a.table[static_cast<int64_t>(s) * a.width + j] : -1;
+    const bool is_last = part && j == last;
+    int out = s >= 0 && (j < last || is_last) ? a.table[static_cast<int64_t>(s) * a.width + j] : -1;
     if (in >= a.n_pages || out >= a.n_pages) {
         atomicOr(&g_pages_err, kErrBadPage);
         in = in >= a.n_pages ? -1 : in;
         out = out >= a.n_pages ? -1 : out;
     }
-    if (copies && j == last) out = -1;
-    a.out_table[static_cast<int64_t>(i) * a.width + j] = out < 0 ? -1 : out;
+    out = out < 0 ? -1 : out;
+    if (is_last) {
+        w.last_of[i] = out >= 0 ? out : -2 - s;
+        atomicMin(w.keep + (out >= 0 ? out : static_cast<int64_t>(a.n_pages) + s), i);
+    } else {
+        if (out >= 0) *static_cast<volatile int32_t *>(w.keep + out) = -1;
+        if (j == 0 && !part) w.last_of[i] = -1;
+    }
+    a.out_table[static_cast<int64_t>(i) * a.width + j] = out;
     if (in != out) {
         if (in >= 0) atomicSub(a.out_ref + in, 1);
         if (out >= 0) atomicAdd(a.out_ref + out, 1);
@@ -282,69 +305,65 @@ __device__ __forceinline__ void fork_entry(const TableArgs &a, int i, int j, int
 }
 
 // Rows' tables and the holders of everything but the fresh pages.  Block (x, i): a stretch of
-// row i.  pend[i]: row i wants a page of its own.
+// row i.
 __global__ void __launch_bounds__(kThreads) fork_table_kernel(const TableArgs a, const int32_t *src,
-                                                              const int32_t *len, int32_t *pend) {
+                                                              const int32_t *len, const ForkWs w) {
     let_next_start();
     wait_for_previous();
     for (int i = blockIdx.y; i < a.B; i += gridDim.y) {
         int s, n;
         const bool ok = fork_source(a, src, len, i, s, n);
         if (!ok && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(&g_pages_err, kErrBadPosition);
-        const int part = n % a.ps, last = n / a.ps, used = last + (part ? 1 : 0);
-        // the lowest row that continues s keeps its last page
-        int other = 0;
-        if (s >= 0 && part)
-            for (int k = threadIdx.x; k < i && !other; k += kThreads) other = src[k] == s;
-        const bool copies = __syncthreads_or(other) != 0;
-        if (blockIdx.x == 0 && threadIdx.x == 0) pend[i] = copies ? 1 : 0;
+        const int part = n % a.ps, last = n / a.ps;
         for (int j = blockIdx.x * kThreads + threadIdx.x; j < a.width; j += gridDim.x * kThreads)
-            fork_entry(a, i, j, s, used, last, copies);
+            fork_entry(a, w, i, j, s, part, last);
     }
 }
 
 // One block: fresh pages for the rows that want one, lowest first in the order of the rows.
 __device__ __forceinline__ void fork_alloc(ScanSmem &sm, const TableArgs &a, const int32_t *src, const int32_t *len,
-                                           const int32_t *pend, int32_t *row_of, int32_t *list, Move *moves,
+                                           const ForkWs &w, int32_t *row_of, int32_t *list, Move *moves,
                                            int32_t *n_moves) {
     int want = 0;
     for (int64_t base = 0; base < a.B; base += kScanItems * kScanThreads)
         want = scan_step(
-            sm, base, a.B, want, [&](int i) { return pend[i] != 0; }, [&](int i, int r) { row_of[r] = i; });
+            sm, base, a.B, want, [&](int i) { return wants_own(a, w, i); }, [&](int i, int r) { row_of[r] = i; });
     const int found = want ? take_free(sm, a.out_ref, a.n_pages, min(want, a.n_pages), list) : 0;
     __syncthreads();
     for (int r = threadIdx.x; r < want; r += kScanThreads) {
         const int i = row_of[r], s = src[i], n = len[s], last = n / a.ps;
-        const int old = a.table[static_cast<int64_t>(s) * a.width + last];
+        const int old = w.last_of[i];
+        // (whoever keeps the page still holds it, so it was not among the free ones)
+        if (old >= 0) atomicSub(a.out_ref + old, 1);
         Move m{-1, -1, n % a.ps, 0};
         if (r < found) {
             m.dst = list[r];
             a.out_ref[m.dst] = 1;
-            a.out_table[static_cast<int64_t>(i) * a.width + last] = m.dst;
-            if (old >= 0 && old < a.n_pages) m.src = old;
+            if (old >= 0) m.src = old;
             else atomicOr(&g_pages_err, kErrBadPage);
         } else {
             atomicOr(&g_pages_err, kErrNoPage);
         }
+        a.out_table[static_cast<int64_t>(i) * a.width + last] = m.dst;
         moves[r] = m;
     }
     if (threadIdx.x == 0) *n_moves = want;
 }
 
 __global__ void __launch_bounds__(kScanThreads) fork_alloc_kernel(const TableArgs a, const int32_t *src,
-                                                                  const int32_t *len, const int32_t *pend,
+                                                                  const int32_t *len, const ForkWs w,
                                                                   int32_t *row_of, int32_t *list, Move *moves,
                                                                   int32_t *n_moves) {
     __shared__ ScanSmem sm;
     let_next_start();
     wait_for_previous();
-    fork_alloc(sm, a, src, len, pend, row_of, list, moves, n_moves);
+    fork_alloc(sm, a, src, len, w, row_of, list, moves, n_moves);
 }
 
 // All of that for small tables by one cluster, whose barriers order the counts' copy, the rows and
 // the fresh pages: one launch instead of three.  A warp per 32 entries of a row.
 __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kScanThreads)
-    fork_plan_kernel(const TableArgs a, const int32_t *src, const int32_t *len, int32_t *pend, int32_t *row_of,
+    fork_plan_kernel(const TableArgs a, const int32_t *src, const int32_t *len, const ForkWs w, int32_t *row_of,
                      int32_t *list, Move *moves, int32_t *n_moves) {
     __shared__ ScanSmem sm;
     let_next_start();
@@ -353,26 +372,21 @@ __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kScanThreads
     auto cluster_sync = [] {
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     };
-    if (a.ref != a.out_ref) {
-        for (int p = t; p < a.n_pages; p += kForkCtas * kScanThreads) a.out_ref[p] = a.ref[p];
-        cluster_sync();
+    for (int p = t; p < a.n_pages + a.B; p += kForkCtas * kScanThreads) {
+        if (p < a.n_pages && a.ref != a.out_ref) a.out_ref[p] = a.ref[p];
+        w.keep[p] = INT_MAX;
     }
+    cluster_sync();
     const int parts = (a.width + 31) / 32;
     for (int u = t >> 5; u < a.B * parts; u += kForkCtas * kScanWarps) {
         const int i = u / parts, j = u % parts * 32 + lane;
         int s, n;
         const bool ok = fork_source(a, src, len, i, s, n);
         if (!ok && j == 0) atomicOr(&g_pages_err, kErrBadPosition);
-        const int part = n % a.ps, last = n / a.ps, used = last + (part ? 1 : 0);
-        int other = 0;  // (a lower row that continues s keeps its last page)
-        if (s >= 0 && part)
-            for (int k = lane; k < i && !other; k += 32) other = src[k] == s;
-        const bool copies = __any_sync(0xffffffffu, other != 0);
-        if (j == 0) pend[i] = copies ? 1 : 0;
-        if (j < a.width) fork_entry(a, i, j, s, used, last, copies);
+        if (j < a.width) fork_entry(a, w, i, j, s, n % a.ps, n / a.ps);
     }
     cluster_sync();
-    if (blockIdx.x == 0) fork_alloc(sm, a, src, len, pend, row_of, list, moves, n_moves);
+    if (blockIdx.x == 0) fork_alloc(sm, a, src, len, w, row_of, list, moves, n_moves);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -511,7 +525,8 @@ int grid_for(int64_t n, int per_sm) {
     const int64_t blocks = (n + kThreads - 1) / kThreads, cap = static_cast<int64_t>(paged_sm_count()) * per_sm;
     return static_cast<int>(blocks < cap ? (blocks > 0 ? blocks : 1) : cap);
 }
-// The workspace: ints [2 * B], [3 * n_pages], moves [max(B, n_pages)], a count.
+// The workspace: ints [2 * B], [3 * n_pages], [B], moves [max(B, n_pages)], a count.  (A fork takes list1
+// and what follows as one list of n_pages + B.)
 struct PagesWs {
     int32_t *rows0, *rows1, *list0, *list1, *list2, *count;
     Move *moves;
@@ -532,9 +547,10 @@ PagesWs carve(const swa_page_tables *t, void *ws) {
     w.list2 = w.list1 + t->n_pages;
     return w;
 }
-cudaError_t copy_ref(const TableArgs &a, cudaStream_t s) {
-    if (a.ref == a.out_ref) return cudaSuccess;
-    copy_i32_kernel<<<grid_for(a.n_pages, 8), kThreads, 0, s>>>(a.ref, a.out_ref, a.n_pages);
+cudaError_t copy_ref(const TableArgs &a, cudaStream_t s, int32_t *fill = nullptr, int64_t n_fill = 0) {
+    const int64_t n = a.ref == a.out_ref ? 0 : a.n_pages;
+    if (n == 0 && n_fill == 0) return cudaSuccess;
+    copy_i32_kernel<<<grid_for(n > n_fill ? n : n_fill, 8), kThreads, 0, s>>>(a.ref, a.out_ref, n, fill, n_fill);
     return cudaGetLastError();
 }
 template <Moves kWhich>
@@ -550,7 +566,7 @@ cudaError_t launch_moves(const swa_page_pool *p, const PagesWs &w, int64_t most,
 
 size_t pages_workspace_bytes(const swa_page_tables *t) {
     return 256 + up256(moves_of(t) * sizeof(Move)) +
-           up256((2 * static_cast<size_t>(t->B) + 3 * static_cast<size_t>(t->n_pages)) * sizeof(int32_t));
+           up256((3 * static_cast<size_t>(t->B) + 3 * static_cast<size_t>(t->n_pages)) * sizeof(int32_t));
 }
 
 cudaError_t launch_reserve(const swa_page_tables *t, const int32_t *first, const int32_t *end, void *ws,
@@ -573,18 +589,18 @@ cudaError_t launch_fork(const swa_page_tables *t, const swa_page_pool *pool, con
                         void *ws, cudaStream_t s) {
     const TableArgs a = table_args(t);
     const PagesWs w = carve(t, ws);
+    const ForkWs f{w.rows0, w.list1};
     cudaError_t e;
     if (static_cast<int64_t>(a.B) * a.width + a.n_pages <= kFew) {
-        fork_plan_kernel<<<kForkCtas, kScanThreads, 0, s>>>(a, src, len, w.rows0, w.rows1, w.list0, w.moves, w.count);
+        fork_plan_kernel<<<kForkCtas, kScanThreads, 0, s>>>(a, src, len, f, w.rows1, w.list0, w.moves, w.count);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     } else {
-        if ((e = copy_ref(a, s)) != cudaSuccess) return e;
+        if ((e = copy_ref(a, s, f.keep, static_cast<int64_t>(a.n_pages) + a.B)) != cudaSuccess) return e;
         const int gx = (a.width + kThreads - 1) / kThreads;
         const dim3 grid(gx < 64 ? gx : 64, a.B < 65535 ? a.B : 65535);
-        if ((e = launch_dependent(a.ref != a.out_ref, fork_table_kernel, grid, kThreads, 0, s, a, src, len, w.rows0)) !=
-            cudaSuccess)
+        if ((e = launch_dependent(true, fork_table_kernel, grid, kThreads, 0, s, a, src, len, f)) != cudaSuccess)
             return e;
-        if ((e = launch_dependent(true, fork_alloc_kernel, dim3(1), kScanThreads, 0, s, a, src, len, w.rows0, w.rows1,
+        if ((e = launch_dependent(true, fork_alloc_kernel, dim3(1), kScanThreads, 0, s, a, src, len, f, w.rows1,
                                   w.list0, w.moves, w.count)) != cudaSuccess)
             return e;
     }

@@ -149,6 +149,97 @@ def test_fork_of_a_large_table(swa, B, most, ps):
     test_fork(swa, B, most, (1, 1, ps, 8))
 
 
+def fork_by_pages(table, ref, src, lens, ps):
+    """The header's rule, page by page: (new table, new counts, [(from, to, tokens)])."""
+    table, ref = np.array(table), np.array(ref)
+    out = np.full_like(table, -1)
+    full, last = {}, {}  # page -> rows that have it as a full one, as a last one that is not
+    for i, s in enumerate(src):
+        if s >= 0:
+            n, part = divmod(int(lens[s]), ps)
+            out[i, :n] = table[s, :n]
+            for p in out[i, :n]:
+                full.setdefault(int(p), []).append(i)
+            if part:
+                last.setdefault(int(table[s, n]), []).append((i, n, part))
+    copies = []
+    for p, rows in last.items():
+        keeps = 0 if p in full else 1
+        for i, n, _ in rows[:keeps]:
+            out[i, n] = p
+        copies += [(i, n, p, part) for i, n, part in rows[keeps:]]
+    count = lambda t: np.bincount(t[t >= 0], minlength=len(ref))  # noqa: E731
+    ref = ref - count(table) + count(out)
+    free, moves = np.flatnonzero(ref == 0), []
+    for (i, n, p, part), q in zip(sorted(copies), free):
+        out[i, n] = q
+        ref[q] = 1
+        moves.append((p, int(q), part))
+    return out, ref, moves
+
+
+@pytest.mark.parametrize("inplace", [True, False])
+@pytest.mark.parametrize("B,most,ps", [(2, 32, 16), (7, 90, 16), (40, 30, 4), (300, 400, 8)], ids=str)
+def test_forks_of_forks(swa, B, most, ps, inplace):
+    """Rows that share pages already, cut back to lengths inside them or on their borders, and forked
+    again: no row may be left with a last page that it would write to and that another row has."""
+    rng = np.random.default_rng(B)
+    width = -(-most // ps)
+    n_pages = 2 * B * width + B
+    k, v = pools(14, 2, n_pages, 1, ps, 8)
+    wk, wv = R.bits(k), R.bits(v)
+    kd, vd = k.cuda(), v.cuda()
+    table = rng.permutation(n_pages)[:B * width].reshape(B, width).astype(np.int32)
+    ref = np.bincount(table.ravel(), minlength=n_pages).astype(np.int32)
+    lens = np.full(B, most)
+    for turn in range(6):
+        src = rng.integers(0, max(1, B // 3), B) if turn % 2 == 0 else np.arange(B)
+        if turn == 5:
+            src = rng.integers(-1, B, B)
+        wt, wr, moves = fork_by_pages(table, ref, src, lens, ps)
+        for p, q, part in moves:
+            for a in (wk, wv):
+                a[:, q, :, :part] = a[:, p, :, :part]
+        t, r = R.i32(table), R.i32(ref)
+        ot, orf = swa.swa_pages_fork(kd, vd, t, r, R.i32(src), R.i32(lens), out_ref=None if inplace else torch.full_like(r, 9))
+        swa.swa_check_device_error()
+        same(ot, wt)
+        same(orf, wr)
+        np.testing.assert_array_equal(R.bits(kd), wk)
+        np.testing.assert_array_equal(R.bits(vd), wv)
+        table, ref, lens = wt, wr, np.where(src >= 0, lens[src], 0)
+        for i in np.flatnonzero(lens % ps):
+            page = table[i, lens[i] // ps]
+            assert page >= 0 and (table == page).sum() == 1, f"turn {turn}: row {i} shares its last page"
+        # rows cut back: anywhere, or by whole pages
+        cut = rng.integers(0, 2 * ps + 1, B) if turn % 3 else rng.integers(0, 3, B) * ps
+        lens = np.maximum(lens - cut, 0)
+
+
+@pytest.mark.parametrize("lens,want,moves", [
+    ([30, 30], [[0, 1], [0, 2]], [(1, 2, 14)]),
+    ([17, 30], [[0, 1], [0, 2]], [(1, 2, 14)]),
+    ([32, 30], [[0, 1], [0, 2]], [(1, 2, 14)]),  # a full page of row 0
+    ([30, 32], [[0, 2], [0, 1]], [(1, 2, 14)]),  # of row 1
+    ([16, 30], [[0, -1], [0, 1]], []),
+    ([9, 30], [[2, -1], [0, 1]], [(0, 2, 9)]),
+], ids=str)
+@pytest.mark.parametrize("wide", [False, True], ids=["one-cluster", "grids"])
+def test_rows_that_shared_a_page_and_were_cut_back(swa, lens, want, moves, wide):
+    k, v = (x.cuda() for x in pools(15, 2, 4, 2, 16, 8))
+    wk, wv = k.clone(), v.clone()
+    for p, q, n in moves:
+        for a in (wk, wv):
+            a[:, q, :, :n] = a[:, p, :, :n]
+    more = 16 * 1024 if wide else 0
+    t, r = R.i32([[0, 1] + [-1] * more, [0, 1] + [-1] * more]), R.i32([2, 2, 0, 0])
+    ot, orf = swa.swa_pages_fork(k, v, t, r, R.i32([0, 1]), R.i32(lens))
+    swa.swa_check_device_error()
+    same(ot[:, :2], want)
+    same(orf, np.bincount([p for row in want for p in row if p >= 0], minlength=4))
+    assert (ot[:, 2:] == -1).all() and torch.equal(k, wk) and torch.equal(v, wv)
+
+
 def test_fork_refusals_and_broken_data(swa):
     k, v = (x.cuda() for x in pools(8, 1, 5, 1, 16, 8))
     t, r = R.i32([[0, 1], [2, -1], [3, 4]]), R.i32([1, 1, 1, 1, 1])
