@@ -95,6 +95,25 @@ def test_attend_rejects(lib, mutate, status):
     assert lib.swa_paged_workspace_size(ctypes.byref(p), ctypes.byref(c)) == 0
 
 
+@pytest.mark.parametrize("group", [1, 3, 4, 8, 16])
+def test_the_hint_chooses_the_kernel_at_any_size(lib, group):
+    """The workspace is the chosen kernel's: few rows up to 16 rows a group, many above, whatever the
+    number of tokens named."""
+    p, c = valid_paged()
+    c.H_kv, p.H_q = 2, 2 * group
+
+    def size(max_q):
+        p.max_q = max_q
+        return lib.swa_paged_workspace_size(ctypes.byref(p), ctypes.byref(c))
+
+    many, few = size(0), size(1)
+    assert 0 < few != many > 0
+    for t in range(1, 40):
+        assert size(t) == (few if t * group <= 16 else many)
+    for t in (1 << 27, 1 << 28, 1 << 29, 1 << 30, (1 << 32) // group // 2 + 1, (1 << 31) - 1):
+        assert size(min(t, (1 << 31) - 1)) == many, t
+
+
 def test_null_structures_are_refused(lib):
     p, c = valid_paged()
     assert lib.swa_paged_attend(ctypes.byref(p), None, FAKE, BIG, None) == 1
