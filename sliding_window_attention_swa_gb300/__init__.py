@@ -672,8 +672,9 @@ def swa_paged_attend(q, k_pages, v_pages, page_table, p0, window: int = 0, scale
         int(max_q), int(window), int(n_sink), D ** -0.5 if scale is None else float(scale), o.data_ptr(),
         lse.data_ptr(), 0 if row_counts is None else row_counts.data_ptr())
     if workspace is None:
-        # (asked once for each of what it depends on: the question takes 2 us of a 24 us call)
-        key = lib._name, index, Hq, H_kv, d_h, max_q, q_start is None
+        # (asked once for each of what it depends on: the question takes 2 us of a 24 us call; more than
+        # 16 tokens a sequence are many rows for every group, so a longer chunk is no other key)
+        key = lib._name, index, Hq, H_kv, d_h, min(max_q, 17), q_start is None
         size = _paged_ws_size.get(key)
         if size is None:
             size = lib.swa_paged_workspace_size(params, cache)

@@ -375,6 +375,17 @@ def test_one_workspace_for_many_calls(swa):
             run(swa, x, append=turn == 1, workspace=ws, q_start=None if one else x.q_start.cuda())
 
 
+def test_few_workspace_sizes_are_kept(swa):
+    # a server whose longest chunk varies: the sizes looked up stay as few as the kernels' shapes
+    x = R.Batch(48, [(5, 2), (3, 1)], 4, 2, 64, 16)
+    a = x.q.cuda(), x.k_pages.cuda(), x.v_pages.cuda(), x.table.cuda(), x.p0.cuda()
+    start, before = x.q_start.cuda(), len(swa._paged_ws_size)
+    for most in [*range(2, 200), 1 << 20, (1 << 31) - 1]:
+        swa.swa_paged_attend(*a, q_start=start, max_q=most)
+    assert len(swa._paged_ws_size) - before <= 17
+    swa.swa_check_device_error()
+
+
 def test_two_streams_at_once(swa):
     xs = [R.Batch(40 + i, [(3000, 70), (10, 1), (900, 200)], 8, 2, 128, 32, 1000) for i in range(4)]
     streams = [torch.cuda.Stream() for _ in range(2)]
