@@ -75,8 +75,8 @@ __device__ __forceinline__ int kept_keys(const PagedArgs &a, int t) {
 //   stretch of the list for each CTA instead, their working sets together (1.1 MB each for the
 //   Gemma-shape window) exceed L2 and every tile comes from HBM.
 //   Tail: the tiles of the last units (between one and two waves of them, or all units of a
-//   smaller batch) are cut into one stretch a CTA, of such lengths that all CTAs end up with the
-//   same number of tiles, whatever the batch looks like.  The pieces of a unit that crosses a
+//   smaller batch) are cut into one stretch a CTA, of such lengths that every CTA ends up with the
+//   mean number of tiles (one whose waves alone have more gets no stretch).  The pieces of a unit that crosses a
 //   border are joined at the end, which takes as long as about kJoinTiles tiles (10 us); where
 //   dealing every unit whole leaves no CTA further above the mean than that, there is no tail.
 // ---------------------------------------------------------------------------------------------
@@ -232,8 +232,9 @@ __device__ __forceinline__ int dealt_to(int u, int grid) {
 }
 
 // This CTA's share, found by the whole block (kThreads threads; scratch in shared memory; block
-// barriers inside, the result valid after the last).  min_tiles: no stretch of the tail is
-// shorter, so that little work is not cut into pieces that cost more than they save.
+// barriers inside, the result valid after the last).  min_tiles: without waves ahead of it the list is
+// cut into stretches of at least that many tiles (but for the last), so that little work is not cut
+// into pieces that cost more than they save.
 template <int BN, int kThreads, bool kWaves>
 __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_tiles, uint8_t *scratch, Share *out,
                                            unsigned int *err) {
@@ -438,36 +439,17 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
             len = max((total + grid - 1) / grid, static_cast<long long>(min_tiles));
             first = len * c;
         } else {
-            // the tail fills the CTAs up to one level: the least at which all of it fits
-            int ld[kPer], top = 0;
+            // the tail fills the CTAs up to the mean; one whose waves alone are above it gets nothing
+            int ld[kPer];
             long long bulk = 0;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 ld[i] = 32 * i + lane < grid ? loads[32 * i + lane] : INT_MAX;
-                if (32 * i + lane < grid) {
-                    bulk += ld[i];
-                    top = max(top, ld[i]);
-                }
+                if (32 * i + lane < grid) bulk += ld[i];
             }
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) bulk += __shfl_xor_sync(0xffffffffu, bulk, o);
-            top = __reduce_max_sync(0xffffffffu, top);
-            const long long tail = total - bulk;
-            int level = static_cast<int>((total + grid - 1) / grid);
-            if (top > level) {  // (some waves alone are above the mean: the others share what is left)
-                int lo = level, hi = top + static_cast<int>((tail + grid - 1) / grid);
-                while (lo < hi) {
-                    const int mid = lo + ((hi - lo) >> 1);
-                    long long room = 0;
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) room += ld[i] < mid ? mid - ld[i] : 0;
-#pragma unroll
-                    for (int o = 16; o >= 1; o >>= 1) room += __shfl_xor_sync(0xffffffffu, room, o);
-                    if (room >= tail) hi = mid;
-                    else lo = mid + 1;
-                }
-                level = lo;
-            }
+            const int level = static_cast<int>((total + grid - 1) / grid);
             long long at = bulk;
             first = len = 0;
             turn = 0;
