@@ -328,7 +328,8 @@ typedef struct swa_paged_cache {
  * past its end (p0 + its new tokens) -- may hold anything.  What the device finds broken is
  * reported by swa_check_device_error as SWA_ERR_INVALID_ARG, and nothing outside the call's
  * buffers is read or written: a sequence whose q_start or p0 is out of range or that does
- * not fit its table row is skipped, its rows left as they were (SWA_DEVERR_BAD_POSITION); a
+ * not fit its table row is skipped, its rows left as they were (SWA_DEVERR_BAD_POSITION); where a
+ * q_start that goes down makes sequences overlap, their rows hold any one's result or stay as they were; a
  * page that is needed but is missing or not in the pool counts as rows of zeros
  * (SWA_DEVERR_BAD_PAGE).
  * Requirements: H_q % H_kv == 0 and H_q / H_kv <= 16; strides multiples of 8 elements and

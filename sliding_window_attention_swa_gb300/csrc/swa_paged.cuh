@@ -231,6 +231,18 @@ __device__ __forceinline__ int dealt_to(int u, int grid) {
     return w & 1 ? grid - 1 - c : c;
 }
 
+// Units of one kv head, counted in 64 bits, for a batch in which some sequence is broken (by one warp; out
+// of line, which costs the others nothing).  Sequences that do not overlap have at most N / TT + B
+// of them.  A q_start that goes down can give each of the others all rows, more work than any
+// call has and more units than 32 bits count: then there is none.
+static __device__ __noinline__ int units_of_broken(const PagedArgs &a, int TT, int lane) {
+    long long n = 0;
+    for (int b = lane; b < a.B; b += 32) n += (load_seq(a, b).n + TT - 1) / TT;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n <= static_cast<long long>(a.N / TT) + a.B ? static_cast<int>(n) : 0;
+}
+
 // This CTA's share, found by the whole block (kThreads threads; scratch in shared memory; block
 // barriers inside, the result valid after the last).  min_tiles: without waves ahead of it the list is
 // cut into stretches of at least that many tiles (but for the last), so that little work is not cut
@@ -339,15 +351,17 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
     int *units = reinterpret_cast<int *>(scratch + a.B * 8);
     int *all_loads = units + a.B + 1, *bulk_loads = all_loads + kMaxWaveCtas;
     // 1. units of one kv head of each sequence, 2. their running sum
+    bool fine = true;
     for (int b = tid; b < a.B; b += kThreads) {
         const Seq s = load_seq(a, b);
+        fine = fine && s.ok;
         if (!s.ok && blockIdx.x == 0) atomicOr(err, SWA_DEVERR_BAD_POSITION);
         units[b] = (s.n + TT - 1) / TT;
         tiles[b] = 0;
     }
     if (kWaves && grid <= kMaxWaveCtas)
         for (int c = tid; c < grid; c += kThreads) all_loads[c] = bulk_loads[c] = 0;
-    __syncthreads();
+    fine = __syncthreads_and(fine);
     if (warp == 0) {
         int before = 0;
         for (int b0 = 0; b0 < a.B; b0 += 32) {
@@ -361,6 +375,7 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
             if (b0 + lane < a.B) units[b0 + lane] = before + inc - v;
             before += __shfl_sync(0xffffffffu, inc, 31);
         }
+        if (!fine) before = units_of_broken(a, TT, lane);
         if (lane == 0) units[a.B] = before;
     }
     __syncthreads();

@@ -319,6 +319,22 @@ def test_broken_device_data(swa, hint):
 
 
 @pytest.mark.parametrize("hint", [0, 1])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_sequences_that_overlap_are_no_work(swa, D, hint):
+    # q_start goes up and down, so that every other sequence has all rows: reported, and not computed (the
+    # units of many such sequences pass what 32 bits count)
+    B, N = 80, 1280
+    start = R.i32([N * (b % 2) for b in range(B + 1)])
+    k = torch.zeros(N // 16, 1, 16, D, dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(N // 16, dtype=torch.int32, device="cuda").repeat(B, 1)
+    q = torch.zeros(N, 2, D, dtype=torch.bfloat16, device="cuda")
+    o, lse = torch.full_like(q, 7), torch.full((N, 2), 7.0, device="cuda")
+    swa.swa_paged_attend(q, k, k.clone(), table, R.i32([0] * B), q_start=start, max_q=hint, o=o, lse=lse)
+    assert error_bits(swa) == (1, {"prefill": 0, "split": 0, "cache": swa.DEVERR_BAD_POSITION})
+    assert (o == 7).all() and (lse == 7).all()
+
+
+@pytest.mark.parametrize("hint", [0, 1])
 def test_captured_and_replayed(swa, hint):
     # two graphs with workspaces of their own, replayed in turn with other lengths and pages
     def batch(seed, seqs):
