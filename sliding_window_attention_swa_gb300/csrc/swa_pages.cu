@@ -5,6 +5,8 @@
 // rank: the r-th page wanted (in the order of rows, then entries) is the r-th free one.
 // Counts change by integer atomics, whose order cannot show in a result.
 //
+// Rows and entries number up to 2^31 - 1: what counts them in steps is unsigned or has 64 bits.
+//
 // Tables and counts are small beside the pages: they are bound by launches and latency.  The
 // copies of page contents are bound by HBM (2 bytes moved per byte of page).
 #include <climits>
@@ -137,25 +139,27 @@ __global__ void __launch_bounds__(kScanThreads) reserve_kernel(const TableArgs a
     __shared__ ScanSmem sm;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t cap = static_cast<int64_t>(a.width) * a.ps;
+    const uint32_t B = static_cast<uint32_t>(a.B);
     // entries [j0, j1) of row b are wanted
-    auto range = [&](int b, int &j0, int &j1) {
+    auto range = [&](uint32_t b, uint32_t &j0, uint32_t &j1) {
         const int64_t f = first[b], e = end[b];
         j0 = j1 = 0;
         if (e <= f) return true;
         if (f < 0 || e > cap) return false;
-        j0 = static_cast<int>(f / a.ps);
-        j1 = static_cast<int>((e + a.ps - 1) / a.ps);
+        j0 = static_cast<uint32_t>(f / a.ps);
+        j1 = static_cast<uint32_t>((e + a.ps - 1) / a.ps);
         return true;
     };
-    auto missing = [&](int b, int j) {
+    auto missing = [&](uint32_t b, uint32_t j) {
         const int e = a.out_table[static_cast<int64_t>(b) * a.width + j];
         return e < 0 || e >= a.n_pages;
     };
     // 1. pages that each row lacks (a warp per row)
-    for (int b = warp; b < a.B; b += kScanWarps) {
-        int j0, j1, n = 0;
+    for (uint32_t b = warp; b < B; b += kScanWarps) {
+        uint32_t j0, j1;
+        int n = 0;
         if (!range(b, j0, j1) && lane == 0) atomicOr(&g_pages_err, kErrBadPosition);
-        for (int j = j0 + lane; j < j1; j += 32) {
+        for (uint32_t j = j0 + lane; j < j1; j += 32) {
             if (!missing(b, j)) continue;
             if (a.out_table[static_cast<int64_t>(b) * a.width + j] >= a.n_pages) atomicOr(&g_pages_err, kErrBadPage);
             ++n;
@@ -167,9 +171,9 @@ __global__ void __launch_bounds__(kScanThreads) reserve_kernel(const TableArgs a
     // 2. each row's first rank: an exclusive prefix over the rows
     __shared__ int wsum[kScanWarps];
     int total = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kScanThreads) {
-        const int b = b0 + tid;
-        const int n = b < a.B ? ws_row[b] : 0;
+    for (uint32_t b0 = 0; b0 < B; b0 += kScanThreads) {
+        const uint32_t b = b0 + tid;
+        const int n = b < B ? ws_row[b] : 0;
         int inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -183,7 +187,7 @@ __global__ void __launch_bounds__(kScanThreads) reserve_kernel(const TableArgs a
             if (w < warp) before += wsum[w];
             all += wsum[w];
         }
-        if (b < a.B) ws_row[b] = total + before + inc - n;
+        if (b < B) ws_row[b] = total + before + inc - n;
         total += all;
         __syncthreads();
     }
@@ -191,12 +195,12 @@ __global__ void __launch_bounds__(kScanThreads) reserve_kernel(const TableArgs a
     // 3. the lowest free pages, 4. dealt to the rows in order
     const int found = take_free(sm, a.out_ref, a.n_pages, min(total, a.n_pages), list);
     __syncthreads();
-    for (int b = warp; b < a.B; b += kScanWarps) {
-        int j0, j1;
+    for (uint32_t b = warp; b < B; b += kScanWarps) {
+        uint32_t j0, j1;
         range(b, j0, j1);
         int rank = ws_row[b];
-        for (int jb = j0; jb < j1; jb += 32) {
-            const int j = jb + lane;
+        for (uint32_t jb = j0; jb < j1; jb += 32) {
+            const uint32_t j = jb + lane;
             const bool want = j < j1 && missing(b, j);
             const unsigned bal = __ballot_sync(0xffffffffu, want);
             if (want) {
@@ -310,13 +314,14 @@ __global__ void __launch_bounds__(kThreads) fork_table_kernel(const TableArgs a,
                                                               const int32_t *len, const ForkWs w) {
     let_next_start();
     wait_for_previous();
-    for (int i = blockIdx.y; i < a.B; i += gridDim.y) {
+    for (uint32_t y = blockIdx.y; y < static_cast<uint32_t>(a.B); y += gridDim.y) {
+        const int i = static_cast<int>(y);
         int s, n;
         const bool ok = fork_source(a, src, len, i, s, n);
         if (!ok && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(&g_pages_err, kErrBadPosition);
         const int part = n % a.ps, last = n / a.ps;
-        for (int j = blockIdx.x * kThreads + threadIdx.x; j < a.width; j += gridDim.x * kThreads)
-            fork_entry(a, w, i, j, s, part, last);
+        for (uint32_t j = blockIdx.x * kThreads + threadIdx.x; j < static_cast<uint32_t>(a.width); j += gridDim.x * kThreads)
+            fork_entry(a, w, i, static_cast<int>(j), s, part, last);
     }
 }
 
@@ -330,13 +335,13 @@ __device__ __forceinline__ void fork_alloc(ScanSmem &sm, const TableArgs &a, con
             sm, base, a.B, want, [&](int i) { return wants_own(a, w, i); }, [&](int i, int r) { row_of[r] = i; });
     const int found = want ? take_free(sm, a.out_ref, a.n_pages, min(want, a.n_pages), list) : 0;
     __syncthreads();
-    for (int r = threadIdx.x; r < want; r += kScanThreads) {
+    for (uint32_t r = threadIdx.x; r < static_cast<uint32_t>(want); r += kScanThreads) {
         const int i = row_of[r], s = src[i], n = len[s], last = n / a.ps;
         const int old = w.last_of[i];
         // (whoever keeps the page still holds it, so it was not among the free ones)
         if (old >= 0) atomicSub(a.out_ref + old, 1);
         Move m{-1, -1, n % a.ps, 0};
-        if (r < found) {
+        if (r < static_cast<uint32_t>(found)) {
             m.dst = list[r];
             a.out_ref[m.dst] = 1;
             if (old >= 0) m.src = old;
@@ -596,7 +601,7 @@ cudaError_t launch_fork(const swa_page_tables *t, const swa_page_pool *pool, con
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     } else {
         if ((e = copy_ref(a, s, f.keep, static_cast<int64_t>(a.n_pages) + a.B)) != cudaSuccess) return e;
-        const int gx = (a.width + kThreads - 1) / kThreads;
+        const int gx = (a.width - 1) / kThreads + 1;
         const dim3 grid(gx < 64 ? gx : 64, a.B < 65535 ? a.B : 65535);
         if ((e = launch_dependent(true, fork_table_kernel, grid, kThreads, 0, s, a, src, len, f)) != cudaSuccess)
             return e;

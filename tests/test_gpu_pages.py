@@ -290,6 +290,33 @@ def test_compact(swa, B, width, n_pages, shape, inplace):
             same(r, ref)
 
 
+def test_a_row_as_long_as_a_call_takes(swa):
+    # 2^31 - 1 entries: the steps behind the last one pass 2^31
+    last = (1 << 31) - 1
+    k, v = (x.cuda() for x in pools(16, 1, 5, 1, 1, 8))
+    table, ref = torch.full((1, last), -1, dtype=torch.int32, device="cuda"), R.i32([0, 1, 0, 0, 0])
+    swa.swa_pages_reserve(table, ref, R.i32([last - 3]), R.i32([last]), 1)
+    swa.swa_check_device_error()
+    same(table[0, -4:], [-1, 0, 2, 3])
+    same(ref, [1, 1, 1, 1, 0])
+    out, _ = swa.swa_pages_fork(k, v, table, ref, R.i32([0]), R.i32([last]))
+    swa.swa_check_device_error()
+    assert torch.equal(out, table)
+    same(ref, [1, 1, 1, 1, 0])
+    swa.swa_pages_free(table, ref, R.i32([last - 1]), 1, n_sink=last - 2, out_table=out, out_ref=ref.clone())
+    same(out[0, -4:], [-1, 0, -1, 3])
+    swa.swa_pages_free(table, ref, R.i32([last - 2]), 1)
+    swa.swa_check_device_error()
+    same(table[0, -4:], [-1, -1, 2, 3])
+    same(ref, [0, 1, 1, 1, 0])
+    want = k[0, 3].clone()
+    _, _, live = swa.swa_pages_compact(k, v, table, ref)
+    swa.swa_check_device_error()
+    same(table[0, -4:], [-1, -1, 2, 0])
+    same(ref, [1, 1, 1, 0, 0])
+    assert live.item() == 3 and torch.equal(k[0, 0], want) and int((table >= 0).sum()) == 2
+
+
 @pytest.mark.parametrize("layers", [None, 3])
 def test_copy(swa, layers):
     k, v = pools(11, layers or 1, 9, 2, 32, 64)
