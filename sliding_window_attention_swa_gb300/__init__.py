@@ -562,6 +562,12 @@ def _device_index(name, t) -> int:
     return index
 
 
+def _own_workspace(workspace, index: int) -> None:
+    """A workspace that the caller gives: the kernels write to its address, whatever device that is on."""
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{index}")
+
+
 def _raw_stream(index: int) -> int:
     import torch
 
@@ -681,6 +687,8 @@ def swa_paged_attend(q, k_pages, v_pages, page_table, p0, window: int = 0, scale
             if size:  # (0: refused, below)
                 _paged_ws_size[key] = size
         workspace = torch.empty(size or 1, dtype=torch.uint8, device=device)
+    else:
+        _own_workspace(workspace, index)
     st = lib.swa_paged_attend(params, cache, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                               _raw_stream(index))
     if st != 0:
@@ -749,6 +757,8 @@ def _pages_workspace(lib, tables, workspace, device):
 
     if workspace is None:
         workspace = torch.empty(lib.swa_pages_workspace_size(tables) or 1, dtype=torch.uint8, device=device)
+    else:
+        _own_workspace(workspace, device.index)
     return workspace, workspace.numel() * workspace.element_size()
 
 

@@ -498,3 +498,22 @@ def test_refusals(swa):
                                      q_start=torch.zeros(3, dtype=torch.int32, device="cuda"))
     assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
     swa.swa_check_device_error()
+
+
+def test_workspaces_of_another_kind_are_refused(swa):
+    # (one in host memory would be written to by the kernels)
+    x = R.Batch(61, [(5, 2), (3, 1)], 4, 2, 64, 16)
+    a = [t.cuda() for t in (x.q, x.k_pages, x.v_pages, x.table, x.p0)]
+    start, ref = x.q_start.cuda(), torch.zeros(x.n_pages, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for ws in (torch.empty(64 << 20, dtype=torch.uint8), torch.empty(64 << 20, dtype=torch.uint8).pin_memory(),
+               torch.empty(64 << 20, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            swa.swa_paged_attend(*a, q_start=start, workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            swa.swa_pages_reserve(a[3], ref, zero, zero, 16, workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            swa.swa_pages_fork(*a[1:4], ref, zero, zero, workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            swa.swa_pages_compact(*a[1:4], ref, workspace=ws)
+    swa.swa_check_device_error()
