@@ -548,6 +548,21 @@ _PAGE_TABLES = struct.Struct("4P4i")
 _PAGE_POOL = struct.Struct("2Pq5i")
 
 
+def _packed(layout, *values) -> bytes:
+    try:
+        return layout.pack(*values)
+    except struct.error as e:
+        raise ValueError(f"a size, window or hint that 32 bits do not hold: {e}") from None
+
+
+def _int32(name, value) -> int:
+    """An argument of its own (ctypes would pass its low 32 bits)."""
+    value = int(value)
+    if not -(1 << 31) <= value < 1 << 31:
+        raise ValueError(f"{name}: {value} does not fit 32 bits")
+    return value
+
+
 def _i32_wrong(name, shape, index):
     return ValueError(f"{name}: expected a contiguous int32 tensor of shape {list(shape)} on cuda:{index}")
 
@@ -606,8 +621,8 @@ def _paged_cache(k_pages, v_pages, page_table, p0, q_start, N: int):
             not q_start.is_contiguous():
         raise _i32_wrong("q_start", (B + 1,), index)
     n_pages, H_kv, page_size, D = shape
-    return index, _PAGED_CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), n_pages, page_size,
-                                    H_kv, D, B, width), H_kv, D
+    return index, _packed(_PAGED_CACHE, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), n_pages,
+                          page_size, H_kv, D, B, width), H_kv, D
 
 
 def _rows(name, t, index: int, shape) -> tuple:
@@ -673,10 +688,10 @@ def swa_paged_attend(q, k_pages, v_pages, page_table, p0, window: int = 0, scale
         raise _i32_wrong("row_counts", (N, Hq), index)
     if N == 0:
         return o, lse, row_counts
-    params = _PAGED_PARAMS.pack(
-        q.data_ptr(), *new, p0.data_ptr(), 0 if q_start is None else q_start.data_ptr(), *q_st, *new_st, *o_st, N, Hq,
-        int(max_q), int(window), int(n_sink), D ** -0.5 if scale is None else float(scale), o.data_ptr(),
-        lse.data_ptr(), 0 if row_counts is None else row_counts.data_ptr())
+    params = _packed(
+        _PAGED_PARAMS, q.data_ptr(), *new, p0.data_ptr(), 0 if q_start is None else q_start.data_ptr(), *q_st,
+        *new_st, *o_st, N, Hq, int(max_q), int(window), int(n_sink), D ** -0.5 if scale is None else float(scale),
+        o.data_ptr(), lse.data_ptr(), 0 if row_counts is None else row_counts.data_ptr())
     if workspace is None:
         # (asked once for each of what it depends on: the question takes 2 us of a 24 us call; more than
         # 16 tokens a sequence are many rows for every group, so a longer chunk is no other key)
@@ -705,8 +720,8 @@ def swa_paged_append(k_pages, v_pages, page_table, k_new, v_new, p0, *, q_start=
     new, new_st = _new_rows(k_new, v_new, index, (N, H_kv, D))
     if N == 0:
         return
-    params = _PAGED_PARAMS.pack(0, *new, p0.data_ptr(), 0 if q_start is None else q_start.data_ptr(), 0, 0, *new_st,
-                                0, 0, N, 0, 0, 0, 0, 0.0, 0, 0, 0)
+    params = _packed(_PAGED_PARAMS, 0, *new, p0.data_ptr(), 0 if q_start is None else q_start.data_ptr(), 0, 0,
+                     *new_st, 0, 0, N, 0, 0, 0, 0, 0.0, 0, 0, 0)
     st = load_library().swa_paged_append(params, cache, _raw_stream(index))
     if st != 0:
         raise SwaError("swa_paged_append", st)
@@ -729,8 +744,8 @@ def _page_tables(page_table, ref, page_size: int, out_table, out_ref):
     shape, n = page_table.shape, ref.shape
     _lists(index, ("page_table", page_table, shape), ("ref", ref, n), ("out_table", out_table, shape),
            ("out_ref", out_ref, n))
-    return index, _PAGE_TABLES.pack(page_table.data_ptr(), ref.data_ptr(), out_table.data_ptr(), out_ref.data_ptr(),
-                                    shape[0], shape[1], n[0], int(page_size)), shape[0]
+    return index, _packed(_PAGE_TABLES, page_table.data_ptr(), ref.data_ptr(), out_table.data_ptr(),
+                          out_ref.data_ptr(), shape[0], shape[1], n[0], int(page_size)), shape[0]
 
 
 def _page_pool(k_pages, v_pages):
@@ -748,8 +763,8 @@ def _page_pool(k_pages, v_pages):
     n, H, ps, D = shape[-4:]
     if st[-4:] != (H * ps * D, ps * D, D, 1) and not (k_pages if len(shape) == 4 else k_pages[0]).is_contiguous():
         raise ValueError("k_pages, v_pages: expected each layer's pages to be contiguous")
-    return index, _PAGE_POOL.pack(k_pages.data_ptr(), v_pages.data_ptr(), st[0] if len(shape) == 5 else 0, layers, n, H,
-                                  ps, D), ps
+    return index, _packed(_PAGE_POOL, k_pages.data_ptr(), v_pages.data_ptr(), st[0] if len(shape) == 5 else 0, layers,
+                          n, H, ps, D), ps
 
 
 def _pages_workspace(lib, tables, workspace, device):
@@ -787,7 +802,7 @@ def swa_pages_free(page_table, ref, below, page_size: int, *, n_sink: int = 0, o
     out_table, out_ref = page_table if out_table is None else out_table, ref if out_ref is None else out_ref
     index, t, B = _page_tables(page_table, ref, page_size, out_table, out_ref)
     _lists(index, ("below", below, (B,)))
-    st = load_library().swa_pages_free(t, below.data_ptr(), int(n_sink), _raw_stream(index))
+    st = load_library().swa_pages_free(t, below.data_ptr(), _int32("n_sink", n_sink), _raw_stream(index))
     if st != 0:
         raise SwaError("swa_pages_free", st)
     return out_table, out_ref
@@ -850,7 +865,7 @@ def swa_pages_copy(k_pages, v_pages, src, dst, *, stream=None) -> None:
     if src.dim() != 1:
         raise ValueError("src: expected int32 [n]")
     _lists(index, ("src", src, src.shape), ("dst", dst, src.shape))
-    st = load_library().swa_pages_copy(pool, src.data_ptr(), dst.data_ptr(), src.shape[0], _raw_stream(index))
+    st = load_library().swa_pages_copy(pool, src.data_ptr(), dst.data_ptr(), _int32("n", src.shape[0]), _raw_stream(index))
     if st != 0:
         raise SwaError("swa_pages_copy", st)
 

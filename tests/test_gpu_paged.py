@@ -517,3 +517,19 @@ def test_workspaces_of_another_kind_are_refused(swa):
         with pytest.raises(ValueError, match="workspace"):
             swa.swa_pages_compact(*a[1:4], ref, workspace=ws)
     swa.swa_check_device_error()
+
+
+def test_numbers_that_32_bits_do_not_hold_are_refused(swa):
+    x = R.Batch(62, [(5, 2), (3, 1)], 4, 2, 64, 16)
+    a = [t.cuda() for t in (x.q, x.k_pages, x.v_pages, x.table, x.p0)]
+    start, ref = x.q_start.cuda(), torch.ones(x.n_pages, dtype=torch.int32, device="cuda")
+    for kw in (dict(window=1 << 31), dict(n_sink=1 << 32), dict(max_q=1 << 31), dict(scale=1e39)):
+        with pytest.raises(swa.SwaError if "scale" in kw else ValueError):  # (packed as infinity)
+            swa.swa_paged_attend(*a, q_start=start, **kw)
+    below = torch.full((2,), 1 << 20, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        swa.swa_pages_free(a[3], ref, below, 16, n_sink=1 << 32)  # (its low 32 bits are 0)
+    with pytest.raises(ValueError):
+        swa.swa_pages_free(a[3], ref, below, 1 << 31)
+    assert torch.equal(a[3].cpu(), x.table)
+    swa.swa_check_device_error()
