@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedArgs 
             if (lane == 0) atomicOr(&g_paged_err, SWA_DEVERR_BAD_PAGE);
             continue;
         }
+        if (!SWA_IN_BOUNDS(b < a.B && page >= 0 && p >= 0 && p >> a.ps_log2 < a.width, &g_paged_err)) continue;
         const int64_t row = static_cast<int64_t>(page) * a.H_kv * a.ps + (p & (a.ps - 1));
         const int P = a.D / 8;  // 16-byte pieces of one head's row
         for (int x = lane; x < 2 * a.H_kv * P; x += 32) {

@@ -366,7 +366,9 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
             const int t = w * 32 + lane, r = t >> 3, part = t & 7;
             const int64_t tok = p.s.q0 + p.ut * TT + r / a.G;
             const int h = p.kvh * a.G + r % a.G;
-            if (r < rows && SWA_IN_BOUNDS(tok < a.N && h < a.H_q, &g_psplit_err)) {
+            // (a piece's partial result: two slots a CTA)
+            if (r < rows && SWA_IN_BOUNDS(tok < a.N && h < a.H_q && piece_slot(p) < 2 * static_cast<int>(gridDim.x),
+                                          &g_psplit_err)) {
                 float mw = -INFINITY;
 #pragma unroll
                 for (int ww = 0; ww < 4; ++ww) mw = fmaxf(mw, red_m[ww * ROWS + r]);
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
     }
     const Seq s = load_seq(a, rec.y);
     const int i = rec.w * TT + row / a.G;  // token of the sequence
-    if (i >= s.n) return;
+    if (i >= s.n || !SWA_IN_BOUNDS(c + np <= ctas && rec.y < a.B && rec.z < a.H_kv, &g_psplit_err)) return;
     auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)); };
     auto piece = [&](int k) { return *reinterpret_cast<const float2 *>(w.ml + (slot(k) * ROWS + row) * 2); };
     float m = -INFINITY;

@@ -823,7 +823,13 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             const int tq = r / a.G, i0 = wk->ut * TT + (single ? 0 : ow * ta.TQ);  // the tile's first token
             const int64_t tok = static_cast<int64_t>(wk->q0) + i0 + tq;
             const int h = wk->kvh * a.G + r % a.G;
-            const bool store = tq < min(wk->n - i0, ta.TQ) && SWA_IN_BOUNDS(tok < a.N && h < a.H_q, &g_ptile_err);
+            // debug build: the row exists; a shared unit's slots do, of this piece and of all others
+            const bool store =
+                tq < min(wk->n - i0, ta.TQ) &&
+                SWA_IN_BOUNDS(tok < a.N && h < a.H_q &&
+                                  (whole || (wk->slot >= 0 && wk->slot < 2 * static_cast<int>(gridDim.x) && wk->owner >= 0 &&
+                                             wk->owner + unit_pieces <= static_cast<int>(gridDim.x))),
+                              &g_ptile_err);
             uint16_t *orow = a.o + tok * a.o_st[0] + h * a.o_st[1];
             const int pslot = wk->slot, prow = (single ? 0 : ow * BM) + r;
             // (a shared query tile: each warpgroup keeps the maximum and sum beside its half of the columns)

@@ -40,6 +40,9 @@ constexpr int kFew = 16 * 1024;
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Debug build: `x` is an index into n (release build: true).
+__device__ __forceinline__ bool within(int64_t x, int64_t n) { return SWA_IN_BOUNDS(x >= 0 && x < n, &g_pages_err); }
+
 // One page copy: the first `rows` positions of page src go to page dst (src < 0: none).
 // ref: the moved page's holders (compaction).
 struct Move {
@@ -116,7 +119,7 @@ __device__ __forceinline__ int take_free(ScanSmem &sm, const int32_t *ref, int n
         found = scan_step(
             sm, base, n_pages, found, [&](int p) { return ref[p] == 0; },
             [&](int p, int r) {
-                if (r < need) list[r] = p;
+                if (r < need && within(r, n_pages) && within(p, n_pages)) list[r] = p;
             });
     return min(found, need);
 }
@@ -203,12 +206,12 @@ __global__ void __launch_bounds__(kScanThreads) reserve_kernel(const TableArgs a
             const uint32_t j = jb + lane;
             const bool want = j < j1 && missing(b, j);
             const unsigned bal = __ballot_sync(0xffffffffu, want);
-            if (want) {
+            if (want && within(j, a.width)) {
                 const int r = rank + __popc(bal & ((1u << lane) - 1u));
                 int page = -1;
                 if (r < found) {
-                    page = list[r];
-                    a.out_ref[page] = 1;
+                    page = within(r, a.n_pages) ? list[r] : -1;
+                    if (within(page, a.n_pages)) a.out_ref[page] = 1;
                 } else {
                     atomicOr(&g_pages_err, kErrNoPage);
                 }
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) free_kernel(const TableArgs a, const
             atomicOr(&g_pages_err, kErrBadPage);
             e = -1;
         }
-        if (e >= 0 && (bl < 0 || ((j + 1) * a.ps <= bl && j * a.ps >= n_sink))) {
+        if (e >= 0 && within(b, a.B) && within(j, a.width) && (bl < 0 || ((j + 1) * a.ps <= bl && j * a.ps >= n_sink))) {
             if (atomicSub(a.out_ref + e, 1) <= 0) {
                 atomicAdd(a.out_ref + e, 1);
                 atomicOr(&g_pages_err, kErrBadRef);
@@ -285,6 +288,7 @@ __device__ __forceinline__ bool wants_own(const TableArgs &a, const ForkWs &w, i
 // Row i keeps its own holders where both tables have the same entry (no atomics); the others change.
 // Every row gets its last page here; those that want one of their own lose it again in fork_alloc.
 __device__ __forceinline__ void fork_entry(const TableArgs &a, const ForkWs &w, int i, int j, int s, int part, int last) {
+    if (!within(i, a.B) || !within(j, a.width) || !within(s + 1, static_cast<int64_t>(a.B) + 1)) return;
     int in = a.table[static_cast<int64_t>(i) * a.width + j];
     const bool is_last = part && j == last;
     int out = s >= 0 && (j < last || is_last) ? a.table[static_cast<int64_t>(s) * a.width + j] : -1;
@@ -336,7 +340,9 @@ __device__ __forceinline__ void fork_alloc(ScanSmem &sm, const TableArgs &a, con
     const int found = want ? take_free(sm, a.out_ref, a.n_pages, min(want, a.n_pages), list) : 0;
     __syncthreads();
     for (uint32_t r = threadIdx.x; r < static_cast<uint32_t>(want); r += kScanThreads) {
+        if (!within(r, a.B) || !within(row_of[r], a.B) || !within(src[row_of[r]], a.B)) continue;
         const int i = row_of[r], s = src[i], n = len[s], last = n / a.ps;
+        if (!within(last, a.width) || !within(r < static_cast<uint32_t>(found) ? list[r] : 0, a.n_pages)) continue;
         const int old = w.last_of[i];
         // (whoever keeps the page still holds it, so it was not among the free ones)
         if (old >= 0) atomicSub(a.out_ref + old, 1);
@@ -409,7 +415,11 @@ __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const TableA
         live = scan_step(sm, base, a.n_pages, live, [&](int p) { return a.ref[p] > 0; }, [](int, int) {});
     int nh = 0, nm = 0;
     for (int64_t base = 0; base < live; base += kScanItems * kScanThreads)
-        nh = scan_step(sm, base, live, nh, [&](int p) { return a.ref[p] <= 0; }, [&](int p, int r) { holes[r] = p; });
+        nh = scan_step(
+            sm, base, live, nh, [&](int p) { return a.ref[p] <= 0; },
+            [&](int p, int r) {
+                if (within(r, a.n_pages)) holes[r] = p;
+            });
     for (int64_t base = live; base < a.n_pages; base += kScanItems * kScanThreads)
         nm = scan_step(
             sm, base, a.n_pages, nm,
@@ -417,10 +427,14 @@ __global__ void __launch_bounds__(kScanThreads) compact_plan_kernel(const TableA
                 to[p] = -1;  // (a table entry may wrongly name a free page)
                 return a.ref[p] > 0;
             },
-            [&](int p, int r) { movers[r] = p; });
+            [&](int p, int r) {
+                if (within(r, a.n_pages)) movers[r] = p;
+            });
+    (void)within(nm, static_cast<int64_t>(nh) + 1);
     __syncthreads();
     for (int r = threadIdx.x; r < nm; r += kScanThreads) {  // nh == nm: as many holes below M as live pages above
         const int s = movers[r], d = holes[r];
+        if (!within(s, a.n_pages) || !within(d, live)) continue;
         to[s] = d;
         moves[r] = Move{s, d, a.ps, a.ref[s]};
     }
@@ -453,7 +467,8 @@ __device__ __forceinline__ void compact_apply(const ApplyArgs &x, const Move *mo
         if (p >= live) a.out_ref[p] = 0;
         else if (a.ref != a.out_ref && a.ref[p] > 0) a.out_ref[p] = a.ref[p];
     }
-    for (int64_t r = t0; r < nm; r += step) a.out_ref[moves[r].dst] = moves[r].ref;
+    for (int64_t r = t0; r < nm; r += step)
+        if (within(moves[r].dst, live)) a.out_ref[moves[r].dst] = moves[r].ref;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -494,6 +509,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const PoolArgs a, const 
             if (kPairs && x == 0 && lane == 0) atomicOr(&g_pages_err, kErrBadPage);
             continue;
         }
+        if (!within(m.rows, a.ps + 1ll) || !within(l, a.L)) continue;
         const int64_t head = static_cast<int64_t>(a.ps) * a.row, page = head * a.H;
         uint4 *base = (kv ? a.pool[1] : a.pool[0]) + l * a.layer_stride + h * head;
         const uint4 *s = base + m.src * page;

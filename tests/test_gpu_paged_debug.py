@@ -69,3 +69,20 @@ def test_pages(swa):
     PAGES.test_fork(swa, 6, 200, (3, 2, 32, 128))
     PAGES.test_compact(swa, 30, 9, 400, (1, 2, 32, 64), False)
     PAGES.test_serving_run(swa)
+
+
+@pytest.mark.parametrize("inplace", [True, False])
+def test_pages_of_every_plan(swa, inplace):
+    # one cluster's plan of a fork and the grids', tables and pools of several scan steps
+    PAGES.test_forks_of_forks(swa, 40, 30, 4, inplace)
+    PAGES.test_forks_of_forks(swa, 300, 400, 8, inplace)
+    PAGES.test_compact(swa, 9, 4000, 50000, (1, 1, 1, 8), inplace)
+    PAGES.test_free(swa, 700, 33, 20000, 1, 3, inplace)
+    PAGES.test_reserve(swa, 1500, 4, 20000, 128)
+    PAGES.test_copy(swa, 3)
+
+
+def test_tiles_from_hbm_and_pairs(swa):
+    PAGED.test_tiles_that_come_from_hbm(swa, 1024, 400, 32)
+    PAGED.test_pairs_of_one_key_tile_behind_single_query_tiles(swa, (32, 8, 128))
+    PAGED.test_sequences_that_overlap_are_no_work(swa, 64, 0)
