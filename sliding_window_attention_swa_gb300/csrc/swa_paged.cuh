@@ -155,6 +155,53 @@ struct Walk {
     }
 };
 
+// A CTA's pieces one by one, found by one warp: its whole units, one a wave, then its stretch of the
+// list.  The sequences are searched 32 at a time from block b0, whose first unit is u0.
+template <int BN>
+struct Plan {
+    const PagedArgs *args;
+    int TT, waves, w, b0, u0;
+    Walk<BN> walk;
+    __device__ __forceinline__ Plan(const PagedArgs &a, int tt, const Share &sh)
+        : args(&a), TT(tt), waves(sh.waves), w(0), b0(0), u0(0), walk(a, tt, sh) {}
+    __device__ __forceinline__ bool next(Piece &p, int lane) {
+        const PagedArgs &a = *args;
+        if (w >= waves) return walk.next(p);
+        const int grid = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+        const int u = w * grid + (w & 1 ? grid - 1 - c : c);
+        ++w;
+        while (b0 < a.B) {
+            Seq s{};
+            if (b0 + lane < a.B) s = load_seq(a, b0 + lane);
+            const int nu = (s.n + TT - 1) / TT, v = nu * a.H_kv;
+            int inc = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += t;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, u0 + inc > u);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                const int rel = u - u0 - __shfl_sync(0xffffffffu, inc - v, l);
+                const int units = max(__shfl_sync(0xffffffffu, nu, l), 1);
+                p.b = b0 + l;
+                p.kvh = rel / units;
+                p.ut = rel % units;
+                p.s = Seq{__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.n, l),
+                          __shfl_sync(0xffffffffu, s.p0, l), true};
+                p.u = unit_tiles<BN>(a, p.s, p.ut, TT);
+                p.j0 = 0;
+                p.j1 = p.u.n;
+                return true;
+            }
+            u0 += __shfl_sync(0xffffffffu, inc, 31);
+            b0 += 32;
+        }
+        return false;  // (the last wave has no unit for this CTA)
+    }
+};
+
 // Element (row, col) of the partial results of a slot of `rows` rows: 8 columns of a row together,
 // then the same columns of the next row, so that a warp whose lanes have a row each stores whole
 // lines.

@@ -955,49 +955,9 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         // ============================ planner ============================
         regs_dec<C::REG_CTRL>();
         const Share sh = *share;
-        const int grid = static_cast<int>(gridDim.x);
         bool ok = true;
         Piece p{};
-        Walk<BN> walk(a, TT, sh);
-        // Whole units, one a wave: the sequences are searched 32 at a time from block b0, whose first
-        // unit is u0.  Then the share's stretch.
-        int w = 0, b0 = 0, u0 = 0;
-        auto next_piece = [&]() -> bool {
-            if (w >= sh.waves) {
-                return walk.next(p);
-            }
-            const int c = static_cast<int>(blockIdx.x), u = w * grid + (w & 1 ? grid - 1 - c : c);
-            ++w;
-            while (b0 < a.B) {
-                Seq s{};
-                if (b0 + lane < a.B) s = load_seq(a, b0 + lane);
-                const int nu = (s.n + TT - 1) / TT, v = nu * a.H_kv;
-                int inc = v;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int t = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += t;
-                }
-                const unsigned past = __ballot_sync(0xffffffffu, u0 + inc > u);
-                if (past) {
-                    const int l = __ffs(past) - 1;
-                    const int rel = u - u0 - __shfl_sync(0xffffffffu, inc - v, l);
-                    const int units = max(__shfl_sync(0xffffffffu, nu, l), 1);
-                    p.b = b0 + l;
-                    p.kvh = rel / units;
-                    p.ut = rel % units;
-                    p.s = Seq{__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.n, l),
-                              __shfl_sync(0xffffffffu, s.p0, l), true};
-                    p.u = unit_tiles<BN>(a, p.s, p.ut, TT);
-                    p.j0 = 0;
-                    p.j1 = p.u.n;
-                    return true;
-                }
-                u0 += __shfl_sync(0xffffffffu, inc, 31);
-                b0 += 32;
-            }
-            return false;  // (cannot be: the waves' units exist)
-        };
+        Plan<BN> plan(a, TT, sh);
         int k = 0, kq = 0;  // pieces handed over, query tiles loaded
         int loads0 = 0, loads1 = 0, y = 1;  // query tiles of each buffer; y: the last unit of one took that
         bool more = true;
@@ -1016,7 +976,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                         if (!ok) break;
                     }
                 }
-                more = next_piece();
+                more = plan.next(p, lane);
                 if (!more) p.j0 = p.j1 = 0;  // the end of the list
                 if (lane == 0) {
                     volatile TilePiece *t = pieces + e;
