@@ -316,16 +316,44 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 phase ^= 1u;
             }
         };
-        uint32_t mine = 0, mine_phase = 0;  // slots that hold a fill of this warp, and its phase
+        int q0 = -2, q1 = -2, q2 = -2;  // where the query tiles of the last three pieces lie among the fills
         // the slot is free (its last occupant released; at first it is) and `bytes` are expected on it
         auto take_slot = [&](int bytes) -> bool {
             if (fills >= ta.fault_stop_fill) return false;  // planted fault: this fill is never issued
             if (!warp_wait(bar_empty(slot), phase ^ 1u, abort)) return false;
             if (lane == 0) mbar_arrive_expect_tx(bar_full(slot), static_cast<uint32_t>(bytes));
             __syncwarp();
-            mine |= 1u << slot;
-            mine_phase = (mine_phase & ~(1u << slot)) | (phase << slot);
             return true;
+        };
+        // On the way out: until this warp's copies have landed (lane 0).  The other producer may have refilled a
+        // slot since, so that a full barrier is a phase further than this warp's last fill of it: then that
+        // fill was released, and one that was has landed, as have all of this warp's before it.  What can still
+        // be in flight is among the last NSLOT + 2 fills up to this warp's last one.
+        auto drain = [&]() {
+            auto own = [&](int p) -> bool {
+                const bool query = NQT == 1 && (static_cast<unsigned>(p - q0) < 2u || static_cast<unsigned>(p - q1) < 2u ||
+                                                static_cast<unsigned>(p - q2) < 2u);
+                return query ? !values : ((p & 1) != 0) == values;
+            };
+            int last = fills - 1;
+            while (last >= 0 && !own(last)) --last;
+            const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+            while (true) {
+                bool later = false, all = true;
+#pragma unroll 1
+                for (int p = last; p >= 0 && p >= last - NSLOT - 1; --p) {
+                    if (!own(p)) continue;
+                    const bool released = mbar_test_wait(bar_empty(p % NSLOT), fphase(p));
+                    all = all && (later || released || mbar_test_wait(bar_full(p % NSLOT), fphase(p)));
+                    later = later || released;
+                }
+                if (all) break;
+                if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                    atomicOr(&g_ptile_err, kErrDrainTimeout);
+                    break;
+                }
+            }
         };
         // The copies of a tile: the lanes below npg issue one each.  (Copies that the converged warp
         // issues one after the other, by elect.sync, take 43 cycles each instead of 77, and yet made
@@ -351,6 +379,9 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 group8 = ((in_pool ? now.entry : a.n_pages) * a.H_kv + now.kvh) * (a.ps >> 3) + (now.row >> 3);
                 if (NQT == 1 && now.token >= 0) {
                     // a new piece: its query tile, in two halves, comes before its first key tile
+                    q2 = q1;
+                    q1 = q0;
+                    q0 = fills - (values ? 1 : 0);
 #pragma unroll 1
                     for (int hlf = 0; hlf < 2 && ok; ++hlf) {
                         if (!values) {
@@ -362,7 +393,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                                             hlf * (D / 2) + lane * 64, now.kvh * a.G, now.token, 0);
                             __syncwarp();
                         }
-                        skip_fills(1);
+                        if (ok) skip_fills(1);
                     }
                     if (!ok) break;
                 }
@@ -374,9 +405,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             __syncwarp();
             if (ok) skip_fills(2);
         }
-        if (!ok && lane == 0)  // drain this warp's copies that may still be in flight: the last of each slot
-            for (int i2 = 0; i2 < NSLOT; ++i2)
-                if ((mine >> i2) & 1u) mbar_drain(bar_full(i2), (mine_phase >> i2) & 1u, &g_ptile_err);
+        if (!ok && lane == 0) drain();
     } else if (warp == 1) {
         // ============================ MMA issuer ============================
         regs_dec<C::REG_CTRL>();

@@ -50,6 +50,34 @@ def test_producer_stop_times_out_and_recovers(swa, Hq, Hkv, D, seqs, window, fau
     run(swa, x, q_start=start)
 
 
+@pytest.mark.parametrize("stop", [9, 12])
+@pytest.mark.parametrize("Hq,Hkv,D,seqs,window", [
+    pytest.param(8, 2, 64, [(3000, 70)] * 24, 0, id="d64"),
+    pytest.param(8, 2, 128, [(3000, 70)] * 24, 0, id="d128-one-tile"),
+    pytest.param(16, 16, 128, [(900, 5000)], 700, id="d128-two-tiles"),
+    pytest.param(4, 2, 256, [(1500, 70)] * 24, 0, id="d256"),
+    pytest.param(4, 2, 256, [(i % 40, 3) for i in range(600)], 0, id="d256-pieces-of-a-tile"),
+])
+def test_producers_that_stop_late(swa, Hq, Hkv, D, seqs, window, stop):  # noqa: F811
+    """... when both producers have been through every slot of the ring: only the waits behind the missing
+    fills run out, not the producers' own for their copies."""
+    x = R.Batch(72, seqs, Hq, Hkv, D, 16, window)
+    q, k, v, table, p0, start = (t.cuda() for t in (x.q, x.k_pages, x.v_pages, x.table, x.p0, x.q_start))
+    swa.swa_debug_set_faults(band_stop_fill=stop)
+    try:
+        t0 = time.time()
+        swa.swa_paged_attend(q, k, v, table, p0, window, q_start=start)
+        st, words = swa.swa_read_device_errors()
+        waited = time.time() - t0
+    finally:
+        swa.swa_debug_set_faults()
+    assert st == SWA_ERR_TIMEOUT, (st, words)
+    assert words == {"prefill": swa.DEVERR_WAIT_TIMEOUT, "split": 0, "cache": 0}, words
+    assert waited < 4.0, waited  # one limit of about 2.1 s, at the same time everywhere
+    if stop == 12:
+        run(swa, x)
+
+
 @pytest.mark.parametrize("heads", [(16, 16, 128), (32, 8, 128)], ids=str)
 def test_units_of_two_query_tiles(swa, heads):  # noqa: F811
     # head dim 128 and many tokens: pairs of tiles, a last pair of one tile, pairs whose second tile has

@@ -16,7 +16,8 @@ wait that a parity lets pass, the phase counted must be the newest one completed
   * the value rows that are zeroed (in tiles where a sequence, its sinks or the part before its
     window ends) are those of a tile that has landed;
   * O is rescaled when the MMAs that write it are complete;
-  * no order ends in a deadlock.
+  * no order ends in a deadlock;
+  * a producer that gives up returns when, and not before, its own copies have landed.
 A model of the protocol, not of the kernel's code: the orders below restate the kernel's.  The ring
 sizes are the source's.
 """
@@ -75,6 +76,9 @@ class Kernel:
         self.meet = Barrier("meet", 4 * nqt)
         self.piece, self.used = b("piece_full", NP, 1), b("piece_empty", NP, 2 + nqt + 8)
         self.occupant, self.landed, self.in_flight, self.reads = {}, set(), [], {}
+        self.stop = [1 << 30, 1 << 30]  # the producers' first fills that they do not issue
+        self.fills = [0, 1]             # their next fills
+        self.issued = [[], []]
         self.pipe = []   # MMAs and commits in issue order
         self.o_writes = [0, 0]  # MMAs into each accumulator that have not completed
         self.start = []  # tiles before each piece
@@ -112,16 +116,54 @@ class Kernel:
             if k + 1 < len(self.pieces):  # the next piece's pages are looked up ahead
                 yield self.get_piece(k + 1)
                 self.give_back(k + 1)
-            if self.nqt == 1 and not values:
+            if self.nqt == 1:
                 for p in (self.kfill(k, J) - 2, self.kfill(k, J) - 1):
-                    yield self.empty[p % self.nslot], p // self.nslot - 1
-                    self.reads[p] = 1
-                    self.issue(p)
+                    if not values:
+                        if p >= self.stop[0]:
+                            return
+                        yield self.empty[p % self.nslot], p // self.nslot - 1
+                        self.reads[p] = 1
+                        self.issue(p)
+                        self.issued[0].append(p)
+                    self.fills[values] += 1
             for g in range(J, J + n):
                 p = self.kfill(k, g) + values
+                assert p == self.fills[values]
+                if p >= self.stop[values]:
+                    return
                 yield self.empty[p % self.nslot], p // self.nslot - 1
                 self.reads[p] = 2 if self.nqt == 2 and not self.pieces[k][1] else 1
                 self.issue(p)
+                self.issued[values].append(p)
+                self.fills[values] += 2
+
+    # ---- the exit of a producer: may it return?
+    def own(self, values, p):
+        starts = [self.kfill(k, J) - 2 for k, J in enumerate(self.start)]
+        if self.nqt == 1 and (p in starts or p - 1 in starts):
+            return not values
+        return p & 1 == values
+
+    def tests(self, bar, phase):  # (a test of the parity, no claim about the phase)
+        return (bar.done & 1) != (phase & 1)
+
+    def drained(self, values):
+        """As the kernel asks it: its fills among the last NSLOT + 2 up to its last one, the newest first.  One
+        that was released has landed, and so have all before it; one whose full barrier names its phase has."""
+        later, last = False, next((p for p in range(self.fills[values] - 1, -1, -1) if self.own(values, p)), -1)
+        for p in range(last, max(last - self.nslot - 2, -1), -1):
+            if not self.own(values, p):
+                continue
+            released = self.tests(self.empty[p % self.nslot], p // self.nslot)
+            if not (later or released or self.tests(self.full[p % self.nslot], p // self.nslot)):
+                return False
+            later = later or released
+        return True
+
+    def drained_by_slot(self, values):
+        """A fault that the model catches: the last own fill of every slot, whoever has filled it since."""
+        newest = {p % self.nslot: p for p in self.issued[values]}
+        return all(self.tests(self.full[x], p // self.nslot) for x, p in newest.items())
 
     def planner(self):
         k, kq, more, loads, y = 0, 0, True, [0, 0], 1
@@ -343,7 +385,12 @@ class Kernel:
             self.give_back(k)
         yield self.get_piece(len(self.pieces))
 
-    def run(self):
+    def run(self, stopping=False, drained="drained"):
+        """stopping: the producers give up at random fills; the others run on as far as they can."""
+        if stopping:
+            total = sum(n for n, _ in self.pieces) * 2 + 2 * len(self.pieces) * (self.nqt == 1)
+            at = self.rng.randrange(total)
+            self.stop = [at, max(0, at + self.rng.choice((0, 0, 1, -2, 3)))]
         roles = [self.planner(), self.producer(0), self.producer(1), self.mma_warp()]
         roles += [self.softmax_warp(wg, q) for wg in range(self.nqt) for q in range(4)]
         roles += [self.epilogue_warp() for _ in range(4 * (2 - self.nqt))]
@@ -360,8 +407,17 @@ class Kernel:
                     waits[a] = next(roles[a], None)
                     break
             else:
+                if stopping:
+                    break
                 stuck = [f"{w[0].name} phase {w[1]}" for w in waits if w]
                 raise AssertionError(f"deadlock: {self.pieces}, waiting for {stuck}")
+            if stopping and self.rng.random() < 0.2:
+                for v in (0, 1):
+                    if waits[1 + v] is None and getattr(self, drained)(v):
+                        assert not set(self.issued[v]) & set(self.in_flight), "a producer returns before its copies"
+        if stopping:
+            for v in (0, 1):
+                assert getattr(self, drained)(v), f"a drain that runs into its limit: {self.pieces}, stops {self.stop}"
 
 
 # name: head dim, score slots, query tiles a CTA, kinds of pieces (whether of a single query tile)
@@ -386,6 +442,26 @@ def runs(name, nslot, count):
 def test_every_wait_names_its_phase(name):
     for kernel in runs(name, ring_slots(FLAVOURS[name][0]), 300):
         kernel.run()
+
+
+@pytest.mark.parametrize("name", FLAVOURS)
+def test_producers_that_stop_drain_their_copies(name):
+    for kernel in runs(name, ring_slots(FLAVOURS[name][0]), 300):
+        kernel.run(stopping=True)
+
+
+@pytest.mark.parametrize("name", ["d128-single", "d128-pairs", "d256"])
+def test_model_catches_a_drain_by_slot(name):
+    """In an odd ring keys and values take turns in a slot: the other producer's later fill has overtaken the
+    phase of this one's last."""
+    caught = 0
+    for kernel in runs(name, ring_slots(FLAVOURS[name][0]), 60):
+        try:
+            kernel.run(stopping=True, drained="drained_by_slot")
+        except AssertionError as e:
+            assert "runs into its limit" in str(e), e
+            caught += 1
+    assert caught > 0
 
 
 def premature(name, nslot, count, what):
