@@ -320,8 +320,9 @@ typedef struct swa_paged_cache {
  *                keys and values, stored in their pages first (as swa_paged_append does);
  *                both NULL: they are there already.
  *   max_q        the most new tokens of one sequence, as far as the caller knows (0: not
- *                known).  It chooses between kernels for few and for many rows; results are
- *                right whatever it says.
+ *                known).  It chooses between kernels for few rows (max_q * H_q / H_kv <= 16, or
+ *                q_start NULL) and for many; results are right whatever it says.  Unknown, one
+ *                token a sequence mostly takes 6 to 14% longer.
  * The cache must hold every position that a query keeps, in finite numbers (a position that some
  * queries of a sequence keep and others do not shows in the others if it is not finite); what
  * no query of the sequence keeps -- between the sinks and its first new token's window, at or

@@ -17,7 +17,8 @@ __device__ unsigned int g_paged_err = 0;
 constexpr int kThreads = 256;
 
 // ---------------------------------------------------------------------------------------------
-// append: a warp per token
+// append: a warp per token.  Up to 512 tokens (8 heads of 128) 5 us, the latency of finding the sequence,
+// its page, then the rows; 16384 tokens 28.0 us, 128000 208 us, 71 and 74% of the measured copy rate.
 // ---------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedArgs a, int32_t *zero, int n_zero) {
     // the attention kernel behind this one may start: it waits for this grid before it reads a page

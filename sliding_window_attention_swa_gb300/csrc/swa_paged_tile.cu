@@ -103,7 +103,7 @@ struct TileCfg {
     static_assert(sizeof(Share) <= 64, "share");
     static constexpr uint32_t TMEM_COLS = 512;
     // S slots: two, or three where tensor memory has room (head dim 64), so that S(j + 2) is there
-    // when the warpgroup that had tile j is done with it (8192 tokens behind 8000: 910 -> 816 us; now 708)
+    // when the warpgroup that had tile j is done with it (8192 tokens behind 8000: 910 -> 816 us; now 704)
     static constexpr int NS = D == 64 ? 3 : 2;
     __host__ __device__ static constexpr uint32_t tm_s(int slot) { return static_cast<uint32_t>(slot * BN); }
     __host__ __device__ static constexpr uint32_t tm_o(int tile) {
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                         const int f = 2 * (J + i), ks = (f + 2) % NSLOT;
                         v_descs((f + 1) % NSLOT);
                         // (the next keys are waited for here, not between the two products, where a wait leaves
-                        // the tensor cores idle: the Mistral window on pages of 16 651 -> 638 us)
+                        // the tensor cores idle: 2% of the Mistral window on pages of 16)
                         ok = landed(f + 1) && (i + 1 == n || landed(f + 2)) && mma_pv(0, 0, i == 0, np0 + i, -1);
                         if (!ok) break;
                         if (i + 1 < n) {
@@ -1074,7 +1074,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
 // (chunks of 2048 tokens behind 30000: 989 against 1047 us), and single tiles, twice as many
 // units, where there are not (two chunks of 100 tokens 25 against 33 us, a mixed step 78
 // against 91): pairs from two units a CTA, by what the host knows of the batch.  At head dim 64
-// there was nothing between them (856 and 857 us, of what is now 708), so it has no pairs.
+// there was nothing between them (856 and 857 us, of what is now 704), so it has no pairs.
 int tiles_of_unit(const PagedArgs &a) {
     if (a.D != 128) return 1;
     const int64_t pairs = static_cast<int64_t>(a.N) / (2 * (BM / a.G)) * a.H_kv;

@@ -245,6 +245,18 @@ def test_append_alone(swa):
     assert (R.bits(k) == R.bits(x.k_pages)).all() and (R.bits(v) == R.bits(x.v_pages)).all()
 
 
+def test_append_of_one_token_a_sequence(swa):
+    x = R.Batch(16, [(i * 13, 1) for i in range(50)], 8, 4, 64, 32)
+    k, v = (t.cuda() for t in x.without_new())
+    graph = torch.cuda.CUDAGraph()
+    a = x.table.cuda(), x.k_new.cuda(), x.v_new.cuda(), x.p0.cuda()
+    with torch.cuda.graph(graph):
+        swa.swa_paged_append(k, v, *a)
+    graph.replay()
+    swa.swa_check_device_error()
+    assert (R.bits(k) == R.bits(x.k_pages)).all() and (R.bits(v) == R.bits(x.v_pages)).all()
+
+
 def test_offsets_past_32_bits(swa):
     # the pages lie past element 2^31 of their pools
     x = R.Batch(11, [(70, 1), (10, 90)], 8, 8, 128, 64)
