@@ -40,6 +40,8 @@
  *             tokens of a sequence lie in pages of one pool; swa_paged_append stores
  *             tokens, and swa_pages_reserve / _free / _fork / _compact / _copy manage the
  *             pages, their tables and their holders.
+ * swa_paged_rope_append  Stores new tokens with their keys rotated by position, and rotates their
+ *             queries, in one pass; swa_rope_table makes the rotation's table.
  *
  * Conventions
  * -----------
@@ -367,6 +369,45 @@ SWA_API swa_status swa_paged_attend(const swa_paged_params *p, const swa_paged_c
  * (SWA_DEVERR_BAD_PAGE).
  */
 SWA_API swa_status swa_paged_append(const swa_paged_params *p, const swa_paged_cache *c, swa_stream_t stream);
+
+/*
+ * Rotary positions.  A rotation turns pair i of a head's first rot_dim elements at position p by
+ * the angle p * f_i (RoPE; the Gemma 3 note's local layers have f_i = 10000^(-2i/rot_dim)):
+ *     x' = x cos - y sin,  y' = y cos + x sin,
+ * where (x, y) are elements (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved; elements from rot_dim
+ * on stay.  The angles are known by a table
+ *   table   fp32 [n_pos, rot_dim], contiguous: row p holds the rot_dim / 2 cosines of position p, then the sines.
+ */
+typedef struct swa_rope {
+    const float *table;
+    int32_t n_pos, rot_dim, interleaved;
+} swa_rope;
+
+/*
+ * Makes such a table: table[p, i] = scale * cos(p * inv_freq[i]), table[p, rot_dim / 2 + i] = scale *
+ * sin(p * inv_freq[i]) for 0 <= p < n_pos; inv_freq: device fp64 [rot_dim / 2], any finite numbers
+ * (one that is not gives NaN).  The angle is taken modulo a turn with an error below p * 2^-64 turns, so
+ * an entry is off by less than 2^-22 * |scale| at any position.
+ * Requirements: rot_dim a multiple of 16, at most 256; 0 <= n_pos <= 2^30; scale finite; table 16-byte
+ * aligned, inv_freq 8-byte.
+ */
+SWA_API swa_status swa_rope_table(const double *inv_freq, int32_t rot_dim, int32_t n_pos, float scale, float *table,
+                                  swa_stream_t stream);
+
+/*
+ * swa_paged_append with the rotation applied on the way: p->k_new's rows are rotated by their positions
+ * (p->p0, p->q_start as there) and stored with p->v_new's in their pages, and the rows of p->q (bf16 [N, H_q,
+ * d_h], p->q_strides), rotated likewise, go to p->o (p->o_strides), which is p->q itself (same strides) or does
+ * not overlap it.  q NULL: keys and values only; k_new and v_new NULL: queries only.  Nothing else of p is
+ * read.  Products and sums in 32 bits, rounded to bf16 once; elements from rot_dim on and values are copied.
+ * A sequence or position out of range, also of the table (position >= n_pos), leaves its rows of o and the
+ * cache as they were (SWA_DEVERR_BAD_POSITION); a token whose page is missing is not stored, its query is
+ * rotated all the same (SWA_DEVERR_BAD_PAGE).  Rows of no sequence stay as they were.
+ * Requirements: as for swa_paged_attend where given (any H_q that is a multiple of H_kv); rot_dim a multiple
+ * of 16, at most d_h; interleaved 0 or 1; the table 16-byte aligned.
+ */
+SWA_API swa_status swa_paged_rope_append(const swa_paged_params *p, const swa_paged_cache *c, const swa_rope *r,
+                                         swa_stream_t stream);
 
 /*
  * Pages and who holds them.  ref[p] counts the holders of page p -- the table entries that

@@ -2,8 +2,8 @@
 
 The functions here marshal torch tensors into the C ABI of ``include/swa.h``
 (``swa_fwd``, ``swa_decode``, ``swa_cache_append``, ``swa_decode_append``,
-``swa_prefill_chunk``, ``swa_paged_attend``, ``swa_paged_append``, the
-``swa_pages_*`` calls and their workspace queries) and call it on the current
+``swa_prefill_chunk``, ``swa_paged_attend``, ``swa_paged_append``,
+``swa_paged_rope_append``, ``swa_rope_table``, the ``swa_pages_*`` calls and their workspace queries) and call it on the current
 CUDA stream.  Every step of the computation runs in the library's
 kernels; there is no fallback path.  If the library has not been built, the
 first call raises (``build()`` compiles it in-tree with nvcc).
@@ -32,6 +32,7 @@ __all__ = [
     "SwaDeviceErrors", "SwaDebugFaults", "swa_read_device_errors", "swa_debug_set_faults",
     "SwaPagedCache", "SwaPagedParams", "SwaPageTables", "SwaPagePool", "swa_paged_attend", "swa_paged_append",
     "swa_pages_reserve", "swa_pages_free", "swa_pages_fork", "swa_pages_compact", "swa_pages_copy",
+    "SwaRope", "swa_rope_table", "swa_paged_rope_append",
 ]
 
 _c_i64x3 = ctypes.c_int64 * 3
@@ -107,6 +108,15 @@ class SwaPagedParams(ctypes.Structure):
         ("o_strides", _c_i64x2), ("N", ctypes.c_int32), ("H_q", ctypes.c_int32), ("max_q", ctypes.c_int32),
         ("window", ctypes.c_int32), ("n_sink", ctypes.c_int32), ("scale", ctypes.c_float), ("o", ctypes.c_void_p),
         ("lse", ctypes.c_void_p), ("row_counts", ctypes.c_void_p),
+    ]
+
+
+class SwaRope(ctypes.Structure):
+    """Mirror of ``swa_rope`` in include/swa.h."""
+
+    _fields_ = [
+        ("table", ctypes.c_void_p), ("n_pos", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
     ]
 
 
@@ -222,8 +232,10 @@ def load_library(path: str | None = None):
     lib.swa_pages_fork.argtypes = [vp, vp, vp, vp, vp, sz, vp]
     lib.swa_pages_compact.argtypes = [vp, vp, vp, vp, sz, vp]
     lib.swa_pages_copy.argtypes = [vp, vp, vp, ctypes.c_int32, vp]
+    lib.swa_rope_table.argtypes = [vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, vp, vp]
+    lib.swa_paged_rope_append.argtypes = [vp, vp, vp, vp]
     for name in ("swa_paged_attend", "swa_paged_append", "swa_pages_reserve", "swa_pages_free", "swa_pages_fork",
-                 "swa_pages_compact", "swa_pages_copy"):
+                 "swa_pages_compact", "swa_pages_copy", "swa_rope_table", "swa_paged_rope_append"):
         getattr(lib, name).restype = ctypes.c_int
     lib.swa_check_device_error.argtypes = [vp]
     lib.swa_check_device_error.restype = ctypes.c_int
@@ -551,6 +563,7 @@ _PAGED_PARAMS = struct.Struct("5P8q5if3P")
 _PAGED_CACHE = struct.Struct("3P6i")
 _PAGE_TABLES = struct.Struct("4P4i")
 _PAGE_POOL = struct.Struct("2Pq5i")
+_ROPE = struct.Struct("P3i")
 
 
 def _packed(layout, *values) -> bytes:
@@ -731,6 +744,73 @@ def swa_paged_append(k_pages, v_pages, page_table, k_new, v_new, p0, *, q_start=
     st = load_library().swa_paged_append(params, cache, _raw_stream(index))
     if st != 0:
         raise SwaError("swa_paged_append", st)
+
+
+def swa_rope_table(inv_freq, n_pos: int, scale: float = 1.0, *, out=None, stream=None):
+    """The table of a rotation: fp32 [n_pos, R], row p the cosines of p * inv_freq[i], then the sines,
+    times scale; inv_freq fp64 [R/2] (R a multiple of 16).  Returns out."""
+    import torch
+
+    if stream is not None:
+        return _on(stream, swa_rope_table, inv_freq, n_pos, scale, out=out)
+    index = _device_index("inv_freq", inv_freq)
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq: expected a contiguous fp64 tensor [R/2]")
+    n_pos, rot = _int32("n_pos", n_pos), 2 * inv_freq.shape[0]
+    if out is None:
+        out = torch.empty((max(n_pos, 0), rot), dtype=torch.float32, device=inv_freq.device)
+    elif out.dtype is not torch.float32 or out.get_device() != index or out.shape != (n_pos, rot) or \
+            not out.is_contiguous():
+        raise ValueError(f"out: expected a contiguous fp32 tensor {[n_pos, rot]} on cuda:{index}")
+    if n_pos != 0:
+        st = load_library().swa_rope_table(inv_freq.data_ptr(), _int32("R", rot), n_pos, float(scale), out.data_ptr(),
+                                           _raw_stream(index))
+        if st != 0:
+            raise SwaError("swa_rope_table", st)
+    return out
+
+
+def swa_paged_rope_append(q, k_pages, v_pages, page_table, k_new, v_new, p0, rope, *, q_start=None,
+                          interleaved: bool = False, q_out=None, stream=None):
+    """swa_paged_append with q [N,H_q,d] and k_new [N,H_kv,d] rotated by their positions on the way; rope: the
+    rotation's table (fp32 [n_pos,R], swa_rope_table).  interleaved: pairs are neighbours (2i, 2i+1), not
+    (i, i + R/2).  The rotated queries go to q_out (q itself: in place; new if not given), which is
+    returned; rows of no sequence stay as they were.  q None: keys and values only, k_new and v_new None:
+    queries only."""
+    import torch
+
+    if stream is not None:
+        return _on(stream, swa_paged_rope_append, q, k_pages, v_pages, page_table, k_new, v_new, p0, rope,
+                   q_start=q_start, interleaved=interleaved, q_out=q_out)
+    rows = k_new if q is None else q
+    if rows is None or rows.dim() != 3:
+        raise ValueError("q, k_new: expected [N, heads, d], one of them at least")
+    N = rows.shape[0]
+    index, cache, H_kv, D = _paged_cache(k_pages, v_pages, page_table, p0, q_start, N)
+    new, new_st = _new_rows(k_new, v_new, index, (N, H_kv, D))
+    if rope.dtype is not torch.float32 or rope.get_device() != index or rope.dim() != 2 or not rope.is_contiguous():
+        raise ValueError(f"rope: expected a contiguous fp32 tensor [n_pos, R] on cuda:{index}")
+    q_at, o_at, q_st, o_st, Hq = 0, 0, (0, 0), (0, 0), 0
+    if q is not None:
+        Hq = q.shape[1]
+        q_st = _rows("q", q, index, (N, Hq, D))
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        o_st = _rows("q_out", q_out, index, (N, Hq, D))
+        q_at, o_at = q.data_ptr(), q_out.data_ptr()
+        if o_at == q_at and o_st != q_st:
+            raise ValueError("q_out: in place, its strides are q's")
+    elif q_out is not None:
+        raise ValueError("q_out: given without q")
+    if N == 0:
+        return q_out
+    params = _packed(_PAGED_PARAMS, q_at, *new, p0.data_ptr(), 0 if q_start is None else q_start.data_ptr(), *q_st,
+                     *new_st, *o_st, N, Hq, 0, 0, 0, 0.0, o_at, 0, 0)
+    st = load_library().swa_paged_rope_append(params, cache, _packed(_ROPE, rope.data_ptr(), *rope.shape,
+                                                                     bool(interleaved)), _raw_stream(index))
+    if st != 0:
+        raise SwaError("swa_paged_rope_append", st)
+    return q_out
 
 
 def _lists(index: int, *named) -> None:

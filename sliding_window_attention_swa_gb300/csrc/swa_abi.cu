@@ -732,6 +732,37 @@ swa_status swa_paged_append(const swa_paged_params *p, const swa_paged_cache *c,
     return SWA_OK;
 }
 
+swa_status swa_rope_table(const double *inv_freq, int32_t rot_dim, int32_t n_pos, float scale, float *table,
+                          swa_stream_t stream) {
+    if (!inv_freq || !table || rot_dim < 1 || n_pos < 0 || !std::isfinite(scale)) return SWA_ERR_INVALID_ARG;
+    if (rot_dim % 16 != 0 || rot_dim > 256 || n_pos > (1 << 30) || reinterpret_cast<uintptr_t>(inv_freq) % 8 != 0 ||
+        !aligned16(table))
+        return SWA_ERR_UNSUPPORTED;
+    if (n_pos == 0) return SWA_OK;
+    if (failed(swa::launch_rope_table(inv_freq, rot_dim, n_pos, scale, table, reinterpret_cast<cudaStream_t>(stream))))
+        return SWA_ERR_CUDA;
+    return SWA_OK;
+}
+
+swa_status swa_paged_rope_append(const swa_paged_params *p, const swa_paged_cache *c, const swa_rope *r,
+                                 swa_stream_t stream) {
+    const swa_status st = paged_rows_check(p, c, false);
+    if (st != SWA_OK) return st;
+    if (!r || !r->table || r->n_pos < 1 || r->rot_dim < 1 || r->rot_dim > c->d_h) return SWA_ERR_INVALID_ARG;
+    if (r->rot_dim % 16 != 0 || !aligned16(r->table) || (r->interleaved & ~1) != 0) return SWA_ERR_UNSUPPORTED;
+    if (!p->q && !p->k_new) return SWA_ERR_INVALID_ARG;
+    if (p->q) {
+        if (!p->o || p->H_q < 1 || p->H_q % c->H_kv != 0) return SWA_ERR_INVALID_ARG;
+        if (!strides2_ok(p->q_strides) || !strides2_ok(p->o_strides) || !aligned16(p->q) || !aligned16(p->o))
+            return SWA_ERR_UNSUPPORTED;
+    }
+    if (p->N == 0) return SWA_OK;
+    const swa::RopeArgs ra{r->table, r->n_pos, r->rot_dim, r->interleaved};
+    if (failed(swa::launch_rope_append(paged_args(p, c), ra, reinterpret_cast<cudaStream_t>(stream))))
+        return SWA_ERR_CUDA;
+    return SWA_OK;
+}
+
 size_t swa_pages_workspace_size(const swa_page_tables *t) {
     // (the same for every call: whether the tables are in place does not matter here)
     if (tables_check(t, InPlace::kNo) != SWA_OK && tables_check(t, InPlace::kEither) != SWA_OK) return 0;
@@ -805,7 +836,7 @@ swa_status swa_read_device_errors(swa_stream_t stream, swa_device_errors *out) {
     swa_device_errors e;
     e.prefill = swa::band_read_clear_error();
     e.split = swa::split_read_clear_error();
-    e.cache = swa::cache_read_clear_error() | swa::pages_read_clear_error();
+    e.cache = swa::cache_read_clear_error() | swa::pages_read_clear_error() | swa::rope_read_clear_error();
     unsigned int data, split, prefill;
     swa::paged_read_clear_error(&data, &split, &prefill);
     e.cache |= data;

@@ -114,6 +114,17 @@ size_t paged_workspace_bytes(const PagedArgs &a);
 // zero, n_zero: words that the kernel sets to 0 beside its own work (n_zero may be 0).
 cudaError_t launch_paged_append(const PagedArgs &a, int32_t *zero, int n_zero, cudaStream_t s);
 cudaError_t launch_paged_attend(const PagedArgs &a, void *ws, cudaStream_t s);
+
+// The table of a rotation and how it turns a head (swa_rope.cu).
+struct RopeArgs {
+    const float *table;  // [n_pos, rot]: cosines, then sines
+    int n_pos, rot, interleaved;
+};
+cudaError_t launch_rope_table(const double *inv_freq, int rot, int n_pos, float scale, float *out, cudaStream_t s);
+// a.q may be nullptr (keys and values only), a.kn too (queries only); rotated queries go to a.o.
+cudaError_t launch_rope_append(const PagedArgs &a, const RopeArgs &r, cudaStream_t s);
+unsigned int rope_read_clear_error();
+
 // Errors of the data (cache word), of the few-row and of the many-row kernels.
 void paged_read_clear_error(unsigned int *data, unsigned int *split, unsigned int *prefill);
 
