@@ -40,6 +40,8 @@
  *             tokens of a sequence lie in pages of one pool; swa_paged_append stores
  *             tokens, and swa_pages_reserve / _free / _fork / _compact / _copy manage the
  *             pages, their tables and their holders.
+ * swa_paged_attend_shared  The same for sequences that share leading pages (swa_pages_fork makes such):
+ *             a prefix is read once for all of them.
  * swa_paged_rope_append  Stores new tokens with their keys rotated by position, and rotates their
  *             queries, in one pass; swa_rope_table makes the rotation's table.
  *
@@ -362,6 +364,26 @@ typedef struct swa_paged_params {
 SWA_API size_t swa_paged_workspace_size(const swa_paged_params *p, const swa_paged_cache *c);
 SWA_API swa_status swa_paged_attend(const swa_paged_params *p, const swa_paged_cache *c, void *workspace,
                                     size_t workspace_bytes, swa_stream_t stream);
+
+/*
+ * swa_paged_attend for sequences that share leading pages (several answers to one prompt, beams, questions
+ * about one document): group g is sequences group_start[g] .. group_start[g+1]-1 (device int32 [n_groups + 1],
+ * not decreasing, within [0, B]; sequences of no group are computed alone).  What the sequences of a group share
+ * is found from their rows of the page table -- the leading entries that are alike in all of them that have
+ * new tokens, below the least p0, an entry that a sequence has no use for (behind its window, no sink) being
+ * alike to any -- and is read once for all their new tokens; the rest is read for each sequence.  The result is
+ * swa_paged_attend's up to rounding, whatever the rows hold: a group that shares nothing is computed as if it
+ * were none, and so is one of which a sequence is out of range, and all of them where group_start is (which is
+ * reported: SWA_DEVERR_BAD_POSITION).  A position that some queries of the group keep must be finite in the
+ * shared pages, as swa_paged_attend asks of each sequence's own.
+ * p, c, errors and requirements as swa_paged_attend; 1 <= n_groups <= 8192.
+ * Workspace: swa_paged_shared_workspace_size bytes, 256-byte aligned: beside swa_paged_attend's the prefix parts' results,
+ * fp32 [N, H_q, d_h].
+ */
+SWA_API size_t swa_paged_shared_workspace_size(const swa_paged_params *p, const swa_paged_cache *c, int32_t n_groups);
+SWA_API swa_status swa_paged_attend_shared(const swa_paged_params *p, const swa_paged_cache *c, const int32_t *group_start,
+                                           int32_t n_groups, void *workspace, size_t workspace_bytes,
+                                           swa_stream_t stream);
 
 /*
  * Stores the new tokens' keys and values in their pages: p->k_new, p->v_new, p->p0, p->q_start

@@ -724,6 +724,25 @@ swa_status swa_paged_attend(const swa_paged_params *p, const swa_paged_cache *c,
     return SWA_OK;
 }
 
+size_t swa_paged_shared_workspace_size(const swa_paged_params *p, const swa_paged_cache *c, int32_t n_groups) {
+    if (paged_check(p, c) != SWA_OK || n_groups < 1 || n_groups > swa::kPagedMaxB) return 0;
+    return swa::paged_shared_workspace_bytes(paged_args(p, c), n_groups);
+}
+
+swa_status swa_paged_attend_shared(const swa_paged_params *p, const swa_paged_cache *c, const int32_t *group_start,
+                                   int32_t n_groups, void *workspace, size_t workspace_bytes, swa_stream_t stream) {
+    swa_status st = paged_check(p, c);
+    if (st != SWA_OK) return st;
+    if (!group_start || n_groups < 1) return SWA_ERR_INVALID_ARG;
+    if (n_groups > swa::kPagedMaxB || !aligned4(group_start)) return SWA_ERR_UNSUPPORTED;
+    const swa::PagedArgs a = paged_args(p, c);
+    st = workspace_ok(workspace, workspace_bytes, swa::paged_shared_workspace_bytes(a, n_groups));
+    if (st != SWA_OK || a.N == 0) return st;
+    if (failed(swa::launch_paged_shared(a, group_start, n_groups, workspace, reinterpret_cast<cudaStream_t>(stream))))
+        return SWA_ERR_CUDA;
+    return SWA_OK;
+}
+
 swa_status swa_paged_append(const swa_paged_params *p, const swa_paged_cache *c, swa_stream_t stream) {
     const swa_status st = paged_rows_check(p, c, true);
     if (st != SWA_OK || p->N == 0) return st;
@@ -836,7 +855,8 @@ swa_status swa_read_device_errors(swa_stream_t stream, swa_device_errors *out) {
     swa_device_errors e;
     e.prefill = swa::band_read_clear_error();
     e.split = swa::split_read_clear_error();
-    e.cache = swa::cache_read_clear_error() | swa::pages_read_clear_error() | swa::rope_read_clear_error();
+    e.cache = swa::cache_read_clear_error() | swa::pages_read_clear_error() | swa::rope_read_clear_error() |
+              swa::paged_shared_read_clear_error();
     unsigned int data, split, prefill;
     swa::paged_read_clear_error(&data, &split, &prefill);
     e.cache |= data;

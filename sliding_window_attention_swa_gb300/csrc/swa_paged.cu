@@ -105,8 +105,8 @@ bool paged_pool_map(CUtensorMap *m, const PagedArgs &a, const void *pool, int ro
 
 // Few rows: every sequence's new tokens fit one unit of the split kernel (16 rows).  With more of
 // them that kernel would read the keys once per 16 rows.
-static bool few_rows(const PagedArgs &a) { return !a.q_start || (a.max_q > 0 && a.max_q <= 16 / a.G); }
-static PagedShape shape_of(const PagedArgs &a) { return few_rows(a) ? paged_split_shape(a) : paged_tile_shape(a); }
+bool paged_few_rows(const PagedArgs &a) { return !a.q_start || (a.max_q > 0 && a.max_q <= 16 / a.G); }
+static PagedShape shape_of(const PagedArgs &a) { return paged_few_rows(a) ? paged_split_shape(a) : paged_tile_shape(a); }
 
 size_t paged_workspace_bytes(const PagedArgs &a) { return paged_ws_bytes(shape_of(a), a.D); }
 
@@ -119,7 +119,7 @@ cudaError_t launch_paged_append(const PagedArgs &a, int32_t *zero, int n_zero, c
 
 cudaError_t launch_paged_attend(const PagedArgs &args, void *ws, cudaStream_t s) {
     PagedArgs a = args;
-    const bool few = few_rows(a);
+    const bool few = paged_few_rows(a);
     const PagedShape x = shape_of(a);
     const PagedWs w = paged_carve(ws, x, a.D);
     const int n_done = few ? 0 : x.ctas * 8;

@@ -12,13 +12,29 @@ namespace swa {
 
 // New tokens q0 .. q0 + n - 1 of sequence b at positions p0 ..; ok: its rows lie in [0, N) and
 // its positions in its table row (otherwise n = 0 and the sequence is skipped).
+// Of a part: kOwn: positions are counted from `base` on.  kPrefix: a group, its rows' positions between p0 and
+// `top`, its keys below `base`, its pages those of sequence `row`.
 struct Seq {
     int q0, n, p0;
     bool ok;
+    int base = 0, row = 0, top = 0;
 };
 
+template <Part PT = Part::kAll>
 __device__ __forceinline__ Seq load_seq(const PagedArgs &a, int b) {
     Seq s;
+    if constexpr (PT == Part::kPrefix) {
+        const int4 *g = reinterpret_cast<const int4 *>(a.groups + b);
+        const int4 x = __ldcg(g), y = __ldcg(g + 1);  // (written by the kernel before this one)
+        s.q0 = x.x;
+        s.n = x.y;
+        s.p0 = x.z;
+        s.ok = true;
+        s.base = x.w;
+        s.row = y.x;
+        s.top = y.y;
+        return s;
+    }
     int q1;
     if (a.q_start) {
         s.q0 = __ldg(a.q_start + b);
@@ -31,7 +47,17 @@ __device__ __forceinline__ Seq load_seq(const PagedArgs &a, int b) {
     s.ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= a.N && s.p0 >= 0 &&
            static_cast<int64_t>(s.p0) + (q1 - s.q0) <= (static_cast<int64_t>(a.width) << a.ps_log2);
     s.n = s.ok ? q1 - s.q0 : 0;
+    if constexpr (PT == Part::kOwn) {
+        s.base = s.ok ? __ldcg(a.base + b) : 0;
+        s.p0 -= s.base;
+    }
     return s;
+}
+
+// The sinks among a part's positions.
+template <Part PT>
+__device__ __forceinline__ int sinks_of(const PagedArgs &a, int base) {
+    return PT == Part::kOwn ? max(a.n_sink - base, 0) : a.n_sink;
 }
 
 // The sequence of token n, looked up by a whole warp: the last b with q_start[b] <= n (for a
@@ -85,12 +111,20 @@ struct UnitTiles {
     __device__ __forceinline__ int tile(int j) const { return j < sink ? j : lo + (j - sink); }
 };
 
-template <int BN>
+template <int BN, Part PT = Part::kAll>
 __device__ __forceinline__ UnitTiles unit_tiles(const PagedArgs &a, const Seq &s, int ut, int TT) {
+    if constexpr (PT == Part::kPrefix) {  // (the same for every block of rows)
+        UnitTiles u;
+        u.lo = s.p0 >= a.window ? (s.p0 - a.window + 1) / BN : 0;
+        u.sink = a.n_sink > 0 ? min(u.lo, (min(a.n_sink, s.base) + BN - 1) / BN) : 0;
+        u.n = u.sink + (s.base - 1) / BN - u.lo + 1;
+        return u;
+    }
+    const int n_sink = sinks_of<PT>(a, s.base);
     const int t0 = s.p0 + ut * TT, t1 = s.p0 + min(s.n, (ut + 1) * TT) - 1;
     UnitTiles u;
     u.lo = t0 >= a.window ? (t0 - a.window + 1) / BN : 0;
-    u.sink = a.n_sink > 0 ? min(u.lo, (min(a.n_sink, t0 + 1) + BN - 1) / BN) : 0;
+    u.sink = n_sink > 0 ? min(u.lo, (min(n_sink, t0 + 1) + BN - 1) / BN) : 0;
     u.n = u.sink + t1 / BN - u.lo + 1;
     return u;
 }
@@ -114,14 +148,14 @@ struct Piece {
 };
 
 // Walks a share piece by piece; every role of a CTA walks it alike.
-template <int BN>
+template <int BN, Part PT = Part::kAll>
 struct Walk {
     const PagedArgs *args;
     int TT, b, kvh, ut, j, left;
     Seq s;
     __device__ __forceinline__ Walk(const PagedArgs &a, int tt, const Share &sh)
         : args(&a), TT(tt), b(sh.b), kvh(sh.kvh), ut(sh.ut), j(sh.j), left(sh.left) {
-        if (left > 0) s = load_seq(a, b);
+        if (left > 0) s = load_seq<PT>(a, b);
     }
     __device__ __forceinline__ bool next(Piece &p) {
         const PagedArgs &a = *args;
@@ -137,7 +171,7 @@ struct Walk {
                             left = 0;
                             return false;
                         }
-                        s = load_seq(a, b);
+                        s = load_seq<PT>(a, b);
                     } while (s.n == 0);
                 }
             }
@@ -146,7 +180,7 @@ struct Walk {
         p.b = b;
         p.kvh = kvh;
         p.ut = ut;
-        p.u = unit_tiles<BN>(a, s, ut, TT);
+        p.u = unit_tiles<BN, PT>(a, s, ut, TT);
         p.j0 = j;
         p.j1 = min(p.u.n, j + left);
         left -= p.j1 - p.j0;
@@ -157,11 +191,11 @@ struct Walk {
 
 // A CTA's pieces one by one, found by one warp: its whole units, one a wave, then its stretch of the
 // list.  The sequences are searched 32 at a time from block b0, whose first unit is u0.
-template <int BN>
+template <int BN, Part PT = Part::kAll>
 struct Plan {
     const PagedArgs *args;
     int TT, waves, w, b0, u0;
-    Walk<BN> walk;
+    Walk<BN, PT> walk;
     __device__ __forceinline__ Plan(const PagedArgs &a, int tt, const Share &sh)
         : args(&a), TT(tt), waves(sh.waves), w(0), b0(0), u0(0), walk(a, tt, sh) {}
     __device__ __forceinline__ bool next(Piece &p, int lane) {
@@ -172,7 +206,7 @@ struct Plan {
         ++w;
         while (b0 < a.B) {
             Seq s{};
-            if (b0 + lane < a.B) s = load_seq(a, b0 + lane);
+            if (b0 + lane < a.B) s = load_seq<PT>(a, b0 + lane);
             const int nu = (s.n + TT - 1) / TT, v = nu * a.H_kv;
             int inc = v;
 #pragma unroll
@@ -190,7 +224,12 @@ struct Plan {
                 p.ut = rel % units;
                 p.s = Seq{__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.n, l),
                           __shfl_sync(0xffffffffu, s.p0, l), true};
-                p.u = unit_tiles<BN>(a, p.s, p.ut, TT);
+                if constexpr (PT != Part::kAll) p.s.base = __shfl_sync(0xffffffffu, s.base, l);
+                if constexpr (PT == Part::kPrefix) {
+                    p.s.row = __shfl_sync(0xffffffffu, s.row, l);
+                    p.s.top = __shfl_sync(0xffffffffu, s.top, l);
+                }
+                p.u = unit_tiles<BN, PT>(a, p.s, p.ut, TT);
                 p.j0 = 0;
                 p.j1 = p.u.n;
                 return true;
@@ -219,7 +258,7 @@ struct Place {
     int b, kvh, ut, j, n;
 };
 // Looked up by one warp; tiles: tiles of one kv head of each sequence.
-template <int BN>
+template <int BN, Part PT = Part::kAll>
 __device__ __forceinline__ Place find_tile(const PagedArgs &a, int TT, const long long *tiles, long long X, int lane) {
     Place r{0, 0, 0, 0, 1};
     long long before = 0;
@@ -243,10 +282,10 @@ __device__ __forceinline__ Place find_tile(const PagedArgs &a, int TT, const lon
     const long long per = max(tiles[r.b], 1ll);
     r.kvh = static_cast<int>((X - before) / per);
     long long rel = X - before - r.kvh * per;
-    const Seq s = load_seq(a, r.b);
+    const Seq s = load_seq<PT>(a, r.b);
     const int nu = (s.n + TT - 1) / TT;
     for (int u0 = 0; u0 < nu; u0 += 32) {
-        const int v = u0 + lane < nu ? unit_tiles<BN>(a, s, u0 + lane, TT).n : 0;
+        const int v = u0 + lane < nu ? unit_tiles<BN, PT>(a, s, u0 + lane, TT).n : 0;
         long long inc = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -294,7 +333,7 @@ static __device__ __noinline__ int units_of_broken(const PagedArgs &a, int TT, i
 // barriers inside, the result valid after the last).  min_tiles: without waves ahead of it the list is
 // cut into stretches of at least that many tiles (but for the last), so that little work is not cut
 // into pieces that cost more than they save.
-template <int BN, int kThreads, bool kWaves>
+template <int BN, int kThreads, bool kWaves, Part PT = Part::kAll>
 __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_tiles, uint8_t *scratch, Share *out,
                                            unsigned int *err) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grid = static_cast<int>(gridDim.x);
@@ -306,7 +345,7 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
         if (warp == 0) {
             Seq s{};
             if (lane < a.B) {
-                s = load_seq(a, lane);
+                s = load_seq<PT>(a, lane);
                 if (!s.ok && blockIdx.x == 0) atomicOr(err, SWA_DEVERR_BAD_POSITION);
             }
             const int nu = (s.n + TT - 1) / TT;
@@ -316,7 +355,7 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
                 int n[kFew], sum = 0;
 #pragma unroll
                 for (int ut = 0; ut < kFew; ++ut) {
-                    n[ut] = ut < nu ? unit_tiles<BN>(a, s, ut, TT).n : 0;
+                    n[ut] = ut < nu ? unit_tiles<BN, PT>(a, s, ut, TT).n : 0;
                     sum += n[ut];
                 }
                 long long inc = static_cast<long long>(sum) * a.H_kv;
@@ -400,7 +439,7 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
     // 1. units of one kv head of each sequence, 2. their running sum
     bool fine = true;
     for (int b = tid; b < a.B; b += kThreads) {
-        const Seq s = load_seq(a, b);
+        const Seq s = load_seq<PT>(a, b);
         fine = fine && s.ok;
         if (!s.ok && blockIdx.x == 0) atomicOr(err, SWA_DEVERR_BAD_POSITION);
         units[b] = (s.n + TT - 1) / TT;
@@ -447,9 +486,9 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
         const bool in = x < n_units;
         int n = 0;
         if (in) {
-            const Seq s = load_seq(a, b);
+            const Seq s = load_seq<PT>(a, b);
             const int ut = x - units[b];
-            n = unit_tiles<BN>(a, s, ut, TT).n;
+            n = unit_tiles<BN, PT>(a, s, ut, TT).n;
             if (deal) {
                 const int nu = (s.n + TT - 1) / TT;
                 for (int h = 0, u = units[b] * a.H_kv + ut; h < a.H_kv; ++h, u += nu) {
@@ -548,7 +587,7 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
         if (warp == 0 && waves >= 0) {
             Share sh{first, 0, 0, 0, 0, left, waves, mine + left, turn, 0, 0, 0};
             if (left > 0) {
-                const Place p = find_tile<BN>(a, TT, tiles, first, lane);
+                const Place p = find_tile<BN, PT>(a, TT, tiles, first, lane);
                 sh.b = p.b;
                 sh.kvh = p.kvh;
                 sh.ut = p.ut;
@@ -573,7 +612,7 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
             }
         } else if (kWaves && warp == 1 && left > 0) {
             const long long X = first + left - 1;
-            const Place p = find_tile<BN>(a, TT, tiles, X, lane);
+            const Place p = find_tile<BN, PT>(a, TT, tiles, X, lane);
             const int n = turn_of(X - p.j + p.n - 1) - turn + 1;
             if (lane == 0) out->open_pieces = n;
         }

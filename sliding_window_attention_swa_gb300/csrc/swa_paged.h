@@ -8,6 +8,18 @@
 
 namespace swa {
 
+// What a launch of an attention kernel computes.  kAll: the whole of swa_paged_attend.  Of
+// swa_paged_attend_shared, kPrefix: every group's new tokens over the positions that its sequences
+// share, kOwn: each sequence's new tokens over the positions behind those, joined with that.
+enum class Part { kAll, kPrefix, kOwn };
+
+// A group's prefix part: n packed rows from q0 on, of several sequences, over the positions below
+// `end` (of which those at or past the window of p0, the least position stored next of them, and the
+// sinks matter) in the pages of sequence `row`; top: the largest position of a row.  n = 0: nothing shared.
+struct PagedGroup {
+    int32_t q0, n, p0, end, row, top, unused[2];
+};
+
 // One call of swa_paged_attend / swa_paged_append, as the kernels take it.
 struct PagedArgs {
     const uint16_t *q;  // [N, H_q, D] bf16 bits; element strides of (token, head)
@@ -27,6 +39,13 @@ struct PagedArgs {
     int n_sink;
     int max_q;  // 0: not known
     float scale_log2;
+    // parts: kPrefix reads groups (B is their number) and, with a window, the rows' positions, and writes
+    // pre_*; kOwn reads base and pre_*
+    const PagedGroup *groups;
+    const int32_t *pos;   // [N]
+    const int32_t *base;  // [B]: the positions below it are in the prefix part
+    float *pre_lse;       // [N, H_q]: log2 of the prefix part's sum of weights (-inf: it has no key of the row)
+    float *pre_o;         // [N, H_q, D]: its weighted mean
 };
 
 constexpr int kPagedMaxB = 8192;
@@ -75,12 +94,15 @@ PagedShape paged_split_shape(const PagedArgs &a);
 // Its shared units are joined by launch_paged_merge.
 // after_append: launched as a programmatic dependent of the append kernel just before it on the
 // stream (everything up to the first copy of a page overlaps that kernel).
-cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s);
+cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s,
+                               Part part = Part::kAll);
 void paged_split_read_clear_error(unsigned int *data, unsigned int *wait);
-cudaError_t launch_paged_merge(const PagedArgs &a, const PagedWs &w, const PagedShape &x, cudaStream_t s);
+cudaError_t launch_paged_merge(const PagedArgs &a, const PagedWs &w, const PagedShape &x, cudaStream_t s,
+                               Part part = Part::kAll);
 // Many rows (swa_paged_tile.cu); w.done is zero at its start.
 PagedShape paged_tile_shape(const PagedArgs &a);
-cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s);
+cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s,
+                              Part part = Part::kAll);
 void paged_tile_read_clear_error(unsigned int *data, unsigned int *wait);
 
 // bf16 maps with 128-B swizzle.
@@ -110,7 +132,12 @@ cudaError_t launch_dependent(bool dependent, void (*kernel)(P...), dim3 grid, in
     cfg.numAttrs = dependent ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+bool paged_few_rows(const PagedArgs &a);  // the few-row kernel takes the batch
 size_t paged_workspace_bytes(const PagedArgs &a);
+// Groups of sequences that share leading pages (swa_paged_shared.cu).
+size_t paged_shared_workspace_bytes(const PagedArgs &a, int n_groups);
+cudaError_t launch_paged_shared(const PagedArgs &a, const int32_t *group_start, int n_groups, void *ws, cudaStream_t s);
+unsigned int paged_shared_read_clear_error();
 // zero, n_zero: words that the kernel sets to 0 beside its own work (n_zero may be 0).
 cudaError_t launch_paged_append(const PagedArgs &a, int32_t *zero, int n_zero, cudaStream_t s);
 cudaError_t launch_paged_attend(const PagedArgs &a, void *ws, cudaStream_t s);

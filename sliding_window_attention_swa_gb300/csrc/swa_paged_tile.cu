@@ -62,6 +62,7 @@ constexpr float kRescaleTau = 8.0f;  // log2 units: rescale O when the max grows
 // result goes; the unit's others lie in 2 * owner + 1, 2 * owner + 2, 2 * owner + 4, ...: `pieces`.
 struct TilePiece {
     int b, kvh, ut, q0, n, p0, sink, lo, nt, j0, j1, slot, owner, pieces;
+    int base, row, top;  // of a part (Seq)
     __device__ __forceinline__ int tile(int i) const volatile { return j0 + i < sink ? j0 + i : lo + (j0 + i - sink); }
     __device__ __forceinline__ bool open() const volatile { return j1 < nt; }
 };
@@ -157,7 +158,20 @@ __device__ __forceinline__ void store_row16(uint16_t *dst, const float *f, bool 
     }
 }
 
-template <int D>
+// f += w * the values of a row of the prefix part
+template <int N>
+__device__ __forceinline__ void add_prefix(float (&f)[N], const float *pre, float w) {
+#pragma unroll
+    for (int x = 0; x < N / 4; ++x) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(pre) + x);
+        f[4 * x] += w * v.x;
+        f[4 * x + 1] += w * v.y;
+        f[4 * x + 2] += w * v.z;
+        f[4 * x + 3] += w * v.w;
+    }
+}
+
+template <int D, Part PT>
 __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TileArgs ta) {
@@ -233,8 +247,13 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     }
     const int TT = ta.TT;
     tc_fence_before();
+    if constexpr (PT != Part::kAll) {
+        // the kernels before this one have found the groups; of kOwn's, have written the prefix part
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if constexpr (PT == Part::kPrefix) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
     // (its block barriers also publish the mbarriers and the TMEM address)
-    find_share<BN, C::THREADS, true>(a, TT, ta.min_tiles, sgen + C::OFF_RING, share, &g_ptile_data);
+    find_share<BN, C::THREADS, true, PT>(a, TT, ta.min_tiles, sgen + C::OFF_RING, share, &g_ptile_data);
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     const int cta_tiles = share->tiles;
@@ -276,6 +295,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         bool ok = true;
         int np = 0, i = 0, n = 0;  // pieces taken, next tile of the current one, its tiles
         int b = 0, kvh = 0, lo = 0, t1 = 0, end = 0, sink = 0, t_first = 0, j0 = 0, looked = 0, token = 0;
+        int n_sink = a.n_sink, entry0 = 0;  // of a part: its sinks, its first page
         auto look_up = [&]() -> Group {
             if (i >= n) {
                 volatile TilePiece *p = get_piece(np, ok);
@@ -291,6 +311,15 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 t1 = p->p0 + min(p->n, (p->ut + 1) * TT) - 1;
                 lo = t0 >= a.window ? t0 - a.window + 1 : 0;
                 end = p->p0 + p->n;
+                if constexpr (PT == Part::kPrefix) {
+                    b = p->row;
+                    lo = p->p0 >= a.window ? p->p0 - a.window + 1 : 0;
+                    end = p->base;
+                    t1 = end - 1;
+                } else if constexpr (PT == Part::kOwn) {
+                    n_sink = sinks_of<PT>(a, p->base);
+                    entry0 = p->base >> a.ps_log2;
+                }
                 token = p->q0 + p->ut * TT;
                 give_back(np++);
             }
@@ -301,8 +330,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             i += tiles;
             looked += tiles;
             return Group{tiles, kvh, kp & (a.ps - 1),
-                         there ? __ldg(a.table + static_cast<int64_t>(b) * a.width + (kp >> a.ps_log2)) : -1,
-                         there && kp <= t1 && (kp + box > lo || kp < a.n_sink), head};
+                         there ? __ldg(a.table + static_cast<int64_t>(b) * a.width + entry0 + (kp >> a.ps_log2)) : -1,
+                         there && kp <= t1 && (kp + box > lo || kp < n_sink), head};
         };
         // The next fill: its slot and its phase.  The loop below is kept short: beside two softmax warps
         // on its sub-partition an instruction of this warp takes about ten cycles.
@@ -602,10 +631,11 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             if (!wk) break;
             const int n = wk->j1 - wk->j0;
             const bool single = is_single(wk->n, wk->ut);
-            const int t = wk->p0 + wk->ut * TT + (single ? 0 : ow * ta.TQ) + r / a.G;  // this row's position
+            int t = wk->p0 + wk->ut * TT + (single ? 0 : ow * ta.TQ) + r / a.G;  // this row's position
+            const int n_sink = PT == Part::kOwn ? sinks_of<PT>(a, wk->base) : a.n_sink;
             // the tile's first position, and the first key that its last row's window keeps
             const int tlo = t - r / a.G;
-            const int thi = min(tlo + ta.TQ, max(wk->p0 + wk->n, tlo + 1)) - 1;
+            const int thi = PT == Part::kPrefix ? wk->top : min(tlo + ta.TQ, max(wk->p0 + wk->n, tlo + 1)) - 1;
             // tiles [ia, ib) of the piece lie in every row's window; iz is the one the sequence ends in, iw
             // the first of the window if in it or in the one before are keys that no query keeps
             int ia, ib, iz, iw;
@@ -613,15 +643,18 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 const int lo_thi = thi >= a.window ? thi - a.window + 1 : 0;
                 const int first = wk->sink - wk->j0 - wk->lo;  // index of tile x of the window: first + x
                 ia = max(first + wk->lo, first + (lo_thi + BN - 1) / BN);
-                ib = first + (tlo + 1) / BN;
+                ib = first + (PT == Part::kPrefix ? wk->base : tlo + 1) / BN;
                 const int lo_p0 = wk->p0 >= a.window ? wk->p0 - a.window + 1 : 0;
-                iw = lo_p0 > a.n_sink && (wk->sink > 0 || wk->lo * BN < lo_p0) ? wk->sink - wk->j0 : -8;
-                iz = !wk->open() && (wk->tile(n - 1) + 1) * BN > wk->p0 + wk->n ? n - 1 : -1;
+                iw = lo_p0 > n_sink && (wk->sink > 0 || wk->lo * BN < lo_p0) ? wk->sink - wk->j0 : -8;
+                // (a prefix ends with a page: what is past it in its last tile comes as zeros)
+                iz = PT != Part::kPrefix && !wk->open() && (wk->tile(n - 1) + 1) * BN > wk->p0 + wk->n ? n - 1 : -1;
             }
             // A warp without a row hands its P over as it finds it: rows of other warps do not see it,
             // and its own are not stored.  The exponentials of one sub-partition's warps are what bounds a
             // tile, so the others' (a single token has rows in one warp of four) are not spent.
             const bool idle = __all_sync(0xffffffffu, (r / a.G >= ta.TQ) || t >= wk->p0 + wk->n);
+            if constexpr (PT == Part::kPrefix)  // the rows' own positions, where they matter
+                t = a.window != INT_MAX && r / a.G < ta.TQ && t < wk->p0 + wk->n ? __ldcg(a.pos + wk->q0 + (t - wk->p0)) : wk->p0;
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
             for (int i = takes_tiles ? (single ? wg : 0) : n; i < n; i += single ? 2 : 1) {
@@ -632,9 +665,10 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     // zero the value rows that no query keeps, in boxes that also hold others (the rest came as
                     // zeros), while S is under way.  The first P V of the tile waits for this warpgroup's P, and
                     // with two query tiles the second is issued after it.
-                    const int box = min(a.ps, BN), k0 = wk->tile(i) * BN, p0 = wk->p0, end = p0 + wk->n;
+                    const int box = min(a.ps, BN), k0 = wk->tile(i) * BN, p0 = wk->p0;
+                    const int end = PT == Part::kPrefix ? wk->base : p0 + wk->n;
                     const int lo = p0 >= a.window ? p0 - a.window + 1 : 0;
-                    const bool below = k0 < lo && k0 + BN > a.n_sink, past = k0 + BN > end;
+                    const bool below = k0 < lo && k0 + BN > n_sink, past = PT != Part::kPrefix && k0 + BN > end;
                     const int fv = kfill(k, g) + 1;
                     if ((below || past) && !warp_wait(bar_full(fv % NSLOT), fphase(fv), abort)) {
                         ok = false;
@@ -652,8 +686,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     };
                     if (past) zero(end, (end + box - 1) & -box);
                     if (below) {
-                        zero(a.n_sink, min(lo, (a.n_sink + box - 1) & -box));
-                        zero(max(a.n_sink, lo & -box), lo);
+                        zero(n_sink, min(lo, (n_sink + box - 1) & -box));
+                        zero(max(n_sink, lo & -box), lo);
                     }
                     if (below || past) fence_proxy_async_smem();
                 }
@@ -695,9 +729,9 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                 // ---- mask: columns [lo, hi) and those of sinks (only tiles that some row cuts)
                 if (i < ia || i >= ib) {
                     const int k0 = wk->tile(i) * BN;
-                    const int hi = min(max(t - k0 + 1, 0), BN);
+                    const int hi = min(max((PT == Part::kPrefix ? wk->base : t + 1) - k0, 0), BN);
                     int lo = min(max((t >= a.window ? t - a.window + 1 : 0) - k0, 0), BN);
-                    const int sk = min(max(a.n_sink - k0, 0), hi);
+                    const int sk = min(max(n_sink - k0, 0), hi);
                     if (sk >= lo) lo = 0;
                     {
                         // 32 columns at a time, as a word of bits
@@ -846,9 +880,12 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             }
             const int unit_pieces = wk->pieces;
             const bool whole = unit_pieces == 0;
-            const float inv_l = whole ? 1.f / l : 1.f;  // (of a whole unit: every row keeps its own key)
-            wa *= inv_l;
-            wb *= inv_l;
+            // (every row keeps its own key, but may have none of a prefix)
+            const float inv_l = !whole ? 1.f : PT == Part::kPrefix && l == 0.f ? 0.f : 1.f / l;
+            if constexpr (PT != Part::kOwn) {
+                wa *= inv_l;
+                wb *= inv_l;
+            }
             const int tq = r / a.G, i0 = wk->ut * TT + (single ? 0 : ow * ta.TQ);  // the tile's first token
             const int64_t tok = static_cast<int64_t>(wk->q0) + i0 + tq;
             const int h = wk->kvh * a.G + r % a.G;
@@ -860,6 +897,27 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                                              wk->owner + unit_pieces <= static_cast<int>(gridDim.x))),
                               &g_ptile_err);
             uint16_t *orow = a.o + tok * a.o_st[0] + h * a.o_st[1];
+            // this row of the prefix part, and (kOwn) its weight
+            float *pre = PT == Part::kAll ? nullptr : a.pre_o + (tok * a.H_q + h) * D;
+            float wp = 0.f;
+            // joins the row's own part (m, l) with the prefix's: returns the weight of the own part
+            auto with_prefix = [&]() -> float {
+                const float pl = store && wk->base > 0 ? __ldcg(a.pre_lse + tok * a.H_q + h) : -INFINITY;
+                const float mn = fmaxf(m, pl), wo = ex2(m - mn);
+                wp = ex2(pl - mn);
+                l = l * wo + wp;
+                m = mn;
+                const float inv = 1.f / l;
+                wp *= inv;
+                return wo * inv;
+            };
+            if constexpr (PT == Part::kOwn) {
+                if (whole) {
+                    const float wo = with_prefix();
+                    wa *= wo;
+                    wb *= wo;
+                }
+            }
             const int pslot = wk->slot, prow = (single ? 0 : ow * BM) + r;
             // (a shared query tile: each warpgroup keeps the maximum and sum beside its half of the columns)
             const int mrow = ow * BM + r;
@@ -891,7 +949,16 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                         for (int e = 0; e < 8; ++e) wv[e] = __float_as_uint(f[q8 * 8 + e]);
                         st_global_v8(ta.ws.acc + partial_at<D>(pslot, NQT * BM, prow, c * 32 + q8 * 8), wv);
                     }
+                } else if (store && PT == Part::kPrefix) {
+#pragma unroll
+                    for (int q8 = 0; q8 < 4; ++q8) {
+                        uint32_t wv[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) wv[e] = __float_as_uint(f[q8 * 8 + e]);
+                        st_global_v8(pre + c * 32 + q8 * 8, wv);
+                    }
                 } else if (store) {
+                    if (PT == Part::kOwn && wp > 0.f) add_prefix<32>(f, pre + c * 32, wp);
                     store_row16(orow + c * 32, f, ta.o_align32);
                     store_row16(orow + c * 32 + 16, f + 16, ta.o_align32);
                 }
@@ -935,7 +1002,10 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                         for (int e = 0; e < 4; ++e) l += v4[e].y * ex2(v4[e].x - ms);
                         m = mn;
                     }
-                    const float inv = 1.f / l;  // (a row keeps its own key: some piece's maximum is finite)
+                    // (a row keeps its own key: some piece's maximum is finite; of a prefix it may have none)
+                    float inv = PT == Part::kPrefix && l == 0.f ? 0.f : 1.f / l;
+                    const float m_own = PT == Part::kPrefix && m == -INFINITY ? 0.f : m;
+                    if constexpr (PT == Part::kOwn) inv = with_prefix();
                     if (unit_pieces > 4) four(0, v4);
                     if (store) {
 #pragma unroll 1
@@ -958,7 +1028,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
-                                    const float wt = ex2(v4[e].x - m) * inv;  // (0 past the last piece)
+                                    const float wt = ex2(v4[e].x - m_own) * inv;  // (0 past the last piece)
 #pragma unroll
                                     for (int x = 0; x < 4; ++x) {
                                         f[4 * x] += wt * v[e][x].x;
@@ -968,14 +1038,26 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                                     }
                                 }
                             }
-                            store_row16(orow + c * 16, f, ta.o_align32);
+                            if constexpr (PT == Part::kPrefix) {
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    reinterpret_cast<float4 *>(pre + c * 16)[x] =
+                                        make_float4(f[4 * x], f[4 * x + 1], f[4 * x + 2], f[4 * x + 3]);
+                            } else {
+                                if (PT == Part::kOwn && wp > 0.f) add_prefix<16>(f, pre + c * 16, wp);
+                                store_row16(orow + c * 16, f, ta.o_align32);
+                            }
                         }
                     }
                 }
             }
             if (store && (!single || ow == 0) && (whole || joined)) {
-                a.lse[tok * a.H_q + h] = (m + log2f(l)) * 0.69314718055994531f;
-                if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, t);
+                if constexpr (PT == Part::kPrefix) {
+                    a.pre_lse[tok * a.H_q + h] = l == 0.f ? -INFINITY : m + log2f(l);
+                } else {
+                    a.lse[tok * a.H_q + h] = (m + log2f(l)) * 0.69314718055994531f;
+                    if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, PT == Part::kOwn ? t + wk->base : t);
+                }
             }
             give_back(k);
             J += n;
@@ -986,7 +1068,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         const Share sh = *share;
         bool ok = true;
         Piece p{};
-        Plan<BN> plan(a, TT, sh);
+        Plan<BN, PT> plan(a, TT, sh);
         int k = 0, kq = 0;  // pieces handed over, query tiles loaded
         int loads0 = 0, loads1 = 0, y = 1;  // query tiles of each buffer; y: the last unit of one took that
         bool more = true;
@@ -1015,6 +1097,11 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     t->q0 = p.s.q0;
                     t->n = p.s.n;
                     t->p0 = p.s.p0;
+                    if constexpr (PT != Part::kAll) t->base = p.s.base;
+                    if constexpr (PT == Part::kPrefix) {
+                        t->row = p.s.row;
+                        t->top = p.s.top;
+                    }
                     t->sink = p.u.sink;
                     t->lo = p.u.lo;
                     t->nt = p.u.n;
@@ -1081,15 +1168,15 @@ int tiles_of_unit(const PagedArgs &a) {
     return pairs >= 2 * static_cast<int64_t>(paged_sm_count()) ? 2 : 1;
 }
 
-template <int D>
-cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s) {
+template <int D, Part PT>
+cudaError_t launch_part(const PagedArgs &a, const PagedWs &w, bool dependent, cudaStream_t s) {
     using C = TileCfg<D>;
     // the dynamic shared-memory limit is a per-device function attribute: set once per device
     static std::atomic<bool> configured[64];
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) dev = -1;
     if (dev < 0 || !configured[dev].load(std::memory_order_acquire)) {
-        cudaError_t e = cudaFuncSetAttribute(paged_tile_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        cudaError_t e = cudaFuncSetAttribute(paged_tile_kernel<D, PT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
         if (dev >= 0) configured[dev].store(true, std::memory_order_release);
     }
@@ -1107,7 +1194,16 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cu
     t.min_tiles = 4;
     t.o_align32 = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.o_st[0] % 16 == 0 && a.o_st[1] % 16 == 0;
     t.fault_stop_fill = fault_plan().band_stop_fill;
-    return launch_dependent(after_append, paged_tile_kernel<D>, dim3(x.ctas), C::THREADS, C::SMEM, s, mq, mk, mv, t);
+    return launch_dependent(dependent, paged_tile_kernel<D, PT>, dim3(x.ctas), C::THREADS, C::SMEM, s, mq, mk, mv, t);
+}
+
+template <int D>
+cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s, Part part) {
+    switch (part) {
+        case Part::kPrefix: return launch_part<D, Part::kPrefix>(a, w, true, s);
+        case Part::kOwn: return launch_part<D, Part::kOwn>(a, w, true, s);
+        default: return launch_part<D, Part::kAll>(a, w, after_append, s);
+    }
 }
 
 }  // namespace
@@ -1116,11 +1212,11 @@ PagedShape paged_tile_shape(const PagedArgs &a) {
     return PagedShape{paged_sm_count(), a.D <= 128 ? 2 : 1, BM, BM / a.G};
 }
 
-cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s) {
+cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s, Part part) {
     switch (a.D) {
-        case 64: return launch_d<64>(a, w, after_append, s);
-        case 128: return launch_d<128>(a, w, after_append, s);
-        case 256: return launch_d<256>(a, w, after_append, s);
+        case 64: return launch_d<64>(a, w, after_append, s, part);
+        case 128: return launch_d<128>(a, w, after_append, s, part);
+        case 256: return launch_d<256>(a, w, after_append, s, part);
         default: return cudaErrorInvalidValue;
     }
 }
