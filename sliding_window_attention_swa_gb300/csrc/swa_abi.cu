@@ -862,6 +862,8 @@ swa_status swa_read_device_errors(swa_stream_t stream, swa_device_errors *out) {
     e.cache |= data;
     e.split |= split;
     e.prefill |= prefill;
+    e.split |= swa::shared_rows_read_clear_error(&data);
+    e.cache |= data;
     if (out) *out = e;
     constexpr uint32_t kTimeout = SWA_DEVERR_WAIT_TIMEOUT | SWA_DEVERR_DRAIN_TIMEOUT;
     if ((e.prefill | e.split) & kTimeout) return SWA_ERR_TIMEOUT;

@@ -307,6 +307,11 @@ __device__ __forceinline__ Place find_tile(const PagedArgs &a, int TT, const lon
 
 constexpr int kMaxWaveCtas = 256;
 constexpr int kJoinTiles = 12;
+// (a prefix part's pieces are not joined by its kernel, and cost little more than to be written)
+template <Part PT>
+__device__ __forceinline__ constexpr int join_tiles() {
+    return PT == Part::kPrefix ? 2 : kJoinTiles;
+}
 // Scratch of find_share: tiles [B] (64 bits), first units [B + 1], and with waves loads [2][CTAs].
 __host__ __device__ constexpr int share_scratch(int B) { return B * 12 + 4; }
 constexpr int kShareScratch = share_scratch(kPagedMaxB) + 2 * kMaxWaveCtas * 4;
@@ -387,7 +392,7 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
 #pragma unroll
                 for (int ut = 0; ut < kFew; ++ut) longest = max(longest, n[ut]);
                 longest = __reduce_max_sync(0xffffffffu, longest);
-                if (kWaves && longest <= len + kJoinTiles) {  // unit c whole
+                if (kWaves && longest <= len + join_tiles<PT>()) {  // unit c whole
                     int units = nu * a.H_kv;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
@@ -525,7 +530,7 @@ __device__ __forceinline__ void find_share(const PagedArgs &a, int TT, int min_t
             int top = 0;
             for (int i = lane; i < grid; i += 32) top = max(top, all_loads[i]);
             top = __reduce_max_sync(0xffffffffu, top);
-            if (top <= max((total + grid - 1) / grid, static_cast<long long>(min_tiles)) + kJoinTiles) {
+            if (top <= max((total + grid - 1) / grid, static_cast<long long>(min_tiles)) + join_tiles<PT>()) {
                 if (warp == 0 && lane == 0)
                     *out = Share{total, 0, 0, 0, 0, 0, static_cast<int>((all_units + grid - 1) / grid), all_loads[c],
                                  0, 0, 0, 0};

@@ -10,14 +10,16 @@ namespace swa {
 
 // What a launch of an attention kernel computes.  kAll: the whole of swa_paged_attend.  Of
 // swa_paged_attend_shared, kPrefix: every group's new tokens over the positions that its sequences
-// share, kOwn: each sequence's new tokens over the positions behind those, joined with that.
+// share, kOwn: each sequence's new tokens over the positions behind those; the parts are joined by a
+// kernel of their own (swa_paged_shared.cu).
 enum class Part { kAll, kPrefix, kOwn };
 
-// A group's prefix part: n packed rows from q0 on, of several sequences, over the positions below
-// `end` (of which those at or past the window of p0, the least position stored next of them, and the
-// sinks matter) in the pages of sequence `row`; top: the largest position of a row.  n = 0: nothing shared.
+// A group's prefix part: the packed rows of n tokens from q0 on, of several sequences, over the positions
+// below `end` (of which those at or past the window of p0, the least position stored next of them, and
+// the sinks matter) in the pages of sequence `row`; top: the largest position of a row.  n = 0: nothing
+// for the many-row kernel; few: the tokens of a part that the kernel for few rows has.
 struct PagedGroup {
-    int32_t q0, n, p0, end, row, top, unused[2];
+    int32_t q0, n, p0, end, row, top, few, unused;
 };
 
 // One call of swa_paged_attend / swa_paged_append, as the kernels take it.
@@ -39,13 +41,16 @@ struct PagedArgs {
     int n_sink;
     int max_q;  // 0: not known
     float scale_log2;
-    // parts: kPrefix reads groups (B is their number) and, with a window, the rows' positions, and writes
-    // pre_*; kOwn reads base and pre_*
+    // parts: kPrefix reads groups (B is their number) and, with a window, the rows' positions, kOwn reads base
     const PagedGroup *groups;
     const int32_t *pos;   // [N]
     const int32_t *base;  // [B]: the positions below it are in the prefix part
-    float *pre_lse;       // [N, H_q]: log2 of the prefix part's sum of weights (-inf: it has no key of the row)
-    float *pre_o;         // [N, H_q, D]: its weighted mean
+    // A part's results, fp32.  A unit that one CTA has whole: here; one that several have: in their slots of
+    // PagedWs.  units, at (q0 / TT + b + ut) * H_kv + kvh: the CTA that begins the unit, and its
+    // pieces (0: whole).
+    float2 *part_ml;  // [N, H_q]: maximum (log2 units), sum of weights
+    float *part_o;    // [N, H_q, D]: unnormalised weighted values
+    int2 *part_units;
 };
 
 constexpr int kPagedMaxB = 8192;
@@ -94,13 +99,12 @@ PagedShape paged_split_shape(const PagedArgs &a);
 // Its shared units are joined by launch_paged_merge.
 // after_append: launched as a programmatic dependent of the append kernel just before it on the
 // stream (everything up to the first copy of a page overlaps that kernel).
-cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s,
-                               Part part = Part::kAll);
+cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s);
 void paged_split_read_clear_error(unsigned int *data, unsigned int *wait);
-cudaError_t launch_paged_merge(const PagedArgs &a, const PagedWs &w, const PagedShape &x, cudaStream_t s,
-                               Part part = Part::kAll);
+cudaError_t launch_paged_merge(const PagedArgs &a, const PagedWs &w, const PagedShape &x, cudaStream_t s);
 // Many rows (swa_paged_tile.cu); w.done is zero at its start.
 PagedShape paged_tile_shape(const PagedArgs &a);
+int paged_tile_tokens(const PagedArgs &a, Part part);  // tokens of a unit
 cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s,
                               Part part = Part::kAll);
 void paged_tile_read_clear_error(unsigned int *data, unsigned int *wait);
@@ -138,6 +142,7 @@ size_t paged_workspace_bytes(const PagedArgs &a);
 size_t paged_shared_workspace_bytes(const PagedArgs &a, int n_groups);
 cudaError_t launch_paged_shared(const PagedArgs &a, const int32_t *group_start, int n_groups, void *ws, cudaStream_t s);
 unsigned int paged_shared_read_clear_error();
+unsigned int shared_rows_read_clear_error(unsigned int *data);
 // zero, n_zero: words that the kernel sets to 0 beside its own work (n_zero may be 0).
 cudaError_t launch_paged_append(const PagedArgs &a, int32_t *zero, int n_zero, cudaStream_t s);
 cudaError_t launch_paged_attend(const PagedArgs &a, void *ws, cudaStream_t s);

@@ -1,19 +1,25 @@
 // swa_paged_shared.cu -- attention of sequences that share leading pages: each group's prefix is read
 // once for the new tokens of all its sequences.
 //
-// A row's softmax is the same over its keys in any two parts (m, l, acc), joined by their maxima:
-//   1. plan (here): finds for every group how many leading positions its sequences share.
-//   2. prefix part (paged_tile_kernel, kPrefix): the group's packed rows, of all its sequences, are the rows of
-//      the tensor cores' tiles; each row's mean and log2 of its sum go to the workspace in fp32.
-//   3. own part (the few-row or the many-row kernel, kOwn): each sequence over the positions behind, counted
-//      from there, and where a unit's rows are written the prefix part joins them as one piece more.
+// A row's softmax over its keys is that over any two parts of them, joined by their maxima:
+//   1. plan (here): finds for every group how many leading positions its sequences share, and lists the
+//      stretches that the kernel for few rows takes.
+//   2. prefix part: the group's packed rows, of all its sequences, over the shared positions: tiles of the tensor
+//      cores (paged_tile_kernel, kPrefix), or, where a group has at most 16 rows, stretches.
+//   3. own part: each sequence over the positions behind those: stretches (paged_rows_kernel), or, where a
+//      sequence has more than 16 rows, tiles again (paged_tile_kernel, kOwn).
+//   4. merge (here): the partial results of every row, all of them in fp32, are joined and rounded once.
+// The kernels follow one another by programmatic dependence: the own part's blocks start where the
+// prefix part's have ended, without waiting for all of them.
 // With single tokens a group of R sequences reads its prefix once instead of R times, and its products go to
 // the tensor cores in tiles of 128 rows instead of 16.
+#include <algorithm>
 #include <climits>
+#include <cmath>
 
 #include <cooperative_groups.h>
 
-#include "swa_paged.cuh"
+#include "swa_paged_shared.cuh"
 
 namespace swa {
 namespace {
@@ -27,17 +33,9 @@ constexpr int kFewGroups = 32;  // below it a cluster plans a group, else a bloc
 constexpr int kCluster = 8;
 constexpr int kChunk = 256;  // entries that a warp compares at a time: eight loads a lane and row in flight
 
-struct PlanArgs {
-    PagedArgs a;
-    const int32_t *group_start;  // [n_groups + 1]
-    int n_groups;
-    PagedGroup *groups;
-    int32_t *base, *pos;
-    int32_t *zero;  // words that the kernels behind this one want zero
-    int n_zero;
-    int TQ;          // tokens of a tile of the prefix part
-    int own_tokens;  // tokens that the own part's kernel has in a tile (0: any sequence's)
-};
+// Shared positions below which a group is computed as none: a part of its own costs more than they do.
+constexpr int kLeastShared = 64;
+constexpr int kTileRows = 128;  // rows of a query tile of the many-row kernel
 
 // Of a group's sequences that have new tokens.
 struct Members {
@@ -66,8 +64,72 @@ __device__ __forceinline__ Members shuffled(const Members &x, int o) {
 // says of the tables: a group that shares nothing is computed as if it were none.
 // Bound by latency: the list, the sequences' lengths, then the table's rows, all of them once.
 // ---------------------------------------------------------------------------------------------
-__global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_constant__ PlanArgs pa) {
-    const PagedArgs &a = pa.a;
+// Puts the stretches of the warp's units (a unit a lane, `count` of them, of keys k) on the list.
+__device__ __forceinline__ void list_stretches(const SharedArgs &sa, const Keys &k, int count, Stretch t) {
+    const int lane = threadIdx.x & 31;
+    int inc = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    int at = 0;
+    if (lane == 31 && inc > 0) at = atomicAdd(sa.n_stretches, inc);
+    at = __shfl_sync(0xffffffffu, at, 31) + inc - count;
+    for (int i = 0; i < count; ++i) {
+        // (more than there is room for: sequences that overlap, from a q_start that goes down)
+        if (at + i >= sa.cap) {
+            atomicOr(&g_shared_err, SWA_DEVERR_BAD_POSITION);
+            break;
+        }
+        t.k0 = k.begin(i);
+        t.k1 = k.close(i);
+        t.plane = i < k.count ? i : sa.part[0].planes - 1;
+        int4 *dst = reinterpret_cast<int4 *>(sa.stretches + at + i);
+        dst[0] = make_int4(t.row, t.q0, t.n, t.plane);
+        dst[1] = make_int4(t.k0, t.k1, t.part, 0);
+    }
+}
+
+// What the other kernels need to know of sequences b0 .. b1 - 1 (of group g, with `base` positions in its prefix
+// part): a warp of `warps` has every 32nd, number `w` of them.
+__device__ __forceinline__ void put_sequences(const SharedArgs &sa, int b0, int b1, int g, int base, int w, int warps) {
+    const PagedArgs &a = sa.a;
+    const int lane = threadIdx.x & 31, TT = kStretchRows / a.G;
+    for (int first = b0 + w * 32; first < b1; first += warps * 32) {
+        const int b = first + lane;
+        Seq s{};
+        if (b < b1) {
+            s = load_seq(a, b);
+            if (!s.ok) atomicOr(&g_shared_err, SWA_DEVERR_BAD_POSITION);
+            // (a sequence without new tokens may end inside what the others share)
+            sa.base[b] = s.n > 0 ? base : 0;
+            sa.group_of[b] = s.n > 0 && base > 0 ? g : -1;
+        }
+        const int longest = __reduce_max_sync(0xffffffffu, s.n);
+        if (sa.few || (base > 0 && a.window != INT_MAX)) {  // the rows' positions
+            if (longest <= 8) {
+                for (int i = 0; i < s.n; ++i) sa.pos[s.q0 + i] = s.p0 + i;
+            } else {
+                for (int l = 0; l < 32; ++l) {
+                    const int n = __shfl_sync(0xffffffffu, s.n, l), q0 = __shfl_sync(0xffffffffu, s.q0, l),
+                              p0 = __shfl_sync(0xffffffffu, s.p0, l);
+                    for (int i = lane; i < n; i += 32) sa.pos[q0 + i] = p0 + i;
+                }
+            }
+        }
+        if (!sa.few) continue;
+        for (int ut = 0; ut * TT < longest; ++ut) {
+            const bool unit = ut * TT < s.n;
+            const Keys k = unit ? own_keys(a, s, base, ut, TT, sa.part[0].planes) : Keys{};
+            list_stretches(sa, k, unit ? k.stretches() : 0,
+                           Stretch{b, s.q0 + ut * TT, min(TT, s.n - ut * TT), 0, 0, 0, 0, 0});
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_constant__ SharedArgs sa) {
+    const PagedArgs &a = sa.a;
     const cg::cluster_group cluster = cg::this_cluster();
     __shared__ Members sums[kWarps];
     __shared__ int first;  // of the group's entries in question: the first that is not shared
@@ -75,30 +137,27 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
     const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
     const int clusters = static_cast<int>(gridDim.x) / ranks, c = static_cast<int>(blockIdx.x) / ranks;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (int i = static_cast<int>(blockIdx.x) * kThreads + tid; i < pa.n_zero; i += static_cast<int>(gridDim.x) * kThreads)
-        pa.zero[i] = 0;
     bool fine = true;
-    for (int i = tid; i < pa.n_groups; i += kThreads) {
-        const int b0 = __ldg(pa.group_start + i), b1 = __ldg(pa.group_start + i + 1);
+    for (int i = tid; i < sa.n_groups; i += kThreads) {
+        const int b0 = __ldg(sa.group_start + i), b1 = __ldg(sa.group_start + i + 1);
         fine = fine && b0 >= 0 && b1 >= b0 && b1 <= a.B;
     }
     fine = __syncthreads_and(fine);
     if (!fine && blockIdx.x == 0 && tid == 0) atomicOr(&g_shared_err, SWA_DEVERR_BAD_POSITION);
     if (c == 0) {  // sequences of no group
-        const int lo = fine ? __ldg(pa.group_start) : a.B, hi = fine ? __ldg(pa.group_start + pa.n_groups) : a.B;
-        for (int b = rank * kThreads + tid; b < a.B; b += ranks * kThreads)
-            if (b < lo || b >= hi) pa.base[b] = 0;
+        const int lo = fine ? __ldg(sa.group_start) : a.B, hi = fine ? __ldg(sa.group_start + sa.n_groups) : a.B;
+        put_sequences(sa, 0, lo, -1, 0, rank * kWarps + warp, ranks * kWarps);
+        put_sequences(sa, hi, a.B, -1, 0, rank * kWarps + warp, ranks * kWarps);
     }
-    for (int g = c; g < pa.n_groups; g += clusters) {
-        const int b0 = fine ? __ldg(pa.group_start + g) : 0, b1 = fine ? __ldg(pa.group_start + g + 1) : 0;
+    for (int g = c; g < sa.n_groups; g += clusters) {
+        const int b0 = fine ? __ldg(sa.group_start + g) : 0, b1 = fine ? __ldg(sa.group_start + g + 1) : 0;
         Members m{~0ull, -1, 0, 0, 0, 0};
         for (int b = b0 + tid; b < b1; b += kThreads) {
             const Seq s = load_seq(a, b);
             if (!s.ok) m.broken = 1;
             if (s.n > 0)
                 m = join(m, Members{static_cast<unsigned long long>(s.p0) << 13 | static_cast<unsigned int>(b - b0),
-                                    s.p0 + s.n - 1, 1, pa.own_tokens ? (s.n + pa.own_tokens - 1) / pa.own_tokens : 1, 0,
-                                    s.n});
+                                    s.p0 + s.n - 1, 1, sa.few ? 1 : (s.n + sa.own_tokens - 1) / sa.own_tokens, 0, s.n});
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) m = join(m, shuffled(m, o));
@@ -112,7 +171,9 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         for (int w = 1; w < kWarps; ++w) m = join(m, sums[w]);
         int base = 0, leader = 0, p0 = 0;
         // A prefix part that has as many tiles of rows as the sequences alone would save nothing.
-        const bool shares = !m.broken && m.count >= 2 && (m.tokens + pa.TQ - 1) / pa.TQ < m.tiles;
+        const bool stretch = sa.few && m.tokens * a.G <= kStretchRows;
+        const bool shares = !m.broken && m.count >= 2 && (m.tokens + sa.prefix_tokens - 1) / sa.prefix_tokens < m.tiles &&
+                            (stretch || sa.any_tiles);
         if (shares) {  // (the same for every thread of the cluster)
             leader = b0 + static_cast<int>(m.least & ((1u << 13) - 1));
             p0 = static_cast<int>(m.least >> 13);
@@ -152,61 +213,208 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
             else __syncthreads();
             const int f = min(ranks > 1 ? *cluster.map_shared_rank(&first, 0) : first, n);
             base = f < sinks ? 0 : (e_lo + f - sinks) << a.ps_log2;
-            if (base <= lo) base = 0;  // nothing of a window
+            if (base - lo < kLeastShared) base = 0;
         }
         // (read by the other blocks before it is set for the next group; the sums, too)
         if (ranks > 1) cluster.sync();
         else __syncthreads();
-        if (rank == 0 && tid == 0) {
+        if (rank == 0 && warp == 0) {
             PagedGroup out{};
             if (base > 0) {
                 out.q0 = a.q_start ? __ldg(a.q_start + b0) : b0;
-                out.n = static_cast<int>(m.tokens);
+                (stretch ? out.few : out.n) = static_cast<int>(m.tokens);
                 out.p0 = p0;
                 out.end = base;
                 out.row = leader;
                 out.top = m.top;
             }
-            pa.groups[g] = out;
+            if (lane == 0) sa.groups[g] = out;
+            if (out.few > 0) {
+                const Keys k = prefix_keys(a, p0, base, sa.few_prefix.planes);
+                list_stretches(sa, k, lane == 0 ? k.stretches() : 0, Stretch{leader, out.q0, out.few, 0, 0, 0, 1, 0});
+            }
         }
-        for (int b = b0 + rank * kWarps + warp; b < b1; b += ranks * kWarps) {
-            const Seq s = load_seq(a, b);
-            if (lane == 0) pa.base[b] = s.n > 0 ? base : 0;
-            if (base > 0 && a.window != INT_MAX)
-                for (int i = lane; i < s.n; i += 32)
-                    if (SWA_IN_BOUNDS(s.q0 + i < a.N, &g_shared_err)) pa.pos[s.q0 + i] = s.p0 + i;
-        }
+        put_sequences(sa, b0, b1, g, base, rank * kWarps + warp, ranks * kWarps);
     }
     // (behind an append: what waits for this kernel waits for that, too)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// ---------------------------------------------------------------------------------------------
+// merge: a warp a row.  A row's results (m, l, acc), of its own part and of its group's prefix part, each in
+// planes or in the slots of the CTAs that share a unit, are joined: with M the largest m, o = sum 2^(m - M) acc /
+// sum 2^(m - M) l.  Bound by latency: the row's sequence, its group, then the maxima, then the values.
+// ---------------------------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ SharedArgs sa) {
+    constexpr int E = D / 32;  // columns of a lane
+    const PagedArgs &a = sa.a;
+    const int lane = threadIdx.x & 31;
+    const int64_t x = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int n = static_cast<int>(x / a.H_q), h = static_cast<int>(x % a.H_q), kvh = h / a.G;
+    if (n >= a.N) return;  // (the grid has blocks of whole rows; nothing waits for these warps)
+    const int b = find_sequence(a, n, lane);
+    const Seq s = b >= 0 ? load_seq(a, b) : Seq{};
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (b < 0 || !s.ok || n < s.q0 || n >= s.q0 + s.n) return;
+    const int base = __ldcg(sa.base + b), g = __ldcg(sa.group_of + b);
+    const int i = n - s.q0;
+    // the parts: how many results, where
+    struct Where {
+        const PartResults *p;
+        int count, sink, owner, row;  // sink: the number of the sinks' stretch (their plane is the last)
+        bool pieces;
+    };
+    auto in_tiles = [&](const PartResults &p, int q0, int number) -> Where {
+        const int tok = n - q0, ut = tok / p.TT, r = tok % p.TT;
+        const int64_t at = (static_cast<int64_t>(q0 / p.TT) + number + ut) * a.H_kv + kvh;
+        const int2 u = __ldcg(p.units + at);
+        // (a unit that was never finished, after an expired wait, has any record)
+        if (u.y <= 0 || u.x < 0 || u.y > p.ctas || u.x > p.ctas - u.y) return Where{&p, 1, -1, 0, 0, false};
+        return Where{&p, u.y, -1, u.x, r / p.TQ * kTileRows + r % p.TQ * a.G + h % a.G, true};
+    };
+    auto in_planes = [&](const PartResults &p, const Keys &k) -> Where {
+        return Where{&p, k.stretches(), k.count, 0, 0, false};
+    };
+    const int TT = kStretchRows / a.G;
+    Where own, pre{nullptr, 0, -1, 0, 0, false};
+    if (sa.few) own = in_planes(sa.part[0], own_keys(a, s, base, i / TT, TT, sa.part[0].planes));
+    else own = in_tiles(sa.part[0], s.q0, b);
+    if (g >= 0 && g < sa.n_groups) {
+        const int4 *gp = reinterpret_cast<const int4 *>(sa.groups + g);
+        const int4 u = __ldcg(gp), v = __ldcg(gp + 1);  // q0 n p0 end, row top few
+        if (v.z > 0) pre = in_planes(sa.few_prefix, prefix_keys(a, u.z, u.w, sa.few_prefix.planes));
+        else if (u.y > 0) pre = in_tiles(sa.part[1], u.x, g);
+    }
+    const int64_t row = static_cast<int64_t>(n) * a.H_q + h, plane = static_cast<int64_t>(a.N) * a.H_q;
+    auto result = [&](int c, const float2 *&ml, const float *&o, int &step) {
+        const bool first = c < own.count;
+        const Where &w = first ? own : pre;
+        const int k = first ? c : c - own.count;
+        const PartResults &p = *w.p;
+        if (w.pieces) {
+            const int64_t slot = k == 0 ? 2 * w.owner + 1 : 2 * (w.owner + k);
+            ml = reinterpret_cast<const float2 *>(p.ws.ml) + slot * p.rows + w.row;
+            o = p.ws.acc + partial_at<D>(slot, p.rows, w.row, 0);
+            step = p.rows * 8;  // from eight columns to the next eight
+        } else {
+            const int64_t at = (k == w.sink ? p.planes - 1 : k) * plane + row;
+            ml = p.ml + at;
+            o = p.o + at * D;
+            step = 8;
+        }
+    };
+    const int count = own.count + pre.count;
+    float acc[E], m = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int c0 = 0; c0 < count; c0 += 32) {
+        const int in = min(32, count - c0);
+        float2 v = make_float2(-INFINITY, 0.f);
+        const float2 *ml;
+        const float *o = nullptr;
+        int step = 8;
+        if (lane < in) {
+            result(c0 + lane, ml, o, step);
+            v = __ldcg(ml);
+        }
+        float mn = m;
+        mn = fmaxf(mn, v.x);
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+        const float ms = mn == -INFINITY ? 0.f : mn, old = ex2(m - ms);
+        const float f = ex2(v.x - ms);
+        L = L * old + f * v.y;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= old;
+        m = mn;
+#pragma unroll 4
+        for (int k = 0; k < in; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            const float *src = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), k));
+            const int st = __shfl_sync(0xffffffffu, step, k);
+            // columns lane * E .. (E <= 8 of them lie in one block of eight)
+            const float *at = src + static_cast<int64_t>(lane * E / 8) * st + lane * E % 8;
+            // (a result that kept nothing of this row has weight 0 and finite values)
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 t = __ldcg(reinterpret_cast<const float2 *>(at + e));
+                acc[e] += fk * t.x;
+                acc[e + 1] += fk * t.y;
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+    if (!SWA_IN_BOUNDS(n < a.N && h < a.H_q && b < a.B, &g_shared_err)) return;
+    const float inv = 1.f / L;  // every row keeps its own key
+    uint16_t *op = a.o + n * a.o_st[0] + h * a.o_st[1] + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(op + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0) {
+        a.lse[row] = (m + log2f(L)) * 0.69314718055994531f;
+        if (a.counts) a.counts[row] = kept_keys(a, s.p0 + i);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------------------------
 struct Layout {
-    PagedShape prefix, own;
-    size_t done, base, groups, pos, lse, o, bytes;
+    bool few, tiles;  // tiles: prefixes may go to the many-row kernel
+    int planes, prefix_planes, cap;
+    PagedShape shape;  // of the many-row kernel
+    size_t slots[2], base, group_of, groups, pos, count, list, units[2], ml[2], o[2], few_ml, few_o, bytes;
 };
 
 Layout layout(const PagedArgs &a, int n_groups) {
     Layout l{};
-    l.prefix = paged_tile_shape(a);
-    l.own = paged_few_rows(a) ? paged_split_shape(a) : paged_tile_shape(a);
-    const size_t x = paged_ws_bytes(l.prefix, a.D), y = paged_ws_bytes(l.own, a.D);
-    // (one after the other: the parts' partial results share their place)
-    l.done = x > y ? x : y;
-    l.base = l.done + paged_up(static_cast<size_t>(l.own.ctas) * 32);
-    l.groups = l.base + paged_up(static_cast<size_t>(a.B) * 4);
-    l.pos = l.groups + paged_up(static_cast<size_t>(n_groups) * sizeof(PagedGroup));
-    l.lse = l.pos + paged_up(static_cast<size_t>(a.N) * 4);
-    l.o = l.lse + paged_up(static_cast<size_t>(a.N) * a.H_q * 4);
-    l.bytes = l.o + paged_up(static_cast<size_t>(a.N) * a.H_q * a.D * 4);
+    l.few = paged_few_rows(a);
+    // (no group of a batch of so few rows has more than a stretch takes)
+    l.tiles = !l.few || static_cast<int64_t>(a.N) * a.G > kStretchRows;
+    l.shape = paged_tile_shape(a);
+    const int TT = kStretchRows / a.G;
+    const int64_t units = std::min<int64_t>(a.N, static_cast<int64_t>(a.N) / TT + a.B);
+    // Stretches of a unit: about four for every resident warp where units are few, two at least.
+    const int64_t want = (4 * static_cast<int64_t>(shared_rows_warps(a.D)) + units * a.H_kv - 1) / (units * a.H_kv);
+    l.planes = l.few ? static_cast<int>(std::min<int64_t>(std::max<int64_t>(want, 2), 128)) + 1 : 1;
+    l.prefix_planes = l.few ? l.planes : 0;
+    const int64_t cap = l.few ? units * l.planes + std::min<int64_t>(n_groups, a.N / 2 + 1) * l.planes : 0;
+    l.cap = static_cast<int>(std::min<int64_t>(cap, INT_MAX / a.H_kv));
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t x = at;
+        at += paged_up(bytes);
+        return x;
+    };
+    const size_t rows = static_cast<size_t>(a.N) * a.H_q;
+    const bool tiles[2] = {!l.few, l.tiles};
+    for (int p = 0; p < 2; ++p) {
+        const int TU = paged_tile_tokens(a, p ? Part::kPrefix : Part::kOwn);
+        const size_t n_units = (static_cast<size_t>(a.N) / TU + (p ? n_groups : a.B) + 2) * a.H_kv;
+        const size_t planes = p ? 1 : l.planes;
+        l.slots[p] = take(tiles[p] ? paged_ws_bytes(l.shape, a.D) : 0);
+        l.units[p] = take(tiles[p] ? n_units * sizeof(int2) : 0);
+        l.ml[p] = take(tiles[p] || !p ? planes * rows * 8 : 0);
+        l.o[p] = take(tiles[p] || !p ? planes * rows * a.D * 4 : 0);
+    }
+    l.few_ml = take(l.prefix_planes * rows * 8);
+    l.few_o = take(l.prefix_planes * rows * a.D * 4);
+    l.base = take(static_cast<size_t>(a.B) * 4);
+    l.group_of = take(static_cast<size_t>(a.B) * 4);
+    l.groups = take(static_cast<size_t>(n_groups) * sizeof(PagedGroup));
+    l.pos = take(static_cast<size_t>(a.N) * 4);
+    l.count = take(4);
+    l.list = take(static_cast<size_t>(l.cap) * sizeof(Stretch));
+    l.bytes = at;
     return l;
 }
 
-cudaError_t launch_plan(const PlanArgs &pa, bool after_append, cudaStream_t s) {
-    const int ranks = pa.n_groups < kFewGroups ? kCluster : 1;
+cudaError_t launch_plan(const SharedArgs &sa, bool after_append, cudaStream_t s) {
+    const int ranks = sa.n_groups < kFewGroups ? kCluster : 1;
     const int most = paged_sm_count() * 4;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ranks * (pa.n_groups < most ? pa.n_groups : most));
+    cfg.gridDim = dim3(ranks * (sa.n_groups < most ? sa.n_groups : most));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -217,58 +425,83 @@ cudaError_t launch_plan(const PlanArgs &pa, bool after_append, cudaStream_t s) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = after_append ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, paged_plan_kernel, pa);
+    return cudaLaunchKernelEx(&cfg, paged_plan_kernel, sa);
+}
+
+cudaError_t launch_join(const SharedArgs &sa, cudaStream_t s) {
+    const int64_t blocks = (static_cast<int64_t>(sa.a.N) * sa.a.H_q + kWarps - 1) / kWarps;
+    if (blocks > INT_MAX) return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned int>(blocks));
+    switch (sa.a.D) {
+        case 64: return launch_dependent(true, paged_join_kernel<64>, grid, kThreads, 0, s, sa);
+        case 128: return launch_dependent(true, paged_join_kernel<128>, grid, kThreads, 0, s, sa);
+        case 256: return launch_dependent(true, paged_join_kernel<256>, grid, kThreads, 0, s, sa);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace
 
-size_t paged_shared_workspace_bytes(const PagedArgs &a, int n_groups) { return layout(a, n_groups).bytes; }
+size_t paged_shared_workspace_bytes(const PagedArgs &a, int n_groups) {
+    return a.N > 0 ? layout(a, n_groups).bytes : 256;
+}
 
-cudaError_t launch_paged_shared(const PagedArgs &args, const int32_t *group_start, int n_groups, void *ws,
+cudaError_t launch_paged_shared(const PagedArgs &a, const int32_t *group_start, int n_groups, void *ws,
                                 cudaStream_t s) {
-    PagedArgs a = args;
-    const bool few = paged_few_rows(a);
     const Layout l = layout(a, n_groups);
     char *p = static_cast<char *>(ws);
-    PagedWs w_prefix = paged_carve(ws, l.prefix, a.D), w_own = paged_carve(ws, l.own, a.D);
-    // the counters of shared units: those of the prefix part lie at the partial results' end, those of the own
-    // part, which the prefix part's partial results must not overwrite, in a place of their own
-    if (!few) w_own.done = reinterpret_cast<int32_t *>(p + l.done);
-    a.base = reinterpret_cast<const int32_t *>(p + l.base);
-    a.groups = reinterpret_cast<const PagedGroup *>(p + l.groups);
-    a.pos = reinterpret_cast<const int32_t *>(p + l.pos);
-    a.pre_lse = reinterpret_cast<float *>(p + l.lse);
-    a.pre_o = reinterpret_cast<float *>(p + l.o);
-    cudaError_t e = cudaSuccess;
-    const bool append = a.kn && a.q_start;  // (one token a sequence: stored by the attention kernel)
-    if (append) {
-        e = launch_paged_append(a, w_prefix.done, l.prefix.ctas * 8, s);
-        if (e != cudaSuccess) return e;
-        a.kn = a.vn = nullptr;
-    } else {
-        e = cudaMemsetAsync(w_prefix.done, 0, l.prefix.ctas * 32, s);
-        if (e != cudaSuccess) return e;
+    SharedArgs sa{};
+    sa.a = a;
+    sa.a.kn = sa.a.vn = nullptr;
+    sa.group_start = group_start;
+    sa.n_groups = n_groups;
+    sa.groups = reinterpret_cast<PagedGroup *>(p + l.groups);
+    sa.base = reinterpret_cast<int32_t *>(p + l.base);
+    sa.group_of = reinterpret_cast<int32_t *>(p + l.group_of);
+    sa.pos = reinterpret_cast<int32_t *>(p + l.pos);
+    sa.stretches = reinterpret_cast<Stretch *>(p + l.list);
+    sa.n_stretches = reinterpret_cast<int32_t *>(p + l.count);
+    sa.cap = l.cap;
+    sa.few = l.few;
+    sa.any_tiles = l.tiles;
+    sa.prefix_tokens = sa.own_tokens = l.shape.TQ;
+    for (int x = 0; x < 2; ++x) {
+        PartResults &r = sa.part[x];
+        r.ml = reinterpret_cast<float2 *>(p + l.ml[x]);
+        r.o = reinterpret_cast<float *>(p + l.o[x]);
+        r.planes = x ? 1 : l.planes;
+        r.units = reinterpret_cast<const int2 *>(p + l.units[x]);
+        r.ws = paged_carve(p + l.slots[x], l.shape, a.D);
+        r.ctas = l.shape.ctas;
+        r.rows = l.shape.tiles * l.shape.rows;
+        r.TQ = l.shape.TQ;
+        r.TT = paged_tile_tokens(a, x ? Part::kPrefix : Part::kOwn);
     }
-    PlanArgs pa{};
-    pa.a = a;
-    pa.group_start = group_start;
-    pa.n_groups = n_groups;
-    pa.groups = reinterpret_cast<PagedGroup *>(p + l.groups);
-    pa.base = reinterpret_cast<int32_t *>(p + l.base);
-    pa.pos = reinterpret_cast<int32_t *>(p + l.pos);
-    pa.zero = reinterpret_cast<int32_t *>(p + l.done);
-    pa.n_zero = few ? 0 : l.own.ctas * 8;
-    pa.TQ = l.prefix.TQ;
-    pa.own_tokens = few ? 0 : l.own.TQ;
-    e = launch_plan(pa, append, s);
+    sa.few_prefix.ml = reinterpret_cast<float2 *>(p + l.few_ml);
+    sa.few_prefix.o = reinterpret_cast<float *>(p + l.few_o);
+    sa.few_prefix.planes = l.prefix_planes;
+    auto part_args = [&](int x) {
+        PagedArgs t = sa.a;
+        t.groups = sa.groups;
+        t.pos = sa.pos;
+        t.base = sa.base;
+        t.part_ml = sa.part[x].ml;
+        t.part_o = sa.part[x].o;
+        t.part_units = reinterpret_cast<int2 *>(p + l.units[x]);
+        if (x) t.B = n_groups;
+        return t;
+    };
+    const bool append = a.kn != nullptr;
+    // (not by the append kernel, which the plan does not wait for before it counts)
+    cudaError_t e = l.few ? cudaMemsetAsync(sa.n_stretches, 0, 4, s) : cudaSuccess;
+    if (e == cudaSuccess && append) e = launch_paged_append(a, nullptr, 0, s);
     if (e != cudaSuccess) return e;
-    PagedArgs g = a;
-    g.B = n_groups;
-    e = launch_paged_tile(g, w_prefix, true, s, Part::kPrefix);
+    e = launch_plan(sa, append, s);
     if (e != cudaSuccess) return e;
-    if (!few) return launch_paged_tile(a, w_own, true, s, Part::kOwn);
-    e = launch_paged_split(a, w_own, true, s, Part::kOwn);
-    return e != cudaSuccess ? e : launch_paged_merge(a, w_own, l.own, s, Part::kOwn);
+    if (l.tiles) e = launch_paged_tile(part_args(1), sa.part[1].ws, true, s, Part::kPrefix);
+    if (e != cudaSuccess) return e;
+    e = l.few ? launch_shared_rows(sa, l.tiles, s) : launch_paged_tile(part_args(0), sa.part[0].ws, true, s, Part::kOwn);
+    return e != cudaSuccess ? e : launch_join(sa, s);
 }
 
 unsigned int paged_shared_read_clear_error() {

@@ -1,0 +1,85 @@
+// swa_paged_shared.cuh -- what the kernels of swa_paged_attend_shared agree on: the stretches of keys that
+// the kernel for few rows takes one at a time, and where their results lie.
+#pragma once
+
+#include "swa_paged.cuh"
+
+namespace swa {
+
+constexpr int kStretchRows = 16;  // rows of a unit of the kernel for few rows (mma.sync M)
+constexpr int kStretchKeys = 256;  // least keys of a stretch
+
+// One stretch: tokens q0 .. q0 + n - 1 (n * G <= 16 rows) over the keys k0 .. k1 - 1 in the pages of row
+// `row` of the table; its result goes to plane `plane` of part `part` (0: own, 1: prefix).
+struct Stretch {
+    int32_t row, q0, n, plane, k0, k1, part, unused;
+};
+
+// A unit's keys: [lo, end) in `count` stretches, stretch i the part within [first + i * keys, first + (i + 1) *
+// keys), and, if sink1 > sink0, one more, [sink0, sink1), in the last plane.
+struct Keys {
+    int lo, end, sink0, sink1, first, keys, count;
+    __device__ __forceinline__ int stretches() const { return count + (sink1 > sink0 ? 1 : 0); }
+    __device__ __forceinline__ int begin(int i) const { return i < count ? max(lo, first + i * keys) : sink0; }
+    __device__ __forceinline__ int close(int i) const { return i < count ? min(end, first + (i + 1) * keys) : sink1; }
+};
+
+// planes: of a part; at most planes - 1 stretches and the sinks'.
+__device__ __forceinline__ Keys split_keys(int lo, int end, int sink0, int sink1, int planes) {
+    Keys k;
+    k.lo = lo;
+    k.end = end;
+    k.sink0 = sink0;
+    k.sink1 = sink1;
+    k.first = lo & ~15;
+    const int n = end - k.first, most = planes - 1;
+    k.keys = max(kStretchKeys, ((n + most - 1) / most + 15) & ~15);
+    k.count = (n + k.keys - 1) / k.keys;
+    return k;
+}
+
+// Keys at or past base of the unit of tokens ut * TT .. of sequence s.
+__device__ __forceinline__ Keys own_keys(const PagedArgs &a, const Seq &s, int base, int ut, int TT, int planes) {
+    const int t0 = s.p0 + ut * TT, t1 = s.p0 + min(s.n, (ut + 1) * TT) - 1;
+    const int lo = max(base, t0 >= a.window ? t0 - a.window + 1 : 0);
+    return split_keys(lo, t1 + 1, base, min(a.n_sink, lo), planes);
+}
+
+// Keys of a prefix.
+__device__ __forceinline__ Keys prefix_keys(const PagedArgs &a, int p0, int end, int planes) {
+    const int lo = p0 >= a.window ? p0 - a.window + 1 : 0;
+    return split_keys(lo, end, 0, min(a.n_sink, lo), planes);
+}
+
+// The results of both parts.  Rows of a part are [N, H_q] in each of `planes` planes (one, of the many-row kernel).
+struct PartResults {
+    float2 *ml;
+    float *o;
+    int planes;
+    // the many-row kernel's units that several CTAs have (units == nullptr: the part is the few-row kernel's)
+    const int2 *units;
+    PagedWs ws;
+    int ctas, rows, TQ, TT;
+};
+
+struct SharedArgs {
+    PagedArgs a;
+    const int32_t *group_start;  // [n_groups + 1]
+    int n_groups;
+    PagedGroup *groups;
+    int32_t *base, *group_of;  // [B]; group_of: -1: none
+    int32_t *pos;              // [N]
+    Stretch *stretches;        // [cap]
+    int32_t *n_stretches;      // zero at the plan's start
+    int cap;
+    int few;                   // own parts (and prefixes of few rows) are cut into stretches
+    int any_tiles;             // prefixes may go to the many-row kernel
+    int prefix_tokens, own_tokens;  // tokens of a query tile of the many-row kernel
+    PartResults part[2];       // own, prefix in tiles
+    PartResults few_prefix;
+};
+
+cudaError_t launch_shared_rows(const SharedArgs &sa, bool behind_tiles, cudaStream_t s);
+int shared_rows_warps(int D);  // warps that are resident at a time
+
+}  // namespace swa

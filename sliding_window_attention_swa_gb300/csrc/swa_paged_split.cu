@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t sw128(int row, int pc) {
                                  (((pc & 7) ^ (row & 7)) << 4));
 }
 
-template <int D, Part PT>
+template <int D>
 __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::CTAS_PER_SM == 2 ? 168 : 255)
     paged_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const PagedArgs a, const PagedWs ws, const int TT, const int min_tiles, const int scratch_off,
@@ -103,16 +103,14 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    // (a part's sequences are known, and the prefix part is written, by the kernels before this one)
-    if constexpr (PT != Part::kAll) asm volatile("griddepcontrol.wait;" ::: "memory");
     // (its block barriers also publish the mbarriers)
-    find_share<CH, kThreads, false, PT>(a, TT, min_tiles, sgen + scratch_off, &share, &g_psplit_data);
+    find_share<CH, kThreads, false>(a, TT, min_tiles, sgen + scratch_off, &share, &g_psplit_data);
     volatile int *abort = &abort_flag;
     // the merge grid may be scheduled from here on: its blocks wait (griddepcontrol.wait)
     // for this grid to complete before they read the partials
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Share sh = share;
-    Walk<CH, PT> walk(a, TT, sh);
+    Walk<CH> walk(a, TT, sh);
     Piece p;
 
     if (warp == 0) {
@@ -129,8 +127,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
             if (p.open() && !p.begun()) open = make_int4(p.u.n - p.j1, p.b, p.kvh, p.ut);
             const int t0 = p.s.p0 + p.ut * TT, t1 = p.s.p0 + min(p.s.n, (p.ut + 1) * TT) - 1;
             const int lo = t0 >= a.window ? t0 - a.window + 1 : 0;
-            const int n_sink = sinks_of<PT>(a, p.s.base), entry0 = PT == Part::kOwn ? p.s.base >> a.ps_log2 : 0;
-            auto entry = [&](int j) { return page_of(a, p.b, entry0 + ((p.u.tile(j) * CH + my_pg * box) >> a.ps_log2)); };
+            auto entry = [&](int j) { return page_of(a, p.b, (p.u.tile(j) * CH + my_pg * box) >> a.ps_log2); };
             int page = entry(p.j0);
 #pragma unroll 1
             for (int j = p.j0; j < p.j1; ++j) {
@@ -141,7 +138,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
                 }
                 const int k0 = p.u.tile(j) * CH, kp = k0 + my_pg * box;
                 // a page that some row keeps a key of has to be there
-                if (page == a.n_pages && kp <= t1 && (kp + box > lo || kp < n_sink))
+                if (page == a.n_pages && kp <= t1 && (kp + box > lo || kp < a.n_sink))
                     atomicOr(&g_psplit_data, SWA_DEVERR_BAD_PAGE);
                 const int st = seq % NST;
                 if (seq >= NST) {
@@ -199,7 +196,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
         while (ok && walk.next(p)) {
             const int n_tok = min(p.s.n - p.ut * TT, TT), rows = n_tok * a.G;
             const int tb = p.s.p0 + p.ut * TT, t1 = tb + n_tok - 1;  // first and last token's positions
-            const int end = p.s.p0 + p.s.n, n_sink = sinks_of<PT>(a, p.s.base);
+            const int end = p.s.p0 + p.s.n;
             const int tr0 = tb + r0 / a.G, tr1 = tb + r1 / a.G;
             const int lo0 = tr0 >= a.window ? tr0 - a.window + 1 : 0, lo1 = tr1 >= a.window ? tr1 - a.window + 1 : 0;
             const int lo_last = t1 >= a.window ? t1 - a.window + 1 : 0;  // keys from here on are in every row's window
@@ -234,16 +231,16 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
                     break;
                 }
                 const int k0 = p.u.tile(j) * CH + 16 * w;  // this warp's first key
-                if (k0 <= t1 && (k0 + 15 >= lo_first || k0 < n_sink)) {
+                if (k0 <= t1 && (k0 + 15 >= lo_first || k0 < a.n_sink)) {
                     const uint32_t ks = sbase + C::OFF_RING + st * C::STAGE;
                     const uint32_t vs = ks + C::STAGE / 2;
-                    if (k0 + 15 >= end || (k0 < lo_first && k0 + 15 >= n_sink)) {
+                    if (k0 + 15 >= end || (k0 < lo_first && k0 + 15 >= a.n_sink)) {
                         // zero the value rows that no row keeps: past the sequence's end, or between the
                         // sinks and the window (they may hold anything, even NaN)
                         uint8_t *vg = sgen + C::OFF_RING + st * C::STAGE + C::STAGE / 2;
                         for (int idx = lane; idx < 16 * (D / 8); idx += 32) {
                             const int rr = idx / (D / 8), pc = idx % (D / 8);
-                            if (k0 + rr >= end || (k0 + rr < lo_first && k0 + rr >= n_sink))
+                            if (k0 + rr >= end || (k0 + rr < lo_first && k0 + rr >= a.n_sink))
                                 *reinterpret_cast<uint4 *>(vg + sw128<D>(16 * w + rr, pc)) = make_uint4(0, 0, 0, 0);
                         }
                         __syncwarp();
@@ -264,14 +261,14 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
                     }
                     float mx0 = -INFINITY, mx1 = -INFINITY;
                     // every row keeps every key of this warp
-                    const bool whole = k0 + 15 <= tb && (k0 >= lo_last || k0 + 15 < n_sink);
+                    const bool whole = k0 + 15 <= tb && (k0 >= lo_last || k0 + 15 < a.n_sink);
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int s = k0 + 8 * nt + kq + (e & 1);
                             const int t = e < 2 ? tr0 : tr1, lo = e < 2 ? lo0 : lo1;
-                            const bool keep = whole || (s <= t && (s >= lo || s < n_sink));
+                            const bool keep = whole || (s <= t && (s >= lo || s < a.n_sink));
                             sc[nt][e] = keep ? sc[nt][e] * a.scale_log2 : -INFINITY;
                         }
                         mx0 = fmaxf(mx0, fmaxf(sc[nt][0], sc[nt][1]));
@@ -382,17 +379,6 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
                     L += red_l[ww * ROWS + r] * f[ww];
                 }
                 const bool whole = !p.begun() && !p.open();
-                // joined with the row's prefix part
-                float wp = 0.f;
-                const float *pre = PT == Part::kOwn ? a.pre_o + (tok * a.H_q + h) * D : nullptr;
-                if (PT == Part::kOwn && whole && p.s.base > 0) {
-                    const float pl = __ldcg(a.pre_lse + tok * a.H_q + h), mn = fmaxf(mw, pl), wo = ex2(mw - mn);
-                    wp = ex2(pl - mn);
-#pragma unroll
-                    for (int ww = 0; ww < 4; ++ww) f[ww] *= wo;
-                    L = L * wo + wp;
-                    mw = mn;
-                }
                 const float inv = 1.f / L;  // (of a whole unit: every row keeps its own key)
                 const int64_t slot = static_cast<int64_t>(piece_slot(p)) * ROWS + r;
                 uint16_t *o = a.o + tok * a.o_st[0] + h * a.o_st[1];
@@ -408,13 +394,6 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
                         acc4.z += c4.z * f[ww];
                         acc4.w += c4.w * f[ww];
                     }
-                    if (PT == Part::kOwn && wp > 0.f) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(pre + col));
-                        acc4.x += wp * v.x;
-                        acc4.y += wp * v.y;
-                        acc4.z += wp * v.z;
-                        acc4.w += wp * v.w;
-                    }
                     if (whole)
                         *reinterpret_cast<uint2 *>(o + col) = make_uint2(pack_bf16x2(acc4.x * inv, acc4.y * inv),
                                                                          pack_bf16x2(acc4.z * inv, acc4.w * inv));
@@ -424,9 +403,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
                 if (part == 0) {
                     if (whole) {
                         a.lse[tok * a.H_q + h] = (mw + log2f(L)) * 0.69314718055994531f;
-                        if (a.counts)
-                            a.counts[tok * a.H_q + h] =
-                                kept_keys(a, static_cast<int>(tb + r / a.G) + (PT == Part::kOwn ? p.s.base : 0));
+                        if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, static_cast<int>(tb + r / a.G));
                     } else {
                         *reinterpret_cast<float2 *>(ws.ml + slot * 2) = make_float2(mw, L);
                     }
@@ -448,7 +425,7 @@ __global__ void __maxnreg__(SplitCfg<D>::CTAS_PER_SM == 3 ? 128 : SplitCfg<D>::C
 // ---------------------------------------------------------------------------------------------
 constexpr int kMergeThreads = 256, kMergeRows = kMergeThreads / 32;
 
-template <int D, Part PT>
+template <int D>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedArgs a, const PagedWs w, const int ctas,
                                                                     const int TT) {
     constexpr int E = D / 32;  // columns of a lane
@@ -469,7 +446,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
         np += n;
         if (n < 32) break;
     }
-    const Seq s = load_seq<PT>(a, rec.y);
+    const Seq s = load_seq(a, rec.y);
     const int i = rec.w * TT + row / a.G;  // token of the sequence
     if (i >= s.n || !SWA_IN_BOUNDS(c + np <= ctas && rec.y < a.B && rec.z < a.H_kv, &g_psplit_err)) return;
     auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)); };
@@ -478,25 +455,9 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
     for (int k = lane; k < np; k += 32) m = fmaxf(m, piece(k).x);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const int64_t tok = s.q0 + i;
-    const int h = rec.z * a.G + row % a.G;
-    if (!SWA_IN_BOUNDS(tok < a.N && h < a.H_q, &g_psplit_err)) return;
     float acc[E], L = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    if (PT == Part::kOwn && s.base > 0) {  // the row's prefix part, a piece of weight 2^(its lse - m)
-        const float pl = __ldcg(a.pre_lse + tok * a.H_q + h);
-        m = fmaxf(m, pl);
-        const float wp = ex2(pl - m);
-        L = lane == 0 ? wp : 0.f;
-        const float *v = a.pre_o + (tok * a.H_q + h) * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            const float2 t = __ldcg(reinterpret_cast<const float2 *>(v + e));
-            acc[e] = wp * t.x;
-            acc[e + 1] = wp * t.y;
-        }
-    }
     for (int k0 = 0; k0 < np; k0 += 32) {
         float2 ml = make_float2(-INFINITY, 0.f);
         if (k0 + lane < np) ml = piece(k0 + lane);
@@ -518,17 +479,20 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const int64_t tok = s.q0 + i;
+    const int h = rec.z * a.G + row % a.G;
+    if (!SWA_IN_BOUNDS(tok < a.N && h < a.H_q, &g_psplit_err)) return;
     const float inv = 1.f / L;  // every row keeps its own key
     uint16_t *op = a.o + tok * a.o_st[0] + h * a.o_st[1] + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(op + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
     if (lane == 0) {
         a.lse[tok * a.H_q + h] = (m + log2f(L)) * 0.69314718055994531f;
-        if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, s.p0 + i + (PT == Part::kOwn ? s.base : 0));
+        if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, s.p0 + i);
     }
 }
 
-template <int D, Part PT>
+template <int D>
 cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s) {
     using C = SplitCfg<D>;
     // the dynamic shared-memory limit is a per-device function attribute: set once per device
@@ -536,7 +500,7 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cu
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) dev = -1;
     if (dev < 0 || !configured[dev].load(std::memory_order_acquire)) {
-        cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<D, PT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(paged_split_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::smem(kPagedMaxB));
         if (e != cudaSuccess) return e;
         if (dev >= 0) configured[dev].store(true, std::memory_order_release);
@@ -546,7 +510,7 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cu
     if (!paged_pool_map(&mk, a, a.k_pages, rows) || !paged_pool_map(&mv, a, a.v_pages, rows))
         return cudaErrorInvalidValue;
     const PagedShape x = paged_split_shape(a);
-    return launch_dependent(after_append, paged_split_kernel<D, PT>, dim3(x.ctas), kThreads, C::smem(a.B), s, mk, mv, a, w,
+    return launch_dependent(after_append, paged_split_kernel<D>, dim3(x.ctas), kThreads, C::smem(a.B), s, mk, mv, a, w,
                             x.TQ, kMinTiles, C::scratch_off(a.B), fault_plan().split_stop_stage);
 }
 
@@ -559,30 +523,21 @@ PagedShape paged_split_shape(const PagedArgs &a) {
     return PagedShape{paged_sm_count() * per_sm, 1, ROWS, ROWS / a.G};
 }
 
-cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s, Part part) {
-    const bool own = part == Part::kOwn;
+cudaError_t launch_paged_split(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s) {
     switch (a.D) {
-        case 64: return own ? launch_d<64, Part::kOwn>(a, w, true, s) : launch_d<64, Part::kAll>(a, w, after_append, s);
-        case 128: return own ? launch_d<128, Part::kOwn>(a, w, true, s) : launch_d<128, Part::kAll>(a, w, after_append, s);
-        case 256: return own ? launch_d<256, Part::kOwn>(a, w, true, s) : launch_d<256, Part::kAll>(a, w, after_append, s);
+        case 64: return launch_d<64>(a, w, after_append, s);
+        case 128: return launch_d<128>(a, w, after_append, s);
+        case 256: return launch_d<256>(a, w, after_append, s);
         default: return cudaErrorInvalidValue;
     }
 }
 
-namespace {
-template <int D>
-cudaError_t launch_merge_d(const PagedArgs &a, const PagedWs &w, const PagedShape &x, cudaStream_t s, Part part) {
+cudaError_t launch_paged_merge(const PagedArgs &a, const PagedWs &w, const PagedShape &x, cudaStream_t s) {
     const dim3 grid(x.ctas, (x.TQ * a.G + kMergeRows - 1) / kMergeRows);
-    return launch_dependent(true, part == Part::kOwn ? paged_merge_kernel<D, Part::kOwn> : paged_merge_kernel<D, Part::kAll>,
-                            grid, kMergeThreads, 0, s, a, w, x.ctas, x.TQ);
-}
-}  // namespace
-
-cudaError_t launch_paged_merge(const PagedArgs &a, const PagedWs &w, const PagedShape &x, cudaStream_t s, Part part) {
     switch (a.D) {
-        case 64: return launch_merge_d<64>(a, w, x, s, part);
-        case 128: return launch_merge_d<128>(a, w, x, s, part);
-        case 256: return launch_merge_d<256>(a, w, x, s, part);
+        case 64: return launch_dependent(true, paged_merge_kernel<64>, grid, kMergeThreads, 0, s, a, w, x.ctas, x.TQ);
+        case 128: return launch_dependent(true, paged_merge_kernel<128>, grid, kMergeThreads, 0, s, a, w, x.ctas, x.TQ);
+        case 256: return launch_dependent(true, paged_merge_kernel<256>, grid, kMergeThreads, 0, s, a, w, x.ctas, x.TQ);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -158,19 +158,6 @@ __device__ __forceinline__ void store_row16(uint16_t *dst, const float *f, bool 
     }
 }
 
-// f += w * the values of a row of the prefix part
-template <int N>
-__device__ __forceinline__ void add_prefix(float (&f)[N], const float *pre, float w) {
-#pragma unroll
-    for (int x = 0; x < N / 4; ++x) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(pre) + x);
-        f[4 * x] += w * v.x;
-        f[4 * x + 1] += w * v.y;
-        f[4 * x + 2] += w * v.z;
-        f[4 * x + 3] += w * v.w;
-    }
-}
-
 template <int D, Part PT>
 __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -248,9 +235,11 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     const int TT = ta.TT;
     tc_fence_before();
     if constexpr (PT != Part::kAll) {
-        // the kernels before this one have found the groups; of kOwn's, have written the prefix part
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        if constexpr (PT == Part::kPrefix) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        // The prefix part waits for the plan (and the append before it), and only then lets the own part start, which
+        // thus finds what they wrote.  The own part needs nothing of the prefix part: it waits for that at its end, so
+        // that what waits for it waits for both.
+        if constexpr (PT == Part::kPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
     // (its block barriers also publish the mbarriers and the TMEM address)
     find_share<BN, C::THREADS, true, PT>(a, TT, ta.min_tiles, sgen + C::OFF_RING, share, &g_ptile_data);
@@ -282,7 +271,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         regs_dec<C::REG_CTRL>();
         // the scratch of the work split lies in the ring: order its generic accesses before the copies
         fence_proxy_async_smem();
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // (the append before this kernel has stored its rows)
+        if constexpr (PT != Part::kOwn)
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // (the append before this kernel has stored its rows)
         // A tile is npg boxes (pages or a part of one).  The pages are looked up 32 boxes at a time,
         // lane i that of box i, a group ahead of their use.
         const int box = min(a.ps, BN), npg = BN / box, per_group = 32 / npg;
@@ -880,12 +870,10 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             }
             const int unit_pieces = wk->pieces;
             const bool whole = unit_pieces == 0;
-            // (every row keeps its own key, but may have none of a prefix)
-            const float inv_l = !whole ? 1.f : PT == Part::kPrefix && l == 0.f ? 0.f : 1.f / l;
-            if constexpr (PT != Part::kOwn) {
-                wa *= inv_l;
-                wb *= inv_l;
-            }
+            // (of a whole unit every row keeps its own key; a part's rows are joined with their others later)
+            const float inv_l = PT == Part::kAll && whole ? 1.f / l : 1.f;
+            wa *= inv_l;
+            wb *= inv_l;
             const int tq = r / a.G, i0 = wk->ut * TT + (single ? 0 : ow * ta.TQ);  // the tile's first token
             const int64_t tok = static_cast<int64_t>(wk->q0) + i0 + tq;
             const int h = wk->kvh * a.G + r % a.G;
@@ -897,27 +885,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                                              wk->owner + unit_pieces <= static_cast<int>(gridDim.x))),
                               &g_ptile_err);
             uint16_t *orow = a.o + tok * a.o_st[0] + h * a.o_st[1];
-            // this row of the prefix part, and (kOwn) its weight
-            float *pre = PT == Part::kAll ? nullptr : a.pre_o + (tok * a.H_q + h) * D;
-            float wp = 0.f;
-            // joins the row's own part (m, l) with the prefix's: returns the weight of the own part
-            auto with_prefix = [&]() -> float {
-                const float pl = store && wk->base > 0 ? __ldcg(a.pre_lse + tok * a.H_q + h) : -INFINITY;
-                const float mn = fmaxf(m, pl), wo = ex2(m - mn);
-                wp = ex2(pl - mn);
-                l = l * wo + wp;
-                m = mn;
-                const float inv = 1.f / l;
-                wp *= inv;
-                return wo * inv;
-            };
-            if constexpr (PT == Part::kOwn) {
-                if (whole) {
-                    const float wo = with_prefix();
-                    wa *= wo;
-                    wb *= wo;
-                }
-            }
             const int pslot = wk->slot, prow = (single ? 0 : ow * BM) + r;
             // (a shared query tile: each warpgroup keeps the maximum and sum beside its half of the columns)
             const int mrow = ow * BM + r;
@@ -941,24 +908,18 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) f[e] += __uint_as_float(ov[e]) * wb;
                 }
-                if (store && !whole) {
+                if (store && (PT != Part::kAll || !whole)) {
 #pragma unroll
                     for (int q8 = 0; q8 < 4; ++q8) {
                         uint32_t wv[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) wv[e] = __float_as_uint(f[q8 * 8 + e]);
-                        st_global_v8(ta.ws.acc + partial_at<D>(pslot, NQT * BM, prow, c * 32 + q8 * 8), wv);
-                    }
-                } else if (store && PT == Part::kPrefix) {
-#pragma unroll
-                    for (int q8 = 0; q8 < 4; ++q8) {
-                        uint32_t wv[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) wv[e] = __float_as_uint(f[q8 * 8 + e]);
-                        st_global_v8(pre + c * 32 + q8 * 8, wv);
+                        float *dst = PT != Part::kAll && whole
+                                         ? a.part_o + (tok * a.H_q + h) * D + c * 32 + q8 * 8
+                                         : ta.ws.acc + partial_at<D>(pslot, NQT * BM, prow, c * 32 + q8 * 8);
+                        st_global_v8(dst, wv);
                     }
                 } else if (store) {
-                    if (PT == Part::kOwn && wp > 0.f) add_prefix<32>(f, pre + c * 32, wp);
                     store_row16(orow + c * 32, f, ta.o_align32);
                     store_row16(orow + c * 32 + 16, f + 16, ta.o_align32);
                 }
@@ -968,7 +929,13 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_of(ow));
             bool joined = false;
-            if (!whole) {
+            if constexpr (PT != Part::kAll) {
+                if (store) *(whole ? a.part_ml + tok * a.H_q + h : ml_at(pslot)) = make_float2(m, l);
+                // (every warp of every piece writes the same)
+                if (lane == 0)
+                    a.part_units[(static_cast<int64_t>(wk->q0 / TT) + wk->b + wk->ut) * a.H_kv + wk->kvh] =
+                        make_int2(wk->owner, unit_pieces);
+            } else if (!whole) {
                 // The piece is written.  Warps of the same place have the same rows and columns of it in
                 // every CTA that shares the unit, so the last of them to arrive joins those: a row's
                 // weight of a piece is 2^(m_piece - m), o = sum of weighted values / sum of weighted sums.
@@ -1002,10 +969,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                         for (int e = 0; e < 4; ++e) l += v4[e].y * ex2(v4[e].x - ms);
                         m = mn;
                     }
-                    // (a row keeps its own key: some piece's maximum is finite; of a prefix it may have none)
-                    float inv = PT == Part::kPrefix && l == 0.f ? 0.f : 1.f / l;
-                    const float m_own = PT == Part::kPrefix && m == -INFINITY ? 0.f : m;
-                    if constexpr (PT == Part::kOwn) inv = with_prefix();
+                    const float inv = 1.f / l;  // (a row keeps its own key: some piece's maximum is finite)
                     if (unit_pieces > 4) four(0, v4);
                     if (store) {
 #pragma unroll 1
@@ -1028,7 +992,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
-                                    const float wt = ex2(v4[e].x - m_own) * inv;  // (0 past the last piece)
+                                    const float wt = ex2(v4[e].x - m) * inv;  // (0 past the last piece)
 #pragma unroll
                                     for (int x = 0; x < 4; ++x) {
                                         f[4 * x] += wt * v[e][x].x;
@@ -1038,26 +1002,14 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                                     }
                                 }
                             }
-                            if constexpr (PT == Part::kPrefix) {
-#pragma unroll
-                                for (int x = 0; x < 4; ++x)
-                                    reinterpret_cast<float4 *>(pre + c * 16)[x] =
-                                        make_float4(f[4 * x], f[4 * x + 1], f[4 * x + 2], f[4 * x + 3]);
-                            } else {
-                                if (PT == Part::kOwn && wp > 0.f) add_prefix<16>(f, pre + c * 16, wp);
-                                store_row16(orow + c * 16, f, ta.o_align32);
-                            }
+                            store_row16(orow + c * 16, f, ta.o_align32);
                         }
                     }
                 }
             }
-            if (store && (!single || ow == 0) && (whole || joined)) {
-                if constexpr (PT == Part::kPrefix) {
-                    a.pre_lse[tok * a.H_q + h] = l == 0.f ? -INFINITY : m + log2f(l);
-                } else {
-                    a.lse[tok * a.H_q + h] = (m + log2f(l)) * 0.69314718055994531f;
-                    if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, PT == Part::kOwn ? t + wk->base : t);
-                }
+            if (PT == Part::kAll && store && (!single || ow == 0) && (whole || joined)) {
+                a.lse[tok * a.H_q + h] = (m + log2f(l)) * 0.69314718055994531f;
+                if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, t);
             }
             give_back(k);
             J += n;
@@ -1155,6 +1107,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+    if constexpr (PT == Part::kOwn) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Query tiles of a unit.  At head dim 128 pairs take 6% less time where there are enough of them
@@ -1190,8 +1143,8 @@ cudaError_t launch_part(const PagedArgs &a, const PagedWs &w, bool dependent, cu
     t.a = a;
     t.ws = w;
     t.TQ = x.TQ;
-    t.TT = x.TQ * tiles_of_unit(a);
-    t.min_tiles = 4;
+    t.TT = paged_tile_tokens(a, PT);
+    t.min_tiles = PT == Part::kPrefix ? 2 : 4;
     t.o_align32 = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.o_st[0] % 16 == 0 && a.o_st[1] % 16 == 0;
     t.fault_stop_fill = fault_plan().band_stop_fill;
     return launch_dependent(dependent, paged_tile_kernel<D, PT>, dim3(x.ctas), C::THREADS, C::SMEM, s, mq, mk, mv, t);
@@ -1210,6 +1163,14 @@ cudaError_t launch_d(const PagedArgs &a, const PagedWs &w, bool after_append, cu
 
 PagedShape paged_tile_shape(const PagedArgs &a) {
     return PagedShape{paged_sm_count(), a.D <= 128 ? 2 : 1, BM, BM / a.G};
+}
+
+int paged_tile_tokens(const PagedArgs &a, Part part) {
+    const int TQ = BM / a.G;
+    // A prefix is read once for two tiles of its group's rows, from HBM as a rule, where there are more rows than
+    // one tile has (64 sequences behind 32768: 259 MB read by single tiles, 134 by pairs).
+    if (part == Part::kPrefix) return a.D == 128 && a.N > TQ ? 2 * TQ : TQ;
+    return TQ * tiles_of_unit(a);
 }
 
 cudaError_t launch_paged_tile(const PagedArgs &a, const PagedWs &w, bool after_append, cudaStream_t s, Part part) {
