@@ -27,30 +27,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedArgs 
     const int lane = threadIdx.x & 31;
     const int step = gridDim.x * (kThreads / 32);
     for (int n = (blockIdx.x * kThreads + threadIdx.x) >> 5; n < a.N; n += step) {
-        const int b = find_sequence(a, n, lane);
-        if (b < 0) continue;
-        const Seq s = load_seq(a, b);
-        if (!s.ok) {
-            if (lane == 0) atomicOr(&g_paged_err, SWA_DEVERR_BAD_POSITION);
-            continue;
-        }
-        const int p = s.p0 + (n - s.q0);
-        const int page = page_of(a, b, p >> a.ps_log2);
-        if (page >= a.n_pages) {
-            if (lane == 0) atomicOr(&g_paged_err, SWA_DEVERR_BAD_PAGE);
-            continue;
-        }
-        if (!SWA_IN_BOUNDS(b < a.B && page >= 0 && p >= 0 && p >> a.ps_log2 < a.width, &g_paged_err)) continue;
-        const int64_t row = static_cast<int64_t>(page) * a.H_kv * a.ps + (p & (a.ps - 1));
-        const int P = a.D / 8;  // 16-byte pieces of one head's row
-        for (int x = lane; x < 2 * a.H_kv * P; x += 32) {
-            const int pc = x % P, h = (x / P) % a.H_kv;
-            const bool is_v = x >= a.H_kv * P;
-            const uint16_t *src = is_v ? a.vn + static_cast<int64_t>(n) * a.vn_st[0] + h * a.vn_st[1]
-                                       : a.kn + static_cast<int64_t>(n) * a.kn_st[0] + h * a.kn_st[1];
-            uint16_t *dst = (is_v ? a.v_pages : a.k_pages) + (row + static_cast<int64_t>(h) * a.ps) * a.D;
-            reinterpret_cast<uint4 *>(dst)[pc] = reinterpret_cast<const uint4 *>(src)[pc];
-        }
+        store_token(a, n, lane, &g_paged_err);
     }
 }
 

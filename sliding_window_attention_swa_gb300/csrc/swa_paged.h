@@ -45,6 +45,7 @@ struct PagedArgs {
     const PagedGroup *groups;
     const int32_t *pos;   // [N]
     const int32_t *base;  // [B]: the positions below it are in the prefix part
+    const int32_t *tile_groups;  // kPrefix: the groups with rows, 0: there are none
     // A part's results, fp32.  A unit that one CTA has whole: here; one that several have: in their slots of
     // PagedWs.  units, at (q0 / TT + b + ut) * H_kv + kvh: the CTA that begins the unit, and its
     // pieces (0: whole).

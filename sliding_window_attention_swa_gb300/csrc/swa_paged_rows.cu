@@ -1,7 +1,7 @@
 // swa_paged_rows.cu -- stretches of at most 16 query rows over a few hundred keys of a paged cache: the
 // sequences' own parts of swa_paged_attend_shared with few new tokens, and prefixes of few rows.
 //
-// A warp takes a stretch by itself: it copies 16 keys and values at a time by TMA into a ring of its own,
+// A warp takes a stretch by itself: it copies 16 or 32 keys and values at a time by TMA into a ring of its own,
 // scores them (mma.sync, the rows are M), keeps the running maximum and sum, and writes the unnormalised result.  No two
 // warps wait for one another, so that the latencies of a stretch -- its rows, its pages, its first copies, its end -- are
 // hidden by the other warps' work and by its own copies: the next stretch's first steps are on their way
@@ -10,6 +10,7 @@
 // 135 sequences of 250 tokens on average behind what they share, 72 us of it for 141 MB.
 // Bound by HBM.  P is rounded to bf16 for the second product; the sum takes it unrounded.
 // Every wait is bounded; on expiry the warp records an error word, drains its copies and returns.
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -22,14 +23,14 @@ namespace {
 __device__ unsigned int g_rows_err = 0;   // waits and bounds
 __device__ unsigned int g_rows_data = 0;  // broken device data
 
-constexpr int kStep = 16;  // keys a step
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 
 template <int D>
 struct RowsCfg {
-    static constexpr int STAGE = 2 * kStep * D * 2;  // keys and values of a step
-    static constexpr int NST = 3;
-    static constexpr int CTAS_PER_SM = D <= 64 ? 4 : D <= 128 ? 2 : 1;
+    static constexpr int KS = D == 64 ? 32 : 16;  // keys a step
+    static constexpr int STAGE = 2 * KS * D * 2;  // keys and values of a step
+    static constexpr int NST = D == 64 ? 2 : 3;
+    static constexpr int CTAS_PER_SM = D <= 64 ? 3 : D <= 128 ? 2 : 1;
     static constexpr int OFF_BAR = kWarps * NST * STAGE;
     static constexpr int SMEM = OFF_BAR + kWarps * NST * 8 + 1024;
     static_assert((SMEM + 1024) * CTAS_PER_SM <= 233472, "shared memory budget");
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D>::CTAS_PER_SM)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ SharedArgs sa, const int behind_tiles, const int fault_stop) {
     using C = RowsCfg<D>;
-    constexpr int NST = C::NST;
+    constexpr int NST = C::NST, KS = C::KS;
     const PagedArgs &a = sa.a;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int abort_flag;
@@ -77,8 +78,14 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D>::CTAS_PER_SM)
     if (!behind_tiles) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const int n_items = min(__ldcg(sa.n_stretches), sa.cap) * a.H_kv;
-    const int stride = static_cast<int>(gridDim.x) * kWarps;
+    const int n_items = min(__ldcg(sa.counts + kStretches), sa.cap) * a.H_kv;
+    // A warp's first is its own, the next ones go to whichever warp is free (results do not depend on which).
+    const int firsts = static_cast<int>(gridDim.x) * kWarps;
+    auto take = [&]() -> int {
+        int x = 0;
+        if (lane == 0) x = atomicAdd(sa.counts + kTaken, 1);
+        return firsts + __shfl_sync(0xffffffffu, x, 0);
+    };
     // Neighbouring warps take the heads of one stretch, which lie side by side in its pages.
     auto load_work = [&](int item) -> Work {
         Work w{};
@@ -87,43 +94,44 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D>::CTAS_PER_SM)
             const int4 x = __ldcg(p), y = __ldcg(p + 1);
             w.row = x.x, w.q0 = x.y, w.n = x.z, w.plane = x.w, w.k0 = y.x, w.k1 = y.y, w.part = y.z;
             w.kvh = item % a.H_kv;
-            w.first = w.k0 & ~(kStep - 1);
-            w.steps = (w.k1 - w.first + kStep - 1) / kStep;
+            w.first = w.k0 & ~(KS - 1);
+            w.steps = (w.k1 - w.first + KS - 1) / KS;
         }
         return w;
     };
-    // lane i: the page of step `from` + i
+    // A step is one box, a page of 16 half of one.  The pages of 32 boxes are looked up at a time, lane i that of
+    // box i from step `from` on; -1: the box is outside the stretch, n_pages: there is none.
+    const int box = min(a.ps, KS), boxes = KS / box, window = 32 / boxes;
     auto pages_of = [&](const Work &w, int from) -> int {
-        const int i = from + lane;
-        return i < w.steps ? page_of(a, w.row, (w.first + i * kStep) >> a.ps_log2) : a.n_pages;
+        const int key = w.first + from * KS + lane * box;
+        return from < w.steps && key < w.k1 && key + box > w.k0 ? page_of(a, w.row, key >> a.ps_log2) : -1;
     };
     int issued = 0, taken = 0;  // steps copied and used so far
     bool ok = true;
     auto issue = [&](const Work &w, int i, int pages) {
         if (issued >= fault_stop) return;  // planted fault: this step is never copied
-        const int page = __shfl_sync(0xffffffffu, pages, i & 31), st = issued % NST;
-        if (lane == 0) {
+        const int j = lane % boxes, st = issued % NST;
+        const int page = __shfl_sync(0xffffffffu, pages, (i * boxes + j) & 31);
+        if (lane == 0) mbar_arrive_expect_tx(bar(st), C::STAGE);
+        __syncwarp();
+        if (lane < 2 * boxes) {  // keys, then values, a lane each
+            const int v = lane / boxes, row = (w.first + i * KS + j * box) & (a.ps - 1);
             if (page >= a.n_pages) atomicOr(&g_rows_data, SWA_DEVERR_BAD_PAGE);
-            const int row = (w.first + i * kStep) & (a.ps - 1);
             // debug build: the box lies in the page, the head exists
-            (void)SWA_IN_BOUNDS(row + kStep <= a.ps && w.kvh < a.H_kv && page >= 0 && page <= a.n_pages, &g_rows_err);
-            const int group8 = (page * a.H_kv + w.kvh) * (a.ps >> 3) + (row >> 3);
-            mbar_arrive_expect_tx(bar(st), C::STAGE);
-            tma_load_4d(ring + st * C::STAGE, &tm_k, bar(st), 0, 0, 0, group8);
-            tma_load_4d(ring + st * C::STAGE + C::STAGE / 2, &tm_v, bar(st), 0, 0, 0, group8);
+            (void)SWA_IN_BOUNDS(row + box <= a.ps && w.kvh < a.H_kv && page <= a.n_pages, &g_rows_err);
+            tma_load_4d(ring + st * C::STAGE + v * (C::STAGE / 2) + j * box * D * 2, v ? &tm_v : &tm_k, bar(st), 0, 0, 0,
+                        ((page < 0 ? a.n_pages : page) * a.H_kv + w.kvh) * (a.ps >> 3) + (row >> 3));
         }
         __syncwarp();
         ++issued;
     };
 
-    int item = static_cast<int>(blockIdx.x) * kWarps + warp;
-    Work w = load_work(item);
+    Work w = load_work(static_cast<int>(blockIdx.x) * kWarps + warp);
     int pages = pages_of(w, 0), at = 0;  // at: steps of w that are issued
     const int r0 = lane >> 2, r1 = r0 + 8, kq = 2 * (lane & 3);
     while (ok && w.steps > 0) {
-        while (at < w.steps && at < 32 && issued - taken < NST) issue(w, at++, pages);
-        item += stride;
-        const Work next = load_work(item);
+        while (at < w.steps && at < window && issued - taken < NST) issue(w, at++, pages);
+        const Work next = load_work(take());
         const int next_pages = pages_of(next, 0);
         int next_at = 0;
         // ---- the rows: fragments of rows r0, r1 of the 16-row M tile, and which keys each keeps
@@ -159,21 +167,22 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D>::CTAS_PER_SM)
                 break;
             }
             const uint32_t ks = ring + st * C::STAGE, vs = ks + C::STAGE / 2;
-            const int key = w.first + i * kStep;
-            const bool edge = key < w.k0 || key + kStep > w.k1;
+            const int key = w.first + i * KS;
+            const bool edge = key < w.k0 || key + KS > w.k1;
             if (edge) {  // value rows outside the stretch may hold anything, even NaN
                 uint8_t *vg = ring_gen + st * C::STAGE + C::STAGE / 2;
-                for (int idx = lane; idx < kStep * (D / 8); idx += 32) {
+                for (int idx = lane; idx < KS * (D / 8); idx += 32) {
                     const int rr = idx / (D / 8), pc = idx % (D / 8);
                     if (key + rr < w.k0 || key + rr >= w.k1)
                         *reinterpret_cast<uint4 *>(vg + sw128<D>(rr, pc)) = make_uint4(0, 0, 0, 0);
                 }
                 __syncwarp();
             }
-            // S = Q K^T over 16 keys (two n-tiles of 8)
-            float sc[2][4];
+            // S = Q K^T (n-tiles of 8 keys)
+            constexpr int NT = KS / 8;
+            float sc[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
+            for (int nt = 0; nt < NT; ++nt) {
                 sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
                 const int row = 8 * nt + (lane & 7);
 #pragma unroll
@@ -185,10 +194,10 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D>::CTAS_PER_SM)
                 }
             }
             // (a row keeps every key of most steps)
-            const bool whole = __all_sync(0xffffffffu, !edge && key >= lo0 && key >= lo1 && key + kStep <= hi0 && key + kStep <= hi1);
+            const bool whole = __all_sync(0xffffffffu, !edge && key >= lo0 && key >= lo1 && key + KS <= hi0 && key + KS <= hi1);
             float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int s = key + 8 * nt + kq + (e & 1);
@@ -217,37 +226,41 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D>::CTAS_PER_SM)
             }
             m0 = mn0;
             m1 = mn1;
-            float pr[2][4], s0 = 0.f, s1 = 0.f;
+            float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                pr[nt][0] = ex2(sc[nt][0] - ms0);
-                pr[nt][1] = ex2(sc[nt][1] - ms0);
-                pr[nt][2] = ex2(sc[nt][2] - ms1);
-                pr[nt][3] = ex2(sc[nt][3] - ms1);
-                s0 += pr[nt][0] + pr[nt][1];
-                s1 += pr[nt][2] + pr[nt][3];
+            for (int nt = 0; nt < NT; ++nt) {
+                sc[nt][0] = ex2(sc[nt][0] - ms0);
+                sc[nt][1] = ex2(sc[nt][1] - ms0);
+                sc[nt][2] = ex2(sc[nt][2] - ms1);
+                sc[nt][3] = ex2(sc[nt][3] - ms1);
+                s0 += sc[nt][0] + sc[nt][1];
+                s1 += sc[nt][2] + sc[nt][3];
             }
             l0 = l0 * al0 + s0;
             l1 = l1 * al1 + s1;
-            const uint32_t pa[4] = {pack_bf16x2(pr[0][0], pr[0][1]), pack_bf16x2(pr[0][2], pr[0][3]),
-                                    pack_bf16x2(pr[1][0], pr[1][1]), pack_bf16x2(pr[1][2], pr[1][3])};
             // O += P V (V^T fragments via transposing ldmatrix)
-            const int vrow = 8 * ((lane >> 3) & 1) + (lane & 7);
 #pragma unroll
-            for (int d2 = 0; d2 < D / 16; ++d2) {
-                uint32_t b0, b1, b2, b3;
-                ldsm_x4_t(vs + sw128<D>(vrow, 2 * d2 + (lane >> 4)), b0, b1, b2, b3);
-                mma_bf16_16816(acc[2 * d2], pa, b0, b1);
-                mma_bf16_16816(acc[2 * d2 + 1], pa, b2, b3);
+            for (int kk = 0; kk < NT / 2; ++kk) {
+                const uint32_t pa[4] = {pack_bf16x2(sc[2 * kk][0], sc[2 * kk][1]), pack_bf16x2(sc[2 * kk][2], sc[2 * kk][3]),
+                                        pack_bf16x2(sc[2 * kk + 1][0], sc[2 * kk + 1][1]),
+                                        pack_bf16x2(sc[2 * kk + 1][2], sc[2 * kk + 1][3])};
+                const int vrow = 16 * kk + 8 * ((lane >> 3) & 1) + (lane & 7);
+#pragma unroll
+                for (int d2 = 0; d2 < D / 16; ++d2) {
+                    uint32_t b0, b1, b2, b3;
+                    ldsm_x4_t(vs + sw128<D>(vrow, 2 * d2 + (lane >> 4)), b0, b1, b2, b3);
+                    mma_bf16_16816(acc[2 * d2], pa, b0, b1);
+                    mma_bf16_16816(acc[2 * d2 + 1], pa, b2, b3);
+                }
             }
             // the stage is free: this warp's zeroed rows before the next copy into it
             if (edge) fence_proxy_async_smem();
             __syncwarp();
             ++taken;
             if (at < w.steps) {
-                if ((at & 31) == 0) pages = pages_of(w, at);
+                if ((at & (window - 1)) == 0) pages = pages_of(w, at);
                 issue(w, at++, pages);
-            } else if (next_at < next.steps && next_at < 32) {
+            } else if (next_at < next.steps && next_at < window) {
                 issue(next, next_at++, next_pages);
             }
         }
@@ -298,7 +311,8 @@ cudaError_t launch_d(const SharedArgs &sa, bool behind_tiles, cudaStream_t s) {
         if (dev >= 0) configured[dev].store(true, std::memory_order_release);
     }
     CUtensorMap mk, mv;
-    if (!paged_pool_map(&mk, sa.a, sa.a.k_pages, kStep) || !paged_pool_map(&mv, sa.a, sa.a.v_pages, kStep))
+    const int box = std::min(sa.a.ps, C::KS);
+    if (!paged_pool_map(&mk, sa.a, sa.a.k_pages, box) || !paged_pool_map(&mv, sa.a, sa.a.v_pages, box))
         return cudaErrorInvalidValue;
     return launch_dependent(true, paged_rows_kernel<D>, dim3(paged_sm_count() * C::CTAS_PER_SM), kThreads, C::SMEM, s, mk,
                             mv, sa, static_cast<int>(behind_tiles), fault_plan().split_stop_stage);

@@ -74,7 +74,7 @@ __device__ __forceinline__ void list_stretches(const SharedArgs &sa, const Keys 
         if (lane >= o) inc += x;
     }
     int at = 0;
-    if (lane == 31 && inc > 0) at = atomicAdd(sa.n_stretches, inc);
+    if (lane == 31 && inc > 0) at = atomicAdd(sa.counts + kStretches, inc);
     at = __shfl_sync(0xffffffffu, at, 31) + inc - count;
     for (int i = 0; i < count; ++i) {
         // (more than there is room for: sequences that overlap, from a q_start that goes down)
@@ -91,11 +91,11 @@ __device__ __forceinline__ void list_stretches(const SharedArgs &sa, const Keys 
     }
 }
 
-// What the other kernels need to know of sequences b0 .. b1 - 1 (of group g, with `base` positions in its prefix
-// part): a warp of `warps` has every 32nd, number `w` of them.
-__device__ __forceinline__ void put_sequences(const SharedArgs &sa, int b0, int b1, int g, int base, int w, int warps) {
+// What the other kernels need to know of sequences b0 .. b1 - 1 (of group g): a warp of `warps` has every 32nd, number `w` of them.
+__device__ __forceinline__ void put_sequences(const SharedArgs &sa, int b0, int b1, const PagedGroup &group, int g, int w,
+                                              int warps) {
     const PagedArgs &a = sa.a;
-    const int lane = threadIdx.x & 31, TT = kStretchRows / a.G;
+    const int lane = threadIdx.x & 31, TT = kStretchRows / a.G, base = group.end;
     for (int first = b0 + w * 32; first < b1; first += warps * 32) {
         const int b = first + lane;
         Seq s{};
@@ -103,8 +103,10 @@ __device__ __forceinline__ void put_sequences(const SharedArgs &sa, int b0, int 
             s = load_seq(a, b);
             if (!s.ok) atomicOr(&g_shared_err, SWA_DEVERR_BAD_POSITION);
             // (a sequence without new tokens may end inside what the others share)
-            sa.base[b] = s.n > 0 ? base : 0;
-            sa.group_of[b] = s.n > 0 && base > 0 ? g : -1;
+            if (!sa.few) sa.base[b] = s.n > 0 ? base : 0;
+            int4 *info = sa.info + 2 * static_cast<int64_t>(b);
+            info[0] = s.n > 0 ? make_int4(base, group.n, group.few, group.q0) : make_int4(0, 0, 0, 0);
+            info[1] = make_int4(group.p0, g, 0, 0);
         }
         const int longest = __reduce_max_sync(0xffffffffu, s.n);
         if (sa.few || (base > 0 && a.window != INT_MAX)) {  // the rows' positions
@@ -135,8 +137,15 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
     __shared__ int first;  // of the group's entries in question: the first that is not shared
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
-    const int clusters = static_cast<int>(gridDim.x) / ranks, c = static_cast<int>(blockIdx.x) / ranks;
+    const int clusters = sa.clusters, c = static_cast<int>(blockIdx.x) / ranks;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (c >= clusters) {  // the blocks behind those of the plan store the new tokens, a warp a token
+        const int w0 = (static_cast<int>(blockIdx.x) - clusters * ranks) * kWarps + warp;
+        const int warps = (static_cast<int>(gridDim.x) - clusters * ranks) * kWarps;
+        for (int n = w0; n < a.N; n += warps) store_token(a, n, lane, &g_shared_err);
+        return;
+    }
+    if (clusters == 1 && rank == 0 && tid < kCounts) sa.counts[tid] = 0;  // (seen by the cluster behind its first barrier)
     bool fine = true;
     for (int i = tid; i < sa.n_groups; i += kThreads) {
         const int b0 = __ldg(sa.group_start + i), b1 = __ldg(sa.group_start + i + 1);
@@ -144,11 +153,6 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
     }
     fine = __syncthreads_and(fine);
     if (!fine && blockIdx.x == 0 && tid == 0) atomicOr(&g_shared_err, SWA_DEVERR_BAD_POSITION);
-    if (c == 0) {  // sequences of no group
-        const int lo = fine ? __ldg(sa.group_start) : a.B, hi = fine ? __ldg(sa.group_start + sa.n_groups) : a.B;
-        put_sequences(sa, 0, lo, -1, 0, rank * kWarps + warp, ranks * kWarps);
-        put_sequences(sa, hi, a.B, -1, 0, rank * kWarps + warp, ranks * kWarps);
-    }
     for (int g = c; g < sa.n_groups; g += clusters) {
         const int b0 = fine ? __ldg(sa.group_start + g) : 0, b1 = fine ? __ldg(sa.group_start + g + 1) : 0;
         Members m{~0ull, -1, 0, 0, 0, 0};
@@ -218,26 +222,32 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         // (read by the other blocks before it is set for the next group; the sums, too)
         if (ranks > 1) cluster.sync();
         else __syncthreads();
+        PagedGroup out{};
+        if (base > 0) {
+            out.q0 = a.q_start ? __ldg(a.q_start + b0) : b0;
+            (stretch ? out.few : out.n) = static_cast<int>(m.tokens);
+            out.p0 = p0;
+            out.end = base;
+            out.row = leader;
+            out.top = m.top;
+        }
         if (rank == 0 && warp == 0) {
-            PagedGroup out{};
-            if (base > 0) {
-                out.q0 = a.q_start ? __ldg(a.q_start + b0) : b0;
-                (stretch ? out.few : out.n) = static_cast<int>(m.tokens);
-                out.p0 = p0;
-                out.end = base;
-                out.row = leader;
-                out.top = m.top;
+            if (lane == 0) {
+                sa.groups[g] = out;
+                if (out.n > 0) atomicAdd(sa.counts + kTileGroups, 1);
             }
-            if (lane == 0) sa.groups[g] = out;
             if (out.few > 0) {
                 const Keys k = prefix_keys(a, p0, base, sa.few_prefix.planes);
                 list_stretches(sa, k, lane == 0 ? k.stretches() : 0, Stretch{leader, out.q0, out.few, 0, 0, 0, 1, 0});
             }
         }
-        put_sequences(sa, b0, b1, g, base, rank * kWarps + warp, ranks * kWarps);
+        put_sequences(sa, b0, b1, out, g, rank * kWarps + warp, ranks * kWarps);
     }
-    // (behind an append: what waits for this kernel waits for that, too)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (c == 0) {  // sequences of no group
+        const int lo = fine ? __ldg(sa.group_start) : a.B, hi = fine ? __ldg(sa.group_start + sa.n_groups) : a.B;
+        put_sequences(sa, 0, lo, PagedGroup{}, -1, rank * kWarps + warp, ranks * kWarps);
+        put_sequences(sa, hi, a.B, PagedGroup{}, -1, rank * kWarps + warp, ranks * kWarps);
+    }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -245,6 +255,20 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
 // planes or in the slots of the CTAs that share a unit, are joined: with M the largest m, o = sum 2^(m - M) acc /
 // sum 2^(m - M) l.  Bound by latency: the row's sequence, its group, then the maxima, then the values.
 // ---------------------------------------------------------------------------------------------
+template <int E>
+__device__ __forceinline__ void load_columns(float (&x)[E], const float *src) {
+    if constexpr (E == 2) {
+        const float2 t = __ldcg(reinterpret_cast<const float2 *>(src));
+        x[0] = t.x, x[1] = t.y;
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+            const float4 t = __ldcg(reinterpret_cast<const float4 *>(src + e));
+            x[e] = t.x, x[e + 1] = t.y, x[e + 2] = t.z, x[e + 3] = t.w;
+        }
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ SharedArgs sa) {
     constexpr int E = D / 32;  // columns of a lane
@@ -257,8 +281,9 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     const Seq s = b >= 0 ? load_seq(a, b) : Seq{};
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (b < 0 || !s.ok || n < s.q0 || n >= s.q0 + s.n) return;
-    const int base = __ldcg(sa.base + b), g = __ldcg(sa.group_of + b);
-    const int i = n - s.q0;
+    const int4 *info = sa.info + 2 * static_cast<int64_t>(b);
+    const int4 u = __ldcg(info), v = __ldcg(info + 1);  // base, the group's tokens in tiles, in stretches, its first; its p0, number
+    const int base = u.x, i = n - s.q0;
     // the parts: how many results, where
     struct Where {
         const PartResults *p;
@@ -280,14 +305,10 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     Where own, pre{nullptr, 0, -1, 0, 0, false};
     if (sa.few) own = in_planes(sa.part[0], own_keys(a, s, base, i / TT, TT, sa.part[0].planes));
     else own = in_tiles(sa.part[0], s.q0, b);
-    if (g >= 0 && g < sa.n_groups) {
-        const int4 *gp = reinterpret_cast<const int4 *>(sa.groups + g);
-        const int4 u = __ldcg(gp), v = __ldcg(gp + 1);  // q0 n p0 end, row top few
-        if (v.z > 0) pre = in_planes(sa.few_prefix, prefix_keys(a, u.z, u.w, sa.few_prefix.planes));
-        else if (u.y > 0) pre = in_tiles(sa.part[1], u.x, g);
-    }
+    if (u.z > 0) pre = in_planes(sa.few_prefix, prefix_keys(a, v.x, base, sa.few_prefix.planes));
+    else if (u.y > 0) pre = in_tiles(sa.part[1], u.w, v.y);
     const int64_t row = static_cast<int64_t>(n) * a.H_q + h, plane = static_cast<int64_t>(a.N) * a.H_q;
-    auto result = [&](int c, const float2 *&ml, const float *&o, int &step) {
+    auto result = [&](int c, const float2 *&ml, const float *&o) {
         const bool first = c < own.count;
         const Where &w = first ? own : pre;
         const int k = first ? c : c - own.count;
@@ -295,52 +316,56 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
         if (w.pieces) {
             const int64_t slot = k == 0 ? 2 * w.owner + 1 : 2 * (w.owner + k);
             ml = reinterpret_cast<const float2 *>(p.ws.ml) + slot * p.rows + w.row;
-            o = p.ws.acc + partial_at<D>(slot, p.rows, w.row, 0);
-            step = p.rows * 8;  // from eight columns to the next eight
+            o = p.ws.acc + (slot * p.rows + w.row) * D;
         } else {
             const int64_t at = (k == w.sink ? p.planes - 1 : k) * plane + row;
             ml = p.ml + at;
             o = p.o + at * D;
-            step = 8;
         }
     };
     const int count = own.count + pre.count;
+    constexpr int kAtOnce = 8;  // results whose values are on their way at a time
     float acc[E], m = -INFINITY, L = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
     for (int c0 = 0; c0 < count; c0 += 32) {
         const int in = min(32, count - c0);
-        float2 v = make_float2(-INFINITY, 0.f);
-        const float2 *ml;
+        float2 v2 = make_float2(-INFINITY, 0.f);
         const float *o = nullptr;
-        int step = 8;
         if (lane < in) {
-            result(c0 + lane, ml, o, step);
-            v = __ldcg(ml);
+            const float2 *ml;
+            result(c0 + lane, ml, o);
+            v2 = __ldcg(ml);
         }
-        float mn = m;
-        mn = fmaxf(mn, v.x);
+        float x[kAtOnce][E];
+        auto load = [&](int k0) {
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const auto src = reinterpret_cast<const float *>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (k0 + k) & 31));
+                if (k0 + k < in) load_columns<E>(x[k], src + lane * E);
+                else
+#pragma unroll
+                    for (int e = 0; e < E; ++e) x[k][e] = 0.f;
+            }
+        };
+        load(0);
+        float mn = fmaxf(m, v2.x);
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
-        const float ms = mn == -INFINITY ? 0.f : mn, old = ex2(m - ms);
-        const float f = ex2(v.x - ms);
-        L = L * old + f * v.y;
+        // (a result that kept nothing of this row has weight 0 and finite values)
+        const float ms = mn == -INFINITY ? 0.f : mn, old = ex2(m - ms), f = ex2(v2.x - ms);
+        L = L * old + f * v2.y;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] *= old;
         m = mn;
-#pragma unroll 4
-        for (int k = 0; k < in; ++k) {
-            const float fk = __shfl_sync(0xffffffffu, f, k);
-            const float *src = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), k));
-            const int st = __shfl_sync(0xffffffffu, step, k);
-            // columns lane * E .. (E <= 8 of them lie in one block of eight)
-            const float *at = src + static_cast<int64_t>(lane * E / 8) * st + lane * E % 8;
-            // (a result that kept nothing of this row has weight 0 and finite values)
+        for (int k0 = 0; k0 < in; k0 += kAtOnce) {
+            if (k0 > 0) load(k0);
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 t = __ldcg(reinterpret_cast<const float2 *>(at + e));
-                acc[e] += fk * t.x;
-                acc[e + 1] += fk * t.y;
+            for (int k = 0; k < kAtOnce; ++k) {
+                const float fk = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] += fk * x[k][e];
             }
         }
     }
@@ -364,7 +389,7 @@ struct Layout {
     bool few, tiles;  // tiles: prefixes may go to the many-row kernel
     int planes, prefix_planes, cap;
     PagedShape shape;  // of the many-row kernel
-    size_t slots[2], base, group_of, groups, pos, count, list, units[2], ml[2], o[2], few_ml, few_o, bytes;
+    size_t slots[2], base, info, groups, pos, count, list, units[2], ml[2], o[2], few_ml, few_o, bytes;
 };
 
 Layout layout(const PagedArgs &a, int n_groups) {
@@ -375,8 +400,8 @@ Layout layout(const PagedArgs &a, int n_groups) {
     l.shape = paged_tile_shape(a);
     const int TT = kStretchRows / a.G;
     const int64_t units = std::min<int64_t>(a.N, static_cast<int64_t>(a.N) / TT + a.B);
-    // Stretches of a unit: about four for every resident warp where units are few, two at least.
-    const int64_t want = (4 * static_cast<int64_t>(shared_rows_warps(a.D)) + units * a.H_kv - 1) / (units * a.H_kv);
+    // Stretches of a unit at most: about sixteen for every resident warp where units are few, two at least.
+    const int64_t want = (16 * static_cast<int64_t>(shared_rows_warps(a.D)) + units * a.H_kv - 1) / (units * a.H_kv);
     l.planes = l.few ? static_cast<int>(std::min<int64_t>(std::max<int64_t>(want, 2), 128)) + 1 : 1;
     l.prefix_planes = l.few ? l.planes : 0;
     const int64_t cap = l.few ? units * l.planes + std::min<int64_t>(n_groups, a.N / 2 + 1) * l.planes : 0;
@@ -401,30 +426,34 @@ Layout layout(const PagedArgs &a, int n_groups) {
     l.few_ml = take(l.prefix_planes * rows * 8);
     l.few_o = take(l.prefix_planes * rows * a.D * 4);
     l.base = take(static_cast<size_t>(a.B) * 4);
-    l.group_of = take(static_cast<size_t>(a.B) * 4);
+    l.info = take(static_cast<size_t>(a.B) * 32);
     l.groups = take(static_cast<size_t>(n_groups) * sizeof(PagedGroup));
     l.pos = take(static_cast<size_t>(a.N) * 4);
-    l.count = take(4);
+    l.count = take(kCounts * 4);
     l.list = take(static_cast<size_t>(l.cap) * sizeof(Stretch));
     l.bytes = at;
     return l;
 }
 
-cudaError_t launch_plan(const SharedArgs &sa, bool after_append, cudaStream_t s) {
+cudaError_t launch_plan(SharedArgs &sa, cudaStream_t s) {
     const int ranks = sa.n_groups < kFewGroups ? kCluster : 1;
-    const int most = paged_sm_count() * 4;
+    sa.clusters = std::min(sa.n_groups, paged_sm_count() * 4);
+    if (sa.clusters > 1) {
+        const cudaError_t e = cudaMemsetAsync(sa.counts, 0, kCounts * 4, s);
+        if (e != cudaSuccess) return e;
+    }
+    int append = 0;
+    if (sa.a.kn) append = std::min((sa.a.N + kWarps - 1) / kWarps, paged_sm_count() * 8);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ranks * (sa.n_groups < most ? sa.n_groups : most));
+    cfg.gridDim = dim3(ranks * (sa.clusters + (append + ranks - 1) / ranks));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ranks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = after_append ? 2 : 1;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, paged_plan_kernel, sa);
 }
 
@@ -452,15 +481,14 @@ cudaError_t launch_paged_shared(const PagedArgs &a, const int32_t *group_start, 
     char *p = static_cast<char *>(ws);
     SharedArgs sa{};
     sa.a = a;
-    sa.a.kn = sa.a.vn = nullptr;
     sa.group_start = group_start;
     sa.n_groups = n_groups;
     sa.groups = reinterpret_cast<PagedGroup *>(p + l.groups);
     sa.base = reinterpret_cast<int32_t *>(p + l.base);
-    sa.group_of = reinterpret_cast<int32_t *>(p + l.group_of);
+    sa.info = reinterpret_cast<int4 *>(p + l.info);
     sa.pos = reinterpret_cast<int32_t *>(p + l.pos);
     sa.stretches = reinterpret_cast<Stretch *>(p + l.list);
-    sa.n_stretches = reinterpret_cast<int32_t *>(p + l.count);
+    sa.counts = reinterpret_cast<int32_t *>(p + l.count);
     sa.cap = l.cap;
     sa.few = l.few;
     sa.any_tiles = l.tiles;
@@ -482,6 +510,8 @@ cudaError_t launch_paged_shared(const PagedArgs &a, const int32_t *group_start, 
     sa.few_prefix.planes = l.prefix_planes;
     auto part_args = [&](int x) {
         PagedArgs t = sa.a;
+        t.kn = t.vn = nullptr;
+        t.tile_groups = sa.counts + kTileGroups;
         t.groups = sa.groups;
         t.pos = sa.pos;
         t.base = sa.base;
@@ -491,12 +521,7 @@ cudaError_t launch_paged_shared(const PagedArgs &a, const int32_t *group_start, 
         if (x) t.B = n_groups;
         return t;
     };
-    const bool append = a.kn != nullptr;
-    // (not by the append kernel, which the plan does not wait for before it counts)
-    cudaError_t e = l.few ? cudaMemsetAsync(sa.n_stretches, 0, 4, s) : cudaSuccess;
-    if (e == cudaSuccess && append) e = launch_paged_append(a, nullptr, 0, s);
-    if (e != cudaSuccess) return e;
-    e = launch_plan(sa, append, s);
+    cudaError_t e = launch_plan(sa, s);
     if (e != cudaSuccess) return e;
     if (l.tiles) e = launch_paged_tile(part_args(1), sa.part[1].ws, true, s, Part::kPrefix);
     if (e != cudaSuccess) return e;

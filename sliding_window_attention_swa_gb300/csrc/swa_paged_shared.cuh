@@ -62,15 +62,20 @@ struct PartResults {
     int ctas, rows, TQ, TT;
 };
 
+// Stretches on the list, groups with rows for the many-row kernel, stretches taken beyond each warp's first.
+enum { kStretches, kTileGroups, kTaken, kCounts };
+
 struct SharedArgs {
     PagedArgs a;
     const int32_t *group_start;  // [n_groups + 1]
     int n_groups;
     PagedGroup *groups;
-    int32_t *base, *group_of;  // [B]; group_of: -1: none
+    int32_t *base;             // [B]
+    int4 *info;                // [B][2]: base, its group's n, few, q0; p0, the group's number
     int32_t *pos;              // [N]
     Stretch *stretches;        // [cap]
-    int32_t *n_stretches;      // zero at the plan's start
+    int32_t *counts;           // [kCounts]
+    int clusters;              // of the plan
     int cap;
     int few;                   // own parts (and prefixes of few rows) are cut into stretches
     int any_tiles;             // prefixes may go to the many-row kernel

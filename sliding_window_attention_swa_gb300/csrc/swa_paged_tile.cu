@@ -174,6 +174,14 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         return;
     }
 
+    if constexpr (PT != Part::kAll) {
+        // The prefix part waits for the plan (and the append before it), and only then lets the own part start, which
+        // thus finds what they wrote.  The own part needs nothing of the prefix part: it waits for that at its end, so
+        // that what waits for it waits for both.
+        if constexpr (PT == Part::kPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if (PT == Part::kPrefix && __ldcg(a.tile_groups) == 0) return;  // (no group has more rows than a stretch)
+    }
     const uint32_t sQ = sbase + C::OFF_Q, sRing = sbase + C::OFF_RING;
     const uint32_t bars = sbase + C::OFF_BAR;
     auto bar_qf = [&](int x) { return bars + 8u * x; };
@@ -234,13 +242,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     }
     const int TT = ta.TT;
     tc_fence_before();
-    if constexpr (PT != Part::kAll) {
-        // The prefix part waits for the plan (and the append before it), and only then lets the own part start, which
-        // thus finds what they wrote.  The own part needs nothing of the prefix part: it waits for that at its end, so
-        // that what waits for it waits for both.
-        if constexpr (PT == Part::kPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    }
     // (its block barriers also publish the mbarriers and the TMEM address)
     find_share<BN, C::THREADS, true, PT>(a, TT, ta.min_tiles, sgen + C::OFF_RING, share, &g_ptile_data);
     tc_fence_after();
@@ -914,9 +915,11 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                         uint32_t wv[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) wv[e] = __float_as_uint(f[q8 * 8 + e]);
-                        float *dst = PT != Part::kAll && whole
-                                         ? a.part_o + (tok * a.H_q + h) * D + c * 32 + q8 * 8
-                                         : ta.ws.acc + partial_at<D>(pslot, NQT * BM, prow, c * 32 + q8 * 8);
+                        // (a part's pieces row by row: the kernel that joins them reads a row at a time)
+                        float *dst = PT == Part::kAll ? ta.ws.acc + partial_at<D>(pslot, NQT * BM, prow, c * 32 + q8 * 8)
+                                     : whole ? a.part_o + (tok * a.H_q + h) * D + c * 32 + q8 * 8
+                                             : ta.ws.acc + (static_cast<int64_t>(pslot) * (NQT * BM) + prow) * D +
+                                                   c * 32 + q8 * 8;
                         st_global_v8(dst, wv);
                     }
                 } else if (store) {
