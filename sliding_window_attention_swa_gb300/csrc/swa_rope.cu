@@ -16,12 +16,13 @@ constexpr int kThreads = 256;
 // ---------------------------------------------------------------------------------------------
 // table: out[p, i] = scale cos(p f_i), out[p, R/2 + i] = scale sin(p f_i).
 // An angle is only needed modulo a turn, and f_i / (2 pi) modulo 1 is held as a 64-bit fraction G_i: p G_i mod
-// 2^64 is then the angle of position p in units of 2^-64 turns, off by p 2^-65, with one integer
-// product in place of 64-bit floating point, of which an SM has two lanes.
-// The fraction's eighth of a turn goes to fp32 with an error of 2^-25 of it; sincospif does the rest.
-// Bound by HBM writes and, as near, by the instructions of sincospif.
+// 2^64 is then the angle of position p in units of 2^-64 turns, off by p 2^-64 at most, by integer
+// arithmetic alone.  (An SM has two lanes for 64-bit floating point: a block uses them once a column.)
+// The angle's nearest quarter turn goes into signs and a swap; the rest y, in eighths of a turn, |y| <= 1, into the
+// Taylor polynomials of sin and cos at y pi/4, of degree 9 and 10 (remainders below 2e-9).
+// Bound by HBM writes and, as near, by the instructions of the polynomials (about 30 a pair).
 // ---------------------------------------------------------------------------------------------
-constexpr int kTableRows = 8;  // rows of a thread: the fractions of its four columns are made once for them
+constexpr int kTableCols = 128;  // most columns (half a head of 256)
 
 // frac(f / (2 pi)) in units of 2^-64
 __device__ __forceinline__ unsigned long long turn_fraction(double f) {
@@ -35,46 +36,56 @@ __device__ __forceinline__ unsigned long long turn_fraction(double f) {
     return f < 0.0 ? 0ull - g : g;
 }
 
-__global__ void __launch_bounds__(kThreads) rope_table_kernel(const double *inv_freq, int half, int n_pos, float scale,
-                                                              float *out) {
-    const int per_row = half / 4;
-    const int64_t x = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int col = static_cast<int>(x % per_row) * 4;
-    const int64_t p_first = x / per_row * kTableRows;
-    if (p_first >= n_pos) return;
-    unsigned long long g[4];
-    bool finite[4];
+// cos and sin of x 2^-64 turns
+__device__ __forceinline__ void cos_sin(unsigned long long x, float &c, float &s) {
+    // the angle in units of 2^-32 turns, to the nearest; q: its nearest quarter, r: the rest
+    const unsigned int t = static_cast<unsigned int>((x + 0x80000000ull) >> 32);
+    const unsigned int q = (t + 0x20000000u) >> 30;
+    const int r = static_cast<int>(t - (q << 30));
+    const float y = static_cast<float>(r) * 1.862645149230957e-9f, z = y * y;  // 2^-29
+    // (-1)^k (pi/4)^n / n! for n = 2 k + 1 and n = 2 k
+    const float sn = y * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 3.13361681492097e-07f, -3.657620254671201e-05f), 0.002490394515916705f), -0.08074551075696945f), 0.7853981852531433f);
+    const float cs = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.461136894282845e-08f, 3.5908603877032874e-06f), -0.0003259918885305524f), 0.01585434377193451f), -0.3084251284599304f), 1.0f);
+    const float a = q & 1u ? sn : cs, b = q & 1u ? cs : sn;
+    // quarters 1, 2 turn the cosine's sign, 2, 3 the sine's
+    c = __uint_as_float(__float_as_uint(a) ^ (((q + 1u) & 2u) << 30));
+    s = __uint_as_float(__float_as_uint(b) ^ ((q & 2u) << 30));
+}
+
+// A block has `steps` rows of each of its threads, which have four columns each.
+__global__ void __launch_bounds__(kThreads) rope_table_kernel(const double *inv_freq, int half, int n_pos, int steps,
+                                                              float scale, float *out) {
+    __shared__ unsigned long long fraction[kTableCols];
+    __shared__ float factor[kTableCols];  // scale, or NaN
+    for (int i = threadIdx.x; i < half; i += kThreads) {
+        const double f = __ldg(inv_freq + i);
+        const bool finite = isfinite(f);
+        fraction[i] = finite ? turn_fraction(f) : 0ull;
+        factor[i] = finite ? scale : NAN;
+    }
+    __syncthreads();
+    const int per_row = half / 4, rows = kThreads / per_row;  // (threads behind the last whole row have none)
+    const int row = static_cast<int>(threadIdx.x) / per_row, col = static_cast<int>(threadIdx.x) % per_row * 4;
+    if (row >= rows) return;
+    int64_t p = static_cast<int64_t>(blockIdx.x) * (rows * steps) + row;
+    unsigned long long x[4], step[4];
+    float k[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const double f = __ldg(inv_freq + col + e);
-        finite[e] = isfinite(f);
-        g[e] = finite[e] ? turn_fraction(f) : 0ull;
+        x[e] = fraction[col + e] * static_cast<unsigned long long>(p);
+        step[e] = fraction[col + e] * static_cast<unsigned long long>(rows);
+        k[e] = factor[col + e];
     }
-    const int rows = static_cast<int>(min(static_cast<int64_t>(kTableRows), n_pos - p_first));
-#pragma unroll 2
-    for (int i = 0; i < rows; ++i) {
-        const unsigned long long p = static_cast<unsigned long long>(p_first + i);
+    float *at = out + p * (2 * half) + col;
+    for (int i = 0; i < steps && p < n_pos; ++i, p += rows, at += static_cast<int64_t>(rows) * (2 * half)) {
         float c[4], s[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            // the angle in units of 2^-32 turns, to the nearest; q: its nearest quarter, r: the rest
-            const unsigned int t = static_cast<unsigned int>((p * g[e] + 0x80000000ull) >> 32);
-            const unsigned int q = (t + 0x20000000u) >> 30;
-            const int r = static_cast<int>(t - (q << 30));
-            float sn, cs;
-            sincospif(static_cast<float>(r) * 4.656612873077392578125e-10f, &sn, &cs);  // 2^-31
-            const bool swap = q & 1u;
-            c[e] = swap ? sn : cs;
-            s[e] = swap ? cs : sn;
-            // quarters 1, 2 turn the cosine's sign, 2, 3 the sine's
-            c[e] = (q == 1u || q == 2u) ? -c[e] : c[e];
-            s[e] = q >= 2u ? -s[e] : s[e];
-            c[e] = finite[e] ? c[e] * scale : NAN;
-            s[e] = finite[e] ? s[e] * scale : NAN;
+            cos_sin(x[e], c[e], s[e]);
+            x[e] += step[e];
         }
-        float *row = out + (p_first + i) * (2 * half) + col;
-        *reinterpret_cast<float4 *>(row) = make_float4(c[0], c[1], c[2], c[3]);
-        *reinterpret_cast<float4 *>(row + half) = make_float4(s[0], s[1], s[2], s[3]);
+        *reinterpret_cast<float4 *>(at) = make_float4(c[0] * k[0], c[1] * k[1], c[2] * k[2], c[3] * k[3]);
+        *reinterpret_cast<float4 *>(at + half) = make_float4(s[0] * k[0], s[1] * k[1], s[2] * k[2], s[3] * k[3]);
     }
 }
 
@@ -115,7 +126,7 @@ __device__ __forceinline__ void turn(uint4 &a, uint4 &b, const float (&c)[8], co
 }
 
 template <int D, bool kPairs>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const PagedArgs a, const RopeArgs r, int chunks,
+__global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const PagedArgs a, const RopeArgs r, int chunks,
                                                                int tokens) {
     constexpr int CS = D / 16, HPI = 32 / CS;  // lanes a head, heads a step
     const int lane = threadIdx.x & 31;
@@ -189,7 +200,9 @@ cudaError_t launch_d(const PagedArgs &a, const RopeArgs &r, cudaStream_t s) {
     constexpr int kHeads = 32 / (D / 16) * kUnroll;  // of a warp
     const int heads = (a.q ? a.H_q : 0) + (a.kn ? 2 * a.H_kv : 0);
     const int chunks = (heads + kHeads - 1) / kHeads;
-    const int tokens = 1;
+    // Up to four tokens of a warp, one after the other, where there are warps enough: a sequence is looked up once.
+    const int64_t want = static_cast<int64_t>(a.N) * chunks / (40 * paged_sm_count());
+    const int tokens = static_cast<int>(want < 1 ? 1 : want > 4 ? 4 : want);
     const int64_t warps = (static_cast<int64_t>(a.N) + tokens - 1) / tokens * chunks;
     const int64_t blocks = (warps * 32 + kThreads - 1) / kThreads;
     if (blocks > INT_MAX) return cudaErrorInvalidValue;
@@ -201,10 +214,13 @@ cudaError_t launch_d(const PagedArgs &a, const RopeArgs &r, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_rope_table(const double *inv_freq, int rot, int n_pos, float scale, float *out, cudaStream_t s) {
-    const int64_t rows = (static_cast<int64_t>(n_pos) + kTableRows - 1) / kTableRows;
-    const int64_t blocks = (rows * (rot / 8) + kThreads - 1) / kThreads;
+    const int64_t rows = kThreads / (rot / 8);  // of a step
+    // (up to sixteen steps of a block where there are blocks enough: the columns' fractions are made once a block)
+    const int64_t all = (static_cast<int64_t>(n_pos) + rows - 1) / rows, want = all / (8 * paged_sm_count());
+    const int steps = static_cast<int>(want < 1 ? 1 : want > 16 ? 16 : want);
+    const int64_t blocks = (all + steps - 1) / steps;
     if (blocks > INT_MAX) return cudaErrorInvalidValue;
-    rope_table_kernel<<<static_cast<int>(blocks), kThreads, 0, s>>>(inv_freq, rot / 2, n_pos, scale, out);
+    rope_table_kernel<<<static_cast<int>(blocks), kThreads, 0, s>>>(inv_freq, rot / 2, n_pos, steps, scale, out);
     return cudaGetLastError();
 }
 
