@@ -123,7 +123,7 @@ __device__ __forceinline__ void put_sequences(const SharedArgs &sa, int b0, int 
         if (!sa.few) continue;
         for (int ut = 0; ut * TT < longest; ++ut) {
             const bool unit = ut * TT < s.n;
-            const Keys k = unit ? own_keys(a, s, base, ut, TT, sa.part[0].planes) : Keys{};
+            const Keys k = unit ? own_keys(a, s, base, ut, TT, sa.part[0]) : Keys{};
             list_stretches(sa, k, unit ? k.stretches() : 0,
                            Stretch{b, s.q0 + ut * TT, min(TT, s.n - ut * TT), 0, 0, 0, 0, 0});
         }
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         if (lane == 0) sums[warp] = m;
         if (tid == 0) first = INT_MAX;
         // (the words that the cluster's other blocks write to are set before any of them does)
-        if (ranks > 1) cluster.sync();
-        else __syncthreads();
+        if (ranks > 1) cluster.barrier_arrive();
+        __syncthreads();
         m = sums[0];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) m = join(m, sums[w]);
@@ -212,16 +212,18 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
                     if (x[k] != y[k]) differs = min(differs, i0 + k * 32 + lane);
             }
             differs = __reduce_min_sync(0xffffffffu, differs);
+            if (ranks > 1) cluster.barrier_wait();
             if (lane == 0 && differs < INT_MAX) atomicMin(ranks > 1 ? cluster.map_shared_rank(&first, 0) : &first, differs);
             if (ranks > 1) cluster.sync();
             else __syncthreads();
             const int f = min(ranks > 1 ? *cluster.map_shared_rank(&first, 0) : first, n);
             base = f < sinks ? 0 : (e_lo + f - sinks) << a.ps_log2;
             if (base - lo < kLeastShared) base = 0;
+        } else if (ranks > 1) {
+            cluster.barrier_wait();
         }
         // (read by the other blocks before it is set for the next group; the sums, too)
-        if (ranks > 1) cluster.sync();
-        else __syncthreads();
+        if (ranks > 1) cluster.barrier_arrive();
         PagedGroup out{};
         if (base > 0) {
             out.q0 = a.q_start ? __ldg(a.q_start + b0) : b0;
@@ -237,11 +239,13 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
                 if (out.n > 0) atomicAdd(sa.counts + kTileGroups, 1);
             }
             if (out.few > 0) {
-                const Keys k = prefix_keys(a, p0, base, sa.few_prefix.planes);
+                const Keys k = prefix_keys(a, p0, base, sa.few_prefix);
                 list_stretches(sa, k, lane == 0 ? k.stretches() : 0, Stretch{leader, out.q0, out.few, 0, 0, 0, 1, 0});
             }
         }
         put_sequences(sa, b0, b1, out, g, rank * kWarps + warp, ranks * kWarps);
+        if (ranks > 1) cluster.barrier_wait();
+        else __syncthreads();
     }
     if (c == 0) {  // sequences of no group
         const int lo = fine ? __ldg(sa.group_start) : a.B, hi = fine ? __ldg(sa.group_start + sa.n_groups) : a.B;
@@ -279,10 +283,11 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     if (n >= a.N) return;  // (the grid has blocks of whole rows; nothing waits for these warps)
     const int b = find_sequence(a, n, lane);
     const Seq s = b >= 0 ? load_seq(a, b) : Seq{};
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (b < 0 || !s.ok || n < s.q0 || n >= s.q0 + s.n) return;
+    // (the plan's: the kernels before this one have waited for it before they let this grid start)
     const int4 *info = sa.info + 2 * static_cast<int64_t>(b);
     const int4 u = __ldcg(info), v = __ldcg(info + 1);  // base, the group's tokens in tiles, in stretches, its first; its p0, number
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int base = u.x, i = n - s.q0;
     // the parts: how many results, where
     struct Where {
@@ -303,9 +308,9 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     };
     const int TT = kStretchRows / a.G;
     Where own, pre{nullptr, 0, -1, 0, 0, false};
-    if (sa.few) own = in_planes(sa.part[0], own_keys(a, s, base, i / TT, TT, sa.part[0].planes));
+    if (sa.few) own = in_planes(sa.part[0], own_keys(a, s, base, i / TT, TT, sa.part[0]));
     else own = in_tiles(sa.part[0], s.q0, b);
-    if (u.z > 0) pre = in_planes(sa.few_prefix, prefix_keys(a, v.x, base, sa.few_prefix.planes));
+    if (u.z > 0) pre = in_planes(sa.few_prefix, prefix_keys(a, v.x, base, sa.few_prefix));
     else if (u.y > 0) pre = in_tiles(sa.part[1], u.w, v.y);
     const int64_t row = static_cast<int64_t>(n) * a.H_q + h, plane = static_cast<int64_t>(a.N) * a.H_q;
     auto result = [&](int c, const float2 *&ml, const float *&o) {
@@ -324,7 +329,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
         }
     };
     const int count = own.count + pre.count;
-    constexpr int kAtOnce = 8;  // results whose values are on their way at a time
+    constexpr int kAtOnce = E <= 4 ? 12 : 8;  // results whose values are on their way at a time
     float acc[E], m = -INFINITY, L = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;

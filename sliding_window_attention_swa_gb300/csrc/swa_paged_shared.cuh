@@ -7,49 +7,15 @@
 namespace swa {
 
 constexpr int kStretchRows = 16;  // rows of a unit of the kernel for few rows (mma.sync M)
-constexpr int kStretchKeys = 256;  // least keys of a stretch
+// Least keys of a stretch.  256 instead: 135 sequences of 250 tokens on average behind their prefixes 100 us instead of 91,
+// 31 small groups 110.5 instead of 105; 64 sequences with prefixes in tiles 86 instead of 89.
+constexpr int kStretchKeys = 64;
 
 // One stretch: tokens q0 .. q0 + n - 1 (n * G <= 16 rows) over the keys k0 .. k1 - 1 in the pages of row
 // `row` of the table; its result goes to plane `plane` of part `part` (0: own, 1: prefix).
 struct Stretch {
     int32_t row, q0, n, plane, k0, k1, part, unused;
 };
-
-// A unit's keys: [lo, end) in `count` stretches, stretch i the part within [first + i * keys, first + (i + 1) *
-// keys), and, if sink1 > sink0, one more, [sink0, sink1), in the last plane.
-struct Keys {
-    int lo, end, sink0, sink1, first, keys, count;
-    __device__ __forceinline__ int stretches() const { return count + (sink1 > sink0 ? 1 : 0); }
-    __device__ __forceinline__ int begin(int i) const { return i < count ? max(lo, first + i * keys) : sink0; }
-    __device__ __forceinline__ int close(int i) const { return i < count ? min(end, first + (i + 1) * keys) : sink1; }
-};
-
-// planes: of a part; at most planes - 1 stretches and the sinks'.
-__device__ __forceinline__ Keys split_keys(int lo, int end, int sink0, int sink1, int planes) {
-    Keys k;
-    k.lo = lo;
-    k.end = end;
-    k.sink0 = sink0;
-    k.sink1 = sink1;
-    k.first = lo & ~15;
-    const int n = end - k.first, most = planes - 1;
-    k.keys = max(kStretchKeys, ((n + most - 1) / most + 15) & ~15);
-    k.count = (n + k.keys - 1) / k.keys;
-    return k;
-}
-
-// Keys at or past base of the unit of tokens ut * TT .. of sequence s.
-__device__ __forceinline__ Keys own_keys(const PagedArgs &a, const Seq &s, int base, int ut, int TT, int planes) {
-    const int t0 = s.p0 + ut * TT, t1 = s.p0 + min(s.n, (ut + 1) * TT) - 1;
-    const int lo = max(base, t0 >= a.window ? t0 - a.window + 1 : 0);
-    return split_keys(lo, t1 + 1, base, min(a.n_sink, lo), planes);
-}
-
-// Keys of a prefix.
-__device__ __forceinline__ Keys prefix_keys(const PagedArgs &a, int p0, int end, int planes) {
-    const int lo = p0 >= a.window ? p0 - a.window + 1 : 0;
-    return split_keys(lo, end, 0, min(a.n_sink, lo), planes);
-}
 
 // The results of both parts.  Rows of a part are [N, H_q] in each of `planes` planes (one, of the many-row kernel).
 struct PartResults {
@@ -61,6 +27,43 @@ struct PartResults {
     PagedWs ws;
     int ctas, rows, TQ, TT;
 };
+
+// A unit's keys: [lo, end) in `count` stretches, stretch i the part within [first + i * keys, first + (i + 1) *
+// keys), and, if sink1 > sink0, one more, [sink0, sink1), in the last plane.
+struct Keys {
+    int lo, end, sink0, sink1, first, keys, count;
+    __device__ __forceinline__ int stretches() const { return count + (sink1 > sink0 ? 1 : 0); }
+    __device__ __forceinline__ int begin(int i) const { return i < count ? max(lo, first + i * keys) : sink0; }
+    __device__ __forceinline__ int close(int i) const { return i < count ? min(end, first + (i + 1) * keys) : sink1; }
+};
+
+// At most p.planes - 1 stretches, and the sinks'.
+__device__ __forceinline__ Keys split_keys(int lo, int end, int sink0, int sink1, const PartResults &p) {
+    Keys k;
+    k.lo = lo;
+    k.end = end;
+    k.sink0 = sink0;
+    k.sink1 = sink1;
+    k.first = lo & ~15;
+    const int n = end - k.first, most = p.planes - 1;
+    k.keys = max(kStretchKeys, ((n + most - 1) / most + 15) & ~15);
+    k.count = (n + k.keys - 1) / k.keys;
+    return k;
+}
+
+// Keys at or past base of the unit of tokens ut * TT .. of sequence s.
+__device__ __forceinline__ Keys own_keys(const PagedArgs &a, const Seq &s, int base, int ut, int TT,
+                                         const PartResults &p) {
+    const int t0 = s.p0 + ut * TT, t1 = s.p0 + min(s.n, (ut + 1) * TT) - 1;
+    const int lo = max(base, t0 >= a.window ? t0 - a.window + 1 : 0);
+    return split_keys(lo, t1 + 1, base, min(a.n_sink, lo), p);
+}
+
+// Keys of a prefix.
+__device__ __forceinline__ Keys prefix_keys(const PagedArgs &a, int p0, int end, const PartResults &p) {
+    const int lo = p0 >= a.window ? p0 - a.window + 1 : 0;
+    return split_keys(lo, end, 0, min(a.n_sink, lo), p);
+}
 
 // Stretches on the list, groups with rows for the many-row kernel, stretches taken beyond each warp's first.
 enum { kStretches, kTileGroups, kTaken, kCounts };
