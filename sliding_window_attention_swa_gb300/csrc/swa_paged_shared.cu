@@ -8,7 +8,7 @@
 //      cores (paged_tile_kernel, kPrefix), or, where a group has at most 16 rows, stretches.
 //   3. own part: each sequence over the positions behind those: stretches (paged_rows_kernel), or, where a
 //      sequence has more than 16 rows, tiles again (paged_tile_kernel, kOwn).
-//   4. merge (here): the partial results of every row, all of them in fp32, are joined and rounded once.
+//   4. join (here): the partial results of every row, all of them in fp32, are joined and rounded once.
 // The kernels follow one another by programmatic dependence: the own part's blocks start where the
 // prefix part's have ended, without waiting for all of them.
 // With single tokens a group of R sequences reads its prefix once instead of R times, and its products go to
@@ -255,9 +255,11 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
 }
 
 // ---------------------------------------------------------------------------------------------
-// merge: a warp a row.  A row's results (m, l, acc), of its own part and of its group's prefix part, each in
-// planes or in the slots of the CTAs that share a unit, are joined: with M the largest m, o = sum 2^(m - M) acc /
-// sum 2^(m - M) l.  Bound by latency: the row's sequence, its group, then the maxima, then the values.
+// join: `kLanes` lanes a row, a warp the rows of a few heads of one token.  A row's results (m, l, acc), of its own
+// part and of its group's prefix part, each in planes or in the slots of the CTAs that share a unit, are joined:
+// with M the largest m, o = sum 2^(m - M) acc / sum 2^(m - M) l.  Bound by latency -- the row's sequence, its
+// units, the maxima, the values, each read from L2 or HBM behind the last --, so 8 lanes a row where there are
+// rows for every warp several times over (76000 rows of 128: 105 us with 32 lanes each), 32 where there are not.
 // ---------------------------------------------------------------------------------------------
 template <int E>
 __device__ __forceinline__ void load_columns(float (&x)[E], const float *src) {
@@ -273,15 +275,17 @@ __device__ __forceinline__ void load_columns(float (&x)[E], const float *src) {
     }
 }
 
-template <int D>
+template <int D, int kLanes>
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ SharedArgs sa) {
-    constexpr int E = D / 32;  // columns of a lane
+    // columns of a lane: kV neighbours in each of E / kV blocks of kLanes * kV
+    constexpr int E = D / kLanes, kV = E < 4 ? E : 4, kHeads = 32 / kLanes;
+    constexpr int kAtOnce = E <= 4 ? 12 : E <= 8 ? 8 : E <= 16 ? 4 : 2;  // results whose values are on their way at a time
     const PagedArgs &a = sa.a;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, part = lane % kLanes;
     const int64_t x = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int n = static_cast<int>(x / a.H_q), h = static_cast<int>(x % a.H_q), kvh = h / a.G;
-    if (n >= a.N) return;  // (the grid has blocks of whole rows; nothing waits for these warps)
-    const int b = find_sequence(a, n, lane);
+    const int blocks = (a.H_q + kHeads - 1) / kHeads;  // of a token's heads
+    const int n = static_cast<int>(x / blocks), h = static_cast<int>(x % blocks) * kHeads + lane / kLanes;
+    const int b = n < a.N ? find_sequence(a, n, lane) : -1;
     const Seq s = b >= 0 ? load_seq(a, b) : Seq{};
     if (b < 0 || !s.ok || n < s.q0 || n >= s.q0 + s.n) return;
     // (the plan's: the kernels before this one have waited for it before they let this grid start)
@@ -289,6 +293,8 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     const int4 u = __ldcg(info), v = __ldcg(info + 1);  // base, the group's tokens in tiles, in stretches, its first; its p0, number
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int base = u.x, i = n - s.q0;
+    const bool row_there = h < a.H_q;
+    const int head = row_there ? h : 0, kvh = head / a.G;
     // the parts: how many results, where
     struct Where {
         const PartResults *p;
@@ -298,10 +304,11 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     auto in_tiles = [&](const PartResults &p, int q0, int number) -> Where {
         const int tok = n - q0, ut = tok / p.TT, r = tok % p.TT;
         const int64_t at = (static_cast<int64_t>(q0 / p.TT) + number + ut) * a.H_kv + kvh;
-        const int2 u = __ldcg(p.units + at);
+        const int2 rec = __ldcg(p.units + at);
+        if (rec.y < 0) return Where{&p, 0, -1, 0, 0, false};  // the rows are final
         // (a unit that was never finished, after an expired wait, has any record)
-        if (u.y <= 0 || u.x < 0 || u.y > p.ctas || u.x > p.ctas - u.y) return Where{&p, 1, -1, 0, 0, false};
-        return Where{&p, u.y, -1, u.x, r / p.TQ * kTileRows + r % p.TQ * a.G + h % a.G, true};
+        if (rec.y == 0 || rec.x < 0 || rec.y > p.ctas || rec.x > p.ctas - rec.y) return Where{&p, 1, -1, 0, 0, false};
+        return Where{&p, rec.y, -1, rec.x, r / p.TQ * kTileRows + r % p.TQ * a.G + head % a.G, true};
     };
     auto in_planes = [&](const PartResults &p, const Keys &k) -> Where {
         return Where{&p, k.stretches(), k.count, 0, 0, false};
@@ -312,7 +319,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     else own = in_tiles(sa.part[0], s.q0, b);
     if (u.z > 0) pre = in_planes(sa.few_prefix, prefix_keys(a, v.x, base, sa.few_prefix));
     else if (u.y > 0) pre = in_tiles(sa.part[1], u.w, v.y);
-    const int64_t row = static_cast<int64_t>(n) * a.H_q + h, plane = static_cast<int64_t>(a.N) * a.H_q;
+    const int64_t row = static_cast<int64_t>(n) * a.H_q + head, plane = static_cast<int64_t>(a.N) * a.H_q;
     auto result = [&](int c, const float2 *&ml, const float *&o) {
         const bool first = c < own.count;
         const Where &w = first ? own : pre;
@@ -328,60 +335,76 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
             o = p.o + at * D;
         }
     };
-    const int count = own.count + pre.count;
-    constexpr int kAtOnce = E <= 4 ? 12 : 8;  // results whose values are on their way at a time
+    // (heads of a token have as many results each, but for those of units that several CTAs have)
+    const int count = !row_there || own.count == 0 ? 0 : own.count + pre.count;
+    const int most = __reduce_max_sync(0xffffffffu, count);
     float acc[E], m = -INFINITY, L = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int c0 = 0; c0 < count; c0 += 32) {
-        const int in = min(32, count - c0);
+    for (int c0 = 0; c0 < most; c0 += kLanes) {
+        const int in = min(kLanes, count - c0);
         float2 v2 = make_float2(-INFINITY, 0.f);
         const float *o = nullptr;
-        if (lane < in) {
+        if (part < in) {
             const float2 *ml;
-            result(c0 + lane, ml, o);
+            result(c0 + part, ml, o);
             v2 = __ldcg(ml);
         }
-        float x[kAtOnce][E];
+        float val[kAtOnce][E];
         auto load = [&](int k0) {
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
                 const auto src = reinterpret_cast<const float *>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (k0 + k) & 31));
-                if (k0 + k < in) load_columns<E>(x[k], src + lane * E);
-                else
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (k0 + k) % kLanes, kLanes));
+                float t[kV];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) x[k][e] = 0.f;
+                for (int e = 0; e < E; e += kV) {
+                    if (k0 + k < in) {
+                        load_columns<kV>(t, src + (e / kV * kLanes + part) * kV);
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < kV; ++z) t[z] = 0.f;
+                    }
+#pragma unroll
+                    for (int z = 0; z < kV; ++z) val[k][e + z] = t[z];
+                }
             }
         };
         load(0);
         float mn = fmaxf(m, v2.x);
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+        for (int d = kLanes / 2; d >= 1; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
         // (a result that kept nothing of this row has weight 0 and finite values)
         const float ms = mn == -INFINITY ? 0.f : mn, old = ex2(m - ms), f = ex2(v2.x - ms);
         L = L * old + f * v2.y;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] *= old;
         m = mn;
-        for (int k0 = 0; k0 < in; k0 += kAtOnce) {
+        for (int k0 = 0; k0 < min(kLanes, most - c0); k0 += kAtOnce) {
             if (k0 > 0) load(k0);
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
-                const float fk = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+                const float fk = __shfl_sync(0xffffffffu, f, (k0 + k) % kLanes, kLanes);
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] += fk * x[k][e];
+                for (int e = 0; e < E; ++e) acc[e] += fk * val[k][e];
             }
         }
     }
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-    if (!SWA_IN_BOUNDS(n < a.N && h < a.H_q && b < a.B, &g_shared_err)) return;
+    for (int d = kLanes / 2; d >= 1; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+    if (count == 0 || !SWA_IN_BOUNDS(n < a.N && head < a.H_q && b < a.B, &g_shared_err)) return;
     const float inv = 1.f / L;  // every row keeps its own key
-    uint16_t *op = a.o + n * a.o_st[0] + h * a.o_st[1] + lane * E;
+    uint16_t *op = a.o + n * a.o_st[0] + head * a.o_st[1];
 #pragma unroll
-    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(op + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0) {
+    for (int e = 0; e < E; e += kV) {
+        uint16_t *at = op + (e / kV * kLanes + part) * kV;
+        if constexpr (kV == 2)
+            *reinterpret_cast<uint32_t *>(at) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+        else
+            *reinterpret_cast<uint2 *>(at) = make_uint2(pack_bf16x2(acc[e] * inv, acc[e + 1] * inv),
+                                                        pack_bf16x2(acc[e + 2] * inv, acc[e + 3] * inv));
+    }
+    if (part == 0) {
         a.lse[row] = (m + log2f(L)) * 0.69314718055994531f;
         if (a.counts) a.counts[row] = kept_keys(a, s.p0 + i);
     }
@@ -462,14 +485,23 @@ cudaError_t launch_plan(SharedArgs &sa, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, paged_plan_kernel, sa);
 }
 
-cudaError_t launch_join(const SharedArgs &sa, cudaStream_t s) {
-    const int64_t blocks = (static_cast<int64_t>(sa.a.N) * sa.a.H_q + kWarps - 1) / kWarps;
+template <int D>
+cudaError_t launch_join_d(const SharedArgs &sa, cudaStream_t s) {
+    const int64_t rows = static_cast<int64_t>(sa.a.N) * sa.a.H_q;
+    const bool many = rows > static_cast<int64_t>(paged_sm_count()) * 128;
+    const int heads = many ? 4 : 1;  // of a warp
+    const int64_t warps = static_cast<int64_t>(sa.a.N) * ((sa.a.H_q + heads - 1) / heads);
+    const int64_t blocks = (warps + kWarps - 1) / kWarps;
     if (blocks > INT_MAX) return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned int>(blocks));
+    return launch_dependent(true, many ? paged_join_kernel<D, 8> : paged_join_kernel<D, 32>,
+                            dim3(static_cast<unsigned int>(blocks)), kThreads, 0, s, sa);
+}
+
+cudaError_t launch_join(const SharedArgs &sa, cudaStream_t s) {
     switch (sa.a.D) {
-        case 64: return launch_dependent(true, paged_join_kernel<64>, grid, kThreads, 0, s, sa);
-        case 128: return launch_dependent(true, paged_join_kernel<128>, grid, kThreads, 0, s, sa);
-        case 256: return launch_dependent(true, paged_join_kernel<256>, grid, kThreads, 0, s, sa);
+        case 64: return launch_join_d<64>(sa, s);
+        case 128: return launch_join_d<128>(sa, s);
+        case 256: return launch_join_d<256>(sa, s);
         default: return cudaErrorInvalidValue;
     }
 }

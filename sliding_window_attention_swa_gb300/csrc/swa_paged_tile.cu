@@ -871,8 +871,10 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             }
             const int unit_pieces = wk->pieces;
             const bool whole = unit_pieces == 0;
-            // (of a whole unit every row keeps its own key; a part's rows are joined with their others later)
-            const float inv_l = PT == Part::kAll && whole ? 1.f / l : 1.f;
+            // A whole unit's rows are final, but for those of a prefix part and those that have one; of a part that is not
+            // they are joined with the others later.  (A final row keeps its own key.)
+            const bool final = whole && (PT == Part::kAll || (PT == Part::kOwn && wk->base == 0));
+            const float inv_l = final ? 1.f / l : 1.f;
             wa *= inv_l;
             wb *= inv_l;
             const int tq = r / a.G, i0 = wk->ut * TT + (single ? 0 : ow * ta.TQ);  // the tile's first token
@@ -909,7 +911,7 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) f[e] += __uint_as_float(ov[e]) * wb;
                 }
-                if (store && (PT != Part::kAll || !whole)) {
+                if (store && !final) {
 #pragma unroll
                     for (int q8 = 0; q8 < 4; ++q8) {
                         uint32_t wv[8];
@@ -933,11 +935,11 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             if (lane == 0) mbar_arrive(bar_of(ow));
             bool joined = false;
             if constexpr (PT != Part::kAll) {
-                if (store) *(whole ? a.part_ml + tok * a.H_q + h : ml_at(pslot)) = make_float2(m, l);
-                // (every warp of every piece writes the same)
+                if (store && !final) *(whole ? a.part_ml + tok * a.H_q + h : ml_at(pslot)) = make_float2(m, l);
+                // (every warp of every piece writes the same; -1: the rows are final)
                 if (lane == 0)
                     a.part_units[(static_cast<int64_t>(wk->q0 / TT) + wk->b + wk->ut) * a.H_kv + wk->kvh] =
-                        make_int2(wk->owner, unit_pieces);
+                        make_int2(wk->owner, final ? -1 : unit_pieces);
             } else if (!whole) {
                 // The piece is written.  Warps of the same place have the same rows and columns of it in
                 // every CTA that shares the unit, so the last of them to arrive joins those: a row's
@@ -1010,9 +1012,9 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
                     }
                 }
             }
-            if (PT == Part::kAll && store && (!single || ow == 0) && (whole || joined)) {
+            if (store && (!single || ow == 0) && (final || joined)) {
                 a.lse[tok * a.H_q + h] = (m + log2f(l)) * 0.69314718055994531f;
-                if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, t);
+                if (a.counts) a.counts[tok * a.H_q + h] = kept_keys(a, t);  // (a final row's t counts from 0)
             }
             give_back(k);
             J += n;
