@@ -84,7 +84,7 @@ __device__ __forceinline__ void list_stretches(const SharedArgs &sa, const Keys 
         }
         t.k0 = k.begin(i);
         t.k1 = k.close(i);
-        t.plane = i < k.count ? i : sa.part[0].planes - 1;
+        t.plane = i < k.count ? i : (t.part ? sa.few_prefix : sa.part[0]).planes - 1;
         int4 *dst = reinterpret_cast<int4 *>(sa.stretches + at + i);
         dst[0] = make_int4(t.row, t.q0, t.n, t.plane);
         dst[1] = make_int4(t.k0, t.k1, t.part, 0);
@@ -428,11 +428,18 @@ Layout layout(const PagedArgs &a, int n_groups) {
     l.shape = paged_tile_shape(a);
     const int TT = kStretchRows / a.G;
     const int64_t units = std::min<int64_t>(a.N, static_cast<int64_t>(a.N) / TT + a.B);
-    // Stretches of a unit at most: about sixteen for every resident warp where units are few, two at least.
-    const int64_t want = (16 * static_cast<int64_t>(shared_rows_warps(a.D)) + units * a.H_kv - 1) / (units * a.H_kv);
-    l.planes = l.few ? static_cast<int>(std::min<int64_t>(std::max<int64_t>(want, 2), 128)) + 1 : 1;
-    l.prefix_planes = l.few ? l.planes : 0;
-    const int64_t cap = l.few ? units * l.planes + std::min<int64_t>(n_groups, a.N / 2 + 1) * l.planes : 0;
+    // Planes: the stretches that a unit of each part has at most, and the sinks'.  So many that there are six own
+    // stretches for every resident warp where all are as long as that, two of prefixes, whose results have more rows;
+    // two a unit at least.  (31 groups of up to 13 rows: 1, 2, 8, 24 prefix stretches a warp 130, 108, 124, 153 us;
+    // 64 histories of 4096 tokens that share nothing: 4, 6, 16 own ones 193, 194, 217 us.)
+    auto planes = [&](int64_t each, int64_t n) {
+        const int64_t want = (each * shared_rows_warps(a.D) + n * a.H_kv - 1) / (n * a.H_kv);
+        return static_cast<int>(std::min<int64_t>(std::max<int64_t>(want, 2), 128)) + 1;
+    };
+    const int64_t prefixes = std::max<int64_t>(std::min<int64_t>(n_groups, a.N / 2), 1);
+    l.planes = l.few ? planes(6, units) : 1;
+    l.prefix_planes = l.few ? planes(2, prefixes) : 0;
+    const int64_t cap = l.few ? units * l.planes + prefixes * l.prefix_planes : 0;
     l.cap = static_cast<int>(std::min<int64_t>(cap, INT_MAX / a.H_kv));
     size_t at = 0;
     auto take = [&](size_t bytes) {

@@ -420,3 +420,30 @@ def test_samples_of_one_prompt(swa):
             R.check(o[b:b + 1], lse[b:b + 1], cnt[b:b + 1], [t.cpu() for t in ref], f"step {step}, sample {b}")
         p0 = p0 + 1
     swa.swa_check_device_error()
+
+
+@pytest.mark.parametrize("hint", [0, 1])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_sequences_that_overlap(swa, D, hint):
+    """A q_start that goes up and down gives sequences rows that others have, too: work that ends, reported, nothing
+    outside the call's buffers, and the next call is right."""
+    x = Shared(50, [(300, [(300, 4)] * 60)], 4, 2, D, 16, lead=2, tail=3)
+    good = x.q_start.clone()
+    for wrong in (0, 1, 17, 100, x.N):
+        x.q_start[1::3] = wrong
+        o, lse, cnt, *_ = call(swa, x, max_q=hint)
+        st, words = swa.swa_read_device_errors()
+        assert st in (0, 1) and words["prefill"] == words["split"] == 0, words
+        assert (o[-3:] == 7).all() or wrong == x.N
+        x.q_start = good.clone()
+    run(swa, x, max_q=hint)
+
+
+def test_one_workspace_for_many_calls(swa):
+    """Calls one after the other in one workspace, whatever the last one left there: shapes, parts and hints change."""
+    ws = torch.empty(1 << 29, dtype=torch.uint8, device="cuda").fill_(0x5a)
+    xs = [(Shared(60, ONES, 8, 2, 128, 16), 1), (Shared(61, MIXED, 8, 2, 64, 32, 300, 5), 0),
+          (Shared(62, MIXED, 4, 2, 256, 64), 1), (Shared(63, ONES[2:3], 8, 2, 128, 16), 0), (Shared(64, MIXED, 16, 1, 128, 16), 0)]
+    for _ in range(2):
+        for x, hint in xs:
+            run(swa, x, max_q=hint, workspace=ws)
