@@ -667,11 +667,27 @@ def _new_rows(k_new, v_new, index: int, shape) -> tuple:
     return (k_new.data_ptr(), v_new.data_ptr()), st
 
 
-def _attend_args(q, k_pages, v_pages, page_table, p0, window, scale, q_start, n_sink, max_q, k_new, v_new, o, lse, row_counts,
-                 want_counts):
-    """(device index, swa_paged_params (None: no rows), swa_paged_cache, o, lse, row_counts), checked."""
+def swa_paged_attend(q, k_pages, v_pages, page_table, p0, window: int = 0, scale: float | None = None, *, q_start=None,
+                     n_sink: int = 0, max_q: int = 0, k_new=None, v_new=None, o=None, lse=None, row_counts=None,
+                     want_counts: bool = False, workspace=None, stream=None, _group_start=None):
+    """Attention of new tokens over a paged cache: q [N,H_q,d] (bf16, any token and head strides),
+    pools [n_pages,H_kv,page_size,d], page_table int32 [B,table_width], p0 int32 [B].
+
+    Rows q_start[b] .. q_start[b+1]-1 (int32 [B+1]; None: one row a sequence) are sequence b's
+    new tokens at positions p0[b] + i; the query at position t keeps the keys at positions s <= t
+    with s > t - window (window 0: all) or s < n_sink.  k_new, v_new [N,H_kv,d]: stored in their
+    pages first.  max_q: the most new tokens of one sequence if known (a hint; without it a
+    batch with q_start goes to the kernel for many rows, which mostly takes 6 to 14% longer for
+    one token a sequence).  Rows outside every sequence keep what o, lse and row_counts hold.
+    Returns (o [N,H_q,d] bf16, lse [N,H_q] fp32, row_counts [N,H_q] int32 or None).
+    """
     import torch
 
+    if stream is not None:
+        return _on(stream, swa_paged_attend, q, k_pages, v_pages, page_table, p0, window, scale, q_start=q_start,
+                   n_sink=n_sink, max_q=max_q, k_new=k_new, v_new=v_new, o=o, lse=lse, row_counts=row_counts,
+                   want_counts=want_counts, workspace=workspace, _group_start=_group_start)
+    lib = load_library()
     if q.dim() != 3:
         raise ValueError("q: expected [N, H_q, d]")
     N, Hq, D = shape = q.shape
@@ -693,51 +709,39 @@ def _attend_args(q, k_pages, v_pages, page_table, p0, window, scale, q_start, n_
     elif row_counts.dtype is not torch.int32 or row_counts.get_device() != index or row_counts.shape != (N, Hq) or \
             not row_counts.is_contiguous():
         raise _i32_wrong("row_counts", (N, Hq), index)
-    params = None if N == 0 else _packed(
+    n_groups = 0
+    if _group_start is not None:  # (the call is swa_paged_attend_shared)
+        if _group_start.dim() != 1 or _group_start.shape[0] < 2:
+            raise ValueError("group_start: expected int32 [n_groups + 1], one group at least")
+        _lists(index, ("group_start", _group_start, _group_start.shape))
+        n_groups = _int32("n_groups", _group_start.shape[0] - 1)
+    if N == 0:
+        return o, lse, row_counts
+    params = _packed(
         _PAGED_PARAMS, q.data_ptr(), *new, p0.data_ptr(), 0 if q_start is None else q_start.data_ptr(), *q_st,
         *new_st, *o_st, N, Hq, int(max_q), int(window), int(n_sink), D ** -0.5 if scale is None else float(scale),
         o.data_ptr(), lse.data_ptr(), 0 if row_counts is None else row_counts.data_ptr())
-    return index, params, cache, o, lse, row_counts
-
-
-def swa_paged_attend(q, k_pages, v_pages, page_table, p0, window: int = 0, scale: float | None = None, *, q_start=None,
-                     n_sink: int = 0, max_q: int = 0, k_new=None, v_new=None, o=None, lse=None, row_counts=None,
-                     want_counts: bool = False, workspace=None, stream=None):
-    """Attention of new tokens over a paged cache: q [N,H_q,d] (bf16, any token and head strides),
-    pools [n_pages,H_kv,page_size,d], page_table int32 [B,table_width], p0 int32 [B].
-
-    Rows q_start[b] .. q_start[b+1]-1 (int32 [B+1]; None: one row a sequence) are sequence b's
-    new tokens at positions p0[b] + i; the query at position t keeps the keys at positions s <= t
-    with s > t - window (window 0: all) or s < n_sink.  k_new, v_new [N,H_kv,d]: stored in their
-    pages first.  max_q: the most new tokens of one sequence if known (a hint; without it a
-    batch with q_start goes to the kernel for many rows, which mostly takes 6 to 14% longer for
-    one token a sequence).  Rows outside every sequence keep what o, lse and row_counts hold.
-    Returns (o [N,H_q,d] bf16, lse [N,H_q] fp32, row_counts [N,H_q] int32 or None).
-    """
-    import torch
-
-    if stream is not None:
-        return _on(stream, swa_paged_attend, q, k_pages, v_pages, page_table, p0, window, scale, q_start=q_start,
-                   n_sink=n_sink, max_q=max_q, k_new=k_new, v_new=v_new, o=o, lse=lse, row_counts=row_counts,
-                   want_counts=want_counts, workspace=workspace)
-    lib = load_library()
-    index, params, cache, o, lse, row_counts = _attend_args(
-        q, k_pages, v_pages, page_table, p0, window, scale, q_start, n_sink, max_q, k_new, v_new, o, lse, row_counts,
-        want_counts)
-    if params is None:
-        return o, lse, row_counts
-    if workspace is None:
+    if workspace is not None:
+        _own_workspace(workspace, index)
+    elif n_groups:
+        workspace = torch.empty(lib.swa_paged_shared_workspace_size(params, cache, n_groups) or 1, dtype=torch.uint8,
+                                device=device)
+    else:
         # (asked once for each of what it depends on: the question takes 2 us of a 24 us call; more than
         # 16 tokens a sequence are many rows for every group, so a longer chunk is no other key)
-        key = lib._name, index, q.shape[1], k_pages.shape[1], q.shape[2], min(max_q, 17), q_start is None
+        key = lib._name, index, Hq, H_kv, d_h, min(max_q, 17), q_start is None
         size = _paged_ws_size.get(key)
         if size is None:
             size = lib.swa_paged_workspace_size(params, cache)
             if size:  # (0: refused, below)
                 _paged_ws_size[key] = size
-        workspace = torch.empty(size or 1, dtype=torch.uint8, device=q.device)
-    else:
-        _own_workspace(workspace, index)
+        workspace = torch.empty(size or 1, dtype=torch.uint8, device=device)
+    if n_groups:
+        st = lib.swa_paged_attend_shared(params, cache, _group_start.data_ptr(), n_groups, workspace.data_ptr(),
+                                         workspace.numel() * workspace.element_size(), _raw_stream(index))
+        if st != 0:
+            raise SwaError("swa_paged_attend_shared", st)
+        return o, lse, row_counts
     st = lib.swa_paged_attend(params, cache, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                               _raw_stream(index))
     if st != 0:
@@ -753,32 +757,11 @@ def swa_paged_attend_shared(q, k_pages, v_pages, page_table, p0, group_start, wi
     .. group_start[g+1]-1 (int32 [n_groups+1]) are a group.  What they share is found from their rows of
     page_table, so a group that shares little or nothing is as right; sequences of no group are computed alone.
     Arguments and results as swa_paged_attend."""
-    import torch
-
-    if stream is not None:
-        return _on(stream, swa_paged_attend_shared, q, k_pages, v_pages, page_table, p0, group_start, window, scale,
-                   q_start=q_start, n_sink=n_sink, max_q=max_q, k_new=k_new, v_new=v_new, o=o, lse=lse,
-                   row_counts=row_counts, want_counts=want_counts, workspace=workspace)
-    lib = load_library()
-    index, params, cache, o, lse, row_counts = _attend_args(
-        q, k_pages, v_pages, page_table, p0, window, scale, q_start, n_sink, max_q, k_new, v_new, o, lse, row_counts,
-        want_counts)
-    if group_start.dim() != 1 or group_start.shape[0] < 2:
+    if group_start is None:
         raise ValueError("group_start: expected int32 [n_groups + 1], one group at least")
-    _lists(index, ("group_start", group_start, group_start.shape))
-    if params is None:
-        return o, lse, row_counts
-    n_groups = _int32("n_groups", group_start.shape[0] - 1)
-    if workspace is None:
-        size = lib.swa_paged_shared_workspace_size(params, cache, n_groups)
-        workspace = torch.empty(size or 1, dtype=torch.uint8, device=q.device)
-    else:
-        _own_workspace(workspace, index)
-    st = lib.swa_paged_attend_shared(params, cache, group_start.data_ptr(), n_groups, workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _raw_stream(index))
-    if st != 0:
-        raise SwaError("swa_paged_attend_shared", st)
-    return o, lse, row_counts
+    return swa_paged_attend(q, k_pages, v_pages, page_table, p0, window, scale, q_start=q_start, n_sink=n_sink,
+                            max_q=max_q, k_new=k_new, v_new=v_new, o=o, lse=lse, row_counts=row_counts,
+                            want_counts=want_counts, workspace=workspace, stream=stream, _group_start=group_start)
 
 
 def swa_paged_append(k_pages, v_pages, page_table, k_new, v_new, p0, *, q_start=None, stream=None) -> None:
