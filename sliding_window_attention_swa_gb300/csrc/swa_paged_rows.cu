@@ -78,7 +78,6 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D>::CTAS_PER_SM)
     if (!behind_tiles) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    const int n_items = min(__ldcg(sa.counts + kStretches), sa.cap) * a.H_kv;
     // A warp's first is its own, the next ones go to whichever warp is free (results do not depend on which).
     const int firsts = static_cast<int>(gridDim.x) * kWarps;
     auto take = [&]() -> int {
@@ -87,10 +86,14 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D>::CTAS_PER_SM)
         return firsts + __shfl_sync(0xffffffffu, x, 0);
     };
     // Neighbouring warps take the heads of one stretch, which lie side by side in its pages.
+    // Prefixes first: theirs are the longer ones.
+    const int n_prefix = min(__ldcg(sa.counts + kPrefixStretches), sa.prefix_cap);
+    const int n_items = (n_prefix + min(__ldcg(sa.counts + kOwnStretches), sa.own_cap)) * a.H_kv;
     auto load_work = [&](int item) -> Work {
         Work w{};
         if (item < n_items) {
-            const int4 *p = reinterpret_cast<const int4 *>(sa.stretches + item / a.H_kv);
+            const int e = item / a.H_kv;
+            const int4 *p = reinterpret_cast<const int4 *>(sa.stretches + (e < n_prefix ? e : sa.prefix_cap + e - n_prefix));
             const int4 x = __ldcg(p), y = __ldcg(p + 1);
             w.row = x.x, w.q0 = x.y, w.n = x.z, w.plane = x.w, w.k0 = y.x, w.k1 = y.y, w.part = y.z;
             w.kvh = item % a.H_kv;
@@ -106,6 +109,8 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D>::CTAS_PER_SM)
         const int key = w.first + from * KS + lane * box;
         return from < w.steps && key < w.k1 && key + box > w.k0 ? page_of(a, w.row, key >> a.ps_log2) : -1;
     };
+    // what is streamed once leaves L2 before the parts' results do
+    const uint64_t policy = l2_evict_first();
     int issued = 0, taken = 0;  // steps copied and used so far
     bool ok = true;
     auto issue = [&](const Work &w, int i, int pages) {
@@ -120,13 +125,14 @@ __global__ void __launch_bounds__(kThreads, RowsCfg<D>::CTAS_PER_SM)
             // debug build: the box lies in the page, the head exists
             (void)SWA_IN_BOUNDS(row + box <= a.ps && w.kvh < a.H_kv && page <= a.n_pages, &g_rows_err);
             tma_load_4d(ring + st * C::STAGE + v * (C::STAGE / 2) + j * box * D * 2, v ? &tm_v : &tm_k, bar(st), 0, 0, 0,
-                        ((page < 0 ? a.n_pages : page) * a.H_kv + w.kvh) * (a.ps >> 3) + (row >> 3));
+                        ((page < 0 ? a.n_pages : page) * a.H_kv + w.kvh) * (a.ps >> 3) + (row >> 3), policy);
         }
         __syncwarp();
         ++issued;
     };
 
-    Work w = load_work(static_cast<int>(blockIdx.x) * kWarps + warp);
+    const int own = static_cast<int>(blockIdx.x) * kWarps + warp;
+    Work w = load_work(own);
     int pages = pages_of(w, 0), at = 0;  // at: steps of w that are issued
     const int r0 = lane >> 2, r1 = r0 + 8, kq = 2 * (lane & 3);
     while (ok && w.steps > 0) {

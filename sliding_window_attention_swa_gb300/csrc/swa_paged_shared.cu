@@ -31,7 +31,7 @@ __device__ unsigned int g_shared_err = 0;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kFewGroups = 32;  // below it a cluster plans a group, else a block
 constexpr int kCluster = 8;
-constexpr int kChunk = 256;  // entries that a warp compares at a time: eight loads a lane and row in flight
+constexpr int kChunk = 512;  // entries that a warp compares at a time: sixteen loads a lane and row in flight
 
 // Shared positions below which a group is computed as none: a part of its own costs more than they do.
 constexpr int kLeastShared = 64;
@@ -64,68 +64,67 @@ __device__ __forceinline__ Members shuffled(const Members &x, int o) {
 // says of the tables: a group that shares nothing is computed as if it were none.
 // Bound by latency: the list, the sequences' lengths, then the table's rows, all of them once.
 // ---------------------------------------------------------------------------------------------
-// Puts the stretches of the warp's units (a unit a lane, `count` of them, of keys k) on the list.
-__device__ __forceinline__ void list_stretches(const SharedArgs &sa, const Keys &k, int count, Stretch t) {
-    const int lane = threadIdx.x & 31;
-    int inc = count;
+// Puts the stretches of a warp's units on the list: `lanes` lanes have a unit, `count` stretches of keys k.
+__device__ __forceinline__ void list_stretches(const SharedArgs &sa, const Keys &k, int count, Stretch t, int lanes) {
+    const int lane = threadIdx.x & 31, sub = lane & (lanes - 1);
+    const int mine = sub == 0 ? count : 0;
+    int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += x;
     }
     int at = 0;
-    if (lane == 31 && inc > 0) at = atomicAdd(sa.counts + kStretches, inc);
-    at = __shfl_sync(0xffffffffu, at, 31) + inc - count;
-    for (int i = 0; i < count; ++i) {
+    if (lane == 31 && inc > 0) at = atomicAdd(sa.counts + (t.part ? kPrefixStretches : kOwnStretches), inc);
+    at = __shfl_sync(0xffffffffu, at, 31) + __shfl_sync(0xffffffffu, inc - mine, lane - sub);
+    for (int i = sub; i < count; i += lanes) {
         // (more than there is room for: sequences that overlap, from a q_start that goes down)
-        if (at + i >= sa.cap) {
+        if (at + i >= (t.part ? sa.prefix_cap : sa.own_cap)) {
             atomicOr(&g_shared_err, SWA_DEVERR_BAD_POSITION);
             break;
         }
         t.k0 = k.begin(i);
         t.k1 = k.close(i);
         t.plane = i < k.count ? i : (t.part ? sa.few_prefix : sa.part[0]).planes - 1;
-        int4 *dst = reinterpret_cast<int4 *>(sa.stretches + at + i);
+        int4 *dst = reinterpret_cast<int4 *>(sa.stretches + (t.part ? 0 : sa.prefix_cap) + at + i);
         dst[0] = make_int4(t.row, t.q0, t.n, t.plane);
         dst[1] = make_int4(t.k0, t.k1, t.part, 0);
     }
 }
 
-// What the other kernels need to know of sequences b0 .. b1 - 1 (of group g): a warp of `warps` has every 32nd, number `w` of them.
+// What the other kernels need to know of sequences b0 .. b1 - 1 (of group g), by `warps` warps, of which this is
+// number w; a warp has as many sequences at a time as leave none to another turn, 32 at most.
 __device__ __forceinline__ void put_sequences(const SharedArgs &sa, int b0, int b1, const PagedGroup &group, int g, int w,
                                               int warps) {
     const PagedArgs &a = sa.a;
-    const int lane = threadIdx.x & 31, TT = kStretchRows / a.G, base = group.end;
-    for (int first = b0 + w * 32; first < b1; first += warps * 32) {
-        const int b = first + lane;
+    const int TT = kStretchRows / a.G, base = group.end;
+    int each = 1;
+    while (each < 32 && each * warps < b1 - b0) each *= 2;
+    const int lane = threadIdx.x & 31, lanes = 32 / each, sub = lane & (lanes - 1);
+    for (int first = b0 + w * each; first < b1; first += warps * each) {
+        const int b = first + lane / lanes;
         Seq s{};
         if (b < b1) {
             s = load_seq(a, b);
             if (!s.ok) atomicOr(&g_shared_err, SWA_DEVERR_BAD_POSITION);
-            // (a sequence without new tokens may end inside what the others share)
-            if (!sa.few) sa.base[b] = s.n > 0 ? base : 0;
-            int4 *info = sa.info + 2 * static_cast<int64_t>(b);
-            info[0] = s.n > 0 ? make_int4(base, group.n, group.few, group.q0) : make_int4(0, 0, 0, 0);
-            info[1] = make_int4(group.p0, g, 0, 0);
-        }
-        const int longest = __reduce_max_sync(0xffffffffu, s.n);
-        if (sa.few || (base > 0 && a.window != INT_MAX)) {  // the rows' positions
-            if (longest <= 8) {
-                for (int i = 0; i < s.n; ++i) sa.pos[s.q0 + i] = s.p0 + i;
-            } else {
-                for (int l = 0; l < 32; ++l) {
-                    const int n = __shfl_sync(0xffffffffu, s.n, l), q0 = __shfl_sync(0xffffffffu, s.q0, l),
-                              p0 = __shfl_sync(0xffffffffu, s.p0, l);
-                    for (int i = lane; i < n; i += 32) sa.pos[q0 + i] = p0 + i;
-                }
+            if (sub == 0) {
+                // (a sequence without new tokens may end inside what the others share)
+                if (!sa.few) sa.base[b] = s.n > 0 ? base : 0;
+                int4 *info = sa.info + 2 * static_cast<int64_t>(b);
+                info[0] = s.n > 0 ? make_int4(base, group.n, group.few, group.q0) : make_int4(0, 0, 0, 0);
+                info[1] = make_int4(group.p0, g, 0, 0);
             }
         }
+        if (sa.few || (base > 0 && a.window != INT_MAX))  // the rows' positions
+            for (int i = sub; i < s.n; i += lanes)
+                if (SWA_IN_BOUNDS(s.q0 + i < a.N, &g_shared_err)) sa.pos[s.q0 + i] = s.p0 + i;
         if (!sa.few) continue;
+        const int longest = __reduce_max_sync(0xffffffffu, s.n);
         for (int ut = 0; ut * TT < longest; ++ut) {
             const bool unit = ut * TT < s.n;
             const Keys k = unit ? own_keys(a, s, base, ut, TT, sa.part[0]) : Keys{};
             list_stretches(sa, k, unit ? k.stretches() : 0,
-                           Stretch{b, s.q0 + ut * TT, min(TT, s.n - ut * TT), 0, 0, 0, 0, 0});
+                           Stretch{b, s.q0 + ut * TT, min(TT, s.n - ut * TT), 0, 0, 0, 0, 0}, lanes);
         }
     }
 }
@@ -146,6 +145,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         return;
     }
     if (clusters == 1 && rank == 0 && tid < kCounts) sa.counts[tid] = 0;  // (seen by the cluster behind its first barrier)
+    const int first_b = __ldg(sa.group_start), end_b = __ldg(sa.group_start + sa.n_groups);
     bool fine = true;
     for (int i = tid; i < sa.n_groups; i += kThreads) {
         const int b0 = __ldg(sa.group_start + i), b1 = __ldg(sa.group_start + i + 1);
@@ -194,22 +194,24 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
                 const int i0 = static_cast<int>(t % chunks) * kChunk, b = b0 + static_cast<int>(t / chunks);
                 if (i0 >= differs || b == leader) continue;
                 const Seq s = load_seq(a, b);
-                if (s.n == 0) continue;
                 const int my_lo = s.p0 >= a.window ? s.p0 - a.window + 1 : 0;
                 const int32_t *row = a.table + static_cast<int64_t>(b) * a.width;
                 int x[kChunk / 32], y[kChunk / 32];
 #pragma unroll
                 for (int k = 0; k < kChunk / 32; ++k) {
                     const int i = i0 + k * 32 + lane, j = i < sinks ? i : e_lo + i - sinks;
-                    // (needed: some position of the entry is in reach of the sequence's first new token, or a sink)
-                    const bool needed = i < n && ((static_cast<int64_t>(j) + 1) << a.ps_log2 > my_lo || j < e_sink) &&
-                                        SWA_IN_BOUNDS(j >= 0 && j < a.width, &g_shared_err);
-                    x[k] = needed ? __ldg(row0 + j) : 0;
-                    y[k] = needed ? __ldg(row + j) : 0;
+                    const bool in = i < n && SWA_IN_BOUNDS(j >= 0 && j < a.width, &g_shared_err);
+                    x[k] = in ? __ldg(row0 + j) : 0;
+                    y[k] = in ? __ldg(row + j) : 0;
                 }
+                if (s.n == 0) continue;
 #pragma unroll
-                for (int k = kChunk / 32 - 1; k >= 0; --k)
-                    if (x[k] != y[k]) differs = min(differs, i0 + k * 32 + lane);
+                for (int k = kChunk / 32 - 1; k >= 0; --k) {
+                    const int i = i0 + k * 32 + lane, j = i < sinks ? i : e_lo + i - sinks;
+                    // (needed: some position of the entry is in reach of the sequence's first new token, or a sink)
+                    const bool needed = (static_cast<int64_t>(j) + 1) << a.ps_log2 > my_lo || j < e_sink;
+                    if (x[k] != y[k] && needed) differs = min(differs, i);
+                }
             }
             differs = __reduce_min_sync(0xffffffffu, differs);
             if (ranks > 1) cluster.barrier_wait();
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
             }
             if (out.few > 0) {
                 const Keys k = prefix_keys(a, p0, base, sa.few_prefix);
-                list_stretches(sa, k, lane == 0 ? k.stretches() : 0, Stretch{leader, out.q0, out.few, 0, 0, 0, 1, 0});
+                list_stretches(sa, k, k.stretches(), Stretch{leader, out.q0, out.few, 0, 0, 0, 1, 0}, 32);
             }
         }
         put_sequences(sa, b0, b1, out, g, rank * kWarps + warp, ranks * kWarps);
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         else __syncthreads();
     }
     if (c == 0) {  // sequences of no group
-        const int lo = fine ? __ldg(sa.group_start) : a.B, hi = fine ? __ldg(sa.group_start + sa.n_groups) : a.B;
+        const int lo = fine ? first_b : a.B, hi = fine ? end_b : a.B;
         put_sequences(sa, 0, lo, PagedGroup{}, -1, rank * kWarps + warp, ranks * kWarps);
         put_sequences(sa, hi, a.B, PagedGroup{}, -1, rank * kWarps + warp, ranks * kWarps);
     }
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
 // ---------------------------------------------------------------------------------------------
 struct Layout {
     bool few, tiles;  // tiles: prefixes may go to the many-row kernel
-    int planes, prefix_planes, cap;
+    int planes, prefix_planes, own_cap, prefix_cap;
     PagedShape shape;  // of the many-row kernel
     size_t slots[2], base, info, groups, pos, count, list, units[2], ml[2], o[2], few_ml, few_o, bytes;
 };
@@ -439,8 +441,9 @@ Layout layout(const PagedArgs &a, int n_groups) {
     const int64_t prefixes = std::max<int64_t>(std::min<int64_t>(n_groups, a.N / 2), 1);
     l.planes = l.few ? planes(6, units) : 1;
     l.prefix_planes = l.few ? planes(2, prefixes) : 0;
-    const int64_t cap = l.few ? units * l.planes + prefixes * l.prefix_planes : 0;
-    l.cap = static_cast<int>(std::min<int64_t>(cap, INT_MAX / a.H_kv));
+    const int64_t most = INT_MAX / 2 / a.H_kv;  // (the items of both, a head each, are counted in 32 bits)
+    l.own_cap = l.few ? static_cast<int>(std::min(units * l.planes, most)) : 0;
+    l.prefix_cap = l.few ? static_cast<int>(std::min(prefixes * l.prefix_planes, most)) : 0;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t x = at;
@@ -465,7 +468,7 @@ Layout layout(const PagedArgs &a, int n_groups) {
     l.groups = take(static_cast<size_t>(n_groups) * sizeof(PagedGroup));
     l.pos = take(static_cast<size_t>(a.N) * 4);
     l.count = take(kCounts * 4);
-    l.list = take(static_cast<size_t>(l.cap) * sizeof(Stretch));
+    l.list = take((static_cast<size_t>(l.prefix_cap) + l.own_cap) * sizeof(Stretch));
     l.bytes = at;
     return l;
 }
@@ -533,7 +536,8 @@ cudaError_t launch_paged_shared(const PagedArgs &a, const int32_t *group_start, 
     sa.pos = reinterpret_cast<int32_t *>(p + l.pos);
     sa.stretches = reinterpret_cast<Stretch *>(p + l.list);
     sa.counts = reinterpret_cast<int32_t *>(p + l.count);
-    sa.cap = l.cap;
+    sa.own_cap = l.own_cap;
+    sa.prefix_cap = l.prefix_cap;
     sa.few = l.few;
     sa.any_tiles = l.tiles;
     sa.prefix_tokens = sa.own_tokens = l.shape.TQ;

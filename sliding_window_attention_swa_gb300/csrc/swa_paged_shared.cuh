@@ -65,8 +65,8 @@ __device__ __forceinline__ Keys prefix_keys(const PagedArgs &a, int p0, int end,
     return split_keys(lo, end, 0, min(a.n_sink, lo), p);
 }
 
-// Stretches on the list, groups with rows for the many-row kernel, stretches taken beyond each warp's first.
-enum { kStretches, kTileGroups, kTaken, kCounts };
+// Stretches on the lists, groups with rows for the many-row kernel, stretches taken beyond each warp's first.
+enum { kOwnStretches, kPrefixStretches, kTileGroups, kTaken, kCounts };
 
 struct SharedArgs {
     PagedArgs a;
@@ -76,10 +76,10 @@ struct SharedArgs {
     int32_t *base;             // [B]
     int4 *info;                // [B][2]: base, its group's n, few, q0; p0, the group's number
     int32_t *pos;              // [N]
-    Stretch *stretches;        // [cap]
+    Stretch *stretches;        // [prefix_cap + own_cap]: prefixes', then own ones
     int32_t *counts;           // [kCounts]
     int clusters;              // of the plan
-    int cap;
+    int prefix_cap, own_cap;
     int few;                   // own parts (and prefixes of few rows) are cut into stretches
     int any_tiles;             // prefixes may go to the many-row kernel
     int prefix_tokens, own_tokens;  // tokens of a query tile of the many-row kernel

@@ -134,6 +134,7 @@ struct TileArgs {
     int TT;             // tokens per unit: TQ or (head dim 128) 2 * TQ
     int min_tiles;      // least share of a CTA
     int o_align32;      // o and its strides are 32-byte aligned: rows stored 32 bytes at a time
+    int read_once;        // prefix part: few query tiles read a key
     int fault_stop_fill;  // planted fault: no ring fill numbered at or past this (INT_MAX: off)
 };
 
@@ -381,6 +382,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         // chunks of 2048 tokens behind 30000 1017 -> 1097 us.)
         const CUtensorMap *map = values ? &tm_v : &tm_k;
         const uint32_t my_off = sRing + static_cast<uint32_t>(lane * box * D * 2);
+        // (a prefix that few CTAs read leaves L2 before the parts' results do)
+        const uint64_t policy = PT == Part::kPrefix && ta.read_once ? l2_evict_first() : l2_evict_normal();
         Group now{0, 0, 0, 0, false, -1}, then = now;
         if (cta_tiles > 0) then = look_up();
         int at = 0, group8 = 0;  // next tile of the group; this lane's box as a group of eight rows of the pool
@@ -421,7 +424,12 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             const int from = __shfl_sync(0xffffffffu, group8, (at * npg + lane) & 31);
             ++at;
             ok = ok && take_slot(C::TBYTES);
-            if (ok && lane < npg) tma_load_4d(my_off + slot * C::TBYTES, map, bar_full(slot), 0, 0, 0, from);
+            if (ok && lane < npg) {
+                if constexpr (PT == Part::kPrefix)
+                    tma_load_4d(my_off + slot * C::TBYTES, map, bar_full(slot), 0, 0, 0, from, policy);
+                else
+                    tma_load_4d(my_off + slot * C::TBYTES, map, bar_full(slot), 0, 0, 0, from);
+            }
             __syncwarp();
             if (ok) skip_fills(2);
         }
@@ -1151,6 +1159,7 @@ cudaError_t launch_part(const PagedArgs &a, const PagedWs &w, bool dependent, cu
     t.TT = paged_tile_tokens(a, PT);
     t.min_tiles = PT == Part::kPrefix ? 2 : 4;
     t.o_align32 = reinterpret_cast<uintptr_t>(a.o) % 32 == 0 && a.o_st[0] % 16 == 0 && a.o_st[1] % 16 == 0;
+    t.read_once = PT == Part::kPrefix && a.N <= 4 * t.TT;
     t.fault_stop_fill = fault_plan().band_stop_fill;
     return launch_dependent(dependent, paged_tile_kernel<D, PT>, dim3(x.ctas), C::THREADS, C::SMEM, s, mq, mk, mv, t);
 }
