@@ -23,16 +23,20 @@ namespace {
 __device__ unsigned int g_rows_err = 0;   // waits and bounds
 __device__ unsigned int g_rows_data = 0;  // broken device data
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
 
 template <int D>
 struct RowsCfg {
     static constexpr int KS = D == 64 ? 32 : 16;  // keys a step
     static constexpr int STAGE = 2 * KS * D * 2;  // keys and values of a step
-    static constexpr int NST = D == 64 ? 2 : 3;
+    // A ring a warp: more warps or deeper rings, as shared memory allows both.  Drafts of 256-wide heads with one block of
+    // four warps and three steps each 100 us, two of three warps and two steps 96, one of seven and two 95; 31 small groups of
+    // 64-wide heads (three blocks of four, two steps) 102, four of four and three steps of 16 keys 112; 64 sequences of
+    // 128-wide ones (two of four, three steps) 73, three of four and two 76.
+    static constexpr int NST = D == 128 ? 3 : 2;
+    static constexpr int WARPS = D <= 128 ? 4 : 7;
     static constexpr int CTAS_PER_SM = D <= 64 ? 3 : D <= 128 ? 2 : 1;
-    static constexpr int OFF_BAR = kWarps * NST * STAGE;
-    static constexpr int SMEM = OFF_BAR + kWarps * NST * 8 + 1024;
+    static constexpr int OFF_BAR = WARPS * NST * STAGE;
+    static constexpr int SMEM = OFF_BAR + WARPS * NST * 8 + 1024;
     static_assert((SMEM + 1024) * CTAS_PER_SM <= 233472, "shared memory budget");
 };
 
@@ -48,11 +52,11 @@ struct Work : Stretch {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, RowsCfg<D>::CTAS_PER_SM)
+__global__ void __launch_bounds__(RowsCfg<D>::WARPS * 32, RowsCfg<D>::CTAS_PER_SM)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ SharedArgs sa, const int behind_tiles, const int fault_stop) {
     using C = RowsCfg<D>;
-    constexpr int NST = C::NST, KS = C::KS;
+    constexpr int NST = C::NST, KS = C::KS, kWarps = C::WARPS;
     const PagedArgs &a = sa.a;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int abort_flag;
@@ -320,15 +324,16 @@ cudaError_t launch_d(const SharedArgs &sa, bool behind_tiles, cudaStream_t s) {
     const int box = std::min(sa.a.ps, C::KS);
     if (!paged_pool_map(&mk, sa.a, sa.a.k_pages, box) || !paged_pool_map(&mv, sa.a, sa.a.v_pages, box))
         return cudaErrorInvalidValue;
-    return launch_dependent(true, paged_rows_kernel<D>, dim3(paged_sm_count() * C::CTAS_PER_SM), kThreads, C::SMEM, s, mk,
+    return launch_dependent(true, paged_rows_kernel<D>, dim3(paged_sm_count() * C::CTAS_PER_SM), C::WARPS * 32, C::SMEM, s, mk,
                             mv, sa, static_cast<int>(behind_tiles), fault_plan().split_stop_stage);
 }
 
 }  // namespace
 
 int shared_rows_warps(int D) {
-    return paged_sm_count() * kWarps *
-           (D <= 64 ? RowsCfg<64>::CTAS_PER_SM : D <= 128 ? RowsCfg<128>::CTAS_PER_SM : RowsCfg<256>::CTAS_PER_SM);
+    return paged_sm_count() * (D <= 64    ? RowsCfg<64>::CTAS_PER_SM * RowsCfg<64>::WARPS
+                               : D <= 128 ? RowsCfg<128>::CTAS_PER_SM * RowsCfg<128>::WARPS
+                                          : RowsCfg<256>::CTAS_PER_SM * RowsCfg<256>::WARPS);
 }
 
 cudaError_t launch_shared_rows(const SharedArgs &sa, bool behind_tiles, cudaStream_t s) {
