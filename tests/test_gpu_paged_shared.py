@@ -71,10 +71,11 @@ class Shared(R.Batch):
             self.v_new[starts[b]:starts[b] + n] = self.vals[b][p:]
             lo = max(0, p - window + 1) if window else 0
             for j, x in rows[b]:
-                for t in range(j * ps, min((j + 1) * ps, p + n)):
-                    if n and (t >= lo or t < n_sink) or junk == 0:
-                        self.k_pages[place[x], :, t % ps] = self.keys[b][t]
-                        self.v_pages[place[x], :, t % ps] = self.vals[b][t]
+                end = min((j + 1) * ps, p + n)
+                for t0, t1 in [(j * ps, end)] if junk == 0 else [(max(j * ps, lo), end), (j * ps, min(end, n_sink))] if n else []:
+                    if t0 < t1:
+                        self.k_pages[place[x], :, t0 - j * ps:t1 - j * ps] = self.keys[b][t0:t1].transpose(0, 1)
+                        self.v_pages[place[x], :, t0 - j * ps:t1 - j * ps] = self.vals[b][t0:t1].transpose(0, 1)
         first, at = len(before), []
         for _, f in groups:
             at.append(first)
@@ -108,16 +109,16 @@ def run(swa, x, append=False, **kw):
 # prefixes that end in and with a page, shorter and longer than a tile; one sequence, none; sequences that hold
 # less than the others; lengths of zero
 ONES = [(300, [(300, 1), (301, 1), (555, 1)]), (64, [(64, 1)]), (0, [(5, 1), (0, 1), (17, 1)]),
-        (1000, [(1000 + 3 * i, 1) for i in range(21)]), (128, [(128, 1), (129, 1)]), (500, [(200, 1), (900, 1), (450, 1)]),
+        (1000, [(1000 + 3 * i, 1) for i in range(21)]), (128, [(128, 1), (129, 1)]), (256, [(256, 1), (257, 1)]), (500, [(200, 1), (900, 1), (450, 1)]),
         (2048, [(2050, 1)] * 40)]
 MIXED = [(300, [(300, 5), (301, 1), (555, 33)]), (64, [(64, 70)]), (0, [(5, 3), (0, 0), (0, 9)]),
-         (1000, [(1000 + 3 * i, 1 + i % 4) for i in range(21)]), (128, [(128, 0), (129, 2), (140, 1), (128, 0)]),
+         (1000, [(1000 + 3 * i, 1 + i % 4) for i in range(21)]), (256, [(256, 0), (257, 2), (268, 1), (256, 0)]),
          (700, [(100, 3), (900, 1), (0, 0), (450, 7)]), (2048, [(2050, 0), (2048, 200), (2049, 40), (2100, 1)])]
 SHAPES = [
     # Hq, Hkv, D, page, window, sinks
-    (8, 2, 128, 16, 0, 0), (8, 2, 128, 64, 100, 4), (4, 4, 64, 32, 0, 0), (32, 2, 64, 16, 257, 37), (7, 1, 128, 128, 1200, 0),
+    (8, 2, 128, 16, 0, 0), (8, 2, 128, 64, 100, 4), (4, 4, 64, 32, 0, 0), (32, 2, 64, 16, 357, 37), (7, 1, 128, 128, 1200, 0),
     (6, 2, 256, 64, 1000, 1), (16, 1, 256, 16, 0, 0), (3, 3, 256, 128, 700, 130), (5, 1, 64, 128, 450, 0),
-    (12, 1, 128, 32, 300, 3), (16, 1, 64, 64, 1, 0), (2, 2, 128, 128, 2000, 300),
+    (12, 1, 128, 32, 400, 3), (16, 1, 64, 64, 1, 0), (2, 2, 128, 128, 2000, 300), (4, 4, 64, 16, 900, 250), (16, 2, 256, 32, 333, 20),
 ]
 
 
@@ -152,13 +153,13 @@ def random_tree(rng, D):
     ps = rng.choice([16, 32, 64, 128])
     groups = []
     for _ in range(rng.randrange(1, 7)):
-        prefix = rng.choice([0, rng.randrange(1, 200), rng.randrange(200, 4000)])
+        prefix = rng.choice([0, rng.randrange(1, 400), rng.randrange(200, 4000)])
         longest = rng.choice([1, 1, 4, 90])
         groups.append((prefix, [(rng.choice([prefix, prefix + rng.randrange(300), rng.randrange(prefix + 1)]),
                                  rng.choice([0, 1, 1, rng.randrange(longest + 1)])) for _ in range(rng.randrange(1, 30))]))
     G = rng.choice([1, 2, 3, 5, 8, 16])
     H = rng.choice([1, 2, 3])
-    window = rng.choice([0, 0, 1, 64, 300, 1500])
+    window = rng.choice([0, 0, 1, 64, 300, 700, 1500])
     return groups, G * H, H, ps, window, rng.choice([0, 1, 40, 200]) if window else 0
 
 
@@ -178,8 +179,8 @@ def test_long_prefixes_and_many_groups(swa, D, ps):
     # prefixes spread over every CTA and joined again; many groups, more than the kernels' lists hold at a time
     run(swa, Shared(5, [(20000, [(20000 + i, 1) for i in range(9)])], 4, 1, D, ps), q_start=None)
     run(swa, Shared(6, [(12000, [(12000 + 7 * i, 3 + i) for i in range(33)])], 4, 1, D, ps))
-    run(swa, Shared(7, [(100 + i % 70, [(170 + i % 9, 1)] * (1 + i % 3)) for i in range(700)], 4, 1, D, ps), q_start=None)
-    run(swa, Shared(8, [(200, [(200, 2)] * 2)] * 300, 4, 1, D, ps, 77, 3))
+    run(swa, Shared(7, [(300 + i % 70, [(370 + i % 9, 1)] * (1 + i % 3)) for i in range(700)], 4, 1, D, ps), q_start=None)
+    run(swa, Shared(8, [(500, [(500, 2)] * 2)] * 300, 4, 1, D, ps, 377, 3))
 
 
 def test_units_of_two_query_tiles(swa):
@@ -190,7 +191,7 @@ def test_units_of_two_query_tiles(swa):
 
 
 def test_as_many_sequences_and_groups_as_a_call_takes(swa):
-    x = Shared(10, [(32, [(32 + i % 9, 1 if i % 3 else 0) for i in range(2)]) for _ in range(4096)], 2, 1, 64, 16)
+    x = Shared(10, [(208, [(208 + i % 9, 1 if j % 3 else 0) for i in range(2)]) for j in range(4096)], 2, 1, 64, 16)
     assert len(x.seqs) == 8192
     run(swa, x)
     run(swa, x, groups=torch.tensor([0, 8192], dtype=torch.int32))
@@ -200,7 +201,7 @@ def test_as_many_sequences_and_groups_as_a_call_takes(swa):
         call(swa, x, groups=torch.zeros(8194, dtype=torch.int32))
 
 
-@pytest.mark.parametrize("case", [(8, 2, 128, 16, 100, 4), (4, 4, 64, 64, 300, 130), (6, 2, 256, 32, 65, 37),
+@pytest.mark.parametrize("case", [(8, 2, 128, 16, 400, 4), (4, 4, 64, 64, 300, 130), (6, 2, 256, 32, 365, 37),
                                   (2, 1, 64, 128, 1000, 0)], ids=str)
 def test_positions_that_no_query_keeps_may_hold_anything(swa, case):
     # pages that are there all the same, with NaN between the sinks and every window

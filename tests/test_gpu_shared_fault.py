@@ -39,3 +39,28 @@ def test_producer_stop_times_out_and_recovers(swa, groups, D, hint, fault, word)
     assert waited < 30.0
     run(swa, x, max_q=hint)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("what,shared", [("same", True), ("window", True), ("freed", True), ("sinks", True),
+                                         ("other", False), ("behind", False), ("short", False)])
+def test_what_is_shared(swa, what, shared):  # noqa: F811
+    """A group whose prefix goes to the many-row kernel waits for its producers, one that shares nothing does not."""
+    seqs = [(2000 + i, 1) for i in range(30)]
+    window, sinks = {"window": (700, 0), "freed": (700, 0), "sinks": (700, 40), "behind": (300, 0)}.get(what, (0, 0))
+    if what == "freed":  # (a page that the first sequence needs and the others have given up)
+        seqs = [(2000, 1)] + [(2300 + i, 1) for i in range(29)]
+    if what == "behind":  # (all but the first look behind what they share)
+        seqs = [(2250, 1)] + [(2700 + i, 1) for i in range(29)]
+    x = Shared(71, [(150 if what == "short" else 2000, seqs)], 8, 2, 64, 16, window, sinks)
+    if what == "other":  # one sequence has a page of its own at the start, with the same tokens
+        free = [p for p in range(x.n_pages) if p not in x.table.unique().tolist()][0]
+        x.k_pages[free], x.v_pages[free] = x.k_pages[int(x.table[3, 0])], x.v_pages[int(x.table[3, 0])]
+        x.table[3, 0] = free
+    swa.swa_debug_set_faults(band_stop_fill=0)
+    try:
+        call(swa, x, q_start=None)
+        st, words = swa.swa_read_device_errors()
+    finally:
+        swa.swa_debug_set_faults()
+    assert (st == SWA_ERR_TIMEOUT) == shared and words["prefill"] == (swa.DEVERR_WAIT_TIMEOUT if shared else 0), words
+    run(swa, x, q_start=None)
