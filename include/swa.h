@@ -377,8 +377,8 @@ SWA_API swa_status swa_paged_attend(const swa_paged_params *p, const swa_paged_c
  * reported: SWA_DEVERR_BAD_POSITION).  A position that some queries of the group keep must be finite in the
  * shared pages, as swa_paged_attend asks of each sequence's own.
  * p, c, errors and requirements as swa_paged_attend; 1 <= n_groups <= 8192.
- * Workspace: swa_paged_shared_workspace_size bytes, 256-byte aligned: beside swa_paged_attend's the prefix parts' results,
- * fp32 [N, H_q, d_h].
+ * Workspace: swa_paged_shared_workspace_size bytes, 256-byte aligned: the partial results, fp32 [N, H_q, d_h] for each of
+ * the two parts, several times that where sequences have few new tokens.  It does not depend on device data.
  */
 SWA_API size_t swa_paged_shared_workspace_size(const swa_paged_params *p, const swa_paged_cache *c, int32_t n_groups);
 SWA_API swa_status swa_paged_attend_shared(const swa_paged_params *p, const swa_paged_cache *c, const int32_t *group_start,

@@ -23,7 +23,6 @@ namespace {
 __device__ unsigned int g_rows_err = 0;   // waits and bounds
 __device__ unsigned int g_rows_data = 0;  // broken device data
 
-
 template <int D>
 struct RowsCfg {
     static constexpr int KS = D == 64 ? 32 : 16;  // keys a step
@@ -81,6 +80,8 @@ __global__ void __launch_bounds__(RowsCfg<D>::WARPS * 32, RowsCfg<D>::CTAS_PER_S
     // for here; else the plan has.
     if (!behind_tiles) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // (rows that the plan's launch has stored, ahead of their copies)
+    asm volatile("fence.proxy.async.global;" ::: "memory");
 
     // A warp's first is its own, the next ones go to whichever warp is free (results do not depend on which).
     const int firsts = static_cast<int>(gridDim.x) * kWarps;

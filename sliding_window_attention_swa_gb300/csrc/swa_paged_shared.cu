@@ -42,17 +42,24 @@ constexpr int kTileRows = 128;  // rows of a query tile of the many-row kernel
 // Of a group's sequences that have new tokens.
 struct Members {
     unsigned long long least;  // least p0, and the first sequence with it: p0 << 13 | (b - b0)
+    unsigned long long next;   // the second least
     int top, count, tiles, broken;
     long long tokens;
 };
 static_assert(kPagedMaxB <= 1 << 13, "the first sequence's number");
 
 __device__ __forceinline__ Members join(const Members &x, const Members &y) {
-    return Members{min(x.least, y.least), max(x.top, y.top), x.count + y.count, x.tiles + y.tiles, x.broken | y.broken,
+    return Members{min(x.least, y.least),
+                   min(max(x.least, y.least), min(x.next, y.next)),
+                   max(x.top, y.top),
+                   x.count + y.count,
+                   x.tiles + y.tiles,
+                   x.broken | y.broken,
                    x.tokens + y.tokens};
 }
 __device__ __forceinline__ Members shuffled(const Members &x, int o) {
-    return Members{__shfl_xor_sync(0xffffffffu, x.least, o), __shfl_xor_sync(0xffffffffu, x.top, o),
+    return Members{__shfl_xor_sync(0xffffffffu, x.least, o), __shfl_xor_sync(0xffffffffu, x.next, o),
+                   __shfl_xor_sync(0xffffffffu, x.top, o),
                    __shfl_xor_sync(0xffffffffu, x.count, o), __shfl_xor_sync(0xffffffffu, x.tiles, o),
                    __shfl_xor_sync(0xffffffffu, x.broken, o), __shfl_xor_sync(0xffffffffu, x.tokens, o)};
 }
@@ -157,13 +164,13 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
     if (!fine && blockIdx.x == 0 && tid == 0) atomicOr(&g_shared_err, SWA_DEVERR_BAD_POSITION);
     for (int g = c; g < sa.n_groups; g += clusters) {
         const int b0 = fine ? __ldg(sa.group_start + g) : 0, b1 = fine ? __ldg(sa.group_start + g + 1) : 0;
-        Members m{~0ull, -1, 0, 0, 0, 0};
+        Members m{~0ull, ~0ull, -1, 0, 0, 0, 0};
         for (int b = b0 + tid; b < b1; b += kThreads) {
             const Seq s = load_seq(a, b);
             if (!s.ok) m.broken = 1;
             if (s.n > 0)
                 m = join(m, Members{static_cast<unsigned long long>(s.p0) << 13 | static_cast<unsigned int>(b - b0),
-                                    s.p0 + s.n - 1, 1, sa.few ? 1 : (s.n + sa.own_tokens - 1) / sa.own_tokens, 0, s.n});
+                                    ~0ull, s.p0 + s.n - 1, 1, sa.few ? 1 : (s.n + sa.own_tokens - 1) / sa.own_tokens, 0, s.n});
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) m = join(m, shuffled(m, o));
@@ -222,7 +229,9 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
             else __syncthreads();
             const int f = min(ranks > 1 ? *cluster.map_shared_rank(&first, 0) : first, n);
             base = f < sinks ? 0 : (e_lo + f - sinks) << a.ps_log2;
-            if (base - lo < kLeastShared) base = 0;
+            // (what two sequences at least have a use for; the others look behind it)
+            const int p1 = static_cast<int>(m.next >> 13);
+            if (base - (p1 >= a.window ? p1 - a.window + 1 : 0) < kLeastShared) base = 0;
         } else if (ranks > 1) {
             cluster.barrier_wait();
         }
@@ -291,11 +300,12 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     const int n = static_cast<int>(x / blocks), h = static_cast<int>(x % blocks) * kHeads + lane / kLanes;
     const int b = n < a.N ? find_sequence(a, n, lane) : -1;
     const Seq s = b >= 0 ? load_seq(a, b) : Seq{};
-    if (b < 0 || !s.ok || n < s.q0 || n >= s.q0 + s.n) return;
     // (the plan's: the kernels before this one have waited for it before they let this grid start)
-    const int4 *info = sa.info + 2 * static_cast<int64_t>(b);
+    const int4 *info = sa.info + 2 * static_cast<int64_t>(max(b, 0));
     const int4 u = __ldcg(info), v = __ldcg(info + 1);  // base, the group's tokens in tiles, in stretches, its first; its p0, number
+    // (by every warp, with a row or without, so that what waits for this grid waits for those before it)
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (b < 0 || !s.ok || n < s.q0 || n >= s.q0 + s.n) return;
     const int base = u.x, i = n - s.q0;
     const bool row_there = h < a.H_q;
     const int head = row_there ? h : 0, kvh = head / a.G;

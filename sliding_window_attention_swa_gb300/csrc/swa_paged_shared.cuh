@@ -22,7 +22,7 @@ struct PartResults {
     float2 *ml;
     float *o;
     int planes;
-    // the many-row kernel's units that several CTAs have (units == nullptr: the part is the few-row kernel's)
+    // of the many-row kernel: its units, and the slots of those that several CTAs have
     const int2 *units;
     PagedWs ws;
     int ctas, rows, TQ, TT;

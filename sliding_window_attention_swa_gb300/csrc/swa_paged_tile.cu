@@ -275,6 +275,8 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         fence_proxy_async_smem();
         if constexpr (PT != Part::kOwn)
             asm volatile("griddepcontrol.wait;" ::: "memory");  // (the append before this kernel has stored its rows)
+        else
+            asm volatile("fence.proxy.async.global;" ::: "memory");  // (the prefix part has waited for it)
         // A tile is npg boxes (pages or a part of one).  The pages are looked up 32 boxes at a time,
         // lane i that of box i, a group ahead of their use.
         const int box = min(a.ps, BN), npg = BN / box, per_group = 32 / npg;
