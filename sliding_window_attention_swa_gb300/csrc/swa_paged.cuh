@@ -61,16 +61,26 @@ __device__ __forceinline__ int sinks_of(const PagedArgs &a, int base) {
 }
 
 // The sequence of token n, looked up by a whole warp: the last b with q_start[b] <= n (for a
-// list that does not decrease); -1 if none has it.  Each step cuts the range 32-fold.
+// list that does not decrease); -1 if none has it.  Each step cuts the range 128-fold, by four loads
+// a lane that are in flight together.
 __device__ __forceinline__ int find_sequence(const PagedArgs &a, int n, int lane) {
     if (!a.q_start) return n < a.B ? n : -1;
+    constexpr int kProbes = 4;
     int lo = 0, len = a.B;  // candidates lo .. lo + len - 1
     while (len > 1) {
-        const int part = (len + 31) / 32;
-        const int at = lo + lane * part;
-        const bool le = lane * part < len && __ldg(a.q_start + at) <= n;
-        const unsigned bal = __ballot_sync(0xffffffffu, le);
-        const int k = bal ? 31 - __clz(bal) : 0;
+        const int part = (len + 32 * kProbes - 1) / (32 * kProbes);
+        bool le[kProbes];
+#pragma unroll
+        for (int i = 0; i < kProbes; ++i) {
+            const int x = (i * 32 + lane) * part;
+            le[i] = x < len && __ldg(a.q_start + lo + x) <= n;
+        }
+        int k = 0;
+#pragma unroll
+        for (int i = 0; i < kProbes; ++i) {
+            const unsigned bal = __ballot_sync(0xffffffffu, le[i]);
+            if (bal) k = i * 32 + 31 - __clz(bal);
+        }
         const int end = lo + len;
         lo += k * part;
         len = min(part, end - lo);
