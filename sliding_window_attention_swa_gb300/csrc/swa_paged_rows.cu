@@ -6,9 +6,10 @@
 // warps wait for one another, so that the latencies of a stretch -- its rows, its pages, its first copies, its end -- are
 // hidden by the other warps' work and by its own copies: the next stretch's first steps are on their way
 // while the last one ends.  Own parts are short (a sample's answer so far), and it is these latencies, not
-// the bytes, that the kernel for long histories (a block a unit) spends its time on there:
-// 135 sequences of 250 tokens on average behind what they share, 72 us of it for 141 MB.
-// Bound by HBM.  P is rounded to bf16 for the second product; the sum takes it unrounded.
+// the bytes, that the kernel for long histories (a block a unit) spends its time on there: 135 sequences of 250
+// tokens on average behind what they share, 141 MB, 72 us of that kernel, about 25 of this one.
+// Bound by HBM: 31 prefixes of up to 13 rows and 227 own parts, head dim 64, 513 MB in 87 us (5.9 TB/s, 87% of the
+// measured copy rate).  P is rounded to bf16 for the second product; the sum takes it unrounded.
 // Every wait is bounded; on expiry the warp records an error word, drains its copies and returns.
 #include <algorithm>
 #include <atomic>

@@ -185,9 +185,11 @@ def test_long_prefixes_and_many_groups(swa, D, ps):
 
 def test_units_of_two_query_tiles(swa):
     # head dim 128 and many rows: pairs of query tiles in the prefix part, and in the own part
-    for Hq, Hkv, window in ((16, 16, 0), (16, 16, 700), (32, 8, 0)):
-        run(swa, Shared(9, [(900, [(900 + i, 100 + 7 * i) for i in range(24)]), (300, [(300, 2000), (310, 700)])], Hq, Hkv, 128,
-                        32, window, 2 if window else 0), want_counts=False)
+    for Hq, Hkv, window, most in ((16, 16, 700, 2000), (32, 8, 0, 900)):
+        x = Shared(9, [(900, [(900 + i, 100 + 7 * i) for i in range(most // 90)]), (300, [(300, most), (310, most // 2)])], Hq,
+                   Hkv, 128, 32, window, 2 if window else 0)
+        assert x.N // (2 * (128 // (Hq // Hkv))) * Hkv >= 2 * 152  # (pairs in the own part, too)
+        run(swa, x, want_counts=False)
 
 
 def test_as_many_sequences_and_groups_as_a_call_takes(swa):

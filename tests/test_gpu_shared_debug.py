@@ -60,7 +60,6 @@ def test_drawn_batches(swa, seed, D):
 
 
 def test_many_groups_and_broken_data(swa):
-    SHARED.test_long_prefixes_and_many_groups(swa, 128, 16)
     SHARED.test_as_many_sequences_and_groups_as_a_call_takes(swa)
     SHARED.test_broken_device_data(swa)
 
