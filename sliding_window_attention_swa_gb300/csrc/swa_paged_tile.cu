@@ -181,14 +181,6 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
         return;
     }
 
-    if constexpr (PT != Part::kAll) {
-        // The prefix part waits for the plan (and the append before it), and only then lets the own part start, which
-        // thus finds what they wrote.  The own part needs nothing of the prefix part: it waits for that at its end, so
-        // that what waits for it waits for both.
-        if constexpr (PT == Part::kPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        if (PT == Part::kPrefix && __ldcg(a.tile_groups) == 0) return;  // (no group has more rows than a stretch)
-    }
     const uint32_t sQ = sbase + C::OFF_Q, sRing = sbase + C::OFF_RING;
     const uint32_t bars = sbase + C::OFF_BAR;
     auto bar_qf = [&](int x) { return bars + 8u * x; };
@@ -249,6 +241,19 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
     }
     const int TT = ta.TT;
     tc_fence_before();
+    if constexpr (PT != Part::kAll) {
+        // The prefix part waits for the plan (and the append beside it), and only then lets the own part start, which
+        // thus finds what they wrote.  The own part needs nothing of the prefix part: it waits for that at its end, so
+        // that what waits for it waits for both.
+        if constexpr (PT == Part::kPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if (PT == Part::kPrefix && __ldcg(a.tile_groups) == 0) {  // no group has more rows than a stretch
+            __syncthreads();
+            tc_fence_after();
+            if (warp == 1) tmem_dealloc(*tmem_holder, C::TMEM_COLS);
+            return;
+        }
+    }
     // (its block barriers also publish the mbarriers and the TMEM address)
     find_share<BN, C::THREADS, true, PT>(a, TT, ta.min_tiles, sgen + C::OFF_RING, share, &g_ptile_data);
     tc_fence_after();
