@@ -450,3 +450,34 @@ def test_one_workspace_for_many_calls(swa):
     for _ in range(2):
         for x, hint in xs:
             run(swa, x, max_q=hint, workspace=ws)
+
+
+@pytest.mark.parametrize("hint", [0, 1])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_calls_in_a_row_with_cold_and_warm_caches(swa, D, hint):
+    """Two batches in turn in one workspace, without a wait between the calls, their pages in L2 or not: what a call
+    leaves in the workspace (lengths, lists, results) is never taken for the next one's, and copies may land
+    late: every result is bit for bit the first one, which is checked."""
+    ps = 16 if D == 128 else 64
+    xs = [Shared(80, [(3000, [(3000 + 17 * i, 1) for i in range(40)]), (500, [(500 + i, 1) for i in range(3)])], 8, 2, D, ps),
+          Shared(81, [(700, [(700 + i, 1) for i in range(9)]), (2500, [(2500 + 5 * i, 1) for i in range(30)]),
+                      (64, [(300, 1)] * 4)], 8, 2, D, ps)]
+    assert len(xs[0].seqs) == len(xs[1].seqs)
+    ws = torch.empty(1 << 28, dtype=torch.uint8, device="cuda").fill_(0x77)
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")  # more than L2
+    dev = [[t.cuda() for t in (x.q, x.k_pages, x.v_pages, x.table, x.p0, x.groups)] for x in xs]
+    start = xs[0].q_start.cuda()
+    first, got = [], [[], []]
+    for i, x in enumerate(xs):
+        first.append(call(swa, x, q_start=None if hint else start, workspace=ws)[:2])
+        swa.swa_check_device_error()
+        verify(x, *first[i], None)
+    for turn in range(30):
+        if turn % 3 == 0:
+            flush.fill_(turn)
+        for i in (0, 1, 1, 0):
+            got[i].append(swa.swa_paged_attend_shared(*dev[i], q_start=None if hint else start, workspace=ws)[:2])
+    swa.swa_check_device_error()
+    for i in range(2):
+        for turn, (o, lse) in enumerate(got[i]):
+            assert torch.equal(o, first[i][0]) and torch.equal(lse, first[i][1]), f"batch {i}, call {turn}"
