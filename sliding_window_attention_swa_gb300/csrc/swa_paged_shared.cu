@@ -37,6 +37,17 @@ constexpr int kChunk = 512;  // entries that a warp compares at a time: sixteen 
 // 32 heads of 128, 200 tokens of their own: up to 128 shared positions 24.6 us, 22.6 without the part, up to 256 in groups of
 // four 24.6 against 28.7, in groups of 64 28.7 against 33).
 constexpr int kLeastShared = 192;
+// With many new tokens a sequence the prefix part saves what its tiles of rows are fewer than the sequences' own, and its
+// parts are written and joined again. Below this many positions saved per own tile that costs more (12 sequences of 16
+// tokens, 6 tiles for 12, 32 heads of 128 on 8: 6000 shared positions 60 us, 56 as none; 24000 94 against 148; 48
+// sequences of 80 tokens, 120 tiles for 144: 1024 positions 222 us, 146 as none; 12 such, 24000: 304 against 361; 48 of 4
+// tokens, 6 tiles for 48: 1024 positions 60 against 57, 6000 76 against 135). The build that checks indices shares
+// wherever there is anything to save: its tests are to reach every part.
+#ifdef SWA_DEBUG
+constexpr int kLeastSaved = 1;
+#else
+constexpr int kLeastSaved = 3500;
+#endif
 constexpr int kTileRows = 128;  // rows of a query tile of the many-row kernel
 
 // Of a group's sequences that have new tokens.
@@ -186,8 +197,8 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
         int base = 0, leader = 0, p0 = 0;
         // A prefix part that has as many tiles of rows as the sequences alone would save nothing.
         const bool stretch = sa.few && m.tokens * a.G <= kStretchRows;
-        const bool shares = !m.broken && m.count >= 2 && (m.tokens + sa.prefix_tokens - 1) / sa.prefix_tokens < m.tiles &&
-                            (stretch || sa.any_tiles);
+        const int64_t prefix_tiles = (m.tokens + sa.prefix_tokens - 1) / sa.prefix_tokens;
+        const bool shares = !m.broken && m.count >= 2 && prefix_tiles < m.tiles && (stretch || sa.any_tiles);
         if (shares) {  // (the same for every thread of the cluster)
             leader = b0 + static_cast<int>(m.least & ((1u << 13) - 1));
             p0 = static_cast<int>(m.least >> 13);
@@ -232,7 +243,9 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
             base = f < sinks ? 0 : (e_lo + f - sinks) << a.ps_log2;
             // (what two sequences at least have a use for; the others look behind it)
             const int p1 = static_cast<int>(m.next >> 13);
-            if (base - (p1 >= a.window ? p1 - a.window + 1 : 0) < kLeastShared) base = 0;
+            const int used = base - (p1 >= a.window ? p1 - a.window + 1 : 0);
+            const int64_t saved = static_cast<int64_t>(used) * (m.tiles - prefix_tiles);
+            if (used < kLeastShared || (!sa.few && saved < static_cast<int64_t>(kLeastSaved) * m.tiles)) base = 0;
         } else if (ranks > 1) {
             cluster.barrier_wait();
         }

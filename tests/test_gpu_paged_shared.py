@@ -192,6 +192,23 @@ def test_units_of_two_query_tiles(swa):
         run(swa, x, want_counts=False)
 
 
+@pytest.mark.parametrize("append", [False, True], ids=["stored", "append"])
+@pytest.mark.parametrize("shape", [(8, 2, 64, 16, 0, 0), (8, 2, 64, 64, 5500, 200), (4, 1, 128, 128, 0, 0), (7, 1, 128, 32, 7000, 3),
+                                   (4, 2, 256, 64, 0, 0), (8, 1, 256, 128, 6500, 1), (16, 16, 128, 64, 6000, 40)], ids=str)
+def test_chunks_behind_long_prefixes(swa, shape, append):
+    # prefixes long enough for chunks to share them; sequences that hold less or have nothing new
+    Hq, Hkv = shape[:2]
+    per_tile = 128 // (Hq // Hkv)
+    lists = [(9000, [(9000 + 3 * i, 1 + i % 7) for i in range(24)] + [(9000, 0), (9111, per_tile + 3)]), (300, [(300, 9)] * 3),
+             (7777, [(7777, 2)] * 3 + [(8000 + i, 1 + 9 * (i % 2)) for i in range(30)])]
+    if Hq == 16 == Hkv:  # pairs of query tiles
+        lists = [(9000, [(9000 + i, 30) for i in range(96)])]
+    for prefix, f in lists[::2]:
+        own = sum(-(-n // per_tile) for _, n in f)
+        assert (own + -sum(n for _, n in f) // per_tile) * min(prefix, (shape[4] or prefix) - 600) > 3600 * own
+    run(swa, Shared(24, lists, *shape, lead=2, tail=3), append)
+
+
 def test_as_many_sequences_and_groups_as_a_call_takes(swa):
     x = Shared(10, [(208, [(208 + i % 9, 1 if j % 3 else 0) for i in range(2)]) for j in range(4096)], 2, 1, 64, 16)
     assert len(x.seqs) == 8192

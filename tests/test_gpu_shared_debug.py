@@ -1,6 +1,6 @@
 """The rotation and the attention of shared prefixes through the debug build of the library (libswa_debug.so),
-whose kernels check every index they compute before the access.  The results must match the references as
-before, and no check may fire."""
+whose kernels check every index they compute before the access, and which shares prefixes of chunks however
+short.  The results must match the references as before, and no check may fire."""
 import pytest
 
 import test_gpu_paged_shared as SHARED
@@ -54,7 +54,7 @@ def test_ragged_groups(swa, shape, hint):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("seed", range(12))
 def test_drawn_batches(swa, seed, D):
     SHARED.test_drawn_batches(swa, seed, D)
 
@@ -67,3 +67,17 @@ def test_many_groups_and_broken_data(swa):
 @pytest.mark.parametrize("hint", [0, 1])
 def test_lists_in_disorder(swa, hint):
     SHARED.test_sequences_that_overlap(swa, 64, hint)
+
+
+@pytest.mark.parametrize("D,ps", [(64, 16), (128, 32), (256, 64)])
+def test_groups_and_long_prefixes(swa, D, ps):
+    SHARED.test_same_as_each_by_itself(swa, D, ps)
+    SHARED.test_long_prefixes_and_many_groups(swa, D, ps)
+
+
+def test_chunks(swa):
+    SHARED.test_units_of_two_query_tiles(swa)
+    SHARED.test_rows_that_keep_nothing_of_the_prefix(swa)
+    SHARED.test_chunks_behind_long_prefixes(swa, (8, 2, 64, 64, 5500, 200), True)
+    for case in ((8, 2, 128, 16, 400, 4), (4, 4, 64, 64, 300, 130), (6, 2, 256, 32, 365, 37)):
+        SHARED.test_positions_that_no_query_keeps_may_hold_anything(swa, case)

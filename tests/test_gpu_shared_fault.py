@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 
 SWA_ERR_TIMEOUT = 4
 FEW = [(2000, [(2000 + i, 1) for i in range(30)]), (500, [(500, 1)] * 3)]
-MANY = [(2000, [(2000 + i, 7) for i in range(30)]), (500, [(500, 90)] * 3)]
+MANY = [(8000, [(8000 + i, 7) for i in range(30)]), (500, [(500, 90)] * 3)]
 
 
 @pytest.mark.parametrize("groups,D,hint,fault,word", [
