@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 
@@ -31,7 +32,8 @@ __device__ unsigned int g_shared_err = 0;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kFewGroups = 32;  // below it a cluster plans a group, else a block
 constexpr int kCluster = 8;
-constexpr int kChunk = 512;  // entries that a warp compares at a time: sixteen loads a lane and row in flight
+// Entries that a warp compares at a time: sixteen loads a lane and row in flight.
+constexpr int kWords = 16, kChunk = 32 * kWords;
 
 // Shared positions below which a group is computed as none: a part of its own costs more than they do (64 sequences of
 // 32 heads of 128, 200 tokens of their own: up to 128 shared positions 24.6 us, 22.6 without the part, up to 256 in groups of
@@ -209,31 +211,44 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
             const int n = sinks + e_end - e_lo;  // entries in question: those of the sinks, then the window's
             const int chunks = (n + kChunk - 1) / kChunk;
             const int32_t *row0 = a.table + static_cast<int64_t>(leader) * a.width;
-            const int64_t tasks = static_cast<int64_t>(b1 - b0) * chunks;
+            // Where rows are short and there are more than warps, a warp compares several at a time (2048 sequences of 64
+            // entries: the kernel takes 23 us, 40 with one; 512 of 32 10, 15 with one).
+            int words = kWords;  // of a row that a lane loads
+            while (words > 1 && 2 * n <= 32 * words && (b1 - b0) * words > ranks * kWarps * kWords) words /= 2;
             int differs = INT_MAX;
-            for (int64_t t = rank * kWarps + warp; t < tasks; t += ranks * kWarps) {
-                const int i0 = static_cast<int>(t % chunks) * kChunk, b = b0 + static_cast<int>(t / chunks);
-                if (i0 >= differs || b == leader) continue;
-                const Seq s = load_seq(a, b);
-                const int my_lo = s.p0 >= a.window ? s.p0 - a.window + 1 : 0;
-                const int32_t *row = a.table + static_cast<int64_t>(b) * a.width;
-                int x[kChunk / 32], y[kChunk / 32];
+            auto compare = [&](auto rows) {
+                constexpr bool several = decltype(rows)::value;
+                const int w = several ? words : kWords, w_log2 = __ffs(w) - 1, each = kWords >> w_log2;
+                const int64_t tasks = static_cast<int64_t>((b1 - b0 + each - 1) / each) * chunks;
+                for (int64_t t = rank * kWarps + warp; t < tasks; t += ranks * kWarps) {
+                    const int i0 = static_cast<int>(t % chunks) * kChunk, b = b0 + static_cast<int>(t / chunks) * each;
+                    if (__all_sync(0xffffffffu, i0 >= differs)) continue;
+                    const Seq s = load_seq(a, min(b + (lane & (each - 1)), b1 - 1));  // (the last one's several times over)
+                    // (a sequence without new tokens needs nothing)
+                    const int my_lo = s.n == 0 ? -1 : s.p0 >= a.window ? s.p0 - a.window + 1 : 0;
+                    int x[kWords], y[kWords];
 #pragma unroll
-                for (int k = 0; k < kChunk / 32; ++k) {
-                    const int i = i0 + k * 32 + lane, j = i < sinks ? i : e_lo + i - sinks;
-                    const bool in = i < n && SWA_IN_BOUNDS(j >= 0 && j < a.width, &g_shared_err);
-                    x[k] = in ? __ldg(row0 + j) : 0;
-                    y[k] = in ? __ldg(row + j) : 0;
-                }
-                if (s.n == 0) continue;
+                    for (int k = 0; k < kWords; ++k) {
+                        const int i = i0 + (k & (w - 1)) * 32 + lane, e = several ? min(i, n - 1) : i;
+                        const int j = e < sinks ? e : e_lo + e - sinks;
+                        // (several: all loads, so that they are on their way at a time; one: those there are)
+                        const bool in = e < n && SWA_IN_BOUNDS(j >= 0 && j < a.width, &g_shared_err);
+                        x[k] = in ? __ldg(row0 + j) : 0;
+                        y[k] = in ? __ldg(a.table + static_cast<int64_t>(min(b + (k >> w_log2), b1 - 1)) * a.width + j) : 0;
+                    }
 #pragma unroll
-                for (int k = kChunk / 32 - 1; k >= 0; --k) {
-                    const int i = i0 + k * 32 + lane, j = i < sinks ? i : e_lo + i - sinks;
-                    // (needed: some position of the entry is in reach of the sequence's first new token, or a sink)
-                    const bool needed = (static_cast<int64_t>(j) + 1) << a.ps_log2 > my_lo || j < e_sink;
-                    if (x[k] != y[k] && needed) differs = min(differs, i);
+                    for (int k = kWords - 1; k >= 0; --k) {
+                        const int i = i0 + (k & (w - 1)) * 32 + lane, e = several ? min(i, n - 1) : i;
+                        const int j = e < sinks ? e : e_lo + e - sinks;
+                        const int lo_k = several ? __shfl_sync(0xffffffffu, my_lo, k >> w_log2) : my_lo;
+                        // (needed: some position of the entry is in reach of the sequence's first new token, or a sink)
+                        const bool needed = lo_k >= 0 && ((static_cast<int64_t>(j) + 1) << a.ps_log2 > lo_k || j < e_sink);
+                        if (x[k] != y[k] && needed) differs = min(differs, e);
+                    }
                 }
-            }
+            };
+            if (words < kWords) compare(std::true_type{});
+            else compare(std::false_type{});
             differs = __reduce_min_sync(0xffffffffu, differs);
             if (ranks > 1) cluster.barrier_wait();
             if (lane == 0 && differs < INT_MAX) atomicMin(ranks > 1 ? cluster.map_shared_rank(&first, 0) : &first, differs);
@@ -285,9 +300,10 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
 // join: `kLanes` lanes a row, a warp the rows of a few heads of one token.  A row's results (m, l, acc), of its own
 // part and of its group's prefix part, each in planes or in the slots of the CTAs that share a unit, are joined:
 // with M the largest m, o = sum 2^(m - M) acc / sum 2^(m - M) l.  Bound by latency -- the row's sequence, its
-// units, the maxima, the values, each read from L2 or HBM behind the last --, so 8 lanes a row where there are
-// rows for every warp several times over (76000 rows of 128: 105 us with 32 lanes each, 35 with 8), 32 where there
-// are not (2048 rows with 22 results each: 7 us).
+// units, the maxima, the values, each read from L2 or HBM behind the last --, so 8 lanes a row where warps of one row
+// would fill the SMs a good part (76000 rows of 128: 105 us with 32 lanes each, 35 with 8; 14400 and 8192 rows, the whole
+// call: 150 and 132 us, 137 and 125 with 8; 4160 rows the same), 32 where they would not (2048 rows with 22 results
+// each: 7 us, 12 with 8).
 // ---------------------------------------------------------------------------------------------
 template <int E>
 __device__ __forceinline__ void load_columns(float (&x)[E], const float *src) {
@@ -525,7 +541,7 @@ cudaError_t launch_plan(SharedArgs &sa, cudaStream_t s) {
 template <int D>
 cudaError_t launch_join_d(const SharedArgs &sa, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(sa.a.N) * sa.a.H_q;
-    const bool many = rows > static_cast<int64_t>(paged_sm_count()) * 128;
+    const bool many = rows > static_cast<int64_t>(paged_sm_count()) * 20;
     const int heads = many ? 4 : 1;  // of a warp
     const int64_t warps = static_cast<int64_t>(sa.a.N) * ((sa.a.H_q + heads - 1) / heads);
     const int64_t blocks = (warps + kWarps - 1) / kWarps;
