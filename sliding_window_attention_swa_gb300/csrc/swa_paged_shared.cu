@@ -152,7 +152,9 @@ __device__ __forceinline__ void put_sequences(const SharedArgs &sa, int b0, int 
     }
 }
 
-__global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_constant__ SharedArgs sa) {
+// (two blocks an SM: the blocks that store tokens are many; with one and 222 registers the plan of 64 sequences takes 6.4
+// us, 6.7 with two, and that of 5700 new tokens 23.4 instead of 16.5)
+__global__ void __launch_bounds__(kThreads, 2) paged_plan_kernel(const __grid_constant__ SharedArgs sa) {
     const PagedArgs &a = sa.a;
     const cg::cluster_group cluster = cg::this_cluster();
     __shared__ Members sums[kWarps];
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const __grid_const
             const int chunks = (n + kChunk - 1) / kChunk;
             const int32_t *row0 = a.table + static_cast<int64_t>(leader) * a.width;
             // Where rows are short and there are more than warps, a warp compares several at a time (2048 sequences of 64
-            // entries: the kernel takes 23 us, 40 with one; 512 of 32 10, 15 with one).
+            // entries: the kernel takes 18 us, 40 with one; 512 of 32 9, 15 with one).
             int words = kWords;  // of a row that a lane loads
             while (words > 1 && 2 * n <= 32 * words && (b1 - b0) * words > ranks * kWarps * kWords) words /= 2;
             int differs = INT_MAX;
