@@ -47,11 +47,15 @@ struct PagedArgs {
     const int32_t *base;  // [B]: the positions below it are in the prefix part
     const int32_t *tile_groups;  // kPrefix: the groups with rows, 0: there are none
     // A part's results, fp32.  A unit that one CTA has whole: here; one that several have: in their slots of
-    // PagedWs.  units, at (q0 / TT + b + ut) * H_kv + kvh: the CTA that begins the unit, and its
-    // pieces (0: whole).
+    // PagedWs.  Units of kPrefix, at (q0 / TT + b + ut) * H_kv + kvh: the CTA that begins the unit, and its
+    // pieces (0: whole); those of kOwn whose rows are not final, in any order, two entries each: the
+    // same, b, ut * H_kv + kvh; q0, n, and of the sequence's group its first token (-1: no prefix) and number.
     float2 *part_ml;  // [N, H_q]: maximum (log2 units), sum of weights
     float *part_o;    // [N, H_q, D]: unnormalised weighted values
     int2 *part_units;
+    int4 *part_list;
+    int32_t *part_count, part_cap;  // of the list: units
+    const int4 *part_info;  // [B][2], the plan's
 };
 
 constexpr int kPagedMaxB = 8192;

@@ -51,6 +51,8 @@ constexpr int kLeastSaved = 1;
 constexpr int kLeastSaved = 3500;
 #endif
 constexpr int kTileRows = 128;  // rows of a query tile of the many-row kernel
+// Of the join of units, for an SM (two at a time; 22 chunks of up to 16 tokens: 72 us, 75 with two, 72 with eight).
+constexpr int kJoinBlocks = 4;
 
 // Of a group's sequences that have new tokens.
 struct Members {
@@ -321,51 +323,39 @@ __device__ __forceinline__ void load_columns(float (&x)[E], const float *src) {
     }
 }
 
+// Where the results of a row's part are: in planes, or in the slots of the CTAs that share its unit.
+struct Where {
+    const PartResults *p = nullptr;
+    int count = 0, sink = -1, owner = 0, row = 0;  // sink: the number of the sinks' stretch (their plane is the last)
+    bool pieces = false;
+};
+__device__ __forceinline__ Where in_planes(const PartResults &p, const Keys &k) {
+    return Where{&p, k.stretches(), k.count, 0, 0, false};
+}
+// Of a unit of the many-row kernel with owner and pieces x, a row of it.
+__device__ __forceinline__ Where in_unit(const PartResults &p, int2 x, int row) {
+    // (a unit that was never finished, after an expired wait, has any record)
+    if (x.y <= 0 || x.x < 0 || x.y > p.ctas || x.x > p.ctas - x.y) return Where{&p, 1, -1, 0, 0, false};
+    return Where{&p, x.y, -1, x.x, row, true};
+}
+// Of a row's prefix part in tiles; q0, number: of the group.
+__device__ __forceinline__ Where in_prefix_tiles(const SharedArgs &sa, int q0, int number, int n, int head) {
+    const PagedArgs &a = sa.a;
+    const PartResults &p = sa.part[1];
+    const int tok = n - q0, ut = tok / p.TT, r = tok % p.TT;
+    const int2 rec = __ldcg(p.units + (static_cast<int64_t>(q0 / p.TT) + number + ut) * a.H_kv + head / a.G);
+    return in_unit(p, rec, r / p.TQ * kTileRows + r % p.TQ * a.G + head % a.G);
+}
+
+// Joins the row of token n of sequence b (s) and a head, by kLanes lanes; row_there: whether they have one.
 template <int D, int kLanes>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ SharedArgs sa) {
+__device__ __forceinline__ void join_row(const SharedArgs &sa, int b, const Seq &s, int n, int head, bool row_there,
+                                         const Where &own, const Where &pre) {
     // columns of a lane: kV neighbours in each of E / kV blocks of kLanes * kV
-    constexpr int E = D / kLanes, kV = E < 4 ? E : 4, kHeads = 32 / kLanes;
+    constexpr int E = D / kLanes, kV = E < 4 ? E : 4;
     constexpr int kAtOnce = E <= 4 ? 12 : E <= 8 ? 8 : E <= 16 ? 4 : 2;  // results whose values are on their way at a time
     const PagedArgs &a = sa.a;
-    const int lane = threadIdx.x & 31, part = lane % kLanes;
-    const int64_t x = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int blocks = (a.H_q + kHeads - 1) / kHeads;  // of a token's heads
-    const int n = static_cast<int>(x / blocks), h = static_cast<int>(x % blocks) * kHeads + lane / kLanes;
-    const int b = n < a.N ? find_sequence(a, n, lane) : -1;
-    const Seq s = b >= 0 ? load_seq(a, b) : Seq{};
-    // (the plan's: the kernels before this one have waited for it before they let this grid start)
-    const int4 *info = sa.info + 2 * static_cast<int64_t>(max(b, 0));
-    const int4 u = __ldcg(info), v = __ldcg(info + 1);  // base, the group's tokens in tiles, in stretches, its first; its p0, number
-    // (by every warp, with a row or without, so that what waits for this grid waits for those before it)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (b < 0 || !s.ok || n < s.q0 || n >= s.q0 + s.n) return;
-    const int base = u.x, i = n - s.q0;
-    const bool row_there = h < a.H_q;
-    const int head = row_there ? h : 0, kvh = head / a.G;
-    // the parts: how many results, where
-    struct Where {
-        const PartResults *p;
-        int count, sink, owner, row;  // sink: the number of the sinks' stretch (their plane is the last)
-        bool pieces;
-    };
-    auto in_tiles = [&](const PartResults &p, int q0, int number) -> Where {
-        const int tok = n - q0, ut = tok / p.TT, r = tok % p.TT;
-        const int64_t at = (static_cast<int64_t>(q0 / p.TT) + number + ut) * a.H_kv + kvh;
-        const int2 rec = __ldcg(p.units + at);
-        if (rec.y < 0) return Where{&p, 0, -1, 0, 0, false};  // the rows are final
-        // (a unit that was never finished, after an expired wait, has any record)
-        if (rec.y == 0 || rec.x < 0 || rec.y > p.ctas || rec.x > p.ctas - rec.y) return Where{&p, 1, -1, 0, 0, false};
-        return Where{&p, rec.y, -1, rec.x, r / p.TQ * kTileRows + r % p.TQ * a.G + head % a.G, true};
-    };
-    auto in_planes = [&](const PartResults &p, const Keys &k) -> Where {
-        return Where{&p, k.stretches(), k.count, 0, 0, false};
-    };
-    const int TT = kStretchRows / a.G;
-    Where own, pre{nullptr, 0, -1, 0, 0, false};
-    if (sa.few) own = in_planes(sa.part[0], own_keys(a, s, base, i / TT, TT, sa.part[0]));
-    else own = in_tiles(sa.part[0], s.q0, b);
-    if (u.z > 0) pre = in_planes(sa.few_prefix, prefix_keys(a, v.x, base, sa.few_prefix));
-    else if (u.y > 0) pre = in_tiles(sa.part[1], u.w, v.y);
+    const int part = threadIdx.x % kLanes;
     const int64_t row = static_cast<int64_t>(n) * a.H_q + head, plane = static_cast<int64_t>(a.N) * a.H_q;
     auto result = [&](int c, const float2 *&ml, const float *&o) {
         const bool first = c < own.count;
@@ -453,7 +443,65 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     }
     if (part == 0) {
         a.lse[row] = (m + log2f(L)) * 0.69314718055994531f;
-        if (a.counts) a.counts[row] = kept_keys(a, s.p0 + i);
+        if (a.counts) a.counts[row] = kept_keys(a, s.p0 + n - s.q0);
+    }
+}
+
+// By rows: own parts in stretches, every row is joined.
+template <int D, int kLanes>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_constant__ SharedArgs sa) {
+    constexpr int kHeads = 32 / kLanes;
+    const PagedArgs &a = sa.a;
+    const int lane = threadIdx.x & 31;
+    const int64_t x = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int blocks = (a.H_q + kHeads - 1) / kHeads;  // of a token's heads
+    const int n = static_cast<int>(x / blocks), h = static_cast<int>(x % blocks) * kHeads + lane / kLanes;
+    const int b = n < a.N ? find_sequence(a, n, lane) : -1;
+    const Seq s = b >= 0 ? load_seq(a, b) : Seq{};
+    // (the plan's: the kernels before this one have waited for it before they let this grid start)
+    const int4 *info = sa.info + 2 * static_cast<int64_t>(max(b, 0));
+    const int4 u = __ldcg(info), v = __ldcg(info + 1);  // base, the group's tokens in tiles, in stretches, its first; its p0, number
+    // (by every warp, with a row or without, so that what waits for this grid waits for those before it)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (b < 0 || !s.ok || n < s.q0 || n >= s.q0 + s.n) return;
+    const bool row_there = h < a.H_q;
+    const int head = row_there ? h : 0, TT = kStretchRows / a.G;
+    const Where own = in_planes(sa.part[0], own_keys(a, s, u.x, (n - s.q0) / TT, TT, sa.part[0]));
+    const Where pre = u.z > 0   ? in_planes(sa.few_prefix, prefix_keys(a, v.x, u.x, sa.few_prefix))
+                      : u.y > 0 ? in_prefix_tiles(sa, u.w, v.y, n, head)
+                                : Where{};
+    join_row<D, kLanes>(sa, b, s, n, head, row_there, own, pre);
+}
+
+// By units: own parts in tiles of rows, whose units are on a list if their rows are not final (two chunks of 12981
+// tokens that share nothing, 16 heads of 256: the call takes 198 us, 255 by rows, which find that next to none is to be
+// joined; 14 chunks of up to 500 tokens 358, 376; 57 short ones about three prefixes, where all are, 62, 59).
+// A block has as many rows of a unit at a time as it has lanes for.
+template <int D, int kLanes>
+__global__ void __launch_bounds__(kThreads, 2) paged_join_units_kernel(const __grid_constant__ SharedArgs sa) {
+    constexpr int kRows = kThreads / kLanes;
+    const PagedArgs &a = sa.a;
+    const PartResults &p = sa.part[0];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int subs = p.TT / p.TQ * (kTileRows / kRows);
+    int64_t x = blockIdx.x;
+    // (an entry is on its way while the one before it is used, the first one with the list's length)
+    int4 next = __ldcg(sa.own_units + x / subs * 2), next_seq = __ldcg(sa.own_units + x / subs * 2 + 1);
+    const int64_t items = static_cast<int64_t>(min(__ldcg(sa.counts + kOwnUnits), sa.own_units_cap)) * subs;
+    while (x < items) {
+        const int4 unit = next, seq = next_seq;
+        const int r = static_cast<int>(x % subs) * kRows + static_cast<int>(threadIdx.x) / kLanes, y = r % kTileRows;
+        x += gridDim.x;
+        if (x < items) next = __ldcg(sa.own_units + x / subs * 2), next_seq = __ldcg(sa.own_units + x / subs * 2 + 1);
+        const int b = unit.z, ut = unit.w / a.H_kv, kvh = unit.w % a.H_kv;
+        if (!SWA_IN_BOUNDS(b >= 0 && b < a.B && ut >= 0 && kvh >= 0 && seq.x >= 0 && seq.x + seq.y <= a.N, &g_shared_err)) continue;
+        const Seq s{seq.x, seq.y, __ldg(a.p0 + b), true};
+        const int i = ut * p.TT + r / kTileRows * p.TQ + y / a.G;
+        const bool row_there = y < p.TQ * a.G && i < s.n;
+        const int n = s.q0 + (row_there ? i : 0), head = kvh * a.G + y % a.G;
+        if (__all_sync(0xffffffffu, !row_there)) continue;
+        const Where pre = seq.z >= 0 ? in_prefix_tiles(sa, seq.z, seq.w, n, head) : Where{};
+        join_row<D, kLanes>(sa, b, s, n, head, row_there, in_unit(p, make_int2(unit.x, unit.y), r), pre);
     }
 }
 
@@ -464,6 +512,7 @@ struct Layout {
     bool few, tiles;  // tiles: prefixes may go to the many-row kernel
     int planes, prefix_planes, own_cap, prefix_cap;
     PagedShape shape;  // of the many-row kernel
+    int own_units;  // units of the own part, at most
     size_t slots[2], base, info, groups, pos, count, list, units[2], ml[2], o[2], few_ml, few_o, bytes;
 };
 
@@ -502,7 +551,8 @@ Layout layout(const PagedArgs &a, int n_groups) {
         const size_t n_units = (static_cast<size_t>(a.N) / TU + (p ? n_groups : a.B) + 2) * a.H_kv;
         const size_t planes = p ? 1 : l.planes;
         l.slots[p] = take(tiles[p] ? paged_ws_bytes(l.shape, a.D) : 0);
-        l.units[p] = take(tiles[p] ? n_units * sizeof(int2) : 0);
+        l.units[p] = take(tiles[p] ? n_units * (p ? sizeof(int2) : 2 * sizeof(int4)) : 0);
+        if (!p) l.own_units = tiles[p] ? static_cast<int>(std::min<size_t>(n_units, INT_MAX / 2)) : 0;
         l.ml[p] = take(tiles[p] || !p ? planes * rows * 8 : 0);
         l.o[p] = take(tiles[p] || !p ? planes * rows * a.D * 4 : 0);
     }
@@ -545,6 +595,13 @@ cudaError_t launch_join_d(const SharedArgs &sa, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(sa.a.N) * sa.a.H_q;
     const bool many = rows > static_cast<int64_t>(paged_sm_count()) * 20;
     const int heads = many ? 4 : 1;  // of a warp
+    if (!sa.few) {
+        const PartResults &p = sa.part[0];
+        const int64_t items = static_cast<int64_t>(sa.own_units_cap) * (p.TT / p.TQ * kTileRows / (kWarps * heads));
+        const int blocks = static_cast<int>(std::min<int64_t>(items, paged_sm_count() * kJoinBlocks));
+        return launch_dependent(true, many ? paged_join_units_kernel<D, 8> : paged_join_units_kernel<D, 32>, dim3(blocks),
+                                kThreads, 0, s, sa);
+    }
     const int64_t warps = static_cast<int64_t>(sa.a.N) * ((sa.a.H_q + heads - 1) / heads);
     const int64_t blocks = (warps + kWarps - 1) / kWarps;
     if (blocks > INT_MAX) return cudaErrorInvalidValue;
@@ -583,6 +640,8 @@ cudaError_t launch_paged_shared(const PagedArgs &a, const int32_t *group_start, 
     sa.counts = reinterpret_cast<int32_t *>(p + l.count);
     sa.own_cap = l.own_cap;
     sa.prefix_cap = l.prefix_cap;
+    sa.own_units = reinterpret_cast<const int4 *>(p + l.units[0]);
+    sa.own_units_cap = l.own_units;
     sa.few = l.few;
     sa.any_tiles = l.tiles;
     sa.prefix_tokens = sa.own_tokens = l.shape.TQ;
@@ -591,7 +650,7 @@ cudaError_t launch_paged_shared(const PagedArgs &a, const int32_t *group_start, 
         r.ml = reinterpret_cast<float2 *>(p + l.ml[x]);
         r.o = reinterpret_cast<float *>(p + l.o[x]);
         r.planes = x ? 1 : l.planes;
-        r.units = reinterpret_cast<const int2 *>(p + l.units[x]);
+        if (x) r.units = reinterpret_cast<const int2 *>(p + l.units[x]);
         r.ws = paged_carve(p + l.slots[x], l.shape, a.D);
         r.ctas = l.shape.ctas;
         r.rows = l.shape.tiles * l.shape.rows;
@@ -610,7 +669,14 @@ cudaError_t launch_paged_shared(const PagedArgs &a, const int32_t *group_start, 
         t.base = sa.base;
         t.part_ml = sa.part[x].ml;
         t.part_o = sa.part[x].o;
-        t.part_units = reinterpret_cast<int2 *>(p + l.units[x]);
+        if (x) {
+            t.part_units = reinterpret_cast<int2 *>(p + l.units[1]);
+        } else {
+            t.part_list = reinterpret_cast<int4 *>(p + l.units[0]);
+            t.part_count = sa.counts + kOwnUnits;
+            t.part_cap = l.own_units;
+            t.part_info = sa.info;
+        }
         if (x) t.B = n_groups;
         return t;
     };

@@ -22,7 +22,7 @@ struct PartResults {
     float2 *ml;
     float *o;
     int planes;
-    // of the many-row kernel: its units, and the slots of those that several CTAs have
+    // of the many-row kernel: its units (the prefix's), and the slots of those that several CTAs have
     const int2 *units;
     PagedWs ws;
     int ctas, rows, TQ, TT;
@@ -65,8 +65,9 @@ __device__ __forceinline__ Keys prefix_keys(const PagedArgs &a, int p0, int end,
     return split_keys(lo, end, 0, min(a.n_sink, lo), p);
 }
 
-// Stretches on the lists, groups with rows for the many-row kernel, stretches taken beyond each warp's first.
-enum { kOwnStretches, kPrefixStretches, kTileGroups, kTaken, kCounts };
+// Stretches on the lists, groups with rows for the many-row kernel, stretches taken beyond each warp's first, own units
+// of the many-row kernel to be joined.
+enum { kOwnStretches, kPrefixStretches, kTileGroups, kTaken, kOwnUnits, kCounts };
 
 struct SharedArgs {
     PagedArgs a;
@@ -80,6 +81,8 @@ struct SharedArgs {
     int32_t *counts;           // [kCounts]
     int clusters;              // of the plan
     int prefix_cap, own_cap;
+    const int4 *own_units;     // [own_units_cap][2]: see PagedArgs::part_list
+    int own_units_cap;
     int few;                   // own parts (and prefixes of few rows) are cut into stretches
     int any_tiles;             // prefixes may go to the many-row kernel
     int prefix_tokens, own_tokens;  // tokens of a query tile of the many-row kernel

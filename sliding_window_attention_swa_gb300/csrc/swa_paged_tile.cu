@@ -957,10 +957,23 @@ __global__ void __launch_bounds__(TileCfg<D>::THREADS, 1)
             bool joined = false;
             if constexpr (PT != Part::kAll) {
                 if (store && !final) *(whole ? a.part_ml + tok * a.H_q + h : ml_at(pslot)) = make_float2(m, l);
-                // (every warp of every piece writes the same; -1: the rows are final)
-                if (lane == 0)
+                if (PT == Part::kPrefix && lane == 0)  // (every warp of every piece writes the same)
                     a.part_units[(static_cast<int64_t>(wk->q0 / TT) + wk->b + wk->ut) * a.H_kv + wk->kvh] =
-                        make_int2(wk->owner, final ? -1 : unit_pieces);
+                        make_int2(wk->owner, unit_pieces);
+                // one warp of a unit's first piece
+                if (PT == Part::kOwn && !final && (NQT == 1 || wg == 0) && quarter == 0 && lane == 0 && (whole || pslot == 2 * wk->owner + 1)) {
+                    int first = -1, number = 0;
+                    if (wk->base > 0) {
+                        const int *info = reinterpret_cast<const int *>(a.part_info + 2 * static_cast<int64_t>(wk->b));
+                        first = __ldcg(info + 3), number = __ldcg(info + 5);
+                    }
+                    const int at = atomicAdd(a.part_count, 1);
+                    // (more than there is room for: sequences that overlap, from a q_start that goes down, which is reported)
+                    if (at < a.part_cap) {
+                        a.part_list[2 * at] = make_int4(wk->owner, unit_pieces, wk->b, wk->ut * a.H_kv + wk->kvh);
+                        a.part_list[2 * at + 1] = make_int4(wk->q0, wk->n, first, number);
+                    }
+                }
             } else if (!whole) {
                 // The piece is written.  Warps of the same place have the same rows and columns of it in
                 // every CTA that shares the unit, so the last of them to arrive joins those: a row's

@@ -459,6 +459,16 @@ def test_sequences_that_overlap(swa, D, hint):
     run(swa, x, max_q=hint)
 
 
+@pytest.mark.parametrize("hint", [0, 1])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_nothing_is_read_that_the_call_has_not_written(swa, shape, hint):
+    # a workspace of NaN: a value of it would show even with a weight of zero
+    ws = torch.empty(1 << 31, dtype=torch.uint8, device="cuda").fill_(0xff)
+    run(swa, Shared(25, MIXED, *shape, lead=3, tail=5, before=[(9, 1), (40, 2)], behind=[(100, 3), (0, 1)]), max_q=hint, workspace=ws)
+    long = [(9000, [(9000 + 3 * i, 1 + i % 7) for i in range(24)] + [(9111, 128 // (shape[0] // shape[1]) + 3)])]
+    run(swa, Shared(26, long, *shape[:4], 0, 0), max_q=hint, workspace=ws.fill_(0xff))
+
+
 def test_one_workspace_for_many_calls(swa):
     """Calls one after the other in one workspace, whatever the last one left there: shapes, parts and hints change."""
     ws = torch.empty(1 << 29, dtype=torch.uint8, device="cuda").fill_(0x5a)
