@@ -373,9 +373,9 @@ SWA_API swa_status swa_paged_attend(const swa_paged_params *p, const swa_paged_c
  * new tokens, below the least p0, an entry that a sequence has no use for (behind its window, no sink) being
  * alike to any -- and is read once for all their new tokens; the rest is read for each sequence.  The result is
  * swa_paged_attend's up to rounding, whatever the rows hold: a group that shares nothing is computed as if it
- * were none, and so is one of which a sequence is out of range, and all of them where group_start is (which is
- * reported: SWA_DEVERR_BAD_POSITION).  A position that some queries of the group keep must be finite in the
- * shared pages, as swa_paged_attend asks of each sequence's own.
+ * were none, and so is one of which a sequence is out of range, and all of them where group_start is or where
+ * q_start goes down (which is reported: SWA_DEVERR_BAD_POSITION).  A position that some queries of the group keep must
+ * be finite in the shared pages, as swa_paged_attend asks of each sequence's own.
  * p, c, errors and requirements as swa_paged_attend; 1 <= n_groups <= 8192.
  * Workspace: swa_paged_shared_workspace_size bytes, 256-byte aligned: the partial results, fp32 [N, H_q, d_h] for each of
  * the two parts, several times that where sequences have few new tokens.  It does not depend on device data.

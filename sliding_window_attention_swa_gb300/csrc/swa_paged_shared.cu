@@ -178,6 +178,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_plan_kernel(const __grid_co
         const int b0 = __ldg(sa.group_start + i), b1 = __ldg(sa.group_start + i + 1);
         fine = fine && b0 >= 0 && b1 >= b0 && b1 <= a.B;
     }
+    // (A q_start that goes down can give many groups the same rows, and each of them all rows: more work than any call
+    // has.  Then there is no group.)
+    if (a.q_start) {
+#pragma unroll 8
+        for (int b = tid; b < a.B; b += kThreads) fine = fine && __ldg(a.q_start + b) <= __ldg(a.q_start + b + 1);
+    }
     fine = __syncthreads_and(fine);
     if (!fine && blockIdx.x == 0 && tid == 0) atomicOr(&g_shared_err, SWA_DEVERR_BAD_POSITION);
     for (int g = c; g < sa.n_groups; g += clusters) {
