@@ -103,7 +103,7 @@ __device__ __forceinline__ void list_stretches(const SharedArgs &sa, const Keys 
     if (lane == 31 && inc > 0) at = atomicAdd(sa.counts + (t.part ? kPrefixStretches : kOwnStretches), inc);
     at = __shfl_sync(0xffffffffu, at, 31) + __shfl_sync(0xffffffffu, inc - mine, lane - sub);
     for (int i = sub; i < count; i += lanes) {
-        // (more than there is room for: sequences that overlap, from a q_start that goes down)
+        // (no list has more than there is room for: the units' sequences have no row in common)
         if (at + i >= (t.part ? sa.prefix_cap : sa.own_cap)) {
             atomicOr(&g_shared_err, SWA_DEVERR_BAD_POSITION);
             break;
@@ -117,8 +117,19 @@ __device__ __forceinline__ void list_stretches(const SharedArgs &sa, const Keys 
     }
 }
 
+// Whether another sequence has rows of sequence b (s), too, as a q_start that goes down can make it.
+__device__ __forceinline__ bool rows_in_common(const PagedArgs &a, const Seq &s, int b) {
+    for (int c = 0; c < a.B; ++c) {
+        const Seq t = load_seq(a, c);
+        if (c != b && in_common(s, t)) return true;
+    }
+    return false;
+}
+
 // What the other kernels need to know of sequences b0 .. b1 - 1 (of group g), by `warps` warps, of which this is
 // number w; a warp has as many sequences at a time as leave none to another turn, 32 at most.
+// kOrdered: q_start does not go down.
+template <bool kOrdered>
 __device__ __forceinline__ void put_sequences(const SharedArgs &sa, int b0, int b1, const PagedGroup &group, int g, int w,
                                               int warps) {
     const PagedArgs &a = sa.a;
@@ -132,17 +143,21 @@ __device__ __forceinline__ void put_sequences(const SharedArgs &sa, int b0, int 
         if (b < b1) {
             s = load_seq(a, b);
             if (!s.ok) atomicOr(&g_shared_err, SWA_DEVERR_BAD_POSITION);
+            if (!kOrdered && sa.few && s.n > 0 && rows_in_common(a, s, b)) s.n = 0;
             if (sub == 0) {
                 // (a sequence without new tokens may end inside what the others share)
                 if (!sa.few) sa.base[b] = s.n > 0 ? base : 0;
                 int4 *info = sa.info + 2 * static_cast<int64_t>(b);
                 info[0] = s.n > 0 ? make_int4(base, group.n, group.few, group.q0) : make_int4(0, 0, 0, 0);
-                info[1] = make_int4(group.p0, g, 0, 0);
+                info[1] = make_int4(group.p0, g, s.n > 0, 0);
             }
         }
         if (sa.few || (base > 0 && a.window != INT_MAX))  // the rows' positions
             for (int i = sub; i < s.n; i += lanes)
-                if (SWA_IN_BOUNDS(s.q0 + i < a.N, &g_shared_err)) sa.pos[s.q0 + i] = s.p0 + i;
+                if (SWA_IN_BOUNDS(s.q0 + i < a.N, &g_shared_err)) {
+                    sa.pos[s.q0 + i] = s.p0 + i;
+                    if (sa.few) sa.seq[s.q0 + i] = b;
+                }
         if (!sa.few) continue;
         const int longest = __reduce_max_sync(0xffffffffu, s.n);
         for (int ut = 0; ut * TT < longest; ++ut) {
@@ -152,6 +167,14 @@ __device__ __forceinline__ void put_sequences(const SharedArgs &sa, int b0, int 
                            Stretch{b, s.q0 + ut * TT, min(TT, s.n - ut * TT), 0, 0, 0, 0, 0}, lanes);
         }
     }
+}
+
+// All sequences, alone.  Stretches write their results by rows, so of sequences that have rows in common, as a q_start that
+// goes down can make them, none is taken: their rows stay as they were.  Thus the units are no more than the lists have
+// room for, and are counted in 32 bits.  (Out of line: for broken lists alone.)
+__device__ __noinline__ void put_alone(const SharedArgs &sa, bool ordered, int w, int warps) {
+    if (ordered) put_sequences<true>(sa, 0, sa.a.B, PagedGroup{}, -1, w, warps);
+    else put_sequences<false>(sa, 0, sa.a.B, PagedGroup{}, -1, w, warps);
 }
 
 // (two blocks an SM: the blocks that store tokens are many; with one and 222 registers the plan of 64 sequences takes 6.4
@@ -173,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_plan_kernel(const __grid_co
     }
     if (clusters == 1 && rank == 0 && tid < kCounts) sa.counts[tid] = 0;  // (seen by the cluster behind its first barrier)
     const int first_b = __ldg(sa.group_start), end_b = __ldg(sa.group_start + sa.n_groups);
-    bool fine = true;
+    bool fine = true, ordered = true;
     for (int i = tid; i < sa.n_groups; i += kThreads) {
         const int b0 = __ldg(sa.group_start + i), b1 = __ldg(sa.group_start + i + 1);
         fine = fine && b0 >= 0 && b1 >= b0 && b1 <= a.B;
@@ -182,9 +205,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_plan_kernel(const __grid_co
     // has.  Then there is no group.)
     if (a.q_start) {
 #pragma unroll 8
-        for (int b = tid; b < a.B; b += kThreads) fine = fine && __ldg(a.q_start + b) <= __ldg(a.q_start + b + 1);
+        for (int b = tid; b < a.B; b += kThreads) ordered = ordered && __ldg(a.q_start + b) <= __ldg(a.q_start + b + 1);
     }
-    fine = __syncthreads_and(fine);
+    fine = __syncthreads_and(fine && ordered);
+    ordered = fine || __syncthreads_and(ordered);
     if (!fine && blockIdx.x == 0 && tid == 0) atomicOr(&g_shared_err, SWA_DEVERR_BAD_POSITION);
     for (int g = c; g < sa.n_groups; g += clusters) {
         const int b0 = fine ? __ldg(sa.group_start + g) : 0, b1 = fine ? __ldg(sa.group_start + g + 1) : 0;
@@ -295,14 +319,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_plan_kernel(const __grid_co
                 list_stretches(sa, k, k.stretches(), Stretch{leader, out.q0, out.few, 0, 0, 0, 1, 0}, 32);
             }
         }
-        put_sequences(sa, b0, b1, out, g, rank * kWarps + warp, ranks * kWarps);
+        put_sequences<true>(sa, b0, b1, out, g, rank * kWarps + warp, ranks * kWarps);
         if (ranks > 1) cluster.barrier_wait();
         else __syncthreads();
     }
-    if (c == 0) {  // sequences of no group
-        const int lo = fine ? first_b : a.B, hi = fine ? end_b : a.B;
-        put_sequences(sa, 0, lo, PagedGroup{}, -1, rank * kWarps + warp, ranks * kWarps);
-        put_sequences(sa, hi, a.B, PagedGroup{}, -1, rank * kWarps + warp, ranks * kWarps);
+    if (c == 0 && fine) {  // sequences of no group
+        put_sequences<true>(sa, 0, first_b, PagedGroup{}, -1, rank * kWarps + warp, ranks * kWarps);
+        put_sequences<true>(sa, end_b, a.B, PagedGroup{}, -1, rank * kWarps + warp, ranks * kWarps);
+    } else if (c == 0) {
+        put_alone(sa, ordered, rank * kWarps + warp, ranks * kWarps);
     }
 }
 
@@ -462,14 +487,17 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     const int64_t x = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const int blocks = (a.H_q + kHeads - 1) / kHeads;  // of a token's heads
     const int n = static_cast<int>(x / blocks), h = static_cast<int>(x % blocks) * kHeads + lane / kLanes;
-    const int b = n < a.N ? find_sequence(a, n, lane) : -1;
+    // (the plan's: the kernels before this one have waited for it before they let this grid start; of a row of no
+    // sequence any number)
+    const int at = n < a.N ? __ldcg(sa.seq + n) : -1;
+    const int b = at >= 0 && at < a.B ? at : -1;
     const Seq s = b >= 0 ? load_seq(a, b) : Seq{};
-    // (the plan's: the kernels before this one have waited for it before they let this grid start)
     const int4 *info = sa.info + 2 * static_cast<int64_t>(max(b, 0));
-    const int4 u = __ldcg(info), v = __ldcg(info + 1);  // base, the group's tokens in tiles, in stretches, its first; its p0, number
+    // base, the group's tokens in tiles, in stretches, its first; its p0, number, whether the sequence is taken
+    const int4 u = __ldcg(info), v = __ldcg(info + 1);
     // (by every warp, with a row or without, so that what waits for this grid waits for those before it)
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (b < 0 || !s.ok || n < s.q0 || n >= s.q0 + s.n) return;
+    if (b < 0 || !v.z || n < s.q0 || n >= s.q0 + s.n) return;
     const bool row_there = h < a.H_q;
     const int head = row_there ? h : 0, TT = kStretchRows / a.G;
     const Where own = in_planes(sa.part[0], own_keys(a, s, u.x, (n - s.q0) / TT, TT, sa.part[0]));
@@ -519,7 +547,7 @@ struct Layout {
     int planes, prefix_planes, own_cap, prefix_cap;
     PagedShape shape;  // of the many-row kernel
     int own_units;  // units of the own part, at most
-    size_t slots[2], base, info, groups, pos, count, list, units[2], ml[2], o[2], few_ml, few_o, bytes;
+    size_t slots[2], base, info, groups, pos, seq, count, list, units[2], ml[2], o[2], few_ml, few_o, bytes;
 };
 
 Layout layout(const PagedArgs &a, int n_groups) {
@@ -568,6 +596,7 @@ Layout layout(const PagedArgs &a, int n_groups) {
     l.info = take(static_cast<size_t>(a.B) * 32);
     l.groups = take(static_cast<size_t>(n_groups) * sizeof(PagedGroup));
     l.pos = take(static_cast<size_t>(a.N) * 4);
+    l.seq = take(l.few ? static_cast<size_t>(a.N) * 4 : 0);
     l.count = take(kCounts * 4);
     l.list = take((static_cast<size_t>(l.prefix_cap) + l.own_cap) * sizeof(Stretch));
     l.bytes = at;
@@ -642,6 +671,7 @@ cudaError_t launch_paged_shared(const PagedArgs &a, const int32_t *group_start, 
     sa.base = reinterpret_cast<int32_t *>(p + l.base);
     sa.info = reinterpret_cast<int4 *>(p + l.info);
     sa.pos = reinterpret_cast<int32_t *>(p + l.pos);
+    sa.seq = reinterpret_cast<int32_t *>(p + l.seq);
     sa.stretches = reinterpret_cast<Stretch *>(p + l.list);
     sa.counts = reinterpret_cast<int32_t *>(p + l.count);
     sa.own_cap = l.own_cap;

@@ -32,13 +32,13 @@ struct PartResults {
 // keys), and, if sink1 > sink0, one more, [sink0, sink1), in the last plane.
 struct Keys {
     int lo, end, sink0, sink1, first, keys, count;
-    __device__ __forceinline__ int stretches() const { return count + (sink1 > sink0 ? 1 : 0); }
-    __device__ __forceinline__ int begin(int i) const { return i < count ? max(lo, first + i * keys) : sink0; }
-    __device__ __forceinline__ int close(int i) const { return i < count ? min(end, first + (i + 1) * keys) : sink1; }
+    __host__ __device__ __forceinline__ int stretches() const { return count + (sink1 > sink0 ? 1 : 0); }
+    __host__ __device__ __forceinline__ int begin(int i) const { return i < count ? max(lo, first + i * keys) : sink0; }
+    __host__ __device__ __forceinline__ int close(int i) const { return i < count ? min(end, first + (i + 1) * keys) : sink1; }
 };
 
 // At most p.planes - 1 stretches, and the sinks'.
-__device__ __forceinline__ Keys split_keys(int lo, int end, int sink0, int sink1, const PartResults &p) {
+__host__ __device__ __forceinline__ Keys split_keys(int lo, int end, int sink0, int sink1, const PartResults &p) {
     Keys k;
     k.lo = lo;
     k.end = end;
@@ -52,7 +52,7 @@ __device__ __forceinline__ Keys split_keys(int lo, int end, int sink0, int sink1
 }
 
 // Keys at or past base of the unit of tokens ut * TT .. of sequence s.
-__device__ __forceinline__ Keys own_keys(const PagedArgs &a, const Seq &s, int base, int ut, int TT,
+__host__ __device__ __forceinline__ Keys own_keys(const PagedArgs &a, const Seq &s, int base, int ut, int TT,
                                          const PartResults &p) {
     const int t0 = s.p0 + ut * TT, t1 = s.p0 + min(s.n, (ut + 1) * TT) - 1;
     const int lo = max(base, t0 >= a.window ? t0 - a.window + 1 : 0);
@@ -60,9 +60,14 @@ __device__ __forceinline__ Keys own_keys(const PagedArgs &a, const Seq &s, int b
 }
 
 // Keys of a prefix.
-__device__ __forceinline__ Keys prefix_keys(const PagedArgs &a, int p0, int end, const PartResults &p) {
+__host__ __device__ __forceinline__ Keys prefix_keys(const PagedArgs &a, int p0, int end, const PartResults &p) {
     const int lo = p0 >= a.window ? p0 - a.window + 1 : 0;
     return split_keys(lo, end, 0, min(a.n_sink, lo), p);
+}
+
+// Whether two sequences have rows in common.
+__host__ __device__ __forceinline__ bool in_common(const Seq &s, const Seq &t) {
+    return s.n > 0 && t.n > 0 && s.q0 < t.q0 + t.n && t.q0 < s.q0 + s.n;
 }
 
 // Stretches on the lists, groups with rows for the many-row kernel, stretches taken beyond each warp's first, own units
@@ -75,8 +80,9 @@ struct SharedArgs {
     int n_groups;
     PagedGroup *groups;
     int32_t *base;             // [B]
-    int4 *info;                // [B][2]: base, its group's n, few, q0; p0, the group's number
+    int4 *info;                // [B][2]: base, its group's n, few, q0; p0, the group's number, whether it has rows
     int32_t *pos;              // [N]
+    int32_t *seq;              // [N], with few new tokens: the sequence (rows of none: anything)
     Stretch *stretches;        // [prefix_cap + own_cap]: prefixes', then own ones
     int32_t *counts;           // [kCounts]
     int clusters;              // of the plan

@@ -5,6 +5,7 @@ import time
 import pytest
 import torch
 
+import paged_reference as R
 from test_gpu_paged_shared import Shared, call, run, swa  # noqa: F401  (swa: the module's fixture)
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +53,61 @@ def test_a_list_that_goes_down_at_its_end(swa):  # noqa: F811
     finally:
         swa.swa_debug_set_faults()
     assert st == 1 and words == {"prefill": 0, "split": 0, "cache": swa.DEVERR_BAD_POSITION}, words
+
+
+def check_rows(swa, x, got, kept):  # noqa: F811
+    """Rows of the sequences `kept` hold their results, all others are as they were."""
+    o, lse, cnt, *_ = got
+    mine = torch.zeros(x.N, dtype=torch.bool)
+    for b in kept:
+        q0, n = int(x.q_start[b]), x.seqs[b][1]
+        mine[q0:q0 + n] = True
+        R.check(o[q0:q0 + n], lse[q0:q0 + n], cnt[q0:q0 + n], x.reference(b), f"sequence {b}")
+    assert (o.cpu()[~mine] == 7).all() and (lse.cpu()[~mine] == 7).all() and (cnt.cpu()[~mine] == 7).all()
+
+
+@pytest.mark.parametrize("hint", [0, 4])
+@pytest.mark.parametrize("D,B", [(64, 9), (128, 300), (256, 40)])
+def test_sequences_beside_broken_ones(swa, D, B, hint):  # noqa: F811
+    """An entry of q_start that is too small or too large breaks the two sequences that it parts; all the others have
+    their results, whatever their number."""
+    good = Shared(92, [(260, [(260 + i % 5, 1 + i % 4) for i in range(B)])], 4, 2, D, 16)
+    for entry in sorted({1, 2, B // 2, B - 2}):
+        for wrong in (-3, good.N + 1, (1 << 31) - 1):
+            start = good.q_start.clone()
+            good.q_start[entry] = wrong
+            got = call(swa, good, max_q=hint)
+            good.q_start = start
+            st, words = swa.swa_read_device_errors()
+            assert st == 1 and words == {"prefill": 0, "split": 0, "cache": swa.DEVERR_BAD_POSITION}, words
+            check_rows(swa, good, got, [b for b in range(B) if b not in (entry - 1, entry)])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_of_sequences_with_rows_in_common_none_is_taken(swa, D):  # noqa: F811
+    """Few new tokens: rows that two sequences have stay as they were, the others hold their results."""
+    x = Shared(93, [(300, [(300, 4)] * 30 + [(400, 4)])], 4, 2, D, 16, lead=2, tail=3)  # (room for 16 more in a row)
+    start = x.q_start.clone()
+    # sequence 4 ends where 2 begins, and 5 begins there: it has the rows of 2 to 5
+    x.q_start[5] = start[2]
+    x.seqs[5] = (300, int(start[6] - start[2]))
+    got = call(swa, x, max_q=4)
+    st, words = swa.swa_read_device_errors()
+    assert st == 1 and words == {"prefill": 0, "split": 0, "cache": swa.DEVERR_BAD_POSITION}, words
+    check_rows(swa, x, got, [b for b in range(31) if b not in (2, 3, 4, 5)])
+
+
+@pytest.mark.parametrize("hint", [0, 1])
+def test_as_many_sequences_as_a_call_takes_have_all_rows_each(swa, hint):  # noqa: F811
+    x = Shared(94, [(64, [(64, 1)] * 8191 + [(700, 1)])], 16, 1, 64, 16)  # (room for 600 in a row)
+    x.N = 600
+    x.q = x.q[:600]
+    x.q_start = torch.tensor([0, 600] * 4096 + [0], dtype=torch.int32)
+    t0 = time.time()
+    o, lse, *_ = call(swa, x, max_q=hint)
+    st, words = swa.swa_read_device_errors()
+    assert time.time() - t0 < 20.0
+    assert st == 1 and words == {"prefill": 0, "split": 0, "cache": swa.DEVERR_BAD_POSITION}, words
+    assert hint == 0 or ((o == 7).all() and (lse == 7).all())
+    y = Shared(95, [(260, [(260, 1)] * 64)], 16, 1, 64, 16)
+    run(swa, y, max_q=hint)
