@@ -377,8 +377,12 @@ SWA_API swa_status swa_paged_attend(const swa_paged_params *p, const swa_paged_c
  * q_start goes down (which is reported: SWA_DEVERR_BAD_POSITION).  A position that some queries of the group keep must
  * be finite in the shared pages, as swa_paged_attend asks of each sequence's own.
  * p, c, errors and requirements as swa_paged_attend; 1 <= n_groups <= 8192.
- * Workspace: swa_paged_shared_workspace_size bytes, 256-byte aligned: the partial results, fp32 [N, H_q, d_h] for each of
- * the two parts, several times that where sequences have few new tokens.  It does not depend on device data.
+ * Workspace: swa_paged_shared_workspace_size bytes, 256-byte aligned.  It does not depend on device data.  For the
+ * partial results, fp32 [N, H_q, d_h + 2] for each of the two parts, and three of the first where sequences have few new
+ * tokens; beside that, whatever N is, some 40 MB for units that several CTAs share and, with few new tokens, stretches
+ * enough for every warp (32 heads of 128 on 8, one token a sequence, by the number of groups: 17 MB for 4 sequences, 66
+ * to 80 for 64, 0.6 to 1 GB for 8192).  More groups never need less, nor, with q_start NULL, do more sequences; for
+ * another N or B beside a q_start, ask anew.
  */
 SWA_API size_t swa_paged_shared_workspace_size(const swa_paged_params *p, const swa_paged_cache *c, int32_t n_groups);
 SWA_API swa_status swa_paged_attend_shared(const swa_paged_params *p, const swa_paged_cache *c, const int32_t *group_start,

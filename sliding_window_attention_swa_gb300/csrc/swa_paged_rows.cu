@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::WARPS * 32, RowsCfg<D>::CTAS_PER_S
             const int e = item / a.H_kv;
             const int4 *p = reinterpret_cast<const int4 *>(sa.stretches + (e < n_prefix ? e : sa.prefix_cap + e - n_prefix));
             const int4 x = __ldcg(p), y = __ldcg(p + 1);
-            w.row = x.x, w.q0 = x.y, w.n = x.z, w.plane = x.w, w.k0 = y.x, w.k1 = y.y, w.part = y.z;
+            w.row = x.x, w.q0 = x.y, w.n = x.z, w.plane = x.w, w.k0 = y.x, w.k1 = y.y, w.part = y.z, w.place = y.w;
             w.kvh = item % a.H_kv;
             w.first = w.k0 & ~(KS - 1);
             w.steps = (w.k1 - w.first + KS - 1) / KS;
@@ -284,9 +284,9 @@ __global__ void __launch_bounds__(RowsCfg<D>::WARPS * 32, RowsCfg<D>::CTAS_PER_S
             l1 += __shfl_xor_sync(0xffffffffu, l1, o);
         }
         const PartResults &pt = w.part ? sa.few_prefix : sa.part[0];
-        const int64_t plane = static_cast<int64_t>(w.plane) * a.N;
-        const int64_t at0 = (plane + tok0) * a.H_q + h0, at1 = (plane + tok1) * a.H_q + h1;
-        const bool there = SWA_IN_BOUNDS(w.plane < pt.planes && h1 < a.H_q, &g_rows_err);
+        const int64_t first = static_cast<int64_t>(w.plane) * pt.tokens + (w.place - w.q0);
+        const int64_t at0 = (first + tok0) * a.H_q + h0, at1 = (first + tok1) * a.H_q + h1;
+        const bool there = SWA_IN_BOUNDS(w.plane < pt.planes && w.place >= 0 && w.place + w.n <= pt.tokens && h1 < a.H_q, &g_rows_err);
         if (v0 && there) {
 #pragma unroll
             for (int n = 0; n < D / 8; ++n)

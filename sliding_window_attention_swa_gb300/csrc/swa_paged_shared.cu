@@ -50,6 +50,7 @@ constexpr int kLeastSaved = 1;
 #else
 constexpr int kLeastSaved = 3500;
 #endif
+constexpr int kMostPlanes = 129;  // of a part in stretches
 constexpr int kTileRows = 128;  // rows of a query tile of the many-row kernel
 // Of the join of units, for an SM (two at a time; 22 chunks of up to 16 tokens: 72 us, 75 with two, 72 with eight).
 constexpr int kJoinBlocks = 4;
@@ -113,7 +114,7 @@ __device__ __forceinline__ void list_stretches(const SharedArgs &sa, const Keys 
         t.plane = i < k.count ? i : (t.part ? sa.few_prefix : sa.part[0]).planes - 1;
         int4 *dst = reinterpret_cast<int4 *>(sa.stretches + (t.part ? 0 : sa.prefix_cap) + at + i);
         dst[0] = make_int4(t.row, t.q0, t.n, t.plane);
-        dst[1] = make_int4(t.k0, t.k1, t.part, 0);
+        dst[1] = make_int4(t.k0, t.k1, t.part, t.place);
     }
 }
 
@@ -133,7 +134,7 @@ template <bool kOrdered>
 __device__ __forceinline__ void put_sequences(const SharedArgs &sa, int b0, int b1, const PagedGroup &group, int g, int w,
                                               int warps) {
     const PagedArgs &a = sa.a;
-    const int TT = kStretchRows / a.G, base = group.end;
+    const int TT = few_tokens(a.G), base = group.end;
     int each = 1;
     while (each < 32 && each * warps < b1 - b0) each *= 2;
     const int lane = threadIdx.x & 31, lanes = 32 / each, sub = lane & (lanes - 1);
@@ -164,7 +165,7 @@ __device__ __forceinline__ void put_sequences(const SharedArgs &sa, int b0, int 
             const bool unit = ut * TT < s.n;
             const Keys k = unit ? own_keys(a, s, base, ut, TT, sa.part[0]) : Keys{};
             list_stretches(sa, k, unit ? k.stretches() : 0,
-                           Stretch{b, s.q0 + ut * TT, min(TT, s.n - ut * TT), 0, 0, 0, 0, 0}, lanes);
+                           Stretch{b, s.q0 + ut * TT, min(TT, s.n - ut * TT), 0, 0, 0, 0, s.q0 + ut * TT}, lanes);
         }
     }
 }
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_plan_kernel(const __grid_co
             }
             if (out.few > 0) {
                 const Keys k = prefix_keys(a, p0, base, sa.few_prefix);
-                list_stretches(sa, k, k.stretches(), Stretch{leader, out.q0, out.few, 0, 0, 0, 1, 0}, 32);
+                list_stretches(sa, k, k.stretches(), Stretch{leader, out.q0, out.few, 0, 0, 0, 1, prefix_place(sa, g, out.q0)}, 32);
             }
         }
         put_sequences<true>(sa, b0, b1, out, g, rank * kWarps + warp, ranks * kWarps);
@@ -357,16 +358,17 @@ __device__ __forceinline__ void load_columns(float (&x)[E], const float *src) {
 // Where the results of a row's part are: in planes, or in the slots of the CTAs that share its unit.
 struct Where {
     const PartResults *p = nullptr;
-    int count = 0, sink = -1, owner = 0, row = 0;  // sink: the number of the sinks' stretch (their plane is the last)
+    int count = 0, sink = -1, owner = 0;  // sink: the number of the sinks' stretch (their plane is the last)
+    int row = 0;  // of the unit, or the token's place in a plane
     bool pieces = false;
 };
-__device__ __forceinline__ Where in_planes(const PartResults &p, const Keys &k) {
-    return Where{&p, k.stretches(), k.count, 0, 0, false};
+__device__ __forceinline__ Where in_planes(const PartResults &p, const Keys &k, int place) {
+    return Where{&p, k.stretches(), k.count, 0, place, false};
 }
-// Of a unit of the many-row kernel with owner and pieces x, a row of it.
-__device__ __forceinline__ Where in_unit(const PartResults &p, int2 x, int row) {
+// Of a unit of the many-row kernel with owner and pieces x, a row of it, of token n.
+__device__ __forceinline__ Where in_unit(const PartResults &p, int2 x, int row, int n) {
     // (a unit that was never finished, after an expired wait, has any record)
-    if (x.y <= 0 || x.x < 0 || x.y > p.ctas || x.x > p.ctas - x.y) return Where{&p, 1, -1, 0, 0, false};
+    if (x.y <= 0 || x.x < 0 || x.y > p.ctas || x.x > p.ctas - x.y) return Where{&p, 1, -1, 0, n, false};
     return Where{&p, x.y, -1, x.x, row, true};
 }
 // Of a row's prefix part in tiles; q0, number: of the group.
@@ -375,7 +377,7 @@ __device__ __forceinline__ Where in_prefix_tiles(const SharedArgs &sa, int q0, i
     const PartResults &p = sa.part[1];
     const int tok = n - q0, ut = tok / p.TT, r = tok % p.TT;
     const int2 rec = __ldcg(p.units + (static_cast<int64_t>(q0 / p.TT) + number + ut) * a.H_kv + head / a.G);
-    return in_unit(p, rec, r / p.TQ * kTileRows + r % p.TQ * a.G + head % a.G);
+    return in_unit(p, rec, r / p.TQ * kTileRows + r % p.TQ * a.G + head % a.G, n);
 }
 
 // Joins the row of token n of sequence b (s) and a head, by kLanes lanes; row_there: whether they have one.
@@ -387,7 +389,7 @@ __device__ __forceinline__ void join_row(const SharedArgs &sa, int b, const Seq 
     constexpr int kAtOnce = E <= 4 ? 12 : E <= 8 ? 8 : E <= 16 ? 4 : 2;  // results whose values are on their way at a time
     const PagedArgs &a = sa.a;
     const int part = threadIdx.x % kLanes;
-    const int64_t row = static_cast<int64_t>(n) * a.H_q + head, plane = static_cast<int64_t>(a.N) * a.H_q;
+    const int64_t row = static_cast<int64_t>(n) * a.H_q + head;
     auto result = [&](int c, const float2 *&ml, const float *&o) {
         const bool first = c < own.count;
         const Where &w = first ? own : pre;
@@ -398,7 +400,7 @@ __device__ __forceinline__ void join_row(const SharedArgs &sa, int b, const Seq 
             ml = reinterpret_cast<const float2 *>(p.ws.ml) + slot * p.rows + w.row;
             o = p.ws.acc + (slot * p.rows + w.row) * D;
         } else {
-            const int64_t at = (k == w.sink ? p.planes - 1 : k) * plane + row;
+            const int64_t at = (static_cast<int64_t>(k == w.sink ? p.planes - 1 : k) * p.tokens + w.row) * a.H_q + head;
             ml = p.ml + at;
             o = p.o + at * D;
         }
@@ -499,9 +501,10 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const __grid_const
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (b < 0 || !v.z || n < s.q0 || n >= s.q0 + s.n) return;
     const bool row_there = h < a.H_q;
-    const int head = row_there ? h : 0, TT = kStretchRows / a.G;
-    const Where own = in_planes(sa.part[0], own_keys(a, s, u.x, (n - s.q0) / TT, TT, sa.part[0]));
-    const Where pre = u.z > 0   ? in_planes(sa.few_prefix, prefix_keys(a, v.x, u.x, sa.few_prefix))
+    const int head = row_there ? h : 0, TT = few_tokens(a.G);
+    const Where own = in_planes(sa.part[0], own_keys(a, s, u.x, (n - s.q0) / TT, TT, sa.part[0]), n);
+    const Where pre = u.z > 0   ? in_planes(sa.few_prefix, prefix_keys(a, v.x, u.x, sa.few_prefix),
+                                            prefix_place(sa, v.y, u.w) + n - u.w)
                       : u.y > 0 ? in_prefix_tiles(sa, u.w, v.y, n, head)
                                 : Where{};
     join_row<D, kLanes>(sa, b, s, n, head, row_there, own, pre);
@@ -535,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_join_units_kernel(const __g
         const int n = s.q0 + (row_there ? i : 0), head = kvh * a.G + y % a.G;
         if (__all_sync(0xffffffffu, !row_there)) continue;
         const Where pre = seq.z >= 0 ? in_prefix_tiles(sa, seq.z, seq.w, n, head) : Where{};
-        join_row<D, kLanes>(sa, b, s, n, head, row_there, in_unit(p, make_int2(unit.x, unit.y), r), pre);
+        join_row<D, kLanes>(sa, b, s, n, head, row_there, in_unit(p, make_int2(unit.x, unit.y), r, n), pre);
     }
 }
 
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_join_units_kernel(const __g
 // ---------------------------------------------------------------------------------------------
 struct Layout {
     bool few, tiles;  // tiles: prefixes may go to the many-row kernel
-    int planes, prefix_planes, own_cap, prefix_cap;
+    int planes, prefix_planes, prefix_tokens, own_cap, prefix_cap;
     PagedShape shape;  // of the many-row kernel
     int own_units;  // units of the own part, at most
     size_t slots[2], base, info, groups, pos, seq, count, list, units[2], ml[2], o[2], few_ml, few_o, bytes;
@@ -556,7 +559,7 @@ Layout layout(const PagedArgs &a, int n_groups) {
     // (no group of a batch of so few rows has more than a stretch takes)
     l.tiles = !l.few || static_cast<int64_t>(a.N) * a.G > kStretchRows;
     l.shape = paged_tile_shape(a);
-    const int TT = kStretchRows / a.G;
+    const int TT = few_tokens(a.G);
     const int64_t units = std::min<int64_t>(a.N, static_cast<int64_t>(a.N) / TT + a.B);
     // Planes: the stretches that a unit of each part has at most, and the sinks'.  So many that there are six own
     // stretches for every resident warp where all are as long as that, two of prefixes, whose results have more rows;
@@ -564,41 +567,53 @@ Layout layout(const PagedArgs &a, int n_groups) {
     // 64 histories of 4096 tokens that share nothing: 4, 6, 16 own ones 193, 194, 217 us.)
     auto planes = [&](int64_t each, int64_t n) {
         const int64_t want = (each * shared_rows_warps(a.D) + n * a.H_kv - 1) / (n * a.H_kv);
-        return static_cast<int>(std::min<int64_t>(std::max<int64_t>(want, 2), 128)) + 1;
+        return static_cast<int>(std::min<int64_t>(std::max<int64_t>(want, 2), kMostPlanes - 1)) + 1;
     };
-    const int64_t prefixes = std::max<int64_t>(std::min<int64_t>(n_groups, a.N / 2), 1);
+    // At least planes(each, n) * n, and not less for more n, so that the size does not shrink where the call grows.
+    auto room = [&](int64_t each, int64_t n) {
+        const int64_t stretches = (each * shared_rows_warps(a.D) + a.H_kv - 1) / a.H_kv;
+        return std::min<int64_t>(kMostPlanes * n, std::max(stretches + 2 * n, 3 * n));
+    };
+    // A prefix of few rows is that of two tokens at least, and of no more than a stretch takes: as many places each.
+    const int64_t prefixes = std::min<int64_t>(n_groups, (static_cast<int64_t>(a.N) + 1) / 2);
+    const bool few_prefixes = l.few && TT >= 2 && a.N >= 2;
     l.planes = l.few ? planes(6, units) : 1;
-    l.prefix_planes = l.few ? planes(2, prefixes) : 0;
+    l.prefix_planes = few_prefixes ? planes(2, prefixes) : 0;
+    l.prefix_tokens = few_prefixes ? static_cast<int>(std::min<int64_t>(a.N, static_cast<int64_t>(n_groups) * TT)) : 0;
     const int64_t most = INT_MAX / 2 / a.H_kv;  // (the items of both, a head each, are counted in 32 bits)
     l.own_cap = l.few ? static_cast<int>(std::min(units * l.planes, most)) : 0;
-    l.prefix_cap = l.few ? static_cast<int>(std::min(prefixes * l.prefix_planes, most)) : 0;
+    l.prefix_cap = few_prefixes ? static_cast<int>(std::min(prefixes * l.prefix_planes, most)) : 0;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t x = at;
         at += paged_up(bytes);
         return x;
     };
-    const size_t rows = static_cast<size_t>(a.N) * a.H_q;
     const bool tiles[2] = {!l.few, l.tiles};
     for (int p = 0; p < 2; ++p) {
         const int TU = paged_tile_tokens(a, p ? Part::kPrefix : Part::kOwn);
         const size_t n_units = (static_cast<size_t>(a.N) / TU + (p ? n_groups : a.B) + 2) * a.H_kv;
-        const size_t planes = p ? 1 : l.planes;
+        // (tokens times planes)
+        const size_t results = p || !l.few ? a.N : (static_cast<size_t>(room(6, units)) * a.N + units - 1) / units;
         l.slots[p] = take(tiles[p] ? paged_ws_bytes(l.shape, a.D) : 0);
         l.units[p] = take(tiles[p] ? n_units * (p ? sizeof(int2) : 2 * sizeof(int4)) : 0);
         if (!p) l.own_units = tiles[p] ? static_cast<int>(std::min<size_t>(n_units, INT_MAX / 2)) : 0;
-        l.ml[p] = take(tiles[p] || !p ? planes * rows * 8 : 0);
-        l.o[p] = take(tiles[p] || !p ? planes * rows * a.D * 4 : 0);
+        l.ml[p] = take(tiles[p] || !p ? results * a.H_q * 8 : 0);
+        l.o[p] = take(tiles[p] || !p ? results * a.H_q * a.D * 4 : 0);
     }
-    l.few_ml = take(l.prefix_planes * rows * 8);
-    l.few_o = take(l.prefix_planes * rows * a.D * 4);
+    // (prefix_tokens * prefix_planes at least: groups * TT are all tokens or those of all groups, and fewer groups do not
+    // have fewer planes)
+    const int64_t groups = std::min<int64_t>(prefixes, (static_cast<int64_t>(a.N) + TT - 1) / TT);
+    const size_t results = few_prefixes ? static_cast<size_t>(room(2, groups)) * TT : 0;
+    l.few_ml = take(results * a.H_q * 8);
+    l.few_o = take(results * a.H_q * a.D * 4);
     l.base = take(static_cast<size_t>(a.B) * 4);
     l.info = take(static_cast<size_t>(a.B) * 32);
     l.groups = take(static_cast<size_t>(n_groups) * sizeof(PagedGroup));
     l.pos = take(static_cast<size_t>(a.N) * 4);
     l.seq = take(l.few ? static_cast<size_t>(a.N) * 4 : 0);
     l.count = take(kCounts * 4);
-    l.list = take((static_cast<size_t>(l.prefix_cap) + l.own_cap) * sizeof(Stretch));
+    l.list = take(((few_prefixes ? room(2, prefixes) : 0) + (l.few ? room(6, units) : 0)) * sizeof(Stretch));
     l.bytes = at;
     return l;
 }
@@ -686,6 +701,7 @@ cudaError_t launch_paged_shared(const PagedArgs &a, const int32_t *group_start, 
         r.ml = reinterpret_cast<float2 *>(p + l.ml[x]);
         r.o = reinterpret_cast<float *>(p + l.o[x]);
         r.planes = x ? 1 : l.planes;
+        r.tokens = a.N;
         if (x) r.units = reinterpret_cast<const int2 *>(p + l.units[x]);
         r.ws = paged_carve(p + l.slots[x], l.shape, a.D);
         r.ctas = l.shape.ctas;
@@ -696,6 +712,7 @@ cudaError_t launch_paged_shared(const PagedArgs &a, const int32_t *group_start, 
     sa.few_prefix.ml = reinterpret_cast<float2 *>(p + l.few_ml);
     sa.few_prefix.o = reinterpret_cast<float *>(p + l.few_o);
     sa.few_prefix.planes = l.prefix_planes;
+    sa.few_prefix.tokens = l.prefix_tokens;
     auto part_args = [&](int x) {
         PagedArgs t = sa.a;
         t.kn = t.vn = nullptr;

@@ -12,21 +12,26 @@ constexpr int kStretchRows = 16;  // rows of a unit of the kernel for few rows (
 constexpr int kStretchKeys = 64;
 
 // One stretch: tokens q0 .. q0 + n - 1 (n * G <= 16 rows) over the keys k0 .. k1 - 1 in the pages of row
-// `row` of the table; its result goes to plane `plane` of part `part` (0: own, 1: prefix).
+// `row` of the table; its result goes to plane `plane` of part `part` (0: own, 1: prefix), to tokens `place` on there.
 struct Stretch {
-    int32_t row, q0, n, plane, k0, k1, part, unused;
+    int32_t row, q0, n, plane, k0, k1, part, place;
 };
 
-// The results of both parts.  Rows of a part are [N, H_q] in each of `planes` planes (one, of the many-row kernel).
+// The results of a part: rows [tokens, H_q] in each of `planes` planes (one, of the many-row kernel).  A token has its
+// own number in a plane, but for prefixes of few rows where the groups are too few to have all tokens: there group g
+// has the places from g * few_tokens(G) on.
 struct PartResults {
     float2 *ml;
     float *o;
-    int planes;
+    int planes, tokens;
     // of the many-row kernel: its units (the prefix's), and the slots of those that several CTAs have
     const int2 *units;
     PagedWs ws;
     int ctas, rows, TQ, TT;
 };
+
+// Tokens that a stretch has at most.
+__host__ __device__ __forceinline__ int few_tokens(int G) { return kStretchRows / G; }
 
 // A unit's keys: [lo, end) in `count` stretches, stretch i the part within [first + i * keys, first + (i + 1) *
 // keys), and, if sink1 > sink0, one more, [sink0, sink1), in the last plane.
@@ -95,6 +100,11 @@ struct SharedArgs {
     PartResults part[2];       // own, prefix in tiles
     PartResults few_prefix;
 };
+
+// Where the prefix of group g, of few rows, from token q0 on, has its results.
+__device__ __forceinline__ int prefix_place(const SharedArgs &sa, int g, int q0) {
+    return sa.few_prefix.tokens < sa.a.N ? g * few_tokens(sa.a.G) : q0;
+}
 
 cudaError_t launch_shared_rows(const SharedArgs &sa, bool behind_tiles, cudaStream_t s);
 int shared_rows_warps(int D);  // warps that are resident at a time
