@@ -412,8 +412,9 @@ typedef struct swa_rope {
 /*
  * Makes such a table: table[p, i] = scale * cos(p * inv_freq[i]), table[p, rot_dim / 2 + i] = scale *
  * sin(p * inv_freq[i]) for 0 <= p < n_pos; inv_freq: device fp64 [rot_dim / 2], any finite numbers
- * (one that is not gives NaN).  The angle is taken modulo a turn with an error below p * 2^-64 turns, so
- * an entry is off by less than 2^-22 * |scale| at any position.
+ * (one that is not gives NaN).  For |inv_freq| up to 2^43 the angle is taken modulo a turn with an error below
+ * p * 2^-64 turns, so an entry is off by less than 2^-22 * |scale| at any position; above, the angle's error is
+ * p * |inv_freq| * 2^-107 turns.
  * Requirements: rot_dim a multiple of 16, at most 256; 0 <= n_pos <= 2^30; scale finite; table 16-byte
  * aligned, inv_freq 8-byte.
  */

@@ -25,7 +25,7 @@ constexpr int kThreads = 256;
 // ---------------------------------------------------------------------------------------------
 constexpr int kTableCols = 128;  // most columns (half a head of 256)
 
-// frac(f / (2 pi)) in units of 2^-64
+// frac(f / (2 pi)) in units of 2^-64, off by less than one up to |f| = 2^43 (the two numbers hold 107 bits of 1 / (2 pi))
 __device__ __forceinline__ unsigned long long turn_fraction(double f) {
     // |f| / (2 pi) as an unevaluated sum hi + lo, 1 / (2 pi) being one of two 64-bit numbers
     const double x = fabs(f), inv = 0.15915494309189535, inv_lo = -9.839338337591243e-18;
