@@ -431,7 +431,7 @@ SWA_API swa_status swa_rope_table(const double *inv_freq, int32_t rot_dim, int32
  * cache as they were (SWA_DEVERR_BAD_POSITION); a token whose page is missing is not stored, its query is
  * rotated all the same (SWA_DEVERR_BAD_PAGE).  Rows of no sequence stay as they were.
  * Requirements: as for swa_paged_attend where given (any H_q that is a multiple of H_kv); rot_dim a multiple
- * of 16, at most d_h; interleaved 0 or 1; the table 16-byte aligned.
+ * of 16, at most d_h; n_pos at least 1; interleaved 0 or 1; the table 16-byte aligned.
  */
 SWA_API swa_status swa_paged_rope_append(const swa_paged_params *p, const swa_paged_cache *c, const swa_rope *r,
                                          swa_stream_t stream);

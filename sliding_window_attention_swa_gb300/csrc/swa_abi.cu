@@ -774,6 +774,9 @@ swa_status swa_paged_rope_append(const swa_paged_params *p, const swa_paged_cach
         if (!p->o || p->H_q < 1 || p->H_q % c->H_kv != 0) return SWA_ERR_INVALID_ARG;
         if (!strides2_ok(p->q_strides) || !strides2_ok(p->o_strides) || !aligned16(p->q) || !aligned16(p->o))
             return SWA_ERR_UNSUPPORTED;
+        // in place, a row lies where it lay
+        if (p->o == p->q && ((p->N > 1 && p->o_strides[0] != p->q_strides[0]) || (p->H_q > 1 && p->o_strides[1] != p->q_strides[1])))
+            return SWA_ERR_INVALID_ARG;
     }
     if (p->N == 0) return SWA_OK;
     const swa::RopeArgs ra{r->table, r->n_pos, r->rot_dim, r->interleaved};
