@@ -52,3 +52,51 @@ def test_no_list_has_more_than_there_is_room_for(lib, seed):
         q_start[rng.randrange(B + 1)] = rng.choice([rng.randrange(N + 1), -3, N + 1, 0, N])
     every, taken = counted(lib, q_start, p0, N, TT, planes)
     assert taken <= min(every, room(N, B, TT, planes))
+
+
+# ---------------------------------------------------------------------------------------------
+# how a unit's keys are cut
+# ---------------------------------------------------------------------------------------------
+def own(lib, p0, n, base, ut, TT, window, sinks, planes):
+    out = (ctypes.c_int * (2 * planes))()
+    count = lib.own_stretches(p0, n, base, ut, TT, window, sinks, planes, out)
+    return [tuple(out[2 * i:2 * i + 2]) for i in range(count)]
+
+
+def prefix(lib, p0, end, window, sinks, planes):
+    out = (ctypes.c_int * (2 * planes))()
+    count = lib.prefix_stretches(p0, end, window, sinks, planes, out)
+    return [tuple(out[2 * i:2 * i + 2]) for i in range(count)]
+
+
+@pytest.mark.parametrize("seed", range(120))
+def test_the_kernels_stretches_cover_the_kept_keys_once(lib, seed):
+    """A unit's own stretches and its group's: every key that a token of it keeps lies in exactly one, and they are no
+    more than there are planes, the sinks' among them."""
+    rng = random.Random(seed)
+    window, sinks = rng.choice([0, 1, 50, 300, 1000]), rng.choice([0, 1, 40, 400])
+    ps, TT = rng.choice([16, 32, 64, 128]), rng.choice([1, 4, 16])
+    least = rng.choice([rng.randrange(0, 3000), (1 << 30) - 4000])  # the least p0 of a group
+    base = rng.choice([0, rng.randrange(0, least // ps + 1) * ps])
+    if least > 4000:
+        window, base = window or 700, rng.choice([0, (least - 300) // ps * ps])
+    lo = max(0, least - window + 1) if window else 0
+    if base <= lo:
+        base = 0
+    for _ in range(4):
+        p0, n, planes = least + rng.choice([0, rng.randrange(900)]), rng.randrange(1, 40), rng.randrange(3, 20)
+        shared = prefix(lib, least, base, window, sinks, planes) if base else []
+        assert len(shared) <= planes
+        for ut in range(-(-n // TT)):
+            mine = own(lib, p0, n, base, ut, TT, window, sinks, planes)
+            assert 0 < len(mine) <= planes
+            parts = sorted(shared + mine)
+            assert all(a < b for a, b in parts) and all(x[1] <= y[0] for x, y in zip(parts, parts[1:]))
+            for t in range(p0 + ut * TT, p0 + min(n, (ut + 1) * TT)):
+                first = max(0, t - window + 1) if window else 0
+                for a, b in ([(0, min(sinks, first))] if min(sinks, first) > 0 else []) + [(first, t + 1)]:
+                    # [a, b) lies in the stretches
+                    for x, y in parts:
+                        if x <= a < y:
+                            a = y
+                    assert a >= b, (t, a, b, parts)
