@@ -48,7 +48,7 @@ __device__ __forceinline__ uint32_t sw128(int row, int pc) {
 }
 
 struct Work : Stretch {
-    int kvh, first, steps;  // first: the first step's first key
+    int kvh, key0, steps;  // key0: the first step's first key
 };
 
 template <int D>
@@ -101,10 +101,10 @@ __global__ void __launch_bounds__(RowsCfg<D>::WARPS * 32, RowsCfg<D>::CTAS_PER_S
             const int e = item / a.H_kv;
             const int4 *p = reinterpret_cast<const int4 *>(sa.stretches + (e < n_prefix ? e : sa.prefix_cap + e - n_prefix));
             const int4 x = __ldcg(p), y = __ldcg(p + 1);
-            w.row = x.x, w.q0 = x.y, w.n = x.z, w.plane = x.w, w.k0 = y.x, w.k1 = y.y, w.part = y.z, w.place = y.w;
+            w.row = x.x, w.q0 = x.y, w.n = x.z, w.first = x.w, w.k0 = y.x, w.k1 = y.y, w.part = y.z;
             w.kvh = item % a.H_kv;
-            w.first = w.k0 & ~(KS - 1);
-            w.steps = (w.k1 - w.first + KS - 1) / KS;
+            w.key0 = w.k0 & ~(KS - 1);
+            w.steps = (w.k1 - w.key0 + KS - 1) / KS;
         }
         return w;
     };
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::WARPS * 32, RowsCfg<D>::CTAS_PER_S
     // box i from step `from` on; -1: the box is outside the stretch, n_pages: there is none.
     const int box = min(a.ps, KS), boxes = KS / box, window = 32 / boxes;
     auto pages_of = [&](const Work &w, int from) -> int {
-        const int key = w.first + from * KS + lane * box;
+        const int key = w.key0 + from * KS + lane * box;
         return from < w.steps && key < w.k1 && key + box > w.k0 ? page_of(a, w.row, key >> a.ps_log2) : -1;
     };
     // what is streamed once leaves L2 before the parts' results do
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::WARPS * 32, RowsCfg<D>::CTAS_PER_S
         if (lane == 0) mbar_arrive_expect_tx(bar(st), C::STAGE);
         __syncwarp();
         if (lane < 2 * boxes) {  // keys, then values, a lane each
-            const int v = lane / boxes, row = (w.first + i * KS + j * box) & (a.ps - 1);
+            const int v = lane / boxes, row = (w.key0 + i * KS + j * box) & (a.ps - 1);
             if (page >= a.n_pages) atomicOr(&g_rows_data, SWA_DEVERR_BAD_PAGE);
             // debug build: the box lies in the page, the head exists
             (void)SWA_IN_BOUNDS(row + box <= a.ps && w.kvh < a.H_kv && page <= a.n_pages, &g_rows_err);
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::WARPS * 32, RowsCfg<D>::CTAS_PER_S
                 break;
             }
             const uint32_t ks = ring + st * C::STAGE, vs = ks + C::STAGE / 2;
-            const int key = w.first + i * KS;
+            const int key = w.key0 + i * KS;
             const bool edge = key < w.k0 || key + KS > w.k1;
             if (edge) {  // value rows outside the stretch may hold anything, even NaN
                 uint8_t *vg = ring_gen + st * C::STAGE + C::STAGE / 2;
@@ -284,9 +284,8 @@ __global__ void __launch_bounds__(RowsCfg<D>::WARPS * 32, RowsCfg<D>::CTAS_PER_S
             l1 += __shfl_xor_sync(0xffffffffu, l1, o);
         }
         const PartResults &pt = w.part ? sa.few_prefix : sa.part[0];
-        const int64_t first = static_cast<int64_t>(w.plane) * pt.tokens + (w.place - w.q0);
-        const int64_t at0 = (first + tok0) * a.H_q + h0, at1 = (first + tok1) * a.H_q + h1;
-        const bool there = SWA_IN_BOUNDS(w.plane < pt.planes && w.place >= 0 && w.place + w.n <= pt.tokens && h1 < a.H_q, &g_rows_err);
+        const int64_t at0 = static_cast<int64_t>(w.first + tok0) * a.H_q + h0, at1 = static_cast<int64_t>(w.first + tok1) * a.H_q + h1;
+        const bool there = SWA_IN_BOUNDS(w.first + w.q0 >= 0 && w.first + w.q0 + w.n <= pt.planes * pt.tokens && h1 < a.H_q, &g_rows_err);
         if (v0 && there) {
 #pragma unroll
             for (int n = 0; n < D / 8; ++n)

@@ -90,7 +90,8 @@ __device__ __forceinline__ Members shuffled(const Members &x, int o) {
 // Bound by latency: the list, the sequences' lengths, then the table's rows, all of them once, then the lists: 64
 // sequences of 512 shared entries 6.8 us, 31 groups 9.
 // ---------------------------------------------------------------------------------------------
-// Puts the stretches of a warp's units on the list: `lanes` lanes have a unit, `count` stretches of keys k.
+// Puts the stretches of a warp's units on the list: `lanes` lanes have a unit, `count` stretches of keys k; t.first: of
+// the first plane.  (Tokens in planes are counted in 32 bits: each has 256 bytes at least.)
 __device__ __forceinline__ void list_stretches(const SharedArgs &sa, const Keys &k, int count, Stretch t, int lanes) {
     const int lane = threadIdx.x & 31, sub = lane & (lanes - 1);
     const int mine = sub == 0 ? count : 0;
@@ -102,6 +103,8 @@ __device__ __forceinline__ void list_stretches(const SharedArgs &sa, const Keys 
     }
     int at = 0;
     if (lane == 31 && inc > 0) at = atomicAdd(sa.counts + (t.part ? kPrefixStretches : kOwnStretches), inc);
+    const PartResults &part = t.part ? sa.few_prefix : sa.part[0];
+    const int first = t.first;
     at = __shfl_sync(0xffffffffu, at, 31) + __shfl_sync(0xffffffffu, inc - mine, lane - sub);
     for (int i = sub; i < count; i += lanes) {
         // (no list has more than there is room for: the units' sequences have no row in common)
@@ -111,10 +114,10 @@ __device__ __forceinline__ void list_stretches(const SharedArgs &sa, const Keys 
         }
         t.k0 = k.begin(i);
         t.k1 = k.close(i);
-        t.plane = i < k.count ? i : (t.part ? sa.few_prefix : sa.part[0]).planes - 1;
+        t.first = first + (i < k.count ? i : part.planes - 1) * part.tokens;
         int4 *dst = reinterpret_cast<int4 *>(sa.stretches + (t.part ? 0 : sa.prefix_cap) + at + i);
-        dst[0] = make_int4(t.row, t.q0, t.n, t.plane);
-        dst[1] = make_int4(t.k0, t.k1, t.part, t.place);
+        dst[0] = make_int4(t.row, t.q0, t.n, t.first);
+        dst[1] = make_int4(t.k0, t.k1, t.part, 0);
     }
 }
 
@@ -165,7 +168,7 @@ __device__ __forceinline__ void put_sequences(const SharedArgs &sa, int b0, int 
             const bool unit = ut * TT < s.n;
             const Keys k = unit ? own_keys(a, s, base, ut, TT, sa.part[0]) : Keys{};
             list_stretches(sa, k, unit ? k.stretches() : 0,
-                           Stretch{b, s.q0 + ut * TT, min(TT, s.n - ut * TT), 0, 0, 0, 0, s.q0 + ut * TT}, lanes);
+                           Stretch{b, s.q0 + ut * TT, min(TT, s.n - ut * TT), 0, 0, 0, 0, 0}, lanes);
         }
     }
 }
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_plan_kernel(const __grid_co
             }
             if (out.few > 0) {
                 const Keys k = prefix_keys(a, p0, base, sa.few_prefix);
-                list_stretches(sa, k, k.stretches(), Stretch{leader, out.q0, out.few, 0, 0, 0, 1, prefix_place(sa, g, out.q0)}, 32);
+                list_stretches(sa, k, k.stretches(), Stretch{leader, out.q0, out.few, prefix_place(sa, g, out.q0) - out.q0, 0, 0, 1, 0}, 32);
             }
         }
         put_sequences<true>(sa, b0, b1, out, g, rank * kWarps + warp, ranks * kWarps);

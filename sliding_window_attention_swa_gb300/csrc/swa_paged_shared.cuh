@@ -12,9 +12,9 @@ constexpr int kStretchRows = 16;  // rows of a unit of the kernel for few rows (
 constexpr int kStretchKeys = 64;
 
 // One stretch: tokens q0 .. q0 + n - 1 (n * G <= 16 rows) over the keys k0 .. k1 - 1 in the pages of row
-// `row` of the table; its result goes to plane `plane` of part `part` (0: own, 1: prefix), to tokens `place` on there.
+// `row` of the table; the result of token t goes to token first + t of the planes of part `part` (0: own, 1: prefix).
 struct Stretch {
-    int32_t row, q0, n, plane, k0, k1, part, place;
+    int32_t row, q0, n, first, k0, k1, part, unused;
 };
 
 // The results of a part: rows [tokens, H_q] in each of `planes` planes (one, of the many-row kernel).  A token has its
