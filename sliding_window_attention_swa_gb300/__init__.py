@@ -755,8 +755,8 @@ def swa_paged_attend_shared(q, k_pages, v_pages, page_table, p0, group_start, wi
                             stream=None):
     """swa_paged_attend for sequences that share leading pages, each prefix read once: sequences group_start[g]
     .. group_start[g+1]-1 (int32 [n_groups+1]) are a group.  What they share is found from their rows of
-    page_table, so a group that shares little or nothing is as right; sequences of no group are computed alone.
-    Arguments and results as swa_paged_attend."""
+    page_table, so a group that shares little or nothing is as right (and slower than swa_paged_attend, by 3
+    to 20 us); sequences of no group are computed alone.  Arguments and results as swa_paged_attend."""
     if group_start is None:
         raise ValueError("group_start: expected int32 [n_groups + 1], one group at least")
     return swa_paged_attend(q, k_pages, v_pages, page_table, p0, window, scale, q_start=q_start, n_sink=n_sink,
