@@ -1,5 +1,6 @@
 """Attention of shared prefixes where q_start goes up and down: what that makes of the groups and the sequences,
 and that it is reported."""
+import random
 import time
 
 import pytest
@@ -111,3 +112,48 @@ def test_as_many_sequences_as_a_call_takes_have_all_rows_each(swa, hint):  # noq
     assert hint == 0 or ((o == 7).all() and (lse == 7).all())
     y = Shared(95, [(260, [(260, 1)] * 64)], 16, 1, 64, 16)
     run(swa, y, max_q=hint)
+
+
+@pytest.mark.parametrize("library", ["release", "debug"])
+@pytest.mark.parametrize("seed", range(10))
+def test_drawn_lists_in_disorder(swa, seed, library):  # noqa: F811
+    """Some entries of q_start are anything: with few new tokens exactly the sequences in range that have no row in
+    common with another have their results, and all other rows stay as they were; no check of the bounds-checking build
+    fires."""
+    prev = swa.use_library(swa.load_library(swa.build(debug=True))) if library == "debug" else None
+    try:
+        rng = random.Random(seed)
+        B = rng.choice([3, 12, 40, 200])
+        seqs = [(400 + rng.randrange(60), rng.randrange(5)) for _ in range(B)] + [(900, 1)]  # (room in the table's rows)
+        x = Shared(96 + seed, [(400, seqs)], 4, 2, rng.choice([64, 128]), 16, lead=rng.randrange(3), tail=rng.randrange(4))
+        good = x.q_start.clone()
+        for _ in range(6):
+            for _ in range(rng.randrange(1, 5)):
+                x.q_start[rng.randrange(B + 2)] = rng.choice([-1, 0, x.N, x.N + 1, rng.randrange(x.N + 1), int(good[rng.randrange(B)])])
+            start = x.q_start.tolist()
+            ok = [a >= 0 and a <= b <= x.N for a, b in zip(start, start[1:])]
+            down = any(a > b for a, b in zip(start, start[1:]))
+            spans = [(a, b) if y else (0, 0) for a, b, y in zip(start, start[1:], ok)]
+            common = lambda s, t: s[0] < s[1] and t[0] < t[1] and s[0] < t[1] and t[0] < s[1]  # noqa: E731
+            kept = [b for b in range(B + 1) if ok[b] and spans[b][1] - spans[b][0] == x.seqs[b][1] > 0
+                    and not any(common(spans[b], s) for c, s in enumerate(spans) if c != b)]
+            # (others in range whose number of rows is not their own: computed, of keys that the batch does not have)
+            loose = [b for b in range(B + 1) if ok[b] and b not in kept and spans[b][0] < spans[b][1]
+                     and not any(common(spans[b], s) for c, s in enumerate(spans) if c != b)]
+            o, lse, cnt, *_ = call(swa, x, max_q=4)
+            st, words = swa.swa_read_device_errors()
+            assert words["prefill"] == words["split"] == 0, words
+            assert words["cache"] & ~(swa.DEVERR_BAD_POSITION | swa.DEVERR_BAD_PAGE) == 0, words
+            assert bool(words["cache"] & swa.DEVERR_BAD_POSITION) == (down or not all(ok)), words
+            mine = torch.zeros(x.N, dtype=torch.bool)
+            for b in kept:
+                q0, q1 = spans[b]
+                mine[q0:q1] = True
+                R.check(o[q0:q1], lse[q0:q1], cnt[q0:q1], x.reference(b), f"sequence {b}")
+            for b in loose:
+                mine[spans[b][0]:spans[b][1]] = True
+            assert (o.cpu()[~mine] == 7).all() and (lse.cpu()[~mine] == 7).all() and (cnt.cpu()[~mine] == 7).all()
+            x.q_start = good.clone()
+    finally:
+        if prev is not None:
+            swa.use_library(prev)

@@ -42,3 +42,16 @@ def test_the_least_that_is_shared(swa, name, prefix, seqs, window):  # noqa: F81
         swa.swa_debug_set_faults()
     assert (st == SWA_ERR_TIMEOUT) == shared and words["prefill"] == (swa.DEVERR_WAIT_TIMEOUT if shared else 0), words
     run(swa, x, q_start=None)
+
+
+@pytest.mark.parametrize("sinks", [0, 5, 130])
+@pytest.mark.parametrize("D,ps", [(64, 16), (128, 64), (256, 128)])
+def test_rows_of_a_tile_that_keep_nothing_of_the_prefix(swa, D, ps, sinks):  # noqa: F811
+    """Two sequences look at what all share, the windows of the others begin behind it (their sinks do not): a tile's
+    rows of both kinds, in two tiles of rows."""
+    seqs = [(2048, 1), (2058, 1)] + [(2600 + 7 * i, 1) for i in range(60)]
+    assert of_use(seqs, 2048, 300, ps) >= LEAST and len(seqs) * 4 > 128
+    for order in (seqs, seqs[::-1], seqs[30:] + seqs[:30]):
+        x = Shared(141, [(2048, order)], 8, 2, D, ps, 300, sinks)
+        run(swa, x, q_start=None)
+        run(swa, x, True, q_start=None)
