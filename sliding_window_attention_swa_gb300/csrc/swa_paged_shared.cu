@@ -37,13 +37,15 @@ constexpr int kWords = 16, kChunk = 32 * kWords;
 
 // Shared positions below which a group is computed as none: a part of its own costs more than they do (64 sequences of
 // 32 heads of 128, 200 tokens of their own: up to 128 shared positions 24.6 us, 22.6 without the part, up to 256 in groups of
-// four 24.6 against 28.7, in groups of 64 28.7 against 33).
+// four 24.6 against 28.7, in groups of 64 28.7 against 33).  It is a limit against this call without the part, for many
+// sequences: swa_paged_attend is faster for few (four behind 900 positions: 15.5 us, 20.6 shared).
 constexpr int kLeastShared = 192;
 // With many new tokens a sequence the prefix part saves what its tiles of rows are fewer than the sequences' own, and its
 // parts are written and joined again. Below this many positions saved per own tile that costs more (12 sequences of 16
 // tokens, 6 tiles for 12, 32 heads of 128 on 8: 6000 shared positions 60 us, 56 as none; 24000 94 against 148; 48
 // sequences of 80 tokens, 120 tiles for 144: 1024 positions 222 us, 146 as none; 12 such, 24000: 304 against 361; 48 of 4
-// tokens, 6 tiles for 48: 1024 positions 60 against 57, 6000 76 against 135). The build that checks indices shares
+// tokens, 6 tiles for 48: 1024 positions 60 against 57, 6000 76 against 135). Measured there alone: 57 sequences of up
+// to three tokens in three groups, 16 heads on one, behind 9000 are above it, and take 62 us (swa_paged_attend 41). The build that checks indices shares
 // wherever there is anything to save: its tests are to reach every part.
 #ifdef SWA_DEBUG
 constexpr int kLeastSaved = 1;
